@@ -481,6 +481,85 @@ mesa_status mesa_qk_preprocess(int32_t B, int32_t H, int32_t T, int32_t d, int32
                                void* q_out, void* k_out, void* q_hist_out, void* k_hist_out,
                                hipStream_t stream);
 
+/* ---- gated linear recurrence ---------------------------------------------------
+ *
+ * MesaNet page, "architecture" section: the Hawk-Mesa hybrid alternates the
+ * Mesa layer with a gated linear recurrent layer.  Its recurrence, channel by
+ * channel, from the projections x, ga (recurrence gate) and gi (input gate)
+ * of every token and a parameter lam per channel:
+ *
+ *   a_t = exp(-c softplus(lam) sigmoid(ga_t))          0 < a_t <= 1
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(gi_t) x_t,    y_t = h_t
+ *
+ *   x, ga, gi [B, T, D] dtype   token t of sequence b starts at element
+ *                               (b T + t) ld: ld = D is a dense tensor, a
+ *                               larger ld a slice of a wider one (the three
+ *                               can be parts of one projection's output)
+ *   lam       [D]       fp32
+ *   h0        [B, D]    fp32 or NULL    state before token 0 (NULL = 0)
+ *   lengths   [B]       int32 or NULL   valid tokens of each sequence (device
+ *                               memory; values outside 0..T count as 0 or T).
+ *                               Rows at and behind a length are not used (they
+ *                               may hold anything, NaN included); their
+ *                               outputs are written as zeros.  NULL: all T
+ *   y         [B, T, D] dtype dense     out, rounded once to nearest even
+ *   h_final   [B, D]    fp32 or NULL    out: the state behind the last valid
+ *                               token (h0 for a length of 0); the next call's
+ *                               h0 and a decode state.  May be h0 itself
+ *   workspace           mesa_lru_workspace_bytes(d) bytes; on return its first
+ *                       part holds the state before every 64th token, for
+ *                       mesa_lru_bwd
+ *
+ * Arithmetic and states are fp32 for either dtype.  Every sum is formed in a
+ * fixed order: equal inputs give bitwise equal results.
+ * Supported: any D >= 1, ld >= D, T >= 0, B >= 1 with B T ld <= 2^40 and
+ * B ceil(T/64) ceil(D/64) < 2^31; c > 0, finite (else MESA_ERR_INVALID_ARG).
+ * Two calls may not use one workspace at the same time. */
+typedef struct {
+  int32_t B, T, D;   /* sequences, tokens per (padded) sequence, channels             */
+  int32_t ld;        /* elements from one token of x, ga, gi to the next (>= D)       */
+  float c;           /* decay scale (8 is usual)                                      */
+  mesa_dtype dtype;  /* of x, ga, gi, y and their gradients                           */
+} mesa_lru_desc;
+
+/* Scratch bytes of mesa_lru_fwd and mesa_lru_bwd; 0 for an invalid or
+ * unsupported descriptor and for T == 0. */
+size_t mesa_lru_workspace_bytes(const mesa_lru_desc* d);
+
+mesa_status mesa_lru_fwd(const mesa_lru_desc* d, const void* x, const void* ga, const void* gi,
+                         const float* lam, const float* h0, const int32_t* lengths,
+                         void* y, float* h_final, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+
+/* Gradients of L = sum_t <dy_t, y_t> + <d_hfinal, h_final> of a mesa_lru_fwd
+ * call.  With g_t = dy_t + a_{t+1} g_{t+1} (d_hfinal behind the last token):
+ *   dx = g m s_i,   dgi = g m x s_i (1 - s_i),   dga = v (1 - s_r),
+ *   dlam = sum_{b,t} v sigmoid(lam) / softplus(lam),   dh0 = a_0 g_0,
+ * where s_r = sigmoid(ga), s_i = sigmoid(gi), m = sqrt(1 - a^2) and
+ * v = -log(a) g ((a^2 / m) s_i x - a h_{t-1}) (0 where m = 0).
+ *
+ *   d .. lengths  the forward's (ld: the inputs' token stride)
+ *   dy            [B, T, D] dtype dense
+ *   d_hfinal      [B, D] fp32 or NULL (zero)
+ *   dx, dga, dgi  [B, T, D] dtype out, token stride ld_grad >= D (elements);
+ *                 zeros behind a length
+ *   dlam [D], dh0 [B, D] or NULL   fp32 out
+ *   states_in_workspace  1: the forward ran with this same workspace, same
+ *                 descriptor and inputs, and the states it left are used;
+ *                 0: they are formed again (x, ga, gi are read once more) */
+mesa_status mesa_lru_bwd(const mesa_lru_desc* d, const void* x, const void* ga, const void* gi,
+                         const float* lam, const float* h0, const int32_t* lengths,
+                         const void* dy, const float* d_hfinal,
+                         void* dx, void* dga, void* dgi, int32_t ld_grad, float* dlam, float* dh0,
+                         int32_t states_in_workspace, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+
+/* One token of N sequences: x, ga, gi [N, D] with row stride ld (elements),
+ * h_state [N, D] fp32 in/out, y [N, D] dtype dense out.  N >= 0. */
+mesa_status mesa_lru_step(int32_t N, int32_t D, int32_t ld, float c, mesa_dtype dtype,
+                          const void* x, const void* ga, const void* gi, const float* lam,
+                          float* h_state, void* y, hipStream_t stream);
+
 /* Static text for a status code. */
 const char* mesa_status_string(mesa_status s);
 

@@ -63,7 +63,8 @@ def lru_backward(x, ga, gi, lam, dy, *, c: float = 8.0, h0=None, lengths=None, d
     x, dy, lam = _f64(x), _f64(dy), _f64(lam)
     B, T, D = x.shape
     n = np.full(B, T) if lengths is None else np.clip(np.asarray(lengths), 0, T)
-    w, a, m, sr, si = lru_gates(x, ga, gi, lam, c)
+    w, a, m, _, si = lru_gates(x, ga, gi, lam, c)
+    sr1, si1 = _sigmoid(-_f64(ga)), _sigmoid(-_f64(gi))   # 1 - sigmoid, without the cancellation
     prev = lru_forward(x, ga, gi, lam, c=c, h0=h0, lengths=lengths)["prev"]
     out = {k: np.zeros((B, T, D)) for k in ("dx", "dga", "dgi")}
     dloglam = np.zeros(D)
@@ -76,8 +77,8 @@ def lru_backward(x, ga, gi, lam, dy, *, c: float = 8.0, h0=None, lengths=None, d
         ratio = np.divide(a[L, t] ** 2, m[L, t], out=np.zeros_like(g), where=m[L, t] > 0)
         v = 0.5 * w[L, t] * g * (ratio * si[L, t] * x[L, t] - a[L, t] * prev[L, t])
         out["dx"][L, t] = g * m[L, t] * si[L, t]
-        out["dgi"][L, t] = g * m[L, t] * x[L, t] * si[L, t] * (1.0 - si[L, t])
-        out["dga"][L, t] = v * (1.0 - sr[L, t])
+        out["dgi"][L, t] = g * m[L, t] * x[L, t] * si[L, t] * si1[L, t]
+        out["dga"][L, t] = v * sr1[L, t]
         dloglam += v.sum(0)
         after[L] = a[L, t] * g
     out["dlam"] = dloglam * _sigmoid(lam) / _softplus(lam)

@@ -123,6 +123,32 @@ struct PrepParams {
   float inv_eps;           // 1 / eps
 };
 
+// Tokens per kept state of the gated linear recurrence.
+constexpr int kLruChunk = 64;
+
+// Gated linear recurrence (mesa_lru_gate.h has the cell).
+struct LruParams {
+  const void* x;            // [B, T] rows of D, token stride ld
+  const void* ga;
+  const void* gi;
+  const float* lam;         // [D]
+  const float* h0;          // [B, D] or null
+  const int32_t* lengths;   // [B] or null
+  void* y;                  // [B, T, D], or null: states only
+  float* h_final;           // [B, D] or null (may be h0); the step's state
+  float* states;            // [B, NC, D]: state before token kLruChunk * c
+  const void* dy;           // backward: [B, T, D]
+  const float* d_hfinal;    // [B, D] or null
+  void* dx;                 // [B, T] rows of D, token stride ld_grad
+  void* dga;
+  void* dgi;
+  float* dlam;              // [D]
+  float* dh0;               // [B, D] or null
+  float* lam_part;          // partial sums of dL / d log w
+  int B, T, D, ld, ld_grad, NC;
+  float c;
+};
+
 // Backward pass (bf16 inputs, chunk 64).
 struct BwdParams {
   const void* k;            // [BH, T, D] bf16
@@ -192,6 +218,11 @@ hipError_t launch_qk_prep(bool bf16, int D, const PrepParams& p, hipStream_t s);
 hipError_t launch_sym_pack(int D, int count, const float* full, float* packed, hipStream_t s);
 hipError_t launch_sym_unpack(int D, int count, const float* packed, float* full, hipStream_t s);
 size_t sym_state_floats(int D);
+// states into LruParams::states, and y and h_final when given
+hipError_t launch_lru_fwd(bool bf16, const LruParams& p, hipStream_t s);
+// gradients, from the states launch_lru_fwd left
+hipError_t launch_lru_bwd(bool bf16, const LruParams& p, hipStream_t s);
+hipError_t launch_lru_step(bool bf16, const LruParams& p, hipStream_t s);
 
 // Bytes of one (b, h, chunk) boundary snapshot of H (or of G).
 inline size_t snapshot_bytes(bool bf16, int D) { return (size_t)D * D * (bf16 ? 2 : 4); }

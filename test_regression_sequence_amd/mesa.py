@@ -17,6 +17,7 @@ __all__ = [
     "MesaError", "lib", "library_path", "FwdDesc", "MESA_F32", "MESA_BF16",
     "workspace_bytes", "fwd_chunked", "fwd_chunked_noalloc", "fwd_chunked_prep", "fwd_scan", "fwd_solve", "decode_step", "abi_version",
     "status_string", "sym_state_floats", "sym_pack", "sym_unpack", "decode_step_symh",
+    "lru_workspace_bytes", "lru_fwd", "lru_bwd", "lru_step",
 ]
 
 MESA_F32 = 0
@@ -37,6 +38,11 @@ class FwdDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("T", ctypes.c_int32),
                 ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("chunk", ctypes.c_int32),
                 ("max_steps", ctypes.c_int32), ("tol", ctypes.c_float), ("in_dtype", ctypes.c_int)]
+
+
+class LruDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32), ("ld", ctypes.c_int32),
+                ("c", ctypes.c_float), ("dtype", ctypes.c_int)]
 
 
 def library_path() -> str:
@@ -99,6 +105,15 @@ def lib() -> ctypes.CDLL:
         L.mesa_sym_pack.argtypes = [I32, I32, P, P, P]
         L.mesa_sym_unpack.restype = ctypes.c_int
         L.mesa_sym_unpack.argtypes = [I32, I32, P, P, P]
+        D = ctypes.POINTER(LruDesc)
+        L.mesa_lru_workspace_bytes.restype = S
+        L.mesa_lru_workspace_bytes.argtypes = [D]
+        L.mesa_lru_fwd.restype = ctypes.c_int
+        L.mesa_lru_fwd.argtypes = [D] + [P] * 9 + [S, P]
+        L.mesa_lru_bwd.restype = ctypes.c_int
+        L.mesa_lru_bwd.argtypes = [D] + [P] * 11 + [I32, P, P, I32, P, S, P]
+        L.mesa_lru_step.restype = ctypes.c_int
+        L.mesa_lru_step.argtypes = [I32, I32, I32, F, ctypes.c_int] + [P] * 7
         _LIB = L
     return _LIB
 
@@ -562,4 +577,179 @@ def decode_step_ex(q, k, v, gamma, beta, lam, h_state, g_state, *, x_state=None,
                                       _ptr(g_state), _ptr(x_state), _ptr(res["o"]), _ptr(res.get("steps")),
                                       _ptr(res.get("x")), int(max_steps), float(tol), _stream(stream))
     _check(code_, "mesa_decode_step_ex")
+    return res
+
+
+# ---- operators around the layer ------------------------------------------------
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+class _Launch:
+    """The device and stream of a call: every tensor has to be on that device, and
+    what the call allocates belongs to the stream it is used on, so that its memory
+    is given on in that stream's order."""
+
+    def __init__(self, dev: torch.device, stream, named):
+        for name, t in named:
+            if t is not None and t.device != dev:
+                raise MesaError(f"{name} is on {t.device}, expected {dev}")
+        if stream is not None and stream.device != dev:
+            raise MesaError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+        self.dev, self.stream = dev, stream
+        self.handle = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        if self.stream is None:
+            return torch.empty(shape, device=self.dev, dtype=dtype)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, device=self.dev, dtype=dtype)
+
+    def result(self, out: Optional[dict], key: str, shape, dtype) -> torch.Tensor:
+        """out[key], checked, or a new tensor."""
+        t = out.get(key) if out else None
+        if t is None:
+            return self.empty(shape, dtype)
+        _need(t, key, shape, dtype)
+        if t.device != self.dev:
+            raise MesaError(f"{key} is on {t.device}, expected {self.dev}")
+        return t
+
+    def scratch(self, workspace: Optional[torch.Tensor], need: int):
+        """(the workspace or a new one, its bytes)"""
+        if workspace is None:
+            workspace = self.empty(need, torch.uint8)
+        elif not workspace.is_contiguous() or workspace.device != self.dev:
+            raise MesaError(f"workspace must be contiguous and on {self.dev}")
+        return workspace, workspace.numel() * workspace.element_size()
+
+    def call(self, what: str, *args):
+        """The library's function `what` with this device current (launches go to the current device)."""
+        fn = getattr(lib(), what)
+        if self.dev.index == torch.cuda.current_device():
+            code = fn(*args, self.handle)
+        else:
+            with torch.cuda.device(self.dev):
+                code = fn(*args, self.handle)
+        _check(code, what)
+
+
+def _code_of(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.float32:
+        return MESA_F32
+    if t.dtype == torch.bfloat16:
+        return MESA_BF16
+    raise MesaError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _token_stride(named, shape, dtype) -> int:
+    """The common token stride of [..., D] tensors: dense, or equal slices of wider
+    rows (last index contiguous, every leading index of the row-major order)."""
+    ld = None
+    for name, t in named:
+        if not t.is_cuda:
+            raise MesaError(f"{name} must be a device tensor")
+        if tuple(t.shape) != shape:
+            raise MesaError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        if t.dtype != dtype:
+            raise MesaError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.is_contiguous():
+            own = shape[-1]
+        else:
+            own = t.stride(-2) if t.shape[-2] > 1 else (t.stride(0) // t.shape[-2] if t.dim() == 3 else shape[-1])
+            if t.stride(-1) != 1 or own < shape[-1] or (t.dim() == 3 and t.shape[0] > 1 and t.stride(0) != own * t.shape[1]):
+                raise MesaError(f"{name} has strides {tuple(t.stride())}: rows must be slices of one row-major tensor")
+        if ld is not None and own != ld:
+            raise MesaError(f"{name} has token stride {own}, expected {ld}")
+        ld = own
+    return ld
+
+
+def lru_workspace_bytes(B, T, D, *, dtype=torch.bfloat16) -> int:
+    """Scratch bytes of lru_fwd and lru_bwd at these sizes."""
+    desc = LruDesc(B, T, D, D, 1.0, MESA_BF16 if dtype == torch.bfloat16 else MESA_F32)
+    return int(lib().mesa_lru_workspace_bytes(ctypes.byref(desc)))
+
+
+def _lru_setup(x, ga, gi, lam, c, h0, lengths):
+    """The descriptor, by reference, and the workspace bytes, after the checks of the common inputs."""
+    B, T, D = x.shape
+    code = _code_of(x, "x")
+    ld = _token_stride((("x", x), ("ga", ga), ("gi", gi)), (B, T, D), x.dtype)
+    _need(lam, "lam", (D,), torch.float32)
+    if h0 is not None:
+        _need(h0, "h0", (B, D), torch.float32)
+    if lengths is not None:
+        _need(lengths, "lengths", (B,), torch.int32)
+    desc = ctypes.byref(LruDesc(B, T, D, ld, float(c), code))
+    return desc, int(lib().mesa_lru_workspace_bytes(desc))
+
+
+def lru_fwd(x, ga, gi, lam, *, c: float = 8.0, h0=None, lengths=None, return_state: bool = False, out=None,
+            workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gated linear recurrence over whole sequences; x, ga, gi [B, T, D] (fp32 or
+    bf16): dense, or equal slices of one wider row-major tensor.
+
+    a_t = exp(-c softplus(lam) sigmoid(ga_t)), h_t = a_t h_{t-1} +
+    sqrt(1 - a_t^2) sigmoid(gi_t) x_t.  lam [D] fp32; h0 [B, D] fp32 or None;
+    lengths [B] int32 or None (valid tokens; outputs behind them are zeros).
+    Returns a dict with ``y`` [B, T, D] in x's dtype and, with return_state,
+    ``h_final`` [B, D] fp32.  ``workspace`` (lru_workspace_bytes long) keeps the
+    states that ``lru_bwd`` can take over."""
+    B, T, D = x.shape
+    desc, need = _lru_setup(x, ga, gi, lam, c, h0, lengths)
+    go = _Launch(x.device, stream, (("ga", ga), ("gi", gi), ("lam", lam), ("h0", h0), ("lengths", lengths)))
+    res = {"y": go.result(out, "y", (B, T, D), x.dtype)}
+    if return_state:
+        res["h_final"] = go.result(out, "h_final", (B, D), torch.float32)
+    workspace, wbytes = go.scratch(workspace, need)
+    go.call("mesa_lru_fwd", desc, _addr(x), _addr(ga), _addr(gi), _addr(lam), _addr(h0), _addr(lengths),
+            _addr(res["y"]), _addr(res.get("h_final")), _addr(workspace), wbytes)
+    return res
+
+
+def lru_bwd(x, ga, gi, lam, dy, *, c: float = 8.0, h0=None, lengths=None, d_hfinal=None, state_grads: bool = False,
+            out=None, workspace: Optional[torch.Tensor] = None, states_in_workspace: bool = False,
+            stream=None) -> dict:
+    """Gradients of lru_fwd: dy [B, T, D] in x's dtype, d_hfinal [B, D] fp32 or None.
+    Returns ``dx``, ``dga``, ``dgi`` in x's dtype, ``dlam`` [D] fp32 and, with
+    state_grads, ``dh0`` [B, D] fp32.  ``out`` may hold dx, dga and dgi as equal
+    slices of one wider tensor.  states_in_workspace: the forward ran with
+    ``workspace`` and left its states there, so they are not formed again."""
+    B, T, D = x.shape
+    f32 = torch.float32
+    if states_in_workspace and workspace is None:
+        raise MesaError("states_in_workspace needs the forward's workspace")
+    desc, need = _lru_setup(x, ga, gi, lam, c, h0, lengths)
+    _need(dy, "dy", (B, T, D), x.dtype)
+    if d_hfinal is not None:
+        _need(d_hfinal, "d_hfinal", (B, D), f32)
+    given = {key: out.get(key) if out else None for key in ("dx", "dga", "dgi")}
+    go = _Launch(x.device, stream, (("ga", ga), ("gi", gi), ("lam", lam), ("h0", h0), ("lengths", lengths),
+                                    ("dy", dy), ("d_hfinal", d_hfinal), *given.items()))
+    res = {key: go.empty((B, T, D), x.dtype) if t is None else t for key, t in given.items()}
+    ld_grad = _token_stride(res.items(), (B, T, D), x.dtype)
+    res["dlam"] = go.result(out, "dlam", (D,), f32)
+    if state_grads:
+        res["dh0"] = go.result(out, "dh0", (B, D), f32)
+    workspace, wbytes = go.scratch(workspace, need)
+    go.call("mesa_lru_bwd", desc, _addr(x), _addr(ga), _addr(gi), _addr(lam), _addr(h0), _addr(lengths), _addr(dy),
+            _addr(d_hfinal), _addr(res["dx"]), _addr(res["dga"]), _addr(res["dgi"]), ld_grad, _addr(res["dlam"]),
+            _addr(res.get("dh0")), 1 if states_in_workspace else 0, _addr(workspace), wbytes)
+    return res
+
+
+def lru_step(x, ga, gi, lam, h_state, *, c: float = 8.0, out=None, stream=None) -> dict:
+    """One token of N sequences: x, ga, gi [N, D] (rows dense or slices of wider
+    ones), h_state [N, D] fp32 updated in place.  Returns ``y`` [N, D] in x's dtype."""
+    N, D = x.shape
+    code = _code_of(x, "x")
+    ld = _token_stride((("x", x), ("ga", ga), ("gi", gi)), (N, D), x.dtype)
+    _need(lam, "lam", (D,), torch.float32)
+    _need(h_state, "h_state", (N, D), torch.float32)
+    go = _Launch(x.device, stream, (("ga", ga), ("gi", gi), ("lam", lam), ("h_state", h_state)))
+    res = {"y": go.result(out, "y", (N, D), x.dtype)}
+    go.call("mesa_lru_step", N, D, ld, float(c), code, _addr(x), _addr(ga), _addr(gi), _addr(lam), _addr(h_state),
+            _addr(res["y"]))
     return res

@@ -163,8 +163,8 @@ MUTATIONS = {
     "adjoint_not_decayed": ("after[L] = a[L, t] * g", "after[L] = g"),
     "decay_gradient_current_state": ("a[L, t] * prev[L, t])", "a[L, t] * (a[L, t] * prev[L, t] + m[L, t] * si[L, t] * x[L, t]))"),
     "decay_gradient_without_input_scale": ("(ratio * si[L, t] * x[L, t] - ", "(0 * ratio * si[L, t] * x[L, t] - "),
-    "gate_gradient_slope": ("v * (1.0 - sr[L, t])", "v * sr[L, t]"),
-    "input_gate_gradient_slope": ("si[L, t] * (1.0 - si[L, t])", "(1.0 - si[L, t])"),
+    "gate_gradient_slope": ("v * sr1[L, t]", "v * (1.0 - sr1[L, t])"),
+    "input_gate_gradient_slope": ("si[L, t] * si1[L, t]", "si1[L, t]"),
     "lam_gradient_slope": ("dloglam * _sigmoid(lam) / _softplus(lam)", "dloglam / _softplus(lam)"),
     "norm_eps_outside_root": ("np.sqrt((s * s).mean(1, keepdims=True) + eps)\n    out",
                               "(np.sqrt((s * s).mean(1, keepdims=True)) + eps)\n    out"),
