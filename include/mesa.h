@@ -560,6 +560,99 @@ mesa_status mesa_lru_step(int32_t N, int32_t D, int32_t ld, float c, mesa_dtype 
                           const void* x, const void* ga, const void* gi, const float* lam,
                           float* h_state, void* y, hipStream_t stream);
 
+/* ---- residual addition and RMS norm ---------------------------------------------
+ *
+ * MesaNet page, "architecture" section: residual blocks, each holding a Mesa
+ * layer (or, in the hybrid, the gated linear recurrence) and an MLP.  In front
+ * of either, row by row of the R tokens,
+ *
+ *   s = x + residual,   y = w s / sqrt(mean(s^2) + eps)
+ *
+ *   x            [R, D] dtype           the last layer's output
+ *   residual     [R, D] res_dtype or NULL (s = x)
+ *   w            [D] fp32
+ *   eps          >= 2^-126, finite
+ *   out          MESA_NORM_OUT_DTYPE: y [R, D] in dtype; scale is not used
+ *                MESA_NORM_OUT_E4M3: y [R, D] holds e4m3 bytes (4 exponent and
+ *                3 mantissa bits, largest value 448, as the matrix cores take
+ *                them) of y / scale, and scale [R, groups] fp32 the scales:
+ *                max|y| / 448 over the row (group = 0, one scale) or over each
+ *                128 consecutive channels (group = 128, ceil(D/128) scales;
+ *                the last may cover fewer).  max|y| counts as at least 2^-100,
+ *                so a row of zeros has a finite scale
+ *   residual_out [R, D] res_dtype or NULL: s, the stream behind the addition.
+ *                May be residual itself, or x when the types are equal
+ *
+ * s, the mean and y are fp32; s is normalised before it is rounded to
+ * res_dtype.  Rounding is to nearest even, y / scale being formed as
+ * y * (448 / max|y|).  Rows are independent; a row whose squares overflow fp32
+ * (or that holds infinities or NaN) gives unspecified values in that row.
+ * Supported: 1 <= D <= 32768, R >= 0, R D <= 2^40, (dtype, res_dtype) of (f32,
+ * f32), (bf16, bf16), (bf16, f32). */
+typedef enum { MESA_NORM_OUT_DTYPE = 0, MESA_NORM_OUT_E4M3 = 1 } mesa_norm_out;
+
+mesa_status mesa_rmsnorm(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_dtype,
+                         const void* x, const void* residual, const float* w, float eps,
+                         mesa_norm_out out, int32_t group, void* y, float* scale,
+                         void* residual_out, hipStream_t stream);
+
+/* Gradients of mesa_rmsnorm (its y in dtype) at s and w.  With r = 1 / sqrt(mean(s^2)
+ * + eps), n = s r and g = dy w:
+ *   ds = r (g - n mean(g n)) + d_residual,    dw = sum_rows dy n.
+ *
+ *   s          [R, D] res_dtype  the stream the forward left (residual_out)
+ *   dy         [R, D] dtype
+ *   d_residual [R, D] res_dtype or NULL (zero): what reaches s along the
+ *              residual stream
+ *   ds         [R, D] res_dtype out: the gradient of the residual and of x.
+ *              May be d_residual itself
+ *   dx         [R, D] dtype out or NULL: ds rounded to x's type, for a bf16 x
+ *              on an fp32 stream
+ *   dw         [D] fp32 out, summed in a fixed order
+ *   workspace  mesa_rmsnorm_bwd_workspace_bytes(R, D) bytes
+ * Sizes and types as in mesa_rmsnorm. */
+size_t mesa_rmsnorm_bwd_workspace_bytes(int32_t R, int32_t D);
+
+mesa_status mesa_rmsnorm_bwd(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_dtype,
+                             const void* s, const float* w, const void* dy, const void* d_residual,
+                             float eps, void* ds, void* dx, float* dw,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---- gradient of the query/key preprocessing ---------------------------------------
+ *
+ * Gradients of mesa_qk_preprocess (MesaNet page, "architecture" section), from
+ * those of the layer's q and k (the dq and dk of mesa_bwd_chunked) to the raw
+ * projections and the taps.  With y_t = sum_i w_i x_{t-i}, n = ||y_t|| and
+ * o = y_t / max(n, eps), for queries and keys alike,
+ *   e_t = (d_t - o <o, d_t>) / n  where n > eps,   d_t / eps  elsewhere,
+ *   dx_s = sum_i w_i e_{s+i}  (s + i < T; s runs over the history rows too),
+ *   dw[h][j][i] = sum_{b,t} e_t[j] x_{t-i}[j].
+ *
+ *   q_raw .. eps     the forward's arguments (no outputs of it are needed)
+ *   d_q, d_k         [B, H, T, d] fp32
+ *   d_q_hist_out, d_k_hist_out  [B, H, window-1, d] dtype or NULL (zero): what
+ *                    reaches the history outputs, the dq_hist, dk_hist of the
+ *                    call that continued the sequence; added to the raw rows
+ *                    they are copies of
+ *   dq_raw, dk_raw   [B, H, T, d] dtype out
+ *   dw_q, dw_k       [H, d, window] fp32 out, summed in a fixed order
+ *   dq_hist, dk_hist [B, H, window-1, d] dtype out or NULL
+ *   workspace        mesa_qk_preprocess_bwd_workspace_bytes(...) bytes
+ * Sizes as in mesa_qk_preprocess, B >= 1.  dq_raw, dk_raw, dq_hist and dk_hist
+ * may not overlap the inputs (MESA_ERR_INVALID_ARG). */
+size_t mesa_qk_preprocess_bwd_workspace_bytes(int32_t B, int32_t H, int32_t T, int32_t d,
+                                              int32_t window, mesa_dtype dtype);
+
+mesa_status mesa_qk_preprocess_bwd(int32_t B, int32_t H, int32_t T, int32_t d, int32_t window,
+                                   mesa_dtype dtype, const void* q_raw, const void* k_raw,
+                                   const float* w_q, const float* w_k,
+                                   const void* q_hist, const void* k_hist, float eps,
+                                   const float* d_q, const float* d_k,
+                                   const void* d_q_hist_out, const void* d_k_hist_out,
+                                   void* dq_raw, void* dk_raw, float* dw_q, float* dw_k,
+                                   void* dq_hist, void* dk_hist,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Static text for a status code. */
 const char* mesa_status_string(mesa_status s);
 

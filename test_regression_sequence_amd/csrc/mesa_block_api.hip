@@ -108,3 +108,128 @@ mesa_status mesa_lru_step(int32_t N, int32_t D, int32_t ld, float c, mesa_dtype 
 }
 
 }  // extern "C"
+
+// ---- residual RMS norm ------------------------------------------------------
+
+namespace {
+
+mesa_status check_norm(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_dtype, float eps) {
+  if (R < 0 || D < 1 || !dtype_ok(dtype) || !dtype_ok(res_dtype)) return MESA_ERR_INVALID_ARG;
+  if (!(eps >= 0x1p-126f) || std::isinf(eps)) return MESA_ERR_INVALID_ARG;
+  if (D > 32768 || (double)R * D > (double)(1LL << 40)) return MESA_ERR_UNSUPPORTED;
+  if (dtype == MESA_F32 && res_dtype == MESA_BF16) return MESA_ERR_UNSUPPORTED;
+  return MESA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mesa_status mesa_rmsnorm(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_dtype, const void* x,
+                         const void* residual, const float* w, float eps, mesa_norm_out out, int32_t group, void* y,
+                         float* scale, void* residual_out, hipStream_t stream) {
+  const mesa_status st = check_norm(R, D, dtype, res_dtype, eps);
+  if (st != MESA_OK) return st;
+  if (out != MESA_NORM_OUT_DTYPE && out != MESA_NORM_OUT_E4M3) return MESA_ERR_INVALID_ARG;
+  const bool e4m3 = out == MESA_NORM_OUT_E4M3;
+  if (e4m3 && group < 0) return MESA_ERR_INVALID_ARG;
+  if (e4m3 && group != 0 && group != 128) return MESA_ERR_UNSUPPORTED;
+  if (R == 0) return MESA_OK;
+  if (!x || !w || !y || (e4m3 && !scale)) return MESA_ERR_INVALID_ARG;
+  if (!all_aligned({x, residual, w, y, scale, residual_out})) return MESA_ERR_ALIGNMENT;
+  mesa::NormParams p{};
+  p.x = x; p.residual = residual; p.w = w; p.y = y; p.scale = scale; p.residual_out = residual_out;
+  p.R = R; p.D = D; p.eps = eps; p.e4m3 = e4m3 ? 1 : 0; p.group = e4m3 ? group : 0;
+  return mesa::launch_rmsnorm(dtype == MESA_BF16, res_dtype == MESA_BF16, p, stream) == hipSuccess ? MESA_OK
+                                                                                                   : MESA_ERR_HIP;
+}
+
+size_t mesa_rmsnorm_bwd_workspace_bytes(int32_t R, int32_t D) {
+  if (check_norm(R, D, MESA_F32, MESA_F32, 1.f) != MESA_OK || R == 0) return 0;
+  return mesa::rmsnorm_bwd_scratch(R, D);
+}
+
+mesa_status mesa_rmsnorm_bwd(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_dtype, const void* s,
+                             const float* w, const void* dy, const void* d_residual, float eps, void* ds, void* dx,
+                             float* dw, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const mesa_status st = check_norm(R, D, dtype, res_dtype, eps);
+  if (st != MESA_OK) return st;
+  if (!dw || (R > 0 && (!s || !w || !dy || !ds))) return MESA_ERR_INVALID_ARG;
+  if (!all_aligned({s, w, dy, d_residual, ds, dx, dw, workspace})) return MESA_ERR_ALIGNMENT;
+  const size_t need = mesa_rmsnorm_bwd_workspace_bytes(R, D);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MESA_ERR_WORKSPACE;
+  mesa::NormParams p{};
+  p.x = s; p.residual = d_residual; p.w = w; p.dy = dy; p.y = ds; p.residual_out = dx; p.dw = dw; p.part = workspace;
+  p.R = R; p.D = D; p.eps = eps;
+  return mesa::launch_rmsnorm_bwd(dtype == MESA_BF16, res_dtype == MESA_BF16, p, stream) == hipSuccess ? MESA_OK
+                                                                                                       : MESA_ERR_HIP;
+}
+
+}  // extern "C"
+
+// ---- gradient of the query/key preprocessing -----------------------------------
+
+namespace {
+
+mesa_status check_prep(int32_t B, int32_t H, int32_t T, int32_t d, int32_t window, mesa_dtype dtype) {
+  if (B < 1 || H < 1 || T < 0 || window < 1 || !dtype_ok(dtype)) return MESA_ERR_INVALID_ARG;
+  if ((d != 16 && d != 64 && d != 128) || window > 4) return MESA_ERR_UNSUPPORTED;
+  if ((long long)B * H > 65535) return MESA_ERR_UNSUPPORTED;
+  return MESA_OK;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b || na == 0 || nb == 0) return false;
+  const char* pa = static_cast<const char*>(a);
+  const char* pb = static_cast<const char*>(b);
+  return pa < pb + nb && pb < pa + na;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mesa_qk_preprocess_bwd_workspace_bytes(int32_t B, int32_t H, int32_t T, int32_t d, int32_t window,
+                                              mesa_dtype dtype) {
+  if (check_prep(B, H, T, d, window, dtype) != MESA_OK || T == 0) return 0;
+  return mesa::qk_prep_bwd_scratch(B * H, T, d, window);
+}
+
+mesa_status mesa_qk_preprocess_bwd(int32_t B, int32_t H, int32_t T, int32_t d, int32_t window, mesa_dtype dtype,
+                                   const void* q_raw, const void* k_raw, const float* w_q, const float* w_k,
+                                   const void* q_hist, const void* k_hist, float eps, const float* d_q,
+                                   const float* d_k, const void* d_q_hist_out, const void* d_k_hist_out,
+                                   void* dq_raw, void* dk_raw, float* dw_q, float* dw_k, void* dq_hist, void* dk_hist,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const mesa_status st = check_prep(B, H, T, d, window, dtype);
+  if (st != MESA_OK) return st;
+  // the forward's rule: finite and at least 2^-63
+  if (!(eps >= 0x1p-63f) || std::isinf(eps)) return MESA_ERR_INVALID_ARG;
+  if (!w_q || !w_k || !dw_q || !dw_k) return MESA_ERR_INVALID_ARG;
+  if (T > 0 && (!q_raw || !k_raw || !d_q || !d_k || !dq_raw || !dk_raw)) return MESA_ERR_INVALID_ARG;
+  if (!all_aligned({q_raw, k_raw, w_q, w_k, q_hist, k_hist, d_q, d_k, d_q_hist_out, d_k_hist_out, dq_raw, dk_raw, dw_q,
+                    dw_k, dq_hist, dk_hist, workspace}))
+    return MESA_ERR_ALIGNMENT;
+  const size_t need = mesa_qk_preprocess_bwd_workspace_bytes(B, H, T, d, window, dtype);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MESA_ERR_WORKSPACE;
+  // every input row is read by up to `window` output rows
+  const size_t esz = dtype == MESA_BF16 ? 2 : 4;
+  const size_t seq = (size_t)B * H * T * d, hist = (size_t)B * H * (window - 1) * d;
+  const void* ins[] = {q_raw, k_raw, d_q, d_k, q_hist, k_hist, d_q_hist_out, d_k_hist_out};
+  const size_t in_bytes[] = {seq * esz, seq * esz, seq * 4, seq * 4, hist * esz, hist * esz, hist * esz, hist * esz};
+  const void* outs[] = {dq_raw, dk_raw, dq_hist, dk_hist};
+  const size_t out_bytes[] = {seq * esz, seq * esz, hist * esz, hist * esz};
+  for (int a = 0; a < 4; ++a)
+    for (int b = 0; b < 8; ++b)
+      if (overlap(outs[a], out_bytes[a], ins[b], in_bytes[b])) return MESA_ERR_INVALID_ARG;
+
+  mesa::PrepBwdParams p{};
+  p.x[0] = q_raw; p.x[1] = k_raw; p.w[0] = w_q; p.w[1] = w_k; p.hist_in[0] = q_hist; p.hist_in[1] = k_hist;
+  p.d[0] = d_q; p.d[1] = d_k; p.d_hist[0] = d_q_hist_out; p.d_hist[1] = d_k_hist_out;
+  p.dx[0] = dq_raw; p.dx[1] = dk_raw; p.dw[0] = dw_q; p.dw[1] = dw_k; p.dhist[0] = dq_hist; p.dhist[1] = dk_hist;
+  p.part = static_cast<float*>(workspace);
+  p.BH = B * H; p.H = H; p.T = T; p.W = window; p.inv_eps = 1.0f / eps;
+  return mesa::launch_qk_prep_bwd(dtype == MESA_BF16, d, p, stream) == hipSuccess ? MESA_OK : MESA_ERR_HIP;
+}
+
+}  // extern "C"

@@ -149,6 +149,37 @@ struct LruParams {
   float c;
 };
 
+// Residual addition and RMS norm over R rows of D channels.
+struct NormParams {
+  const void* x;            // forward: [R, D]; backward: the stream s [R, D]
+  const void* residual;     // forward: or null; backward: d_residual, or null
+  const float* w;           // [D]
+  const void* dy;           // backward: [R, D]
+  void* y;                  // forward: [R, D], or e4m3 bytes; backward: ds [R, D]
+  float* scale;             // [R, groups]
+  void* residual_out;       // forward: [R, D] or null; backward: dx [R, D] or null
+  float* dw;                // backward: [D]
+  void* part;               // backward: scratch
+  int R, D;
+  float eps;
+  int e4m3, group;
+};
+
+// Gradient of the query/key preprocessing: index 0 = queries, 1 = keys.
+struct PrepBwdParams {
+  const void* x[2];         // raw [BH, T, D]
+  const float* w[2];        // taps [H, D, W]
+  const void* hist_in[2];   // [BH, W-1, D] or null
+  const float* d[2];        // gradients at the outputs [BH, T, D]
+  const void* d_hist[2];    // gradients at the history outputs [BH, W-1, D] or null
+  void* dx[2];              // [BH, T, D]
+  float* dw[2];             // [H, D, W]
+  void* dhist[2];           // [BH, W-1, D] or null
+  float* part;              // scratch
+  int BH, H, T, W;
+  float inv_eps;
+};
+
 // Backward pass (bf16 inputs, chunk 64).
 struct BwdParams {
   const void* k;            // [BH, T, D] bf16
@@ -223,6 +254,11 @@ hipError_t launch_lru_fwd(bool bf16, const LruParams& p, hipStream_t s);
 // gradients, from the states launch_lru_fwd left
 hipError_t launch_lru_bwd(bool bf16, const LruParams& p, hipStream_t s);
 hipError_t launch_lru_step(bool bf16, const LruParams& p, hipStream_t s);
+hipError_t launch_rmsnorm(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s);
+hipError_t launch_rmsnorm_bwd(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s);
+size_t rmsnorm_bwd_scratch(int R, int D);
+hipError_t launch_qk_prep_bwd(bool bf16, int D, const PrepBwdParams& p, hipStream_t s);
+size_t qk_prep_bwd_scratch(int BH, int T, int D, int W);
 
 // Bytes of one (b, h, chunk) boundary snapshot of H (or of G).
 inline size_t snapshot_bytes(bool bf16, int D) { return (size_t)D * D * (bf16 ? 2 : 4); }

@@ -18,6 +18,8 @@ __all__ = [
     "workspace_bytes", "fwd_chunked", "fwd_chunked_noalloc", "fwd_chunked_prep", "fwd_scan", "fwd_solve", "decode_step", "abi_version",
     "status_string", "sym_state_floats", "sym_pack", "sym_unpack", "decode_step_symh",
     "lru_workspace_bytes", "lru_fwd", "lru_bwd", "lru_step",
+    "rmsnorm", "rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes",
+    "qk_preprocess_bwd", "qk_preprocess_bwd_workspace_bytes",
 ]
 
 MESA_F32 = 0
@@ -114,6 +116,17 @@ def lib() -> ctypes.CDLL:
         L.mesa_lru_bwd.argtypes = [D] + [P] * 11 + [I32, P, P, I32, P, S, P]
         L.mesa_lru_step.restype = ctypes.c_int
         L.mesa_lru_step.argtypes = [I32, I32, I32, F, ctypes.c_int] + [P] * 7
+        L.mesa_rmsnorm.restype = ctypes.c_int
+        L.mesa_rmsnorm.argtypes = [I32, I32, ctypes.c_int, ctypes.c_int, P, P, P, F, ctypes.c_int, I32, P, P, P, P]
+        L.mesa_rmsnorm_bwd_workspace_bytes.restype = S
+        L.mesa_rmsnorm_bwd_workspace_bytes.argtypes = [I32, I32]
+        L.mesa_rmsnorm_bwd.restype = ctypes.c_int
+        L.mesa_rmsnorm_bwd.argtypes = [I32, I32, ctypes.c_int, ctypes.c_int, P, P, P, P, F, P, P, P, P, S, P]
+        L.mesa_qk_preprocess_bwd_workspace_bytes.restype = S
+        L.mesa_qk_preprocess_bwd_workspace_bytes.argtypes = [I32, I32, I32, I32, I32, ctypes.c_int]
+        L.mesa_qk_preprocess_bwd.restype = ctypes.c_int
+        L.mesa_qk_preprocess_bwd.argtypes = ([I32, I32, I32, I32, I32, ctypes.c_int] + [P] * 6 + [F] + [P] * 11
+                                             + [S, P])
         _LIB = L
     return _LIB
 
@@ -752,4 +765,108 @@ def lru_step(x, ga, gi, lam, h_state, *, c: float = 8.0, out=None, stream=None) 
     res = {"y": go.result(out, "y", (N, D), x.dtype)}
     go.call("mesa_lru_step", N, D, ld, float(c), code, _addr(x), _addr(ga), _addr(gi), _addr(lam), _addr(h_state),
             _addr(res["y"]))
+    return res
+
+
+def rmsnorm(x, w, *, residual=None, eps: float = 1e-6, quant_group: Optional[int] = None,
+            return_residual: Optional[bool] = None, out=None, stream=None) -> dict:
+    """Residual addition and RMS norm of the rows of x [R, D] (fp32 or bf16):
+    s = x + residual, y = w s / sqrt(mean(s^2) + eps).  w [D] fp32; residual
+    [R, D] in x's dtype or fp32, or None.
+
+    quant_group None: ``y`` in x's dtype.  0 or 128: ``y`` as
+    ``torch.float8_e4m3fn`` with fp32 ``scale`` [R, 1] (per row) or
+    [R, ceil(D/128)] (per 128 channels).  ``residual`` is s in the residual's
+    dtype (return_residual; default: when a residual is given).  ``out`` may pass
+    result tensors; out["residual"] may be the residual itself."""
+    R, D = x.shape
+    code = _code_of(x, "x")
+    _need(x, "x", (R, D))
+    _need(w, "w", (D,), torch.float32)
+    res_dtype = x.dtype if residual is None else residual.dtype
+    if residual is not None:
+        _need(residual, "residual", (R, D))
+    go = _Launch(x.device, stream, (("w", w), ("residual", residual)))
+    res = {"y": go.result(out, "y", (R, D), x.dtype if quant_group is None else torch.float8_e4m3fn)}
+    if quant_group is not None:
+        groups = -(-D // quant_group) if quant_group > 0 else 1
+        res["scale"] = go.result(out, "scale", (R, groups), torch.float32)
+    if return_residual if return_residual is not None else residual is not None:
+        res["residual"] = go.result(out, "residual", (R, D), res_dtype)
+    go.call("mesa_rmsnorm", R, D, code, code if residual is None else _code_of(residual, "residual"), _addr(x),
+            _addr(residual), _addr(w), float(eps), 0 if quant_group is None else 1, quant_group or 0, _addr(res["y"]),
+            _addr(res.get("scale")), _addr(res.get("residual")))
+    return res
+
+
+def rmsnorm_bwd_workspace_bytes(R, D) -> int:
+    """Scratch bytes of rmsnorm_bwd."""
+    return int(lib().mesa_rmsnorm_bwd_workspace_bytes(R, D))
+
+
+def rmsnorm_bwd(s, w, dy, *, d_residual=None, eps: float = 1e-6, out=None,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of rmsnorm at s [R, D] (the ``residual`` it returned, or x where
+    there was none) and w: dy [R, D]; d_residual [R, D] in s's dtype or None, what
+    reaches s along the residual stream.  Returns ``ds`` in s's dtype (the gradient
+    of the residual and of x), ``dw`` [D] fp32 and, where dy is bf16 and s fp32,
+    ``dx``: ds in bf16.  out["ds"] may be d_residual itself."""
+    R, D = s.shape
+    _need(s, "s", (R, D))
+    _need(w, "w", (D,), torch.float32)
+    _need(dy, "dy", (R, D))
+    if d_residual is not None:
+        _need(d_residual, "d_residual", (R, D), s.dtype)
+    go = _Launch(s.device, stream, (("w", w), ("dy", dy), ("d_residual", d_residual)))
+    res = {"ds": go.result(out, "ds", (R, D), s.dtype), "dw": go.result(out, "dw", (D,), torch.float32)}
+    if dy.dtype != s.dtype:
+        res["dx"] = go.result(out, "dx", (R, D), dy.dtype)
+    workspace, wbytes = go.scratch(workspace, rmsnorm_bwd_workspace_bytes(R, D))
+    go.call("mesa_rmsnorm_bwd", R, D, _code_of(dy, "dy"), _code_of(s, "s"), _addr(s), _addr(w), _addr(dy),
+            _addr(d_residual), float(eps), _addr(res["ds"]), _addr(res.get("dx")), _addr(res["dw"]), _addr(workspace),
+            wbytes)
+    return res
+
+
+def qk_preprocess_bwd_workspace_bytes(B, H, T, d, window, *, dtype=torch.bfloat16) -> int:
+    """Scratch bytes of qk_preprocess_bwd."""
+    code = MESA_BF16 if dtype == torch.bfloat16 else MESA_F32
+    return int(lib().mesa_qk_preprocess_bwd_workspace_bytes(B, H, T, d, window, code))
+
+
+def qk_preprocess_bwd(q_raw, k_raw, w_q, w_k, d_q, d_k, *, q_hist=None, k_hist=None, d_q_hist_out=None,
+                      d_k_hist_out=None, eps: float = 1e-6, history_grads: bool = False, out=None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of qk_preprocess: d_q, d_k [B, H, T, d] fp32 at its outputs (bwd_chunked's
+    dq and dk), d_q_hist_out, d_k_hist_out [B, H, W-1, d] at its history outputs or None.
+    Returns ``dq_raw``, ``dk_raw`` in the raw dtype, ``dw_q``, ``dw_k`` [H, d, W] fp32 and,
+    with history_grads, ``dq_hist``, ``dk_hist``."""
+    B, H, T, d = q_raw.shape
+    W = w_q.shape[-1]
+    dt, f32 = q_raw.dtype, torch.float32
+    code = _code_of(q_raw, "q_raw")
+    named = {"q_raw": q_raw, "k_raw": k_raw, "w_q": w_q, "w_k": w_k, "d_q": d_q, "d_k": d_k, "q_hist": q_hist,
+             "k_hist": k_hist, "d_q_hist_out": d_q_hist_out, "d_k_hist_out": d_k_hist_out}
+    for name, t in named.items():
+        if t is None:
+            continue
+        if name in ("q_raw", "k_raw"):
+            _need(t, name, (B, H, T, d), dt)
+        elif name in ("d_q", "d_k"):
+            _need(t, name, (B, H, T, d), f32)
+        elif name in ("w_q", "w_k"):
+            _need(t, name, (H, d, W), f32)
+        else:
+            _need(t, name, (B, H, W - 1, d), dt)
+    go = _Launch(q_raw.device, stream, named.items())
+    res = {key: go.result(out, key, (B, H, T, d), dt) for key in ("dq_raw", "dk_raw")}
+    res.update((key, go.result(out, key, (H, d, W), f32)) for key in ("dw_q", "dw_k"))
+    if history_grads:
+        res.update((key, go.result(out, key, (B, H, W - 1, d), dt)) for key in ("dq_hist", "dk_hist"))
+    need = int(lib().mesa_qk_preprocess_bwd_workspace_bytes(B, H, T, d, W, code))
+    workspace, wbytes = go.scratch(workspace, need)
+    go.call("mesa_qk_preprocess_bwd", B, H, T, d, W, code, _addr(q_raw), _addr(k_raw), _addr(w_q), _addr(w_k),
+            _addr(q_hist), _addr(k_hist), float(eps), _addr(d_q), _addr(d_k), _addr(d_q_hist_out),
+            _addr(d_k_hist_out), _addr(res["dq_raw"]), _addr(res["dk_raw"]), _addr(res["dw_q"]), _addr(res["dw_k"]),
+            _addr(res.get("dq_hist")), _addr(res.get("dk_hist")), _addr(workspace), wbytes)
     return res

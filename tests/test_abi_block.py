@@ -91,3 +91,90 @@ def test_lru_step_validation():
     for name in ("x", "ga", "gi", "lam", "h", "y"):
         assert call(**{name: 0}) == 1
         assert call(**{name: FAKE + 2}) == 3
+
+
+def call_norm(R=4, D=100, dtype=1, res=1, eps=1e-6, out=0, group=0, **kw):
+    a = dict(x=FAKE, residual=FAKE, w=FAKE)
+    b = dict(y=FAKE, scale=0, residual_out=0)
+    for k, v in kw.items():
+        (a if k in a else b)[k] = v
+    p = lambda m: [P(v) if v else None for v in m.values()]  # noqa: E731
+    return mesa.lib().mesa_rmsnorm(R, D, dtype, res, *p(a), ctypes.c_float(eps), out, group, *p(b), None)
+
+
+def call_norm_bwd(R=4, D=100, dtype=1, res=1, eps=1e-6, wbytes=1 << 40, workspace=FAKE, **kw):
+    a = dict(s=FAKE, w=FAKE, dy=FAKE, d_residual=0)
+    b = dict(ds=FAKE, dx=0, dw=FAKE)
+    for k, v in kw.items():
+        (a if k in a else b)[k] = v
+    p = lambda m: [P(v) if v else None for v in m.values()]  # noqa: E731
+    return mesa.lib().mesa_rmsnorm_bwd(R, D, dtype, res, *p(a), ctypes.c_float(eps), *p(b),
+                                       P(workspace) if workspace else None, wbytes, None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(R=-1), 1), (dict(D=0), 1), (dict(dtype=2), 1), (dict(res=-1), 1), (dict(eps=0.0), 1), (dict(eps=-1.0), 1),
+    (dict(eps=2.0 ** -127), 1), (dict(eps=float("inf")), 1), (dict(eps=float("nan")), 1), (dict(D=32769), 2),
+    (dict(dtype=0, res=1), 2), (dict(R=2 ** 31 - 1, D=32768), 2),
+])
+def test_norm_rejects_bad_sizes_and_types(kw, expect):
+    assert call_norm(**kw) == expect
+    assert call_norm_bwd(**kw) == expect
+
+
+def test_norm_rejects_missing_and_misaligned_pointers():
+    for name in ("x", "w", "y"):
+        assert call_norm(**{name: 0}) == 1, name
+    for name in ("x", "residual", "w", "y", "scale", "residual_out"):
+        assert call_norm(**{name: FAKE + 4}) == 3, name
+    assert call_norm(out=2) == 1
+    assert call_norm(out=1) == 1                       # e4m3 needs scales
+    assert call_norm(out=1, scale=FAKE, group=-1) == 1
+    assert call_norm(out=1, scale=FAKE, group=64) == 2
+    assert call_norm(R=0, x=0) == 0                    # nothing to do, nothing launched
+    for name in ("s", "w", "dy", "ds", "dw"):
+        assert call_norm_bwd(**{name: 0}) == 1, name
+    for name in ("s", "w", "dy", "d_residual", "ds", "dx", "dw", "workspace"):
+        assert call_norm_bwd(**{name: FAKE + 8}) == 3, name
+    need = mesa.lib().mesa_rmsnorm_bwd_workspace_bytes(4, 100)
+    assert need > 0
+    assert call_norm_bwd(wbytes=need - 1) == 4
+    assert call_norm_bwd(workspace=0) == 4
+    assert mesa.lib().mesa_rmsnorm_bwd_workspace_bytes(-1, 100) == 0
+
+
+def test_preprocess_backward_validation():
+    L = mesa.lib()
+    A, G, O = 0x7F0000000000, 0x7F1000000000, 0x7F2000000000   # distinct 16-byte aligned fake ranges
+    M = 0x100000
+
+    def call(B=2, H=2, T=8, d=128, W=4, dtype=1, eps=1e-6, workspace=A + 32 * M, wbytes=1 << 40, **kw):
+        ins = dict(q=A, k=A + M, wq=A + 2 * M, wk=A + 3 * M, qh=0, kh=0)
+        gin = dict(dq=G, dk=G + M, dqh=0, dkh=0)
+        outs = dict(dqr=O, dkr=O + M, dwq=O + 2 * M, dwk=O + 3 * M, dqhist=0, dkhist=0)
+        for k, v in kw.items():
+            next(m for m in (ins, gin, outs) if k in m)[k] = v
+        p = lambda m: [P(v) if v else None for v in m.values()]  # noqa: E731
+        return L.mesa_qk_preprocess_bwd(B, H, T, d, W, dtype, *p(ins), ctypes.c_float(eps), *p(gin), *p(outs),
+                                        P(workspace) if workspace else None, wbytes, None)
+
+    need = L.mesa_qk_preprocess_bwd_workspace_bytes(2, 2, 8, 128, 4, 1)
+    assert need > 0 and L.mesa_qk_preprocess_bwd_workspace_bytes(2, 2, 0, 128, 4, 1) == 0
+    assert call(d=96) == 2
+    assert call(W=5) == 2
+    assert call(B=65536, H=1) == 2
+    assert call(W=0) == 1
+    assert call(B=0) == 1
+    assert call(T=-1) == 1
+    assert call(dtype=3) == 1
+    for eps in (0.0, 2.0 ** -64, float("inf"), float("nan")):
+        assert call(eps=eps) == 1
+    for name in ("q", "k", "wq", "wk", "dq", "dk", "dqr", "dkr", "dwq", "dwk"):
+        assert call(**{name: 0}) == 1, name
+    for name in ("q", "k", "wq", "wk", "qh", "kh", "dq", "dk", "dqh", "dkh", "dqr", "dkr", "dwq", "dwk", "dqhist", "dkhist"):
+        assert call(**{name: O + 8 * M + 4}) == 3, name
+    assert call(dqr=A) == 1               # over the raw input
+    assert call(dkr=G) == 1               # over the incoming gradient
+    assert call(qh=A + 4 * M, dqhist=A + 4 * M) == 1
+    assert call(workspace=0) == 4
+    assert call(wbytes=need - 1) == 4
