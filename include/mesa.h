@@ -587,7 +587,7 @@ mesa_status mesa_lru_step(int32_t N, int32_t D, int32_t ld, float c, mesa_dtype 
  * res_dtype.  Rounding is to nearest even, y / scale being formed as
  * y * (448 / max|y|).  Rows are independent; a row whose squares overflow fp32
  * (or that holds infinities or NaN) gives unspecified values in that row.
- * Supported: 1 <= D <= 32768, R >= 0, R D <= 2^40, (dtype, res_dtype) of (f32,
+ * Supported: 1 <= D <= 16384, R >= 0, R D <= 2^40, (dtype, res_dtype) of (f32,
  * f32), (bf16, bf16), (bf16, f32). */
 typedef enum { MESA_NORM_OUT_DTYPE = 0, MESA_NORM_OUT_E4M3 = 1 } mesa_norm_out;
 

@@ -116,7 +116,7 @@ namespace {
 mesa_status check_norm(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_dtype, float eps) {
   if (R < 0 || D < 1 || !dtype_ok(dtype) || !dtype_ok(res_dtype)) return MESA_ERR_INVALID_ARG;
   if (!(eps >= 0x1p-126f) || std::isinf(eps)) return MESA_ERR_INVALID_ARG;
-  if (D > 32768 || (double)R * D > (double)(1LL << 40)) return MESA_ERR_UNSUPPORTED;
+  if (D > 16384 || (double)R * D > (double)(1LL << 40)) return MESA_ERR_UNSUPPORTED;
   if (dtype == MESA_F32 && res_dtype == MESA_BF16) return MESA_ERR_UNSUPPORTED;
   return MESA_OK;
 }

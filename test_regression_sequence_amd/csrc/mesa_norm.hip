@@ -2,134 +2,347 @@
 // and its gradient (MesaNet page, "architecture": the residual blocks' norm).
 //     s = x + residual,  r = 1 / sqrt(mean(s^2) + eps),  y = w s r
 //     ds = r (g - n mean(g n)) + d_residual,  g = dy w,  n = s r,  dw = sum_rows dy n
+//
+// Both are bound by HBM: every input is read once and every output written
+// once.  A row is held in registers by TPR lanes of NV vectors of 8 channels
+// each, from its loads to its stores, so nothing is read twice; the smallest
+// (TPR, NV) that covers D is taken, which keeps lanes busy and, up to D = 2048,
+// a row within one wave (its sums then need no LDS and no barrier).  Row groups
+// walk rows a grid apart and load the next row before they work on this one;
+// w, and the backward's sums for dw, stay in their registers meanwhile.
+#include <type_traits>
+
 #include "mesa_common.h"
 #include "mesa_kernels.h"
+#include "mesa_rows.h"
 
 namespace mesa {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr float kE4m3Max = 448.f;
 constexpr float kAmaxFloor = 0x1p-100f;
-constexpr int kGroup = 128;
+constexpr int kCus = 256;
 
-template <bool BF16>
-__device__ __forceinline__ void store1(void* base, size_t idx, float v) {
-  if constexpr (BF16) {
-    static_cast<uint16_t*>(base)[idx] = __builtin_bit_cast(uint16_t, f32_to_bf16(v));
+template <int TPR>
+struct NormShape {
+  static constexpr int kThreads = TPR <= 256 ? 256 : TPR;
+  static constexpr int kRows = kThreads / TPR;  // rows a workgroup holds at a time
+};
+
+// Sums (a, b) over the TPR lanes of a row; the same bits in every lane.  Rows
+// wider than a wave go through LDS, two buffers in turn: one barrier a call.
+template <int TPR>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float2 (*lds)[8], int& turn) {
+  if constexpr (TPR <= 64) {
+    a = group_sum<TPR>(a);
+    b = group_sum<TPR>(b);
   } else {
-    static_cast<float*>(base)[idx] = v;
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if ((threadIdx.x & 63) == 0) lds[turn][threadIdx.x >> 6] = float2{a, b};
+    __syncthreads();
+    a = 0.f;
+    b = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 64; ++i) {
+      a += lds[turn][i].x;
+      b += lds[turn][i].y;
+    }
+    turn ^= 1;
   }
 }
 
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
-  v = fminf(fmaxf(v, -kE4m3Max), kE4m3Max);
-  return (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false);
-}
-
-__device__ __forceinline__ float block_sum(float v, float* lds) {
-  v = wave_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.f;
-  for (int i = 0; i < kThreads / 64; ++i) s += lds[i];
-  return s;
-}
-
-// One workgroup per row, every pass over the row re-reading it.
-template <bool BF16, bool RBF16>
-__global__ __launch_bounds__(kThreads) void rmsnorm_kernel(NormParams p) {
-  __shared__ float lds[kThreads];
-  const size_t row = blockIdx.x;
-  auto at = [&](int c) {
-    float v = load1<BF16>(p.x, row * p.D + c);
-    if (p.residual) v += load1<RBF16>(p.residual, row * p.D + c);
+template <int TPR>
+__device__ __forceinline__ float row_max(float v, float2 (*lds)[8], int& turn) {
+  if constexpr (TPR <= 64) {
+    return group_max<TPR>(v);
+  } else {
+    v = group_max<64>(v);
+    if ((threadIdx.x & 63) == 0) lds[turn][threadIdx.x >> 6].x = v;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TPR / 64; ++i) v = fmaxf(v, lds[turn][i].x);
+    turn ^= 1;
     return v;
+  }
+}
+
+// The first n of 8 channels as e4m3 bytes.  |y| / scale is at most 448 but for
+// rounding, well inside the range that rounds to 448.
+__device__ __forceinline__ void store_e4m3(void* base, size_t elem, const float (&y)[8], float inv, int n) {
+  uint32_t lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] * inv, y[1] * inv, lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] * inv, y[3] * inv, lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4] * inv, y[5] * inv, hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6] * inv, y[7] * inv, hi, true);
+  uint8_t* q = static_cast<uint8_t*>(base) + elem;
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  typedef u32x2 __attribute__((aligned(1))) u32x2_any;
+  if (n >= 8) {
+    *reinterpret_cast<u32x2_any*>(q) = u32x2{lo, hi};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e < n) q[e] = (uint8_t)((e < 4 ? lo : hi) >> (8 * (e & 3)));
+  }
+}
+
+template <bool BF16, bool RBF16, int TPR, int NV>
+__global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormParams p) {
+  using Sh = NormShape<TPR>;
+  __shared__ float2 lds[2][8];
+  int turn = 0;
+  const int lane = threadIdx.x % TPR, D = p.D;
+  const int stride = gridDim.x * Sh::kRows;
+  int row = blockIdx.x * Sh::kRows + threadIdx.x / TPR;
+  Raw8<BF16> rx[NV];
+  Raw8<RBF16> rr[NV];
+  auto load = [&](int at) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = 8 * (lane + TPR * k);
+      rx[k] = load_raw8<BF16>(p.x, (size_t)at * D + c, D - c);
+      if (p.residual) rr[k] = load_raw8<RBF16>(p.residual, (size_t)at * D + c, D - c);
+    }
   };
-  float ss = 0.f;
-  for (int c = threadIdx.x; c < p.D; c += kThreads) ss = __builtin_fmaf(at(c), at(c), ss);
-  const float r = 1.f / sqrtf(block_sum(ss, lds) / p.D + p.eps);
-  const int group = p.group ? p.group : p.D;
-  for (int g0 = 0; g0 < p.D; g0 += group) {
-    const int g1 = min(g0 + group, p.D);
-    float inv = 1.f;
-    if (p.e4m3) {
-      float m = 0.f;
-      for (int c = g0 + threadIdx.x; c < g1; c += kThreads) m = fmaxf(m, fabsf(at(c) * r * p.w[c]));
-      __syncthreads();
-      lds[threadIdx.x] = m;
-      __syncthreads();
-      m = kAmaxFloor;
-      for (int i = 0; i < kThreads; ++i) m = fmaxf(m, lds[i]);
-      inv = kE4m3Max / m;
-      if (threadIdx.x == 0) p.scale[row * ((p.D + group - 1) / group) + g0 / group] = m / kE4m3Max;
+  if (row < p.R) load(row);
+  float w[NV][8];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int c = 8 * (lane + TPR * k);
+    const Raw8<false> v = load_raw8<false>(p.w, c, D - c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[k][e] = v.at(e);
+  }
+  const float inv_d = 1.f / (float)D;
+  while (row < p.R) {
+    float s[NV][8], ss = 0.f, unused = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s[k][e] = rx[k].at(e);
+        if (p.residual) s[k][e] += rr[k].at(e);
+        ss = __builtin_fmaf(s[k][e], s[k][e], ss);
+      }
+    const int here = row;
+    row += stride;
+    if (row < p.R) load(row);
+    if (p.residual_out) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int c = 8 * (lane + TPR * k);
+        store_raw8<RBF16>(p.residual_out, (size_t)here * D + c, s[k], D - c);
+      }
     }
-    for (int c = g0 + threadIdx.x; c < g1; c += kThreads) {
-      const float v = at(c), y = v * r * p.w[c];
-      if (p.e4m3) static_cast<uint8_t*>(p.y)[row * p.D + c] = to_e4m3(y * inv);
-      else store1<BF16>(p.y, row * p.D + c, y);
-      if (p.residual_out) store1<RBF16>(p.residual_out, row * p.D + c, v);
+    row_sum2<TPR>(ss, unused, lds, turn);
+    const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, inv_d, p.eps));
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[k][e] *= r * w[k][e];
+    if (!p.e4m3) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int c = 8 * (lane + TPR * k);
+        store_raw8<BF16>(p.y, (size_t)here * D + c, s[k], D - c);
+      }
+      continue;
+    }
+    float m[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      m[k] = kAmaxFloor;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m[k] = fmaxf(m[k], fabsf(s[k][e]));
+    }
+    if (p.group) {  // 128 channels are the same vector of 16 neighbouring lanes
+      const int groups = (D + 127) / 128;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        m[k] = group_max<16>(m[k]);
+        const int g = (lane + TPR * k) / 16;
+        if (lane % 16 == 0 && g < groups) p.scale[(size_t)here * groups + g] = m[k] * (1.f / kE4m3Max);
+      }
+    } else {
+#pragma unroll
+      for (int k = 1; k < NV; ++k) m[0] = fmaxf(m[0], m[k]);
+      m[0] = row_max<TPR>(m[0], lds, turn);
+#pragma unroll
+      for (int k = 1; k < NV; ++k) m[k] = m[0];
+      if (lane == 0) p.scale[here] = m[0] * (1.f / kE4m3Max);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = 8 * (lane + TPR * k);
+      store_e4m3(p.y, (size_t)here * D + c, s[k], kE4m3Max * __builtin_amdgcn_rcpf(m[k]), D - c);
     }
   }
 }
 
-template <bool BF16, bool RBF16>
-__global__ __launch_bounds__(kThreads) void rmsnorm_bwd_kernel(NormParams p) {
-  __shared__ float lds[kThreads];
-  const size_t row = blockIdx.x;
-  float ss = 0.f, gs = 0.f;
-  for (int c = threadIdx.x; c < p.D; c += kThreads) {
-    const float v = load1<RBF16>(p.x, row * p.D + c);
-    ss = __builtin_fmaf(v, v, ss);
-    gs = __builtin_fmaf(load1<BF16>(p.dy, row * p.D + c) * p.w[c], v, gs);
+// The same rows; dw is summed per lane over the rows that a group walks, then
+// over the workgroup's groups through LDS, into one partial row per workgroup.
+template <bool BF16, bool RBF16, int TPR, int NV>
+__global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_bwd_kernel(NormParams p) {
+  using Sh = NormShape<TPR>;
+  __shared__ float2 lds[2][8];
+  __shared__ float sums[Sh::kRows][TPR * 8];
+  int turn = 0;
+  const int lane = threadIdx.x % TPR, D = p.D;
+  const int stride = gridDim.x * Sh::kRows;
+  int row = blockIdx.x * Sh::kRows + threadIdx.x / TPR;
+  Raw8<RBF16> rs[NV], rr[NV];
+  Raw8<BF16> rd[NV];
+  auto load = [&](int at) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = 8 * (lane + TPR * k);
+      rs[k] = load_raw8<RBF16>(p.x, (size_t)at * D + c, D - c);
+      rd[k] = load_raw8<BF16>(p.dy, (size_t)at * D + c, D - c);
+      if (p.residual) rr[k] = load_raw8<RBF16>(p.residual, (size_t)at * D + c, D - c);
+    }
+  };
+  if (row < p.R) load(row);
+  float w[NV][8], dw[NV][8];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int c = 8 * (lane + TPR * k);
+    const Raw8<false> v = load_raw8<false>(p.w, c, D - c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      w[k][e] = v.at(e);
+      dw[k][e] = 0.f;
+    }
   }
-  const float r = 1.f / sqrtf(block_sum(ss, lds) / p.D + p.eps);
-  const float k = block_sum(gs, lds) * r / p.D;  // mean(g n)
-  if (threadIdx.x == 0) static_cast<float*>(p.part)[row] = r;
-  for (int c = threadIdx.x; c < p.D; c += kThreads) {
-    const size_t e = row * p.D + c;
-    const float n = load1<RBF16>(p.x, e) * r;
-    float v = r * (load1<BF16>(p.dy, e) * p.w[c] - n * k);
-    if (p.residual) v += load1<RBF16>(p.residual, e);
-    store1<RBF16>(p.y, e, v);
-    if (p.residual_out) store1<BF16>(p.residual_out, e, v);
+  const float inv_d = 1.f / (float)D;
+  while (row < p.R) {
+    float ss = 0.f, gs = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float s = rs[k].at(e);
+        ss = __builtin_fmaf(s, s, ss);
+        gs = __builtin_fmaf(rd[k].at(e) * w[k][e], s, gs);
+      }
+    row_sum2<TPR>(ss, gs, lds, turn);
+    const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, inv_d, p.eps));
+    const float kk = gs * inv_d * r * r;  // mean(g n) r: ds = r g - n (mean(g n) r)
+    const int here = row;
+    row += stride;
+    float ds[NV][8];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float n = rs[k].at(e) * r, d = rd[k].at(e);
+        ds[k][e] = __builtin_fmaf(-n, kk, r * (d * w[k][e]));
+        if (p.residual) ds[k][e] += rr[k].at(e);
+        dw[k][e] = __builtin_fmaf(d, n, dw[k][e]);
+      }
+    if (row < p.R) load(row);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = 8 * (lane + TPR * k);
+      store_raw8<RBF16>(p.y, (size_t)here * D + c, ds[k], D - c);
+      if (p.residual_out) store_raw8<BF16>(p.residual_out, (size_t)here * D + c, ds[k], D - c);
+    }
+  }
+  float* part = static_cast<float*>(p.part) + (size_t)blockIdx.x * D;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[threadIdx.x / TPR][8 * lane + e] = dw[k][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < TPR * 8; i += Sh::kThreads) {
+      float v = 0.f;
+#pragma unroll
+      for (int g = 0; g < Sh::kRows; ++g) v += sums[g][i];
+      const int c = TPR * 8 * k + i;
+      if (c < D) part[c] = v;
+    }
   }
 }
 
-template <bool BF16, bool RBF16>
-__global__ __launch_bounds__(kThreads) void rmsnorm_dw_kernel(NormParams p) {
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  if (c >= p.D) return;
-  float s = 0.f;
-  for (int row = 0; row < p.R; ++row) {
-    const size_t e = (size_t)row * p.D + c;
-    s += load1<BF16>(p.dy, e) * load1<RBF16>(p.x, e) * static_cast<const float*>(p.part)[row];
+// dw from G partial rows [G, D]: 16 channels a workgroup, 16 threads a channel.
+__global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* part, float* dw, int G, int D) {
+  __shared__ float sums[16][16];
+  const int j = threadIdx.x % 16, slice = threadIdx.x / 16, c = blockIdx.x * 16 + j;
+  float v = 0.f;
+  if (c < D)
+    for (int g = slice; g < G; g += 16) v += part[(size_t)g * D + c];
+  sums[slice][j] = v;
+  __syncthreads();
+  if (slice == 0 && c < D) {
+    for (int i = 1; i < 16; ++i) v += sums[i][j];
+    dw[c] = v;
   }
-  p.dw[c] = s;
+}
+
+// Calls fn(TPR, NV) as constants for the smallest row group that holds D channels.
+template <typename F>
+auto norm_shape(int D, F&& fn) {
+  using std::integral_constant;
+  if (D <= 128) return fn(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  if (D <= 256) return fn(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+  if (D <= 512) return fn(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (D <= 1024) return fn(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  if (D <= 2048) return fn(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+  if (D <= 4096) return fn(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  if (D <= 8192) return fn(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  return fn(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+}
+
+// Workgroups of a launch: as many as rows need, at most `per_cu` a CU.
+int norm_groups(int R, int rows, int per_cu) {
+  const long long need = ((long long)R + rows - 1) / rows;
+  return (int)(need < (long long)kCus * per_cu ? need : (long long)kCus * per_cu);
+}
+
+constexpr int kFwdPerCu = 4, kBwdPerCu = 2;
+
+template <bool BF16, bool RBF16>
+hipError_t launch_fwd_t(const NormParams& p, hipStream_t s) {
+  return norm_shape(p.D, [&](auto tpr, auto nv) {
+    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+    using Sh = NormShape<TPR>;
+    hipLaunchKernelGGL((rmsnorm_kernel<BF16, RBF16, TPR, NV>), dim3(norm_groups(p.R, Sh::kRows, kFwdPerCu)),
+                       dim3(Sh::kThreads), 0, s, p);
+    return hipGetLastError();
+  });
+}
+
+int bwd_groups(int R, int D) {
+  return norm_shape(D, [&](auto tpr, auto) {
+    return norm_groups(R, NormShape<decltype(tpr)::value>::kRows, kBwdPerCu);
+  });
 }
 
 template <bool BF16, bool RBF16>
 hipError_t launch_bwd_t(const NormParams& p, hipStream_t s) {
-  if (p.R > 0) {
-    hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, RBF16>), dim3(p.R), dim3(kThreads), 0, s, p);
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  const int G = p.R > 0 ? bwd_groups(p.R, p.D) : 0;
+  if (G > 0) {
+    const hipError_t e = norm_shape(p.D, [&](auto tpr, auto nv) {
+      constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+      hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, RBF16, TPR, NV>), dim3(G), dim3(NormShape<TPR>::kThreads), 0, s, p);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((rmsnorm_dw_kernel<BF16, RBF16>), dim3((p.D + kThreads - 1) / kThreads), dim3(kThreads), 0, s, p);
+  hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3((p.D + 15) / 16), dim3(256), 0, s, static_cast<const float*>(p.part), p.dw,
+                     G, p.D);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t rmsnorm_bwd_scratch(int R, int) { return (size_t)R * 4; }
+size_t rmsnorm_bwd_scratch(int R, int D) { return (size_t)bwd_groups(R, D) * D * 4; }
 
 hipError_t launch_rmsnorm(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s) {
-  const dim3 grid(p.R), block(kThreads);
-  if (!bf16) hipLaunchKernelGGL((rmsnorm_kernel<false, false>), grid, block, 0, s, p);
-  else if (res_bf16) hipLaunchKernelGGL((rmsnorm_kernel<true, true>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((rmsnorm_kernel<true, false>), grid, block, 0, s, p);
-  return hipGetLastError();
+  if (!bf16) return launch_fwd_t<false, false>(p, s);
+  return res_bf16 ? launch_fwd_t<true, true>(p, s) : launch_fwd_t<true, false>(p, s);
 }
 
 hipError_t launch_rmsnorm_bwd(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s) {

@@ -77,7 +77,7 @@ def check_forward(d, r, dtype, res, group, eps, residual=True):
 
 
 SIZES = [(1, 1), (3, 7), (5, 16), (2, 64), (9, 100), (4, 128), (33, 129), (2, 255), (7, 256), (3, 1001), (65, 2048),
-         (2, 2056), (3, 5000), (2, 8192), (2, 20001), (2, 32768)]
+         (2, 2056), (3, 5000), (2, 8192), (2, 12001), (2, 16384), (4500, 40), (2100, 515)]
 
 
 @pytest.mark.parametrize("dtype,res", TYPES)
@@ -136,7 +136,7 @@ def test_rows_of_zeros_and_extremes():
 def test_in_place_residual():
     """out["residual"] may be the residual, and the backward's ds may be d_residual: same values as apart."""
     for dtype, res in TYPES:
-        for D in (96, 1001, 4096, 20000):
+        for D in (96, 1001, 4096, 12000):
             d, t = draw(5, D, dtype, res, seed=4)
             a = mesa.rmsnorm(t["x"], t["w"], residual=t["residual"], quant_group=128)
             b_res = t["residual"].clone()
