@@ -512,8 +512,8 @@ mesa_status mesa_qk_preprocess(int32_t B, int32_t H, int32_t T, int32_t d, int32
  *
  * Arithmetic and states are fp32 for either dtype.  Every sum is formed in a
  * fixed order: equal inputs give bitwise equal results.
- * Supported: any D >= 1, ld >= D, T >= 0, B >= 1 with B T ld <= 2^40 and
- * B ceil(T/64) ceil(D/64) < 2^31; c > 0, finite (else MESA_ERR_INVALID_ARG).
+ * Supported: 1 <= D <= ld <= 2^20, T >= 0, B >= 1 with B ceil(T/64) ceil(D/64)
+ * <= 2^23; c > 0, finite (else MESA_ERR_INVALID_ARG).
  * Two calls may not use one workspace at the same time. */
 typedef struct {
   int32_t B, T, D;   /* sequences, tokens per (padded) sequence, channels             */

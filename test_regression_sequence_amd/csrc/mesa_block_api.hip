@@ -23,12 +23,15 @@ size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
 // ---- gated linear recurrence ----------------------------------------------
 
+constexpr int kLruMaxStride = 1 << 20;
+
 mesa_status check_lru(const mesa_lru_desc* d) {
   if (!d || d->B < 1 || d->T < 0 || d->D < 1 || d->ld < d->D || !dtype_ok(d->dtype)) return MESA_ERR_INVALID_ARG;
   if (!(d->c > 0.f) || std::isinf(d->c)) return MESA_ERR_INVALID_ARG;
-  if ((double)d->B * d->T * d->ld > (double)(1LL << 40)) return MESA_ERR_UNSUPPORTED;
-  const double tiles = (double)d->B * ((d->T + 63) / 64) * ((d->D + 63) / 64);
-  if (tiles >= 2147483648.0) return MESA_ERR_UNSUPPORTED;
+  // offsets within a tile of tokens are 32-bit; a launch has at most 2^32 threads
+  if (d->ld > kLruMaxStride) return MESA_ERR_UNSUPPORTED;
+  const double tiles = (double)d->B * (((long long)d->T + 63) / 64) * ((d->D + 63) / 64);
+  if (tiles > 8388608.0) return MESA_ERR_UNSUPPORTED;
   return MESA_OK;
 }
 
@@ -43,6 +46,12 @@ mesa::LruParams lru_params(const mesa_lru_desc* d, const void* x, const void* ga
   mesa::LruParams p{};
   p.x = x; p.ga = ga; p.gi = gi; p.lam = lam; p.h0 = h0; p.lengths = lengths;
   p.states = static_cast<float*>(workspace);
+  if (workspace) {  // states, published pairs and ticket, the backward's partial sums
+    char* words = static_cast<char*>(workspace) + lru_state_bytes(d);
+    const size_t n = mesa::lru_word_bytes(d->B, d->T, d->D);
+    p.words = reinterpret_cast<uint64_t*>(words);
+    p.ticket = reinterpret_cast<unsigned*>(words + n - 256);
+  }
   p.B = d->B; p.T = d->T; p.D = d->D; p.ld = d->ld; p.NC = lru_chunks(d); p.c = d->c;
   return p;
 }
@@ -53,7 +62,7 @@ extern "C" {
 
 size_t mesa_lru_workspace_bytes(const mesa_lru_desc* d) {
   if (check_lru(d) != MESA_OK || d->T == 0) return 0;
-  return lru_state_bytes(d) + lru_part_bytes(d);
+  return lru_state_bytes(d) + mesa::lru_word_bytes(d->B, d->T, d->D) + lru_part_bytes(d);
 }
 
 mesa_status mesa_lru_fwd(const mesa_lru_desc* d, const void* x, const void* ga, const void* gi, const float* lam,
@@ -77,7 +86,7 @@ mesa_status mesa_lru_bwd(const mesa_lru_desc* d, const void* x, const void* ga, 
   const mesa_status st = check_lru(d);
   if (st != MESA_OK) return st;
   if (ld_grad < d->D || (states_in_workspace != 0 && states_in_workspace != 1)) return MESA_ERR_INVALID_ARG;
-  if ((double)d->B * d->T * ld_grad > (double)(1LL << 40)) return MESA_ERR_UNSUPPORTED;
+  if (ld_grad > kLruMaxStride) return MESA_ERR_UNSUPPORTED;
   if (!lam || !dlam || (d->T > 0 && (!x || !ga || !gi || !dy || !dx || !dga || !dgi))) return MESA_ERR_INVALID_ARG;
   if (!all_aligned({x, ga, gi, lam, h0, lengths, dy, d_hfinal, dx, dga, dgi, dlam, dh0, workspace}))
     return MESA_ERR_ALIGNMENT;
@@ -87,7 +96,8 @@ mesa_status mesa_lru_bwd(const mesa_lru_desc* d, const void* x, const void* ga, 
   mesa::LruParams p = lru_params(d, x, ga, gi, lam, h0, lengths, workspace);
   if (d->T > 0) {
     if (!states_in_workspace && mesa::launch_lru_fwd(bf16, p, stream) != hipSuccess) return MESA_ERR_HIP;
-    p.lam_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + lru_state_bytes(d));
+    p.lam_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + lru_state_bytes(d) +
+                                            mesa::lru_word_bytes(d->B, d->T, d->D));
   }
   p.dy = dy; p.d_hfinal = d_hfinal;
   p.dx = dx; p.dga = dga; p.dgi = dgi; p.ld_grad = ld_grad; p.dlam = dlam; p.dh0 = dh0;

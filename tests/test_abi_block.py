@@ -41,13 +41,17 @@ def call_lru_bwd(d, ld_grad=100, flag=0, wbytes=1 << 40, **kw):
 BAD_LRU = [
     (dict(B=0), 1), (dict(T=-1), 1), (dict(D=0, ld=100), 1), (dict(ld=99), 1), (dict(c=0.0), 1), (dict(c=-1.0), 1),
     (dict(c=float("inf")), 1), (dict(c=float("nan")), 1), (dict(dtype=2), 1),
-    (dict(B=1 << 20, T=1 << 20, ld=1 << 20), 2), (dict(B=1 << 30, T=64, D=1000, ld=1000), 2),
+    (dict(ld=(1 << 20) + 1), 2), (dict(B=1 << 19, T=64 * 8, D=128, ld=128), 0), (dict(B=1 << 19, T=64 * 8 + 1, D=128, ld=128), 2),
+    (dict(B=2 ** 31 - 1, T=2 ** 31 - 1), 2),
 ]
 
 
 @pytest.mark.parametrize("kw,expect", BAD_LRU)
 def test_lru_rejects_bad_descriptors(kw, expect):
     d = lru_desc(**kw)
+    if expect == 0:  # the largest: accepted up to the workspace
+        assert call_lru_fwd(d, workspace=0) == 4 and call_lru_bwd(d, ld_grad=1 << 20, workspace=0) == 4 and lru_ws(d) > 0
+        return
     assert call_lru_fwd(d) == expect
     assert call_lru_bwd(d, ld_grad=1 << 20) == expect
     assert lru_ws(d) == 0
@@ -70,8 +74,8 @@ def test_lru_rejects_missing_and_misaligned_pointers_and_small_workspaces():
     assert call_lru_bwd(d, ld_grad=99) == 1
     assert call_lru_bwd(d, flag=2) == 1
     assert call_lru_bwd(d, flag=-1) == 1
-    assert call_lru_bwd(d, ld_grad=2 ** 31 - 1, workspace=0) == 4
-    assert call_lru_bwd(lru_desc(T=1 << 20), ld_grad=1 << 20) == 2
+    assert call_lru_bwd(d, ld_grad=1 << 20, workspace=0) == 4
+    assert call_lru_bwd(d, ld_grad=(1 << 20) + 1) == 2
     assert call_lru_bwd(d, wbytes=need - 1) == 4
     assert lru_ws(lru_desc(T=0)) == 0
 
