@@ -1,6 +1,7 @@
 // C ABI of the operators around the Mesa layer: argument validation, workspace
 // carving, kernel launches.  Every check runs before the first launch, so a
 // failing call writes nothing.
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/mesa.h"
@@ -39,19 +40,21 @@ int lru_chunks(const mesa_lru_desc* d) { return (d->T + mesa::kLruChunk - 1) / m
 
 size_t lru_state_bytes(const mesa_lru_desc* d) { return pad256((size_t)d->B * lru_chunks(d) * d->D * 4); }
 
-size_t lru_part_bytes(const mesa_lru_desc* d) { return pad256((size_t)d->B * d->D * 4); }
+size_t lru_word_bytes(const mesa_lru_desc* d) {
+  const bool bf16 = d->dtype == MESA_BF16;
+  return std::max(mesa::lru_fwd_word_bytes(bf16, d->B, d->T, d->D), mesa::lru_bwd_word_bytes(bf16, d->B, d->T, d->D));
+}
 
 mesa::LruParams lru_params(const mesa_lru_desc* d, const void* x, const void* ga, const void* gi, const float* lam,
                            const float* h0, const int32_t* lengths, void* workspace) {
   mesa::LruParams p{};
   p.x = x; p.ga = ga; p.gi = gi; p.lam = lam; p.h0 = h0; p.lengths = lengths;
   p.states = static_cast<float*>(workspace);
-  if (workspace) {  // states, published pairs and ticket, the backward's partial sums
-    char* words = static_cast<char*>(workspace) + lru_state_bytes(d);
-    const size_t n = mesa::lru_word_bytes(d->B, d->T, d->D);
-    p.words = reinterpret_cast<uint64_t*>(words);
-    p.ticket = reinterpret_cast<unsigned*>(words + n - 256);
-  }
+  char* at = static_cast<char*>(workspace) + lru_state_bytes(d);
+  p.tickets = reinterpret_cast<unsigned*>(at);
+  p.rates = reinterpret_cast<float*>(at += mesa::kLruTicketBytes);
+  p.words = reinterpret_cast<uint64_t*>(at += pad256((size_t)d->D * 4));
+  p.lam_part = reinterpret_cast<float*>(at += lru_word_bytes(d));
   p.B = d->B; p.T = d->T; p.D = d->D; p.ld = d->ld; p.NC = lru_chunks(d); p.c = d->c;
   return p;
 }
@@ -62,7 +65,8 @@ extern "C" {
 
 size_t mesa_lru_workspace_bytes(const mesa_lru_desc* d) {
   if (check_lru(d) != MESA_OK || d->T == 0) return 0;
-  return lru_state_bytes(d) + mesa::lru_word_bytes(d->B, d->T, d->D) + lru_part_bytes(d);
+  return lru_state_bytes(d) + mesa::kLruTicketBytes + pad256((size_t)d->D * 4) +
+         lru_word_bytes(d) + pad256(mesa::lru_bwd_part_bytes(d->dtype == MESA_BF16, d->B, d->T, d->D));
 }
 
 mesa_status mesa_lru_fwd(const mesa_lru_desc* d, const void* x, const void* ga, const void* gi, const float* lam,
@@ -94,11 +98,8 @@ mesa_status mesa_lru_bwd(const mesa_lru_desc* d, const void* x, const void* ga, 
   if (need > 0 && (!workspace || workspace_bytes < need)) return MESA_ERR_WORKSPACE;
   const bool bf16 = d->dtype == MESA_BF16;
   mesa::LruParams p = lru_params(d, x, ga, gi, lam, h0, lengths, workspace);
-  if (d->T > 0) {
-    if (!states_in_workspace && mesa::launch_lru_fwd(bf16, p, stream) != hipSuccess) return MESA_ERR_HIP;
-    p.lam_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + lru_state_bytes(d) +
-                                            mesa::lru_word_bytes(d->B, d->T, d->D));
-  }
+  if (d->T > 0 && !states_in_workspace && mesa::launch_lru_fwd(bf16, p, stream) != hipSuccess) return MESA_ERR_HIP;
+  if (d->T == 0) p.lam_part = nullptr;
   p.dy = dy; p.d_hfinal = d_hfinal;
   p.dx = dx; p.dga = dga; p.dgi = dgi; p.ld_grad = ld_grad; p.dlam = dlam; p.dh0 = dh0;
   return mesa::launch_lru_bwd(bf16, p, stream) == hipSuccess ? MESA_OK : MESA_ERR_HIP;

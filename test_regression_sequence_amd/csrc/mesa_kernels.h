@@ -145,8 +145,9 @@ struct LruParams {
   float* dlam;              // [D]
   float* dh0;               // [B, D] or null
   float* lam_part;          // partial sums of dL / d log w
+  float* rates;             // [D]: 2 c softplus(lam)
   uint64_t* words;          // published pairs (mesa_lru_tile.h)
-  unsigned* ticket;         // tiles handed out
+  unsigned* tickets;        // tiles handed out, by class
   int B, T, D, ld, ld_grad, NC;
   float c;
 };
@@ -255,8 +256,13 @@ size_t sym_state_floats(int D);
 hipError_t launch_lru_fwd(bool bf16, const LruParams& p, hipStream_t s);
 // gradients, from the states launch_lru_fwd left
 hipError_t launch_lru_bwd(bool bf16, const LruParams& p, hipStream_t s);
-// Bytes of the published pairs and the ticket (the ticket in the last 256).
-size_t lru_word_bytes(int B, int T, int D);
+// Bytes of the ticket counters, of the published pairs and of the partial sums.
+constexpr size_t kLruTicketBytes = 4096;
+size_t lru_fwd_word_bytes(bool bf16, int B, int T, int D);
+size_t lru_bwd_word_bytes(bool bf16, int B, int T, int D);
+size_t lru_bwd_part_bytes(bool bf16, int B, int T, int D);
+// clears the words and tickets and forms the rates
+hipError_t launch_lru_ready(const LruParams& p, size_t words, hipStream_t s);
 hipError_t launch_lru_step(bool bf16, const LruParams& p, hipStream_t s);
 hipError_t launch_rmsnorm(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s);
 hipError_t launch_rmsnorm_bwd(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s);

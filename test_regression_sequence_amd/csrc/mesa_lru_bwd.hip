@@ -1,0 +1,270 @@
+// Backward pass of the gated linear recurrence (mesa_lru_gate.h: the cell and
+// its gradients; mesa_lru_tile.h: tiles and their joining).
+//
+// With c_t the adjoint of the state behind token t, g_t = c_t + dy_t and
+// c_{t-1} = a_t g_t: a scan of the maps c -> a_t c + a_t dy_t, last token first.
+// A tile reads x, ga, gi and dy once, forms decays, inputs and gradient factors
+// in registers, walks the states again from the forward's kept state before
+// its chunk (they need no other tile), joins its adjoints with the tiles behind
+// it, and writes dx, dga and dgi.
+#include <algorithm>
+
+#include "mesa_common.h"
+#include "mesa_kernels.h"
+#include "mesa_lru_gate.h"
+#include "mesa_lru_tile.h"
+
+namespace mesa {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+template <bool BF16>
+struct BwdTile {
+  static constexpr int TW = 4, NW = 4, L = 4 * NW * TW;
+  static constexpr int CW = kLruChunk / (4 * TW);  // waves of a chunk of the kept states
+  static_assert(NW >= 4 && NW % CW == 0, "three waves wait for other tiles; tiles hold whole chunks");
+};
+
+template <bool BF16>
+__global__ __launch_bounds__(256, 2) void lru_bwd_kernel(LruParams p) {
+  using Sh = BwdTile<BF16>;
+  constexpr int TW = Sh::TW, NW = Sh::NW, L = Sh::L, CW = Sh::CW;
+  constexpr uint32_t ES = BF16 ? 2 : 4;
+  __shared__ Pair waves[NW][kLruSlab], pre[NW][kLruSlab], fwd[NW][kLruSlab];
+  __shared__ LruCarry carry;
+  __shared__ float sums[NW][kLruSlab];
+  __shared__ unsigned ticket;
+  const LruGrid grid(p.B, p.T, p.D, L);
+  const int tiles = grid.tiles;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane >> 4, c4 = 4 * (lane & 15);
+  int i, chain;  // i: the tile's place in the scan
+  if (!grid.take(p.tickets, &ticket, i, chain)) return;
+  const int b = chain / grid.slabs, c0 = (chain % grid.slabs) * kLruSlab;
+  const int ch = c0 + c4, nch = p.D - ch;
+  const int n = lru_length(p, b), live = (n + L - 1) / L;
+  const int j = i < live ? live - 1 - i : i;             // the tiles with valid tokens, last first; then the others
+  const int tw0 = (4 * wave + row) * TW, t0 = j * L + tw0;  // this lane's first token
+  const size_t first = (size_t)b * p.T + (size_t)j * L;     // the tile's first row of the tensors
+  const size_t grad = first * p.ld_grad * ES;
+  const uint32_t grow = p.ld_grad * ES, goff = tw0 * grow + ch * ES;
+  float* part = p.lam_part ? p.lam_part + ((size_t)b * tiles + j) * p.D + c0 + lane : nullptr;
+  const bool mine = c0 + lane < p.D;
+
+  if (i >= live) {  // behind the length: zeros
+    if (wave == 0 && mine) {
+      const size_t e = (size_t)b * p.D + c0 + lane;
+      if (part) *part = 0.f;
+      if (i == 0 && p.dh0) p.dh0[e] = p.d_hfinal ? p.d_hfinal[e] : 0.f;
+    }
+    const float zero[4] = {};
+#pragma unroll
+    for (int s = 0; s < TW; ++s)
+      if (t0 + s < p.T) {
+        store_raw4<BF16>(static_cast<char*>(p.dx) + grad, goff + s * grow, zero, nch);
+        store_raw4<BF16>(static_cast<char*>(p.dga) + grad, goff + s * grow, zero, nch);
+        store_raw4<BF16>(static_cast<char*>(p.dgi) + grad, goff + s * grow, zero, nch);
+      }
+    return;
+  }
+  const bool whole = (j + 1) * L <= n;
+
+  Raw4<BF16> x[TW], dy[TW];
+  float a[TW][4], dxg[TW][4], q[TW][4], va[TW][4], vu[TW][4], sr1[TW][4], h[4];
+  {
+    Raw4<BF16> ga[TW], gi[TW];
+    uint32_t off[TW], doff[TW];
+#pragma unroll
+    for (int s = 0; s < TW; ++s) {  // rows behind n read row n - 1 and are not used
+      const int t = whole ? tw0 + s : min(tw0 + s, n - 1 - j * L);
+      off[s] = ((uint32_t)t * p.ld + ch) * ES;
+      doff[s] = ((uint32_t)t * p.D + ch) * ES;
+    }
+    const size_t in = first * p.ld * ES;
+    load_raw4<BF16>(static_cast<const char*>(p.ga) + in, off, nch, ga);
+    load_raw4<BF16>(static_cast<const char*>(p.gi) + in, off, nch, gi);
+    load_raw4<BF16>(static_cast<const char*>(p.x) + in, off, nch, x);
+    load_raw4<BF16>(static_cast<const char*>(p.dy) + first * p.D * ES, doff, nch, dy);
+    {  // the state before this lane's chunk
+      const int chunk = min(t0, n - 1) / kLruChunk;
+      const uint32_t none[1] = {0};
+      Raw4<false> r[1];
+      load_raw4<false>(p.states + ((size_t)b * p.NC + chunk) * p.D + ch, none, nch, r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = r[0].at(e);
+    }
+    float rate[4];
+    lru_rates(p, tiles > 1, ch, nch, rate);
+#pragma unroll
+    for (int s = 0; s < TW; ++s) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const LruGrad r = lru_cell_grad(x[s].at(e), ga[s].at(e), gi[s].at(e), rate[e]);
+        a[s][e] = r.a;
+        dxg[s][e] = r.dx_g;
+        q[s][e] = r.q;
+        va[s][e] = r.v_a;
+        vu[s][e] = r.v_u;
+        sr1[s][e] = r.sr1;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  // behind n: the state and the adjoint pass, and every gradient is 0
+  if (!whole) {
+#pragma unroll
+    for (int s = 0; s < TW; ++s) {
+      const bool off = t0 + s >= n;
+      clear_if(off, x[s]);
+      clear_if(off, dy[s]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        a[s][e] = __builtin_unpredictable(off) ? 1.f : a[s][e];
+        dxg[s][e] = __builtin_unpredictable(off) ? 0.f : dxg[s][e];
+        q[s][e] = __builtin_unpredictable(off) ? 0.f : q[s][e];
+        va[s][e] = __builtin_unpredictable(off) ? 0.f : va[s][e];
+        vu[s][e] = __builtin_unpredictable(off) ? 0.f : vu[s][e];
+        sr1[s][e] = __builtin_unpredictable(off) ? 0.f : sr1[s][e];
+      }
+    }
+  }
+  Pair before[4], earlier[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    Pair all;
+    Pair back{a[TW - 1][e], a[TW - 1][e] * dy[TW - 1].at(e)};
+#pragma unroll
+    for (int s = TW - 2; s >= 0; --s) back = join(back, Pair{a[s][e], a[s][e] * dy[s].at(e)});
+    join_rows<true>(back, row, before[e], all);
+    if (row == 0) waves[wave][c4 + e] = all;
+    Pair on{a[0][e], dxg[0][e] * x[0].at(e)};
+#pragma unroll
+    for (int s = 1; s < TW; ++s) on = join(on, Pair{a[s][e], dxg[s][e] * x[s].at(e)});
+    join_rows<false>(on, row, earlier[e], all);
+    if (CW > 1 && row == 0) fwd[wave][c4 + e] = all;
+  }
+  __syncthreads();
+  uint64_t* words = p.words + (size_t)chain * lru_chain_words(tiles);
+  Pair tile{1.f, 0.f};
+  if (wave == 0) {
+#pragma unroll
+    for (int w = NW - 1; w >= 0; --w) {
+      pre[w][lane] = tile;
+      tile = join(tile, waves[w][lane]);
+    }
+    if (tiles > 1) publish(words + (size_t)i * kLruSlab + lane, tile);
+  } else if (wave == 1) {
+    const float g = p.d_hfinal && mine ? p.d_hfinal[(size_t)b * p.D + c0 + lane] : 0.f;
+    carry_groups(words, tiles, i, lane, g, carry.h);
+  } else if (wave < 4) {
+    carry_tiles(words, i, wave - 2, lane, wave == 2 ? carry.early : carry.late);
+  }
+  // the states before this lane's tokens, and with them v / g = vu - va h
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (CW > 1) {
+      const int w0 = wave / CW * CW;
+#pragma unroll
+      for (int w = 0; w < CW - 1; ++w)
+        if (w0 + w < wave) h[e] = apply(fwd[w0 + w][c4 + e], h[e]);
+    }
+    h[e] = apply(earlier[e], h[e]);
+#pragma unroll
+    for (int s = 0; s < TW; ++s) {
+      vu[s][e] = __builtin_fmaf(-va[s][e], h[e], vu[s][e]);
+      h[e] = __builtin_fmaf(a[s][e], h[e], dxg[s][e] * x[s].at(e));
+    }
+  }
+  __syncthreads();
+  if (wave == 0 && i % kLruGroup == kLruGroup - 1)
+    publish(words + (size_t)(tiles + i / kLruGroup) * kLruSlab + lane,
+            join(join(carry.early[lane], carry.late[lane]), tile));
+  float c[4], vsum[4] = {};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    c[e] = apply(carry.late[c4 + e], apply(carry.early[c4 + e], carry.h[c4 + e]));
+    c[e] = apply(before[e], apply(pre[wave][c4 + e], c[e]));
+  }
+#pragma unroll
+  for (int s = TW - 1; s >= 0; --s) {
+    float dx[4], dga[4], dgi[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float g = c[e] + dy[s].at(e), v = g * vu[s][e];
+      vsum[e] += v;
+      dx[e] = g * dxg[s][e];
+      dgi[e] = dx[e] * q[s][e];
+      dga[e] = v * sr1[s][e];
+      c[e] = a[s][e] * g;
+    }
+    if (whole || t0 + s < p.T) {
+      store_raw4<BF16>(static_cast<char*>(p.dx) + grad, goff + s * grow, dx, nch);
+      store_raw4<BF16>(static_cast<char*>(p.dga) + grad, goff + s * grow, dga, nch);
+      store_raw4<BF16>(static_cast<char*>(p.dgi) + grad, goff + s * grow, dgi, nch);
+    }
+  }
+  if (p.dh0 && t0 == 0) store_raw4<false>(p.dh0, ((size_t)b * p.D + ch) * 4, c, nch);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    vsum[e] = sum_lane_groups(vsum[e]);
+    if (row == 0) sums[wave][c4 + e] = vsum[e];
+  }
+  __syncthreads();
+  if (wave == 0 && mine) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v += sums[w][lane];
+    *part = v;
+  }
+}
+
+// dlam from `rows` partial sums [rows, D] of dL / d log w: 16 channels a
+// workgroup, 16 threads a channel.
+__global__ __launch_bounds__(kThreads) void lru_dlam_kernel(const float* part, const float* lam, float* dlam, int rows,
+                                                            int D) {
+  __shared__ float sums[16][16];
+  const int k = threadIdx.x % 16, slice = threadIdx.x / 16, ch = blockIdx.x * 16 + k;
+  float v = 0.f;
+  if (ch < D) {
+#pragma unroll 8
+    for (int r = slice; r < rows; r += 16) v += part[(size_t)r * D + ch];
+  }
+  sums[slice][k] = v;
+  __syncthreads();
+  if (slice == 0 && ch < D) {
+    for (int i = 1; i < 16; ++i) v += sums[i][k];
+    dlam[ch] = v * lru_rate_slope(lam[ch]);
+  }
+}
+
+template <bool BF16>
+hipError_t launch_t(const LruParams& p, hipStream_t s) {
+  const LruGrid grid(p.B, p.T, p.D, BwdTile<BF16>::L);
+  if (grid.tiles > 1) {
+    if (const hipError_t e = launch_lru_ready(p, grid.chains * lru_chain_words(grid.tiles), s); e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((lru_bwd_kernel<BF16>), dim3(grid.workgroups()), dim3(64 * BwdTile<BF16>::NW), 0, s, p);
+  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  hipLaunchKernelGGL(lru_dlam_kernel, dim3((p.D + 15) / 16), dim3(kThreads), 0, s, p.lam_part, p.lam, p.dlam,
+                     p.T > 0 ? p.B * grid.tiles : 0, p.D);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t lru_bwd_word_bytes(bool bf16, int B, int T, int D) {
+  const LruGrid grid(B, T, D, bf16 ? BwdTile<true>::L : BwdTile<false>::L);
+  return grid.chains * lru_chain_words(grid.tiles) * sizeof(uint64_t);
+}
+
+size_t lru_bwd_part_bytes(bool bf16, int B, int T, int D) {
+  const LruGrid grid(B, T, D, bf16 ? BwdTile<true>::L : BwdTile<false>::L);
+  return (size_t)B * grid.tiles * D * sizeof(float);
+}
+
+hipError_t launch_lru_bwd(bool bf16, const LruParams& p, hipStream_t s) {
+  return bf16 ? launch_t<true>(p, s) : launch_t<false>(p, s);
+}
+
+}  // namespace mesa

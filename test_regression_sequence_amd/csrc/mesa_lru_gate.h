@@ -32,14 +32,16 @@ __device__ __forceinline__ float lru_sigmoid(float z) {
 // 1 - exp(-w) for w >= 0, given a = exp(-w/2).  Above w = 1/4, 1 - a^2 keeps
 // all but two bits.  Below it the difference would cancel, so the alternating
 // series w (1 - w/2 + w^2/6 - ...) is summed to w^5/720: the first term left
-// out is below w^6/5040 = 5e-8 of the value.
+// out is below w^6/5040 = 5e-8 of the value.  Both are formed and one selected:
+// marked unpredictable, or the compiler makes a branch of every element.
 __device__ __forceinline__ float lru_one_minus_a2(float w, float a) {
   float p = __builtin_fmaf(w, -1.f / 720.f, 1.f / 120.f);
   p = __builtin_fmaf(w, p, -1.f / 24.f);
   p = __builtin_fmaf(w, p, 1.f / 6.f);
   p = __builtin_fmaf(w, p, -0.5f);
   p = __builtin_fmaf(w, p, 1.f);
-  return w < 0.25f ? w * p : __builtin_fmaf(-a, a, 1.f);
+  const float series = w * p, direct = __builtin_fmaf(-a, a, 1.f);
+  return __builtin_unpredictable(w < 0.25f) ? series : direct;
 }
 
 // Decay a and input u of one token: h_t = a h_{t-1} + u.
@@ -51,10 +53,11 @@ __device__ __forceinline__ void lru_cell(float x, float ga, float gi, float rate
 
 // The same with what the gradients need.  With g the adjoint of h_t and h1 the
 // state before the token:
-//     dx = g dx_g,  dgi = g dgi_g,  v = g (v_u - v_a h1),  dga = v sr1,
-// v = dL / d log w = (w/2) g ((a^2/m) s_i x - a h1).
+//     dx = g dx_g,  dgi = dx q,  v = g (v_u - v_a h1),  dga = v sr1,
+// q = x (1 - s_i), v = dL / d log w = (w/2) g ((a^2/m) s_i x - a h1); the input
+// is u = dx_g x.
 struct LruGrad {
-  float a, u, dx_g, dgi_g, v_u, v_a, sr1;
+  float a, dx_g, q, v_u, v_a, sr1;
 };
 
 // 1 - sigmoid comes as exp(-z) sigmoid(z), which keeps its bits for large z;
@@ -74,8 +77,7 @@ __device__ __forceinline__ LruGrad lru_cell_grad(float x, float ga, float gi, fl
   const float m = m2 * rm;
   r.sr1 = er * sr;
   r.dx_g = m * si;
-  r.u = r.dx_g * x;
-  r.dgi_g = r.u * (ei * si);
+  r.q = x * (ei * si);
   const float wa = 0.5f * w * r.a;
   r.v_a = wa;
   r.v_u = wa * r.a * rm * (si * x);

@@ -16,6 +16,7 @@
 
 #include "mesa_common.h"
 #include "mesa_kernels.h"
+#include "mesa_lru_gate.h"
 #include "mesa_rows.h"
 
 namespace mesa {
@@ -59,6 +60,38 @@ __device__ __forceinline__ void join_rows(Pair own, int row, Pair& before, Pair&
   before = Pair{later2 ? both.A : in_two.A, later2 ? both.E : in_two.E};
 }
 
+// Tiles of different chains need no order, so chains are dealt to at most 64
+// classes, each with a ticket counter on a cache line of its own: one counter
+// for all hands out a ticket every 14 ns, which took longer than the tiles.
+// Workgroup i takes one tile of class i % classes; a class's tickets run over
+// its chains, then over time.
+constexpr int kLruClasses = 64, kLruCounterStride = 16;  // (in 4-byte words)
+
+struct LruGrid {
+  int slabs, tiles, chains, classes, share;
+  __host__ __device__ LruGrid(int B, int T, int D, int L)
+      : slabs((D + kLruSlab - 1) / kLruSlab), tiles(T > L ? (T + L - 1) / L : 1), chains(B * slabs),
+        share((chains + kLruClasses - 1) / kLruClasses) {  // chains of a class; the last may have fewer
+    classes = (chains + share - 1) / share;
+  }
+  __host__ unsigned workgroups() const { return tiles > 1 ? (unsigned)classes * share * tiles : (unsigned)chains; }
+  // This workgroup's tile (in the scan's order) and chain; false if its class has none left.
+  __device__ bool take(unsigned* tickets, unsigned* lds, int& j, int& chain) const {
+    if (tiles == 1) {
+      j = 0;
+      chain = blockIdx.x;
+      return true;
+    }
+    const int q = blockIdx.x % classes, m = (chains - q + classes - 1) / classes;
+    if (threadIdx.x == 0) *lds = atomicAdd(tickets + q * kLruCounterStride, 1u);
+    __syncthreads();
+    const unsigned t = __builtin_amdgcn_readfirstlane(*lds);
+    j = t / m;
+    chain = q + classes * (int)(t % m);
+    return j < tiles;
+  }
+};
+
 // A published pair is one 64-bit word, so that a reader sees it whole or not at
 // all and no ordering with other memory is needed.  kLruEmpty (written by
 // lru_clear_kernel before the tiles run) marks a word not yet published; its
@@ -90,82 +123,104 @@ __device__ __forceinline__ void await(const uint64_t* word, int count, Pair (&p)
     p[i] = i < count ? Pair{__uint_as_float((uint32_t)v[i]), __uint_as_float((uint32_t)(v[i] >> 32))} : Pair{1.f, 0.f};
 }
 
-// The state before tile j (of `tiles`, counted in the scan's direction) of one
-// chain, from the state before tile 0, in a wave with one lane per channel.
-// Publishes this tile's pair first, so nobody waits for this wave longer than
-// for its own loads; then folds the pairs of whole groups of tiles and of the
-// tiles before j in its own group, each in order.  Which words are folded in
-// which order depends on j alone: the result has the same bits in every run.
-// Every wait ends: tiles take tickets in order, so a tile that is waited for is
-// already running, and it publishes before it waits; a group's pair is
-// published by its last tile, which waits for tiles only.
-__device__ __forceinline__ float lru_carry(uint64_t* words, int tiles, int j, int lane, Pair own, float h) {
-  uint64_t* tile_words = words + lane;
-  uint64_t* group_words = words + (size_t)tiles * kLruSlab + lane;
-  publish(tile_words + (size_t)j * kLruSlab, own);
-  const int g = j / kLruGroup, i = j % kLruGroup;
-  constexpr int N = 8;
-  static_assert(kLruGroup == 2 * N, "a group's earlier tiles are two batches");
-  // the group's pair first: later groups wait for it
-  Pair tile0[N], tile1[N];
-  await<N>(tile_words + (size_t)g * kLruGroup * kLruSlab, i, tile0);
-  await<N>(tile_words + ((size_t)g * kLruGroup + N) * kLruSlab, i - N, tile1);
-  if (i == kLruGroup - 1) {
-    Pair all = tile0[0];
+// How tile j of a chain gets the state before it, from the state before tile 0:
+// the pairs of the whole groups before its own are folded in order, then those
+// of the earlier tiles of its group.  Which words are folded in which order
+// depends on j alone, so the result has the same bits in every run.  The tile
+// publishes its own pair before it waits for any; the last tile of a group also
+// publishes the group's, once it has the others.  Every wait ends: a class's
+// tiles are handed out by tickets in the scan's order, so the first tile of a
+// class that is not finished belongs to a workgroup that is running, and all
+// that it waits for is published.
+constexpr int kLruBatch = kLruGroup / 2;  // words one wave waits for at a time
+
+// Three waves share the waiting, one lane per channel; each leaves its part of
+// the fold in LDS.
+struct LruCarry {
+  Pair early[kLruSlab], late[kLruSlab];  // the group's earlier tiles, in two batches
+  float h[kLruSlab];                     // the state behind the last whole group
+};
+
+template <int N>
+__device__ __forceinline__ Pair fold(const Pair (&p)[N]) {
+  Pair all = p[0];
 #pragma unroll
-    for (int k = 1; k < N; ++k) all = join(all, tile0[k]);
-#pragma unroll
-    for (int k = 0; k < N; ++k) all = join(all, tile1[k]);
-    publish(group_words + (size_t)g * kLruSlab, join(all, own));
-  }
-  for (int g0 = 0; g0 < g; g0 += N) {
-    Pair p[N];
-    await<N>(group_words + (size_t)g0 * kLruSlab, g - g0, p);
-#pragma unroll
-    for (int k = 0; k < N; ++k) h = apply(p[k], h);
-  }
-#pragma unroll
-  for (int k = 0; k < N; ++k) h = apply(tile0[k], h);
-#pragma unroll
-  for (int k = 0; k < N; ++k) h = apply(tile1[k], h);
-  return h;
+  for (int k = 1; k < N; ++k) all = join(all, p[k]);
+  return all;
 }
 
-// 4 neighbouring channels of a token.
+__device__ __forceinline__ void carry_tiles(const uint64_t* words, int j, int part, int lane, Pair* to) {
+  const int g = j / kLruGroup, i = j % kLruGroup - part * kLruBatch;
+  Pair p[kLruBatch];
+  await<kLruBatch>(words + (size_t)(g * kLruGroup + part * kLruBatch) * kLruSlab + lane, i, p);
+  to[lane] = fold(p);
+}
+
+__device__ __forceinline__ void carry_groups(const uint64_t* words, int tiles, int j, int lane, float h, float* to) {
+  const int g = j / kLruGroup;
+  const uint64_t* group = words + (size_t)tiles * kLruSlab + lane;
+  for (int g0 = 0; g0 < g; g0 += kLruBatch) {
+    Pair p[kLruBatch];
+    await<kLruBatch>(group + (size_t)g0 * kLruSlab, g - g0, p);
+#pragma unroll
+    for (int k = 0; k < kLruBatch; ++k) h = apply(p[k], h);
+  }
+  to[lane] = h;
+}
+
+// 4 neighbouring channels of a token as stored (bf16: two to a word, so that the
+// compiler keeps them packed).
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 __attribute__((aligned(2))) u32x2_any;
 template <bool BF16>
 struct Raw4;
 template <>
 struct Raw4<true> {
-  u16x4 v;
-  __device__ __forceinline__ float at(int e) const { return bf16_to_f32(v[e]); }
+  u32x2 v;
+  __device__ __forceinline__ float at(int e) const {
+    return __uint_as_float(e & 1 ? v[e >> 1] & 0xFFFF0000u : v[e >> 1] << 16);
+  }
 };
 template <>
 struct Raw4<false> {
   f32x4 v;
   __device__ __forceinline__ float at(int e) const { return v[e]; }
 };
+template <bool BF16>
+__device__ __forceinline__ void clear_if(bool off, Raw4<BF16>& r) {
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 2 : 4); ++i) r.v[i] = __builtin_unpredictable(off) ? 0 : r.v[i];
+}
 
-// Channels off[t] .. off[t]+3 from `q` on of N rows, the first n of them the row's.
+// The 4 channels at `base` (uniform) + off[t] bytes of N rows, of which the
+// first n are the row's.  One branch for all rows: only the last lanes of a slab
+// that D ends in take the second.
 template <bool BF16, int N>
-__device__ __forceinline__ void load_raw4(const void* q_, const uint32_t (&off)[N], int n, Raw4<BF16> (&r)[N]) {
-  typedef typename std::conditional<BF16, uint16_t, float>::type T;
-  typedef typename std::conditional<BF16, u16x4_any, f32x4_any>::type V;
-  const T* q = static_cast<const T*>(q_);
+__device__ __forceinline__ void load_raw4(const void* base, const uint32_t (&off)[N], int n, Raw4<BF16> (&r)[N]) {
+  typedef typename std::conditional<BF16, u32x2_any, f32x4_any>::type V;
+  const char* q = static_cast<const char*>(base);
   if (n >= 4) {
 #pragma unroll
     for (int t = 0; t < N; ++t) r[t].v = *reinterpret_cast<const V*>(q + off[t]);
   } else {
 #pragma unroll
-    for (int t = 0; t < N; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) r[t].v[e] = e < n ? q[off[t] + e] : T(0);
+    for (int t = 0; t < N; ++t) {
+      if constexpr (BF16) {
+        const uint16_t* e = reinterpret_cast<const uint16_t*>(q + off[t]);
+        r[t].v = u32x2{(n > 0 ? e[0] : 0u) | (n > 1 ? (uint32_t)e[1] << 16 : 0u), n > 2 ? e[2] : 0u};
+      } else {
+        const float* e = reinterpret_cast<const float*>(q + off[t]);
+        r[t].v = f32x4{n > 0 ? e[0] : 0.f, n > 1 ? e[1] : 0.f, n > 2 ? e[2] : 0.f, 0.f};
+      }
+    }
   }
 }
 
+// The first n of 4 channels to `base` + off bytes, rounded to nearest even.
 template <bool BF16>
-__device__ __forceinline__ void store_raw4(void* base, size_t elem, const float (&y)[4], int n) {
+__device__ __forceinline__ void store_raw4(void* base, size_t off, const float (&y)[4], int n) {
+  char* q = static_cast<char*>(base) + off;
   if constexpr (BF16) {
-    uint16_t* q = static_cast<uint16_t*>(base) + elem;
     u16x4 o;
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = __builtin_bit_cast(uint16_t, f32_to_bf16(y[e]));
@@ -174,17 +229,36 @@ __device__ __forceinline__ void store_raw4(void* base, size_t elem, const float 
     } else {
 #pragma unroll
       for (int e = 0; e < 3; ++e)
-        if (e < n) q[e] = o[e];
+        if (e < n) reinterpret_cast<uint16_t*>(q)[e] = o[e];
     }
   } else {
-    float* q = static_cast<float*>(base) + elem;
     if (n >= 4) {
       *reinterpret_cast<f32x4_any*>(q) = f32x4{y[0], y[1], y[2], y[3]};
     } else {
 #pragma unroll
       for (int e = 0; e < 3; ++e)
-        if (e < n) q[e] = y[e];
+        if (e < n) reinterpret_cast<float*>(q)[e] = y[e];
     }
+  }
+}
+
+__device__ __forceinline__ int lru_length(const LruParams& p, int b) {
+  return p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
+}
+
+// The rates of 4 neighbouring channels, of which the first n are the row's:
+// formed by lru_ready_kernel where it runs, else here.
+__device__ __forceinline__ void lru_rates(const LruParams& p, bool ready, int ch, int n, float (&rate)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) rate[e] = 0.f;
+  if (ready && n >= 4) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(p.rates + ch);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) rate[e] = v[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) rate[e] = ready ? p.rates[ch + e] : lru_rate(p.lam[ch + e], p.c);
   }
 }
 
