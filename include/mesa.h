@@ -507,7 +507,7 @@ mesa_status mesa_qk_preprocess(int32_t B, int32_t H, int32_t T, int32_t d, int32
  *                               token (h0 for a length of 0); the next call's
  *                               h0 and a decode state.  May be h0 itself
  *   workspace           mesa_lru_workspace_bytes(d) bytes; on return its first
- *                       part holds the state before every 64th token, for
+ *                       part holds the state before every 16th token, for
  *                       mesa_lru_bwd
  *
  * Arithmetic and states are fp32 for either dtype.  Every sum is formed in a

@@ -100,6 +100,8 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
 #pragma unroll
     for (int s = 1; s < TW; ++s) own = join(own, Pair{a[s][e], u[s][e]});
     join_rows<false>(own, row, before[e], all);
+    settle(before[e].A);
+    settle(before[e].E);
     if (row == 0) waves[wave][c4 + e] = all;
   }
   __syncthreads();

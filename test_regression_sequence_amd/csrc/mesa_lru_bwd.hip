@@ -23,16 +23,16 @@ constexpr int kThreads = 256;
 template <bool BF16>
 struct BwdTile {
   static constexpr int TW = 4, NW = 4, L = 4 * NW * TW;
-  static constexpr int CW = kLruChunk / (4 * TW);  // waves of a chunk of the kept states
-  static_assert(NW >= 4 && NW % CW == 0, "three waves wait for other tiles; tiles hold whole chunks");
+  static_assert(NW >= 4, "three waves wait for other tiles, one folds this one's");
+  static_assert(4 * TW == kLruChunk, "a wave's tokens start at a kept state");
 };
 
 template <bool BF16>
-__global__ __launch_bounds__(256, 2) void lru_bwd_kernel(LruParams p) {
+__global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
   using Sh = BwdTile<BF16>;
-  constexpr int TW = Sh::TW, NW = Sh::NW, L = Sh::L, CW = Sh::CW;
+  constexpr int TW = Sh::TW, NW = Sh::NW, L = Sh::L;
   constexpr uint32_t ES = BF16 ? 2 : 4;
-  __shared__ Pair waves[NW][kLruSlab], pre[NW][kLruSlab], fwd[NW][kLruSlab];
+  __shared__ Pair waves[NW][kLruSlab], pre[NW][kLruSlab];
   __shared__ LruCarry carry;
   __shared__ float sums[NW][kLruSlab];
   __shared__ unsigned ticket;
@@ -86,8 +86,8 @@ __global__ __launch_bounds__(256, 2) void lru_bwd_kernel(LruParams p) {
     load_raw4<BF16>(static_cast<const char*>(p.gi) + in, off, nch, gi);
     load_raw4<BF16>(static_cast<const char*>(p.x) + in, off, nch, x);
     load_raw4<BF16>(static_cast<const char*>(p.dy) + first * p.D * ES, doff, nch, dy);
-    {  // the state before this lane's chunk
-      const int chunk = min(t0, n - 1) / kLruChunk;
+    {  // the state before this wave's tokens
+      const int chunk = min(j * L + wave * kLruChunk, n - 1) / kLruChunk;
       const uint32_t none[1] = {0};
       Raw4<false> r[1];
       load_raw4<false>(p.states + ((size_t)b * p.NC + chunk) * p.D + ch, none, nch, r);
@@ -129,20 +129,34 @@ __global__ __launch_bounds__(256, 2) void lru_bwd_kernel(LruParams p) {
       }
     }
   }
-  Pair before[4], earlier[4];
+
+#pragma unroll
+  for (int s = 0; s < TW; ++s) repack(x[s]);
+  // the states before this lane's tokens, and with them v / g = vu - va h
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    Pair all;
-    Pair back{a[TW - 1][e], a[TW - 1][e] * dy[TW - 1].at(e)};
+    Pair on{a[0][e], dxg[0][e] * x[0].at(e)}, earlier, all;
+#pragma unroll
+    for (int s = 1; s < TW; ++s) on = join(on, Pair{a[s][e], dxg[s][e] * x[s].at(e)});
+    join_rows<false>(on, row, earlier, all);
+    h[e] = apply(earlier, h[e]);
+#pragma unroll
+    for (int s = 0; s < TW; ++s) {
+      vu[s][e] = __builtin_fmaf(-va[s][e], h[e], vu[s][e]);
+      settle(vu[s][e]);
+      h[e] = __builtin_fmaf(a[s][e], h[e], dxg[s][e] * x[s].at(e));
+    }
+  }
+  Pair before[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    Pair back{a[TW - 1][e], a[TW - 1][e] * dy[TW - 1].at(e)}, all;
 #pragma unroll
     for (int s = TW - 2; s >= 0; --s) back = join(back, Pair{a[s][e], a[s][e] * dy[s].at(e)});
     join_rows<true>(back, row, before[e], all);
+    settle(before[e].A);
+    settle(before[e].E);
     if (row == 0) waves[wave][c4 + e] = all;
-    Pair on{a[0][e], dxg[0][e] * x[0].at(e)};
-#pragma unroll
-    for (int s = 1; s < TW; ++s) on = join(on, Pair{a[s][e], dxg[s][e] * x[s].at(e)});
-    join_rows<false>(on, row, earlier[e], all);
-    if (CW > 1 && row == 0) fwd[wave][c4 + e] = all;
   }
   __syncthreads();
   uint64_t* words = p.words + (size_t)chain * lru_chain_words(tiles);
@@ -160,34 +174,20 @@ __global__ __launch_bounds__(256, 2) void lru_bwd_kernel(LruParams p) {
   } else if (wave < 4) {
     carry_tiles(words, i, wave - 2, lane, wave == 2 ? carry.early : carry.late);
   }
-  // the states before this lane's tokens, and with them v / g = vu - va h
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if constexpr (CW > 1) {
-      const int w0 = wave / CW * CW;
-#pragma unroll
-      for (int w = 0; w < CW - 1; ++w)
-        if (w0 + w < wave) h[e] = apply(fwd[w0 + w][c4 + e], h[e]);
-    }
-    h[e] = apply(earlier[e], h[e]);
-#pragma unroll
-    for (int s = 0; s < TW; ++s) {
-      vu[s][e] = __builtin_fmaf(-va[s][e], h[e], vu[s][e]);
-      h[e] = __builtin_fmaf(a[s][e], h[e], dxg[s][e] * x[s].at(e));
-    }
-  }
   __syncthreads();
   if (wave == 0 && i % kLruGroup == kLruGroup - 1)
     publish(words + (size_t)(tiles + i / kLruGroup) * kLruSlab + lane,
             join(join(carry.early[lane], carry.late[lane]), tile));
+
+#pragma unroll
+  for (int s = 0; s < TW; ++s) repack(dy[s]);
   float c[4], vsum[4] = {};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     c[e] = apply(carry.late[c4 + e], apply(carry.early[c4 + e], carry.h[c4 + e]));
     c[e] = apply(before[e], apply(pre[wave][c4 + e], c[e]));
   }
-#pragma unroll
-  for (int s = TW - 1; s >= 0; --s) {
+  auto token = [&](int s, int valid) {
     float dx[4], dga[4], dgi[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -198,11 +198,16 @@ __global__ __launch_bounds__(256, 2) void lru_bwd_kernel(LruParams p) {
       dga[e] = v * sr1[s][e];
       c[e] = a[s][e] * g;
     }
-    if (whole || t0 + s < p.T) {
-      store_raw4<BF16>(static_cast<char*>(p.dx) + grad, goff + s * grow, dx, nch);
-      store_raw4<BF16>(static_cast<char*>(p.dga) + grad, goff + s * grow, dga, nch);
-      store_raw4<BF16>(static_cast<char*>(p.dgi) + grad, goff + s * grow, dgi, nch);
-    }
+    store_raw4<BF16>(static_cast<char*>(p.dx) + grad, goff + s * grow, dx, valid);
+    store_raw4<BF16>(static_cast<char*>(p.dga) + grad, goff + s * grow, dga, valid);
+    store_raw4<BF16>(static_cast<char*>(p.dgi) + grad, goff + s * grow, dgi, valid);
+  };
+  if (whole && nch >= 4) {
+#pragma unroll
+    for (int s = TW - 1; s >= 0; --s) token(s, 4);
+  } else {
+#pragma unroll
+    for (int s = TW - 1; s >= 0; --s) token(s, t0 + s < p.T ? nch : 0);
   }
   if (p.dh0 && t0 == 0) store_raw4<false>(p.dh0, ((size_t)b * p.D + ch) * 4, c, nch);
 #pragma unroll

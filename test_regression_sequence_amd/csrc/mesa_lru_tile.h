@@ -192,6 +192,21 @@ __device__ __forceinline__ void clear_if(bool off, Raw4<BF16>& r) {
   for (int i = 0; i < (BF16 ? 2 : 4); ++i) r.v[i] = __builtin_unpredictable(off) ? 0 : r.v[i];
 }
 
+// Has v formed here.  The compiler otherwise moves work whose result is needed
+// late behind the barriers, with all of its operands held until then.
+__device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
+
+// Hides that r is still what was loaded, so that a later use unpacks it again
+// instead of holding its floats in registers meanwhile.
+template <bool BF16>
+__device__ __forceinline__ void repack(Raw4<BF16>& r) {
+  if constexpr (BF16) {
+    uint32_t a = r.v[0], b = r.v[1];
+    asm volatile("" : "+v"(a), "+v"(b));
+    r.v = u32x2{a, b};
+  }
+}
+
 // The 4 channels at `base` (uniform) + off[t] bytes of N rows, of which the
 // first n are the row's.  One branch for all rows: only the last lanes of a slab
 // that D ends in take the second.
