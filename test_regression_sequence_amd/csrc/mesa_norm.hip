@@ -271,8 +271,10 @@ __global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* part, floa
   __shared__ float sums[16][16];
   const int j = threadIdx.x % 16, slice = threadIdx.x / 16, c = blockIdx.x * 16 + j;
   float v = 0.f;
-  if (c < D)
+  if (c < D) {
+#pragma unroll 8
     for (int g = slice; g < G; g += 16) v += part[(size_t)g * D + c];
+  }
   sums[slice][j] = v;
   __syncthreads();
   if (slice == 0 && c < D) {

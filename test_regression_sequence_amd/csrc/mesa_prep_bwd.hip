@@ -175,18 +175,33 @@ __global__ __launch_bounds__(256) void prep_bwd_empty_kernel(PrepBwdParams p, lo
     static_cast<float*>(p.dhist[which])[i] = p.d_hist[which] ? static_cast<const float*>(p.d_hist[which])[i] : 0.f;
 }
 
-constexpr int kSteps = 32;
+// Tokens that a group walks.  A walk takes the time of its steps one after the
+// other, so few rows are walked in short pieces, although then (W-1)/8 of the
+// work is done twice.  Short against long walks in us, bf16, W = 4, d = 128, by
+// the waves that long walks would take: 9.9 / 22.4 at 72, 22.8 / 25.6 at 576,
+// 34.9 / 34.3 at 1136, 60.1 / 61.4 at 2272, 122.9 / 118.5 at 4544; the short
+// ones also lose less where a workgroup's rows end behind the sequence (d = 16,
+// T = 4096, fp32: 40.8 / 57.2 at 1064).
+constexpr int kLong = 32, kShort = 8;
 
-int prep_bwd_tiles(int T, int D, int W) {
-  const long long tile = (long long)(kThreads / (D / 8)) * (kSteps - (W - 1));
+int prep_bwd_tiles(int T, int D, int W, int steps) {
+  const long long tile = (long long)(kThreads / (D / 8)) * (steps - (W - 1));
   return (int)((T + tile - 1) / tile);
+}
+
+int prep_bwd_steps(int BH, int T, int D, int W) {
+  const long long waves = 2LL * BH * ((T + kLong - W) / (kLong - W + 1)) * (D / 8) / 64;
+  return waves < 4096 ? kShort : kLong;
 }
 
 template <bool BF16, int D, int W>
 hipError_t launch_w(const PrepBwdParams& p, hipStream_t s) {
-  const int tiles = p.T > 0 ? prep_bwd_tiles(p.T, D, W) : 0;
+  const int steps = prep_bwd_steps(p.BH, p.T, D, W), tiles = p.T > 0 ? prep_bwd_tiles(p.T, D, W, steps) : 0;
   if (tiles > 0) {
-    hipLaunchKernelGGL((prep_bwd_kernel<BF16, D, W, kSteps>), dim3(tiles, p.BH, 2), dim3(kThreads), 0, s, p);
+    if (steps == kShort)
+      hipLaunchKernelGGL((prep_bwd_kernel<BF16, D, W, kShort>), dim3(tiles, p.BH, 2), dim3(kThreads), 0, s, p);
+    else
+      hipLaunchKernelGGL((prep_bwd_kernel<BF16, D, W, kLong>), dim3(tiles, p.BH, 2), dim3(kThreads), 0, s, p);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   } else if (W > 1) {
     const long long n = (long long)p.BH * (W - 1) * D;
@@ -221,7 +236,7 @@ hipError_t launch_t(int D, const PrepBwdParams& p, hipStream_t s) {
 }  // namespace
 
 size_t qk_prep_bwd_scratch(int BH, int T, int D, int W) {
-  return (size_t)2 * BH * prep_bwd_tiles(T, D, W) * D * W * sizeof(float);
+  return (size_t)2 * BH * prep_bwd_tiles(T, D, W, prep_bwd_steps(BH, T, D, W)) * D * W * sizeof(float);
 }
 
 hipError_t launch_qk_prep_bwd(bool bf16, int D, const PrepBwdParams& p, hipStream_t s) {

@@ -594,84 +594,96 @@ def decode_step_ex(q, k, v, gamma, beta, lam, h_state, g_state, *, x_state=None,
 
 
 # ---- operators around the layer ------------------------------------------------
+#
+# Every tensor of a call has to be on one device, the first argument's, and a
+# given stream too; the call is launched there whatever device is current.  What
+# a call allocates belongs to the stream it runs on, so that its memory is given
+# on in that stream's order.
 
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-class _Launch:
-    """The device and stream of a call: every tensor has to be on that device, and
-    what the call allocates belongs to the stream it is used on, so that its memory
-    is given on in that stream's order."""
-
-    def __init__(self, dev: torch.device, stream, named):
-        for name, t in named:
-            if t is not None and t.device != dev:
-                raise MesaError(f"{name} is on {t.device}, expected {dev}")
-        if stream is not None and stream.device != dev:
-            raise MesaError(f"the stream belongs to {stream.device}, the tensors to {dev}")
-        self.dev, self.stream = dev, stream
-        self.handle = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
-
-    def empty(self, shape, dtype) -> torch.Tensor:
-        if self.stream is None:
-            return torch.empty(shape, device=self.dev, dtype=dtype)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, device=self.dev, dtype=dtype)
-
-    def result(self, out: Optional[dict], key: str, shape, dtype) -> torch.Tensor:
-        """out[key], checked, or a new tensor."""
-        t = out.get(key) if out else None
-        if t is None:
-            return self.empty(shape, dtype)
-        _need(t, key, shape, dtype)
-        if t.device != self.dev:
-            raise MesaError(f"{key} is on {t.device}, expected {self.dev}")
-        return t
-
-    def scratch(self, workspace: Optional[torch.Tensor], need: int):
-        """(the workspace or a new one, its bytes)"""
-        if workspace is None:
-            workspace = self.empty(need, torch.uint8)
-        elif not workspace.is_contiguous() or workspace.device != self.dev:
-            raise MesaError(f"workspace must be contiguous and on {self.dev}")
-        return workspace, workspace.numel() * workspace.element_size()
-
-    def call(self, what: str, *args):
-        """The library's function `what` with this device current (launches go to the current device)."""
-        fn = getattr(lib(), what)
-        if self.dev.index == torch.cuda.current_device():
-            code = fn(*args, self.handle)
-        else:
-            with torch.cuda.device(self.dev):
-                code = fn(*args, self.handle)
-        _check(code, what)
-
-
 def _code_of(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.float32:
-        return MESA_F32
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return MESA_BF16
+    if t.dtype is torch.float32:
+        return MESA_F32
     raise MesaError(f"{name} must be float32 or bfloat16, got {t.dtype}")
 
 
-def _token_stride(named, shape, dtype) -> int:
+def _want(t: Optional[torch.Tensor], name: str, shape, dtype, dev):
+    """t (None passes) is a dense tensor of this shape and type on dev."""
+    if t is None or (t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous()):
+        return
+    _need(t, name, shape, dtype)
+    raise MesaError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _home(t: torch.Tensor, name: str, dims: int, stream) -> torch.device:
+    """The device of a call's first argument, which has `dims` dimensions."""
+    if not t.is_cuda:
+        raise MesaError(f"{name} must be a device tensor")
+    if t.dim() != dims:
+        raise MesaError(f"{name} has shape {tuple(t.shape)}, expected {dims} dimensions")
+    if stream is not None and stream.device != t.device:
+        raise MesaError(f"the stream belongs to {stream.device}, {name} is on {t.device}")
+    return t.device
+
+
+def _new(shape, dtype, dev, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, device=dev, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, device=dev, dtype=dtype)
+
+
+def _result(out: Optional[dict], key: str, shape, dtype, dev, stream) -> torch.Tensor:
+    """out[key], checked, or a new tensor."""
+    t = out.get(key) if out else None
+    if t is None:
+        return _new(shape, dtype, dev, stream)
+    _want(t, key, shape, dtype, dev)
+    return t
+
+
+def _scratch(workspace: Optional[torch.Tensor], need, dev, stream):
+    """(a workspace of need() bytes, or the given one; its bytes)"""
+    if workspace is None:
+        workspace = _new(need(), torch.uint8, dev, stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise MesaError(f"workspace must be contiguous and on {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _launch(what: str, dev, stream, *args):
+    """The library's function `what` on the stream (None: dev's current one)."""
+    fn = getattr(lib(), what)
+    handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    if dev.index == torch.cuda.current_device():
+        code = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, handle)
+    if code:
+        _check(code, what)
+
+
+def _token_stride(named, shape, dtype, dev) -> int:
     """The common token stride of [..., D] tensors: dense, or equal slices of wider
     rows (last index contiguous, every leading index of the row-major order)."""
     ld = None
     for name, t in named:
-        if not t.is_cuda:
-            raise MesaError(f"{name} must be a device tensor")
-        if tuple(t.shape) != shape:
-            raise MesaError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-        if t.dtype != dtype:
-            raise MesaError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape or t.dtype is not dtype or t.device != dev:
+            if tuple(t.shape) != tuple(shape):
+                raise MesaError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+            raise MesaError(f"{name} must be {dtype} on {dev}, got {t.dtype} on {t.device}")
         if t.is_contiguous():
             own = shape[-1]
         else:
-            own = t.stride(-2) if t.shape[-2] > 1 else (t.stride(0) // t.shape[-2] if t.dim() == 3 else shape[-1])
-            if t.stride(-1) != 1 or own < shape[-1] or (t.dim() == 3 and t.shape[0] > 1 and t.stride(0) != own * t.shape[1]):
+            tokens = shape[-2]
+            own = t.stride(-2) if tokens > 1 else t.stride(0) if t.dim() == 3 else shape[-1]
+            if t.stride(-1) != 1 or own < shape[-1] or (t.dim() == 3 and shape[0] > 1 and t.stride(0) != own * tokens):
                 raise MesaError(f"{name} has strides {tuple(t.stride())}: rows must be slices of one row-major tensor")
         if ld is not None and own != ld:
             raise MesaError(f"{name} has token stride {own}, expected {ld}")
@@ -682,21 +694,7 @@ def _token_stride(named, shape, dtype) -> int:
 def lru_workspace_bytes(B, T, D, *, dtype=torch.bfloat16) -> int:
     """Scratch bytes of lru_fwd and lru_bwd at these sizes."""
     desc = LruDesc(B, T, D, D, 1.0, MESA_BF16 if dtype == torch.bfloat16 else MESA_F32)
-    return int(lib().mesa_lru_workspace_bytes(ctypes.byref(desc)))
-
-
-def _lru_setup(x, ga, gi, lam, c, h0, lengths):
-    """The descriptor, by reference, and the workspace bytes, after the checks of the common inputs."""
-    B, T, D = x.shape
-    code = _code_of(x, "x")
-    ld = _token_stride((("x", x), ("ga", ga), ("gi", gi)), (B, T, D), x.dtype)
-    _need(lam, "lam", (D,), torch.float32)
-    if h0 is not None:
-        _need(h0, "h0", (B, D), torch.float32)
-    if lengths is not None:
-        _need(lengths, "lengths", (B,), torch.int32)
-    desc = ctypes.byref(LruDesc(B, T, D, ld, float(c), code))
-    return desc, int(lib().mesa_lru_workspace_bytes(desc))
+    return lib().mesa_lru_workspace_bytes(ctypes.byref(desc))
 
 
 def lru_fwd(x, ga, gi, lam, *, c: float = 8.0, h0=None, lengths=None, return_state: bool = False, out=None,
@@ -710,15 +708,19 @@ def lru_fwd(x, ga, gi, lam, *, c: float = 8.0, h0=None, lengths=None, return_sta
     Returns a dict with ``y`` [B, T, D] in x's dtype and, with return_state,
     ``h_final`` [B, D] fp32.  ``workspace`` (lru_workspace_bytes long) keeps the
     states that ``lru_bwd`` can take over."""
-    B, T, D = x.shape
-    desc, need = _lru_setup(x, ga, gi, lam, c, h0, lengths)
-    go = _Launch(x.device, stream, (("ga", ga), ("gi", gi), ("lam", lam), ("h0", h0), ("lengths", lengths)))
-    res = {"y": go.result(out, "y", (B, T, D), x.dtype)}
+    dev, dt, f32 = _home(x, "x", 3, stream), x.dtype, torch.float32
+    shape = x.shape
+    B, T, D = shape
+    code, ld = _code_of(x, "x"), _token_stride((("x", x), ("ga", ga), ("gi", gi)), shape, dt, dev)
+    _want(lam, "lam", (D,), f32, dev)
+    _want(h0, "h0", (B, D), f32, dev)
+    _want(lengths, "lengths", (B,), torch.int32, dev)
+    res = {"y": _result(out, "y", shape, dt, dev, stream)}
     if return_state:
-        res["h_final"] = go.result(out, "h_final", (B, D), torch.float32)
-    workspace, wbytes = go.scratch(workspace, need)
-    go.call("mesa_lru_fwd", desc, _addr(x), _addr(ga), _addr(gi), _addr(lam), _addr(h0), _addr(lengths),
-            _addr(res["y"]), _addr(res.get("h_final")), _addr(workspace), wbytes)
+        res["h_final"] = _result(out, "h_final", (B, D), f32, dev, stream)
+    workspace, wbytes = _scratch(workspace, lambda: lru_workspace_bytes(B, T, D, dtype=dt), dev, stream)
+    _launch("mesa_lru_fwd", dev, stream, ctypes.byref(LruDesc(B, T, D, ld, c, code)), _addr(x), _addr(ga), _addr(gi),
+            _addr(lam), _addr(h0), _addr(lengths), _addr(res["y"]), _addr(res.get("h_final")), _addr(workspace), wbytes)
     return res
 
 
@@ -730,42 +732,46 @@ def lru_bwd(x, ga, gi, lam, dy, *, c: float = 8.0, h0=None, lengths=None, d_hfin
     state_grads, ``dh0`` [B, D] fp32.  ``out`` may hold dx, dga and dgi as equal
     slices of one wider tensor.  states_in_workspace: the forward ran with
     ``workspace`` and left its states there, so they are not formed again."""
-    B, T, D = x.shape
-    f32 = torch.float32
     if states_in_workspace and workspace is None:
         raise MesaError("states_in_workspace needs the forward's workspace")
-    desc, need = _lru_setup(x, ga, gi, lam, c, h0, lengths)
-    _need(dy, "dy", (B, T, D), x.dtype)
-    if d_hfinal is not None:
-        _need(d_hfinal, "d_hfinal", (B, D), f32)
-    given = {key: out.get(key) if out else None for key in ("dx", "dga", "dgi")}
-    go = _Launch(x.device, stream, (("ga", ga), ("gi", gi), ("lam", lam), ("h0", h0), ("lengths", lengths),
-                                    ("dy", dy), ("d_hfinal", d_hfinal), *given.items()))
-    res = {key: go.empty((B, T, D), x.dtype) if t is None else t for key, t in given.items()}
-    ld_grad = _token_stride(res.items(), (B, T, D), x.dtype)
-    res["dlam"] = go.result(out, "dlam", (D,), f32)
+    dev, dt, f32 = _home(x, "x", 3, stream), x.dtype, torch.float32
+    shape = x.shape
+    B, T, D = shape
+    code, ld = _code_of(x, "x"), _token_stride((("x", x), ("ga", ga), ("gi", gi)), shape, dt, dev)
+    _want(lam, "lam", (D,), f32, dev)
+    _want(h0, "h0", (B, D), f32, dev)
+    _want(lengths, "lengths", (B,), torch.int32, dev)
+    _want(dy, "dy", shape, dt, dev)
+    _want(d_hfinal, "d_hfinal", (B, D), f32, dev)
+    res = {}
+    for key in ("dx", "dga", "dgi"):
+        t = out.get(key) if out else None
+        res[key] = _new(shape, dt, dev, stream) if t is None else t
+    ld_grad = _token_stride(res.items(), shape, dt, dev) if out else D
+    res["dlam"] = _result(out, "dlam", (D,), f32, dev, stream)
     if state_grads:
-        res["dh0"] = go.result(out, "dh0", (B, D), f32)
-    workspace, wbytes = go.scratch(workspace, need)
-    go.call("mesa_lru_bwd", desc, _addr(x), _addr(ga), _addr(gi), _addr(lam), _addr(h0), _addr(lengths), _addr(dy),
-            _addr(d_hfinal), _addr(res["dx"]), _addr(res["dga"]), _addr(res["dgi"]), ld_grad, _addr(res["dlam"]),
-            _addr(res.get("dh0")), 1 if states_in_workspace else 0, _addr(workspace), wbytes)
+        res["dh0"] = _result(out, "dh0", (B, D), f32, dev, stream)
+    workspace, wbytes = _scratch(workspace, lambda: lru_workspace_bytes(B, T, D, dtype=dt), dev, stream)
+    _launch("mesa_lru_bwd", dev, stream, ctypes.byref(LruDesc(B, T, D, ld, c, code)), _addr(x), _addr(ga), _addr(gi),
+            _addr(lam), _addr(h0), _addr(lengths), _addr(dy), _addr(d_hfinal), _addr(res["dx"]), _addr(res["dga"]),
+            _addr(res["dgi"]), ld_grad, _addr(res["dlam"]), _addr(res.get("dh0")), 1 if states_in_workspace else 0,
+            _addr(workspace), wbytes)
     return res
 
 
 def lru_step(x, ga, gi, lam, h_state, *, c: float = 8.0, out=None, stream=None) -> dict:
     """One token of N sequences: x, ga, gi [N, D] (rows dense or slices of wider
     ones), h_state [N, D] fp32 updated in place.  Returns ``y`` [N, D] in x's dtype."""
-    N, D = x.shape
-    code = _code_of(x, "x")
-    ld = _token_stride((("x", x), ("ga", ga), ("gi", gi)), (N, D), x.dtype)
-    _need(lam, "lam", (D,), torch.float32)
-    _need(h_state, "h_state", (N, D), torch.float32)
-    go = _Launch(x.device, stream, (("ga", ga), ("gi", gi), ("lam", lam), ("h_state", h_state)))
-    res = {"y": go.result(out, "y", (N, D), x.dtype)}
-    go.call("mesa_lru_step", N, D, ld, float(c), code, _addr(x), _addr(ga), _addr(gi), _addr(lam), _addr(h_state),
-            _addr(res["y"]))
-    return res
+    dev, dt = _home(x, "x", 2, stream), x.dtype
+    shape = x.shape
+    N, D = shape
+    code, ld = _code_of(x, "x"), _token_stride((("x", x), ("ga", ga), ("gi", gi)), shape, dt, dev)
+    _want(lam, "lam", (D,), torch.float32, dev)
+    _want(h_state, "h_state", shape, torch.float32, dev)
+    y = _result(out, "y", shape, dt, dev, stream)
+    _launch("mesa_lru_step", dev, stream, N, D, ld, c, code, _addr(x), _addr(ga), _addr(gi), _addr(lam),
+            _addr(h_state), _addr(y))
+    return {"y": y}
 
 
 def rmsnorm(x, w, *, residual=None, eps: float = 1e-6, quant_group: Optional[int] = None,
@@ -779,29 +785,31 @@ def rmsnorm(x, w, *, residual=None, eps: float = 1e-6, quant_group: Optional[int
     [R, ceil(D/128)] (per 128 channels).  ``residual`` is s in the residual's
     dtype (return_residual; default: when a residual is given).  ``out`` may pass
     result tensors; out["residual"] may be the residual itself."""
-    R, D = x.shape
+    dev, dt = _home(x, "x", 2, stream), x.dtype
+    shape = x.shape
+    R, D = shape
     code = _code_of(x, "x")
-    _need(x, "x", (R, D))
-    _need(w, "w", (D,), torch.float32)
-    res_dtype = x.dtype if residual is None else residual.dtype
+    _want(x, "x", shape, dt, dev)
+    _want(w, "w", (D,), torch.float32, dev)
+    res_dt, res_code = dt, code
     if residual is not None:
-        _need(residual, "residual", (R, D))
-    go = _Launch(x.device, stream, (("w", w), ("residual", residual)))
-    res = {"y": go.result(out, "y", (R, D), x.dtype if quant_group is None else torch.float8_e4m3fn)}
-    if quant_group is not None:
+        res_dt, res_code = residual.dtype, _code_of(residual, "residual")
+        _want(residual, "residual", shape, res_dt, dev)
+    quant = quant_group is not None
+    res = {"y": _result(out, "y", shape, torch.float8_e4m3fn if quant else dt, dev, stream)}
+    if quant:
         groups = -(-D // quant_group) if quant_group > 0 else 1
-        res["scale"] = go.result(out, "scale", (R, groups), torch.float32)
-    if return_residual if return_residual is not None else residual is not None:
-        res["residual"] = go.result(out, "residual", (R, D), res_dtype)
-    go.call("mesa_rmsnorm", R, D, code, code if residual is None else _code_of(residual, "residual"), _addr(x),
-            _addr(residual), _addr(w), float(eps), 0 if quant_group is None else 1, quant_group or 0, _addr(res["y"]),
-            _addr(res.get("scale")), _addr(res.get("residual")))
+        res["scale"] = _result(out, "scale", (R, groups), torch.float32, dev, stream)
+    if residual is not None if return_residual is None else return_residual:
+        res["residual"] = _result(out, "residual", shape, res_dt, dev, stream)
+    _launch("mesa_rmsnorm", dev, stream, R, D, code, res_code, _addr(x), _addr(residual), _addr(w), eps,
+            1 if quant else 0, quant_group or 0, _addr(res["y"]), _addr(res.get("scale")), _addr(res.get("residual")))
     return res
 
 
 def rmsnorm_bwd_workspace_bytes(R, D) -> int:
     """Scratch bytes of rmsnorm_bwd."""
-    return int(lib().mesa_rmsnorm_bwd_workspace_bytes(R, D))
+    return lib().mesa_rmsnorm_bwd_workspace_bytes(R, D)
 
 
 def rmsnorm_bwd(s, w, dy, *, d_residual=None, eps: float = 1e-6, out=None,
@@ -811,27 +819,28 @@ def rmsnorm_bwd(s, w, dy, *, d_residual=None, eps: float = 1e-6, out=None,
     reaches s along the residual stream.  Returns ``ds`` in s's dtype (the gradient
     of the residual and of x), ``dw`` [D] fp32 and, where dy is bf16 and s fp32,
     ``dx``: ds in bf16.  out["ds"] may be d_residual itself."""
-    R, D = s.shape
-    _need(s, "s", (R, D))
-    _need(w, "w", (D,), torch.float32)
-    _need(dy, "dy", (R, D))
-    if d_residual is not None:
-        _need(d_residual, "d_residual", (R, D), s.dtype)
-    go = _Launch(s.device, stream, (("w", w), ("dy", dy), ("d_residual", d_residual)))
-    res = {"ds": go.result(out, "ds", (R, D), s.dtype), "dw": go.result(out, "dw", (D,), torch.float32)}
-    if dy.dtype != s.dtype:
-        res["dx"] = go.result(out, "dx", (R, D), dy.dtype)
-    workspace, wbytes = go.scratch(workspace, rmsnorm_bwd_workspace_bytes(R, D))
-    go.call("mesa_rmsnorm_bwd", R, D, _code_of(dy, "dy"), _code_of(s, "s"), _addr(s), _addr(w), _addr(dy),
-            _addr(d_residual), float(eps), _addr(res["ds"]), _addr(res.get("dx")), _addr(res["dw"]), _addr(workspace),
-            wbytes)
+    dev, dt = _home(s, "s", 2, stream), s.dtype
+    shape = s.shape
+    R, D = shape
+    _want(s, "s", shape, dt, dev)
+    _want(w, "w", (D,), torch.float32, dev)
+    _want(dy, "dy", shape, dy.dtype, dev)
+    _want(d_residual, "d_residual", shape, dt, dev)
+    res = {"ds": _result(out, "ds", shape, dt, dev, stream),
+           "dw": _result(out, "dw", (D,), torch.float32, dev, stream)}
+    if dy.dtype != dt:
+        res["dx"] = _result(out, "dx", shape, dy.dtype, dev, stream)
+    workspace, wbytes = _scratch(workspace, lambda: rmsnorm_bwd_workspace_bytes(R, D), dev, stream)
+    _launch("mesa_rmsnorm_bwd", dev, stream, R, D, _code_of(dy, "dy"), _code_of(s, "s"), _addr(s), _addr(w),
+            _addr(dy), _addr(d_residual), eps, _addr(res["ds"]), _addr(res.get("dx")), _addr(res["dw"]),
+            _addr(workspace), wbytes)
     return res
 
 
 def qk_preprocess_bwd_workspace_bytes(B, H, T, d, window, *, dtype=torch.bfloat16) -> int:
     """Scratch bytes of qk_preprocess_bwd."""
     code = MESA_BF16 if dtype == torch.bfloat16 else MESA_F32
-    return int(lib().mesa_qk_preprocess_bwd_workspace_bytes(B, H, T, d, window, code))
+    return lib().mesa_qk_preprocess_bwd_workspace_bytes(B, H, T, d, window, code)
 
 
 def qk_preprocess_bwd(q_raw, k_raw, w_q, w_k, d_q, d_k, *, q_hist=None, k_hist=None, d_q_hist_out=None,
@@ -841,32 +850,30 @@ def qk_preprocess_bwd(q_raw, k_raw, w_q, w_k, d_q, d_k, *, q_hist=None, k_hist=N
     dq and dk), d_q_hist_out, d_k_hist_out [B, H, W-1, d] at its history outputs or None.
     Returns ``dq_raw``, ``dk_raw`` in the raw dtype, ``dw_q``, ``dw_k`` [H, d, W] fp32 and,
     with history_grads, ``dq_hist``, ``dk_hist``."""
-    B, H, T, d = q_raw.shape
+    dev, dt, f32 = _home(q_raw, "q_raw", 4, stream), q_raw.dtype, torch.float32
+    shape = q_raw.shape
+    B, H, T, d = shape
     W = w_q.shape[-1]
-    dt, f32 = q_raw.dtype, torch.float32
+    taps, hist = (H, d, W), (B, H, W - 1, d)
     code = _code_of(q_raw, "q_raw")
-    named = {"q_raw": q_raw, "k_raw": k_raw, "w_q": w_q, "w_k": w_k, "d_q": d_q, "d_k": d_k, "q_hist": q_hist,
-             "k_hist": k_hist, "d_q_hist_out": d_q_hist_out, "d_k_hist_out": d_k_hist_out}
-    for name, t in named.items():
-        if t is None:
-            continue
-        if name in ("q_raw", "k_raw"):
-            _need(t, name, (B, H, T, d), dt)
-        elif name in ("d_q", "d_k"):
-            _need(t, name, (B, H, T, d), f32)
-        elif name in ("w_q", "w_k"):
-            _need(t, name, (H, d, W), f32)
-        else:
-            _need(t, name, (B, H, W - 1, d), dt)
-    go = _Launch(q_raw.device, stream, named.items())
-    res = {key: go.result(out, key, (B, H, T, d), dt) for key in ("dq_raw", "dk_raw")}
-    res.update((key, go.result(out, key, (H, d, W), f32)) for key in ("dw_q", "dw_k"))
+    _want(q_raw, "q_raw", shape, dt, dev)
+    _want(k_raw, "k_raw", shape, dt, dev)
+    _want(w_q, "w_q", taps, f32, dev)
+    _want(w_k, "w_k", taps, f32, dev)
+    _want(d_q, "d_q", shape, f32, dev)
+    _want(d_k, "d_k", shape, f32, dev)
+    _want(q_hist, "q_hist", hist, dt, dev)
+    _want(k_hist, "k_hist", hist, dt, dev)
+    _want(d_q_hist_out, "d_q_hist_out", hist, dt, dev)
+    _want(d_k_hist_out, "d_k_hist_out", hist, dt, dev)
+    res = {key: _result(out, key, shape, dt, dev, stream) for key in ("dq_raw", "dk_raw")}
+    res.update((key, _result(out, key, taps, f32, dev, stream)) for key in ("dw_q", "dw_k"))
     if history_grads:
-        res.update((key, go.result(out, key, (B, H, W - 1, d), dt)) for key in ("dq_hist", "dk_hist"))
-    need = int(lib().mesa_qk_preprocess_bwd_workspace_bytes(B, H, T, d, W, code))
-    workspace, wbytes = go.scratch(workspace, need)
-    go.call("mesa_qk_preprocess_bwd", B, H, T, d, W, code, _addr(q_raw), _addr(k_raw), _addr(w_q), _addr(w_k),
-            _addr(q_hist), _addr(k_hist), float(eps), _addr(d_q), _addr(d_k), _addr(d_q_hist_out),
+        res.update((key, _result(out, key, hist, dt, dev, stream)) for key in ("dq_hist", "dk_hist"))
+    workspace, wbytes = _scratch(workspace, lambda: qk_preprocess_bwd_workspace_bytes(B, H, T, d, W, dtype=dt), dev,
+                                 stream)
+    _launch("mesa_qk_preprocess_bwd", dev, stream, B, H, T, d, W, code, _addr(q_raw), _addr(k_raw), _addr(w_q),
+            _addr(w_k), _addr(q_hist), _addr(k_hist), eps, _addr(d_q), _addr(d_k), _addr(d_q_hist_out),
             _addr(d_k_hist_out), _addr(res["dq_raw"]), _addr(res["dk_raw"]), _addr(res["dw_q"]), _addr(res["dw_k"]),
             _addr(res.get("dq_hist")), _addr(res.get("dk_hist")), _addr(workspace), wbytes)
     return res
