@@ -506,9 +506,8 @@ mesa_status mesa_qk_preprocess(int32_t B, int32_t H, int32_t T, int32_t d, int32
  *   h_final   [B, D]    fp32 or NULL    out: the state behind the last valid
  *                               token (h0 for a length of 0); the next call's
  *                               h0 and a decode state.  May be h0 itself
- *   workspace           mesa_lru_workspace_bytes(d) bytes; on return its first
- *                       part holds the state before every 16th token, for
- *                       mesa_lru_bwd
+ *   workspace           mesa_lru_workspace_bytes(d) bytes; on return it holds
+ *                       states at fixed distances for mesa_lru_bwd
  *
  * Arithmetic and states are fp32 for either dtype.  Every sum is formed in a
  * fixed order: equal inputs give bitwise equal results.

@@ -41,8 +41,7 @@ int lru_chunks(const mesa_lru_desc* d) { return (d->T + mesa::kLruChunk - 1) / m
 size_t lru_state_bytes(const mesa_lru_desc* d) { return pad256((size_t)d->B * lru_chunks(d) * d->D * 4); }
 
 size_t lru_word_bytes(const mesa_lru_desc* d) {
-  const bool bf16 = d->dtype == MESA_BF16;
-  return std::max(mesa::lru_fwd_word_bytes(bf16, d->B, d->T, d->D), mesa::lru_bwd_word_bytes(bf16, d->B, d->T, d->D));
+  return std::max(mesa::lru_fwd_word_bytes(d->B, d->T, d->D), mesa::lru_bwd_word_bytes(d->B, d->T, d->D));
 }
 
 mesa::LruParams lru_params(const mesa_lru_desc* d, const void* x, const void* ga, const void* gi, const float* lam,
@@ -66,7 +65,7 @@ extern "C" {
 size_t mesa_lru_workspace_bytes(const mesa_lru_desc* d) {
   if (check_lru(d) != MESA_OK || d->T == 0) return 0;
   return lru_state_bytes(d) + mesa::kLruTicketBytes + pad256((size_t)d->D * 4) +
-         lru_word_bytes(d) + pad256(mesa::lru_bwd_part_bytes(d->dtype == MESA_BF16, d->B, d->T, d->D));
+         lru_word_bytes(d) + pad256(mesa::lru_bwd_part_bytes(d->B, d->T, d->D));
 }
 
 mesa_status mesa_lru_fwd(const mesa_lru_desc* d, const void* x, const void* ga, const void* gi, const float* lam,

@@ -124,7 +124,7 @@ struct PrepParams {
 };
 
 // Tokens per kept state of the gated linear recurrence.
-constexpr int kLruChunk = 16;
+constexpr int kLruChunk = 12;
 
 // Gated linear recurrence (mesa_lru_gate.h has the cell).
 struct LruParams {
@@ -258,9 +258,9 @@ hipError_t launch_lru_fwd(bool bf16, const LruParams& p, hipStream_t s);
 hipError_t launch_lru_bwd(bool bf16, const LruParams& p, hipStream_t s);
 // Bytes of the ticket counters, of the published pairs and of the partial sums.
 constexpr size_t kLruTicketBytes = 4096;
-size_t lru_fwd_word_bytes(bool bf16, int B, int T, int D);
-size_t lru_bwd_word_bytes(bool bf16, int B, int T, int D);
-size_t lru_bwd_part_bytes(bool bf16, int B, int T, int D);
+size_t lru_fwd_word_bytes(int B, int T, int D);
+size_t lru_bwd_word_bytes(int B, int T, int D);
+size_t lru_bwd_part_bytes(int B, int T, int D);
 // clears the words and tickets and forms the rates
 hipError_t launch_lru_ready(const LruParams& p, size_t words, hipStream_t s);
 hipError_t launch_lru_step(bool bf16, const LruParams& p, hipStream_t s);

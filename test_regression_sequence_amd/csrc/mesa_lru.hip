@@ -22,29 +22,29 @@ __device__ __forceinline__ void store1(void* base, size_t idx, float v) {
   }
 }
 
-template <bool BF16>
-struct FwdTile {
-  static constexpr int TW = BF16 ? 8 : 4, NW = 4, L = 4 * NW * TW;
-  static_assert(NW >= 4, "three waves wait, one folds the workgroup's own pairs");
-};
+// 96 tokens a tile.  Longer lanes (TW = 16, 128 tokens) leave fewer waves to a
+// CU, shorter ones (TW = 8) more tiles to join: 131 and 125 against 119 us at
+// B=1, T=32768, D=2048, bf16; workgroups of 8 waves were slower throughout.
+constexpr int kTw = 12, kNw = 4, kTile = 2 * kNw * kTw;
+static_assert(kNw >= 4, "three waves wait for other tiles, one folds this one's");
+static_assert(kTw % kLruChunk == 0, "kept states lie at a lane's first token");
 
 template <bool BF16>
 __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
-  using Sh = FwdTile<BF16>;
-  constexpr int TW = Sh::TW, NW = Sh::NW, L = Sh::L;
+  constexpr int TW = kTw, NW = kNw, L = kTile;
   constexpr uint32_t ES = BF16 ? 2 : 4;
   __shared__ Pair waves[NW][kLruSlab], pre[NW][kLruSlab];
   __shared__ LruCarry carry;
   __shared__ unsigned ticket;
   const LruGrid grid(p.B, p.T, p.D, L);
   const int tiles = grid.tiles;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane >> 4, c4 = 4 * (lane & 15);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane >> 5, c2 = 2 * (lane & 31);
   int j, chain;
   if (!grid.take(p.tickets, &ticket, j, chain)) return;
   const int b = chain / grid.slabs, c0 = (chain % grid.slabs) * kLruSlab;
-  const int ch = c0 + c4, nch = p.D - ch;
+  const int ch = c0 + c2, nch = p.D - ch;
   const int n = lru_length(p, b);
-  const int tw0 = (4 * wave + row) * TW, t0 = j * L + tw0;  // this lane's first token
+  const int tw0 = (2 * wave + row) * TW, t0 = j * L + tw0;  // this lane's first token
   const size_t first = (size_t)b * p.T + (size_t)j * L;     // the tile's first row of the tensors
   char* y = p.y ? static_cast<char*>(p.y) + first * p.D * ES : nullptr;
   const uint32_t yrow = p.D * ES, yoff = tw0 * yrow + ch * ES;
@@ -55,18 +55,18 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
       p.h_final[e] = p.h0 ? p.h0[e] : 0.f;
     }
     if (y) {
-      const float zero[4] = {};
+      const float zero[2] = {};
 #pragma unroll
       for (int s = 0; s < TW; ++s)
-        if (t0 + s < p.T) store_raw4<BF16>(y, yoff + s * yrow, zero, nch);
+        if (t0 + s < p.T) store_raw2<BF16>(y, yoff + s * yrow, zero, nch);
     }
     return;
   }
   const bool whole = (j + 1) * L <= n;
 
-  float a[TW][4], u[TW][4];
+  float a[TW][2], u[TW][2];
   {
-    Raw4<BF16> x[TW], ga[TW], gi[TW];
+    Raw2<BF16> x[TW], ga[TW], gi[TW];
     uint32_t off[TW];
 #pragma unroll
     for (int s = 0; s < TW; ++s) {  // rows behind n read row n - 1 and are not used
@@ -74,35 +74,35 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
       off[s] = ((uint32_t)t * p.ld + ch) * ES;
     }
     const size_t in = first * p.ld * ES;
-    load_raw4<BF16>(static_cast<const char*>(p.x) + in, off, nch, x);
-    load_raw4<BF16>(static_cast<const char*>(p.ga) + in, off, nch, ga);
-    load_raw4<BF16>(static_cast<const char*>(p.gi) + in, off, nch, gi);
-    float rate[4];
+    load_raw2<BF16>(static_cast<const char*>(p.x) + in, off, nch, x);
+    load_raw2<BF16>(static_cast<const char*>(p.ga) + in, off, nch, ga);
+    load_raw2<BF16>(static_cast<const char*>(p.gi) + in, off, nch, gi);
+    float rate[2];
     lru_rates(p, tiles > 1, ch, nch, rate);
 #pragma unroll
     for (int s = 0; s < TW; ++s)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) lru_cell(x[s].at(e), ga[s].at(e), gi[s].at(e), rate[e], a[s][e], u[s][e]);
+      for (int e = 0; e < 2; ++e) lru_cell(x[s].at(e), ga[s].at(e), gi[s].at(e), rate[e], a[s][e], u[s][e]);
     if (!whole) {
 #pragma unroll
       for (int s = 0; s < TW; ++s)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 2; ++e) {
           a[s][e] = __builtin_unpredictable(t0 + s >= n) ? 1.f : a[s][e];
           u[s][e] = __builtin_unpredictable(t0 + s >= n) ? 0.f : u[s][e];
         }
     }
   }
-  Pair before[4];
+  Pair before[2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < 2; ++e) {
     Pair own{a[0][e], u[0][e]}, all;
 #pragma unroll
     for (int s = 1; s < TW; ++s) own = join(own, Pair{a[s][e], u[s][e]});
     join_rows<false>(own, row, before[e], all);
     settle(before[e].A);
     settle(before[e].E);
-    if (row == 0) waves[wave][c4 + e] = all;
+    if (row == 0) waves[wave][c2 + e] = all;
   }
   __syncthreads();
   uint64_t* words = p.words + (size_t)chain * lru_chain_words(tiles);
@@ -124,33 +124,33 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
   if (wave == 0 && j % kLruGroup == kLruGroup - 1)
     publish(words + (size_t)(tiles + j / kLruGroup) * kLruSlab + lane,
             join(join(carry.early[lane], carry.late[lane]), tile));
-  float h[4];
+  float h[2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    h[e] = apply(carry.late[c4 + e], apply(carry.early[c4 + e], carry.h[c4 + e]));
-    h[e] = apply(before[e], apply(pre[wave][c4 + e], h[e]));
+  for (int e = 0; e < 2; ++e) {
+    h[e] = apply(carry.late[c2 + e], apply(carry.early[c2 + e], carry.h[c2 + e]));
+    h[e] = apply(before[e], apply(pre[wave][c2 + e], h[e]));
   }
-  if (t0 % kLruChunk == 0 && t0 < n)
-    store_raw4<false>(p.states, (((size_t)b * p.NC + t0 / kLruChunk) * p.D + ch) * 4, h, nch);
+  if (t0 < n)
+    store_raw2<false>(p.states, (((size_t)b * p.NC + t0 / kLruChunk) * p.D + ch) * 4, h, nch);
 #pragma unroll
   for (int s = 0; s < TW; ++s)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 2; ++e) {
       h[e] = __builtin_fmaf(a[s][e], h[e], u[s][e]);
       u[s][e] = h[e];
     }
   // behind n the state stays: a lane's last one is the final state wherever n lies in its tokens
-  if (p.h_final && t0 < n && n <= t0 + TW) store_raw4<false>(p.h_final, ((size_t)b * p.D + ch) * 4, h, nch);
+  if (p.h_final && t0 < n && n <= t0 + TW) store_raw2<false>(p.h_final, ((size_t)b * p.D + ch) * 4, h, nch);
   if (!y) return;
-  if (whole && nch >= 4) {
+  if (whole && nch >= 2) {
 #pragma unroll
-    for (int s = 0; s < TW; ++s) store_raw4<BF16>(y, yoff + s * yrow, u[s], 4);
+    for (int s = 0; s < TW; ++s) store_raw2<BF16>(y, yoff + s * yrow, u[s], 2);
   } else {
 #pragma unroll
     for (int s = 0; s < TW; ++s) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) u[s][e] = t0 + s < n ? u[s][e] : 0.f;
-      if (t0 + s < p.T) store_raw4<BF16>(y, yoff + s * yrow, u[s], nch);
+      for (int e = 0; e < 2; ++e) u[s][e] = t0 + s < n ? u[s][e] : 0.f;
+      if (t0 + s < p.T) store_raw2<BF16>(y, yoff + s * yrow, u[s], nch);
     }
   }
 }
@@ -191,16 +191,16 @@ hipError_t launch_lru_ready(const LruParams& p, size_t words, hipStream_t s) {
 
 template <bool BF16>
 static hipError_t launch_fwd_t(const LruParams& p, hipStream_t s) {
-  const LruGrid grid(p.B, p.T, p.D, FwdTile<BF16>::L);
+  const LruGrid grid(p.B, p.T, p.D, kTile);
   if (grid.tiles > 1) {
     if (const hipError_t e = launch_lru_ready(p, grid.chains * lru_chain_words(grid.tiles), s); e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((lru_fwd_kernel<BF16>), dim3(grid.workgroups()), dim3(64 * FwdTile<BF16>::NW), 0, s, p);
+  hipLaunchKernelGGL((lru_fwd_kernel<BF16>), dim3(grid.workgroups()), dim3(64 * kNw), 0, s, p);
   return hipGetLastError();
 }
 
-size_t lru_fwd_word_bytes(bool bf16, int B, int T, int D) {
-  const LruGrid grid(B, T, D, bf16 ? FwdTile<true>::L : FwdTile<false>::L);
+size_t lru_fwd_word_bytes(int B, int T, int D) {
+  const LruGrid grid(B, T, D, kTile);
   return grid.chains * lru_chain_words(grid.tiles) * sizeof(uint64_t);
 }
 

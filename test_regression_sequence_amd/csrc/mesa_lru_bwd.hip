@@ -20,17 +20,16 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <bool BF16>
-struct BwdTile {
-  static constexpr int TW = 4, NW = 4, L = 4 * NW * TW;
-  static_assert(NW >= 4, "three waves wait for other tiles, one folds this one's");
-  static_assert(4 * TW == kLruChunk, "a wave's tokens start at a kept state");
-};
+// 48 tokens a tile, 12 elements a lane: what the gradients need of 16 leaves room
+// for 3 workgroups a CU, of 12 for 4 (225 against 220 us at B=8, T=4096, D=2048,
+// bf16); 8 elements a lane mean half as many tokens a tile again (229 us).
+constexpr int kTw = kLruChunk / 2, kNw = 4, kTile = 2 * kNw * kTw;
+static_assert(kNw >= 4, "three waves wait for other tiles, one folds this one's");
+static_assert(2 * kTw == kLruChunk, "a wave's tokens start at a kept state");
 
 template <bool BF16>
-__global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
-  using Sh = BwdTile<BF16>;
-  constexpr int TW = Sh::TW, NW = Sh::NW, L = Sh::L;
+__global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
+  constexpr int TW = kTw, NW = kNw, L = kTile;
   constexpr uint32_t ES = BF16 ? 2 : 4;
   __shared__ Pair waves[NW][kLruSlab], pre[NW][kLruSlab];
   __shared__ LruCarry carry;
@@ -38,14 +37,14 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
   __shared__ unsigned ticket;
   const LruGrid grid(p.B, p.T, p.D, L);
   const int tiles = grid.tiles;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane >> 4, c4 = 4 * (lane & 15);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane >> 5, c2 = 2 * (lane & 31);
   int i, chain;  // i: the tile's place in the scan
   if (!grid.take(p.tickets, &ticket, i, chain)) return;
   const int b = chain / grid.slabs, c0 = (chain % grid.slabs) * kLruSlab;
-  const int ch = c0 + c4, nch = p.D - ch;
+  const int ch = c0 + c2, nch = p.D - ch;
   const int n = lru_length(p, b), live = (n + L - 1) / L;
   const int j = i < live ? live - 1 - i : i;             // the tiles with valid tokens, last first; then the others
-  const int tw0 = (4 * wave + row) * TW, t0 = j * L + tw0;  // this lane's first token
+  const int tw0 = (2 * wave + row) * TW, t0 = j * L + tw0;  // this lane's first token
   const size_t first = (size_t)b * p.T + (size_t)j * L;     // the tile's first row of the tensors
   const size_t grad = first * p.ld_grad * ES;
   const uint32_t grow = p.ld_grad * ES, goff = tw0 * grow + ch * ES;
@@ -58,22 +57,22 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
       if (part) *part = 0.f;
       if (i == 0 && p.dh0) p.dh0[e] = p.d_hfinal ? p.d_hfinal[e] : 0.f;
     }
-    const float zero[4] = {};
+    const float zero[2] = {};
 #pragma unroll
     for (int s = 0; s < TW; ++s)
       if (t0 + s < p.T) {
-        store_raw4<BF16>(static_cast<char*>(p.dx) + grad, goff + s * grow, zero, nch);
-        store_raw4<BF16>(static_cast<char*>(p.dga) + grad, goff + s * grow, zero, nch);
-        store_raw4<BF16>(static_cast<char*>(p.dgi) + grad, goff + s * grow, zero, nch);
+        store_raw2<BF16>(static_cast<char*>(p.dx) + grad, goff + s * grow, zero, nch);
+        store_raw2<BF16>(static_cast<char*>(p.dga) + grad, goff + s * grow, zero, nch);
+        store_raw2<BF16>(static_cast<char*>(p.dgi) + grad, goff + s * grow, zero, nch);
       }
     return;
   }
   const bool whole = (j + 1) * L <= n;
 
-  Raw4<BF16> x[TW], dy[TW];
-  float a[TW][4], dxg[TW][4], q[TW][4], va[TW][4], vu[TW][4], sr1[TW][4], h[4];
+  Raw2<BF16> x[TW], dy[TW];
+  float a[TW][2], dxg[TW][2], q[TW][2], va[TW][2], vu[TW][2], sr1[TW][2], h[2];
   {
-    Raw4<BF16> ga[TW], gi[TW];
+    Raw2<BF16> ga[TW], gi[TW];
     uint32_t off[TW], doff[TW];
 #pragma unroll
     for (int s = 0; s < TW; ++s) {  // rows behind n read row n - 1 and are not used
@@ -82,24 +81,24 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
       doff[s] = ((uint32_t)t * p.D + ch) * ES;
     }
     const size_t in = first * p.ld * ES;
-    load_raw4<BF16>(static_cast<const char*>(p.ga) + in, off, nch, ga);
-    load_raw4<BF16>(static_cast<const char*>(p.gi) + in, off, nch, gi);
-    load_raw4<BF16>(static_cast<const char*>(p.x) + in, off, nch, x);
-    load_raw4<BF16>(static_cast<const char*>(p.dy) + first * p.D * ES, doff, nch, dy);
+    load_raw2<BF16>(static_cast<const char*>(p.ga) + in, off, nch, ga);
+    load_raw2<BF16>(static_cast<const char*>(p.gi) + in, off, nch, gi);
+    load_raw2<BF16>(static_cast<const char*>(p.x) + in, off, nch, x);
+    load_raw2<BF16>(static_cast<const char*>(p.dy) + first * p.D * ES, doff, nch, dy);
     {  // the state before this wave's tokens
       const int chunk = min(j * L + wave * kLruChunk, n - 1) / kLruChunk;
       const uint32_t none[1] = {0};
-      Raw4<false> r[1];
-      load_raw4<false>(p.states + ((size_t)b * p.NC + chunk) * p.D + ch, none, nch, r);
+      Raw2<false> r[1];
+      load_raw2<false>(p.states + ((size_t)b * p.NC + chunk) * p.D + ch, none, nch, r);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = r[0].at(e);
+      for (int e = 0; e < 2; ++e) h[e] = r[0].at(e);
     }
-    float rate[4];
+    float rate[2];
     lru_rates(p, tiles > 1, ch, nch, rate);
 #pragma unroll
     for (int s = 0; s < TW; ++s) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 2; ++e) {
         const LruGrad r = lru_cell_grad(x[s].at(e), ga[s].at(e), gi[s].at(e), rate[e]);
         a[s][e] = r.a;
         dxg[s][e] = r.dx_g;
@@ -119,7 +118,7 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
       clear_if(off, x[s]);
       clear_if(off, dy[s]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 2; ++e) {
         a[s][e] = __builtin_unpredictable(off) ? 1.f : a[s][e];
         dxg[s][e] = __builtin_unpredictable(off) ? 0.f : dxg[s][e];
         q[s][e] = __builtin_unpredictable(off) ? 0.f : q[s][e];
@@ -134,7 +133,7 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
   for (int s = 0; s < TW; ++s) repack(x[s]);
   // the states before this lane's tokens, and with them v / g = vu - va h
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < 2; ++e) {
     Pair on{a[0][e], dxg[0][e] * x[0].at(e)}, earlier, all;
 #pragma unroll
     for (int s = 1; s < TW; ++s) on = join(on, Pair{a[s][e], dxg[s][e] * x[s].at(e)});
@@ -147,16 +146,16 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
       h[e] = __builtin_fmaf(a[s][e], h[e], dxg[s][e] * x[s].at(e));
     }
   }
-  Pair before[4];
+  Pair before[2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < 2; ++e) {
     Pair back{a[TW - 1][e], a[TW - 1][e] * dy[TW - 1].at(e)}, all;
 #pragma unroll
     for (int s = TW - 2; s >= 0; --s) back = join(back, Pair{a[s][e], a[s][e] * dy[s].at(e)});
     join_rows<true>(back, row, before[e], all);
     settle(before[e].A);
     settle(before[e].E);
-    if (row == 0) waves[wave][c4 + e] = all;
+    if (row == 0) waves[wave][c2 + e] = all;
   }
   __syncthreads();
   uint64_t* words = p.words + (size_t)chain * lru_chain_words(tiles);
@@ -181,16 +180,16 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
 
 #pragma unroll
   for (int s = 0; s < TW; ++s) repack(dy[s]);
-  float c[4], vsum[4] = {};
+  float c[2], vsum[2] = {};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    c[e] = apply(carry.late[c4 + e], apply(carry.early[c4 + e], carry.h[c4 + e]));
-    c[e] = apply(before[e], apply(pre[wave][c4 + e], c[e]));
+  for (int e = 0; e < 2; ++e) {
+    c[e] = apply(carry.late[c2 + e], apply(carry.early[c2 + e], carry.h[c2 + e]));
+    c[e] = apply(before[e], apply(pre[wave][c2 + e], c[e]));
   }
   auto token = [&](int s, int valid) {
-    float dx[4], dga[4], dgi[4];
+    float dx[2], dga[2], dgi[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 2; ++e) {
       const float g = c[e] + dy[s].at(e), v = g * vu[s][e];
       vsum[e] += v;
       dx[e] = g * dxg[s][e];
@@ -198,22 +197,22 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
       dga[e] = v * sr1[s][e];
       c[e] = a[s][e] * g;
     }
-    store_raw4<BF16>(static_cast<char*>(p.dx) + grad, goff + s * grow, dx, valid);
-    store_raw4<BF16>(static_cast<char*>(p.dga) + grad, goff + s * grow, dga, valid);
-    store_raw4<BF16>(static_cast<char*>(p.dgi) + grad, goff + s * grow, dgi, valid);
+    store_raw2<BF16>(static_cast<char*>(p.dx) + grad, goff + s * grow, dx, valid);
+    store_raw2<BF16>(static_cast<char*>(p.dga) + grad, goff + s * grow, dga, valid);
+    store_raw2<BF16>(static_cast<char*>(p.dgi) + grad, goff + s * grow, dgi, valid);
   };
-  if (whole && nch >= 4) {
+  if (whole && nch >= 2) {
 #pragma unroll
-    for (int s = TW - 1; s >= 0; --s) token(s, 4);
+    for (int s = TW - 1; s >= 0; --s) token(s, 2);
   } else {
 #pragma unroll
     for (int s = TW - 1; s >= 0; --s) token(s, t0 + s < p.T ? nch : 0);
   }
-  if (p.dh0 && t0 == 0) store_raw4<false>(p.dh0, ((size_t)b * p.D + ch) * 4, c, nch);
+  if (p.dh0 && t0 == 0) store_raw2<false>(p.dh0, ((size_t)b * p.D + ch) * 4, c, nch);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    vsum[e] = sum_lane_groups(vsum[e]);
-    if (row == 0) sums[wave][c4 + e] = vsum[e];
+  for (int e = 0; e < 2; ++e) {
+    vsum[e] = add_rows(vsum[e]);
+    if (row == 0) sums[wave][c2 + e] = vsum[e];
   }
   __syncthreads();
   if (wave == 0 && mine) {
@@ -245,11 +244,11 @@ __global__ __launch_bounds__(kThreads) void lru_dlam_kernel(const float* part, c
 
 template <bool BF16>
 hipError_t launch_t(const LruParams& p, hipStream_t s) {
-  const LruGrid grid(p.B, p.T, p.D, BwdTile<BF16>::L);
+  const LruGrid grid(p.B, p.T, p.D, kTile);
   if (grid.tiles > 1) {
     if (const hipError_t e = launch_lru_ready(p, grid.chains * lru_chain_words(grid.tiles), s); e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((lru_bwd_kernel<BF16>), dim3(grid.workgroups()), dim3(64 * BwdTile<BF16>::NW), 0, s, p);
+  hipLaunchKernelGGL((lru_bwd_kernel<BF16>), dim3(grid.workgroups()), dim3(64 * kNw), 0, s, p);
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   hipLaunchKernelGGL(lru_dlam_kernel, dim3((p.D + 15) / 16), dim3(kThreads), 0, s, p.lam_part, p.lam, p.dlam,
                      p.T > 0 ? p.B * grid.tiles : 0, p.D);
@@ -258,13 +257,13 @@ hipError_t launch_t(const LruParams& p, hipStream_t s) {
 
 }  // namespace
 
-size_t lru_bwd_word_bytes(bool bf16, int B, int T, int D) {
-  const LruGrid grid(B, T, D, bf16 ? BwdTile<true>::L : BwdTile<false>::L);
+size_t lru_bwd_word_bytes(int B, int T, int D) {
+  const LruGrid grid(B, T, D, kTile);
   return grid.chains * lru_chain_words(grid.tiles) * sizeof(uint64_t);
 }
 
-size_t lru_bwd_part_bytes(bool bf16, int B, int T, int D) {
-  const LruGrid grid(B, T, D, bf16 ? BwdTile<true>::L : BwdTile<false>::L);
+size_t lru_bwd_part_bytes(int B, int T, int D) {
+  const LruGrid grid(B, T, D, kTile);
   return (size_t)B * grid.tiles * D * sizeof(float);
 }
 

@@ -4,12 +4,15 @@
 // A token range [t0, t1) maps the state before it to the state behind it by
 // h -> A h + E with A = prod a_t and E the state that starts from zero; ranges
 // join as (A1, E1), (A2, E2) -> (A1 A2, A2 E1 + E2).  A workgroup of NW waves
-// holds a tile of 64 channels by L = 4 NW TW tokens in registers: a wave is 4
-// rows of 16 lanes, a lane holds 4 neighbouring channels of TW tokens in turn,
-// row r of wave w those from (4 w + r) TW on.  Each lane folds its tokens, the
-// rows of a wave are joined by cross-row swaps, the waves through LDS, and the
+// holds a tile of 64 channels by L = 2 NW TW tokens in registers: a wave is 2
+// rows of 32 lanes, a lane holds 2 neighbouring channels of TW tokens in turn,
+// row r of wave w those from (2 w + r) TW on.  Each lane folds its tokens, the
+// rows of a wave are joined by a cross-row swap, the waves through LDS, and the
 // tiles of one sequence and slab through device memory, so that every input is
-// read once.
+// read once.  Two channels a lane, not four in four rows of 16 lanes: the loads
+// are half as wide, but joining four rows took 22 instructions a channel, more
+// than a quarter of what a token's gradients take (126 -> 118 us forward, 237 ->
+// 225 us backward at B=8, T=4096, D=2048, bf16).
 #pragma once
 
 #include <type_traits>
@@ -20,6 +23,10 @@
 #include "mesa_rows.h"
 
 namespace mesa {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef f32x2 __attribute__((aligned(4))) f32x2_any;
+typedef uint32_t __attribute__((aligned(2))) u32_any;
 
 constexpr int kLruSlab = 64;    // channels of a tile
 constexpr int kLruGroup = 16;   // tiles whose joined pair is published as one
@@ -38,26 +45,23 @@ __device__ __forceinline__ Pair join(Pair first, Pair second) {
 }
 __device__ __forceinline__ float apply(Pair p, float h) { return __builtin_fmaf(p.A, h, p.E); }
 
-// From each row's pair: the pair of the wave's rows before this one, and of all
-// four (REV: rows run backwards in the scan, row 3 first).
+// From the pairs of a wave's two rows: that of the row before this one (the
+// identity for the first) and of both.  REV: row 1 comes first.
 template <bool REV>
 __device__ __forceinline__ void join_rows(Pair own, int row, Pair& before, Pair& all) {
-  auto swap16 = [](float v) { return __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false); };
-  auto swap32 = [](float v) { return __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false); };
-  const auto a16 = swap16(own.A), e16 = swap16(own.E);
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(own.A), __float_as_uint(own.A), false, false);
+  const auto e = __builtin_amdgcn_permlane32_swap(__float_as_uint(own.E), __float_as_uint(own.E), false, false);
   constexpr int F = REV ? 1 : 0, S = 1 - F;
-  const Pair first{__uint_as_float(a16[F]), __uint_as_float(e16[F])};
-  const Pair second{__uint_as_float(a16[S]), __uint_as_float(e16[S])};
-  const Pair two = join(first, second);
-  const bool later = ((row & 1) != 0) != REV;
-  const Pair in_two{later ? first.A : 1.f, later ? first.E : 0.f};
-  const auto a32 = swap32(two.A), e32 = swap32(two.E);
-  const Pair lo{__uint_as_float(a32[F]), __uint_as_float(e32[F])};
-  const Pair hi{__uint_as_float(a32[S]), __uint_as_float(e32[S])};
-  all = join(lo, hi);
-  const bool later2 = (row >= 2) != REV;
-  const Pair both = join(lo, in_two);
-  before = Pair{later2 ? both.A : in_two.A, later2 ? both.E : in_two.E};
+  const Pair first{__uint_as_float(a[F]), __uint_as_float(e[F])}, second{__uint_as_float(a[S]), __uint_as_float(e[S])};
+  all = join(first, second);
+  const bool later = (row != 0) != REV;
+  before = Pair{later ? first.A : 1.f, later ? first.E : 0.f};
+}
+
+// The sum over a wave's two rows, in every lane.
+__device__ __forceinline__ float add_rows(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
 // Tiles of different chains need no order, so chains are dealt to at most 64
@@ -170,28 +174,24 @@ __device__ __forceinline__ void carry_groups(const uint64_t* words, int tiles, i
   to[lane] = h;
 }
 
-// 4 neighbouring channels of a token as stored (bf16: two to a word, so that the
+// A lane's channels of a token as stored (bf16: both in a word, so that the
 // compiler keeps them packed).
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef u32x2 __attribute__((aligned(2))) u32x2_any;
 template <bool BF16>
-struct Raw4;
+struct Raw2;
 template <>
-struct Raw4<true> {
-  u32x2 v;
-  __device__ __forceinline__ float at(int e) const {
-    return __uint_as_float(e & 1 ? v[e >> 1] & 0xFFFF0000u : v[e >> 1] << 16);
-  }
+struct Raw2<true> {
+  uint32_t v;
+  __device__ __forceinline__ float at(int e) const { return __uint_as_float(e & 1 ? v & 0xFFFF0000u : v << 16); }
 };
 template <>
-struct Raw4<false> {
-  f32x4 v;
+struct Raw2<false> {
+  f32x2 v;
   __device__ __forceinline__ float at(int e) const { return v[e]; }
 };
-template <bool BF16>
-__device__ __forceinline__ void clear_if(bool off, Raw4<BF16>& r) {
+__device__ __forceinline__ void clear_if(bool off, Raw2<true>& r) { r.v = __builtin_unpredictable(off) ? 0 : r.v; }
+__device__ __forceinline__ void clear_if(bool off, Raw2<false>& r) {
 #pragma unroll
-  for (int i = 0; i < (BF16 ? 2 : 4); ++i) r.v[i] = __builtin_unpredictable(off) ? 0 : r.v[i];
+  for (int i = 0; i < 2; ++i) r.v[i] = __builtin_unpredictable(off) ? 0 : r.v[i];
 }
 
 // Has v formed here.  The compiler otherwise moves work whose result is needed
@@ -200,65 +200,43 @@ __device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
 
 // Hides that r is still what was loaded, so that a later use unpacks it again
 // instead of holding its floats in registers meanwhile.
-template <bool BF16>
-__device__ __forceinline__ void repack(Raw4<BF16>& r) {
-  if constexpr (BF16) {
-    uint32_t a = r.v[0], b = r.v[1];
-    asm volatile("" : "+v"(a), "+v"(b));
-    r.v = u32x2{a, b};
-  }
-}
+__device__ __forceinline__ void repack(Raw2<true>& r) { asm volatile("" : "+v"(r.v)); }
+__device__ __forceinline__ void repack(Raw2<false>&) {}
 
-// The tensors are streamed: loads and stores carry the nontemporal hint (forward
-// 131 -> 126 us, backward 256 -> 237 us at B=8, T=4096, D=2048, bf16).
+// The tensors are streamed: loads and stores carry the nontemporal hint (4 %
+// of the forward's time and 7 % of the backward's at that size).
 
-// The 4 channels at `base` (uniform) + off[t] bytes of N rows, of which the
-// first n are the row's.  One branch for all rows: only the last lanes of a slab
-// that D ends in take the second.
+// A lane's channels at `base` (uniform) + off[t] bytes of N rows, of which the
+// first n are the row's.  One branch for all rows: only the last lane of a slab
+// that D ends in takes the second.
 template <bool BF16, int N>
-__device__ __forceinline__ void load_raw4(const void* base, const uint32_t (&off)[N], int n, Raw4<BF16> (&r)[N]) {
-  typedef typename std::conditional<BF16, u32x2_any, f32x4_any>::type V;
+__device__ __forceinline__ void load_raw2(const void* base, const uint32_t (&off)[N], int n, Raw2<BF16> (&r)[N]) {
+  typedef typename std::conditional<BF16, u32_any, f32x2_any>::type V;
   const char* q = static_cast<const char*>(base);
-  if (n >= 4) {
+  if (n >= 2) {
 #pragma unroll
     for (int t = 0; t < N; ++t) r[t].v = __builtin_nontemporal_load(reinterpret_cast<const V*>(q + off[t]));
   } else {
 #pragma unroll
     for (int t = 0; t < N; ++t) {
-      if constexpr (BF16) {
-        const uint16_t* e = reinterpret_cast<const uint16_t*>(q + off[t]);
-        r[t].v = u32x2{(n > 0 ? e[0] : 0u) | (n > 1 ? (uint32_t)e[1] << 16 : 0u), n > 2 ? e[2] : 0u};
-      } else {
-        const float* e = reinterpret_cast<const float*>(q + off[t]);
-        r[t].v = f32x4{n > 0 ? e[0] : 0.f, n > 1 ? e[1] : 0.f, n > 2 ? e[2] : 0.f, 0.f};
-      }
+      if constexpr (BF16) r[t].v = n > 0 ? *reinterpret_cast<const uint16_t*>(q + off[t]) : 0u;
+      else r[t].v = f32x2{n > 0 ? *reinterpret_cast<const float*>(q + off[t]) : 0.f, 0.f};
     }
   }
 }
 
-// The first n of 4 channels to `base` + off bytes, rounded to nearest even.
+// The first n of a lane's channels to `base` + off bytes, rounded to nearest even.
 template <bool BF16>
-__device__ __forceinline__ void store_raw4(void* base, size_t off, const float (&y)[4], int n) {
+__device__ __forceinline__ void store_raw2(void* base, size_t off, const float (&y)[2], int n) {
   char* q = static_cast<char*>(base) + off;
   if constexpr (BF16) {
-    u16x4 o;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = __builtin_bit_cast(uint16_t, f32_to_bf16(y[e]));
-    if (n >= 4) {
-      __builtin_nontemporal_store(o, reinterpret_cast<u16x4_any*>(q));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 3; ++e)
-        if (e < n) reinterpret_cast<uint16_t*>(q)[e] = o[e];
-    }
+    const uint32_t o = __builtin_bit_cast(uint16_t, f32_to_bf16(y[0])) |
+                       (uint32_t)__builtin_bit_cast(uint16_t, f32_to_bf16(y[1])) << 16;
+    if (n >= 2) __builtin_nontemporal_store(o, reinterpret_cast<u32_any*>(q));
+    else if (n > 0) *reinterpret_cast<uint16_t*>(q) = (uint16_t)o;
   } else {
-    if (n >= 4) {
-      __builtin_nontemporal_store(f32x4{y[0], y[1], y[2], y[3]}, reinterpret_cast<f32x4_any*>(q));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 3; ++e)
-        if (e < n) reinterpret_cast<float*>(q)[e] = y[e];
-    }
+    if (n >= 2) __builtin_nontemporal_store(f32x2{y[0], y[1]}, reinterpret_cast<f32x2_any*>(q));
+    else if (n > 0) *reinterpret_cast<float*>(q) = y[0];
   }
 }
 
@@ -266,20 +244,11 @@ __device__ __forceinline__ int lru_length(const LruParams& p, int b) {
   return p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
 }
 
-// The rates of 4 neighbouring channels, of which the first n are the row's:
-// formed by lru_ready_kernel where it runs, else here.
-__device__ __forceinline__ void lru_rates(const LruParams& p, bool ready, int ch, int n, float (&rate)[4]) {
+// The rates of a lane's channels, of which the first n are the row's: formed by
+// lru_ready_kernel where it runs, else here.
+__device__ __forceinline__ void lru_rates(const LruParams& p, bool ready, int ch, int n, float (&rate)[2]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) rate[e] = 0.f;
-  if (ready && n >= 4) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(p.rates + ch);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) rate[e] = v[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < n) rate[e] = ready ? p.rates[ch + e] : lru_rate(p.lam[ch + e], p.c);
-  }
+  for (int e = 0; e < 2; ++e) rate[e] = e < n ? ready ? p.rates[ch + e] : lru_rate(p.lam[ch + e], p.c) : 0.f;
 }
 
 }  // namespace mesa
