@@ -69,10 +69,10 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
   }
   const bool whole = (j + 1) * L <= n;
 
-  Raw2<BF16> x[TW], dy[TW];
-  float a[TW][2], dxg[TW][2], q[TW][2], va[TW][2], vu[TW][2], sr1[TW][2], h[2];
+  Raw2<BF16> dy[TW];
+  float a[TW][2], u[TW][2], dxg[TW][2], q[TW][2], va[TW][2], k[TW][2], sr1[TW][2], h[2];
   {
-    Raw2<BF16> ga[TW], gi[TW];
+    Raw2<BF16> x[TW], ga[TW], gi[TW];
     uint32_t off[TW], doff[TW];
 #pragma unroll
     for (int s = 0; s < TW; ++s) {  // rows behind n read row n - 1 and are not used
@@ -101,49 +101,51 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
       for (int e = 0; e < 2; ++e) {
         const LruGrad r = lru_cell_grad(x[s].at(e), ga[s].at(e), gi[s].at(e), rate[e]);
         a[s][e] = r.a;
+        u[s][e] = r.u;
         dxg[s][e] = r.dx_g;
         q[s][e] = r.q;
-        va[s][e] = r.v_a;
-        vu[s][e] = r.v_u;
+        va[s][e] = r.va;
+        k[s][e] = r.k;
         sr1[s][e] = r.sr1;
+        settle(dxg[s][e]);
+        settle(u[s][e]);
+        settle(q[s][e]);
+        settle(va[s][e]);
+        settle(k[s][e]);
+        settle(sr1[s][e]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  // behind n: the state and the adjoint pass, and every gradient is 0
+  // behind n the state and the adjoint pass, and every gradient is 0 (the rest is
+  // finite there: it comes from row n - 1)
   if (!whole) {
 #pragma unroll
     for (int s = 0; s < TW; ++s) {
       const bool off = t0 + s >= n;
-      clear_if(off, x[s]);
       clear_if(off, dy[s]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         a[s][e] = __builtin_unpredictable(off) ? 1.f : a[s][e];
+        u[s][e] = __builtin_unpredictable(off) ? 0.f : u[s][e];
         dxg[s][e] = __builtin_unpredictable(off) ? 0.f : dxg[s][e];
-        q[s][e] = __builtin_unpredictable(off) ? 0.f : q[s][e];
         va[s][e] = __builtin_unpredictable(off) ? 0.f : va[s][e];
-        vu[s][e] = __builtin_unpredictable(off) ? 0.f : vu[s][e];
-        sr1[s][e] = __builtin_unpredictable(off) ? 0.f : sr1[s][e];
       }
     }
   }
-
-#pragma unroll
-  for (int s = 0; s < TW; ++s) repack(x[s]);
-  // the states before this lane's tokens, and with them v / g = vu - va h
+  // the states before this lane's tokens, and with them v / g = va (k - h)
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    Pair on{a[0][e], dxg[0][e] * x[0].at(e)}, earlier, all;
+    Pair on{a[0][e], u[0][e]}, earlier, all;
 #pragma unroll
-    for (int s = 1; s < TW; ++s) on = join(on, Pair{a[s][e], dxg[s][e] * x[s].at(e)});
+    for (int s = 1; s < TW; ++s) on = join(on, Pair{a[s][e], u[s][e]});
     join_rows<false>(on, row, earlier, all);
     h[e] = apply(earlier, h[e]);
 #pragma unroll
     for (int s = 0; s < TW; ++s) {
-      vu[s][e] = __builtin_fmaf(-va[s][e], h[e], vu[s][e]);
-      settle(vu[s][e]);
-      h[e] = __builtin_fmaf(a[s][e], h[e], dxg[s][e] * x[s].at(e));
+      va[s][e] *= k[s][e] - h[e];
+      settle(va[s][e]);
+      h[e] = __builtin_fmaf(a[s][e], h[e], u[s][e]);
     }
   }
   Pair before[2];
@@ -190,7 +192,7 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
     float dx[2], dga[2], dgi[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float g = c[e] + dy[s].at(e), v = g * vu[s][e];
+      const float g = c[e] + dy[s].at(e), v = g * va[s][e];
       vsum[e] += v;
       dx[e] = g * dxg[s][e];
       dgi[e] = dx[e] * q[s][e];

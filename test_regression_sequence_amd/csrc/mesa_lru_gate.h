@@ -1,8 +1,8 @@
 // The gates of the linear recurrence (MesaNet page, "architecture": the layer
 // that alternates with the Mesa layer in the Hawk-Mesa hybrid), one channel of
 // one token:
-//     s_r = sigmoid(ga),  s_i = sigmoid(gi),  w = 2 c softplus(lam) s_r = -2 log a,
-//     a = exp(-w/2),  m = sqrt(1 - a^2) = sqrt(1 - exp(-w)).
+//     s_r = sigmoid(ga),  s_i = sigmoid(gi),  t = c log2(e) softplus(lam) s_r,
+//     a = 2^-t,  m = sqrt(1 - a^2).
 // Every kernel of the recurrence forms them with these helpers, in fp32.
 #pragma once
 
@@ -10,77 +10,78 @@
 
 namespace mesa {
 
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-// 2 c softplus(lam), in fp32: softplus(z) = max(z, 0) + log(1 + exp(-|z|)).
-__device__ __forceinline__ float lru_rate(float lam, float c) {
-  return 2.f * c * (fmaxf(lam, 0.f) + log1pf(expf(-fabsf(lam))));
-}
+// softplus(z) = max(z, 0) + log(1 + exp(-|z|)).
+__device__ __forceinline__ float lru_softplus(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
 
-// sigmoid(lam) / softplus(lam), the factor from dL/d log w to dL/dlam.  Below
+// c log2(e) softplus(lam): a channel's decay in halvings per token with its gate open.
+__device__ __forceinline__ float lru_rate(float lam, float c) { return kLog2e * c * lru_softplus(lam); }
+
+// sigmoid(lam) / softplus(lam), the factor from dL/d log t to dL/dlam.  Below
 // lam = -15 both are exp(lam) to within exp(-15) = 3e-7 of themselves, and
 // their quotient is 1 - exp(lam)/2 to first order.
 __device__ __forceinline__ float lru_rate_slope(float lam) {
   if (lam < -15.f) return 1.f - 0.5f * expf(lam);
-  return 1.f / ((1.f + expf(-lam)) * (fmaxf(lam, 0.f) + log1pf(expf(-fabsf(lam)))));
+  return 1.f / ((1.f + expf(-lam)) * lru_softplus(lam));
 }
 
 __device__ __forceinline__ float lru_sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * z));
 }
 
-// 1 - exp(-w) for w >= 0, given a = exp(-w/2).  Above w = 1/4, 1 - a^2 keeps
-// all but two bits.  Below it the difference would cancel, so the alternating
-// series w (1 - w/2 + w^2/6 - ...) is summed to w^5/720: the first term left
-// out is below w^6/5040 = 5e-8 of the value.  Both are formed and one selected:
-// marked unpredictable, or the compiler makes a branch of every element.
-__device__ __forceinline__ float lru_one_minus_a2(float w, float a) {
-  float p = __builtin_fmaf(w, -1.f / 720.f, 1.f / 120.f);
-  p = __builtin_fmaf(w, p, -1.f / 24.f);
-  p = __builtin_fmaf(w, p, 1.f / 6.f);
-  p = __builtin_fmaf(w, p, -0.5f);
-  p = __builtin_fmaf(w, p, 1.f);
-  const float series = w * p, direct = __builtin_fmaf(-a, a, 1.f);
-  return __builtin_unpredictable(w < 0.25f) ? series : direct;
+// 1 - 2^-2t for t >= 0, given a = 2^-t.  With w = 2 ln2 t, 1 - a^2 keeps all but
+// two bits above w = 1/4.  Below it the difference would cancel, so the
+// alternating series w (1 - w/2 + w^2/6 - ...) is summed to w^5/720: the first
+// term left out is below w^6/5040 = 5e-8 of the value.  Both are formed and one
+// selected: marked unpredictable, or the compiler makes a branch of every
+// element.  The result is at least the smallest normal float, so that its
+// reciprocal square root is finite.
+__device__ __forceinline__ float lru_one_minus_a2(float t, float a) {
+  constexpr double k = 2 * 0.69314718055994530942;
+  float p = __builtin_fmaf(t, (float)(-k * k * k * k * k * k / 720), (float)(k * k * k * k * k / 120));
+  p = __builtin_fmaf(t, p, (float)(-k * k * k * k / 24));
+  p = __builtin_fmaf(t, p, (float)(k * k * k / 6));
+  p = __builtin_fmaf(t, p, (float)(-k * k / 2));
+  p = __builtin_fmaf(t, p, (float)k);
+  const float series = __builtin_fmaf(t, p, 0x1p-126f), direct = __builtin_fmaf(-a, a, 1.f);
+  return __builtin_unpredictable(t < (float)(0.25 / k)) ? series : direct;
 }
 
-// Decay a and input u of one token: h_t = a h_{t-1} + u.
+// Decay a and input u of one token: h_t = a h_{t-1} + u_t.
 __device__ __forceinline__ void lru_cell(float x, float ga, float gi, float rate, float& a, float& u) {
-  const float w = rate * lru_sigmoid(ga);
-  a = __builtin_amdgcn_exp2f((-0.5f * kLog2e) * w);
-  u = __builtin_amdgcn_sqrtf(lru_one_minus_a2(w, a)) * lru_sigmoid(gi) * x;
+  const float t = rate * lru_sigmoid(ga);
+  a = __builtin_amdgcn_exp2f(-t);
+  u = __builtin_amdgcn_sqrtf(lru_one_minus_a2(t, a)) * lru_sigmoid(gi) * x;
 }
 
 // The same with what the gradients need.  With g the adjoint of h_t and h1 the
 // state before the token:
-//     dx = g dx_g,  dgi = dx q,  v = g (v_u - v_a h1),  dga = v sr1,
-// q = x (1 - s_i), v = dL / d log w = (w/2) g ((a^2/m) s_i x - a h1); the input
-// is u = dx_g x.
+//     dx = g dx_g,  dgi = dx q,  v = g va (k - h1),  dga = v sr1,
+// q = x (1 - s_i), va = ln2 t a, k = (a / m) s_i x, v = dL / d log t.
 struct LruGrad {
-  float a, dx_g, q, v_u, v_a, sr1;
+  float a, u, dx_g, q, va, k, sr1;
 };
 
-// 1 - sigmoid comes as exp(-z) sigmoid(z), which keeps its bits for large z;
-// the exponent is capped at 126 so that exp(-z) stays finite (there sigmoid is
-// 2^-126 and its complement 1).  1/m is the reciprocal square root of 1 - a^2
-// raised to the smallest normal float: at w = 0 every gradient through a is
-// then w times a finite number, 0.
+// 1 - sigmoid comes as exp(-z) sigmoid(z), which keeps its bits for large z.
+// Where exp(-z) overflows that is inf * 0: for ga the product is clamped to
+// [0, 1], which makes it 0 (there t, and with it v, is 0 anyway); for gi, where
+// q has no such range, the exponent is capped at 126 instead.
 __device__ __forceinline__ LruGrad lru_cell_grad(float x, float ga, float gi, float rate) {
   LruGrad r;
-  const float er = __builtin_amdgcn_exp2f(fminf(-kLog2e * ga, 126.f));
+  const float er = __builtin_amdgcn_exp2f(-kLog2e * ga);
   const float ei = __builtin_amdgcn_exp2f(fminf(-kLog2e * gi, 126.f));
   const float sr = __builtin_amdgcn_rcpf(1.f + er), si = __builtin_amdgcn_rcpf(1.f + ei);
-  const float w = rate * sr;
-  r.a = __builtin_amdgcn_exp2f((-0.5f * kLog2e) * w);
-  const float m2 = lru_one_minus_a2(w, r.a);
-  const float rm = __builtin_amdgcn_rsqf(fmaxf(m2, 0x1p-126f));
-  const float m = m2 * rm;
-  r.sr1 = er * sr;
+  const float t = rate * sr;
+  r.a = __builtin_amdgcn_exp2f(-t);
+  const float m2 = lru_one_minus_a2(t, r.a), rm = __builtin_amdgcn_rsqf(m2), m = m2 * rm;
+  const float six = si * x;
+  r.sr1 = __builtin_amdgcn_fmed3f(er * sr, 0.f, 1.f);
   r.dx_g = m * si;
-  r.q = x * (ei * si);
-  const float wa = 0.5f * w * r.a;
-  r.v_a = wa;
-  r.v_u = wa * r.a * rm * (si * x);
+  r.u = m * six;
+  r.q = ei * six;
+  r.va = kLn2 * t * r.a;
+  r.k = r.a * rm * six;
   return r;
 }
 

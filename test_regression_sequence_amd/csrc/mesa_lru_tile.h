@@ -25,6 +25,7 @@
 namespace mesa {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef f32x2 __attribute__((aligned(4))) f32x2_any;
 typedef uint32_t __attribute__((aligned(2))) u32_any;
 
@@ -230,8 +231,7 @@ template <bool BF16>
 __device__ __forceinline__ void store_raw2(void* base, size_t off, const float (&y)[2], int n) {
   char* q = static_cast<char*>(base) + off;
   if constexpr (BF16) {
-    const uint32_t o = __builtin_bit_cast(uint16_t, f32_to_bf16(y[0])) |
-                       (uint32_t)__builtin_bit_cast(uint16_t, f32_to_bf16(y[1])) << 16;
+    const uint32_t o = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{y[0], y[1]}, bf16x2));
     if (n >= 2) __builtin_nontemporal_store(o, reinterpret_cast<u32_any*>(q));
     else if (n > 0) *reinterpret_cast<uint16_t*>(q) = (uint16_t)o;
   } else {
