@@ -51,8 +51,7 @@ mesa::LruParams lru_params(const mesa_lru_desc* d, const void* x, const void* ga
   p.states = static_cast<float*>(workspace);
   char* at = static_cast<char*>(workspace) + lru_state_bytes(d);
   p.tickets = reinterpret_cast<unsigned*>(at);
-  p.rates = reinterpret_cast<float*>(at += mesa::kLruTicketBytes);
-  p.words = reinterpret_cast<uint64_t*>(at += pad256((size_t)d->D * 4));
+  p.words = reinterpret_cast<uint64_t*>(at += mesa::kLruTicketBytes);
   p.lam_part = reinterpret_cast<float*>(at += lru_word_bytes(d));
   p.B = d->B; p.T = d->T; p.D = d->D; p.ld = d->ld; p.NC = lru_chunks(d); p.c = d->c;
   return p;
@@ -64,7 +63,7 @@ extern "C" {
 
 size_t mesa_lru_workspace_bytes(const mesa_lru_desc* d) {
   if (check_lru(d) != MESA_OK || d->T == 0) return 0;
-  return lru_state_bytes(d) + mesa::kLruTicketBytes + pad256((size_t)d->D * 4) +
+  return lru_state_bytes(d) + mesa::kLruTicketBytes +
          lru_word_bytes(d) + pad256(mesa::lru_bwd_part_bytes(d->B, d->T, d->D));
 }
 

@@ -145,7 +145,6 @@ struct LruParams {
   float* dlam;              // [D]
   float* dh0;               // [B, D] or null
   float* lam_part;          // partial sums of dL / d log w
-  float* rates;             // [D]: 2 c softplus(lam)
   uint64_t* words;          // published pairs (mesa_lru_tile.h)
   unsigned* tickets;        // tiles handed out, by class
   int B, T, D, ld, ld_grad, NC;
@@ -261,7 +260,7 @@ constexpr size_t kLruTicketBytes = 4096;
 size_t lru_fwd_word_bytes(int B, int T, int D);
 size_t lru_bwd_word_bytes(int B, int T, int D);
 size_t lru_bwd_part_bytes(int B, int T, int D);
-// clears the words and tickets and forms the rates
+// clears the words and tickets
 hipError_t launch_lru_ready(const LruParams& p, size_t words, hipStream_t s);
 hipError_t launch_lru_step(bool bf16, const LruParams& p, hipStream_t s);
 hipError_t launch_rmsnorm(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s);

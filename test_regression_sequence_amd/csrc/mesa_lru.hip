@@ -13,15 +13,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <bool BF16>
-__device__ __forceinline__ void store1(void* base, size_t idx, float v) {
-  if constexpr (BF16) {
-    static_cast<uint16_t*>(base)[idx] = __builtin_bit_cast(uint16_t, f32_to_bf16(v));
-  } else {
-    static_cast<float*>(base)[idx] = v;
-  }
-}
-
 // 96 tokens a tile.  Longer lanes (TW = 16, 128 tokens) leave fewer waves to a
 // CU, shorter ones (TW = 8) more tiles to join: 131 and 125 against 119 us at
 // B=1, T=32768, D=2048, bf16; workgroups of 8 waves were slower throughout.
@@ -78,7 +69,7 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
     load_raw2<BF16>(static_cast<const char*>(p.ga) + in, off, nch, ga);
     load_raw2<BF16>(static_cast<const char*>(p.gi) + in, off, nch, gi);
     float rate[2];
-    lru_rates(p, tiles > 1, ch, nch, rate);
+    lru_rates(p, ch, nch, rate);
 #pragma unroll
     for (int s = 0; s < TW; ++s)
 #pragma unroll
@@ -155,28 +146,35 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
   }
 }
 
-// What the tiles find ready: every word marked as not published, tickets at 0,
-// the channels' rates.  One thread does all three for its index.
-__global__ __launch_bounds__(kThreads) void lru_ready_kernel(LruParams p, size_t n) {  // n is even: a slab is 64 words
+// Marks every word as not published and sets the tickets to 0.
+__global__ __launch_bounds__(kThreads) void lru_ready_kernel(uint64_t* words, size_t n, unsigned* tickets) {
   const size_t first = (size_t)blockIdx.x * kThreads + threadIdx.x, stride = (size_t)gridDim.x * kThreads;
-  typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
-  for (size_t i = first; i < n / 2; i += stride) reinterpret_cast<u64x2*>(p.words)[i] = u64x2{kLruEmpty, kLruEmpty};
-  for (size_t i = first; i < (size_t)p.D; i += stride) p.rates[i] = lru_rate(p.lam[i], p.c);
-  if (first < kLruClasses * kLruCounterStride) p.tickets[first] = 0;
+  typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));  // (n is even: a slab is 64 words)
+  for (size_t i = first; i < n / 2; i += stride) reinterpret_cast<u64x2*>(words)[i] = u64x2{kLruEmpty, kLruEmpty};
+  if (first < kLruClasses * kLruCounterStride) tickets[first] = 0;
 }
 
+// One token: 8 channels a lane, bound by HBM (x, ga, gi and the state in, the
+// state and y out).
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void lru_step_kernel(LruParams p) {
+  const int groups = (p.D + 7) / 8;
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= (long long)p.B * p.D) return;
-  const long long n = i / p.D;
-  const int ch = (int)(i % p.D);
-  const size_t e = (size_t)n * p.ld + ch;
-  float a, u;
-  lru_cell(load1<BF16>(p.x, e), load1<BF16>(p.ga, e), load1<BF16>(p.gi, e), lru_rate(p.lam[ch], p.c), a, u);
-  const float h = __builtin_fmaf(a, p.h_final[i], u);
-  p.h_final[i] = h;
-  store1<BF16>(p.y, i, h);
+  if (i >= (long long)p.B * groups) return;
+  const size_t row = (size_t)(i / groups);
+  const int ch = (int)(i % groups) * 8, n = p.D - ch;
+  const size_t e = row * p.ld + ch, o = row * p.D + ch;
+  const Raw8<BF16> x = load_raw8<BF16>(p.x, e, n), ga = load_raw8<BF16>(p.ga, e, n), gi = load_raw8<BF16>(p.gi, e, n);
+  const Raw8<false> before = load_raw8<false>(p.h_final, o, n), lam = load_raw8<false>(p.lam, ch, n);
+  float h[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float a, u;
+    lru_cell(x.at(k), ga.at(k), gi.at(k), lru_rate(lam.at(k), p.c), a, u);
+    h[k] = __builtin_fmaf(a, before.at(k), u);
+  }
+  store_raw8<false>(p.h_final, o, h, n);
+  store_raw8<BF16>(p.y, o, h, n);
 }
 
 unsigned blocks(long long n) { return (unsigned)((n + kThreads - 1) / kThreads); }
@@ -184,8 +182,8 @@ unsigned blocks(long long n) { return (unsigned)((n + kThreads - 1) / kThreads);
 }  // namespace
 
 hipError_t launch_lru_ready(const LruParams& p, size_t words, hipStream_t s) {
-  const unsigned need = blocks(std::max<size_t>(std::max(words / 2, (size_t)p.D), kLruClasses * kLruCounterStride));
-  hipLaunchKernelGGL(lru_ready_kernel, dim3(std::min(need, 1024u)), dim3(kThreads), 0, s, p, words);
+  const unsigned need = blocks(std::max<size_t>(words / 2, kLruClasses * kLruCounterStride));
+  hipLaunchKernelGGL(lru_ready_kernel, dim3(std::min(need, 1024u)), dim3(kThreads), 0, s, p.words, words, p.tickets);
   return hipGetLastError();
 }
 
@@ -209,7 +207,7 @@ hipError_t launch_lru_fwd(bool bf16, const LruParams& p, hipStream_t s) {
 }
 
 hipError_t launch_lru_step(bool bf16, const LruParams& p, hipStream_t s) {
-  const dim3 grid(blocks((long long)p.B * p.D));
+  const dim3 grid(blocks((long long)p.B * ((p.D + 7) / 8)));
   if (bf16) hipLaunchKernelGGL((lru_step_kernel<true>), grid, dim3(kThreads), 0, s, p);
   else hipLaunchKernelGGL((lru_step_kernel<false>), grid, dim3(kThreads), 0, s, p);
   return hipGetLastError();

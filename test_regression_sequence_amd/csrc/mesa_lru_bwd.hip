@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
       for (int e = 0; e < 2; ++e) h[e] = r[0].at(e);
     }
     float rate[2];
-    lru_rates(p, tiles > 1, ch, nch, rate);
+    lru_rates(p, ch, nch, rate);
 #pragma unroll
     for (int s = 0; s < TW; ++s) {
 #pragma unroll

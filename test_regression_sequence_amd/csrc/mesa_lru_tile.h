@@ -244,11 +244,10 @@ __device__ __forceinline__ int lru_length(const LruParams& p, int b) {
   return p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
 }
 
-// The rates of a lane's channels, of which the first n are the row's: formed by
-// lru_ready_kernel where it runs, else here.
-__device__ __forceinline__ void lru_rates(const LruParams& p, bool ready, int ch, int n, float (&rate)[2]) {
+// The rates of a lane's channels, of which the first n are the row's.
+__device__ __forceinline__ void lru_rates(const LruParams& p, int ch, int n, float (&rate)[2]) {
 #pragma unroll
-  for (int e = 0; e < 2; ++e) rate[e] = e < n ? ready ? p.rates[ch + e] : lru_rate(p.lam[ch + e], p.c) : 0.f;
+  for (int e = 0; e < 2; ++e) rate[e] = lru_rate(e < n ? p.lam[ch + e] : 0.f, p.c);
 }
 
 }  // namespace mesa
