@@ -256,7 +256,7 @@ hipError_t launch_lru_fwd(bool bf16, const LruParams& p, hipStream_t s);
 // gradients, from the states launch_lru_fwd left
 hipError_t launch_lru_bwd(bool bf16, const LruParams& p, hipStream_t s);
 // Bytes of the ticket counters, of the published pairs and of the partial sums.
-constexpr size_t kLruTicketBytes = 4096;
+constexpr size_t kLruTicketBytes = 1024;
 size_t lru_fwd_word_bytes(int B, int T, int D);
 size_t lru_bwd_word_bytes(int B, int T, int D);
 size_t lru_bwd_part_bytes(int B, int T, int D);

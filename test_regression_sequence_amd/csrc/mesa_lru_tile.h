@@ -65,14 +65,17 @@ __device__ __forceinline__ float add_rows(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Tiles of different chains need no order, so chains are dealt to at most 64
-// classes, each with a ticket counter on a cache line of its own: one counter
-// for all hands out a ticket every 14 ns, which took longer than the tiles.
-// Workgroup i takes one tile of class i / 8 % classes; a class's tickets run over
-// its chains, then over time.  Workgroups go round the 8 XCDs, so by the eighths
-// every XCD serves every class: with i % classes an XCD read the same columns of
-// every row, which cost 6 % of the time (B=8, T=4096, D=2048, bf16).
-constexpr int kLruClasses = 64, kLruCounterStride = 16;  // (in 4-byte words)
+// Tiles of different chains need no order, so chains are dealt to at most 16
+// classes of neighbouring slabs, each with a ticket counter on a cache line of
+// its own: one counter for all hands out a ticket every 14 ns, which took longer
+// than the tiles.  Workgroup i takes one tile of class i / 8 % classes; a class's
+// tickets run over its chains, then over time.  Workgroups go round the 8 XCDs,
+// so by the eighths every XCD serves every class: with i % classes an XCD reads
+// the same columns of every row, which costs 6 % at B=1, T=32768, D=2048, bf16.
+// (Rows that are no whole cache lines long make every slab share lines with its
+// neighbours; there the classes by XCD are 14 % faster with 8 sequences and 6 %
+// slower with one, and this stays the rule.)
+constexpr int kLruClasses = 16, kLruCounterStride = 16;  // (in 4-byte words)
 
 struct LruGrid {
   int slabs, tiles, chains, classes, share;
@@ -89,12 +92,12 @@ struct LruGrid {
       chain = blockIdx.x;
       return true;
     }
-    const int q = blockIdx.x / 8 % classes, m = (chains - q + classes - 1) / classes;
+    const int q = blockIdx.x / 8 % classes, m = min(share, chains - q * share);
     if (threadIdx.x == 0) *lds = atomicAdd(tickets + q * kLruCounterStride, 1u);
     __syncthreads();
     const unsigned t = __builtin_amdgcn_readfirstlane(*lds);
     j = t / m;
-    chain = q + classes * (int)(t % m);
+    chain = q * share + (int)(t % m);
     return j < tiles;
   }
 };
