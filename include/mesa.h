@@ -535,7 +535,7 @@ mesa_status mesa_lru_fwd(const mesa_lru_desc* d, const void* x, const void* ga, 
  *   dx = g m s_i,   dgi = g m x s_i (1 - s_i),   dga = v (1 - s_r),
  *   dlam = sum_{b,t} v sigmoid(lam) / softplus(lam),   dh0 = a_0 g_0,
  * where s_r = sigmoid(ga), s_i = sigmoid(gi), m = sqrt(1 - a^2) and
- * v = -log(a) g ((a^2 / m) s_i x - a h_{t-1}) (0 where m = 0).
+ * v = -log(a) g ((a^2 / m) s_i x - a h_{t-1}) (0 where a = 1).
  *
  *   d .. lengths  the forward's (ld: the inputs' token stride)
  *   dy            [B, T, D] dtype dense
@@ -586,7 +586,7 @@ mesa_status mesa_lru_step(int32_t N, int32_t D, int32_t ld, float c, mesa_dtype 
  * res_dtype.  Rounding is to nearest even, y / scale being formed as
  * y * (448 / max|y|).  Rows are independent; a row whose squares overflow fp32
  * (or that holds infinities or NaN) gives unspecified values in that row.
- * Supported: 1 <= D <= 16384, R >= 0, R D <= 2^40, (dtype, res_dtype) of (f32,
+ * Supported: 1 <= D <= 16384, 0 <= R <= 2^30, R D <= 2^40, (dtype, res_dtype) of (f32,
  * f32), (bf16, bf16), (bf16, f32). */
 typedef enum { MESA_NORM_OUT_DTYPE = 0, MESA_NORM_OUT_E4M3 = 1 } mesa_norm_out;
 
@@ -637,7 +637,7 @@ mesa_status mesa_rmsnorm_bwd(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype 
  *   dw_q, dw_k       [H, d, window] fp32 out, summed in a fixed order
  *   dq_hist, dk_hist [B, H, window-1, d] dtype out or NULL
  *   workspace        mesa_qk_preprocess_bwd_workspace_bytes(...) bytes
- * Sizes as in mesa_qk_preprocess, B >= 1.  dq_raw, dk_raw, dq_hist and dk_hist
+ * Sizes as in mesa_qk_preprocess, B >= 1, T <= 2^30.  dq_raw, dk_raw, dq_hist and dk_hist
  * may not overlap the inputs (MESA_ERR_INVALID_ARG). */
 size_t mesa_qk_preprocess_bwd_workspace_bytes(int32_t B, int32_t H, int32_t T, int32_t d,
                                               int32_t window, mesa_dtype dtype);

@@ -125,7 +125,7 @@ namespace {
 mesa_status check_norm(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_dtype, float eps) {
   if (R < 0 || D < 1 || !dtype_ok(dtype) || !dtype_ok(res_dtype)) return MESA_ERR_INVALID_ARG;
   if (!(eps >= 0x1p-126f) || std::isinf(eps)) return MESA_ERR_INVALID_ARG;
-  if (D > 16384 || (double)R * D > (double)(1LL << 40)) return MESA_ERR_UNSUPPORTED;
+  if (D > 16384 || R > (1 << 30) || (double)R * D > (double)(1LL << 40)) return MESA_ERR_UNSUPPORTED;
   if (dtype == MESA_F32 && res_dtype == MESA_BF16) return MESA_ERR_UNSUPPORTED;
   return MESA_OK;
 }
@@ -183,7 +183,7 @@ namespace {
 mesa_status check_prep(int32_t B, int32_t H, int32_t T, int32_t d, int32_t window, mesa_dtype dtype) {
   if (B < 1 || H < 1 || T < 0 || window < 1 || !dtype_ok(dtype)) return MESA_ERR_INVALID_ARG;
   if ((d != 16 && d != 64 && d != 128) || window > 4) return MESA_ERR_UNSUPPORTED;
-  if ((long long)B * H > 65535) return MESA_ERR_UNSUPPORTED;
+  if ((long long)B * H > 65535 || T > (1 << 30)) return MESA_ERR_UNSUPPORTED;
   return MESA_OK;
 }
 

@@ -95,6 +95,9 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
     settle(before[e].E);
     if (row == 0) waves[wave][c2 + e] = all;
   }
+  float h_in = 0.f;  // the state before tile 0
+  if (wave == 1 && p.h0 && c0 + lane < p.D) h_in = p.h0[(size_t)b * p.D + c0 + lane];
+  settle(h_in);
   __syncthreads();
   uint64_t* words = p.words + (size_t)chain * lru_chain_words(tiles);
   Pair tile{1.f, 0.f};
@@ -106,8 +109,7 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
     }
     if (tiles > 1) publish(words + (size_t)j * kLruSlab + lane, tile);
   } else if (wave == 1) {
-    const float h = p.h0 && c0 + lane < p.D ? p.h0[(size_t)b * p.D + c0 + lane] : 0.f;
-    carry_groups(words, tiles, j, lane, h, carry.h);
+    carry_groups(words, tiles, j, lane, h_in, carry.h);
   } else if (wave < 4) {
     carry_tiles(words, j, wave - 2, lane, wave == 2 ? carry.early : carry.late);
   }

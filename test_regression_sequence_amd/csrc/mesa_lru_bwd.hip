@@ -159,6 +159,9 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
     settle(before[e].E);
     if (row == 0) waves[wave][c2 + e] = all;
   }
+  float c_in = 0.f;  // the adjoint behind the last token
+  if (wave == 1 && p.d_hfinal && mine) c_in = p.d_hfinal[(size_t)b * p.D + c0 + lane];
+  settle(c_in);
   __syncthreads();
   uint64_t* words = p.words + (size_t)chain * lru_chain_words(tiles);
   Pair tile{1.f, 0.f};
@@ -170,8 +173,7 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
     }
     if (tiles > 1) publish(words + (size_t)i * kLruSlab + lane, tile);
   } else if (wave == 1) {
-    const float g = p.d_hfinal && mine ? p.d_hfinal[(size_t)b * p.D + c0 + lane] : 0.f;
-    carry_groups(words, tiles, i, lane, g, carry.h);
+    carry_groups(words, tiles, i, lane, c_in, carry.h);
   } else if (wave < 4) {
     carry_tiles(words, i, wave - 2, lane, wave == 2 ? carry.early : carry.late);
   }
@@ -225,7 +227,7 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
   }
 }
 
-// dlam from `rows` partial sums [rows, D] of dL / d log w: 16 channels a
+// dlam from `rows` partial sums [rows, D] of dL / d log t: 16 channels a
 // workgroup, 16 threads a channel.
 __global__ __launch_bounds__(kThreads) void lru_dlam_kernel(const float* part, const float* lam, float* dlam, int rows,
                                                             int D) {

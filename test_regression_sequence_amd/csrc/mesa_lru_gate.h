@@ -53,8 +53,7 @@ __device__ __forceinline__ float lru_sigmoid(float z) {
 // alternating series w (1 - w/2 + w^2/6 - ...) is summed to w^5/720: the first
 // term left out is below w^6/5040 = 5e-8 of the value.  Both are formed and one
 // selected: marked unpredictable, or the compiler makes a branch of every
-// element.  The result is at least the smallest normal float, so that its
-// reciprocal square root is finite.
+// element.
 __device__ __forceinline__ float lru_one_minus_a2(float t, float a) {
   constexpr double k = 2 * 0.69314718055994530942;
   float p = __builtin_fmaf(t, (float)(-k * k * k * k * k * k / 720), (float)(k * k * k * k * k / 120));
@@ -62,7 +61,7 @@ __device__ __forceinline__ float lru_one_minus_a2(float t, float a) {
   p = __builtin_fmaf(t, p, (float)(k * k * k / 6));
   p = __builtin_fmaf(t, p, (float)(-k * k / 2));
   p = __builtin_fmaf(t, p, (float)k);
-  const float series = __builtin_fmaf(t, p, 0x1p-126f), direct = __builtin_fmaf(-a, a, 1.f);
+  const float series = t * p, direct = __builtin_fmaf(-a, a, 1.f);
   return __builtin_unpredictable(t < (float)(0.25 / k)) ? series : direct;
 }
 
@@ -84,7 +83,8 @@ struct LruGrad {
 // 1 - sigmoid comes as exp(-z) sigmoid(z), which keeps its bits for large z.
 // Where exp(-z) overflows that is inf * 0: for ga the product is clamped to
 // [0, 1], which makes it 0 (there t, and with it v, is 0 anyway); for gi, where
-// q has no such range, the exponent is capped at 126 instead.
+// q has no such range, the exponent is capped at 126 instead.  1/m is formed of
+// 1 - a^2 raised to the smallest normal float: where a = 1, m is 0 and 1/m finite.
 __device__ __forceinline__ LruGrad lru_cell_grad(float x, float ga, float gi, float rate) {
   LruGrad r;
   const float er = __builtin_amdgcn_exp2f(-kLog2e * ga);
@@ -92,7 +92,7 @@ __device__ __forceinline__ LruGrad lru_cell_grad(float x, float ga, float gi, fl
   const float sr = __builtin_amdgcn_rcpf(1.f + er), si = __builtin_amdgcn_rcpf(1.f + ei);
   const float t = rate * sr;
   r.a = __builtin_amdgcn_exp2f(-t);
-  const float m2 = lru_one_minus_a2(t, r.a), rm = __builtin_amdgcn_rsqf(m2), m = m2 * rm;
+  const float m2 = lru_one_minus_a2(t, r.a), rm = __builtin_amdgcn_rsqf(fmaxf(m2, 0x1p-126f)), m = m2 * rm;
   const float six = si * x;
   r.sr1 = __builtin_amdgcn_fmed3f(er * sr, 0.f, 1.f);
   r.dx_g = m * si;

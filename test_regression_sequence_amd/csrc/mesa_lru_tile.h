@@ -104,7 +104,7 @@ struct LruGrid {
 
 // A published pair is one 64-bit word, so that a reader sees it whole or not at
 // all and no ordering with other memory is needed.  kLruEmpty (written by
-// lru_clear_kernel before the tiles run) marks a word not yet published; its
+// lru_ready_kernel before the tiles run) marks a word not yet published; its
 // low half is a NaN pattern that A is replaced in.
 constexpr uint64_t kLruEmpty = ~0ull;
 
@@ -137,7 +137,9 @@ __device__ __forceinline__ void await(const uint64_t* word, int count, Pair (&p)
 // the pairs of the whole groups before its own are folded in order, then those
 // of the earlier tiles of its group.  Which words are folded in which order
 // depends on j alone, so the result has the same bits in every run.  The tile
-// publishes its own pair before it waits for any; the last tile of a group also
+// reads the state before tile 0 before it publishes anything (so that the last
+// tile, which has waited for all, may overwrite it), and publishes its own pair
+// before it waits for any; the last tile of a group also
 // publishes the group's, once it has the others.  Every wait ends: a class's
 // tiles are handed out by tickets in the scan's order, so the first tile of a
 // class that is not finished belongs to a workgroup that is running, and all

@@ -119,7 +119,7 @@ def call_norm_bwd(R=4, D=100, dtype=1, res=1, eps=1e-6, wbytes=1 << 40, workspac
 @pytest.mark.parametrize("kw,expect", [
     (dict(R=-1), 1), (dict(D=0), 1), (dict(dtype=2), 1), (dict(res=-1), 1), (dict(eps=0.0), 1), (dict(eps=-1.0), 1),
     (dict(eps=2.0 ** -127), 1), (dict(eps=float("inf")), 1), (dict(eps=float("nan")), 1), (dict(D=16385), 2),
-    (dict(dtype=0, res=1), 2), (dict(R=2 ** 31 - 1, D=16384), 2),
+    (dict(dtype=0, res=1), 2), (dict(R=2 ** 30, D=16384), 2), (dict(R=2 ** 30 + 1, D=1), 2),
 ])
 def test_norm_rejects_bad_sizes_and_types(kw, expect):
     assert call_norm(**kw) == expect
@@ -167,6 +167,7 @@ def test_preprocess_backward_validation():
     assert call(d=96) == 2
     assert call(W=5) == 2
     assert call(B=65536, H=1) == 2
+    assert call(T=2 ** 30 + 1) == 2
     assert call(W=0) == 1
     assert call(B=0) == 1
     assert call(T=-1) == 1

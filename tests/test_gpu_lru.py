@@ -332,6 +332,33 @@ def test_repeated_calls_are_bitwise_equal():
             assert torch.equal(r[key], first[key]), key
 
 
+def test_final_state_over_the_initial_one():
+    """h_final may be h0 itself, with many tiles reading it and one writing it."""
+    d = draw(2, 6000, 256, "bf16", seed=13, ragged=True)
+    t = to_dev(d, "bf16")
+    want = run_fwd(d, t)
+    for _ in range(5):
+        state = t["h0"].clone()
+        r = mesa.lru_fwd(t["x"], t["ga"], t["gi"], t["lam"], c=C, h0=state, lengths=t["lengths"], return_state=True,
+                         out={"h_final": state})
+        torch.cuda.synchronize()
+        assert r["h_final"] is state
+        assert torch.equal(state, want["h_final"]) and torch.equal(r["y"], want["y"])
+
+
+def test_closed_gates_are_exact():
+    """ga = -inf from a zero state: outputs, and the gradients of x, ga, gi and lam, are 0; dh0 is the sum of dy."""
+    t = {k: torch.randn(2, 150, 64, generator=torch.Generator().manual_seed(i)).cuda() for i, k in enumerate(("x", "gi", "dy"))}
+    ga, lam = torch.full_like(t["x"], -float("inf")), torch.zeros(64, device="cuda")
+    r = mesa.lru_fwd(t["x"], ga, t["gi"], lam, return_state=True)
+    g = mesa.lru_bwd(t["x"], ga, t["gi"], lam, torch.ones_like(t["dy"]), state_grads=True)
+    torch.cuda.synchronize()
+    assert not r["y"].any() and not r["h_final"].any()
+    for key in ("dx", "dga", "dgi", "dlam"):
+        assert not g[key].any(), key
+    assert (g["dh0"] == 150).all()
+
+
 def test_causality():
     """Inputs behind token t change nothing up to it, bit for bit."""
     d = draw(1, 700, 96, "f32", seed=11)
