@@ -511,7 +511,7 @@ mesa_status mesa_qk_preprocess(int32_t B, int32_t H, int32_t T, int32_t d, int32
  *
  * Arithmetic and states are fp32 for either dtype.  Every sum is formed in a
  * fixed order: equal inputs give bitwise equal results.
- * Supported: 1 <= D <= ld <= 2^20, T >= 0, B >= 1 with B ceil(T/64) ceil(D/64)
+ * Supported: 2 <= D <= ld <= 2^20, T >= 0, B >= 1 with B ceil(T/64) ceil(D/64)
  * <= 2^23; c > 0, finite (else MESA_ERR_INVALID_ARG).
  * Two calls may not use one workspace at the same time. */
 typedef struct {

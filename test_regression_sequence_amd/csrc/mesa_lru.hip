@@ -59,17 +59,22 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
   {
     Raw2<BF16> x[TW], ga[TW], gi[TW];
     uint32_t off[TW];
+    const int lc = lru_load_channel(ch, p.D);
 #pragma unroll
     for (int s = 0; s < TW; ++s) {  // rows behind n read row n - 1 and are not used
       const int t = whole ? tw0 + s : min(tw0 + s, n - 1 - j * L);
-      off[s] = ((uint32_t)t * p.ld + ch) * ES;
+      off[s] = ((uint32_t)t * p.ld + lc) * ES;
     }
     const size_t in = first * p.ld * ES;
-    load_raw2<BF16>(static_cast<const char*>(p.x) + in, off, nch, x);
-    load_raw2<BF16>(static_cast<const char*>(p.ga) + in, off, nch, ga);
-    load_raw2<BF16>(static_cast<const char*>(p.gi) + in, off, nch, gi);
-    float rate[2];
-    lru_rates(p, ch, nch, rate);
+    float lam[2];
+    load_lam(p, ch, lam);
+    load_raw2<BF16>(static_cast<const char*>(p.x) + in, off, x);
+    load_raw2<BF16>(static_cast<const char*>(p.ga) + in, off, ga);
+    load_raw2<BF16>(static_cast<const char*>(p.gi) + in, off, gi);
+    to_own_channels(p.D, ch, x);
+    to_own_channels(p.D, ch, ga);
+    to_own_channels(p.D, ch, gi);
+    const float rate[2] = {lru_rate(lam[0], p.c), lru_rate(lam[1], p.c)};
 #pragma unroll
     for (int s = 0; s < TW; ++s)
 #pragma unroll

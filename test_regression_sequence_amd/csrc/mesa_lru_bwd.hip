@@ -48,13 +48,13 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
   const size_t first = (size_t)b * p.T + (size_t)j * L;     // the tile's first row of the tensors
   const size_t grad = first * p.ld_grad * ES;
   const uint32_t grow = p.ld_grad * ES, goff = tw0 * grow + ch * ES;
-  float* part = p.lam_part ? p.lam_part + ((size_t)b * tiles + j) * p.D + c0 + lane : nullptr;
+  float* part = p.lam_part + ((size_t)b * tiles + j) * p.D + c0 + lane;
   const bool mine = c0 + lane < p.D;
 
   if (i >= live) {  // behind the length: zeros
     if (wave == 0 && mine) {
       const size_t e = (size_t)b * p.D + c0 + lane;
-      if (part) *part = 0.f;
+      *part = 0.f;
       if (i == 0 && p.dh0) p.dh0[e] = p.d_hfinal ? p.d_hfinal[e] : 0.f;
     }
     const float zero[2] = {};
@@ -74,27 +74,32 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
   {
     Raw2<BF16> x[TW], ga[TW], gi[TW];
     uint32_t off[TW], doff[TW];
+    const int lc = lru_load_channel(ch, p.D);
 #pragma unroll
     for (int s = 0; s < TW; ++s) {  // rows behind n read row n - 1 and are not used
       const int t = whole ? tw0 + s : min(tw0 + s, n - 1 - j * L);
-      off[s] = ((uint32_t)t * p.ld + ch) * ES;
-      doff[s] = ((uint32_t)t * p.D + ch) * ES;
+      off[s] = ((uint32_t)t * p.ld + lc) * ES;
+      doff[s] = ((uint32_t)t * p.D + lc) * ES;
     }
     const size_t in = first * p.ld * ES;
-    load_raw2<BF16>(static_cast<const char*>(p.ga) + in, off, nch, ga);
-    load_raw2<BF16>(static_cast<const char*>(p.gi) + in, off, nch, gi);
-    load_raw2<BF16>(static_cast<const char*>(p.x) + in, off, nch, x);
-    load_raw2<BF16>(static_cast<const char*>(p.dy) + first * p.D * ES, doff, nch, dy);
-    {  // the state before this wave's tokens
-      const int chunk = min(j * L + wave * kLruChunk, n - 1) / kLruChunk;
-      const uint32_t none[1] = {0};
-      Raw2<false> r[1];
-      load_raw2<false>(p.states + ((size_t)b * p.NC + chunk) * p.D + ch, none, nch, r);
+    float lam[2];
+    load_lam(p, ch, lam);
+    load_raw2<BF16>(static_cast<const char*>(p.ga) + in, off, ga);
+    load_raw2<BF16>(static_cast<const char*>(p.gi) + in, off, gi);
+    load_raw2<BF16>(static_cast<const char*>(p.x) + in, off, x);
+    load_raw2<BF16>(static_cast<const char*>(p.dy) + first * p.D * ES, doff, dy);
+    Raw2<false> state[1];  // before this wave's tokens
+    const int chunk = min(j * L + wave * kLruChunk, n - 1) / kLruChunk;
+    const uint32_t none[1] = {0};
+    load_raw2<false>(p.states + ((size_t)b * p.NC + chunk) * p.D + lc, none, state);
+    to_own_channels(p.D, ch, x);
+    to_own_channels(p.D, ch, ga);
+    to_own_channels(p.D, ch, gi);
+    to_own_channels(p.D, ch, dy);
+    to_own_channels(p.D, ch, state);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) h[e] = r[0].at(e);
-    }
-    float rate[2];
-    lru_rates(p, ch, nch, rate);
+    for (int e = 0; e < 2; ++e) h[e] = state[0].at(e);
+    const float rate[2] = {lru_rate(lam[0], p.c), lru_rate(lam[1], p.c)};
 #pragma unroll
     for (int s = 0; s < TW; ++s) {
 #pragma unroll

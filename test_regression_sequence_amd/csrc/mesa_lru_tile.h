@@ -212,22 +212,36 @@ __device__ __forceinline__ void repack(Raw2<false>&) {}
 // The tensors are streamed: loads and stores carry the nontemporal hint (4 %
 // of the forward's time and 7 % of the backward's at that size).
 
-// A lane's channels at `base` (uniform) + off[t] bytes of N rows, of which the
-// first n are the row's.  One branch for all rows: only the last lane of a slab
-// that D ends in takes the second.
+// The first channel that a lane loads: its own, or where the row ends before it
+// has two, the row's last two.  So loads are never predicated: a branch around
+// them, even one that no lane of most slabs takes, had the compiler wait for all
+// of them before the first use (6 % at B=1, T=32768, D=2048, bf16).
+__device__ __forceinline__ int lru_load_channel(int ch, int D) { return min(ch, D - 2); }
+
+// The two channels at `base` (uniform) + off[t] bytes of N rows.
 template <bool BF16, int N>
-__device__ __forceinline__ void load_raw2(const void* base, const uint32_t (&off)[N], int n, Raw2<BF16> (&r)[N]) {
+__device__ __forceinline__ void load_raw2(const void* base, const uint32_t (&off)[N], Raw2<BF16> (&r)[N]) {
   typedef typename std::conditional<BF16, u32_any, f32x2_any>::type V;
-  const char* q = static_cast<const char*>(base);
-  if (n >= 2) {
 #pragma unroll
-    for (int t = 0; t < N; ++t) r[t].v = __builtin_nontemporal_load(reinterpret_cast<const V*>(q + off[t]));
-  } else {
+  for (int t = 0; t < N; ++t)
+    r[t].v = __builtin_nontemporal_load(reinterpret_cast<const V*>(static_cast<const char*>(base) + off[t]));
+}
+
+// Where a lane's first channel is the row's last one, it was loaded second.
+// (Lanes behind the row hold its last channels; nothing of theirs is stored.)
+template <int N>
+__device__ __forceinline__ void to_own_channels(int D, int ch, Raw2<true> (&r)[N]) {
+  if (D & 1) {
+    const int by = ch == D - 1 ? 16 : 0;
 #pragma unroll
-    for (int t = 0; t < N; ++t) {
-      if constexpr (BF16) r[t].v = n > 0 ? *reinterpret_cast<const uint16_t*>(q + off[t]) : 0u;
-      else r[t].v = f32x2{n > 0 ? *reinterpret_cast<const float*>(q + off[t]) : 0.f, 0.f};
-    }
+    for (int t = 0; t < N; ++t) r[t].v >>= by;
+  }
+}
+template <int N>
+__device__ __forceinline__ void to_own_channels(int D, int ch, Raw2<false> (&r)[N]) {
+  if (D & 1) {
+#pragma unroll
+    for (int t = 0; t < N; ++t) r[t].v[0] = __builtin_unpredictable(ch == D - 1) ? r[t].v[1] : r[t].v[0];
   }
 }
 
@@ -249,10 +263,10 @@ __device__ __forceinline__ int lru_length(const LruParams& p, int b) {
   return p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
 }
 
-// The rates of a lane's channels, of which the first n are the row's.
-__device__ __forceinline__ void lru_rates(const LruParams& p, int ch, int n, float (&rate)[2]) {
+// A lane's channels of lam.
+__device__ __forceinline__ void load_lam(const LruParams& p, int ch, float (&lam)[2]) {
 #pragma unroll
-  for (int e = 0; e < 2; ++e) rate[e] = lru_rate(e < n ? p.lam[ch + e] : 0.f, p.c);
+  for (int e = 0; e < 2; ++e) lam[e] = p.lam[min(ch + e, p.D - 1)];
 }
 
 }  // namespace mesa

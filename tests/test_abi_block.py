@@ -41,7 +41,7 @@ def call_lru_bwd(d, ld_grad=100, flag=0, wbytes=1 << 40, **kw):
 BAD_LRU = [
     (dict(B=0), 1), (dict(T=-1), 1), (dict(D=0, ld=100), 1), (dict(ld=99), 1), (dict(c=0.0), 1), (dict(c=-1.0), 1),
     (dict(c=float("inf")), 1), (dict(c=float("nan")), 1), (dict(dtype=2), 1),
-    (dict(ld=(1 << 20) + 1), 2), (dict(B=1 << 19, T=64 * 8, D=128, ld=128), 0), (dict(B=1 << 19, T=64 * 8 + 1, D=128, ld=128), 2),
+    (dict(ld=(1 << 20) + 1), 2), (dict(D=1), 2), (dict(B=1 << 19, T=64 * 8, D=128, ld=128), 0), (dict(B=1 << 19, T=64 * 8 + 1, D=128, ld=128), 2),
     (dict(B=2 ** 31 - 1, T=2 ** 31 - 1), 2),
 ]
 
@@ -89,6 +89,7 @@ def test_lru_step_validation():
     assert call(N=-1) == 1
     assert call(D=0) == 1
     assert call(ld=99) == 1
+    assert call(D=1) == 2
     assert call(c=0.0) == 1
     assert call(dtype=5) == 1
     assert call(N=0) == 0  # nothing to do, nothing launched

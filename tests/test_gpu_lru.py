@@ -162,7 +162,7 @@ def check_backward(d, r, dtype):
 
 
 SIZES = [  # B, T, D, ragged
-    (1, 1, 1, False), (2, 1, 64, False), (3, 2, 7, True), (1, 63, 256, False), (2, 64, 128, False), (3, 65, 100, True),
+    (1, 1, 2, False), (2, 1, 64, False), (3, 2, 7, True), (2, 150, 3, True), (1, 130, 2, False), (1, 63, 256, False), (2, 64, 128, False), (3, 65, 100, True),
     (2, 127, 260, False), (1, 128, 512, False), (2, 129, 1001, True), (5, 200, 36, True), (1, 1000, 68, False),
     (4, 300, 516, True), (1, 2500, 33, False), (2, 1111, 320, True),
     (3, 47, 65, True), (2, 48, 66, False), (2, 49, 127, False), (1, 95, 130, False), (3, 96, 64, True), (2, 97, 2, False),
@@ -276,7 +276,7 @@ def test_slices_of_one_projection(dtype, D):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("N,D", [(1, 1), (1, 2048), (3, 1001), (256, 130), (17, 4096)])
+@pytest.mark.parametrize("N,D", [(1, 2), (1, 3), (1, 2048), (3, 1001), (256, 130), (17, 4096)])
 def test_step_matches_the_oracle(dtype, N, D):
     d = draw(N, 1, D, dtype, seed=8)
     t = to_dev(d, dtype)
