@@ -48,13 +48,13 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
   const size_t first = (size_t)b * p.T + (size_t)j * L;     // the tile's first row of the tensors
   const size_t grad = first * p.ld_grad * ES;
   const uint32_t grow = p.ld_grad * ES, goff = tw0 * grow + ch * ES;
-  float* part = p.lam_part + ((size_t)b * tiles + j) * p.D + c0 + lane;
+  float* part = p.lam_part ? p.lam_part + ((size_t)b * tiles + j) * p.D + c0 + lane : nullptr;  // (none without tokens)
   const bool mine = c0 + lane < p.D;
 
   if (i >= live) {  // behind the length: zeros
     if (wave == 0 && mine) {
       const size_t e = (size_t)b * p.D + c0 + lane;
-      *part = 0.f;
+      if (part) *part = 0.f;
       if (i == 0 && p.dh0) p.dh0[e] = p.d_hfinal ? p.d_hfinal[e] : 0.f;
     }
     const float zero[2] = {};
