@@ -124,7 +124,7 @@ struct PrepParams {
 };
 
 // Tokens per kept state of the gated linear recurrence.
-constexpr int kLruChunk = 12;
+constexpr int kLruChunk = 16;
 
 // Gated linear recurrence (mesa_lru_gate.h has the cell).
 struct LruParams {

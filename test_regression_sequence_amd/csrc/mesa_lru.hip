@@ -13,14 +13,15 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 96 tokens a tile.  Longer lanes (TW = 16, 128 tokens) leave fewer waves to a
-// CU, shorter ones (TW = 8) more tiles to join: 131 and 125 against 119 us at
-// B=1, T=32768, D=2048, bf16; workgroups of 8 waves were slower throughout.
-constexpr int kTw = 12, kNw = 4, kTile = 2 * kNw * kTw;
+// 128 tokens a tile.  Shorter lanes make more tiles to join, 123 to 131 us (TW =
+// 12) and 120 to 127 (TW = 8) against 111 to 115 at B=1, T=32768, D=2048, bf16;
+// longer ones (TW = 24: 110 to 112) leave more of a tile empty at the end of a
+// sequence.  Workgroups of 8 waves were slower throughout.
+constexpr int kTw = 16, kNw = 4, kTile = 2 * kNw * kTw;
 static_assert(kNw >= 4, "three waves wait for other tiles, one folds this one's");
 static_assert(kTw % kLruChunk == 0, "kept states lie at a lane's first token");
 
-template <bool BF16>
+template <bool BF16, bool LINES>
 __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
   constexpr int TW = kTw, NW = kNw, L = kTile;
   constexpr uint32_t ES = BF16 ? 2 : 4;
@@ -31,7 +32,7 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
   const int tiles = grid.tiles;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane >> 5, c2 = 2 * (lane & 31);
   int j, chain;
-  if (!grid.take(p.tickets, &ticket, j, chain)) return;
+  if (!grid.take<LINES>(p.tickets, &ticket, j, chain)) return;
   const int b = chain / grid.slabs, c0 = (chain % grid.slabs) * kLruSlab;
   const int ch = c0 + c2, nch = p.D - ch;
   const int n = lru_length(p, b);
@@ -49,7 +50,7 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
       const float zero[2] = {};
 #pragma unroll
       for (int s = 0; s < TW; ++s)
-        if (t0 + s < p.T) store_raw2<BF16>(y, yoff + s * yrow, zero, nch);
+        if (t0 + s < p.T) store_raw2<BF16, LINES>(y, yoff + s * yrow, zero, nch);
     }
     return;
   }
@@ -68,9 +69,9 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
     const size_t in = first * p.ld * ES;
     float lam[2];
     load_lam(p, ch, lam);
-    load_raw2<BF16>(static_cast<const char*>(p.x) + in, off, x);
-    load_raw2<BF16>(static_cast<const char*>(p.ga) + in, off, ga);
-    load_raw2<BF16>(static_cast<const char*>(p.gi) + in, off, gi);
+    load_raw2<BF16, LINES>(static_cast<const char*>(p.x) + in, off, x);
+    load_raw2<BF16, LINES>(static_cast<const char*>(p.ga) + in, off, ga);
+    load_raw2<BF16, LINES>(static_cast<const char*>(p.gi) + in, off, gi);
     to_own_channels(p.D, ch, x);
     to_own_channels(p.D, ch, ga);
     to_own_channels(p.D, ch, gi);
@@ -129,7 +130,7 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
     h[e] = apply(before[e], apply(pre[wave][c2 + e], h[e]));
   }
   if (t0 < n)
-    store_raw2<false>(p.states, (((size_t)b * p.NC + t0 / kLruChunk) * p.D + ch) * 4, h, nch);
+    store_raw2<false, LINES>(p.states, (((size_t)b * p.NC + t0 / kLruChunk) * p.D + ch) * 4, h, nch);
 #pragma unroll
   for (int s = 0; s < TW; ++s)
 #pragma unroll
@@ -138,17 +139,17 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
       u[s][e] = h[e];
     }
   // behind n the state stays: a lane's last one is the final state wherever n lies in its tokens
-  if (p.h_final && t0 < n && n <= t0 + TW) store_raw2<false>(p.h_final, ((size_t)b * p.D + ch) * 4, h, nch);
+  if (p.h_final && t0 < n && n <= t0 + TW) store_raw2<false, LINES>(p.h_final, ((size_t)b * p.D + ch) * 4, h, nch);
   if (!y) return;
   if (whole && nch >= 2) {
 #pragma unroll
-    for (int s = 0; s < TW; ++s) store_raw2<BF16>(y, yoff + s * yrow, u[s], 2);
+    for (int s = 0; s < TW; ++s) store_raw2<BF16, LINES>(y, yoff + s * yrow, u[s], 2);
   } else {
 #pragma unroll
     for (int s = 0; s < TW; ++s) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) u[s][e] = t0 + s < n ? u[s][e] : 0.f;
-      if (t0 + s < p.T) store_raw2<BF16>(y, yoff + s * yrow, u[s], nch);
+      if (t0 + s < p.T) store_raw2<BF16, LINES>(y, yoff + s * yrow, u[s], nch);
     }
   }
 }
@@ -194,13 +195,13 @@ hipError_t launch_lru_ready(const LruParams& p, size_t words, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool BF16>
+template <bool BF16, bool LINES>
 static hipError_t launch_fwd_t(const LruParams& p, hipStream_t s) {
   const LruGrid grid(p.B, p.T, p.D, kTile);
   if (grid.tiles > 1) {
     if (const hipError_t e = launch_lru_ready(p, grid.chains * lru_chain_words(grid.tiles), s); e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((lru_fwd_kernel<BF16>), dim3(grid.workgroups()), dim3(64 * kNw), 0, s, p);
+  hipLaunchKernelGGL((lru_fwd_kernel<BF16, LINES>), dim3(grid.workgroups()), dim3(64 * kNw), 0, s, p);
   return hipGetLastError();
 }
 
@@ -210,7 +211,9 @@ size_t lru_fwd_word_bytes(int B, int T, int D) {
 }
 
 hipError_t launch_lru_fwd(bool bf16, const LruParams& p, hipStream_t s) {
-  return bf16 ? launch_fwd_t<true>(p, s) : launch_fwd_t<false>(p, s);
+  const bool lines = lru_whole_lines(bf16, {p.ld, p.D}, {p.x, p.ga, p.gi, p.y});
+  if (bf16) return lines ? launch_fwd_t<true, true>(p, s) : launch_fwd_t<true, false>(p, s);
+  return lines ? launch_fwd_t<false, true>(p, s) : launch_fwd_t<false, false>(p, s);
 }
 
 hipError_t launch_lru_step(bool bf16, const LruParams& p, hipStream_t s) {

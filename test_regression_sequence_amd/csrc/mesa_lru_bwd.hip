@@ -20,15 +20,16 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 48 tokens a tile, 12 elements a lane: what the gradients need of 16 leaves room
-// for 3 workgroups a CU, of 12 for 4 (225 against 220 us at B=8, T=4096, D=2048,
-// bf16); 8 elements a lane mean half as many tokens a tile again (229 us).
+// 64 tokens a tile, 16 elements a lane: with what the gradients need of them 3
+// workgroups fit a CU, with 12 elements 4, with 8 elements 5; 191, 195 and 208 us
+// at B=8, T=4096, D=2048, bf16, and 101 against 138 (12 elements, tiles of 48
+// tokens) at B=256, T=64.
 constexpr int kTw = kLruChunk / 2, kNw = 4, kTile = 2 * kNw * kTw;
 static_assert(kNw >= 4, "three waves wait for other tiles, one folds this one's");
 static_assert(2 * kTw == kLruChunk, "a wave's tokens start at a kept state");
 
-template <bool BF16>
-__global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
+template <bool BF16, bool LINES>
+__global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
   constexpr int TW = kTw, NW = kNw, L = kTile;
   constexpr uint32_t ES = BF16 ? 2 : 4;
   __shared__ Pair waves[NW][kLruSlab], pre[NW][kLruSlab];
@@ -39,7 +40,7 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
   const int tiles = grid.tiles;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane >> 5, c2 = 2 * (lane & 31);
   int i, chain;  // i: the tile's place in the scan
-  if (!grid.take(p.tickets, &ticket, i, chain)) return;
+  if (!grid.take<LINES>(p.tickets, &ticket, i, chain)) return;
   const int b = chain / grid.slabs, c0 = (chain % grid.slabs) * kLruSlab;
   const int ch = c0 + c2, nch = p.D - ch;
   const int n = lru_length(p, b), live = (n + L - 1) / L;
@@ -61,9 +62,9 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
 #pragma unroll
     for (int s = 0; s < TW; ++s)
       if (t0 + s < p.T) {
-        store_raw2<BF16>(static_cast<char*>(p.dx) + grad, goff + s * grow, zero, nch);
-        store_raw2<BF16>(static_cast<char*>(p.dga) + grad, goff + s * grow, zero, nch);
-        store_raw2<BF16>(static_cast<char*>(p.dgi) + grad, goff + s * grow, zero, nch);
+        store_raw2<BF16, LINES>(static_cast<char*>(p.dx) + grad, goff + s * grow, zero, nch);
+        store_raw2<BF16, LINES>(static_cast<char*>(p.dga) + grad, goff + s * grow, zero, nch);
+        store_raw2<BF16, LINES>(static_cast<char*>(p.dgi) + grad, goff + s * grow, zero, nch);
       }
     return;
   }
@@ -84,14 +85,14 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
     const size_t in = first * p.ld * ES;
     float lam[2];
     load_lam(p, ch, lam);
-    load_raw2<BF16>(static_cast<const char*>(p.ga) + in, off, ga);
-    load_raw2<BF16>(static_cast<const char*>(p.gi) + in, off, gi);
-    load_raw2<BF16>(static_cast<const char*>(p.x) + in, off, x);
-    load_raw2<BF16>(static_cast<const char*>(p.dy) + first * p.D * ES, doff, dy);
+    load_raw2<BF16, LINES>(static_cast<const char*>(p.ga) + in, off, ga);
+    load_raw2<BF16, LINES>(static_cast<const char*>(p.gi) + in, off, gi);
+    load_raw2<BF16, LINES>(static_cast<const char*>(p.x) + in, off, x);
+    load_raw2<BF16, LINES>(static_cast<const char*>(p.dy) + first * p.D * ES, doff, dy);
     Raw2<false> state[1];  // before this wave's tokens
     const int chunk = min(j * L + wave * kLruChunk, n - 1) / kLruChunk;
     const uint32_t none[1] = {0};
-    load_raw2<false>(p.states + ((size_t)b * p.NC + chunk) * p.D + lc, none, state);
+    load_raw2<false, LINES>(p.states + ((size_t)b * p.NC + chunk) * p.D + lc, none, state);
     to_own_channels(p.D, ch, x);
     to_own_channels(p.D, ch, ga);
     to_own_channels(p.D, ch, gi);
@@ -206,9 +207,9 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
       dga[e] = v * sr1[s][e];
       c[e] = a[s][e] * g;
     }
-    store_raw2<BF16>(static_cast<char*>(p.dx) + grad, goff + s * grow, dx, valid);
-    store_raw2<BF16>(static_cast<char*>(p.dga) + grad, goff + s * grow, dga, valid);
-    store_raw2<BF16>(static_cast<char*>(p.dgi) + grad, goff + s * grow, dgi, valid);
+    store_raw2<BF16, LINES>(static_cast<char*>(p.dx) + grad, goff + s * grow, dx, valid);
+    store_raw2<BF16, LINES>(static_cast<char*>(p.dga) + grad, goff + s * grow, dga, valid);
+    store_raw2<BF16, LINES>(static_cast<char*>(p.dgi) + grad, goff + s * grow, dgi, valid);
   };
   if (whole && nch >= 2) {
 #pragma unroll
@@ -217,7 +218,7 @@ __global__ __launch_bounds__(256, 4) void lru_bwd_kernel(LruParams p) {
 #pragma unroll
     for (int s = TW - 1; s >= 0; --s) token(s, t0 + s < p.T ? nch : 0);
   }
-  if (p.dh0 && t0 == 0) store_raw2<false>(p.dh0, ((size_t)b * p.D + ch) * 4, c, nch);
+  if (p.dh0 && t0 == 0) store_raw2<false, LINES>(p.dh0, ((size_t)b * p.D + ch) * 4, c, nch);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     vsum[e] = add_rows(vsum[e]);
@@ -251,13 +252,13 @@ __global__ __launch_bounds__(kThreads) void lru_dlam_kernel(const float* part, c
   }
 }
 
-template <bool BF16>
+template <bool BF16, bool LINES>
 hipError_t launch_t(const LruParams& p, hipStream_t s) {
   const LruGrid grid(p.B, p.T, p.D, kTile);
   if (grid.tiles > 1) {
     if (const hipError_t e = launch_lru_ready(p, grid.chains * lru_chain_words(grid.tiles), s); e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((lru_bwd_kernel<BF16>), dim3(grid.workgroups()), dim3(64 * kNw), 0, s, p);
+  hipLaunchKernelGGL((lru_bwd_kernel<BF16, LINES>), dim3(grid.workgroups()), dim3(64 * kNw), 0, s, p);
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   hipLaunchKernelGGL(lru_dlam_kernel, dim3((p.D + 15) / 16), dim3(kThreads), 0, s, p.lam_part, p.lam, p.dlam,
                      p.T > 0 ? p.B * grid.tiles : 0, p.D);
@@ -277,7 +278,9 @@ size_t lru_bwd_part_bytes(int B, int T, int D) {
 }
 
 hipError_t launch_lru_bwd(bool bf16, const LruParams& p, hipStream_t s) {
-  return bf16 ? launch_t<true>(p, s) : launch_t<false>(p, s);
+  const bool lines = lru_whole_lines(bf16, {p.ld, p.D, p.ld_grad}, {p.x, p.ga, p.gi, p.dy, p.dx, p.dga, p.dgi});
+  if (bf16) return lines ? launch_t<true, true>(p, s) : launch_t<true, false>(p, s);
+  return lines ? launch_t<false, true>(p, s) : launch_t<false, false>(p, s);
 }
 
 }  // namespace mesa

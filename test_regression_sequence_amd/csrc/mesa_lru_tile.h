@@ -11,10 +11,11 @@
 // tiles of one sequence and slab through device memory, so that every input is
 // read once.  Two channels a lane, not four in four rows of 16 lanes: the loads
 // are half as wide, but joining four rows took 22 instructions a channel, more
-// than a quarter of what a token's gradients take (126 -> 118 us forward, 237 ->
-// 225 us backward at B=8, T=4096, D=2048, bf16).
+// than a quarter of what a token's gradients take (6 % of the forward's time and
+// 5 % of the backward's at B=8, T=4096, D=2048, bf16).
 #pragma once
 
+#include <initializer_list>
 #include <type_traits>
 
 #include "mesa_common.h"
@@ -67,37 +68,43 @@ __device__ __forceinline__ float add_rows(float v) {
 
 // Tiles of different chains need no order, so chains are dealt to at most 16
 // classes of neighbouring slabs, each with a ticket counter on a cache line of
-// its own: one counter for all hands out a ticket every 14 ns, which took longer
-// than the tiles.  Workgroup i takes one tile of class i / 8 % classes; a class's
-// tickets run over its chains, then over time.  Workgroups go round the 8 XCDs,
-// so by the eighths every XCD serves every class: with i % classes an XCD reads
-// the same columns of every row, which costs 6 % at B=1, T=32768, D=2048, bf16.
-// (Rows that are no whole cache lines long make every slab share lines with its
-// neighbours; there the classes by XCD are 14 % faster with 8 sequences and 6 %
-// slower with one, and this stays the rule.)
+// its own: one counter for all hands out a ticket every 14 ns, which takes longer
+// than the tiles (156 against 111 us forward, 290 against 195 backward at B=8,
+// T=4096, D=2048, bf16).  A class's tickets run over its chains, then over time.
+// Workgroups go round the 8 XCDs, each with a cache of its own.  Where slabs are
+// whole cache lines nothing is shared, and by the eighths (workgroup i takes
+// class i / 8) every XCD serves every class: with two neighbouring classes each
+// an XCD reads the same columns of every row, which takes 124 to 133 against 113
+// to 121 us at B=1, T=32768, D=2048, bf16.  Where slabs share lines, neighbours
+// on one XCD read them once: 75 against 83 us forward, 136 against 163 backward
+// at B=8, T=4096, D=1000, bf16.
 constexpr int kLruClasses = 16, kLruCounterStride = 16;  // (in 4-byte words)
 
 struct LruGrid {
-  int slabs, tiles, chains, classes, share;
+  int slabs, tiles, chains, classes;
   __host__ __device__ LruGrid(int B, int T, int D, int L)
       : slabs((D + kLruSlab - 1) / kLruSlab), tiles(T > L ? (T + L - 1) / L : 1), chains(B * slabs),
-        share((chains + kLruClasses - 1) / kLruClasses) {  // chains of a class; the last may have fewer
-    classes = (chains + share - 1) / share;
+        classes(chains < kLruClasses ? chains : kLruClasses) {}
+  __host__ unsigned workgroups() const {  // 8 at a time, as many for each class as the largest has tiles
+    return tiles > 1 ? 8u * classes * (((chains + classes - 1) / classes * tiles + 7) / 8) : (unsigned)chains;
   }
-  __host__ unsigned workgroups() const { return tiles > 1 ? 8u * classes * ((share * tiles + 7) / 8) : (unsigned)chains; }
+  __device__ int first_chain(int q) const { return (int)((long long)q * chains / classes); }
   // This workgroup's tile (in the scan's order) and chain; false if its class has none left.
+  template <bool LINES>
   __device__ bool take(unsigned* tickets, unsigned* lds, int& j, int& chain) const {
     if (tiles == 1) {
       j = 0;
       chain = blockIdx.x;
       return true;
     }
-    const int q = blockIdx.x / 8 % classes, m = min(share, chains - q * share);
+    int q = blockIdx.x / 8 % classes;
+    if constexpr (!LINES) q = classes == 16 ? blockIdx.x % 8 * 2 + blockIdx.x / 8 % 2 : blockIdx.x % classes;
+    const int at = first_chain(q), m = first_chain(q + 1) - at;
     if (threadIdx.x == 0) *lds = atomicAdd(tickets + q * kLruCounterStride, 1u);
     __syncthreads();
     const unsigned t = __builtin_amdgcn_readfirstlane(*lds);
     j = t / m;
-    chain = q * share + (int)(t % m);
+    chain = at + (int)(t % m);
     return j < tiles;
   }
 };
@@ -209,8 +216,18 @@ __device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
 __device__ __forceinline__ void repack(Raw2<true>& r) { asm volatile("" : "+v"(r.v)); }
 __device__ __forceinline__ void repack(Raw2<false>&) {}
 
-// The tensors are streamed: loads and stores carry the nontemporal hint (4 %
-// of the forward's time and 7 % of the backward's at that size).
+// Where every row starts a cache line (128 bytes; a slab is then whole lines),
+// the tensors are streamed: loads and stores carry the nontemporal hint, which
+// takes 111 instead of 117 us forward and 191 instead of 204 backward at B=8,
+// T=4096, D=2048, bf16.  Otherwise neighbouring slabs share lines, which have to
+// stay in the caches until both are done: with the hint 109 instead of 81 us
+// and 224 instead of 159 at B=8, T=4096, D=1000, bf16.
+inline bool lru_whole_lines(bool bf16, std::initializer_list<int> strides, std::initializer_list<const void*> tensors) {
+  size_t bits = 0;
+  for (const int ld : strides) bits |= (size_t)ld * (bf16 ? 2 : 4);
+  for (const void* q : tensors) bits |= reinterpret_cast<size_t>(q);
+  return bits % 128 == 0;
+}
 
 // The first channel that a lane loads: its own, or where the row ends before it
 // has two, the row's last two.  So loads are never predicated: a branch around
@@ -219,12 +236,15 @@ __device__ __forceinline__ void repack(Raw2<false>&) {}
 __device__ __forceinline__ int lru_load_channel(int ch, int D) { return min(ch, D - 2); }
 
 // The two channels at `base` (uniform) + off[t] bytes of N rows.
-template <bool BF16, int N>
+template <bool BF16, bool LINES, int N>
 __device__ __forceinline__ void load_raw2(const void* base, const uint32_t (&off)[N], Raw2<BF16> (&r)[N]) {
   typedef typename std::conditional<BF16, u32_any, f32x2_any>::type V;
 #pragma unroll
-  for (int t = 0; t < N; ++t)
-    r[t].v = __builtin_nontemporal_load(reinterpret_cast<const V*>(static_cast<const char*>(base) + off[t]));
+  for (int t = 0; t < N; ++t) {
+    const V* q = reinterpret_cast<const V*>(static_cast<const char*>(base) + off[t]);
+    if constexpr (LINES) r[t].v = __builtin_nontemporal_load(q);
+    else r[t].v = *q;
+  }
 }
 
 // Where a lane's first channel is the row's last one, it was loaded second.
@@ -246,16 +266,20 @@ __device__ __forceinline__ void to_own_channels(int D, int ch, Raw2<false> (&r)[
 }
 
 // The first n of a lane's channels to `base` + off bytes, rounded to nearest even.
-template <bool BF16>
+template <bool BF16, bool LINES>
 __device__ __forceinline__ void store_raw2(void* base, size_t off, const float (&y)[2], int n) {
+  typedef typename std::conditional<BF16, uint32_t, f32x2>::type V;
+  typedef typename std::conditional<BF16, u32_any, f32x2_any>::type VAny;
   char* q = static_cast<char*>(base) + off;
-  if constexpr (BF16) {
-    const uint32_t o = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{y[0], y[1]}, bf16x2));
-    if (n >= 2) __builtin_nontemporal_store(o, reinterpret_cast<u32_any*>(q));
-    else if (n > 0) *reinterpret_cast<uint16_t*>(q) = (uint16_t)o;
-  } else {
-    if (n >= 2) __builtin_nontemporal_store(f32x2{y[0], y[1]}, reinterpret_cast<f32x2_any*>(q));
-    else if (n > 0) *reinterpret_cast<float*>(q) = y[0];
+  V o;
+  if constexpr (BF16) o = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{y[0], y[1]}, bf16x2));
+  else o = f32x2{y[0], y[1]};
+  if (n >= 2) {
+    if constexpr (LINES) __builtin_nontemporal_store(o, reinterpret_cast<VAny*>(q));
+    else *reinterpret_cast<VAny*>(q) = o;
+  } else if (n > 0) {
+    if constexpr (BF16) *reinterpret_cast<uint16_t*>(q) = (uint16_t)o;
+    else *reinterpret_cast<float*>(q) = y[0];
   }
 }
 

@@ -166,6 +166,7 @@ SIZES = [  # B, T, D, ragged
     (2, 127, 260, False), (1, 128, 512, False), (2, 129, 1001, True), (5, 200, 36, True), (1, 1000, 68, False),
     (4, 300, 516, True), (1, 2500, 33, False), (2, 1111, 320, True),
     (3, 47, 65, True), (2, 48, 66, False), (2, 49, 127, False), (1, 95, 130, False), (3, 96, 64, True), (2, 97, 2, False),
+    (1, 1023, 63, False), (2, 1025, 129, True), (1, 2048, 64, False), (3, 2049, 70, True),
     (1, 767, 63, False), (2, 769, 129, True), (1, 1535, 64, False), (3, 1537, 70, True), (40, 100, 200, True),
 ]
 
