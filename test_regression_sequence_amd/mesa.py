@@ -631,18 +631,21 @@ def _home(t: torch.Tensor, name: str, dims: int, stream) -> torch.device:
     return t.device
 
 
-def _new(shape, dtype, dev, stream) -> torch.Tensor:
-    if stream is None:
-        return torch.empty(shape, device=dev, dtype=dtype)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, device=dev, dtype=dtype)
+def _new(shape, dtype, dev, stream, like=None) -> torch.Tensor:
+    """like: a tensor of this shape and type (as its twin in half the time, where it is dense)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, device=dev, dtype=dtype)
+    if like is not None and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(shape, device=dev, dtype=dtype)
 
 
-def _result(out: Optional[dict], key: str, shape, dtype, dev, stream) -> torch.Tensor:
+def _result(out: Optional[dict], key: str, shape, dtype, dev, stream, like=None) -> torch.Tensor:
     """out[key], checked, or a new tensor."""
     t = out.get(key) if out else None
     if t is None:
-        return _new(shape, dtype, dev, stream)
+        return _new(shape, dtype, dev, stream, like)
     _want(t, key, shape, dtype, dev)
     return t
 
@@ -715,7 +718,7 @@ def lru_fwd(x, ga, gi, lam, *, c: float = 8.0, h0=None, lengths=None, return_sta
     _want(lam, "lam", (D,), f32, dev)
     _want(h0, "h0", (B, D), f32, dev)
     _want(lengths, "lengths", (B,), torch.int32, dev)
-    res = {"y": _result(out, "y", shape, dt, dev, stream)}
+    res = {"y": _result(out, "y", shape, dt, dev, stream, x)}
     if return_state:
         res["h_final"] = _result(out, "h_final", (B, D), f32, dev, stream)
     workspace, wbytes = _scratch(workspace, lambda: lru_workspace_bytes(B, T, D, dtype=dt), dev, stream)
@@ -746,9 +749,9 @@ def lru_bwd(x, ga, gi, lam, dy, *, c: float = 8.0, h0=None, lengths=None, d_hfin
     res = {}
     for key in ("dx", "dga", "dgi"):
         t = out.get(key) if out else None
-        res[key] = _new(shape, dt, dev, stream) if t is None else t
+        res[key] = _new(shape, dt, dev, stream, dy) if t is None else t
     ld_grad = _token_stride(res.items(), shape, dt, dev) if out else D
-    res["dlam"] = _result(out, "dlam", (D,), f32, dev, stream)
+    res["dlam"] = _result(out, "dlam", (D,), f32, dev, stream, lam)
     if state_grads:
         res["dh0"] = _result(out, "dh0", (B, D), f32, dev, stream)
     workspace, wbytes = _scratch(workspace, lambda: lru_workspace_bytes(B, T, D, dtype=dt), dev, stream)
@@ -768,7 +771,7 @@ def lru_step(x, ga, gi, lam, h_state, *, c: float = 8.0, out=None, stream=None) 
     code, ld = _code_of(x, "x"), _token_stride((("x", x), ("ga", ga), ("gi", gi)), shape, dt, dev)
     _want(lam, "lam", (D,), torch.float32, dev)
     _want(h_state, "h_state", shape, torch.float32, dev)
-    y = _result(out, "y", shape, dt, dev, stream)
+    y = _result(out, "y", shape, dt, dev, stream, x)
     _launch("mesa_lru_step", dev, stream, N, D, ld, c, code, _addr(x), _addr(ga), _addr(gi), _addr(lam),
             _addr(h_state), _addr(y))
     return {"y": y}
@@ -796,12 +799,13 @@ def rmsnorm(x, w, *, residual=None, eps: float = 1e-6, quant_group: Optional[int
         res_dt, res_code = residual.dtype, _code_of(residual, "residual")
         _want(residual, "residual", shape, res_dt, dev)
     quant = quant_group is not None
-    res = {"y": _result(out, "y", shape, torch.float8_e4m3fn if quant else dt, dev, stream)}
+    res = {"y": _result(out, "y", shape, torch.float8_e4m3fn if quant else dt, dev, stream,
+                        None if quant else x)}
     if quant:
         groups = -(-D // quant_group) if quant_group > 0 else 1
         res["scale"] = _result(out, "scale", (R, groups), torch.float32, dev, stream)
     if residual is not None if return_residual is None else return_residual:
-        res["residual"] = _result(out, "residual", shape, res_dt, dev, stream)
+        res["residual"] = _result(out, "residual", shape, res_dt, dev, stream, x if residual is None else residual)
     _launch("mesa_rmsnorm", dev, stream, R, D, code, res_code, _addr(x), _addr(residual), _addr(w), eps,
             1 if quant else 0, quant_group or 0, _addr(res["y"]), _addr(res.get("scale")), _addr(res.get("residual")))
     return res
@@ -826,10 +830,10 @@ def rmsnorm_bwd(s, w, dy, *, d_residual=None, eps: float = 1e-6, out=None,
     _want(w, "w", (D,), torch.float32, dev)
     _want(dy, "dy", shape, dy.dtype, dev)
     _want(d_residual, "d_residual", shape, dt, dev)
-    res = {"ds": _result(out, "ds", shape, dt, dev, stream),
-           "dw": _result(out, "dw", (D,), torch.float32, dev, stream)}
+    res = {"ds": _result(out, "ds", shape, dt, dev, stream, s),
+           "dw": _result(out, "dw", (D,), torch.float32, dev, stream, w)}
     if dy.dtype != dt:
-        res["dx"] = _result(out, "dx", shape, dy.dtype, dev, stream)
+        res["dx"] = _result(out, "dx", shape, dy.dtype, dev, stream, dy)
     workspace, wbytes = _scratch(workspace, lambda: rmsnorm_bwd_workspace_bytes(R, D), dev, stream)
     _launch("mesa_rmsnorm_bwd", dev, stream, R, D, _code_of(dy, "dy"), _code_of(s, "s"), _addr(s), _addr(w),
             _addr(dy), _addr(d_residual), eps, _addr(res["ds"]), _addr(res.get("dx")), _addr(res["dw"]),
@@ -866,8 +870,8 @@ def qk_preprocess_bwd(q_raw, k_raw, w_q, w_k, d_q, d_k, *, q_hist=None, k_hist=N
     _want(k_hist, "k_hist", hist, dt, dev)
     _want(d_q_hist_out, "d_q_hist_out", hist, dt, dev)
     _want(d_k_hist_out, "d_k_hist_out", hist, dt, dev)
-    res = {key: _result(out, key, shape, dt, dev, stream) for key in ("dq_raw", "dk_raw")}
-    res.update((key, _result(out, key, taps, f32, dev, stream)) for key in ("dw_q", "dw_k"))
+    res = {key: _result(out, key, shape, dt, dev, stream, q_raw) for key in ("dq_raw", "dk_raw")}
+    res.update((key, _result(out, key, taps, f32, dev, stream, w_q)) for key in ("dw_q", "dw_k"))
     if history_grads:
         res.update((key, _result(out, key, hist, dt, dev, stream)) for key in ("dq_hist", "dk_hist"))
     workspace, wbytes = _scratch(workspace, lambda: qk_preprocess_bwd_workspace_bytes(B, H, T, d, W, dtype=dt), dev,
