@@ -513,7 +513,9 @@ mesa_status mesa_qk_preprocess(int32_t B, int32_t H, int32_t T, int32_t d, int32
  * fixed order: equal inputs give bitwise equal results.
  * Supported: 2 <= D <= ld <= 2^20, T >= 0, B >= 1 with B ceil(T/64) ceil(D/64)
  * <= 2^23; c > 0, finite (else MESA_ERR_INVALID_ARG).
- * Two calls may not use one workspace at the same time. */
+ * Outputs and workspace may not overlap inputs but as said (MESA_ERR_INVALID_ARG):
+ * h_final may be h0, dh0 may be d_hfinal.  Two calls may not use one workspace at
+ * the same time. */
 typedef struct {
   int32_t B, T, D;   /* sequences, tokens per (padded) sequence, channels             */
   int32_t ld;        /* elements from one token of x, ga, gi to the next (>= D)       */
@@ -586,6 +588,7 @@ mesa_status mesa_lru_step(int32_t N, int32_t D, int32_t ld, float c, mesa_dtype 
  * res_dtype.  Rounding is to nearest even, y / scale being formed as
  * y * (448 / max|y|).  Rows are independent; a row whose squares overflow fp32
  * (or that holds infinities or NaN) gives unspecified values in that row.
+ * Other outputs may not overlap inputs or residual_out (MESA_ERR_INVALID_ARG).
  * Supported: 1 <= D <= 16384, 0 <= R <= 2^30, R D <= 2^40, (dtype, res_dtype) of (f32,
  * f32), (bf16, bf16), (bf16, f32). */
 typedef enum { MESA_NORM_OUT_DTYPE = 0, MESA_NORM_OUT_E4M3 = 1 } mesa_norm_out;
@@ -609,7 +612,8 @@ mesa_status mesa_rmsnorm(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_
  *              on an fp32 stream
  *   dw         [D] fp32 out, summed in a fixed order
  *   workspace  mesa_rmsnorm_bwd_workspace_bytes(R, D) bytes
- * Sizes and types as in mesa_rmsnorm. */
+ * Sizes and types as in mesa_rmsnorm.  Outputs and workspace may not overlap
+ * inputs but as said (MESA_ERR_INVALID_ARG). */
 size_t mesa_rmsnorm_bwd_workspace_bytes(int32_t R, int32_t D);
 
 mesa_status mesa_rmsnorm_bwd(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_dtype,
@@ -637,7 +641,7 @@ mesa_status mesa_rmsnorm_bwd(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype 
  *   dw_q, dw_k       [H, d, window] fp32 out, summed in a fixed order
  *   dq_hist, dk_hist [B, H, window-1, d] dtype out or NULL
  *   workspace        mesa_qk_preprocess_bwd_workspace_bytes(...) bytes
- * Sizes as in mesa_qk_preprocess, B >= 1, T <= 2^30.  dq_raw, dk_raw, dq_hist and dk_hist
+ * Sizes as in mesa_qk_preprocess, B >= 1, T <= 2^30.  Outputs and workspace
  * may not overlap the inputs (MESA_ERR_INVALID_ARG). */
 size_t mesa_qk_preprocess_bwd_workspace_bytes(int32_t B, int32_t H, int32_t T, int32_t d,
                                               int32_t window, mesa_dtype dtype);

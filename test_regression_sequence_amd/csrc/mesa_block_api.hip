@@ -22,7 +22,30 @@ bool dtype_ok(mesa_dtype t) { return t == MESA_F32 || t == MESA_BF16; }
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+
+// Whether an output shares memory with an input.
+template <size_t N, size_t M>
+bool overlap(const Span (&outs)[N], const Span (&ins)[M]) {
+  for (const Span& o : outs)
+    for (const Span& i : ins) {
+      const char *a = static_cast<const char*>(o.at), *b = static_cast<const char*>(i.at);
+      if (a && b && o.bytes > 0 && i.bytes > 0 && a < b + i.bytes && b < a + o.bytes) return true;
+    }
+  return false;
+}
+
+size_t dtype_bytes(mesa_dtype t) { return t == MESA_BF16 ? 2 : 4; }
+
 // ---- gated linear recurrence ----------------------------------------------
+
+// Bytes from the first to the last element of the token rows at stride ld.
+size_t lru_rows_bytes(const mesa_lru_desc* d, int32_t ld) {
+  return d->T > 0 ? (((size_t)d->B * d->T - 1) * ld + d->D) * dtype_bytes(d->dtype) : 0;
+}
 
 constexpr int kLruMaxStride = 1 << 20;
 
@@ -76,6 +99,11 @@ mesa_status mesa_lru_fwd(const mesa_lru_desc* d, const void* x, const void* ga, 
   if (!all_aligned({x, ga, gi, lam, h0, lengths, y, h_final, workspace})) return MESA_ERR_ALIGNMENT;
   const size_t need = mesa_lru_workspace_bytes(d);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MESA_ERR_WORKSPACE;
+  const size_t rows = lru_rows_bytes(d, d->ld), per_channel = (size_t)d->D * 4, state = d->B * per_channel;
+  if (overlap({{y, lru_rows_bytes(d, d->D)}, {h_final, state}, {workspace, need}},
+              {{x, rows}, {ga, rows}, {gi, rows}, {lam, per_channel}, {h0 == h_final ? nullptr : h0, state},
+               {lengths, (size_t)d->B * 4}}))
+    return MESA_ERR_INVALID_ARG;
   mesa::LruParams p = lru_params(d, x, ga, gi, lam, h0, lengths, workspace);
   p.y = y; p.h_final = h_final;
   return mesa::launch_lru_fwd(d->dtype == MESA_BF16, p, stream) == hipSuccess ? MESA_OK : MESA_ERR_HIP;
@@ -95,6 +123,12 @@ mesa_status mesa_lru_bwd(const mesa_lru_desc* d, const void* x, const void* ga, 
   const size_t need = mesa_lru_workspace_bytes(d);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MESA_ERR_WORKSPACE;
   const bool bf16 = d->dtype == MESA_BF16;
+  const size_t rows = lru_rows_bytes(d, d->ld), grads = lru_rows_bytes(d, ld_grad);
+  const size_t per_channel = (size_t)d->D * 4, state = d->B * per_channel;
+  if (overlap({{dx, grads}, {dga, grads}, {dgi, grads}, {dlam, per_channel}, {dh0, state}, {workspace, need}},
+              {{x, rows}, {ga, rows}, {gi, rows}, {lam, per_channel}, {h0, state}, {lengths, (size_t)d->B * 4},
+               {dy, lru_rows_bytes(d, d->D)}, {d_hfinal == dh0 ? nullptr : d_hfinal, state}}))
+    return MESA_ERR_INVALID_ARG;
   mesa::LruParams p = lru_params(d, x, ga, gi, lam, h0, lengths, workspace);
   if (d->T > 0 && !states_in_workspace && mesa::launch_lru_fwd(bf16, p, stream) != hipSuccess) return MESA_ERR_HIP;
   if (d->T == 0) p.lam_part = nullptr;
@@ -111,6 +145,10 @@ mesa_status mesa_lru_step(int32_t N, int32_t D, int32_t ld, float c, mesa_dtype 
   if (st != MESA_OK || N == 0) return st;
   if (!x || !ga || !gi || !lam || !h_state || !y) return MESA_ERR_INVALID_ARG;
   if (!all_aligned({x, ga, gi, lam, h_state, y})) return MESA_ERR_ALIGNMENT;
+  const mesa_lru_desc all{N, 1, D, ld, c, dtype};
+  const size_t rows = lru_rows_bytes(&all, ld), per_channel = (size_t)D * 4, state = N * per_channel;
+  if (overlap({{y, lru_rows_bytes(&all, D)}, {h_state, state}}, {{x, rows}, {ga, rows}, {gi, rows}, {lam, per_channel}}))
+    return MESA_ERR_INVALID_ARG;
   mesa::LruParams p = lru_params(&d, x, ga, gi, lam, nullptr, nullptr, nullptr);
   p.h_final = h_state; p.y = y;
   return mesa::launch_lru_step(dtype == MESA_BF16, p, stream) == hipSuccess ? MESA_OK : MESA_ERR_HIP;
@@ -146,6 +184,14 @@ mesa_status mesa_rmsnorm(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_
   if (R == 0) return MESA_OK;
   if (!x || !w || !y || (e4m3 && !scale)) return MESA_ERR_INVALID_ARG;
   if (!all_aligned({x, residual, w, y, scale, residual_out})) return MESA_ERR_ALIGNMENT;
+  const size_t n = (size_t)R * D, rows = n * dtype_bytes(dtype), stream_rows = n * dtype_bytes(res_dtype);
+  const size_t groups = group ? (D + 127) / 128 : 1, weights = (size_t)D * 4;
+  if (overlap({{y, e4m3 ? n : rows}, {scale, e4m3 ? R * groups * 4 : 0}},
+              {{x, rows}, {residual, stream_rows}, {w, weights}, {residual_out, stream_rows}}) ||
+      overlap({{residual_out, stream_rows}},
+              {{residual_out == x && dtype == res_dtype ? nullptr : x, rows},
+               {residual_out == residual ? nullptr : residual, stream_rows}, {w, weights}}))
+    return MESA_ERR_INVALID_ARG;
   mesa::NormParams p{};
   p.x = x; p.residual = residual; p.w = w; p.y = y; p.scale = scale; p.residual_out = residual_out;
   p.R = R; p.D = D; p.eps = eps; p.e4m3 = e4m3 ? 1 : 0; p.group = e4m3 ? group : 0;
@@ -167,6 +213,11 @@ mesa_status mesa_rmsnorm_bwd(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype 
   if (!all_aligned({s, w, dy, d_residual, ds, dx, dw, workspace})) return MESA_ERR_ALIGNMENT;
   const size_t need = mesa_rmsnorm_bwd_workspace_bytes(R, D);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MESA_ERR_WORKSPACE;
+  const size_t n = (size_t)R * D, rows = n * dtype_bytes(dtype), stream_rows = n * dtype_bytes(res_dtype);
+  const size_t weights = (size_t)D * 4;
+  if (overlap({{ds, stream_rows}, {dx, rows}, {dw, weights}, {workspace, need}},
+              {{s, stream_rows}, {w, weights}, {dy, rows}, {d_residual == ds ? nullptr : d_residual, stream_rows}}))
+    return MESA_ERR_INVALID_ARG;
   mesa::NormParams p{};
   p.x = s; p.residual = d_residual; p.w = w; p.dy = dy; p.y = ds; p.residual_out = dx; p.dw = dw; p.part = workspace;
   p.R = R; p.D = D; p.eps = eps;
@@ -185,13 +236,6 @@ mesa_status check_prep(int32_t B, int32_t H, int32_t T, int32_t d, int32_t windo
   if ((d != 16 && d != 64 && d != 128) || window > 4) return MESA_ERR_UNSUPPORTED;
   if ((long long)B * H > 65535 || T > (1 << 30)) return MESA_ERR_UNSUPPORTED;
   return MESA_OK;
-}
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b || na == 0 || nb == 0) return false;
-  const char* pa = static_cast<const char*>(a);
-  const char* pb = static_cast<const char*>(b);
-  return pa < pb + nb && pb < pa + na;
 }
 
 }  // namespace
@@ -222,15 +266,13 @@ mesa_status mesa_qk_preprocess_bwd(int32_t B, int32_t H, int32_t T, int32_t d, i
   const size_t need = mesa_qk_preprocess_bwd_workspace_bytes(B, H, T, d, window, dtype);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MESA_ERR_WORKSPACE;
   // every input row is read by up to `window` output rows
-  const size_t esz = dtype == MESA_BF16 ? 2 : 4;
-  const size_t seq = (size_t)B * H * T * d, hist = (size_t)B * H * (window - 1) * d;
-  const void* ins[] = {q_raw, k_raw, d_q, d_k, q_hist, k_hist, d_q_hist_out, d_k_hist_out};
-  const size_t in_bytes[] = {seq * esz, seq * esz, seq * 4, seq * 4, hist * esz, hist * esz, hist * esz, hist * esz};
-  const void* outs[] = {dq_raw, dk_raw, dq_hist, dk_hist};
-  const size_t out_bytes[] = {seq * esz, seq * esz, hist * esz, hist * esz};
-  for (int a = 0; a < 4; ++a)
-    for (int b = 0; b < 8; ++b)
-      if (overlap(outs[a], out_bytes[a], ins[b], in_bytes[b])) return MESA_ERR_INVALID_ARG;
+  const size_t n = (size_t)B * H * T * d, seq = n * dtype_bytes(dtype);
+  const size_t hist = (size_t)B * H * (window - 1) * d * dtype_bytes(dtype), taps = (size_t)H * d * window * 4;
+  if (overlap({{dq_raw, seq}, {dk_raw, seq}, {dq_hist, hist}, {dk_hist, hist}, {dw_q, taps}, {dw_k, taps},
+               {workspace, need}},
+              {{q_raw, seq}, {k_raw, seq}, {w_q, taps}, {w_k, taps}, {d_q, n * 4}, {d_k, n * 4}, {q_hist, hist},
+               {k_hist, hist}, {d_q_hist_out, hist}, {d_k_hist_out, hist}}))
+    return MESA_ERR_INVALID_ARG;
 
   mesa::PrepBwdParams p{};
   p.x[0] = q_raw; p.x[1] = k_raw; p.w[0] = w_q; p.w[1] = w_k; p.hist_in[0] = q_hist; p.hist_in[1] = k_hist;

@@ -171,9 +171,11 @@ __global__ __launch_bounds__(kThreads) void lru_step_kernel(LruParams p) {
   if (i >= (long long)p.B * groups) return;
   const size_t row = (size_t)(i / groups);
   const int ch = (int)(i % groups) * 8, n = p.D - ch;
-  const size_t e = row * p.ld + ch, o = row * p.D + ch;
-  const Raw8<BF16> x = load_raw8<BF16>(p.x, e, n), ga = load_raw8<BF16>(p.ga, e, n), gi = load_raw8<BF16>(p.gi, e, n);
-  const Raw8<false> before = load_raw8<false>(p.h_final, o, n), lam = load_raw8<false>(p.lam, ch, n);
+  const size_t in = row * p.ld, out = row * p.D;
+  // (loaded exactly: the state is updated in place, by other waves too)
+  const Raw8<BF16> x = load_part8<BF16>(p.x, in + ch, n), ga = load_part8<BF16>(p.ga, in + ch, n),
+                   gi = load_part8<BF16>(p.gi, in + ch, n);
+  const Raw8<false> before = load_part8<false>(p.h_final, out + ch, n), lam = load_part8<false>(p.lam, ch, n);
   float h[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
@@ -181,8 +183,8 @@ __global__ __launch_bounds__(kThreads) void lru_step_kernel(LruParams p) {
     lru_cell(x.at(k), ga.at(k), gi.at(k), lru_rate(lam.at(k), p.c), a, u);
     h[k] = __builtin_fmaf(a, before.at(k), u);
   }
-  store_raw8<false>(p.h_final, o, h, n);
-  store_raw8<BF16>(p.y, o, h, n);
+  store_raw8<false, true>(p.h_final, out + ch, h, n);
+  store_raw8<BF16, true>(p.y, out + ch, h, n);
 }
 
 unsigned blocks(long long n) { return (unsigned)((n + kThreads - 1) / kThreads); }

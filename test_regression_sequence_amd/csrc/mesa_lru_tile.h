@@ -25,10 +25,7 @@
 
 namespace mesa {
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef f32x2 __attribute__((aligned(4))) f32x2_any;
-typedef uint32_t __attribute__((aligned(2))) u32_any;
 
 constexpr int kLruSlab = 64;    // channels of a tile
 constexpr int kLruGroup = 16;   // tiles whose joined pair is published as one

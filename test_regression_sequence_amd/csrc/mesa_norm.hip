@@ -30,6 +30,14 @@ struct NormShape {
   static constexpr int kRows = kThreads / TPR;  // rows a workgroup holds at a time
 };
 
+// The first row of this lane's group (uniform where a row takes whole waves).
+template <int TPR>
+__device__ __forceinline__ int first_row() {
+  int group = threadIdx.x / TPR;
+  if constexpr (TPR >= 64) group = __builtin_amdgcn_readfirstlane(group);
+  return blockIdx.x * NormShape<TPR>::kRows + group;
+}
+
 // Sums (a, b) over the TPR lanes of a row; the same bits in every lane.  Rows
 // wider than a wave go through LDS, two buffers in turn: one barrier a call.
 template <int TPR>
@@ -70,6 +78,7 @@ __device__ __forceinline__ float row_max(float v, float2 (*lds)[8], int& turn) {
 
 // The first n of 8 channels as e4m3 bytes.  |y| / scale is at most 448 but for
 // rounding, well inside the range that rounds to 448.
+template <bool TAIL>
 __device__ __forceinline__ void store_e4m3(void* base, size_t elem, const float (&y)[8], float inv, int n) {
   uint32_t lo = 0, hi = 0;
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] * inv, y[1] * inv, lo, false);
@@ -81,29 +90,32 @@ __device__ __forceinline__ void store_e4m3(void* base, size_t elem, const float 
   typedef u32x2 __attribute__((aligned(1))) u32x2_any;
   if (n >= 8) {
     *reinterpret_cast<u32x2_any*>(q) = u32x2{lo, hi};
-  } else {
-#pragma unroll
-    for (int e = 0; e < 7; ++e)
-      if (e < n) q[e] = (uint8_t)((e < 4 ? lo : hi) >> (8 * (e & 3)));
+  } else if (TAIL && n > 0) {
+    typedef uint32_t __attribute__((aligned(1))) u32_byte;
+    typedef uint16_t __attribute__((aligned(1))) u16_byte;
+    const uint32_t rest = n & 4 ? hi : lo;
+    if (n & 4) *reinterpret_cast<u32_byte*>(q) = lo;
+    if (n & 2) *reinterpret_cast<u16_byte*>(q + (n & 4)) = (uint16_t)rest;
+    if (n & 1) q[n & 6] = (uint8_t)(n & 2 ? rest >> 16 : rest);
   }
 }
 
-template <bool BF16, bool RBF16, int TPR, int NV>
+template <bool BF16, bool RBF16, bool TAIL, int TPR, int NV>
 __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormParams p) {
   using Sh = NormShape<TPR>;
   __shared__ float2 lds[2][8];
   int turn = 0;
   const int lane = threadIdx.x % TPR, D = p.D;
   const int stride = gridDim.x * Sh::kRows;
-  int row = blockIdx.x * Sh::kRows + threadIdx.x / TPR;
+  int row = first_row<TPR>();
   Raw8<BF16> rx[NV];
   Raw8<RBF16> rr[NV];
   auto load = [&](int at) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = 8 * (lane + TPR * k);
-      rx[k] = load_raw8<BF16>(p.x, (size_t)at * D + c, D - c);
-      if (p.residual) rr[k] = load_raw8<RBF16>(p.residual, (size_t)at * D + c, D - c);
+      rx[k] = load_row8<BF16, TAIL>(p.x, (size_t)at * D, c, D);
+      if (p.residual) rr[k] = load_row8<RBF16, TAIL>(p.residual, (size_t)at * D, c, D);
     }
   };
   if (row < p.R) load(row);
@@ -111,7 +123,8 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormP
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = 8 * (lane + TPR * k);
-    const Raw8<false> v = load_raw8<false>(p.w, c, D - c);
+    Raw8<false> v = load_row8<false, TAIL>(p.w, 0, c, D);
+    if constexpr (TAIL) own_channels(v, c, D);
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[k][e] = v.at(e);
   }
@@ -119,24 +132,33 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormP
   while (row < p.R) {
     float s[NV][8], ss = 0.f, unused = 0.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k) {
+      if constexpr (TAIL) own_channels(rx[k], 8 * (lane + TPR * k), D);
+      if constexpr (TAIL) if (p.residual) own_channels(rr[k], 8 * (lane + TPR * k), D);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         s[k][e] = rx[k].at(e);
         if (p.residual) s[k][e] += rr[k].at(e);
         ss = __builtin_fmaf(s[k][e], s[k][e], ss);
       }
+    }
     const int here = row;
     row += stride;
     if (row < p.R) load(row);
-    if (p.residual_out) {
+    auto store_stream = [&] {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int c = 8 * (lane + TPR * k);
-        store_raw8<RBF16>(p.residual_out, (size_t)here * D + c, s[k], D - c);
+        store_raw8<RBF16, TAIL>(p.residual_out, (size_t)here * D + c, s[k], D - c);
       }
-    }
+    };
+    // residual_out may be an input.  The row's last vector is loaded with channels
+    // of its neighbour's, which may be another wave's: then all waves have their
+    // loads before one stores.
+    constexpr bool kStoreLate = TAIL && TPR > 64;
+    if (!kStoreLate && p.residual_out) store_stream();
     row_sum2<TPR>(ss, unused, lds, turn);
+    if (kStoreLate && p.residual_out) store_stream();
     const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, inv_d, p.eps));
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -146,7 +168,7 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormP
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int c = 8 * (lane + TPR * k);
-        store_raw8<BF16>(p.y, (size_t)here * D + c, s[k], D - c);
+        store_raw8<BF16, TAIL>(p.y, (size_t)here * D + c, s[k], D - c);
       }
       continue;
     }
@@ -176,56 +198,70 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormP
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = 8 * (lane + TPR * k);
-      store_e4m3(p.y, (size_t)here * D + c, s[k], kE4m3Max * __builtin_amdgcn_rcpf(m[k]), D - c);
+      store_e4m3<TAIL>(p.y, (size_t)here * D + c, s[k], kE4m3Max * __builtin_amdgcn_rcpf(m[k]), D - c);
     }
   }
 }
 
 // The same rows; dw is summed per lane over the rows that a group walks, then
 // over the workgroup's groups through LDS, into one partial row per workgroup.
-template <bool BF16, bool RBF16, int TPR, int NV>
+template <bool BF16, bool RBF16, bool TAIL, int TPR, int NV>
 __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_bwd_kernel(NormParams p) {
   using Sh = NormShape<TPR>;
   __shared__ float2 lds[2][8];
   __shared__ float sums[Sh::kRows][TPR * 8];
+  constexpr bool kInLds = TPR == 512;
+  __shared__ Raw8<false> weights[kInLds ? TPR * NV : 1];
   int turn = 0;
   const int lane = threadIdx.x % TPR, D = p.D;
   const int stride = gridDim.x * Sh::kRows;
-  int row = blockIdx.x * Sh::kRows + threadIdx.x / TPR;
+  int row = first_row<TPR>();
   Raw8<RBF16> rs[NV], rr[NV];
   Raw8<BF16> rd[NV];
   auto load = [&](int at) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = 8 * (lane + TPR * k);
-      rs[k] = load_raw8<RBF16>(p.x, (size_t)at * D + c, D - c);
-      rd[k] = load_raw8<BF16>(p.dy, (size_t)at * D + c, D - c);
-      if (p.residual) rr[k] = load_raw8<RBF16>(p.residual, (size_t)at * D + c, D - c);
+      rs[k] = load_row8<RBF16, TAIL>(p.x, (size_t)at * D, c, D);
+      rd[k] = load_row8<BF16, TAIL>(p.dy, (size_t)at * D, c, D);
+      if (p.residual) rr[k] = load_row8<RBF16, TAIL>(p.residual, (size_t)at * D, c, D);
     }
   };
   if (row < p.R) load(row);
-  float w[NV][8], dw[NV][8];
+  Raw8<false> w[kInLds ? 1 : NV];
+  float dw[NV][8] = {};
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = 8 * (lane + TPR * k);
-    const Raw8<false> v = load_raw8<false>(p.w, c, D - c);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[k][e] = v.at(e);
-      dw[k][e] = 0.f;
-    }
+    Raw8<false> v = load_row8<false, TAIL>(p.w, 0, c, D);
+    if constexpr (TAIL) own_channels(v, c, D);
+    if constexpr (!kInLds) w[k] = v;
+    else if (threadIdx.x < TPR) weights[lane + TPR * k] = v;
   }
+  if constexpr (kInLds) __syncthreads();
+  auto weight = [&](int k) {
+    if constexpr (kInLds) return weights[lane + TPR * k];
+    else return w[k];
+  };
   const float inv_d = 1.f / (float)D;
   while (row < p.R) {
     float ss = 0.f, gs = 0.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k) {
+      if constexpr (TAIL) own_channels(rs[k], 8 * (lane + TPR * k), D);
+      if constexpr (TAIL) own_channels(rd[k], 8 * (lane + TPR * k), D);
+      if constexpr (TAIL) if (p.residual) {
+        own_channels(rr[k], 8 * (lane + TPR * k), D);
+        if constexpr (TPR > 64) hold(rr[k]);  // before the barrier: ds may be d_residual (as in the forward)
+      }
+      const Raw8<false> wk = weight(k);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float s = rs[k].at(e);
         ss = __builtin_fmaf(s, s, ss);
-        gs = __builtin_fmaf(rd[k].at(e) * w[k][e], s, gs);
+        gs = __builtin_fmaf(rd[k].at(e) * wk.at(e), s, gs);
       }
+    }
     row_sum2<TPR>(ss, gs, lds, turn);
     const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, inv_d, p.eps));
     const float kk = gs * inv_d * r * r;  // mean(g n) r: ds = r g - n (mean(g n) r)
@@ -233,20 +269,22 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_bwd_kernel(N
     row += stride;
     float ds[NV][8];
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k) {
+      const Raw8<false> wk = weight(k);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float n = rs[k].at(e) * r, d = rd[k].at(e);
-        ds[k][e] = __builtin_fmaf(-n, kk, r * (d * w[k][e]));
+        ds[k][e] = __builtin_fmaf(-n, kk, r * (d * wk.at(e)));
         if (p.residual) ds[k][e] += rr[k].at(e);
         dw[k][e] = __builtin_fmaf(d, n, dw[k][e]);
       }
+    }
     if (row < p.R) load(row);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = 8 * (lane + TPR * k);
-      store_raw8<RBF16>(p.y, (size_t)here * D + c, ds[k], D - c);
-      if (p.residual_out) store_raw8<BF16>(p.residual_out, (size_t)here * D + c, ds[k], D - c);
+      store_raw8<RBF16, TAIL>(p.y, (size_t)here * D + c, ds[k], D - c);
+      if (p.residual_out) store_raw8<BF16, TAIL>(p.residual_out, (size_t)here * D + c, ds[k], D - c);
     }
   }
   float* part = static_cast<float*>(p.part) + (size_t)blockIdx.x * D;
@@ -305,12 +343,12 @@ int norm_groups(int R, int rows, int per_cu) {
 
 constexpr int kFwdPerCu = 4, kBwdPerCu = 2;
 
-template <bool BF16, bool RBF16>
+template <bool BF16, bool RBF16, bool TAIL>
 hipError_t launch_fwd_t(const NormParams& p, hipStream_t s) {
   return norm_shape(p.D, [&](auto tpr, auto nv) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     using Sh = NormShape<TPR>;
-    hipLaunchKernelGGL((rmsnorm_kernel<BF16, RBF16, TPR, NV>), dim3(norm_groups(p.R, Sh::kRows, kFwdPerCu)),
+    hipLaunchKernelGGL((rmsnorm_kernel<BF16, RBF16, TAIL, TPR, NV>), dim3(norm_groups(p.R, Sh::kRows, kFwdPerCu)),
                        dim3(Sh::kThreads), 0, s, p);
     return hipGetLastError();
   });
@@ -322,13 +360,13 @@ int bwd_groups(int R, int D) {
   });
 }
 
-template <bool BF16, bool RBF16>
+template <bool BF16, bool RBF16, bool TAIL>
 hipError_t launch_bwd_t(const NormParams& p, hipStream_t s) {
   const int G = p.R > 0 ? bwd_groups(p.R, p.D) : 0;
   if (G > 0) {
     const hipError_t e = norm_shape(p.D, [&](auto tpr, auto nv) {
       constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-      hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, RBF16, TPR, NV>), dim3(G), dim3(NormShape<TPR>::kThreads), 0, s, p);
+      hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, RBF16, TAIL, TPR, NV>), dim3(G), dim3(NormShape<TPR>::kThreads), 0, s, p);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
@@ -342,14 +380,24 @@ hipError_t launch_bwd_t(const NormParams& p, hipStream_t s) {
 
 size_t rmsnorm_bwd_scratch(int R, int D) { return (size_t)bwd_groups(R, D) * D * 4; }
 
+template <bool TAIL>
+static hipError_t launch_fwd(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s) {
+  if (!bf16) return launch_fwd_t<false, false, TAIL>(p, s);
+  return res_bf16 ? launch_fwd_t<true, true, TAIL>(p, s) : launch_fwd_t<true, false, TAIL>(p, s);
+}
+
+template <bool TAIL>
+static hipError_t launch_bwd(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s) {
+  if (!bf16) return launch_bwd_t<false, false, TAIL>(p, s);
+  return res_bf16 ? launch_bwd_t<true, true, TAIL>(p, s) : launch_bwd_t<true, false, TAIL>(p, s);
+}
+
 hipError_t launch_rmsnorm(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s) {
-  if (!bf16) return launch_fwd_t<false, false>(p, s);
-  return res_bf16 ? launch_fwd_t<true, true>(p, s) : launch_fwd_t<true, false>(p, s);
+  return p.D % 8 ? launch_fwd<true>(bf16, res_bf16, p, s) : launch_fwd<false>(bf16, res_bf16, p, s);
 }
 
 hipError_t launch_rmsnorm_bwd(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s) {
-  if (!bf16) return launch_bwd_t<false, false>(p, s);
-  return res_bf16 ? launch_bwd_t<true, true>(p, s) : launch_bwd_t<true, false>(p, s);
+  return p.D % 8 ? launch_bwd<true>(bf16, res_bf16, p, s) : launch_bwd<false>(bf16, res_bf16, p, s);
 }
 
 }  // namespace mesa

@@ -55,16 +55,16 @@ __global__ __launch_bounds__(kThreads) void prep_bwd_kernel(PrepBwdParams p) {
 #pragma unroll
       for (int u = 0; u < kBlock; ++u) {
         const size_t e = seq + (size_t)min(t + u, T - 1) * D;
-        x[u] = load_raw8<BF16>(p.x[which], e, 8);
-        d[u] = load_raw8<false>(p.d[which], e, 8);
+        x[u] = load_raw8<BF16>(p.x[which], e);
+        d[u] = load_raw8<false>(p.d[which], e);
       }
     };
     load(t0);
 #pragma unroll
     for (int m = 0; m < W - 1; ++m) {
       const int r = t0 - (W - 1) + m;
-      if (r >= 0) win[m] = load_raw8<BF16>(p.x[which], seq + (size_t)r * D, 8);
-      else if (hist) win[m] = load_raw8<BF16>(hist, ((size_t)bh * (W - 1) + (W - 1 + r)) * D + c0, 8);
+      if (r >= 0) win[m] = load_raw8<BF16>(p.x[which], seq + (size_t)r * D);
+      else if (hist) win[m] = load_raw8<BF16>(hist, ((size_t)bh * (W - 1) + (W - 1 + r)) * D + c0);
       else win[m] = Raw8<BF16>{};
     }
     float acc[W][8] = {};  // acc[m]: dx of row t-(W-1)+m so far
@@ -111,12 +111,12 @@ __global__ __launch_bounds__(kThreads) void prep_bwd_kernel(PrepBwdParams p) {
         if (s < T && (s >= t0 || (t0 == 0 && p.dhist[which]))) {
           const int q = s - (T - (W - 1));  // the row of the history output that row s is copied to
           if (q >= 0 && p.d_hist[which]) {
-            const Raw8<BF16> v = load_raw8<BF16>(p.d_hist[which], ((size_t)bh * (W - 1) + q) * D + c0, 8);
+            const Raw8<BF16> v = load_raw8<BF16>(p.d_hist[which], ((size_t)bh * (W - 1) + q) * D + c0);
 #pragma unroll
             for (int c = 0; c < 8; ++c) acc[0][c] += v.at(c);
           }
-          if (s >= t0) store_raw8<BF16>(p.dx[which], seq + (size_t)s * D, acc[0], 8);
-          else store_raw8<BF16>(p.dhist[which], ((size_t)bh * (W - 1) + (W - 1 + s)) * D + c0, acc[0], 8);
+          if (s >= t0) store_raw8<BF16, false>(p.dx[which], seq + (size_t)s * D, acc[0], 8);
+          else store_raw8<BF16, false>(p.dhist[which], ((size_t)bh * (W - 1) + (W - 1 + s)) * D + c0, acc[0], 8);
         }
 #pragma unroll
         for (int m = 0; m < W - 1; ++m) {

@@ -184,3 +184,49 @@ def test_preprocess_backward_validation():
     assert call(qh=A + 4 * M, dqhist=A + 4 * M) == 1
     assert call(workspace=0) == 4
     assert call(wbytes=need - 1) == 4
+
+
+def apart(names):
+    """Distinct fake ranges, far apart."""
+    return {n: 0x7F0000000000 + i * 0x10000000 for i, n in enumerate(names)}
+
+
+def test_outputs_over_inputs_are_refused():
+    """Every output and the workspace against every input, at equal addresses and where one ends in the other."""
+    d = lru_desc()
+    a = apart(("x", "ga", "gi", "lam", "h0", "lengths", "y", "h_final", "workspace"))
+    ins = ("x", "ga", "gi", "lam", "h0", "lengths")
+    for o in ("y", "h_final", "workspace"):
+        for i in ins:
+            if (o, i) != ("h_final", "h0"):
+                assert call_lru_fwd(d, **{**a, o: a[i]}) == 1, (o, i)
+    assert call_lru_fwd(d, **{**a, "h_final": a["h0"] + 16}) == 1
+    assert call_lru_fwd(d, **{**a, "y": a["x"] - 16}) == 1 and call_lru_fwd(d, **{**a, "x": a["y"] - 16}) == 1
+
+    a = apart(ins + ("dy", "d_hfinal", "dx", "dga", "dgi", "dlam", "dh0", "workspace"))
+    for o in ("dx", "dga", "dgi", "dlam", "dh0", "workspace"):
+        for i in ins + ("dy", "d_hfinal"):
+            if (o, i) != ("dh0", "d_hfinal"):
+                assert call_lru_bwd(d, **{**a, o: a[i]}) == 1, (o, i)
+
+    a = apart(("x", "ga", "gi", "lam", "h", "y"))
+    for o in ("h", "y"):
+        for i in ("x", "ga", "gi", "lam"):
+            b = {**a, o: a[i]}
+            assert mesa.lib().mesa_lru_step(2, 100, 100, ctypes.c_float(8.0), 1, *[P(v) for v in b.values()], None) == 1, (o, i)
+
+    a = apart(("x", "residual", "w", "y", "scale", "residual_out"))
+    for kw in (dict(res=1), dict(res=0), dict(res=1, out=1), dict(res=1, out=1, group=128)):
+        for o, over in (("y", ("x", "residual", "w", "residual_out")), ("residual_out", ("w",)),
+                        ("scale", ("x", "residual", "w", "residual_out"))):
+            for i in over:
+                if o != "scale" or "out" in kw:
+                    assert call_norm(**kw, **{**a, o: a[i]}) == 1, (kw, o, i)
+        assert call_norm(**kw, **{**a, "residual_out": a["residual"] + 16}) == 1
+    assert call_norm(res=0, **{**a, "residual_out": a["x"]}) == 1  # an fp32 stream over bf16 rows
+
+    a = apart(("s", "w", "dy", "d_residual", "ds", "dx", "dw", "workspace"))
+    for o in ("ds", "dx", "dw", "workspace"):
+        for i in ("s", "w", "dy", "d_residual"):
+            if (o, i) != ("ds", "d_residual"):
+                assert call_norm_bwd(**{**a, o: a[i]}) == 1, (o, i)

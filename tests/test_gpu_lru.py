@@ -277,7 +277,7 @@ def test_slices_of_one_projection(dtype, D):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("N,D", [(1, 2), (1, 3), (1, 2048), (3, 1001), (256, 130), (17, 4096)])
+@pytest.mark.parametrize("N,D", [(1, 2), (1, 3), (1, 2048), (3, 1001), (5, 4), (2, 5), (70, 6), (3, 7), (2, 9), (300, 15), (65, 4099), (256, 130), (17, 4096)])
 def test_step_matches_the_oracle(dtype, N, D):
     d = draw(N, 1, D, dtype, seed=8)
     t = to_dev(d, dtype)

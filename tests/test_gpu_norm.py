@@ -94,6 +94,22 @@ def test_forward_matches_the_oracle(R, D, dtype, res):
     check_forward(d, r, dtype, dtype, None, 0.5, residual=False)
 
 
+def check_backward(d, g, dtype, res, with_res):
+    s, w, dy = host(d["residual"]), host(d["w"]), host(d["dy"])
+    R, D = s.shape
+    dres = host(d["d_residual"]) if with_res else None
+    ref = rmsnorm_backward(s, w, dy, d_residual=dres, eps=1e-5)
+    rstd = 1 / np.sqrt((s * s).mean(1, keepdims=True) + 1e-5)
+    n, gg = np.abs(s * rstd), np.abs(dy * w)
+    size = rstd * (gg + n * (gg * n).mean(1, keepdims=True))
+    bound = (1.5 * depth(D) + 12) * E * size + 2 * E * np.abs(ref["ds"])
+    close(g["ds"], ref["ds"], bound + half(res) * np.abs(ref["ds"]), "ds")
+    if dtype != res:
+        close(g["dx"], ref["ds"], bound + half(dtype) * np.abs(ref["ds"]), "dx")
+    # at most R additions deep over the rows
+    close(g["dw"], ref["dw"], (R + 0.5 * depth(D) + 12) * E * (np.abs(dy) * n).sum(0), "dw")
+
+
 @pytest.mark.parametrize("dtype,res", TYPES)
 @pytest.mark.parametrize("R,D", SIZES)
 def test_backward_matches_the_oracle(R, D, dtype, res):
@@ -101,18 +117,7 @@ def test_backward_matches_the_oracle(R, D, dtype, res):
     for with_res in (True, False):
         g = mesa.rmsnorm_bwd(t["residual"], t["w"], t["dy"], d_residual=t["d_residual"] if with_res else None, eps=1e-5)
         torch.cuda.synchronize()
-        s, w, dy = host(d["residual"]), host(d["w"]), host(d["dy"])
-        dres = host(d["d_residual"]) if with_res else None
-        ref = rmsnorm_backward(s, w, dy, d_residual=dres, eps=1e-5)
-        rstd = 1 / np.sqrt((s * s).mean(1, keepdims=True) + 1e-5)
-        n, gg = np.abs(s * rstd), np.abs(dy * w)
-        size = rstd * (gg + n * (gg * n).mean(1, keepdims=True))
-        bound = (1.5 * depth(D) + 12) * E * size + 2 * E * np.abs(ref["ds"])
-        close(g["ds"], ref["ds"], bound + half(res) * np.abs(ref["ds"]), "ds")
-        if dtype != res:
-            close(g["dx"], ref["ds"], bound + half(dtype) * np.abs(ref["ds"]), "dx")
-        # at most R additions deep over the rows
-        close(g["dw"], ref["dw"], (R + 0.5 * depth(D) + 12) * E * (np.abs(dy) * n).sum(0), "dw")
+        check_backward(d, g, dtype, res, with_res)
 
 
 def test_rows_of_zeros_and_extremes():
@@ -136,7 +141,8 @@ def test_rows_of_zeros_and_extremes():
 def test_in_place_residual():
     """out["residual"] may be the residual, and the backward's ds may be d_residual: same values as apart."""
     for dtype, res in TYPES:
-        for D in (96, 1001, 4096, 12000):
+        # (2561, 4101: a row's last vector and its neighbour lie in different waves)
+        for D in (3, 96, 1001, 2561, 4096, 4101, 12000, 12295):
             d, t = draw(5, D, dtype, res, seed=4)
             a = mesa.rmsnorm(t["x"], t["w"], residual=t["residual"], quant_group=128)
             b_res = t["residual"].clone()
@@ -197,3 +203,29 @@ def test_gradients_match_differences():
             vals.append(loss(*a))
         num, ana = (vals[0] - vals[1]) / (2 * step), float((g[gk].double() * e.double()).sum())
         assert abs(num - ana) <= 3e-3 * float(g[gk].double().norm()) + 1e-3, (gk, num, ana)
+
+
+@pytest.mark.parametrize("dtype,res", TYPES)
+@pytest.mark.parametrize("D", [2, 5, 9, 10, 11, 12, 13, 14, 15, 134, 518, 1001, 2051, 4109, 12006])
+def test_rows_that_end_within_a_vector(D, dtype, res):
+    """Every remainder of D by 8 against the oracle, and nothing written behind the last row."""
+    R, mark = 3, 77
+    d, t = draw(R, D, dtype, res, seed=5)
+    for group in (None, 0, 128):
+        y_type = TORCH[dtype] if group is None else torch.float8_e4m3fn
+        y, stream = torch.empty(R * D + 16, dtype=y_type, device="cuda"), torch.empty(R * D + 16, dtype=TORCH[res], device="cuda")
+        y.view(torch.uint8).fill_(mark)
+        stream.view(torch.uint8).fill_(mark)
+        r = mesa.rmsnorm(t["x"], t["w"], residual=t["residual"], eps=1e-5, quant_group=group,
+                         out={"y": y[:R * D].view(R, D), "residual": stream[:R * D].view(R, D)})
+        torch.cuda.synchronize()
+        check_forward(d, r, dtype, res, group, 1e-5)
+        assert (y.view(torch.uint8)[R * D * y.element_size():] == mark).all()
+        assert (stream.view(torch.uint8)[R * D * stream.element_size():] == mark).all()
+    ds = torch.empty(R * D + 16, dtype=TORCH[res], device="cuda")
+    ds.view(torch.uint8).fill_(mark)
+    g = mesa.rmsnorm_bwd(t["residual"], t["w"], t["dy"], d_residual=t["d_residual"], eps=1e-5,
+                         out={"ds": ds[:R * D].view(R, D)})
+    torch.cuda.synchronize()
+    check_backward(d, g, dtype, res, True)
+    assert (ds.view(torch.uint8)[R * D * ds.element_size():] == mark).all()
