@@ -100,7 +100,7 @@ __device__ __forceinline__ void store_e4m3(void* base, size_t elem, const float 
   }
 }
 
-template <bool BF16, bool RBF16, bool TAIL, int TPR, int NV>
+template <bool BF16, bool RBF16, RowEnd END, int TPR, int NV>
 __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormParams p) {
   using Sh = NormShape<TPR>;
   __shared__ float2 lds[2][8];
@@ -114,8 +114,8 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormP
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = 8 * (lane + TPR * k);
-      rx[k] = load_row8<BF16, TAIL>(p.x, (size_t)at * D, c, D);
-      if (p.residual) rr[k] = load_row8<RBF16, TAIL>(p.residual, (size_t)at * D, c, D);
+      rx[k] = load_row8<BF16, END>(p.x, (size_t)at * D, c, D);
+      if (p.residual) rr[k] = load_row8<RBF16, END>(p.residual, (size_t)at * D, c, D);
     }
   };
   if (row < p.R) load(row);
@@ -123,8 +123,8 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormP
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = 8 * (lane + TPR * k);
-    Raw8<false> v = load_row8<false, TAIL>(p.w, 0, c, D);
-    if constexpr (TAIL) own_channels(v, c, D);
+    Raw8<false> v = load_row8<false, END>(p.w, 0, c, D);
+    if constexpr (END == RowEnd::kWithin) own_channels(v, c, D);
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[k][e] = v.at(e);
   }
@@ -133,8 +133,8 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormP
     float s[NV][8], ss = 0.f, unused = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if constexpr (TAIL) own_channels(rx[k], 8 * (lane + TPR * k), D);
-      if constexpr (TAIL) if (p.residual) own_channels(rr[k], 8 * (lane + TPR * k), D);
+      if constexpr (END == RowEnd::kWithin) own_channels(rx[k], 8 * (lane + TPR * k), D);
+      if constexpr (END == RowEnd::kWithin) if (p.residual) own_channels(rr[k], 8 * (lane + TPR * k), D);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         s[k][e] = rx[k].at(e);
@@ -149,13 +149,13 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormP
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int c = 8 * (lane + TPR * k);
-        store_raw8<RBF16, TAIL>(p.residual_out, (size_t)here * D + c, s[k], D - c);
+        store_raw8<RBF16, END != RowEnd::kWhole>(p.residual_out, (size_t)here * D + c, s[k], D - c);
       }
     };
     // residual_out may be an input.  The row's last vector is loaded with channels
     // of its neighbour's, which may be another wave's: then all waves have their
     // loads before one stores.
-    constexpr bool kStoreLate = TAIL && TPR > 64;
+    constexpr bool kStoreLate = END == RowEnd::kWithin && TPR > 64;
     if (!kStoreLate && p.residual_out) store_stream();
     row_sum2<TPR>(ss, unused, lds, turn);
     if (kStoreLate && p.residual_out) store_stream();
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormP
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int c = 8 * (lane + TPR * k);
-        store_raw8<BF16, TAIL>(p.y, (size_t)here * D + c, s[k], D - c);
+        store_raw8<BF16, END != RowEnd::kWhole>(p.y, (size_t)here * D + c, s[k], D - c);
       }
       continue;
     }
@@ -198,14 +198,14 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormP
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = 8 * (lane + TPR * k);
-      store_e4m3<TAIL>(p.y, (size_t)here * D + c, s[k], kE4m3Max * __builtin_amdgcn_rcpf(m[k]), D - c);
+      store_e4m3<END != RowEnd::kWhole>(p.y, (size_t)here * D + c, s[k], kE4m3Max * __builtin_amdgcn_rcpf(m[k]), D - c);
     }
   }
 }
 
 // The same rows; dw is summed per lane over the rows that a group walks, then
 // over the workgroup's groups through LDS, into one partial row per workgroup.
-template <bool BF16, bool RBF16, bool TAIL, int TPR, int NV>
+template <bool BF16, bool RBF16, RowEnd END, int TPR, int NV>
 __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_bwd_kernel(NormParams p) {
   using Sh = NormShape<TPR>;
   __shared__ float2 lds[2][8];
@@ -222,9 +222,9 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_bwd_kernel(N
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = 8 * (lane + TPR * k);
-      rs[k] = load_row8<RBF16, TAIL>(p.x, (size_t)at * D, c, D);
-      rd[k] = load_row8<BF16, TAIL>(p.dy, (size_t)at * D, c, D);
-      if (p.residual) rr[k] = load_row8<RBF16, TAIL>(p.residual, (size_t)at * D, c, D);
+      rs[k] = load_row8<RBF16, END>(p.x, (size_t)at * D, c, D);
+      rd[k] = load_row8<BF16, END>(p.dy, (size_t)at * D, c, D);
+      if (p.residual) rr[k] = load_row8<RBF16, END>(p.residual, (size_t)at * D, c, D);
     }
   };
   if (row < p.R) load(row);
@@ -233,8 +233,8 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_bwd_kernel(N
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = 8 * (lane + TPR * k);
-    Raw8<false> v = load_row8<false, TAIL>(p.w, 0, c, D);
-    if constexpr (TAIL) own_channels(v, c, D);
+    Raw8<false> v = load_row8<false, END>(p.w, 0, c, D);
+    if constexpr (END == RowEnd::kWithin) own_channels(v, c, D);
     if constexpr (!kInLds) w[k] = v;
     else if (threadIdx.x < TPR) weights[lane + TPR * k] = v;
   }
@@ -248,9 +248,9 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_bwd_kernel(N
     float ss = 0.f, gs = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if constexpr (TAIL) own_channels(rs[k], 8 * (lane + TPR * k), D);
-      if constexpr (TAIL) own_channels(rd[k], 8 * (lane + TPR * k), D);
-      if constexpr (TAIL) if (p.residual) {
+      if constexpr (END == RowEnd::kWithin) own_channels(rs[k], 8 * (lane + TPR * k), D);
+      if constexpr (END == RowEnd::kWithin) own_channels(rd[k], 8 * (lane + TPR * k), D);
+      if constexpr (END == RowEnd::kWithin) if (p.residual) {
         own_channels(rr[k], 8 * (lane + TPR * k), D);
         if constexpr (TPR > 64) hold(rr[k]);  // before the barrier: ds may be d_residual (as in the forward)
       }
@@ -283,8 +283,8 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_bwd_kernel(N
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = 8 * (lane + TPR * k);
-      store_raw8<RBF16, TAIL>(p.y, (size_t)here * D + c, ds[k], D - c);
-      if (p.residual_out) store_raw8<BF16, TAIL>(p.residual_out, (size_t)here * D + c, ds[k], D - c);
+      store_raw8<RBF16, END != RowEnd::kWhole>(p.y, (size_t)here * D + c, ds[k], D - c);
+      if (p.residual_out) store_raw8<BF16, END != RowEnd::kWhole>(p.residual_out, (size_t)here * D + c, ds[k], D - c);
     }
   }
   float* part = static_cast<float*>(p.part) + (size_t)blockIdx.x * D;
@@ -322,17 +322,19 @@ __global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* part, floa
 }
 
 // Calls fn(TPR, NV) as constants for the smallest row group that holds D channels.
-template <typename F>
+template <RowEnd END, typename F>
 auto norm_shape(int D, F&& fn) {
   using std::integral_constant;
-  if (D <= 128) return fn(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-  if (D <= 256) return fn(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-  if (D <= 512) return fn(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  if (D <= 1024) return fn(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-  if (D <= 2048) return fn(integral_constant<int, 64>{}, integral_constant<int, 4>{});
-  if (D <= 4096) return fn(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  if (D <= 8192) return fn(integral_constant<int, 256>{}, integral_constant<int, 4>{});
-  return fn(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+  if constexpr (END != RowEnd::kShort) {
+    if (D > 8192) return fn(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+    if (D > 4096) return fn(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+    if (D > 2048) return fn(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    if (D > 1024) return fn(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+    if (D > 512) return fn(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    if (D > 256) return fn(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    if (D > 128) return fn(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+  }
+  return fn(integral_constant<int, 16>{}, integral_constant<int, 1>{});
 }
 
 // Workgroups of a launch: as many as rows need, at most `per_cu` a CU.
@@ -343,30 +345,30 @@ int norm_groups(int R, int rows, int per_cu) {
 
 constexpr int kFwdPerCu = 4, kBwdPerCu = 2;
 
-template <bool BF16, bool RBF16, bool TAIL>
+template <bool BF16, bool RBF16, RowEnd END>
 hipError_t launch_fwd_t(const NormParams& p, hipStream_t s) {
-  return norm_shape(p.D, [&](auto tpr, auto nv) {
+  return norm_shape<END>(p.D, [&](auto tpr, auto nv) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     using Sh = NormShape<TPR>;
-    hipLaunchKernelGGL((rmsnorm_kernel<BF16, RBF16, TAIL, TPR, NV>), dim3(norm_groups(p.R, Sh::kRows, kFwdPerCu)),
+    hipLaunchKernelGGL((rmsnorm_kernel<BF16, RBF16, END, TPR, NV>), dim3(norm_groups(p.R, Sh::kRows, kFwdPerCu)),
                        dim3(Sh::kThreads), 0, s, p);
     return hipGetLastError();
   });
 }
 
 int bwd_groups(int R, int D) {
-  return norm_shape(D, [&](auto tpr, auto) {
+  return norm_shape<RowEnd::kWhole>(D, [&](auto tpr, auto) {
     return norm_groups(R, NormShape<decltype(tpr)::value>::kRows, kBwdPerCu);
   });
 }
 
-template <bool BF16, bool RBF16, bool TAIL>
+template <bool BF16, bool RBF16, RowEnd END>
 hipError_t launch_bwd_t(const NormParams& p, hipStream_t s) {
   const int G = p.R > 0 ? bwd_groups(p.R, p.D) : 0;
   if (G > 0) {
-    const hipError_t e = norm_shape(p.D, [&](auto tpr, auto nv) {
+    const hipError_t e = norm_shape<END>(p.D, [&](auto tpr, auto nv) {
       constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-      hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, RBF16, TAIL, TPR, NV>), dim3(G), dim3(NormShape<TPR>::kThreads), 0, s, p);
+      hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, RBF16, END, TPR, NV>), dim3(G), dim3(NormShape<TPR>::kThreads), 0, s, p);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
@@ -380,24 +382,32 @@ hipError_t launch_bwd_t(const NormParams& p, hipStream_t s) {
 
 size_t rmsnorm_bwd_scratch(int R, int D) { return (size_t)bwd_groups(R, D) * D * 4; }
 
-template <bool TAIL>
+template <RowEnd END>
 static hipError_t launch_fwd(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s) {
-  if (!bf16) return launch_fwd_t<false, false, TAIL>(p, s);
-  return res_bf16 ? launch_fwd_t<true, true, TAIL>(p, s) : launch_fwd_t<true, false, TAIL>(p, s);
+  if (!bf16) return launch_fwd_t<false, false, END>(p, s);
+  return res_bf16 ? launch_fwd_t<true, true, END>(p, s) : launch_fwd_t<true, false, END>(p, s);
 }
 
-template <bool TAIL>
+template <RowEnd END>
 static hipError_t launch_bwd(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s) {
-  if (!bf16) return launch_bwd_t<false, false, TAIL>(p, s);
-  return res_bf16 ? launch_bwd_t<true, true, TAIL>(p, s) : launch_bwd_t<true, false, TAIL>(p, s);
+  if (!bf16) return launch_bwd_t<false, false, END>(p, s);
+  return res_bf16 ? launch_bwd_t<true, true, END>(p, s) : launch_bwd_t<true, false, END>(p, s);
 }
 
 hipError_t launch_rmsnorm(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s) {
-  return p.D % 8 ? launch_fwd<true>(bf16, res_bf16, p, s) : launch_fwd<false>(bf16, res_bf16, p, s);
+  switch (row_end(p.D)) {
+    case RowEnd::kWhole: return launch_fwd<RowEnd::kWhole>(bf16, res_bf16, p, s);
+    case RowEnd::kWithin: return launch_fwd<RowEnd::kWithin>(bf16, res_bf16, p, s);
+    default: return launch_fwd<RowEnd::kShort>(bf16, res_bf16, p, s);
+  }
 }
 
 hipError_t launch_rmsnorm_bwd(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s) {
-  return p.D % 8 ? launch_bwd<true>(bf16, res_bf16, p, s) : launch_bwd<false>(bf16, res_bf16, p, s);
+  switch (row_end(p.D)) {
+    case RowEnd::kWhole: return launch_bwd<RowEnd::kWhole>(bf16, res_bf16, p, s);
+    case RowEnd::kWithin: return launch_bwd<RowEnd::kWithin>(bf16, res_bf16, p, s);
+    default: return launch_bwd<RowEnd::kShort>(bf16, res_bf16, p, s);
+  }
 }
 
 }  // namespace mesa

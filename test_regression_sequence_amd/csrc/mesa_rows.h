@@ -87,21 +87,29 @@ __device__ __forceinline__ Raw8<BF16> load_part8(const void* base, size_t elem, 
   return r;
 }
 
-// Channels ch .. ch+7 of the row of D that starts at `row`, 0 behind it.  TAIL: D
-// is no multiple of 8; then a vector that the row ends within is loaded as the
-// row's last 8, and own_channels() has to put them into place.  (A choice made
-// at compile time: the loads of whole vectors alone are 2 to 5 % faster.)
-template <bool BF16, bool TAIL>
+// How rows of D channels end: with a whole vector (D a multiple of 8), within a
+// vector (D > 8), or before the first one does (D < 8).  A choice made at compile
+// time: without the others' code the loads of whole vectors are 2 to 5 % faster.
+enum class RowEnd { kWhole, kWithin, kShort };
+__host__ __device__ constexpr RowEnd row_end(int D) {
+  return D % 8 == 0 ? RowEnd::kWhole : D > 8 ? RowEnd::kWithin : RowEnd::kShort;
+}
+
+// Channels ch .. ch+7 of the row that starts at `row`, 0 behind it.  kWithin: the
+// vector that the row ends within, and those behind it, are loaded as the row's
+// last 8; own_channels() then has to put them into place.
+template <bool BF16, RowEnd END>
 __device__ __forceinline__ Raw8<BF16> load_row8(const void* base, size_t row, int ch, int D) {
   constexpr uint32_t ES = BF16 ? 2 : 4;
-  if constexpr (!TAIL) {
+  if constexpr (END == RowEnd::kWithin) {  // (a uniform row and a 32-bit offset within it)
+    return load_raw8<BF16>(static_cast<const char*>(base) + row * ES + (uint32_t)min(ch, D - 8) * ES, 0);
+  } else if constexpr (END == RowEnd::kWhole) {
     Raw8<BF16> r{};
     if (ch < D) r = load_raw8<BF16>(base, row + ch);
     return r;
+  } else {
+    return load_part8<BF16>(base, row + ch, D - ch);
   }
-  if (D >= 8)  // (a uniform row and a 32-bit offset within it)
-    return load_raw8<BF16>(static_cast<const char*>(base) + row * ES + (uint32_t)min(ch, D - 8) * ES, 0);
-  return load_part8<BF16>(base, row + ch, D - ch);
 }
 
 // Has r's loads finished here.
@@ -111,7 +119,7 @@ __device__ __forceinline__ void hold(Raw8<false>& r) { asm volatile("" : "+v"(r.
 // What load_row8 loaded of channels behind the row becomes 0, the others move
 // from the end of the vector to their places.
 __device__ __forceinline__ void own_channels(Raw8<true>& r, int ch, int D) {
-  if (ch + 8 <= D || D < 8) return;
+  if (ch + 8 <= D) return;
   typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
   const u64x2 v = __builtin_bit_cast(u64x2, r.v);
   const int by = min(16 * (ch + 8 - D), 128);  // bits, at least 16
@@ -121,7 +129,7 @@ __device__ __forceinline__ void own_channels(Raw8<true>& r, int ch, int D) {
   r.v = __builtin_bit_cast(u16x8, o);
 }
 __device__ __forceinline__ void own_channels(Raw8<false>& r, int ch, int D) {
-  if (ch + 8 <= D || D < 8) return;
+  if (ch + 8 <= D) return;
   const int by = min(ch + 8 - D, 8);  // channels
   float v[8];
 #pragma unroll
