@@ -1,5 +1,8 @@
 // Gated linear recurrence: h_t = a_t h_{t-1} + u_t per channel, with decay and
-// input from the token's gates (mesa_lru_gate.h).
+// input from the token's gates (mesa_lru_gate.h).  A tile reads x, ga and gi once,
+// forms a and u in registers, gets its carry (mesa_lru_tile.h), walks its tokens
+// again from it and writes y.  Bound by HBM: at D=2048, bf16, 111 us at B=1,
+// T=32768 and 113 at B=8, T=4096, both 579 MB at 5.1 to 5.2 TB/s (a copy: 5.15).
 #include <algorithm>
 
 #include "mesa_common.h"
@@ -163,7 +166,8 @@ __global__ __launch_bounds__(kThreads) void lru_ready_kernel(uint64_t* words, si
 }
 
 // One token: 8 channels a lane, bound by HBM (x, ga, gi and the state in, the
-// state and y out).
+// state and y out): 46 us at N=4096, D=4096, bf16 (5.7 TB/s), and by the latency
+// of a launch for few tokens (2.3 us).
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void lru_step_kernel(LruParams p) {
   const int groups = (p.D + 7) / 8;

@@ -13,7 +13,8 @@
 // group's and only complete this group's rows, so (W-1)/Steps of the work is
 // done twice.  Loads run one block of tokens ahead.  dw is summed per lane, per
 // workgroup through LDS, and over workgroups by a second kernel, all in a fixed
-// order.
+// order.  At B=8, H=16, T=4096, d=128, W=4, bf16: 222 us, 1.19 GB at 5.4 TB/s, of
+// which 0.11 GB are rows that two groups read.
 #include "mesa_common.h"
 #include "mesa_kernels.h"
 #include "mesa_prep_rows.h"
