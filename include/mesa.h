@@ -511,8 +511,8 @@ mesa_status mesa_qk_preprocess(int32_t B, int32_t H, int32_t T, int32_t d, int32
  *
  * Arithmetic and states are fp32 for either dtype.  Every sum is formed in a
  * fixed order: equal inputs give bitwise equal results.
- * Supported: 2 <= D <= ld <= 2^20, T >= 0, B >= 1 with B ceil(T/64) ceil(D/64)
- * <= 2^23; c > 0, finite (else MESA_ERR_INVALID_ARG).
+ * Supported: 2 <= D <= ld <= 2^20, T >= 0, B >= 1 with B max(ceil(T/64), 1)
+ * ceil(D/64) <= 2^23; c > 0, finite (else MESA_ERR_INVALID_ARG).
  * Outputs and workspace may not overlap inputs but as said (MESA_ERR_INVALID_ARG):
  * h_final may be h0, dh0 may be d_hfinal.  Two calls may not use one workspace at
  * the same time. */

@@ -54,7 +54,7 @@ mesa_status check_lru(const mesa_lru_desc* d) {
   if (!(d->c > 0.f) || std::isinf(d->c)) return MESA_ERR_INVALID_ARG;
   // lanes load two channels; offsets within a tile of tokens are 32-bit; a launch has at most 2^32 threads
   if (d->D < 2 || d->ld > kLruMaxStride) return MESA_ERR_UNSUPPORTED;
-  const double tiles = (double)d->B * (((long long)d->T + 63) / 64) * ((d->D + 63) / 64);
+  const double tiles = (double)d->B * (d->T > 64 ? ((long long)d->T + 63) / 64 : 1) * ((d->D + 63) / 64);
   if (tiles > 8388608.0) return MESA_ERR_UNSUPPORTED;
   return MESA_OK;
 }

@@ -19,7 +19,7 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 // log(1 + e) = 2 artanh(q) = 2 (q + q^3/3 + q^5/5 + ..), q = e / (2 + e) <= 1/3:
 // the first term left out, q^15/15, is below 2e-8 of the sum.
 __device__ __forceinline__ float lru_softplus(float z) {
-  const float y = -fabsf(z), hi = y * kLog2e;
+  const float y = fmaxf(-fabsf(z), -150.f), hi = y * kLog2e;  // (exp(-150) is 0 here; an infinite y would give NaN)
   const float lo = __builtin_fmaf(y, 1.92596303e-8f, __builtin_fmaf(y, kLog2e, -hi));  // log2(e) - kLog2e = 1.926e-8
   float e = __builtin_amdgcn_exp2f(hi);
   e = __builtin_fmaf(e, lo * kLn2, e);
@@ -33,8 +33,9 @@ __device__ __forceinline__ float lru_softplus(float z) {
   return __builtin_fmaf(2.f * q, p, fmaxf(z, 0.f));
 }
 
-// c log2(e) softplus(lam): a channel's decay in halvings per token with its gate open.
-__device__ __forceinline__ float lru_rate(float lam, float c) { return kLog2e * c * lru_softplus(lam); }
+// c log2(e) softplus(lam): a channel's decay in halvings per token with its gate
+// open; finite, so that a closed gate or a decay of 0 leaves no 0 * inf.
+__device__ __forceinline__ float lru_rate(float lam, float c) { return fminf(kLog2e * c * lru_softplus(lam), 0x1p126f); }
 
 // sigmoid(lam) / softplus(lam), the factor from dL/d log t to dL/dlam.  Below
 // lam = -15 both are exp(lam) to within exp(-15) = 3e-7 of themselves, and

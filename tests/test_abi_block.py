@@ -42,7 +42,7 @@ BAD_LRU = [
     (dict(B=0), 1), (dict(T=-1), 1), (dict(D=0, ld=100), 1), (dict(ld=99), 1), (dict(c=0.0), 1), (dict(c=-1.0), 1),
     (dict(c=float("inf")), 1), (dict(c=float("nan")), 1), (dict(dtype=2), 1),
     (dict(ld=(1 << 20) + 1), 2), (dict(D=1), 2), (dict(B=1 << 19, T=64 * 8, D=128, ld=128), 0), (dict(B=1 << 19, T=64 * 8 + 1, D=128, ld=128), 2),
-    (dict(B=2 ** 31 - 1, T=2 ** 31 - 1), 2),
+    (dict(B=2 ** 31 - 1, T=2 ** 31 - 1), 2), (dict(B=2 ** 31 - 1, T=0, D=2), 2), (dict(B=(1 << 23) + 1, T=0, D=2), 2),
 ]
 
 

@@ -360,6 +360,53 @@ def test_closed_gates_are_exact():
     assert (g["dh0"] == 150).all()
 
 
+def test_initial_gradient_over_the_final_one():
+    """dh0 may be d_hfinal itself, with many tiles reading it and one writing it."""
+    d = draw(2, 6000, 129, "bf16", seed=14, ragged=True)
+    t = to_dev(d, "bf16")
+    kw = dict(c=C, h0=t["h0"], lengths=t["lengths"], state_grads=True)
+    last = torch.randn(2, 129, generator=torch.Generator().manual_seed(3)).cuda()
+    want = mesa.lru_bwd(t["x"], t["ga"], t["gi"], t["lam"], t["dy"], d_hfinal=last, **kw)
+    for _ in range(5):
+        both = last.clone()
+        g = mesa.lru_bwd(t["x"], t["ga"], t["gi"], t["lam"], t["dy"], d_hfinal=both, out={"dh0": both}, **kw)
+        torch.cuda.synchronize()
+        assert g["dh0"] is both
+        for key in want:
+            assert torch.equal(g[key], want[key]), key
+
+
+def test_decay_parameters_beyond_every_use():
+    """Where softplus(lam) is 0 in fp32 the state stays and no gradient reaches the inputs; where exp(-c softplus(lam)
+    sigmoid(ga)) is 0, or far below a half step, every token starts anew, y = sigmoid(gi) x; infinities included,
+    nothing is NaN."""
+    lam = torch.tensor([-float("inf"), -1e30, -200.0, 200.0, 1e30, float("inf")]).cuda()
+    gen = torch.Generator().manual_seed(5)
+    x, ga, gi, dy = (torch.randn(2, 300, 6, generator=gen).cuda() for _ in range(4))
+    h0 = torch.randn(2, 6, generator=gen).cuda()
+    for c in (8.0, 1e38):
+        r = mesa.lru_fwd(x, ga, gi, lam, c=c, h0=h0, return_state=True)
+        g = mesa.lru_bwd(x, ga, gi, lam, dy, c=c, h0=h0, state_grads=True)
+        state = h0.clone()
+        y1 = mesa.lru_step(*(v[:, 0].contiguous() for v in (x, ga, gi)), lam, state, c=c)["y"]
+        torch.cuda.synchronize()
+        for v in (r, g):
+            assert all(torch.isfinite(e).all() for e in v.values())
+        assert torch.equal(r["y"][..., :3], h0[:, None, :3].expand(-1, 300, -1))
+        assert torch.equal(y1[:, :3], h0[:, :3]) and torch.equal(state[:, :3], h0[:, :3])
+        assert not any(g[k][..., :3].any() for k in ("dx", "dga", "dgi"))
+        si, xd = torch.sigmoid(gi.double()), x.double()
+        want = {"y": si * xd, "dx": si * dy.double(), "dgi": dy.double() * xd * si * (1 - si)}
+        for k, w in want.items():
+            got = (r if k == "y" else g)[k].double()[..., 3:]
+            assert ((got - w[..., 3:]).abs() <= 16 * E * w[..., 3:].abs()).all(), k
+        assert ((y1.double() - want["y"][:, 0])[:, 3:].abs() <= 16 * E * want["y"][:, 0, 3:].abs()).all()
+        # lam = 200 with c = 8: over these gates (above -4.6, so sigmoid(ga) > 0.01) -log a > 16, a < 1.2e-7 and
+        # -log(a) a < 1.9e-6, which bounds dga / (|g| (|h| + |x|)) with factors below 5 each; elsewhere a is 0
+        assert ga.min() > -4.6 and (g["dga"][..., 3].abs() < 1e-4).all() and (g["dh0"][:, 3].abs() < 1e-6).all()
+        assert not g["dga"][..., 4:].any() and not g["dh0"][:, 4:].any()
+
+
 def test_causality():
     """Inputs behind token t change nothing up to it, bit for bit."""
     d = draw(1, 700, 96, "f32", seed=11)
