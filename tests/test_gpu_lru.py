@@ -407,6 +407,34 @@ def test_decay_parameters_beyond_every_use():
         assert not g["dga"][..., 4:].any() and not g["dh0"][:, 4:].any()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_same_bits_wherever_rows_start_in_a_cache_line(dtype):
+    """Tensors 16 bytes behind a cache line, and rows of a wider tensor, against aligned ones."""
+    d = draw(3, 700, 192, dtype, seed=15, ragged=True)
+    t = to_dev(d, dtype)
+    want = run_fwd(d, t)
+    kw = dict(c=C, h0=t["h0"], lengths=t["lengths"])
+    grads = mesa.lru_bwd(t["x"], t["ga"], t["gi"], t["lam"], t["dy"], **kw)
+    step = 16 // t["x"].element_size()
+    shape, n = t["x"].shape, t["x"].numel()
+
+    def behind(v):
+        buf = torch.empty(n + step, dtype=v.dtype, device="cuda")[step:].view(shape)
+        return buf.copy_(v)
+
+    def wider(v):
+        return torch.cat([v, v[..., :step]], -1)[..., :192]
+
+    for move in (behind, wider):
+        x, ga, gi = (move(t[k]) for k in ("x", "ga", "gi"))
+        r = mesa.lru_fwd(x, ga, gi, t["lam"], return_state=True, **kw)
+        g = mesa.lru_bwd(x, ga, gi, t["lam"], t["dy"], **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(r["y"], want["y"]) and torch.equal(r["h_final"], want["h_final"])
+        for k in grads:
+            assert torch.equal(g[k], grads[k]), (move.__name__, k)
+
+
 def test_causality():
     """Inputs behind token t change nothing up to it, bit for bit."""
     d = draw(1, 700, 96, "f32", seed=11)

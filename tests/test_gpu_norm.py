@@ -205,6 +205,20 @@ def test_gradients_match_differences():
         assert abs(num - ana) <= 3e-3 * float(g[gk].double().norm()) + 1e-3, (gk, num, ana)
 
 
+def test_stream_over_the_rows():
+    """out["residual"] may be x where the types are equal, and without a residual the stream is x itself."""
+    for dtype in ("f32", "bf16"):
+        for D in (5, 130, 2048, 2561, 4101, 9000, 12295):
+            d, t = draw(7, D, dtype, dtype, seed=6)
+            want = mesa.rmsnorm(t["x"], t["w"], residual=t["residual"])
+            x = t["x"].clone()
+            got = mesa.rmsnorm(x, t["w"], residual=t["residual"], out={"residual": x})
+            alone = mesa.rmsnorm(t["x"], t["w"], return_residual=True)
+            torch.cuda.synchronize()
+            assert got["residual"] is x and torch.equal(x, want["residual"]) and torch.equal(got["y"], want["y"])
+            assert torch.equal(alone["residual"], t["x"])
+
+
 @pytest.mark.parametrize("dtype,res", TYPES)
 @pytest.mark.parametrize("D", [2, 5, 9, 10, 11, 12, 13, 14, 15, 134, 518, 1001, 2051, 4109, 12006])
 def test_rows_that_end_within_a_vector(D, dtype, res):
