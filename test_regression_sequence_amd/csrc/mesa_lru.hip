@@ -16,17 +16,20 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 128 tokens a tile.  Shorter lanes make more tiles to join, 123 to 131 us (TW =
-// 12) and 120 to 127 (TW = 8) against 111 to 115 at B=1, T=32768, D=2048, bf16;
-// longer ones (TW = 24: 110 to 112) leave more of a tile empty at the end of a
-// sequence.  Workgroups of 8 waves were slower throughout.
-constexpr int kTw = 16, kNw = 4, kTile = 2 * kNw * kTw;
+// Tokens a lane, of a tile of 8 times as many.  128 tokens a tile: shorter lanes
+// make more tiles to join, 123 to 131 us (TW = 12) and 120 to 127 (TW = 8) against
+// 111 to 115 at B=1, T=32768, D=2048, bf16; longer ones (TW = 24: 110 to 112) leave
+// more of a tile empty at the end of a sequence.  Workgroups of 8 waves were slower
+// throughout.  Short sequences take the smallest of four tiles that holds one: 17,
+// 29 and 56 us with 8, 32 and 64 tokens against 73 to 79 with 128 at B=256, T=8, 32
+// and 64, D=2048, bf16.
+constexpr int kNw = 4, kTw = 16, kTile = 2 * kNw * kTw;
 static_assert(kNw >= 4, "three waves wait for other tiles, one folds this one's");
-static_assert(kTw % kLruChunk == 0, "kept states lie at a lane's first token");
 
-template <bool BF16, bool LINES>
+template <bool BF16, bool LINES, int TW>
 __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
-  constexpr int TW = kTw, NW = kNw, L = kTile;
+  constexpr int NW = kNw, L = 2 * NW * TW;
+  static_assert(TW % kLruChunk == 0 || kLruChunk % TW == 0, "kept states lie at a lane's first token");
   constexpr uint32_t ES = BF16 ? 2 : 4;
   __shared__ Pair waves[NW][kLruSlab], pre[NW][kLruSlab];
   __shared__ LruCarry carry;
@@ -132,7 +135,7 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
     h[e] = apply(carry.late[c2 + e], apply(carry.early[c2 + e], carry.h[c2 + e]));
     h[e] = apply(before[e], apply(pre[wave][c2 + e], h[e]));
   }
-  if (t0 < n)
+  if (t0 < n && t0 % kLruChunk == 0)
     store_raw2<false, LINES>(p.states, (((size_t)b * p.NC + t0 / kLruChunk) * p.D + ch) * 4, h, nch);
 #pragma unroll
   for (int s = 0; s < TW; ++s)
@@ -201,14 +204,22 @@ hipError_t launch_lru_ready(const LruParams& p, size_t words, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool BF16, bool LINES>
+template <bool BF16, bool LINES, int TW>
 static hipError_t launch_fwd_t(const LruParams& p, hipStream_t s) {
-  const LruGrid grid(p.B, p.T, p.D, kTile);
+  const LruGrid grid(p.B, p.T, p.D, 2 * kNw * TW);
   if (grid.tiles > 1) {
     if (const hipError_t e = launch_lru_ready(p, grid.chains * lru_chain_words(grid.tiles), s); e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((lru_fwd_kernel<BF16, LINES>), dim3(grid.workgroups()), dim3(64 * kNw), 0, s, p);
+  hipLaunchKernelGGL((lru_fwd_kernel<BF16, LINES, TW>), dim3(grid.workgroups()), dim3(64 * kNw), 0, s, p);
   return hipGetLastError();
+}
+
+template <bool BF16, bool LINES>
+static hipError_t launch_fwd_tw(const LruParams& p, hipStream_t s) {
+  if (p.T <= 2 * kNw) return launch_fwd_t<BF16, LINES, 1>(p, s);
+  if (p.T <= 8 * kNw) return launch_fwd_t<BF16, LINES, 4>(p, s);
+  if (p.T <= 16 * kNw) return launch_fwd_t<BF16, LINES, 8>(p, s);
+  return launch_fwd_t<BF16, LINES, kTw>(p, s);
 }
 
 size_t lru_fwd_word_bytes(int B, int T, int D) {
@@ -218,8 +229,8 @@ size_t lru_fwd_word_bytes(int B, int T, int D) {
 
 hipError_t launch_lru_fwd(bool bf16, const LruParams& p, hipStream_t s) {
   const bool lines = lru_whole_lines(bf16, {p.ld, p.D}, {p.x, p.ga, p.gi, p.y});
-  if (bf16) return lines ? launch_fwd_t<true, true>(p, s) : launch_fwd_t<true, false>(p, s);
-  return lines ? launch_fwd_t<false, true>(p, s) : launch_fwd_t<false, false>(p, s);
+  if (bf16) return lines ? launch_fwd_tw<true, true>(p, s) : launch_fwd_tw<true, false>(p, s);
+  return lines ? launch_fwd_tw<false, true>(p, s) : launch_fwd_tw<false, false>(p, s);
 }
 
 hipError_t launch_lru_step(bool bf16, const LruParams& p, hipStream_t s) {

@@ -25,13 +25,17 @@ constexpr int kThreads = 256;
 // workgroups fit a CU, with 12 elements 4, with 8 elements 5; 191, 195 and 208 us
 // at B=8, T=4096, D=2048, bf16, and 101 against 138 (12 elements, tiles of 48
 // tokens) at B=256, T=64.
-constexpr int kTw = kLruChunk / 2, kNw = 4, kTile = 2 * kNw * kTw;
+// A wave's tokens then start at a kept state.  Sequences of at most 8 or 32 tokens
+// take one tile of as many (kShort), and the state before a wave's tokens from the
+// waves before it: 26 and 54 us against 80 and 85 with 64 tokens at B=256, T=8 and
+// 32, D=2048, bf16.
+constexpr int kNw = 4, kTw = kLruChunk / 2, kTile = 2 * kNw * kTw;
 static_assert(kNw >= 4, "three waves wait for other tiles, one folds this one's");
-static_assert(2 * kTw == kLruChunk, "a wave's tokens start at a kept state");
 
-template <bool BF16, bool LINES>
+template <bool BF16, bool LINES, int TW>
 __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
-  constexpr int TW = kTw, NW = kNw, L = kTile;
+  constexpr int NW = kNw, L = 2 * NW * TW;
+  constexpr bool kShort = TW < kTw;
   constexpr uint32_t ES = BF16 ? 2 : 4;
   __shared__ Pair waves[NW][kLruSlab], pre[NW][kLruSlab];
   __shared__ LruCarry carry;
@@ -90,8 +94,8 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
     load_raw2<BF16, LINES>(static_cast<const char*>(p.gi) + in, off, gi);
     load_raw2<BF16, LINES>(static_cast<const char*>(p.x) + in, off, x);
     load_raw2<BF16, LINES>(static_cast<const char*>(p.dy) + first * p.D * ES, doff, dy);
-    Raw2<false> state[1];  // before this wave's tokens
-    const int chunk = min(j * L + wave * kLruChunk, n - 1) / kLruChunk;
+    Raw2<false> state[1];  // before this wave's tokens, or the sequence
+    const int chunk = kShort ? 0 : min(j * L + wave * kLruChunk, n - 1) / kLruChunk;
     const uint32_t none[1] = {0};
     load_raw2<false, LINES>(p.states + ((size_t)b * p.NC + chunk) * p.D + lc, none, state);
     to_own_channels(p.D, ch, x);
@@ -141,13 +145,28 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
     }
   }
   // the states before this lane's tokens, and with them v / g = va (k - h)
+  Pair earlier[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    Pair on{a[0][e], u[0][e]}, earlier, all;
+    Pair on{a[0][e], u[0][e]}, all;
 #pragma unroll
     for (int s = 1; s < TW; ++s) on = join(on, Pair{a[s][e], u[s][e]});
-    join_rows<false>(on, row, earlier, all);
-    h[e] = apply(earlier, h[e]);
+    join_rows<false>(on, row, earlier[e], all);
+    if (kShort && row == 0) pre[wave][c2 + e] = all;
+  }
+  if constexpr (kShort) {
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NW - 1; ++w)
+      if (w < wave) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) h[e] = apply(pre[w][c2 + e], h[e]);
+      }
+    // (pre is written again behind the next barrier)
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    h[e] = apply(earlier[e], h[e]);
 #pragma unroll
     for (int s = 0; s < TW; ++s) {
       va[s][e] *= k[s][e] - h[e];
@@ -253,17 +272,24 @@ __global__ __launch_bounds__(kThreads) void lru_dlam_kernel(const float* part, c
   }
 }
 
-template <bool BF16, bool LINES>
+template <bool BF16, bool LINES, int TW>
 hipError_t launch_t(const LruParams& p, hipStream_t s) {
-  const LruGrid grid(p.B, p.T, p.D, kTile);
+  const LruGrid grid(p.B, p.T, p.D, 2 * kNw * TW);
   if (grid.tiles > 1) {
     if (const hipError_t e = launch_lru_ready(p, grid.chains * lru_chain_words(grid.tiles), s); e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((lru_bwd_kernel<BF16, LINES>), dim3(grid.workgroups()), dim3(64 * kNw), 0, s, p);
+  hipLaunchKernelGGL((lru_bwd_kernel<BF16, LINES, TW>), dim3(grid.workgroups()), dim3(64 * kNw), 0, s, p);
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   hipLaunchKernelGGL(lru_dlam_kernel, dim3((p.D + 15) / 16), dim3(kThreads), 0, s, p.lam_part, p.lam, p.dlam,
                      p.T > 0 ? p.B * grid.tiles : 0, p.D);
   return hipGetLastError();
+}
+
+template <bool BF16, bool LINES>
+hipError_t launch_tw(const LruParams& p, hipStream_t s) {
+  if (p.T <= 2 * kNw) return launch_t<BF16, LINES, 1>(p, s);
+  if (p.T <= 8 * kNw) return launch_t<BF16, LINES, 4>(p, s);
+  return launch_t<BF16, LINES, kTw>(p, s);
 }
 
 }  // namespace
@@ -280,8 +306,8 @@ size_t lru_bwd_part_bytes(int B, int T, int D) {
 
 hipError_t launch_lru_bwd(bool bf16, const LruParams& p, hipStream_t s) {
   const bool lines = lru_whole_lines(bf16, {p.ld, p.D, p.ld_grad}, {p.x, p.ga, p.gi, p.dy, p.dx, p.dga, p.dgi});
-  if (bf16) return lines ? launch_t<true, true>(p, s) : launch_t<true, false>(p, s);
-  return lines ? launch_t<false, true>(p, s) : launch_t<false, false>(p, s);
+  if (bf16) return lines ? launch_tw<true, true>(p, s) : launch_tw<true, false>(p, s);
+  return lines ? launch_tw<false, true>(p, s) : launch_tw<false, false>(p, s);
 }
 
 }  // namespace mesa
