@@ -54,14 +54,13 @@ __device__ __forceinline__ Raw8<BF16> load_part8(const void* base, size_t elem, 
   if constexpr (BF16) {
     const uint16_t* q = static_cast<const uint16_t*>(base) + elem;
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    u32x4 w{};
     uint32_t pair = 0, last = 0;
     if (n > 0) {
       if (n & 4) r.v.lo = *reinterpret_cast<const u16x4_any*>(q);
       if (n & 2) pair = *reinterpret_cast<const u32_any*>(q + (n & 4));
       if (n & 1) last = q[n & 6];
     }
-    w = __builtin_bit_cast(u32x4, r.v);
+    u32x4 w = __builtin_bit_cast(u32x4, r.v);
     const uint32_t first = n & 2 ? pair : last, second = n & 2 ? last : 0;
     if (n > 0 && n & 4) {
       w[2] = first;

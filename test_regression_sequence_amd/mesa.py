@@ -598,7 +598,8 @@ def decode_step_ex(q, k, v, gamma, beta, lam, h_state, g_state, *, x_state=None,
 # Every tensor of a call has to be on one device, the first argument's, and a
 # given stream too; the call is launched there whatever device is current.  What
 # a call allocates belongs to the stream it runs on, so that its memory is given
-# on in that stream's order.
+# on in that stream's order.  Tensors passed as `out` may not overlap inputs but
+# where a call says so.
 
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
@@ -703,14 +704,14 @@ def lru_workspace_bytes(B, T, D, *, dtype=torch.bfloat16) -> int:
 def lru_fwd(x, ga, gi, lam, *, c: float = 8.0, h0=None, lengths=None, return_state: bool = False, out=None,
             workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
     """Gated linear recurrence over whole sequences; x, ga, gi [B, T, D] (fp32 or
-    bf16): dense, or equal slices of one wider row-major tensor.
+    bf16, D >= 2): dense, or equal slices of one wider row-major tensor.
 
     a_t = exp(-c softplus(lam) sigmoid(ga_t)), h_t = a_t h_{t-1} +
     sqrt(1 - a_t^2) sigmoid(gi_t) x_t.  lam [D] fp32; h0 [B, D] fp32 or None;
     lengths [B] int32 or None (valid tokens; outputs behind them are zeros).
     Returns a dict with ``y`` [B, T, D] in x's dtype and, with return_state,
-    ``h_final`` [B, D] fp32.  ``workspace`` (lru_workspace_bytes long) keeps the
-    states that ``lru_bwd`` can take over."""
+    ``h_final`` [B, D] fp32 (out["h_final"] may be h0 itself).  ``workspace``
+    (lru_workspace_bytes long) keeps the states that ``lru_bwd`` can take over."""
     dev, dt, f32 = _home(x, "x", 3, stream), x.dtype, torch.float32
     shape = x.shape
     B, T, D = shape
@@ -733,7 +734,7 @@ def lru_bwd(x, ga, gi, lam, dy, *, c: float = 8.0, h0=None, lengths=None, d_hfin
     """Gradients of lru_fwd: dy [B, T, D] in x's dtype, d_hfinal [B, D] fp32 or None.
     Returns ``dx``, ``dga``, ``dgi`` in x's dtype, ``dlam`` [D] fp32 and, with
     state_grads, ``dh0`` [B, D] fp32.  ``out`` may hold dx, dga and dgi as equal
-    slices of one wider tensor.  states_in_workspace: the forward ran with
+    slices of one wider tensor, and d_hfinal itself as dh0.  states_in_workspace: the forward ran with
     ``workspace`` and left its states there, so they are not formed again."""
     if states_in_workspace and workspace is None:
         raise MesaError("states_in_workspace needs the forward's workspace")
