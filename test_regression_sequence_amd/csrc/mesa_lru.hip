@@ -126,9 +126,7 @@ __global__ __launch_bounds__(256, 4) void lru_fwd_kernel(LruParams p) {
     carry_tiles(words, j, wave - 2, lane, wave == 2 ? carry.early : carry.late);
   }
   __syncthreads();
-  if (wave == 0 && j % kLruGroup == kLruGroup - 1)
-    publish(words + (size_t)(tiles + j / kLruGroup) * kLruSlab + lane,
-            join(join(carry.early[lane], carry.late[lane]), tile));
+  if (wave == 0 && j % kLruGroup == kLruGroup - 1) publish_group(words, tiles, j, lane, carry, tile);
   float h[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {

@@ -204,9 +204,7 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
     carry_tiles(words, i, wave - 2, lane, wave == 2 ? carry.early : carry.late);
   }
   __syncthreads();
-  if (wave == 0 && i % kLruGroup == kLruGroup - 1)
-    publish(words + (size_t)(tiles + i / kLruGroup) * kLruSlab + lane,
-            join(join(carry.early[lane], carry.late[lane]), tile));
+  if (wave == 0 && i % kLruGroup == kLruGroup - 1) publish_group(words, tiles, i, lane, carry, tile);
 
 #pragma unroll
   for (int s = 0; s < TW; ++s) repack(dy[s]);

@@ -168,6 +168,7 @@ SIZES = [  # B, T, D, ragged
     (3, 47, 65, True), (2, 48, 66, False), (2, 49, 127, False), (1, 95, 130, False), (3, 96, 64, True), (2, 97, 2, False),
     (7, 2, 100, True), (5, 7, 64, True), (9, 8, 130, True), (3, 9, 65, False), (5, 15, 192, True), (3, 16, 33, False),
     (4, 17, 128, True), (3, 31, 66, True), (2, 32, 1001, True), (3, 33, 64, True), (20, 5, 2048, True), (6, 30, 257, True),
+    (1, 16384, 5, False), (1, 16385, 66, False), (2, 32769, 6, True), (1, 40000, 3, False), (1, 70001, 2, False),
     (1, 1023, 63, False), (2, 1025, 129, True), (1, 2048, 64, False), (3, 2049, 70, True),
     (1, 767, 63, False), (2, 769, 129, True), (1, 1535, 64, False), (3, 1537, 70, True), (40, 100, 200, True),
 ]
