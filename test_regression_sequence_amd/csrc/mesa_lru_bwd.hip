@@ -128,8 +128,9 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  // behind n the state and the adjoint pass, and every gradient is 0 (the rest is
-  // finite there: it comes from row n - 1)
+  // behind n the state and the adjoint pass; what else is formed there comes from row
+  // n - 1, which may hold infinities and NaN, so gradients are selected where they are
+  // stored and summed
   if (!whole) {
 #pragma unroll
     for (int s = 0; s < TW; ++s) {
@@ -139,8 +140,6 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
       for (int e = 0; e < 2; ++e) {
         a[s][e] = __builtin_unpredictable(off) ? 1.f : a[s][e];
         u[s][e] = __builtin_unpredictable(off) ? 0.f : u[s][e];
-        dxg[s][e] = __builtin_unpredictable(off) ? 0.f : dxg[s][e];
-        va[s][e] = __builtin_unpredictable(off) ? 0.f : va[s][e];
       }
     }
   }
@@ -214,15 +213,15 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
     c[e] = apply(carry.late[c2 + e], apply(carry.early[c2 + e], carry.h[c2 + e]));
     c[e] = apply(before[e], apply(pre[wave][c2 + e], c[e]));
   }
-  auto token = [&](int s, int valid) {
+  auto token = [&](int s, int valid, bool live) {
     float dx[2], dga[2], dgi[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float g = c[e] + dy[s].at(e), v = g * va[s][e];
+      const float g = c[e] + dy[s].at(e), v = live ? g * va[s][e] : 0.f;
       vsum[e] += v;
-      dx[e] = g * dxg[s][e];
-      dgi[e] = dx[e] * q[s][e];
-      dga[e] = v * sr1[s][e];
+      dx[e] = live ? g * dxg[s][e] : 0.f;
+      dgi[e] = live ? dx[e] * q[s][e] : 0.f;
+      dga[e] = live ? v * sr1[s][e] : 0.f;
       c[e] = a[s][e] * g;
     }
     store_raw2<BF16, LINES>(static_cast<char*>(p.dx) + grad, goff + s * grow, dx, valid);
@@ -231,10 +230,10 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
   };
   if (whole && nch >= 2) {
 #pragma unroll
-    for (int s = TW - 1; s >= 0; --s) token(s, 2);
+    for (int s = TW - 1; s >= 0; --s) token(s, 2, true);
   } else {
 #pragma unroll
-    for (int s = TW - 1; s >= 0; --s) token(s, t0 + s < p.T ? nch : 0);
+    for (int s = TW - 1; s >= 0; --s) token(s, t0 + s < p.T ? nch : 0, t0 + s < n);
   }
   if (p.dh0 && t0 == 0) store_raw2<false, LINES>(p.dh0, ((size_t)b * p.D + ch) * 4, c, nch);
 #pragma unroll

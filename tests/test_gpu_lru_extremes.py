@@ -1,0 +1,70 @@
+"""The gated linear recurrence where values leave the ordinary range: infinities and NaN
+in valid rows, parameters and states, against what the definition gives.  Needs an MI355X.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle.block_oracle import lru_backward, lru_forward, lru_step
+from test_regression_sequence_amd import mesa
+
+pytestmark = pytest.mark.gpu
+
+E = 2.0 ** -24
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    mesa.lib()
+
+
+def draw(B, T, D, dtype=torch.float32, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    d = {k: torch.randn(B, T, D, generator=gen).to(dtype) for k in ("x", "ga", "gi", "dy")}
+    d["lam"] = torch.rand(D, generator=gen) * 6 - 9
+    d["h0"], d["d_hfinal"] = torch.randn(B, D, generator=gen), torch.randn(B, D, generator=gen)
+    return d
+
+
+def run(d, lengths=None, c=8.0):
+    t = {k: v.cuda() for k, v in d.items()}
+    if lengths is not None:
+        lengths = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    args, kw = (t["x"], t["ga"], t["gi"], t["lam"]), dict(c=c, h0=t["h0"], lengths=lengths)
+    r = mesa.lru_fwd(*args, return_state=True, **kw)
+    r.update(mesa.lru_bwd(*args, t["dy"], d_hfinal=t["d_hfinal"], state_grads=True, **kw))
+    torch.cuda.synchronize()
+    return {k: v.cpu() for k, v in r.items()}
+
+
+# one tile of 8 tokens, of 32, of 64 (backward), of 128 (forward 64), and several tiles
+TILES = [(7, 5), (20, 13), (50, 41), (90, 70), (700, 451)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,n", TILES)
+def test_rows_behind_a_length_are_zeros_whatever_the_valid_ones_hold(T, n, dtype):
+    """Infinities and NaN in the last valid row, in an earlier one, in the initial state and in the
+    final state's gradient: rows behind the length are zeros, other channels and sequences have
+    the bits of a call without them."""
+    B, D, hit = 3, 70, 37
+    lengths = [T, n, n - 1]
+    clean = run(draw(B, T, D, dtype), lengths)
+    for key, at, bad in [(k, t, v) for k in ("x", "ga", "gi", "dy") for t in (n - 1, 1) for v in (NAN, INF, -INF)] + \
+                        [(k, None, v) for k in ("h0", "d_hfinal") for v in (NAN, INF)]:
+        d = draw(B, T, D, dtype)
+        if at is None:
+            d[key][1, hit] = bad
+        else:
+            d[key][1, at, hit] = bad
+        r = run(d, lengths)
+        for name in ("y", "dx", "dga", "dgi"):
+            for b, m in enumerate(lengths):
+                assert (r[name][b, m:] == 0).all(), (key, at, bad, name, b)
+        for name in r:
+            keep = torch.ones_like(r[name], dtype=torch.bool)
+            keep[(hit,) if name == "dlam" else (1, Ellipsis, hit)] = False
+            assert torch.equal(r[name][keep], clean[name][keep]), (key, at, bad, name)
