@@ -34,8 +34,12 @@ __device__ __forceinline__ float lru_softplus(float z) {
 }
 
 // c log2(e) softplus(lam): a channel's decay in halvings per token with its gate
-// open; finite, so that a closed gate or a decay of 0 leaves no 0 * inf.
-__device__ __forceinline__ float lru_rate(float lam, float c) { return fminf(kLog2e * c * lru_softplus(lam), 0x1p126f); }
+// open; finite, so that a closed gate or a decay of 0 leaves no 0 * inf.  (c is
+// multiplied last: with log2(e) it may pass the largest float, and times a
+// softplus of 0 that would be NaN.)
+__device__ __forceinline__ float lru_rate(float lam, float c) {
+  return fminf(c * (kLog2e * lru_softplus(lam)), 0x1p126f);
+}
 
 // sigmoid(lam) / softplus(lam), the factor from dL/d log t to dL/dlam.  Below
 // lam = -15 both are exp(lam) to within exp(-15) = 3e-7 of themselves, and

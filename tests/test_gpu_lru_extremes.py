@@ -68,3 +68,21 @@ def test_rows_behind_a_length_are_zeros_whatever_the_valid_ones_hold(T, n, dtype
             keep = torch.ones_like(r[name], dtype=torch.bool)
             keep[(hit,) if name == "dlam" else (1, Ellipsis, hit)] = False
             assert torch.equal(r[name][keep], clean[name][keep]), (key, at, bad, name)
+
+
+@pytest.mark.parametrize("c", [2.5e38, float(np.finfo(np.float32).max)])
+def test_largest_decay_scales(c):
+    """c up to the largest float: where softplus(lam) is 0 in fp32 the state stays, elsewhere every token starts
+    anew, y = sigmoid(gi) x; nothing is NaN."""
+    d = draw(2, 200, 5, seed=1)
+    d["lam"] = torch.tensor([-INF, -1e30, -200.0, 2.0, INF])
+    r = run(d, c=c)
+    assert all(torch.isfinite(v).all() for v in r.values())
+    assert torch.equal(r["y"][..., :3], d["h0"][:, None, :3].expand(-1, 200, -1))
+    assert torch.equal(r["h_final"][:, :3], d["h0"][:, :3])
+    assert not any(r[k][..., :3].any() for k in ("dx", "dga", "dgi"))
+    want = torch.sigmoid(d["gi"].double()) * d["x"].double()
+    assert ((r["y"].double() - want)[..., 3:].abs() <= 16 * E * want[..., 3:].abs()).all()
+    h = d["h0"].cuda()
+    y = mesa.lru_step(*(d[k][:, 0].contiguous().cuda() for k in ("x", "ga", "gi")), d["lam"].cuda(), h, c=c)["y"].cpu()
+    assert torch.equal(y[:, :3], d["h0"][:, :3]) and ((y.double() - want[:, 0])[:, 3:].abs() <= 16 * E * want[:, 0, 3:].abs()).all()
