@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
   const bool whole = (j + 1) * L <= n;
 
   Raw2<BF16> dy[TW];
-  float a[TW][2], u[TW][2], dxg[TW][2], q[TW][2], va[TW][2], k[TW][2], sr1[TW][2], h[2];
+  float a[TW][2], u[TW][2], dxg[TW][2], q[TW][2], va[TW][2], vu[TW][2], sr1[TW][2], h[2];
   {
     Raw2<BF16> x[TW], ga[TW], gi[TW];
     uint32_t off[TW], doff[TW];
@@ -116,13 +116,13 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
         dxg[s][e] = r.dx_g;
         q[s][e] = r.q;
         va[s][e] = r.va;
-        k[s][e] = r.k;
+        vu[s][e] = r.vu;
         sr1[s][e] = r.sr1;
         settle(dxg[s][e]);
         settle(u[s][e]);
         settle(q[s][e]);
         settle(va[s][e]);
-        settle(k[s][e]);
+        settle(vu[s][e]);
         settle(sr1[s][e]);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
       }
     }
   }
-  // the states before this lane's tokens, and with them v / g = va (k - h)
+  // the states before this lane's tokens, and with them v / g = vu - va h
   Pair earlier[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -168,8 +168,8 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
     h[e] = apply(earlier[e], h[e]);
 #pragma unroll
     for (int s = 0; s < TW; ++s) {
-      va[s][e] *= k[s][e] - h[e];
-      settle(va[s][e]);
+      vu[s][e] = __builtin_fmaf(-va[s][e], h[e], vu[s][e]);
+      settle(vu[s][e]);
       h[e] = __builtin_fmaf(a[s][e], h[e], u[s][e]);
     }
   }
@@ -217,7 +217,7 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
     float dx[2], dga[2], dgi[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float g = c[e] + dy[s].at(e), v = live ? g * va[s][e] : 0.f;
+      const float g = c[e] + dy[s].at(e), v = live ? g * vu[s][e] : 0.f;
       vsum[e] += v;
       dx[e] = live ? g * dxg[s][e] : 0.f;
       dgi[e] = live ? dx[e] * q[s][e] : 0.f;

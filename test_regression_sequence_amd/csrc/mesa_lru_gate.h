@@ -79,10 +79,10 @@ __device__ __forceinline__ void lru_cell(float x, float ga, float gi, float rate
 
 // The same with what the gradients need.  With g the adjoint of h_t and h1 the
 // state before the token:
-//     dx = g dx_g,  dgi = dx q,  v = g va (k - h1),  dga = v sr1,
-// q = x (1 - s_i), va = ln2 t a, k = (a / m) s_i x, v = dL / d log t.
+//     dx = g dx_g,  dgi = dx q,  v = g (vu - va h1),  dga = v sr1,
+// q = x (1 - s_i), va = ln2 t a, vu = va (a / m) s_i x, v = dL / d log t.
 struct LruGrad {
-  float a, u, dx_g, q, va, k, sr1;
+  float a, u, dx_g, q, va, vu, sr1;
 };
 
 // 1 - sigmoid comes as exp(-z) sigmoid(z), which keeps its bits for large z.
@@ -90,6 +90,8 @@ struct LruGrad {
 // [0, 1], which makes it 0 (there t, and with it v, is 0 anyway); for gi, where
 // q has no such range, the exponent is capped at 126 instead.  1/m is formed of
 // 1 - a^2 raised to the smallest normal float: where a = 1, m is 0 and 1/m finite.
+// It is up to 2^63, so vu takes it with va (t / m is of the order of m): times
+// s_i x it could pass the largest float where vu is small or 0.
 __device__ __forceinline__ LruGrad lru_cell_grad(float x, float ga, float gi, float rate) {
   LruGrad r;
   const float er = __builtin_amdgcn_exp2f(-kLog2e * ga);
@@ -104,7 +106,7 @@ __device__ __forceinline__ LruGrad lru_cell_grad(float x, float ga, float gi, fl
   r.u = m * six;
   r.q = ei * six;
   r.va = kLn2 * t * r.a;
-  r.k = r.a * rm * six;
+  r.vu = r.va * rm * (r.a * six);
   return r;
 }
 

@@ -86,3 +86,40 @@ def test_largest_decay_scales(c):
     h = d["h0"].cuda()
     y = mesa.lru_step(*(d[k][:, 0].contiguous().cuda() for k in ("x", "ga", "gi")), d["lam"].cuda(), h, c=c)["y"].cpu()
     assert torch.equal(y[:, :3], d["h0"][:, :3]) and ((y.double() - want[:, 0])[:, 3:].abs() <= 16 * E * want[:, 0, 3:].abs()).all()
+
+
+@pytest.mark.parametrize("T", [7, 20, 300])
+def test_large_inputs_behind_closed_gates(T):
+    """A gate closed in fp32 (a = 1) lets nothing in, whatever x holds: no gradient reaches x, ga, gi or lam through
+    it.  One that is barely open (t = -log2(a) of 1e-37 .. 1e-30) has sigmoid(gi) x / m far beyond fp32 but a finite
+    v = -log(a) (a^2 / m) sigmoid(gi) x g.
+
+    The bound: -log(a) = ln2 t carries (2 |ga| + 16) e of sigmoid, rate and product, m half as much, the products
+    below 16 e together; the state is left out of v (h0 = 0 and inputs of at most m x)."""
+    B, D = 2, 8
+    d = draw(B, T, D, seed=2)
+    d["h0"].zero_()
+    big = torch.tensor([1e20, -3e38, 1e30, 3e25])[torch.arange(T) % 4][None, :, None]
+    d["x"] = big.expand(B, T, D).clone()
+    d["ga"][..., :2] = -200.0
+    d["ga"][..., 2:4] = -INF
+    r = run(d)
+    for k in ("y", "dx", "dga", "dgi"):
+        assert not r[k][..., :4].any(), k
+    assert not r["dlam"][:4].any() and not r["h_final"][:, :4].any()
+
+    d = draw(B, T, D, seed=3)
+    d["h0"].zero_()
+    d["d_hfinal"].zero_()
+    d["lam"] = torch.full((D,), -6.0)
+    d["x"] = torch.full((B, T, D), 4e22)
+    d["ga"] = -torch.linspace(66, 80, D).expand(B, T, D).clone()
+    r = run(d)
+    n = {k: v.numpy() for k, v in d.items()}
+    ref = lru_backward(*(n[k] for k in ("x", "ga", "gi", "lam", "dy")), c=8.0, h0=n["h0"], d_hfinal=n["d_hfinal"])
+    # the sum of dy up to the token's own carries T e of its magnitudes
+    size = lru_backward(*(n[k] for k in ("x", "ga", "gi", "lam")), np.abs(n["dy"]), c=8.0, h0=n["h0"], d_hfinal=n["d_hfinal"])
+    assert np.isfinite(ref["dga"]).all() and np.abs(ref["dga"]).max() > 1
+    for k in ("dx", "dga", "dgi"):
+        tol = (1.5 * (2 * 80 + 16) + 16 + 2 * T) * E * np.abs(size[k]) + 1e-30
+        assert (np.abs(r[k].numpy() - ref[k]) <= tol).all(), k
