@@ -17,7 +17,8 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 // expf and log1pf (every lane forms it for its channels).  e: the product
 // |z| log2(e) is taken in two floats, its rounding error enters to first order.
 // log(1 + e) = 2 artanh(q) = 2 (q + q^3/3 + q^5/5 + ..), q = e / (2 + e) <= 1/3:
-// the first term left out, q^15/15, is below 2e-8 of the sum.
+// the first term left out, q^15/15, is below 2e-8 of the sum.  (fminf and fmaxf
+// return the other operand of a NaN; the last term is a selection that keeps it.)
 __device__ __forceinline__ float lru_softplus(float z) {
   const float y = fmaxf(-fabsf(z), -150.f), hi = y * kLog2e;  // (exp(-150) is 0 here; an infinite y would give NaN)
   const float lo = __builtin_fmaf(y, 1.92596303e-8f, __builtin_fmaf(y, kLog2e, -hi));  // log2(e) - kLog2e = 1.926e-8
@@ -30,7 +31,7 @@ __device__ __forceinline__ float lru_softplus(float z) {
   p = __builtin_fmaf(q2, p, 1.f / 5.f);
   p = __builtin_fmaf(q2, p, 1.f / 3.f);
   p = __builtin_fmaf(q2, p, 1.f);
-  return __builtin_fmaf(2.f * q, p, fmaxf(z, 0.f));
+  return __builtin_fmaf(2.f * q, p, z < 0.f ? 0.f : z);
 }
 
 // c log2(e) softplus(lam): a channel's decay in halvings per token with its gate
@@ -38,7 +39,8 @@ __device__ __forceinline__ float lru_softplus(float z) {
 // multiplied last: with log2(e) it may pass the largest float, and times a
 // softplus of 0 that would be NaN.)
 __device__ __forceinline__ float lru_rate(float lam, float c) {
-  return fminf(c * (kLog2e * lru_softplus(lam)), 0x1p126f);
+  const float rate = c * (kLog2e * lru_softplus(lam));
+  return rate > 0x1p126f ? 0x1p126f : rate;  // (a NaN stays one)
 }
 
 // sigmoid(lam) / softplus(lam), the factor from dL/d log t to dL/dlam.  Below
@@ -88,14 +90,15 @@ struct LruGrad {
 // 1 - sigmoid comes as exp(-z) sigmoid(z), which keeps its bits for large z.
 // Where exp(-z) overflows that is inf * 0: for ga the product is clamped to
 // [0, 1], which makes it 0 (there t, and with it v, is 0 anyway); for gi, where
-// q has no such range, the exponent is capped at 126 instead.  1/m is formed of
+// q has no such range, the factor exp(-z) is capped at 2^126 instead (behind the
+// sigmoid, which keeps a NaN that the cap would lose; dx is 0 there).  1/m is formed of
 // 1 - a^2 raised to the smallest normal float: where a = 1, m is 0 and 1/m finite.
 // It is up to 2^63, so vu takes it with va (t / m is of the order of m): times
 // s_i x it could pass the largest float where vu is small or 0.
 __device__ __forceinline__ LruGrad lru_cell_grad(float x, float ga, float gi, float rate) {
   LruGrad r;
   const float er = __builtin_amdgcn_exp2f(-kLog2e * ga);
-  const float ei = __builtin_amdgcn_exp2f(fminf(-kLog2e * gi, 126.f));
+  const float ei = __builtin_amdgcn_exp2f(-kLog2e * gi);
   const float sr = __builtin_amdgcn_rcpf(1.f + er), si = __builtin_amdgcn_rcpf(1.f + ei);
   const float t = rate * sr;
   r.a = __builtin_amdgcn_exp2f(-t);
@@ -104,7 +107,7 @@ __device__ __forceinline__ LruGrad lru_cell_grad(float x, float ga, float gi, fl
   r.sr1 = __builtin_amdgcn_fmed3f(er * sr, 0.f, 1.f);
   r.dx_g = m * si;
   r.u = m * six;
-  r.q = ei * six;
+  r.q = fminf(ei, 0x1p126f) * six;
   r.va = kLn2 * t * r.a;
   r.vu = r.va * rm * (r.a * six);
   return r;

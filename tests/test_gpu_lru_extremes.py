@@ -123,3 +123,48 @@ def test_large_inputs_behind_closed_gates(T):
     for k in ("dx", "dga", "dgi"):
         tol = (1.5 * (2 * 80 + 16) + 16 + 2 * T) * E * np.abs(size[k]) + 1e-30
         assert (np.abs(r[k].numpy() - ref[k]) <= tol).all(), k
+
+
+def masks(r, ref, clean, hit):
+    """NaN where the definition has it and nowhere else; other channels keep their bits."""
+    for name in r:
+        assert np.array_equal(np.isnan(r[name].float().numpy()), np.isnan(ref[name])), name
+        keep = torch.ones_like(r[name], dtype=torch.bool)
+        keep[..., hit] = False
+        assert torch.equal(r[name][keep], clean[name][keep]), name
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,n", TILES)
+def test_nan_reaches_what_depends_on_it(T, n, dtype):
+    """A NaN in lam, in an element of x, ga, gi or dy, or in a state: forward and backward give NaN exactly where
+    the definition does."""
+    B, D, hit = 2, 66, 65
+    lengths = [n, T]
+    clean = run(draw(B, T, D, dtype), lengths)
+    for key, at in [("lam", (hit,)), ("h0", (0, hit)), ("d_hfinal", (0, hit))] + \
+                   [(k, (0, t, hit)) for k in ("x", "ga", "gi", "dy") for t in (0, n // 2, n - 1)]:
+        d = draw(B, T, D, dtype)
+        d[key][at] = NAN
+        r = run(d, lengths)
+        a = {k: v.float().numpy() for k, v in d.items()}
+        args, kw = [a[k] for k in ("x", "ga", "gi", "lam")], dict(c=8.0, h0=a["h0"], lengths=lengths)
+        with np.errstate(invalid="ignore"):
+            ref = lru_forward(*args, **kw)
+            ref.update(lru_backward(*args, a["dy"], d_hfinal=a["d_hfinal"], **kw))
+        assert any(np.isnan(ref[k]).any() for k in r), key
+        masks(r, ref, clean, hit)
+
+
+@pytest.mark.parametrize("key", ["lam", "x", "ga", "gi", "h0"])
+def test_nan_in_a_step(key):
+    N, D, hit = 3, 66, 9
+    d = draw(N, 1, D, seed=4)
+    v = d[key]
+    v[(hit,) if key == "lam" else (1, hit) if key == "h0" else (1, 0, hit)] = NAN
+    h = d["h0"].cuda()
+    y = mesa.lru_step(*(d[k][:, 0].contiguous().cuda() for k in ("x", "ga", "gi")), d["lam"].cuda(), h)["y"].cpu()
+    with np.errstate(invalid="ignore"):
+        ref = lru_step(*(d[k][:, 0].numpy() for k in ("x", "ga", "gi")), d["lam"].numpy(), d["h0"].numpy())
+    assert np.isnan(ref).any()
+    assert np.array_equal(np.isnan(y.numpy()), np.isnan(ref)) and np.array_equal(np.isnan(h.cpu().numpy()), np.isnan(ref))
