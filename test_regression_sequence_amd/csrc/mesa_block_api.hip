@@ -100,9 +100,10 @@ mesa_status mesa_lru_fwd(const mesa_lru_desc* d, const void* x, const void* ga, 
   const size_t need = mesa_lru_workspace_bytes(d);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MESA_ERR_WORKSPACE;
   const size_t rows = lru_rows_bytes(d, d->ld), per_channel = (size_t)d->D * 4, state = d->B * per_channel;
-  if (overlap({{y, lru_rows_bytes(d, d->D)}, {h_final, state}, {workspace, need}},
-              {{x, rows}, {ga, rows}, {gi, rows}, {lam, per_channel}, {h0 == h_final ? nullptr : h0, state},
-               {lengths, (size_t)d->B * 4}}))
+  const Span ins[] = {{x, rows}, {ga, rows}, {gi, rows}, {lam, per_channel}, {lengths, (size_t)d->B * 4}};
+  const Span outs[] = {{y, lru_rows_bytes(d, d->D)}, {workspace, need}, {h_final, state}}, start{h0, state};
+  // h_final may be h0, and nothing else may lie over h0
+  if (overlap(outs, ins) || overlap({outs[0], outs[1]}, {start}) || (h_final != h0 && overlap({outs[2]}, {start})))
     return MESA_ERR_INVALID_ARG;
   mesa::LruParams p = lru_params(d, x, ga, gi, lam, h0, lengths, workspace);
   p.y = y; p.h_final = h_final;
@@ -125,9 +126,13 @@ mesa_status mesa_lru_bwd(const mesa_lru_desc* d, const void* x, const void* ga, 
   const bool bf16 = d->dtype == MESA_BF16;
   const size_t rows = lru_rows_bytes(d, d->ld), grads = lru_rows_bytes(d, ld_grad);
   const size_t per_channel = (size_t)d->D * 4, state = d->B * per_channel;
-  if (overlap({{dx, grads}, {dga, grads}, {dgi, grads}, {dlam, per_channel}, {dh0, state}, {workspace, need}},
-              {{x, rows}, {ga, rows}, {gi, rows}, {lam, per_channel}, {h0, state}, {lengths, (size_t)d->B * 4},
-               {dy, lru_rows_bytes(d, d->D)}, {d_hfinal == dh0 ? nullptr : d_hfinal, state}}))
+  const Span ins[] = {{x, rows}, {ga, rows}, {gi, rows}, {lam, per_channel}, {h0, state}, {lengths, (size_t)d->B * 4},
+                      {dy, lru_rows_bytes(d, d->D)}};
+  const Span outs[] = {{dx, grads}, {dga, grads}, {dgi, grads}, {dlam, per_channel}, {workspace, need}, {dh0, state}};
+  const Span last{d_hfinal, state};
+  // dh0 may be d_hfinal, and nothing else may lie over d_hfinal
+  if (overlap(outs, ins) || overlap({outs[0], outs[1], outs[2], outs[3], outs[4]}, {last}) ||
+      (dh0 != d_hfinal && overlap({outs[5]}, {last})))
     return MESA_ERR_INVALID_ARG;
   mesa::LruParams p = lru_params(d, x, ga, gi, lam, h0, lengths, workspace);
   if (d->T > 0 && !states_in_workspace && mesa::launch_lru_fwd(bf16, p, stream) != hipSuccess) return MESA_ERR_HIP;
@@ -215,8 +220,11 @@ mesa_status mesa_rmsnorm_bwd(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype 
   if (need > 0 && (!workspace || workspace_bytes < need)) return MESA_ERR_WORKSPACE;
   const size_t n = (size_t)R * D, rows = n * dtype_bytes(dtype), stream_rows = n * dtype_bytes(res_dtype);
   const size_t weights = (size_t)D * 4;
-  if (overlap({{ds, stream_rows}, {dx, rows}, {dw, weights}, {workspace, need}},
-              {{s, stream_rows}, {w, weights}, {dy, rows}, {d_residual == ds ? nullptr : d_residual, stream_rows}}))
+  const Span ins[] = {{s, stream_rows}, {w, weights}, {dy, rows}};
+  const Span outs[] = {{dx, rows}, {dw, weights}, {workspace, need}, {ds, stream_rows}}, along{d_residual, stream_rows};
+  // ds may be d_residual, and nothing else may lie over d_residual
+  if (overlap(outs, ins) || overlap({outs[0], outs[1], outs[2]}, {along}) ||
+      (ds != d_residual && overlap({outs[3]}, {along})))
     return MESA_ERR_INVALID_ARG;
   mesa::NormParams p{};
   p.x = s; p.residual = d_residual; p.w = w; p.dy = dy; p.y = ds; p.residual_out = dx; p.dw = dw; p.part = workspace;
