@@ -41,7 +41,8 @@
  *     beta >= 0, lambda > 0, finite inputs, symmetric h0 / h_state.
  *   - An output buffer may not overlap another output or an input, except
  *     where a call updates a state in place (the decode steps) or says
- *     otherwise.  Only the preprocessing calls check this.
+ *     otherwise.  Only the preprocessing calls and those of the recurrence and
+ *     the norm check this (MESA_ERR_INVALID_ARG).
  *   - Tensors are dense and row-major with the last index fastest.  States are
  *     [.., dk, dk] for H and [.., dv, dk] for G (row = value dimension).
  *   - Supported sizes: dk == dv; dk in {16, 32, 64, 128} for MESA_F32 inputs
@@ -513,8 +514,10 @@ mesa_status mesa_qk_preprocess(int32_t B, int32_t H, int32_t T, int32_t d, int32
  * fixed order: equal inputs give bitwise equal results.
  * Supported: 2 <= D <= ld <= 2^20, T >= 0, B >= 1 with B max(ceil(T/64), 1)
  * ceil(D/64) <= 2^23; c > 0, finite (else MESA_ERR_INVALID_ARG).
- * Outputs and workspace may not overlap inputs but as said (MESA_ERR_INVALID_ARG):
- * h_final may be h0, dh0 may be d_hfinal.  Two calls may not use one workspace at
+ * Outputs and workspace may not overlap inputs or one another but as said
+ * (MESA_ERR_INVALID_ARG): h_final may be h0, dh0 may be d_hfinal.  Rows at one
+ * token stride (x, ga, gi, dx, dga, dgi in one wider tensor) may interleave;
+ * each of these still starts at a multiple of 16 bytes.  Two calls may not use one workspace at
  * the same time. */
 typedef struct {
   int32_t B, T, D;   /* sequences, tokens per (padded) sequence, channels             */
@@ -588,7 +591,7 @@ mesa_status mesa_lru_step(int32_t N, int32_t D, int32_t ld, float c, mesa_dtype 
  * res_dtype.  Rounding is to nearest even, y / scale being formed as
  * y * (448 / max|y|).  Rows are independent; a row whose squares overflow fp32
  * (or that holds infinities or NaN) gives unspecified values in that row.
- * Other outputs may not overlap inputs or residual_out (MESA_ERR_INVALID_ARG).
+ * Other outputs may not overlap inputs, residual_out or one another (MESA_ERR_INVALID_ARG).
  * Supported: 1 <= D <= 16384, 0 <= R <= 2^30, R D <= 2^40, (dtype, res_dtype) of (f32,
  * f32), (bf16, bf16), (bf16, f32). */
 typedef enum { MESA_NORM_OUT_DTYPE = 0, MESA_NORM_OUT_E4M3 = 1 } mesa_norm_out;
@@ -613,7 +616,7 @@ mesa_status mesa_rmsnorm(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_
  *   dw         [D] fp32 out, summed in a fixed order
  *   workspace  mesa_rmsnorm_bwd_workspace_bytes(R, D) bytes
  * Sizes and types as in mesa_rmsnorm.  Outputs and workspace may not overlap
- * inputs but as said (MESA_ERR_INVALID_ARG). */
+ * inputs or one another but as said (MESA_ERR_INVALID_ARG). */
 size_t mesa_rmsnorm_bwd_workspace_bytes(int32_t R, int32_t D);
 
 mesa_status mesa_rmsnorm_bwd(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_dtype,
@@ -642,7 +645,7 @@ mesa_status mesa_rmsnorm_bwd(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype 
  *   dq_hist, dk_hist [B, H, window-1, d] dtype out or NULL
  *   workspace        mesa_qk_preprocess_bwd_workspace_bytes(...) bytes
  * Sizes as in mesa_qk_preprocess, B >= 1, T <= 2^30.  Outputs and workspace
- * may not overlap the inputs (MESA_ERR_INVALID_ARG). */
+ * may not overlap the inputs or one another (MESA_ERR_INVALID_ARG). */
 size_t mesa_qk_preprocess_bwd_workspace_bytes(int32_t B, int32_t H, int32_t T, int32_t d,
                                               int32_t window, mesa_dtype dtype);
 

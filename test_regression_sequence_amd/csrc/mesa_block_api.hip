@@ -22,19 +22,42 @@ bool dtype_ok(mesa_dtype t) { return t == MESA_F32 || t == MESA_BF16; }
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
+// `rows` pieces of `bytes` bytes, `stride` bytes apart: a dense array is one piece.
 struct Span {
   const void* at;
-  size_t bytes;
+  size_t bytes, rows = 1, stride = 0;
 };
+
+// Whether any byte belongs to both.  Rows at one stride (slices of one wider
+// tensor) may interleave; rows at different strides count as filling their range.
+bool share(const Span& x, const Span& y) {
+  if (!x.at || !y.at || x.bytes == 0 || y.bytes == 0 || x.rows == 0 || y.rows == 0) return false;
+  const bool in_order = reinterpret_cast<uintptr_t>(x.at) < reinterpret_cast<uintptr_t>(y.at);
+  const Span &a = in_order ? x : y, &b = in_order ? y : x;  // a starts first
+  const size_t by = reinterpret_cast<uintptr_t>(b.at) - reinterpret_cast<uintptr_t>(a.at);
+  if (by >= (a.rows - 1) * a.stride + a.bytes) return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  if (a.rows > 1 && b.rows > 1 && a.stride != b.stride) return true;
+  // each of b's rows starts `in` bytes behind the start of a row of a (the first behind row `row`)
+  const size_t stride = a.rows > 1 ? a.stride : b.stride, row = by / stride, in = by % stride;
+  return in < a.bytes || (row + 1 < a.rows && stride - in < b.bytes);
+}
 
 // Whether an output shares memory with an input.
 template <size_t N, size_t M>
 bool overlap(const Span (&outs)[N], const Span (&ins)[M]) {
   for (const Span& o : outs)
-    for (const Span& i : ins) {
-      const char *a = static_cast<const char*>(o.at), *b = static_cast<const char*>(i.at);
-      if (a && b && o.bytes > 0 && i.bytes > 0 && a < b + i.bytes && b < a + o.bytes) return true;
-    }
+    for (const Span& i : ins)
+      if (share(o, i)) return true;
+  return false;
+}
+
+// Whether two outputs share memory.
+template <size_t N>
+bool overlap(const Span (&outs)[N]) {
+  for (size_t i = 0; i < N; ++i)
+    for (size_t j = i + 1; j < N; ++j)
+      if (share(outs[i], outs[j])) return true;
   return false;
 }
 
@@ -42,9 +65,10 @@ size_t dtype_bytes(mesa_dtype t) { return t == MESA_BF16 ? 2 : 4; }
 
 // ---- gated linear recurrence ----------------------------------------------
 
-// Bytes from the first to the last element of the token rows at stride ld.
-size_t lru_rows_bytes(const mesa_lru_desc* d, int32_t ld) {
-  return d->T > 0 ? (((size_t)d->B * d->T - 1) * ld + d->D) * dtype_bytes(d->dtype) : 0;
+// The token rows at stride ld.
+Span lru_rows(const mesa_lru_desc* d, const void* at, int32_t ld) {
+  const size_t e = dtype_bytes(d->dtype);
+  return {at, d->D * e, (size_t)d->B * d->T, ld * e};
 }
 
 constexpr int kLruMaxStride = 1 << 20;
@@ -99,11 +123,12 @@ mesa_status mesa_lru_fwd(const mesa_lru_desc* d, const void* x, const void* ga, 
   if (!all_aligned({x, ga, gi, lam, h0, lengths, y, h_final, workspace})) return MESA_ERR_ALIGNMENT;
   const size_t need = mesa_lru_workspace_bytes(d);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MESA_ERR_WORKSPACE;
-  const size_t rows = lru_rows_bytes(d, d->ld), per_channel = (size_t)d->D * 4, state = d->B * per_channel;
-  const Span ins[] = {{x, rows}, {ga, rows}, {gi, rows}, {lam, per_channel}, {lengths, (size_t)d->B * 4}};
-  const Span outs[] = {{y, lru_rows_bytes(d, d->D)}, {workspace, need}, {h_final, state}}, start{h0, state};
+  const size_t per_channel = (size_t)d->D * 4, state = d->B * per_channel;
+  const Span ins[] = {lru_rows(d, x, d->ld), lru_rows(d, ga, d->ld), lru_rows(d, gi, d->ld), {lam, per_channel},
+                      {lengths, (size_t)d->B * 4}};
+  const Span outs[] = {lru_rows(d, y, d->D), {workspace, need}, {h_final, state}}, start{h0, state};
   // h_final may be h0, and nothing else may lie over h0
-  if (overlap(outs, ins) || overlap({outs[0], outs[1]}, {start}) || (h_final != h0 && overlap({outs[2]}, {start})))
+  if (overlap(outs, ins) || overlap(outs) || overlap({outs[0], outs[1]}, {start}) || (h_final != h0 && overlap({outs[2]}, {start})))
     return MESA_ERR_INVALID_ARG;
   mesa::LruParams p = lru_params(d, x, ga, gi, lam, h0, lengths, workspace);
   p.y = y; p.h_final = h_final;
@@ -124,14 +149,14 @@ mesa_status mesa_lru_bwd(const mesa_lru_desc* d, const void* x, const void* ga, 
   const size_t need = mesa_lru_workspace_bytes(d);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MESA_ERR_WORKSPACE;
   const bool bf16 = d->dtype == MESA_BF16;
-  const size_t rows = lru_rows_bytes(d, d->ld), grads = lru_rows_bytes(d, ld_grad);
   const size_t per_channel = (size_t)d->D * 4, state = d->B * per_channel;
-  const Span ins[] = {{x, rows}, {ga, rows}, {gi, rows}, {lam, per_channel}, {h0, state}, {lengths, (size_t)d->B * 4},
-                      {dy, lru_rows_bytes(d, d->D)}};
-  const Span outs[] = {{dx, grads}, {dga, grads}, {dgi, grads}, {dlam, per_channel}, {workspace, need}, {dh0, state}};
+  const Span ins[] = {lru_rows(d, x, d->ld), lru_rows(d, ga, d->ld), lru_rows(d, gi, d->ld), {lam, per_channel},
+                      {h0, state}, {lengths, (size_t)d->B * 4}, lru_rows(d, dy, d->D)};
+  const Span outs[] = {lru_rows(d, dx, ld_grad), lru_rows(d, dga, ld_grad), lru_rows(d, dgi, ld_grad),
+                       {dlam, per_channel}, {workspace, need}, {dh0, state}};
   const Span last{d_hfinal, state};
   // dh0 may be d_hfinal, and nothing else may lie over d_hfinal
-  if (overlap(outs, ins) || overlap({outs[0], outs[1], outs[2], outs[3], outs[4]}, {last}) ||
+  if (overlap(outs, ins) || overlap(outs) || overlap({outs[0], outs[1], outs[2], outs[3], outs[4]}, {last}) ||
       (dh0 != d_hfinal && overlap({outs[5]}, {last})))
     return MESA_ERR_INVALID_ARG;
   mesa::LruParams p = lru_params(d, x, ga, gi, lam, h0, lengths, workspace);
@@ -151,9 +176,10 @@ mesa_status mesa_lru_step(int32_t N, int32_t D, int32_t ld, float c, mesa_dtype 
   if (!x || !ga || !gi || !lam || !h_state || !y) return MESA_ERR_INVALID_ARG;
   if (!all_aligned({x, ga, gi, lam, h_state, y})) return MESA_ERR_ALIGNMENT;
   const mesa_lru_desc all{N, 1, D, ld, c, dtype};
-  const size_t rows = lru_rows_bytes(&all, ld), per_channel = (size_t)D * 4, state = N * per_channel;
-  if (overlap({{y, lru_rows_bytes(&all, D)}, {h_state, state}}, {{x, rows}, {ga, rows}, {gi, rows}, {lam, per_channel}}))
-    return MESA_ERR_INVALID_ARG;
+  const size_t per_channel = (size_t)D * 4, state = N * per_channel;
+  const Span ins[] = {lru_rows(&all, x, ld), lru_rows(&all, ga, ld), lru_rows(&all, gi, ld), {lam, per_channel}};
+  const Span outs[] = {lru_rows(&all, y, D), {h_state, state}};
+  if (overlap(outs, ins) || overlap(outs)) return MESA_ERR_INVALID_ARG;
   mesa::LruParams p = lru_params(&d, x, ga, gi, lam, nullptr, nullptr, nullptr);
   p.h_final = h_state; p.y = y;
   return mesa::launch_lru_step(dtype == MESA_BF16, p, stream) == hipSuccess ? MESA_OK : MESA_ERR_HIP;
@@ -191,8 +217,8 @@ mesa_status mesa_rmsnorm(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_
   if (!all_aligned({x, residual, w, y, scale, residual_out})) return MESA_ERR_ALIGNMENT;
   const size_t n = (size_t)R * D, rows = n * dtype_bytes(dtype), stream_rows = n * dtype_bytes(res_dtype);
   const size_t groups = group ? (D + 127) / 128 : 1, weights = (size_t)D * 4;
-  if (overlap({{y, e4m3 ? n : rows}, {scale, e4m3 ? R * groups * 4 : 0}},
-              {{x, rows}, {residual, stream_rows}, {w, weights}, {residual_out, stream_rows}}) ||
+  const Span outs[] = {{y, e4m3 ? n : rows}, {scale, e4m3 ? R * groups * 4 : 0}};
+  if (overlap(outs, {{x, rows}, {residual, stream_rows}, {w, weights}, {residual_out, stream_rows}}) || overlap(outs) ||
       overlap({{residual_out, stream_rows}},
               {{residual_out == x && dtype == res_dtype ? nullptr : x, rows},
                {residual_out == residual ? nullptr : residual, stream_rows}, {w, weights}}))
@@ -223,7 +249,7 @@ mesa_status mesa_rmsnorm_bwd(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype 
   const Span ins[] = {{s, stream_rows}, {w, weights}, {dy, rows}};
   const Span outs[] = {{dx, rows}, {dw, weights}, {workspace, need}, {ds, stream_rows}}, along{d_residual, stream_rows};
   // ds may be d_residual, and nothing else may lie over d_residual
-  if (overlap(outs, ins) || overlap({outs[0], outs[1], outs[2]}, {along}) ||
+  if (overlap(outs, ins) || overlap(outs) || overlap({outs[0], outs[1], outs[2]}, {along}) ||
       (ds != d_residual && overlap({outs[3]}, {along})))
     return MESA_ERR_INVALID_ARG;
   mesa::NormParams p{};
@@ -276,8 +302,10 @@ mesa_status mesa_qk_preprocess_bwd(int32_t B, int32_t H, int32_t T, int32_t d, i
   // every input row is read by up to `window` output rows
   const size_t n = (size_t)B * H * T * d, seq = n * dtype_bytes(dtype);
   const size_t hist = (size_t)B * H * (window - 1) * d * dtype_bytes(dtype), taps = (size_t)H * d * window * 4;
-  if (overlap({{dq_raw, seq}, {dk_raw, seq}, {dq_hist, hist}, {dk_hist, hist}, {dw_q, taps}, {dw_k, taps},
-               {workspace, need}},
+  const Span outs[] = {{dq_raw, seq}, {dk_raw, seq}, {dq_hist, hist}, {dk_hist, hist}, {dw_q, taps}, {dw_k, taps},
+                       {workspace, need}};
+  if (overlap(outs) ||
+      overlap(outs,
               {{q_raw, seq}, {k_raw, seq}, {w_q, taps}, {w_k, taps}, {d_q, n * 4}, {d_k, n * 4}, {q_hist, hist},
                {k_hist, hist}, {d_q_hist_out, hist}, {d_k_hist_out, hist}}))
     return MESA_ERR_INVALID_ARG;

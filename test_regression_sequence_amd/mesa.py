@@ -598,8 +598,8 @@ def decode_step_ex(q, k, v, gamma, beta, lam, h_state, g_state, *, x_state=None,
 # Every tensor of a call has to be on one device, the first argument's, and a
 # given stream too; the call is launched there whatever device is current.  What
 # a call allocates belongs to the stream it runs on, so that its memory is given
-# on in that stream's order.  Tensors passed as `out` may not overlap inputs but
-# where a call says so.
+# on in that stream's order.  Tensors passed as `out` and workspaces may not overlap
+# inputs or one another but where a call says so.
 
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
