@@ -253,8 +253,9 @@ mesa_status mesa_rmsnorm_bwd(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype 
       (ds != d_residual && overlap({outs[3]}, {along})))
     return MESA_ERR_INVALID_ARG;
   mesa::NormParams p{};
-  p.x = s; p.residual = d_residual; p.w = w; p.dy = dy; p.y = ds; p.residual_out = dx; p.dw = dw; p.part = workspace;
+  p.x = s; p.residual = d_residual; p.w = w; p.dy = dy; p.y = ds; p.residual_out = dx; p.dw = dw;
   p.R = R; p.D = D; p.eps = eps;
+  mesa::rmsnorm_bwd_carve(p, workspace);
   return mesa::launch_rmsnorm_bwd(dtype == MESA_BF16, res_dtype == MESA_BF16, p, stream) == hipSuccess ? MESA_OK
                                                                                                        : MESA_ERR_HIP;
 }

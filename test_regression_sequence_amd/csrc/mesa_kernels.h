@@ -161,7 +161,8 @@ struct NormParams {
   float* scale;             // [R, groups]
   void* residual_out;       // forward: [R, D] or null; backward: dx [R, D] or null
   float* dw;                // backward: [D]
-  void* part;               // backward: scratch
+  float* part;              // backward: partial sums of dw
+  double* acc;              // backward: sums over long runs of rows of more than 8192
   int R, D;
   float eps;
   int e4m3, group;
@@ -265,7 +266,9 @@ hipError_t launch_lru_ready(const LruParams& p, size_t words, hipStream_t s);
 hipError_t launch_lru_step(bool bf16, const LruParams& p, hipStream_t s);
 hipError_t launch_rmsnorm(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s);
 hipError_t launch_rmsnorm_bwd(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s);
+// Bytes of the gradient's workspace, and its parts' places.
 size_t rmsnorm_bwd_scratch(int R, int D);
+void rmsnorm_bwd_carve(NormParams& p, void* workspace);
 hipError_t launch_qk_prep_bwd(bool bf16, int D, const PrepBwdParams& p, hipStream_t s);
 size_t qk_prep_bwd_scratch(int BH, int T, int D, int W);
 

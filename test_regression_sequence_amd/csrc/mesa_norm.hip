@@ -12,10 +12,13 @@
 // w, and the backward's sums for dw, stay in their registers meanwhile.
 //
 // At R = 32768, D = 2048, bf16 rows and stream: 86 us with e4m3 rows (5.5 TB/s),
-// 101 us with bf16 rows (5.3), the gradient 104 (5.2); a copy runs at 5.15 TB/s.
-// Rows over 8192 leave no room for w in the gradient's registers; it is read
-// from LDS there (145 -> 124 us at D = 16384, bf16, 405 -> 294 fp32, which still
-// holds more than its registers take and runs at 3.7 TB/s).
+// 101 us with bf16 rows (5.3), the gradient 107 with its sum for dw; a copy runs at
+// 5.15 TB/s.  Rows over 8192 leave no room for w in the gradient's registers; it is
+// read from LDS there (145 -> 118 us at R = 4096, D = 16384, bf16).  With fp32
+// tensors the gradient's rows of 4 vectors a lane still hold more than the
+// registers: one wave per SIMD at D of 1025 to 2048 and of 4097 to 8192 (R = 32768,
+// D = 2048: 200 us fp32, 203 bf16 on an fp32 stream, both above a copy's rate all
+// the same), spills above 8192 (R = 4096, D = 16384: 303 us fp32, 3.5 TB/s).
 #include <type_traits>
 
 #include "mesa_common.h"
@@ -219,13 +222,19 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormP
   }
 }
 
-// The same rows; dw is summed per lane over the rows that a group walks, then
-// over the workgroup's groups through LDS, into one partial row per workgroup.
+// The same rows; dw is summed per lane over the rows that a group walks, in fp32,
+// then over the workgroup's groups through LDS, in 64 bits, into one partial row
+// per workgroup.  A chain of fp32 additions loses bits as it grows (2^24 rows of
+// 16, all alike: 600 half steps of fp32), so behind every kDwRun rows a lane's sums
+// are added to 64-bit ones: in LDS, or where that holds the weights (TPR = 512) in
+// the workspace.
+constexpr int kDwRun = 64;
+
 template <bool BF16, bool RBF16, RowEnd END, int TPR, int NV>
 __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_bwd_kernel(NormParams p) {
   using Sh = NormShape<TPR>;
   __shared__ float2 lds[2][8];
-  __shared__ float sums[Sh::kRows][TPR * 8];
+  __shared__ float sums[Sh::kRows][Sh::kRows > 1 ? TPR * 8 : 1];
   constexpr bool kInLds = TPR == 512;
   __shared__ Raw8<false> weights[kInLds ? TPR * NV : 1];
   int turn = 0;
@@ -260,71 +269,110 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_bwd_kernel(N
     else return w[k];
   };
   const float inv_d = 1.f / (float)D;
-  while (row < p.R) {
-    float ss = 0.f, gs = 0.f;
+  __shared__ double lds_acc[kInLds ? 1 : TPR * NV * 8];
+  // (each thread adds to, and reads, what it wrote itself)
+  double* acc = kInLds ? p.acc + (size_t)blockIdx.x * (TPR * NV * 8) : lds_acc;
+  float* part = p.part + (size_t)blockIdx.x * D;
+  // Rows are counted alike for all of a workgroup's groups.  (Where it has several, in
+  // one loop: two nested ones take up to 36 registers more.  Where it has one, nested:
+  // 4 to 24 less.)
+  constexpr int kNest = Sh::kRows == 1 ? kDwRun : 1;
+  const int first = blockIdx.x * Sh::kRows;
+  bool fresh = true;
+  int runs = 0;
+  for (int start = first; start < p.R; start += kNest * stride) {
+    for (int run = 0; run < kNest && row < p.R; ++run) {
+      float ss = 0.f, gs = 0.f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if constexpr (END == RowEnd::kWithin) own_channels(rs[k], 8 * (lane + TPR * k), D);
+        if constexpr (END == RowEnd::kWithin) own_channels(rd[k], 8 * (lane + TPR * k), D);
+        if constexpr (END == RowEnd::kWithin) if (p.residual) {
+          own_channels(rr[k], 8 * (lane + TPR * k), D);
+          if constexpr (TPR > 64) hold(rr[k]);  // before the barrier: ds may be d_residual (as in the forward)
+        }
+        const Raw8<false> wk = weight(k);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float s = rs[k].at(e);
+          ss = __builtin_fmaf(s, s, ss);
+          gs = __builtin_fmaf(rd[k].at(e) * wk.at(e), s, gs);
+        }
+      }
+      row_sum2<TPR>(ss, gs, lds, turn);
+      const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, inv_d, p.eps));
+      const float kk = gs * inv_d * r * r;  // mean(g n) r: ds = r g - n (mean(g n) r)
+      const int here = row;
+      row += stride;
+      float ds[NV][8];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const Raw8<false> wk = weight(k);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float n = rs[k].at(e) * r, d = rd[k].at(e);
+          ds[k][e] = __builtin_fmaf(-n, kk, r * (d * wk.at(e)));
+          if (p.residual) ds[k][e] += rr[k].at(e);
+          dw[k][e] = __builtin_fmaf(d, n, dw[k][e]);
+        }
+      }
+      if (row < p.R) load(row);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int c = 8 * (lane + TPR * k);
+        store_raw8<RBF16, END != RowEnd::kWhole>(p.y, (size_t)here * D + c, ds[k], D - c);
+        if (p.residual_out) store_raw8<BF16, END != RowEnd::kWhole>(p.residual_out, (size_t)here * D + c, ds[k], D - c);
+      }
+    }
+    const bool last = start + kNest * stride >= p.R;
+    if (kNest == 1 && ++runs < kDwRun && !last) continue;
+    // The run's sums to the 64-bit ones, the last run's on to the partial row.  (The thread's
+    // number is hidden, or what follows from it is formed ahead of the rows and held in
+    // registers while they are walked.)
+    int thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if constexpr (END == RowEnd::kWithin) own_channels(rs[k], 8 * (lane + TPR * k), D);
-      if constexpr (END == RowEnd::kWithin) own_channels(rd[k], 8 * (lane + TPR * k), D);
-      if constexpr (END == RowEnd::kWithin) if (p.residual) {
-        own_channels(rr[k], 8 * (lane + TPR * k), D);
-        if constexpr (TPR > 64) hold(rr[k]);  // before the barrier: ds may be d_residual (as in the forward)
+      if constexpr (Sh::kRows == 1) {  // a lane's channels are its own
+        if (!(fresh && last))
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            double* at = acc + (8 * k + e) * TPR + thread;
+            const double v = (fresh ? 0. : *at) + dw[k][e];
+            if (!last) *at = v;
+            dw[k][e] = last ? (float)v : 0.f;
+          }
+        const int c = 8 * (thread + TPR * k);
+        if (last) store_raw8<false, END != RowEnd::kWhole>(part, c, dw[k], D - c);
+      } else {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          sums[thread / TPR][8 * (thread % TPR) + e] = dw[k][e];
+          dw[k][e] = 0.f;
+        }
+        __syncthreads();
+        for (int i = thread; i < TPR * 8; i += Sh::kThreads) {
+          const int c = TPR * 8 * k + i;
+          if (c >= D) break;
+          double v = fresh ? 0. : acc[c];
+#pragma unroll
+          for (int g = 0; g < Sh::kRows; ++g) v += sums[g][i];
+          if (last) part[c] = (float)v;
+          else acc[c] = v;
+        }
       }
-      const Raw8<false> wk = weight(k);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float s = rs[k].at(e);
-        ss = __builtin_fmaf(s, s, ss);
-        gs = __builtin_fmaf(rd[k].at(e) * wk.at(e), s, gs);
-      }
     }
-    row_sum2<TPR>(ss, gs, lds, turn);
-    const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, inv_d, p.eps));
-    const float kk = gs * inv_d * r * r;  // mean(g n) r: ds = r g - n (mean(g n) r)
-    const int here = row;
-    row += stride;
-    float ds[NV][8];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const Raw8<false> wk = weight(k);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float n = rs[k].at(e) * r, d = rd[k].at(e);
-        ds[k][e] = __builtin_fmaf(-n, kk, r * (d * wk.at(e)));
-        if (p.residual) ds[k][e] += rr[k].at(e);
-        dw[k][e] = __builtin_fmaf(d, n, dw[k][e]);
-      }
-    }
-    if (row < p.R) load(row);
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = 8 * (lane + TPR * k);
-      store_raw8<RBF16, END != RowEnd::kWhole>(p.y, (size_t)here * D + c, ds[k], D - c);
-      if (p.residual_out) store_raw8<BF16, END != RowEnd::kWhole>(p.residual_out, (size_t)here * D + c, ds[k], D - c);
-    }
-  }
-  float* part = static_cast<float*>(p.part) + (size_t)blockIdx.x * D;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sums[threadIdx.x / TPR][8 * lane + e] = dw[k][e];
-    __syncthreads();
-    for (int i = threadIdx.x; i < TPR * 8; i += Sh::kThreads) {
-      float v = 0.f;
-#pragma unroll
-      for (int g = 0; g < Sh::kRows; ++g) v += sums[g][i];
-      const int c = TPR * 8 * k + i;
-      if (c < D) part[c] = v;
-    }
+    fresh = false;
+    runs = 0;
   }
 }
 
-// dw from G partial rows [G, D]: 16 channels a workgroup, 16 threads a channel.
+// dw from G partial rows [G, D], summed in 64 bits: 16 channels a workgroup, 16 threads a channel.
 __global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* part, float* dw, int G, int D) {
-  __shared__ float sums[16][16];
+  __shared__ double sums[16][16];
   const int j = threadIdx.x % 16, slice = threadIdx.x / 16, c = blockIdx.x * 16 + j;
-  float v = 0.f;
+  double v = 0.;
   if (c < D) {
 #pragma unroll 8
     for (int g = slice; g < G; g += 16) v += part[(size_t)g * D + c];
@@ -333,9 +381,11 @@ __global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* part, floa
   __syncthreads();
   if (slice == 0 && c < D) {
     for (int i = 1; i < 16; ++i) v += sums[i][j];
-    dw[c] = v;
+    dw[c] = (float)v;
   }
 }
+
+constexpr int kMaxD = 512 * 4 * 8;  // the widest row group's channels
 
 // Calls fn(TPR, NV) as constants for the smallest row group that holds D channels.
 template <RowEnd END, typename F>
@@ -378,6 +428,13 @@ int bwd_groups(int R, int D) {
   });
 }
 
+// Bytes of the 64-bit sums that do not fit LDS.
+size_t acc_bytes(int R, int D) {
+  const bool in_lds = norm_shape<RowEnd::kWhole>(D, [](auto tpr, auto) { return decltype(tpr)::value < 512; });
+  const int G = bwd_groups(R, D);  // (a row a workgroup)
+  return in_lds || R <= kDwRun * G ? 0 : (size_t)G * kMaxD * sizeof(double);
+}
+
 template <bool BF16, bool RBF16, RowEnd END>
 hipError_t launch_bwd_t(const NormParams& p, hipStream_t s) {
   const int G = p.R > 0 ? bwd_groups(p.R, p.D) : 0;
@@ -389,14 +446,19 @@ hipError_t launch_bwd_t(const NormParams& p, hipStream_t s) {
     });
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3((p.D + 15) / 16), dim3(256), 0, s, static_cast<const float*>(p.part), p.dw,
+  hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3((p.D + 15) / 16), dim3(256), 0, s, p.part, p.dw,
                      G, p.D);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t rmsnorm_bwd_scratch(int R, int D) { return (size_t)bwd_groups(R, D) * D * 4; }
+size_t rmsnorm_bwd_scratch(int R, int D) { return acc_bytes(R, D) + (size_t)bwd_groups(R, D) * D * sizeof(float); }
+
+void rmsnorm_bwd_carve(NormParams& p, void* workspace) {
+  p.acc = static_cast<double*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + (p.R > 0 ? acc_bytes(p.R, p.D) : 0));
+}
 
 template <RowEnd END>
 static hipError_t launch_fwd(bool bf16, bool res_bf16, const NormParams& p, hipStream_t s) {
