@@ -224,10 +224,10 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormP
 
 // The same rows; dw is summed per lane over the rows that a group walks, in fp32,
 // then over the workgroup's groups through LDS, in 64 bits, into one partial row
-// per workgroup.  A chain of fp32 additions loses bits as it grows (2^24 rows of
-// 16, all alike: 600 half steps of fp32), so behind every kDwRun rows a lane's sums
-// are added to 64-bit ones: in LDS, or where that holds the weights (TPR = 512) in
-// the workspace.
+// per workgroup.  A chain of fp32 additions loses bits as it grows (2^20 rows of
+// 2500, all alike: up to 512 half steps of fp32, 17 as it is), so behind every
+// kDwRun rows a lane's sums are added to 64-bit ones: in LDS, or where that holds
+// the weights (TPR = 512) in the workspace.
 constexpr int kDwRun = 64;
 
 template <bool BF16, bool RBF16, RowEnd END, int TPR, int NV>
