@@ -251,12 +251,14 @@ __global__ __launch_bounds__(256, 3) void lru_bwd_kernel(LruParams p) {
 }
 
 // dlam from `rows` partial sums [rows, D] of dL / d log t: 16 channels a
-// workgroup, 16 threads a channel.
+// workgroup, 16 threads a channel.  A tile's sum has 64 tokens in fp32 (14 roundings);
+// the tiles are summed in 64 bits: in fp32 the error grew with their number, 2200 half
+// steps over 2^14 equal sequences of 200 tokens.
 __global__ __launch_bounds__(kThreads) void lru_dlam_kernel(const float* part, const float* lam, float* dlam, int rows,
                                                             int D) {
-  __shared__ float sums[16][16];
+  __shared__ double sums[16][16];
   const int k = threadIdx.x % 16, slice = threadIdx.x / 16, ch = blockIdx.x * 16 + k;
-  float v = 0.f;
+  double v = 0.;
   if (ch < D) {
 #pragma unroll 8
     for (int r = slice; r < rows; r += 16) v += part[(size_t)r * D + ch];
@@ -265,7 +267,7 @@ __global__ __launch_bounds__(kThreads) void lru_dlam_kernel(const float* part, c
   __syncthreads();
   if (slice == 0 && ch < D) {
     for (int i = 1; i < 16; ++i) v += sums[i][k];
-    dlam[ch] = v * lru_rate_slope(lam[ch]);
+    dlam[ch] = (float)(v * lru_rate_slope(lam[ch]));
   }
 }
 

@@ -45,3 +45,43 @@ def test_norm_weight_gradient_over_many_equal_rows(R, D, dtype, res):
     want = R * dy[0].double() * sd / torch.sqrt(sd.square().mean() + 1e-5)
     bound = (64 + 0.5 * (min(D, 128) + 10) + 8) * E * want.abs()
     assert ((dw - want).abs() <= bound).all(), float(((dw - want).abs() / want.abs()).max() / E)
+
+
+@pytest.mark.parametrize("T,n", [(6, 1 << 18), (30, 1 << 17), (64, 1 << 16), (200, 1 << 14)])
+def test_decay_parameter_gradient_over_many_equal_sequences(T, n):
+    """Copies of one sequence: a power of two times its gradient, bit for bit."""
+    D = 8
+    x, ga, gi, dy = (normal(1, T, D, seed=i) for i in range(4))
+    lam = normal(D, seed=5) - 5
+    one = mesa.lru_bwd(x, ga, gi, lam, dy)["dlam"]
+    many = mesa.lru_bwd(*(copies(v, n) for v in (x, ga, gi)), lam, copies(dy, n))["dlam"]
+    torch.cuda.synchronize()
+    assert one.abs().min() > 0 and torch.equal(many, one * n), float(((many / (one * n)) - 1).abs().max() / E)
+
+
+def test_decay_parameter_gradient_over_a_long_sequence():
+    """Equal tokens from the state that they keep (h = u / (1 - a), g alike): every token's v is the same but for its
+    state's and adjoint's rounding.  2^21 tokens, a = 0.5 .. 0.9.
+
+    v = -log(a) g ((a^2 / m) s_i x - a h).  With w = -2 log(a) <= 2, |ga|, |gi| <= 1 and m >= 0.4, the gates, a, m and the
+    quotient are off by at most 60 e; h and g sum at most 1 / (1 - a) = 10 tokens' worth of such errors; the two terms of
+    the difference add in magnitude.  A tile adds 64 tokens with 14 roundings."""
+    T, D = 1 << 21, 8
+    gen = np.random.default_rng(4)
+    a = np.linspace(0.5, 0.9, D)
+    ga, gi, x, dy = (gen.uniform(-1, 1, D).astype(np.float32) for _ in range(4))
+    sr, si = 1 / (1 + np.exp(-ga.astype(np.float64))), 1 / (1 + np.exp(-gi.astype(np.float64)))
+    lam = np.log(np.expm1(-np.log(a) / (8 * sr))).astype(np.float32)
+    w = 16 * np.log1p(np.exp(lam.astype(np.float64))) * sr
+    a, m = np.exp(-w / 2), np.sqrt(-np.expm1(-w))
+    u = m * si * x
+    h, g = u / (1 - a), dy / (1 - a)
+    slope = 1 / (1 + np.exp(-lam.astype(np.float64))) / np.log1p(np.exp(lam.astype(np.float64)))
+    want = T * 0.5 * w * g * (a * a / m * si * x - a * h) * slope
+    size = T * 0.5 * w * np.abs(g) * (a * a / m * np.abs(si * x) + a * np.abs(h)) * slope
+    dev = lambda v: torch.from_numpy(v).cuda()  # noqa: E731
+    rows = [dev(v)[None, None].expand(1, T, D).contiguous() for v in (x, ga, gi)]
+    got = mesa.lru_bwd(*rows, dev(lam), dev(dy)[None, None].expand(1, T, D).contiguous(), h0=dev(h.astype(np.float32))[None],
+                       d_hfinal=dev((a * g).astype(np.float32))[None])["dlam"].cpu().numpy()
+    # the initial state and the last adjoint are rounded too: 10 e and a few tokens of 2^21
+    assert (np.abs(got - want) <= (2 * 60 * 10 + 14) * E * size).all(), (np.abs(got - want) / size / E).max()
