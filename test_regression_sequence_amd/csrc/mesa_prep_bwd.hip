@@ -11,9 +11,10 @@
 // window, added to the rows t-W+1 .. t, and the first of them is complete.  The
 // first tokens a group walks are its own; the W-1 behind them are the next
 // group's and only complete this group's rows, so (W-1)/Steps of the work is
-// done twice.  Loads run one block of tokens ahead.  dw is summed per lane, per
-// workgroup through LDS, and over workgroups by a second kernel, all in a fixed
-// order.  At B=8, H=16, T=4096, d=128, W=4, bf16: 222 us, 1.19 GB at 5.4 TB/s, of
+// done twice.  Loads run one block of tokens ahead.  dw is summed per lane over its
+// at most 29 to 32 tokens in fp32, per workgroup through LDS and over workgroups by a
+// second kernel in 64 bits (in fp32 the error grew with the sequences: 480 half
+// steps over 2^15 equal ones at d=16), all in a fixed order.  At B=8, H=16, T=4096, d=128, W=4, bf16: 222 us, 1.19 GB at 5.4 TB/s, of
 // which 0.11 GB are rows that two groups read.
 #include "mesa_common.h"
 #include "mesa_kernels.h"
@@ -137,20 +138,20 @@ __global__ __launch_bounds__(kThreads) void prep_bwd_kernel(PrepBwdParams p) {
   __syncthreads();
   float* part = p.part + (((size_t)which * p.BH + bh) * gridDim.x + blockIdx.x) * (D * W);
   for (int i = threadIdx.x; i < D * W; i += kThreads) {
-    float v = 0.f;
+    double v = 0.;
 #pragma unroll 8
     for (int g = 0; g < Sh::NG; ++g) v += sums[g][i];
-    part[i] = v;
+    part[i] = (float)v;
   }
 }
 
 // dw[h][j][i] from the partial sums [2, BH, tiles, n = D W] of the workgroups:
 // 16 sums a workgroup, 16 threads a sum over the head's sequences and tiles.
 __global__ __launch_bounds__(256) void prep_bwd_dw_kernel(PrepBwdParams p, int tiles, int n) {
-  __shared__ float sums[16][16];
+  __shared__ double sums[16][16];
   const int k = threadIdx.x % 16, slice = threadIdx.x / 16, i = blockIdx.x * 16 + k, h = blockIdx.y, which = blockIdx.z;
   const int rows = p.BH / p.H * tiles;  // (n is a multiple of 16)
-  float v = 0.f;
+  double v = 0.;
 #pragma unroll 4
   for (int r = slice; r < rows; r += 16) {
     const size_t bh = (size_t)(r / tiles) * p.H + h;
@@ -160,7 +161,7 @@ __global__ __launch_bounds__(256) void prep_bwd_dw_kernel(PrepBwdParams p, int t
   __syncthreads();
   if (slice == 0) {
     for (int g = 1; g < 16; ++g) v += sums[g][k];
-    p.dw[which][(size_t)h * n + i] = v;
+    p.dw[which][(size_t)h * n + i] = (float)v;
   }
 }
 

@@ -85,3 +85,42 @@ def test_decay_parameter_gradient_over_a_long_sequence():
                        d_hfinal=dev((a * g).astype(np.float32))[None])["dlam"].cpu().numpy()
     # the initial state and the last adjoint are rounded too: 10 e and a few tokens of 2^21
     assert (np.abs(got - want) <= (2 * 60 * 10 + 14) * E * size).all(), (np.abs(got - want) / size / E).max()
+
+
+@pytest.mark.parametrize("d", [16, 64, 128])
+def test_tap_gradient_over_many_equal_sequences(d):
+    """Copies of one token and its history: a power of two times its gradient, bit for bit."""
+    H, W, n = 1, 4, (1 << 15) * 16 // d
+    q, k, qh, kh = (normal(1, H, r, d, seed=i) for i, r in enumerate((1, 1, W - 1, W - 1)))
+    dq, dk = normal(1, H, 1, d, seed=4), normal(1, H, 1, d, seed=5)
+    w = normal(H, d, W, seed=6), normal(H, d, W, seed=7)
+    one = mesa.qk_preprocess_bwd(q, k, *w, dq, dk, q_hist=qh, k_hist=kh)
+    many = mesa.qk_preprocess_bwd(copies(q, n), copies(k, n), *w, copies(dq, n), copies(dk, n), q_hist=copies(qh, n),
+                                  k_hist=copies(kh, n))
+    torch.cuda.synchronize()
+    for key in ("dw_q", "dw_k"):
+        assert torch.equal(many[key], one[key] * n), (key, float(((many[key] / (one[key] * n)) - 1).abs().max() / E))
+
+
+@pytest.mark.parametrize("d,T", [(16, 1 << 22), (128, 1 << 19)])
+def test_tap_gradient_over_many_equal_tokens(d, T):
+    """dw[j][i] = T e[j] x[j] for equal rows (history alike).  e = (d - o <o, d>) / n is off by some 60 e of its terms'
+    magnitudes (5 of the convolution, as much again of the norm's, a tree of 5 levels, quotients); a lane adds at most 29
+    tokens in fp32."""
+    H, W = 1, 4
+    q, dq = normal(1, H, 1, d, seed=1), normal(1, H, 1, d, seed=2)
+    w = normal(H, d, W, seed=3)
+    rows = lambda v, n: v.expand(1, H, n, d).contiguous()  # noqa: E731
+    r = mesa.qk_preprocess_bwd(rows(q, T), rows(q, T), w, w, rows(dq, T), rows(dq, T), q_hist=rows(q, W - 1),
+                               k_hist=rows(q, W - 1))
+    x, g, s = q[0, 0, 0].double(), dq[0, 0, 0].double(), w[0].double().sum(-1)
+    y = s * x
+    n = y.norm()
+    o = y / n
+    e, size = (g - o * (o * g).sum()) / n, (g.abs() + o.abs() * (o * g).abs().sum()) / n
+    # (the taps' sum cancels: the convolution's error counts against their magnitudes)
+    spread = float((w[0].double().abs().sum(-1) * x.abs()).norm() / n)
+    for key in ("dw_q", "dw_k"):
+        got = r[key][0].double()
+        bound = (60 * spread + 29 + 4) * E * T * size * x.abs()
+        assert ((got - (T * e * x)[:, None]).abs() <= bound[:, None]).all(), key
