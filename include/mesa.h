@@ -604,6 +604,8 @@ mesa_status mesa_rmsnorm(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_
 /* Gradients of mesa_rmsnorm (its y in dtype) at s and w.  With r = 1 / sqrt(mean(s^2)
  * + eps), n = s r and g = dy w:
  *   ds = r (g - n mean(g n)) + d_residual,    dw = sum_rows dy n.
+ * A row whose products s s or g s leave fp32's range (they are summed before r is
+ * known) gives unspecified values in that row and in dw.
  *
  *   s          [R, D] res_dtype  the stream the forward left (residual_out)
  *   dy         [R, D] dtype

@@ -178,7 +178,7 @@ __global__ __launch_bounds__(NormShape<TPR>::kThreads) void rmsnorm_kernel(NormP
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[k][e] *= factor * w[k][e];
+      for (int e = 0; e < 8; ++e) s[k][e] = s[k][e] * factor * w[k][e];  // (s r is of order 1; r w may leave fp32)
     if (!p.e4m3) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
