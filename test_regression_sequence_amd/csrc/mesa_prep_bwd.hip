@@ -94,7 +94,8 @@ __global__ __launch_bounds__(kThreads) void prep_bwd_kernel(PrepBwdParams p) {
         ss = group_sum<LPR>(ss);
         dot = group_sum<LPR>(dot);
         const bool own = tt < t0 + S, some = tt < T;
-        const float scale = some ? prep_scale(ss, p.inv_eps) : 0.f;
+        float scale = some ? prep_scale(ss, p.inv_eps) : 0.f;
+        if (some && ss != ss) scale = ss;  // (the minimum in prep_scale loses a NaN: the row would count as below eps)
         const float k = scale < p.inv_eps ? dot * scale * scale : 0.f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {

@@ -40,3 +40,34 @@ def test_norm_of_small_and_large_rows_with_large_and_small_weights(size, weight,
             assert (np.abs(scale - ref["scale"]) <= (rel + 2 * E) * ref["scale"]).all()
             v = ref["y"] / np.repeat(ref["scale"], group or D, axis=1)[:, :D]
             assert (np.abs(y - v) <= np.maximum(2.0 ** -4 * np.abs(v), 2.0 ** -10) * (1 + 1e-5) + (2 * rel + 8 * E) * np.abs(v)).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d,T", [(16, 9), (64, 100), (128, 1), (128, 1500)])
+def test_nan_in_a_row_reaches_every_gradient_through_its_norm(d, T, dtype):
+    """A NaN in a raw row, its history, a tap or an incoming gradient: NaN exactly where the definition has it."""
+    B, H, W = 2, 2, 4
+    rng = np.random.default_rng(d + T)
+
+    def half(a):
+        return torch.from_numpy(a.astype(np.float32)).to(dtype)
+
+    clean = dict(x=half(rng.standard_normal((B, H, T, d))), hist=half(rng.standard_normal((B, H, W - 1, d))),
+                 w=torch.from_numpy(rng.standard_normal((H, d, W)).astype(np.float32)),
+                 d=torch.from_numpy(rng.standard_normal((B, H, T, d)).astype(np.float32)))
+    spots = [("x", (1, 0, t, 3)) for t in {0, T // 2, T - 1}] + [("hist", (1, 0, W - 2, 5)), ("w", (0, 7, 1)), ("d", (1, 0, T // 2, 2))]
+    for key, at in spots:
+        a = {k: v.clone() for k, v in clean.items()}
+        a[key][at] = float("nan")
+        t, c = {k: v.cuda() for k, v in a.items()}, {k: v.cuda() for k, v in clean.items()}
+        # the NaN in the queries only: the keys are clean
+        r = mesa.qk_preprocess_bwd(t["x"], c["x"], t["w"], c["w"], t["d"], c["d"], q_hist=t["hist"], k_hist=c["hist"],
+                                   history_grads=True)
+        n = {k: v.float().numpy() for k, v in a.items()}
+        with np.errstate(invalid="ignore"):
+            ref = qk_preprocess_backward(n["x"], n["w"], n["d"], n["hist"])
+        for got, want in (("dq_raw", "dx"), ("dw_q", "dw"), ("dq_hist", "dhist")):
+            assert np.isnan(ref["dw"]).any()
+            assert np.array_equal(np.isnan(r[got].float().cpu().numpy()), np.isnan(ref[want])), (key, at, got)
+        for got in ("dk_raw", "dw_k", "dk_hist"):
+            assert torch.isfinite(r[got]).all(), (key, at, got)
