@@ -510,8 +510,10 @@ mesa_status mesa_qk_preprocess(int32_t B, int32_t H, int32_t T, int32_t d, int32
  *   workspace           mesa_lru_workspace_bytes(d) bytes; on return it holds
  *                       states at fixed distances for mesa_lru_bwd
  *
- * Arithmetic and states are fp32 for either dtype.  Every sum is formed in a
- * fixed order: equal inputs give bitwise equal results.
+ * Arithmetic and states are fp32 for either dtype, sums over tiles of tokens
+ * (dlam) 64-bit.  Every sum is formed in a fixed order: equal inputs give bitwise
+ * equal results.  A NaN in lam, in a state or in a valid row reaches what depends on
+ * it by these formulas, and no other channel or sequence.
  * Supported: 2 <= D <= ld <= 2^20, T >= 0, B >= 1 with B max(ceil(T/64), 1)
  * ceil(D/64) <= 2^23; c > 0, finite (else MESA_ERR_INVALID_ARG).
  * Outputs and workspace may not overlap inputs or one another but as said
@@ -615,7 +617,7 @@ mesa_status mesa_rmsnorm(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype res_
  *              May be d_residual itself
  *   dx         [R, D] dtype out or NULL: ds rounded to x's type, for a bf16 x
  *              on an fp32 stream
- *   dw         [D] fp32 out, summed in a fixed order
+ *   dw         [D] fp32 out, summed in a fixed order, over more than 64 rows in 64 bits
  *   workspace  mesa_rmsnorm_bwd_workspace_bytes(R, D) bytes
  * Sizes and types as in mesa_rmsnorm.  Outputs and workspace may not overlap
  * inputs or one another but as said (MESA_ERR_INVALID_ARG). */
@@ -643,7 +645,8 @@ mesa_status mesa_rmsnorm_bwd(int32_t R, int32_t D, mesa_dtype dtype, mesa_dtype 
  *                    call that continued the sequence; added to the raw rows
  *                    they are copies of
  *   dq_raw, dk_raw   [B, H, T, d] dtype out
- *   dw_q, dw_k       [H, d, window] fp32 out, summed in a fixed order
+ *   dw_q, dw_k       [H, d, window] fp32 out, summed in a fixed order, over more
+ *                    than 32 tokens in 64 bits
  *   dq_hist, dk_hist [B, H, window-1, d] dtype out or NULL
  *   workspace        mesa_qk_preprocess_bwd_workspace_bytes(...) bytes
  * Sizes as in mesa_qk_preprocess, B >= 1, T <= 2^30.  Outputs and workspace

@@ -7,7 +7,7 @@
 // in registers, walks the states again from the forward's kept state before
 // its chunk (they need no other tile), joins its adjoints with the tiles behind
 // it, and writes dx, dga and dgi.  Bound by HBM with the vector units three quarters
-// busy: 191 to 208 us at B=8, T=4096, D=2048, bf16, 1.01 GB at 4.9 to 5.3 TB/s.
+// busy: 187 to 213 us at B=8, T=4096, D=2048, bf16, 1.01 GB at 4.7 to 5.4 TB/s.
 #include <algorithm>
 
 #include "mesa_common.h"

@@ -14,8 +14,9 @@
 // done twice.  Loads run one block of tokens ahead.  dw is summed per lane over its
 // at most 29 to 32 tokens in fp32, per workgroup through LDS and over workgroups by a
 // second kernel in 64 bits (in fp32 the error grew with the sequences: 480 half
-// steps over 2^15 equal ones at d=16), all in a fixed order.  At B=8, H=16, T=4096, d=128, W=4, bf16: 222 us, 1.19 GB at 5.4 TB/s, of
-// which 0.11 GB are rows that two groups read.
+// steps over 2^15 equal ones at d=16), all in a fixed order.  At B=8, H=16, T=4096,
+// d=128, W=4, bf16: 222 us, 1.19 GB at 5.4 TB/s, of which 0.11 GB are rows that two
+// groups read.
 #include "mesa_common.h"
 #include "mesa_kernels.h"
 #include "mesa_prep_rows.h"
