@@ -47,6 +47,31 @@ def test_norm_weight_gradient_over_many_equal_rows(R, D, dtype, res):
     assert ((dw - want).abs() <= bound).all(), float(((dw - want).abs() / want.abs()).max() / E)
 
 
+@pytest.mark.parametrize("dtype,res", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("R,D", [(600_001, 5), (1_048_577, 16), (540_675, 130), (270_337, 301), (131_073, 1001), (131_071, 2048),
+                                 (32_769, 2501), (65_537, 4104), (33_793, 9001), (65_535, 8200)])
+def test_norm_weight_gradient_over_several_runs_of_rows(R, D, dtype, res):
+    """Random rows in numbers that leave a last run short, full, or to some groups of a workgroup only, in every row
+    group and at every end of a row; the bound as above, of the terms' magnitudes."""
+    t = {"bf16": torch.bfloat16, "f32": torch.float32}
+    s, dy, w = normal(R, D, dtype=t[res], seed=1), normal(R, D, dtype=t[dtype], seed=2), 1 + 0.1 * normal(D, seed=3)
+    dres = normal(R, D, dtype=t[res], seed=4)
+    got = mesa.rmsnorm_bwd(s, w, dy, d_residual=dres, eps=1e-5)
+    want, size = torch.zeros(D, dtype=torch.float64, device="cuda"), torch.zeros(D, dtype=torch.float64, device="cuda")
+    depth = 0.5 * (min(D, 128) + 10)
+    for i in range(0, R, 1 << 15):
+        sd, d = s[i:i + (1 << 15)].double(), dy[i:i + (1 << 15)].double()
+        r = 1 / torch.sqrt(sd.square().mean(1, keepdim=True) + 1e-5)
+        n, g = sd * r, d * w.double()
+        want += (d * n).sum(0)
+        size += (d * n).abs().sum(0)
+        ds = r * (g - n * (g * n).mean(1, keepdim=True)) + dres[i:i + (1 << 15)].double()
+        mag = r * (g.abs() + n.abs() * (g * n).abs().mean(1, keepdim=True))
+        half = 2.0 ** -8 if res == "bf16" else E
+        assert ((got["ds"][i:i + (1 << 15)].double() - ds).abs() <= (3 * depth + 12) * E * mag + (half + 2 * E) * ds.abs()).all(), i
+    assert ((got["dw"].double() - want).abs() <= (64 + depth + 8) * E * size).all()
+
+
 @pytest.mark.parametrize("T,n", [(6, 1 << 18), (30, 1 << 17), (64, 1 << 16), (200, 1 << 14)])
 def test_decay_parameter_gradient_over_many_equal_sequences(T, n):
     """Copies of one sequence: a power of two times its gradient, bit for bit."""
