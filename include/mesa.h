@@ -519,8 +519,8 @@ mesa_status mesa_qk_preprocess(int32_t B, int32_t H, int32_t T, int32_t d, int32
  * Outputs and workspace may not overlap inputs or one another but as said
  * (MESA_ERR_INVALID_ARG): h_final may be h0, dh0 may be d_hfinal.  Rows at one
  * token stride (x, ga, gi, dx, dga, dgi in one wider tensor) may interleave;
- * each of these still starts at a multiple of 16 bytes.  Two calls may not use one workspace at
- * the same time. */
+ * each of these still starts at a multiple of 16 bytes.  Two calls may not use
+ * one workspace at the same time. */
 typedef struct {
   int32_t B, T, D;   /* sequences, tokens per (padded) sequence, channels             */
   int32_t ld;        /* elements from one token of x, ga, gi to the next (>= D)       */

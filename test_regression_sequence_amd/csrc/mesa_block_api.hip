@@ -128,7 +128,8 @@ mesa_status mesa_lru_fwd(const mesa_lru_desc* d, const void* x, const void* ga, 
                       {lengths, (size_t)d->B * 4}};
   const Span outs[] = {lru_rows(d, y, d->D), {workspace, need}, {h_final, state}}, start{h0, state};
   // h_final may be h0, and nothing else may lie over h0
-  if (overlap(outs, ins) || overlap(outs) || overlap({outs[0], outs[1]}, {start}) || (h_final != h0 && overlap({outs[2]}, {start})))
+  if (overlap(outs, ins) || overlap(outs) || overlap({outs[0], outs[1]}, {start}) ||
+      (h_final != h0 && overlap({outs[2]}, {start})))
     return MESA_ERR_INVALID_ARG;
   mesa::LruParams p = lru_params(d, x, ga, gi, lam, h0, lengths, workspace);
   p.y = y; p.h_final = h_final;
