@@ -41,8 +41,8 @@
  *     beta >= 0, lambda > 0, finite inputs, symmetric h0 / h_state.
  *   - An output buffer may not overlap another output or an input, except
  *     where a call updates a state in place (the decode steps) or says
- *     otherwise.  Only the preprocessing calls and those of the recurrence and
- *     the norm check this (MESA_ERR_INVALID_ARG).
+ *     otherwise.  Only the preprocessing calls and those of the recurrence,
+ *     the norm, the delta rule and clipping check this (MESA_ERR_INVALID_ARG).
  *   - Tensors are dense and row-major with the last index fastest.  States are
  *     [.., dk, dk] for H and [.., dv, dk] for G (row = value dimension).
  *   - Supported sizes: dk == dv; dk in {16, 32, 64, 128} for MESA_F32 inputs
@@ -663,6 +663,141 @@ mesa_status mesa_qk_preprocess_bwd(int32_t B, int32_t H, int32_t T, int32_t d, i
                                    void* dq_raw, void* dk_raw, float* dw_q, float* dw_k,
                                    void* dq_hist, void* dk_hist,
                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---- gated delta rule --------------------------------------------------------------
+ *
+ * MesaNet page, technical summary, "Mesa layer" (the contrast with one gradient
+ * step a token) and "results" (Gated DeltaNet among the baselines): the rule that
+ * takes one step on the layer's objective where the layer solves it.  From the
+ * layer's q, k, v, gamma and beta, head by head,
+ *
+ *   w_t = v_t - gamma_t S_{t-1} k_t
+ *   S_t = gamma_t S_{t-1} + beta_t w_t k_t^T,     o_t = S_t q_t      (S: dv x dk)
+ *
+ *   q, k      [B, Hk, T, dk] dtype, v, o [B, H, T, dv] dtype; head h of v, o and the
+ *             gates uses the queries and keys of head h / (H / Hk)
+ *   gamma, beta [B, H, T]    fp32: forget factor in (0, 1] and write strength
+ *   s0        [B, H, dv, dk] fp32 or NULL   state before token 0 (NULL = 0), dense
+ *   lengths   [B] int32 or NULL   valid tokens of each sequence (device memory;
+ *             values outside 0..T count as 0 or T).  Rows and gates at and behind
+ *             a length are not used (they may hold anything, NaN included); their
+ *             outputs and gradients are written as zeros.  NULL: all T
+ *   s_final   [B, H, dv, dk] fp32 or NULL   out: the state behind the last valid
+ *             token (s0 for a length of 0); the next call's s0 and a state of
+ *             mesa_delta_step.  May be s0 itself
+ *   keep_states  1: the workspace is mesa_delta_workspace_bytes(d, 1) bytes and on
+ *             return holds what mesa_delta_bwd can take over; 0: (d, 0) bytes
+ *
+ * Vectors lie densely along dk or dv; mesa_rows gives the elements from one
+ * sequence, head and token to the next, so [B, H, T, d] and [B, T, H, d] tensors and
+ * slices of wider ones are taken as they are.  Strides are not negative; those of q,
+ * k, v, o and their gradients are multiples of 16 bytes (one of a size of 1 does not
+ * matter), gates and their gradients are aligned to 4 bytes, and no two rows of an
+ * output share memory.
+ *
+ * States, gates and sums are fp32.  Products that a state, s_final or an fp32 result
+ * depends on keep fp32's precision (operands in three bf16 parts); a bf16 o is
+ * rounded once, from operands of 16 bits and more.  Every sum is formed in a fixed
+ * order: equal inputs give bitwise equal results.  Valid rows are finite (not
+ * checked): an infinity or NaN in one leaves that head of that sequence unspecified
+ * from the start of the 64 tokens around it, and no other.
+ * Supported: dk in {32, 64, 128}, dv a multiple of 16 up to 1024, H a multiple of
+ * Hk, B H max(ceil(T/64), ceil(dv/64)) <= 2^22.
+ * Outputs and workspace may not overlap inputs or one another but as said
+ * (MESA_ERR_INVALID_ARG); token rows of several outputs may interleave in one wider
+ * tensor.  Two calls may not use one workspace at the same time. */
+typedef struct {
+  int64_t b, h, t;        /* elements from one sequence, head, token to the next     */
+} mesa_rows;
+
+typedef struct {
+  int32_t B, H, Hk, T;    /* sequences, value heads, key heads, tokens               */
+  int32_t dk, dv;
+  mesa_dtype dtype;       /* of q, k, v, o and their gradients                       */
+  mesa_rows q, k, v, o;
+  mesa_rows gamma, beta;
+} mesa_delta_desc;
+
+/* Scratch bytes of mesa_delta_fwd (keep_states 0), or of a forward that leaves its
+ * states and of mesa_delta_bwd (1); 0 for an invalid or unsupported descriptor and
+ * for T == 0. */
+size_t mesa_delta_workspace_bytes(const mesa_delta_desc* d, int32_t keep_states);
+
+mesa_status mesa_delta_fwd(const mesa_delta_desc* d, const void* q, const void* k, const void* v,
+                           const float* gamma, const float* beta, const float* s0,
+                           const int32_t* lengths, void* o, float* s_final, int32_t keep_states,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of L = sum_t <d_o_t, o_t> + <d_sfinal, s_final> of a mesa_delta_fwd
+ * call.  With N_t the gradient at S_t,
+ *   dq_t = S_t^T d_o_t,   N_t = d_o_t q_t^T + gamma_{t+1} (N_{t+1} - dw_{t+1} k_{t+1}^T),
+ *   dw_t = beta_t N_t k_t = dv_t,   dbeta_t = <N_t k_t, w_t>,
+ *   dk_t = beta_t N_t^T w_t - gamma_t S_{t-1}^T dw_t,
+ *   dgamma_t = <N_t - dw_t k_t^T, S_{t-1}>,   ds0 = gamma_0 (N_0 - dw_0 k_0^T);
+ * dq and dk are summed over the value heads that share them.
+ *
+ *   d .. lengths  the forward's (d->o is not used)
+ *   rows          the strides of d_o and of the gradients
+ *   d_o           [B, H, T, dv] dtype
+ *   d_sfinal      [B, H, dv, dk] fp32 or NULL (zero)
+ *   dq, dk [B, Hk, T, dk], dv [B, H, T, dv]  dtype out
+ *   dgamma, dbeta [B, H, T] fp32 out.  dgamma is formed as the gradient at
+ *                 log gamma over gamma: gamma > 0
+ *   ds0           [B, H, dv, dk] fp32 out or NULL.  May be d_sfinal itself
+ *   states_in_workspace  1: the forward ran with keep_states = 1 and this same
+ *                 workspace, descriptor and inputs, and nothing else used the workspace
+ *                 since; 0: the states are formed again
+ *   workspace     mesa_delta_workspace_bytes(d, 1) bytes */
+typedef struct {
+  mesa_rows d_o, dq, dk, dv, dgamma, dbeta;
+} mesa_delta_grad_rows;
+
+mesa_status mesa_delta_bwd(const mesa_delta_desc* d, const mesa_delta_grad_rows* rows,
+                           const void* q, const void* k, const void* v,
+                           const float* gamma, const float* beta, const float* s0,
+                           const int32_t* lengths, const void* d_o, const float* d_sfinal,
+                           void* dq, void* dk, void* dv, float* dgamma, float* dbeta, float* ds0,
+                           int32_t states_in_workspace, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
+/* One token of d->B sequences (d->T is 1; token strides are not used): s_state
+ * [B, H, dv, dk] fp32 dense, in/out.  Every value is formed in fp32. */
+mesa_status mesa_delta_step(const mesa_delta_desc* d, const void* q, const void* k, const void* v,
+                            const float* gamma, const float* beta, float* s_state, void* o,
+                            hipStream_t stream);
+
+/* ---- global gradient norm and clipping -----------------------------------------------
+ *
+ * MesaNet page, "results" section (the models are trained end to end): between the
+ * backward passes and the optimiser's step, over all gradients g_0 .. g_{count-1},
+ *
+ *   norm = sqrt(sum_i sum g_i^2),   scale = min(1, max_norm / (norm + eps)),
+ *   out_i = scale g_i
+ *
+ *   grads, outs   host arrays of `count` device pointers, aligned to their element
+ *                 size; outs[i] may be grads[i] (then nothing is written where scale
+ *                 is 1), and otherwise overlaps no gradient and no other output
+ *   sizes         host array: elements of each (0: the pointers are not used)
+ *   dtypes        host array: MESA_F32 or MESA_BF16, of a gradient and its output
+ *   max_norm      >= 0 (infinity: no bound);  eps  >= 2^-126, finite
+ *   norm, scale   device, one fp32 each, out; scale may be NULL
+ *   workspace     mesa_grad_clip_workspace_bytes() bytes
+ *
+ * Squares and sums are 64-bit, in a fixed order: equal inputs give bitwise equal
+ * results.  g scale is fp32, rounded once to g's type.  A NaN makes norm, scale and
+ * every output NaN; an infinite gradient gives an infinite norm and a scale of 0.
+ * The host arrays are read before the call returns.  Supported: count <= 4096, 2^44
+ * elements in all.  mesa_grad_norm writes the norm alone. */
+size_t mesa_grad_clip_workspace_bytes(void);
+
+mesa_status mesa_grad_norm(int32_t count, const void* const* grads, const int64_t* sizes,
+                           const mesa_dtype* dtypes, float* norm, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
+mesa_status mesa_grad_clip(int32_t count, const void* const* grads, void* const* outs,
+                           const int64_t* sizes, const mesa_dtype* dtypes, float max_norm, float eps,
+                           float* norm, float* scale, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
 
 /* Static text for a status code. */
 const char* mesa_status_string(mesa_status s);

@@ -1,0 +1,74 @@
+// Parameters and launches of the gated delta rule.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace mesa {
+
+constexpr int kDeltaChunk = 64;  // tokens that are taken together
+
+// Vectors of B x heads x T tokens; strides in elements, the last index contiguous.
+struct DeltaRows {
+  void* at;
+  int64_t b, h, t;
+};
+
+// A number for each of B x heads x T tokens.
+struct DeltaGate {
+  float* at;
+  int64_t b, h, t;
+};
+
+// What every kernel needs of a chunk's gates.
+struct DeltaGates {
+  double g[kDeltaChunk];    // log2 of the product of the chunk's forget factors up to and with token t
+  float c[kDeltaChunk];     // that product
+  float tail[kDeltaChunk];  // the product of those behind token t
+  float beta[kDeltaChunk];  // 0 behind the sequence
+};
+
+// Floats of the 10 lower triangular 16x16 blocks of a chunk's 64x64 inverse.
+constexpr int kDeltaInverse = 10 * 256;
+
+struct DeltaParams {
+  DeltaRows q, k, v, o;             // o.at null: the states alone
+  DeltaGate gamma, beta;
+  const float *s0;                  // [B, H, dv, dk] or null
+  float* s_final;                   // [B, H, dv, dk] or null
+  const int32_t* lengths;           // [B] or null
+  int B, H, Hk, T, dk, dv, NC;      // NC chunks a (padded) sequence
+  DeltaGates* gates;                // [B H, NC]
+  float* inverse;                   // [B H, NC, kDeltaInverse]
+  float* states;                    // [B H, NC, dv, dk] before each chunk, or null
+  float* w;                         // [B H, NC, 64, dv]: v_t - gamma_t S_{t-1} k_t, or null
+  // backward
+  DeltaRows d_o, dq, dk_, dv_;
+  DeltaGate dgamma, dbeta;
+  const float* d_sfinal;
+  float* ds0;
+  float* inverse_t;                 // [B H, NC, kDeltaInverse]
+  float* dstates;                   // [B H, NC, dv, dk]: the gradient behind each chunk
+  float* e;                         // [B H, NC, 64, dv]: dv_t / beta_t
+  float *dq_heads, *dk_heads;       // [B, H, T, dk] where heads share keys
+};
+
+// Each returns hipSuccess or the launch error.
+// Gates and inverses of every chunk; `transposed`: the backward pass's inverses.
+hipError_t launch_delta_chunks(bool bf16, bool transposed, const DeltaParams& p, hipStream_t s);
+hipError_t launch_delta_scan(bool bf16, const DeltaParams& p, hipStream_t s);
+hipError_t launch_delta_adjoint(bool bf16, const DeltaParams& p, hipStream_t s);
+hipError_t launch_delta_grads(bool bf16, const DeltaParams& p, hipStream_t s);
+
+struct DeltaStepParams {
+  const void *q, *k, *v;
+  int64_t qn, qh, kn, kh, vn, vh, gn, gh, bn, bh, on, oh;  // strides of a sequence and of a head (elements)
+  const float *gamma, *beta;
+  float* state;
+  void* o;
+  int N, H, Hk, dk, dv;
+};
+hipError_t launch_delta_step(bool bf16, const DeltaStepParams& p, hipStream_t s);
+
+}  // namespace mesa

@@ -1,0 +1,350 @@
+// Gated delta rule, backward: the gradients of one chunk's tokens.
+//
+// With S0 the state before the chunk, dS the gradient at the state behind it, W
+// from the forward walk, U = beta W and E from the walk back,
+//     Z = lower(dO U^T D),   Y = -strict_lower(E U^T D) diag(beta on rows),
+//     dQ = c dO S0 + Z K,    dV = beta E,    dbeta = E . W,
+//     dK = tail U dS - c beta E S0 + Z^T Q + (Y + Y^T) K,
+// and the logarithm of token i's forget factor acts on every pair t >= i > j, on
+// what tokens t >= i read of S0, on what tokens j < i leave behind, and on S0 -> S'.
+//
+// One workgroup a (sequence, head, chunk): a wave owns 16 tokens and half of the
+// key dimension (and of Z and Y one), a lane one token in every result tile, so
+// that rows are scaled by lane constants and leave in pieces of 4 columns.  The first part runs over the value dimension in slices
+// of 32 (S0, dS and U through LDS, the next slice's loads in flight), the second
+// over the chunk's pairs.  What reaches the gates' fp32 gradients is multiplied in
+// three bf16 planes; Z and Y take two where dq and dk are bf16.
+#include <algorithm>
+
+#include "mesa_delta_tile.h"
+
+namespace mesa {
+
+namespace {
+
+template <int DK, bool BF16>
+struct GradLds {
+  static constexpr int NP = BF16 ? 1 : 3, NZ = BF16 ? 2 : 3;
+  static constexpr int kState = 32 * DK * 2, kU = 64 * 64, kPlane = 64 * DK * 2, kZ = 64 * 128;
+  static constexpr int kS = 0, kD = 3 * kState, kUAt = 6 * kState, kFirst = kUAt + 3 * kU;
+  static constexpr int kK = 0, kQ = NP * kPlane, kZAt = 2 * NP * kPlane, kYAt = kZAt + NZ * kZ, kSecond = kYAt + NZ * kZ;
+  static constexpr int kBytes = kFirst > kSecond ? kFirst : kSecond;
+};
+
+template <int DK, bool BF16>
+__global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
+  using L = GradLds<DK, BF16>;
+  using Out = std::conditional_t<BF16, __bf16, float>;
+  constexpr int NP = L::NP, NZ = L::NZ, MH = DK / 32, KS = DK / 32, OMAX = BF16 ? 1 : 2;
+  constexpr int kPieces = 8 * DK, NS = (kPieces + 511) / 512;  // 16-byte pieces of a state's slice
+  __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
+  __shared__ __attribute__((aligned(16))) DeltaGates gates;
+  __shared__ float cols[8][64], part[2][64], behind[2][64], dbetas[2][64], gammas[64], red[8];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int tile = wave & 3, half = wave >> 2;
+  const int64_t unit = blockIdx.x;
+  const int c = (int)(unit % p.NC), bh = (int)(unit / p.NC), b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk);
+  const int t0 = c * 64, live = min(delta_length(p, b) - t0, 64), here = min(p.T - t0, 64);
+  const int own = 16 * tile + r;  // this lane's token
+  const bool there = own < here, valid = own < live;
+  const int64_t tok = t0 + own;
+  const int64_t v_at = b * p.dv_.b + h * p.dv_.h + tok * p.dv_.t + 4 * g;
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+
+  auto put = [&](const f32x4 (&dq)[MH], const f32x4 (&dk)[MH]) {
+    if (!there) return;
+    const int at = 16 * MH * half + 4 * g;
+    if (p.dq_heads) {
+      const int64_t to = ((int64_t)bh * p.T + tok) * DK + at;
+#pragma unroll
+      for (int i = 0; i < MH; ++i) {
+        *reinterpret_cast<f32x4*>(p.dq_heads + to + 16 * i) = dq[i];
+        *reinterpret_cast<f32x4*>(p.dk_heads + to + 16 * i) = dk[i];
+      }
+    } else {
+      const int64_t q_at = b * p.dq.b + hk * p.dq.h + tok * p.dq.t + at, k_at = b * p.dk_.b + hk * p.dk_.h + tok * p.dk_.t + at;
+#pragma unroll
+      for (int i = 0; i < MH; ++i) {
+        store_out4<Out>(p.dq.at, q_at + 16 * i, dq[i]);
+        store_out4<Out>(p.dk_.at, k_at + 16 * i, dk[i]);
+      }
+    }
+  };
+
+  f32x4 aq[MH], ak[MH], ad[MH];  // dO S0, E S0, U dS: columns 16 (MH half + i) + 4 g + e
+#pragma unroll
+  for (int i = 0; i < MH; ++i) aq[i] = ak[i] = ad[i] = zero;
+  if (live <= 0) {
+    put(aq, ak);
+    if (there) {
+      for (int j = half; 16 * j < p.dv; j += 2) store_out4<Out>(p.dv_.at, v_at + 16 * j, zero);
+      if (g == 0 && half == 0) *gate_at(p.dgamma, b, h, tok) = *gate_at(p.dbeta, b, h, tok) = 0.f;
+    }
+    return;
+  }
+
+  if (tid < (int)sizeof(DeltaGates) / 16)
+    reinterpret_cast<u32x4*>(&gates)[tid] = reinterpret_cast<const u32x4*>(p.gates + unit)[tid];
+  if (tid < 64) gammas[tid] = tid < live ? *gate_at(p.gamma, b, h, t0 + tid) : 1.f;
+  cols[wave][lane] = 0.f;
+
+  const float *states = p.states + unit * p.dv * DK, *dstates = p.dstates + unit * p.dv * DK;
+  const float *ws = p.w + unit * 64 * p.dv, *es = p.e + unit * 64 * p.dv;
+  const float beta_own = valid ? *gate_at(p.beta, b, h, tok) : 0.f;
+  const float beta_w = (tid >> 3) < live ? *gate_at(p.beta, b, h, t0 + (tid >> 3)) : 0.f;
+  const int64_t do_at = b * p.d_o.b + h * p.d_o.h + tok * p.d_o.t;
+  f32x4 sl[NS], dl[NS], wl, e_own[2], w_own[2], o_own[2];
+  auto load = [&](int d0) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      const int piece = tid + 512 * n, row = piece / (DK / 4), col = piece % (DK / 4) * 4;
+      sl[n] = dl[n] = zero;
+      if (row < 32 && d0 + row < p.dv) {
+        sl[n] = *reinterpret_cast<const f32x4*>(states + (int64_t)(d0 + row) * DK + col);
+        dl[n] = *reinterpret_cast<const f32x4*>(dstates + (int64_t)(d0 + row) * DK + col);
+      }
+    }
+    const int row = tid >> 3, col = (tid & 7) * 4;
+    wl = zero;
+    if (d0 + col < p.dv) wl = *reinterpret_cast<const f32x4*>(ws + (int64_t)row * p.dv + d0 + col);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int at = d0 + 16 * n + 4 * g;
+      e_own[n] = w_own[n] = o_own[n] = zero;
+      if (at < p.dv) {
+        e_own[n] = *reinterpret_cast<const f32x4*>(es + (int64_t)own * p.dv + at);
+        w_own[n] = *reinterpret_cast<const f32x4*>(ws + (int64_t)own * p.dv + at);
+        if (valid) o_own[n] = load4<BF16>(p.d_o.at, do_at + at);
+      }
+    }
+  };
+
+  f32x4 zy[4] = {zero, zero, zero, zero};  // rows j, a lane's token t: U dO^T (half 0) or U E^T (half 1)
+  float dbeta = 0.f, along = 0.f;
+  RowLoads<DK, BF16, 512> kl, ql;
+  load(0);
+  for (int d0 = 0; d0 < p.dv; d0 += 32) {
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      const int piece = tid + 512 * n, row = piece / (DK / 4), col = piece % (DK / 4) * 4;
+      if (kPieces % 512 != 0 && row >= 32) continue;
+      bf16x4 a[3], d[3];
+      split4<3>(sl[n], a);
+      split4<3>(dl[n], d);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        *reinterpret_cast<bf16x4*>(lds + L::kS + i * L::kState + tile_at<DK>(row, 2 * col)) = a[i];
+        *reinterpret_cast<bf16x4*>(lds + L::kD + i * L::kState + tile_at<DK>(row, 2 * col)) = d[i];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) along = fmaf(sl[n][e], dl[n][e], along);
+    }
+    {
+      bf16x4 a[3];
+      split4<3>(wl * beta_w, a);
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        *reinterpret_cast<bf16x4*>(lds + L::kUAt + i * L::kU + tile_at<32>(tid >> 3, (tid & 7) * 8)) = a[i];
+    }
+    const Planes<NP> of = split8<NP>(o_own[0], o_own[1]);
+    const Planes<3> ef = split8<3>(e_own[0], e_own[1]), uf = split8<3>(w_own[0] * beta_own, w_own[1] * beta_own);
+    {
+      const f32x4 e = half ? e_own[1] : e_own[0], w = half ? w_own[1] : w_own[0];
+      const int at = d0 + 16 * half;
+      if (there && at < p.dv) store_out4<Out>(p.dv_.at, v_at + at, valid ? e * beta_own : zero);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) dbeta = fmaf(e[n], w[n], dbeta);
+    }
+    if (d0 + 32 < p.dv) {
+      load(d0 + 32);
+    } else {
+      kl.load(p.k.at, b * p.k.b + hk * p.k.h + t0 * p.k.t, p.k.t, live, DK, tid);
+      ql.load(p.q.at, b * p.q.b + hk * p.q.h + t0 * p.q.t, p.q.t, live, DK, tid);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MH; ++i) {
+      const Planes<3> s = columns_of<DK, 3>(lds + L::kS, L::kState, 0, MH * half + i, lane);
+      aq[i] = mma<2>(s, of, aq[i]);
+      ak[i] = mma<2>(s, ef, ak[i]);
+      ad[i] = mma<2>(columns_of<DK, 3>(lds + L::kD, L::kState, 0, MH * half + i, lane), uf, ad[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j <= tile) {
+        const Planes<3> u = rows_of<32, 3>(lds + L::kUAt, L::kU, 16 * j, 0, lane);
+        zy[j] = half ? mma<2>(u, ef, zy[j]) : mma<2>(u, of, zy[j]);
+      }
+  }
+
+  __syncthreads();
+  kl.store(lds + L::kK, L::kPlane, tid);
+  ql.store(lds + L::kQ, L::kPlane, tid);
+  __syncthreads();
+
+  float sum = 0.f, carry = 0.f;
+  char* const pairs = lds + (half ? L::kYAt : L::kZAt);
+  {
+    Planes<NP> f[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) f[s] = rows_of<DK, NP>(lds + (half ? L::kK : L::kQ), L::kPlane, 16 * tile, s, lane);
+    const double gt = gates.g[own];
+    const int last = own - half;  // Y has no diagonal
+    const float weight = half ? -beta_own : 1.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f32x4 x = zero;
+      if (j <= tile) {
+        f32x4 dot = zero;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+          dot = mma<2>(rows_of<DK, NP>(lds + L::kK, L::kPlane, 16 * j, s, lane), f[s], dot);
+        float before[4], run = 0.f;  // the sums of this row's pairs in front of each
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int at = 16 * j + 4 * g + e;
+          x[e] = at <= last ? zy[j][e] * decay(gt, gates.g[at]) * weight : 0.f;
+          before[e] = run;
+          run += at <= last ? x[e] * dot[e] : 0.f;
+        }
+        float front = carry;
+#pragma unroll
+        for (int n = 1; n < 4; ++n) {
+          const float of_group = __shfl_up(run, 16 * n);
+          if (g >= n) front += of_group;
+        }
+        carry += sum_lane_groups(run);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int at = 16 * j + 4 * g + e;
+          const float column = group_sum<16>(at <= own ? front + before[e] : 0.f);
+          if (r == 0) cols[wave][at] = column;
+        }
+      }
+      if (j <= (tile | 1)) {
+        bf16x4 a[NZ];
+        split4<NZ>(x, a);
+#pragma unroll
+        for (int n = 0; n < NZ; ++n)
+          *reinterpret_cast<bf16x4*>(pairs + n * L::kZ + tile_at<64>(own, 32 * j + 8 * g)) = a[n];
+      }
+    }
+  }
+  const float cc = gates.c[own], tail = gates.tail[own], cb = cc * beta_own;
+  float left = 0.f;  // what this token leaves behind the chunk
+#pragma unroll
+  for (int i = 0; i < MH; ++i) {
+    const f32x4 q = row_values<DK, NP>(lds + L::kQ, L::kPlane, 16 * tile, MH * half + i, lane);
+    const f32x4 k = row_values<DK, NP>(lds + L::kK, L::kPlane, 16 * tile, MH * half + i, lane);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sum += cc * q[e] * aq[i][e] - cb * k[e] * ak[i][e];
+      left += tail * k[e] * ad[i][e];
+    }
+    aq[i] *= cc;
+    ak[i] = tail * ad[i] - cb * ak[i];
+  }
+  sum = sum_lane_groups(sum);
+  left = sum_lane_groups(left);
+  dbeta = sum_lane_groups(dbeta);
+  along = wave_sum(along);
+  if (g == 0) {
+    part[half][own] = sum;
+    behind[half][own] = left;
+    dbetas[half][own] = dbeta;
+  }
+  if (lane == 0) red[wave] = along;
+  __syncthreads();
+
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    if (2 * s <= tile) {
+      const Planes<NZ> zf = rows_of<64, NZ>(lds + L::kZAt, L::kZ, 16 * tile, s, lane);
+      const Planes<NZ> yf = rows_of<64, NZ>(lds + L::kYAt, L::kZ, 16 * tile, s, lane);
+#pragma unroll
+      for (int i = 0; i < MH; ++i) {
+        const Planes<NP> k = columns_of<DK, NP>(lds + L::kK, L::kPlane, 32 * s, MH * half + i, lane);
+        aq[i] = mma<OMAX>(k, zf, aq[i]);
+        ak[i] = mma<OMAX>(k, yf, ak[i]);
+      }
+    }
+    if (2 * s + 1 >= tile) {
+      const Planes<NZ> zf = columns_of<64, NZ>(lds + L::kZAt, L::kZ, 32 * s, tile, lane);
+      const Planes<NZ> yf = columns_of<64, NZ>(lds + L::kYAt, L::kZ, 32 * s, tile, lane);
+#pragma unroll
+      for (int i = 0; i < MH; ++i) {
+        ak[i] = mma<OMAX>(columns_of<DK, NP>(lds + L::kQ, L::kPlane, 32 * s, MH * half + i, lane), zf, ak[i]);
+        ak[i] = mma<OMAX>(columns_of<DK, NP>(lds + L::kK, L::kPlane, 32 * s, MH * half + i, lane), yf, ak[i]);
+      }
+    }
+  }
+  if (!valid) {
+#pragma unroll
+    for (int i = 0; i < MH; ++i) aq[i] = ak[i] = zero;
+  }
+  put(aq, ak);
+
+  // the gradient at log gamma_i, each term added up where it counts and nowhere taken away again:
+  // what tokens t >= i read of S0, what tokens j < i leave behind, S0 -> S', and pairs t >= i > j
+  if (wave == 0) {
+    double x = (double)part[0][lane] + part[1][lane], y = (double)behind[0][lane] + behind[1][lane], whole = 0.0;
+#pragma unroll
+    for (int off = 1; off < 64; off *= 2) {
+      const double after = __shfl_down(x, off), before = __shfl_up(y, off);
+      if (lane + off < 64) x += after;
+      if (lane >= off) y += before;
+    }
+    y = __shfl_up(y, 1);
+    if (lane > 0) x += y;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      x += cols[n][lane];
+      whole += red[n];
+    }
+    x += gates.c[63] * whole;
+    if (lane < here) {
+      *gate_at(p.dgamma, b, h, t0 + lane) = lane < live ? (float)(x / (double)gammas[lane]) : 0.f;
+      *gate_at(p.dbeta, b, h, t0 + lane) = lane < live ? dbetas[0][lane] + dbetas[1][lane] : 0.f;
+    }
+  }
+}
+
+// Sums over the heads that share keys, in their order: 4 columns a thread.
+template <bool BF16>
+__global__ __launch_bounds__(256) void delta_heads_kernel(DeltaParams p) {
+  using Out = std::conditional_t<BF16, __bf16, float>;
+  const int64_t per = p.dk / 4, n = (int64_t)p.B * p.Hk * p.T * per;
+  for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < n; at += (int64_t)gridDim.x * 256) {
+    const int col = (int)(at % per) * 4, R = p.H / p.Hk;
+    const int64_t row = at / per, t = row % p.T, bh = row / p.T, b = bh / p.Hk, hk = bh % p.Hk;
+    f32x4 q = {0.f, 0.f, 0.f, 0.f}, k = q;
+    for (int i = 0; i < R; ++i) {
+      const int64_t from = ((b * p.H + hk * R + i) * p.T + t) * p.dk + col;
+      q += *reinterpret_cast<const f32x4*>(p.dq_heads + from);
+      k += *reinterpret_cast<const f32x4*>(p.dk_heads + from);
+    }
+    store_out4<Out>(p.dq.at, b * p.dq.b + hk * p.dq.h + t * p.dq.t + col, q);
+    store_out4<Out>(p.dk_.at, b * p.dk_.b + hk * p.dk_.h + t * p.dk_.t + col, k);
+  }
+}
+
+template <int DK, bool BF16>
+hipError_t launch(const DeltaParams& p, hipStream_t s) {
+  delta_grads_kernel<DK, BF16><<<(uint32_t)((int64_t)p.B * p.H * p.NC), 512, 0, s>>>(p);
+  if (p.dq_heads) {
+    const int64_t n = (int64_t)p.B * p.Hk * p.T * (DK / 4);
+    delta_heads_kernel<BF16><<<(uint32_t)std::min<int64_t>((n + 255) / 256, 1 << 20), 256, 0, s>>>(p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_grads(bool bf16, const DeltaParams& p, hipStream_t s) {
+  if (p.dk == 128) return bf16 ? launch<128, true>(p, s) : launch<128, false>(p, s);
+  if (p.dk == 64) return bf16 ? launch<64, true>(p, s) : launch<64, false>(p, s);
+  return bf16 ? launch<32, true>(p, s) : launch<32, false>(p, s);
+}
+
+}  // namespace mesa

@@ -20,6 +20,7 @@ __all__ = [
     "lru_workspace_bytes", "lru_fwd", "lru_bwd", "lru_step",
     "rmsnorm", "rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes",
     "qk_preprocess_bwd", "qk_preprocess_bwd_workspace_bytes",
+    "delta_workspace_bytes", "delta_fwd", "delta_bwd", "delta_step", "grad_norm", "grad_clip",
 ]
 
 MESA_F32 = 0
@@ -45,6 +46,20 @@ class FwdDesc(ctypes.Structure):
 class LruDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32), ("ld", ctypes.c_int32),
                 ("c", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("t", ctypes.c_int64)]
+
+
+class DeltaDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("Hk", ctypes.c_int32), ("T", ctypes.c_int32),
+                ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("q", Rows), ("k", Rows), ("v", Rows), ("o", Rows), ("gamma", Rows), ("beta", Rows)]
+
+
+class DeltaGradRows(ctypes.Structure):
+    _fields_ = [("d_o", Rows), ("dq", Rows), ("dk", Rows), ("dv", Rows), ("dgamma", Rows), ("dbeta", Rows)]
 
 
 def library_path() -> str:
@@ -127,6 +142,21 @@ def lib() -> ctypes.CDLL:
         L.mesa_qk_preprocess_bwd.restype = ctypes.c_int
         L.mesa_qk_preprocess_bwd.argtypes = ([I32, I32, I32, I32, I32, ctypes.c_int] + [P] * 6 + [F] + [P] * 11
                                              + [S, P])
+        D = ctypes.POINTER(DeltaDesc)
+        L.mesa_delta_workspace_bytes.restype = S
+        L.mesa_delta_workspace_bytes.argtypes = [D, I32]
+        L.mesa_delta_fwd.restype = ctypes.c_int
+        L.mesa_delta_fwd.argtypes = [D] + [P] * 9 + [I32, P, S, P]
+        L.mesa_delta_bwd.restype = ctypes.c_int
+        L.mesa_delta_bwd.argtypes = [D, ctypes.POINTER(DeltaGradRows)] + [P] * 15 + [I32, P, S, P]
+        L.mesa_delta_step.restype = ctypes.c_int
+        L.mesa_delta_step.argtypes = [D] + [P] * 8
+        L.mesa_grad_clip_workspace_bytes.restype = S
+        L.mesa_grad_clip_workspace_bytes.argtypes = []
+        L.mesa_grad_norm.restype = ctypes.c_int
+        L.mesa_grad_norm.argtypes = [I32] + [P] * 5 + [S, P]
+        L.mesa_grad_clip.restype = ctypes.c_int
+        L.mesa_grad_clip.argtypes = [I32] + [P] * 4 + [F, F] + [P] * 3 + [S, P]
         _LIB = L
     return _LIB
 
@@ -882,3 +912,197 @@ def qk_preprocess_bwd(q_raw, k_raw, w_q, w_k, d_q, d_k, *, q_hist=None, k_hist=N
             _addr(d_k_hist_out), _addr(res["dq_raw"]), _addr(res["dk_raw"]), _addr(res["dw_q"]), _addr(res["dw_k"]),
             _addr(res.get("dq_hist")), _addr(res.get("dk_hist")), _addr(workspace), wbytes)
     return res
+
+
+def _rows(t: torch.Tensor) -> Rows:
+    """The strides of [B, heads, T, d] (or [B, heads, T]) in elements."""
+    st = t.stride()
+    return Rows(st[0], st[1], st[2])
+
+
+def _delta_in(t: torch.Tensor, name: str, shape, dtype, dev):
+    """t [..., d] of this shape and type on dev, whose last index is contiguous."""
+    if tuple(t.shape) != shape:
+        raise MesaError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype is not dtype or t.device != dev:
+        raise MesaError(f"{name} must be {dtype} on {dev}, got {t.dtype} on {t.device}")
+    if t.stride(-1) != 1 and t.numel():
+        raise MesaError(f"{name} has strides {tuple(t.stride())}: the last index must be contiguous")
+
+
+def _delta_desc(q, k, v, gamma, beta, stream):
+    """(the descriptor but for o, the device, the type) of checked inputs."""
+    dev, dt = _home(q, "q", 4, stream), q.dtype
+    code = _code_of(q, "q")
+    B, Hk, T, dk = q.shape
+    if v.dim() != 4:
+        raise MesaError(f"v has shape {tuple(v.shape)}, expected 4 dimensions")
+    H, dv = v.shape[1], v.shape[3]
+    _delta_in(q, "q", (B, Hk, T, dk), dt, dev)
+    _delta_in(k, "k", (B, Hk, T, dk), dt, dev)
+    _delta_in(v, "v", (B, H, T, dv), dt, dev)
+    _delta_gate(gamma, "gamma", (B, H, T), dev)
+    _delta_gate(beta, "beta", (B, H, T), dev)
+    desc = DeltaDesc(B, H, Hk, T, dk, dv, code, _rows(q), _rows(k), _rows(v), Rows(0, 0, 0), _rows(gamma), _rows(beta))
+    return desc, dev, dt
+
+
+def _delta_gate(t: torch.Tensor, name: str, shape, dev):
+    if tuple(t.shape) != shape or t.dtype is not torch.float32 or t.device != dev:
+        raise MesaError(f"{name} must be float32 {shape} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _delta_out(out, key, like, dev, stream):
+    """out[key], checked, or a new tensor that lies in memory as `like` does (dense where that shares rows)."""
+    t = out.get(key) if out else None
+    if t is not None:
+        if like.dim() == 4:
+            _delta_in(t, key, tuple(like.shape), like.dtype, dev)
+        else:
+            _delta_gate(t, key, tuple(like.shape), dev)
+        return t
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty_like(like)
+    return torch.empty_like(like)
+
+
+def delta_workspace_bytes(q, k, v, gamma, beta, *, keep_states: bool = False) -> int:
+    """Scratch bytes of delta_fwd for these inputs or, with keep_states, of a forward
+    that leaves its states and of delta_bwd."""
+    desc, _, _ = _delta_desc(q, k, v, gamma, beta, None)
+    return lib().mesa_delta_workspace_bytes(ctypes.byref(desc), 1 if keep_states else 0)
+
+
+def delta_fwd(q, k, v, gamma, beta, *, s0=None, lengths=None, return_state: bool = False, keep_states: bool = False,
+              out=None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gated delta rule over whole sequences: S_t = gamma_t S_{t-1} + beta_t (v_t -
+    gamma_t S_{t-1} k_t) k_t^T, o_t = S_t q_t.
+
+    q, k [B, Hk, T, dk], v [B, H, T, dv] (fp32 or bf16; H a multiple of Hk), gamma, beta
+    [B, H, T] fp32: any strides whose last index (of q, k, v) is contiguous, so a
+    transposed [B, T, H, d] tensor or a slice of a wider one is taken as it is.  s0
+    [B, H, dv, dk] fp32 or None; lengths [B] int32 or None (valid tokens; outputs
+    behind them are zeros).  Returns a dict with ``o`` [B, H, T, dv] in v's dtype and
+    layout and, with return_state, ``s_final`` [B, H, dv, dk] fp32 (out["s_final"] may
+    be s0 itself).  With keep_states, ``workspace`` (delta_workspace_bytes(...,
+    keep_states=True) long) keeps the states that ``delta_bwd`` can take over."""
+    desc, dev, dt = _delta_desc(q, k, v, gamma, beta, stream)
+    f32 = torch.float32
+    state = (desc.B, desc.H, desc.dv, desc.dk)
+    _want(s0, "s0", state, f32, dev)
+    _want(lengths, "lengths", (desc.B,), torch.int32, dev)
+    if keep_states and workspace is None:
+        raise MesaError("keep_states needs a workspace")
+    res = {"o": _delta_out(out, "o", v, dev, stream)}
+    desc.o = _rows(res["o"])
+    if return_state:
+        res["s_final"] = _result(out, "s_final", state, f32, dev, stream)
+    keep = 1 if keep_states else 0
+    workspace, wbytes = _scratch(workspace, lambda: lib().mesa_delta_workspace_bytes(ctypes.byref(desc), keep), dev,
+                                 stream)
+    _launch("mesa_delta_fwd", dev, stream, ctypes.byref(desc), _addr(q), _addr(k), _addr(v), _addr(gamma), _addr(beta),
+            _addr(s0), _addr(lengths), _addr(res["o"]), _addr(res.get("s_final")), keep, _addr(workspace), wbytes)
+    return res
+
+
+def delta_bwd(q, k, v, gamma, beta, d_o, *, s0=None, lengths=None, d_sfinal=None, state_grads: bool = False, out=None,
+              workspace: Optional[torch.Tensor] = None, states_in_workspace: bool = False, stream=None) -> dict:
+    """Gradients of delta_fwd: d_o [B, H, T, dv] in v's dtype (any strides whose last
+    index is contiguous), d_sfinal [B, H, dv, dk] fp32 or None.  Returns ``dq``, ``dk``,
+    ``dv``, ``dgamma``, ``dbeta`` in the type and layout of q, k, v, gamma and beta and,
+    with state_grads, ``ds0`` [B, H, dv, dk] fp32.  ``out`` may pass result tensors
+    (slices of one wider tensor too), and d_sfinal itself as ds0.  states_in_workspace: the forward ran with keep_states and
+    ``workspace`` and left its states there, so they are not formed again."""
+    if states_in_workspace and workspace is None:
+        raise MesaError("states_in_workspace needs the forward's workspace")
+    desc, dev, dt = _delta_desc(q, k, v, gamma, beta, stream)
+    f32 = torch.float32
+    state = (desc.B, desc.H, desc.dv, desc.dk)
+    _delta_in(d_o, "d_o", tuple(v.shape), dt, dev)
+    _want(s0, "s0", state, f32, dev)
+    _want(lengths, "lengths", (desc.B,), torch.int32, dev)
+    _want(d_sfinal, "d_sfinal", state, f32, dev)
+    res = {key: _delta_out(out, key, like, dev, stream)
+           for key, like in (("dq", q), ("dk", k), ("dv", v), ("dgamma", gamma), ("dbeta", beta))}
+    if state_grads:
+        res["ds0"] = _result(out, "ds0", state, f32, dev, stream)
+    rows = DeltaGradRows(_rows(d_o), *(_rows(res[key]) for key in ("dq", "dk", "dv", "dgamma", "dbeta")))
+    workspace, wbytes = _scratch(workspace, lambda: lib().mesa_delta_workspace_bytes(ctypes.byref(desc), 1), dev, stream)
+    _launch("mesa_delta_bwd", dev, stream, ctypes.byref(desc), ctypes.byref(rows), _addr(q), _addr(k), _addr(v),
+            _addr(gamma), _addr(beta), _addr(s0), _addr(lengths), _addr(d_o), _addr(d_sfinal), _addr(res["dq"]),
+            _addr(res["dk"]), _addr(res["dv"]), _addr(res["dgamma"]), _addr(res["dbeta"]), _addr(res.get("ds0")),
+            1 if states_in_workspace else 0, _addr(workspace), wbytes)
+    return res
+
+
+def delta_step(q, k, v, gamma, beta, s_state, *, out=None, stream=None) -> dict:
+    """One token of N sequences: q, k [N, Hk, dk], v [N, H, dv] (fp32 or bf16, last index
+    contiguous), gamma, beta [N, H] fp32, s_state [N, H, dv, dk] fp32 updated in place.
+    Returns ``o`` [N, H, dv] in v's dtype."""
+    _home(q, "q", 3, stream)
+    for name, t, dims in (("k", k, 3), ("v", v, 3), ("gamma", gamma, 2), ("beta", beta, 2)):
+        if t.dim() != dims:
+            raise MesaError(f"{name} has shape {tuple(t.shape)}, expected {dims} dimensions")
+    desc, dev, dt = _delta_desc(*(t.unsqueeze(2) for t in (q, k, v, gamma, beta)), stream)
+    _want(s_state, "s_state", (desc.B, desc.H, desc.dv, desc.dk), torch.float32, dev)
+    o = _result(out, "o", v.shape, dt, dev, stream, v)
+    desc.o = Rows(o.stride(0), o.stride(1), 0)
+    _launch("mesa_delta_step", dev, stream, ctypes.byref(desc), _addr(q), _addr(k), _addr(v), _addr(gamma), _addr(beta),
+            _addr(s_state), _addr(o))
+    return {"o": o}
+
+
+_CODES = {torch.float32: MESA_F32, torch.bfloat16: MESA_BF16}
+
+
+def _clip_lists(grads, out, stream):
+    """(the device, count, and the arrays that the library takes) of checked gradients."""
+    if not grads:
+        raise MesaError("grads is empty")
+    dev = grads[0].device
+    if not grads[0].is_cuda:
+        raise MesaError("grads must be device tensors")
+    if stream is not None and stream.device != dev:
+        raise MesaError(f"the stream belongs to {stream.device}, grads are on {dev}")
+    n = len(grads)
+    codes = [_CODES.get(g.dtype) for g in grads]
+    sizes = [g.numel() for g in grads]
+    for i, g in enumerate(grads):
+        if codes[i] is None or g.device != dev or not g.is_contiguous():
+            raise MesaError(f"grads[{i}] must be dense float32 or bfloat16 on {dev}, got {g.dtype} on {g.device}")
+    at = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+    to = at
+    if out is not None and out is not grads:
+        if len(out) != n:
+            raise MesaError(f"out has {len(out)} tensors, grads {n}")
+        for i, (g, o) in enumerate(zip(grads, out)):
+            if o.dtype is not g.dtype or o.shape != g.shape or o.device != dev or not o.is_contiguous():
+                raise MesaError(f"out[{i}] must be as grads[{i}] is")
+        to = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
+    return dev, n, at, to, (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*codes)
+
+
+def grad_norm(grads, *, out=None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """``norm`` [] fp32: the 2-norm of all tensors of the list together (dense fp32 or
+    bf16, at any element's address).  ``out`` may pass the tensor for it."""
+    dev, n, at, _, sizes, codes = _clip_lists(grads, None, stream)
+    norm = _result(out, "norm", (), torch.float32, dev, stream)
+    workspace, wbytes = _scratch(workspace, lambda: lib().mesa_grad_clip_workspace_bytes(), dev, stream)
+    _launch("mesa_grad_norm", dev, stream, n, at, sizes, codes, _addr(norm), _addr(workspace), wbytes)
+    return {"norm": norm}
+
+
+def grad_clip(grads, max_norm: float, *, eps: float = 1e-6, out=None, workspace: Optional[torch.Tensor] = None,
+              stream=None) -> dict:
+    """All gradients times min(1, max_norm / (norm + eps)), norm being the 2-norm of all
+    of them together: in place, or into the tensors of ``out`` (a list; an entry may be
+    its gradient itself).  grads: a list of dense fp32 or bf16 tensors on one device, at
+    any element's address.  Returns ``norm`` and ``scale`` ([] fp32) and ``grads``, the
+    clipped tensors."""
+    dev, n, at, to, sizes, codes = _clip_lists(grads, out, stream)
+    both = _new((2,), torch.float32, dev, stream)
+    workspace, wbytes = _scratch(workspace, lambda: lib().mesa_grad_clip_workspace_bytes(), dev, stream)
+    _launch("mesa_grad_clip", dev, stream, n, at, to, sizes, codes, max_norm, eps, _addr(both), both.data_ptr() + 4,
+            _addr(workspace), wbytes)
+    return {"norm": both[0], "scale": both[1], "grads": grads if out is None else out}
