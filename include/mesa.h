@@ -702,7 +702,7 @@ mesa_status mesa_qk_preprocess_bwd(int32_t B, int32_t H, int32_t T, int32_t d, i
  * checked): an infinity or NaN in one leaves that head of that sequence unspecified
  * from the start of the 64 tokens around it, and no other.
  * Supported: dk in {32, 64, 128}, dv a multiple of 16 up to 1024, H a multiple of
- * Hk, B H max(ceil(T/64), ceil(dv/64)) <= 2^22.
+ * Hk, token strides of rows up to 2^20, B H max(ceil(T/64), ceil(dv/64)) <= 2^22.
  * Outputs and workspace may not overlap inputs or one another but as said
  * (MESA_ERR_INVALID_ARG); token rows of several outputs may interleave in one wider
  * tensor.  Two calls may not use one workspace at the same time. */

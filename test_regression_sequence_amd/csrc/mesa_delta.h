@@ -29,8 +29,9 @@ struct DeltaGates {
   float beta[kDeltaChunk];  // 0 behind the sequence
 };
 
-// Floats of the 10 lower triangular 16x16 blocks of a chunk's 64x64 inverse.
-constexpr int kDeltaInverse = 10 * 256;
+// Bytes of a chunk's two triangular 64x64 matrices as operands of the walks: the
+// inverse in three bf16 parts and the products of its queries and keys in `parts`.
+constexpr size_t delta_matrix_bytes(int parts) { return (3 + parts) * 6 * 1024; }
 
 struct DeltaParams {
   DeltaRows q, k, v, o;             // o.at null: the states alone
@@ -40,7 +41,7 @@ struct DeltaParams {
   const int32_t* lengths;           // [B] or null
   int B, H, Hk, T, dk, dv, NC;      // NC chunks a (padded) sequence
   DeltaGates* gates;                // [B H, NC]
-  float* inverse;                   // [B H, NC, kDeltaInverse]
+  char* matrices;                   // [B H, NC, delta_matrix_bytes(2 or 3)]
   float* states;                    // [B H, NC, dv, dk] before each chunk, or null
   float* w;                         // [B H, NC, 64, dv]: v_t - gamma_t S_{t-1} k_t, or null
   // backward
@@ -48,7 +49,7 @@ struct DeltaParams {
   DeltaGate dgamma, dbeta;
   const float* d_sfinal;
   float* ds0;
-  float* inverse_t;                 // [B H, NC, kDeltaInverse]
+  char* matrices_t;                 // [B H, NC, delta_matrix_bytes(3)]: the backward pass's
   float* dstates;                   // [B H, NC, dv, dk]: the gradient behind each chunk
   float* e;                         // [B H, NC, 64, dv]: dv_t / beta_t
   float *dq_heads, *dk_heads;       // [B, H, T, dk] where heads share keys
@@ -57,7 +58,8 @@ struct DeltaParams {
 // Each returns hipSuccess or the launch error.
 // Gates and inverses of every chunk; `transposed`: the backward pass's inverses.
 hipError_t launch_delta_chunks(bool bf16, bool transposed, const DeltaParams& p, hipStream_t s);
-hipError_t launch_delta_scan(bool bf16, const DeltaParams& p, hipStream_t s);
+hipError_t launch_delta_scan(const DeltaParams& p, hipStream_t s);  // bf16 rows
+hipError_t launch_delta_scan_f32(const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_adjoint(bool bf16, const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_grads(bool bf16, const DeltaParams& p, hipStream_t s);
 

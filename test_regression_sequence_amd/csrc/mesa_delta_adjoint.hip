@@ -14,24 +14,20 @@ namespace mesa {
 
 namespace {
 
-// The place of the 16x32 operand block (row tile i, inner step s) of an upper
-// triangular 64x64 matrix, 8 numbers a lane; (2, 0) and (3, 0) are zero.
-__device__ __forceinline__ constexpr int upper_block(int i, int s) { return i < 2 ? 2 * i + s : 2 + i; }
-
 template <int DK, bool BF16>
 struct AdjointLds {
-  static constexpr int NP = BF16 ? 1 : 3;
-  static constexpr int kPlane = 64 * DK * 2, kBlocks = 6 * 1024;
+  static constexpr int NP = BF16 ? 1 : 3, kBuffers = BF16 ? 2 : 1;
+  static constexpr int kPlane = 64 * DK * 2, kMatrices = (int)delta_matrix_bytes(3);
   static constexpr int kK = 0, kQ = kK + NP * kPlane, kO = kQ + NP * kPlane, kT = kO + NP * 64 * 128,
-                       kA = kT + 3 * kBlocks, kGates = kA + 3 * kBlocks, kBytes = kGates + sizeof(DeltaGates);
+                       kA = kT + 3 * kBlocksBytes, kGates = kT + kMatrices, kBuffer = kGates + sizeof(DeltaGates);
+  static constexpr int kBytes = kBuffers * kBuffer;
 };
 
 template <int DK, bool BF16>
 __global__ __launch_bounds__(256, 1) void delta_adjoint_kernel(DeltaParams p) {
   using L = AdjointLds<DK, BF16>;
   constexpr int NP = L::NP, MT = DK / 16, KS = DK / 32;
-  __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
-  const DeltaGates& gates = *reinterpret_cast<const DeltaGates*>(lds + L::kGates);
+  __shared__ __attribute__((aligned(16))) char buffers[L::kBytes];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
   int bh, slice;
   if (!delta_unit(blockIdx.x, (p.dv + 63) / 64, p.B * p.H, bh, slice)) return;
@@ -48,86 +44,40 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_kernel(DeltaParams p) {
     m[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (mine && p.d_sfinal) m[i] = *reinterpret_cast<const f32x4*>(p.d_sfinal + state_at + 16 * i + 4 * g);
   }
-  // the halves of diagonal blocks below the diagonal: tiles (1, 0) and (3, 2)
-  for (int n = 0; n < 6; ++n)
-    if (tid < 128) *reinterpret_cast<u32x4*>(lds + L::kT + n * L::kBlocks + (tid < 64 ? 2 : 5) * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
-
   RowLoads<DK, BF16, 256> kl, ql;
   RowLoads<64, BF16, 256> ol;
-  f32x4 tl[3];
-  u32x4 gl;
+  CopyLoads<L::kMatrices, 256> ml;
+  CopyLoads<sizeof(DeltaGates), 256> gl;
   auto load = [&](int c) {
     const int live = min(len - 64 * c, 64);
     const int64_t t0 = 64 * (int64_t)c, unit = (int64_t)bh * p.NC + c;
     kl.load(p.k.at, k0 + t0 * p.k.t, p.k.t, live, DK, tid);
     ql.load(p.q.at, q0 + t0 * p.q.t, p.q.t, live, DK, tid);
     ol.load(p.d_o.at, o0 + t0 * p.d_o.t, p.d_o.t, live, cols, tid);
-    const float* inv = p.inverse_t + unit * kDeltaInverse;
-#pragma unroll
-    for (int n = 0; n < 3; ++n)
-      if (tid + 256 * n < 640) tl[n] = *reinterpret_cast<const f32x4*>(inv + (tid + 256 * n) * 4);
-    if (tid < (int)sizeof(DeltaGates) / 16) gl = reinterpret_cast<const u32x4*>(p.gates + unit)[tid];
+    ml.load(p.matrices_t + unit * L::kMatrices, tid);
+    gl.load(p.gates + unit, tid);
   };
-  auto store = [&]() {
+  auto store = [&](char* lds) {
     kl.store(lds + L::kK, L::kPlane, tid);
     ql.store(lds + L::kQ, L::kPlane, tid);
     ol.store(lds + L::kO, 64 * 128, tid);
-#pragma unroll
-    for (int n = 0; n < 3; ++n)
-      if (tid + 256 * n < 640) {  // block (i, j) of the inverse is tile (j, i) of its transpose
-        const int block = wave + 4 * n, i = block >= 6 ? 3 : block >= 3 ? 2 : block >= 1 ? 1 : 0;
-        const int j = block - i * (i + 1) / 2;
-        bf16x4 t[3];
-        split4<3>(tl[n], t);
-#pragma unroll
-        for (int a = 0; a < 3; ++a)
-          *reinterpret_cast<bf16x4*>(lds + L::kT + a * L::kBlocks + upper_block(j, i >> 1) * 1024 + lane * 16 +
-                                     (i & 1) * 8) = t[a];
-      }
-    if (tid < (int)sizeof(DeltaGates) / 16) *reinterpret_cast<u32x4*>(lds + L::kGates + tid * 16) = gl;
-  };
-  auto block_of = [&](int base, int i, int s) {
-    Planes<3> f;
-#pragma unroll
-    for (int n = 0; n < 3; ++n)
-      f.p[n] = *reinterpret_cast<const bf16x8*>(lds + base + n * L::kBlocks + upper_block(i, s) * 1024 + lane * 16);
-    return f;
+    ml.store(lds + L::kT, tid);
+    gl.store(lds + L::kGates, tid);
   };
 
-  if (nc > 0) load(nc - 1);
+  if (nc > 0) {
+    load(nc - 1);
+    store(buffers + ((nc - 1) & (L::kBuffers - 1)) * L::kBuffer);
+    __syncthreads();
+  }
   for (int c = nc - 1; c >= 0; --c) {
     const int64_t unit = (int64_t)bh * p.NC + c;
-    __syncthreads();
-    store();
+    const char* lds = buffers + (c & (L::kBuffers - 1)) * L::kBuffer;
+    const DeltaGates& gates = *reinterpret_cast<const DeltaGates*>(lds + L::kGates);
     if (c > 0) load(c - 1);
-    __syncthreads();
 
-    {  // wave w: row tile w of (D Q K^T)^T, on and right of the diagonal
-      Planes<NP> kf[KS];
-#pragma unroll
-      for (int s = 0; s < KS; ++s) kf[s] = rows_of<DK, NP>(lds + L::kK, L::kPlane, 16 * wave, s, lane);
-      const double gj = gates.g[16 * wave + r];
-      for (int t = wave; t < 4; ++t) {
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-          acc = mma<2>(rows_of<DK, NP>(lds + L::kQ, L::kPlane, 16 * t, s, lane), kf[s], acc);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int at = 16 * t + 4 * g + e;
-          acc[e] = at >= 16 * wave + r ? acc[e] * decay(gates.g[at], gj) : 0.f;
-        }
-        bf16x4 a[3];
-        split4<3>(acc, a);
-#pragma unroll
-        for (int n = 0; n < 3; ++n)
-          *reinterpret_cast<bf16x4*>(lds + L::kA + n * L::kBlocks + upper_block(wave, t >> 1) * 1024 + lane * 16 +
-                                     (t & 1) * 8) = a[n];
-      }
-    }
-
-    f32x4 x[4];  // tail K N
     if (mine) {
+      f32x4 x[4];  // tail K N
       float* to = p.dstates + unit * p.dv * DK + (int64_t)col * DK + 4 * g;
 #pragma unroll
       for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i) = m[i];
@@ -142,23 +92,20 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_kernel(DeltaParams p) {
           acc = mma<2>(rows_of<DK, NP>(lds + L::kK, L::kPlane, 16 * i, s, lane), mp[s], acc);
         x[i] = acc * *reinterpret_cast<const f32x4*>(&gates.tail[16 * i + 4 * g]);
       }
-    }
-    __syncthreads();
-    if (mine) {
       Planes<NP> of[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) of[s] = columns_of<64, NP>(lds + L::kO, 64 * 128, 32 * s, wave, lane);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int s = i / 2; s < 2; ++s) x[i] = mma<2>(block_of(L::kA, i, s), of[s], x[i]);
+        for (int s = i / 2; s < 2; ++s) x[i] = mma<2>(block_of<3>(lds + L::kA, upper_block(i, s), lane), of[s], x[i]);
       const Planes<3> px[2] = {split8<3>(x[0], x[1]), split8<3>(x[2], x[3])};
       f32x4 y[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = i / 2; s < 2; ++s) acc = mma<2>(block_of(L::kT, i, s), px[s], acc);
+        for (int s = i / 2; s < 2; ++s) acc = mma<2>(block_of<3>(lds + L::kT, upper_block(i, s), lane), px[s], acc);
         x[i] = acc;
       }
       float* e_to = p.e + (unit * 64 + 4 * g) * p.dv + col;
@@ -185,6 +132,9 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_kernel(DeltaParams p) {
         }
       }
     }
+    if (L::kBuffers == 1) __syncthreads();
+    if (c > 0) store(buffers + ((c - 1) & (L::kBuffers - 1)) * L::kBuffer);
+    __syncthreads();
   }
 
   if (mine && p.ds0) {

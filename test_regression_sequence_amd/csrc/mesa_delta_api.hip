@@ -65,7 +65,7 @@ bool floats_aligned(const float* const (&ptrs)[N]) {
   return true;
 }
 
-constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxStride = (int64_t)1 << 40, kMaxTokenStride = 1 << 20;
 
 bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
 bool strides_ok(const mesa_rows& r) { return stride_ok(r.b) && stride_ok(r.h) && stride_ok(r.t); }
@@ -85,6 +85,9 @@ mesa_status check_delta(const mesa_delta_desc* d) {
   for (const mesa_rows* r : {&d->q, &d->k, &d->v, &d->o, &d->gamma, &d->beta})
     if (!strides_ok(*r)) return MESA_ERR_INVALID_ARG;
   if ((d->dk != 32 && d->dk != 64 && d->dk != 128) || d->dv % 16 != 0 || d->dv > 1024) return MESA_ERR_UNSUPPORTED;
+  // offsets within a chunk of tokens have 32 bits
+  for (const mesa_rows* r : {&d->q, &d->k, &d->v, &d->o})
+    if (d->T > 1 && r->t > kMaxTokenStride) return MESA_ERR_UNSUPPORTED;
   // launches of at most 2^32 threads
   if ((double)d->B * d->H * std::max(chunks_of(d), (d->dv + 63) / 64) > (double)(1 << 22)) return MESA_ERR_UNSUPPORTED;
   return MESA_OK;
@@ -106,11 +109,11 @@ size_t carve(const mesa_delta_desc* d, bool keep, void* workspace, DeltaParams& 
   Carve w{static_cast<char*>(workspace)};
   const size_t units = (size_t)d->B * d->H * chunks_of(d), state = (size_t)d->dv * d->dk * 4;
   p.gates = w.take<DeltaGates>(units * sizeof(DeltaGates));
-  p.inverse = w.take<float>(units * kDeltaInverse * 4);
+  p.matrices = w.take<char>(units * delta_matrix_bytes(d->dtype == MESA_BF16 ? 2 : 3));
   if (keep) {
     p.states = w.take<float>(units * state);
     p.w = w.take<float>(units * kDeltaChunk * d->dv * 4);
-    p.inverse_t = w.take<float>(units * kDeltaInverse * 4);
+    p.matrices_t = w.take<char>(units * delta_matrix_bytes(3));
     p.dstates = w.take<float>(units * state);
     p.e = w.take<float>(units * kDeltaChunk * d->dv * 4);
     if (d->H != d->Hk) {
@@ -133,6 +136,10 @@ DeltaParams delta_params(const mesa_delta_desc* d, const void* q, const void* k,
   p.beta = gate(beta, d->beta); p.s0 = s0; p.lengths = lengths;
   p.B = d->B; p.H = d->H; p.Hk = d->Hk; p.T = d->T; p.dk = d->dk; p.dv = d->dv; p.NC = chunks_of(d);
   return p;
+}
+
+hipError_t scan(bool bf16, const DeltaParams& p, hipStream_t s) {
+  return bf16 ? launch_delta_scan(p, s) : launch_delta_scan_f32(p, s);
 }
 
 mesa_status launched(hipError_t e) { return e == hipSuccess ? MESA_OK : MESA_ERR_HIP; }
@@ -176,7 +183,7 @@ mesa_status mesa_delta_fwd(const mesa_delta_desc* d, const void* q, const void* 
   const bool bf16 = d->dtype == MESA_BF16;
   if (d->T > 0 && launch_delta_chunks(bf16, false, p, stream) != hipSuccess) return MESA_ERR_HIP;
   if (d->T == 0) p.o.at = nullptr;
-  return launched(launch_delta_scan(bf16, p, stream));
+  return launched(scan(bf16, p, stream));
 }
 
 mesa_status mesa_delta_bwd(const mesa_delta_desc* d, const mesa_delta_grad_rows* gr, const void* q, const void* k,
@@ -189,6 +196,8 @@ mesa_status mesa_delta_bwd(const mesa_delta_desc* d, const mesa_delta_grad_rows*
   if (!gr || (states_in_workspace != 0 && states_in_workspace != 1)) return MESA_ERR_INVALID_ARG;
   for (const mesa_rows* r : {&gr->d_o, &gr->dq, &gr->dk, &gr->dv, &gr->dgamma, &gr->dbeta})
     if (!strides_ok(*r)) return MESA_ERR_INVALID_ARG;
+  for (const mesa_rows* r : {&gr->d_o, &gr->dq, &gr->dk, &gr->dv})
+    if (d->T > 1 && r->t > kMaxTokenStride) return MESA_ERR_UNSUPPORTED;
   if (d->T > 0 && (!q || !k || !v || !gamma || !beta || !d_o || !dq || !dk || !dv || !dgamma || !dbeta))
     return MESA_ERR_INVALID_ARG;
   if (!apart(d, d->Hk, d->dk, gr->dq) || !apart(d, d->Hk, d->dk, gr->dk) || !apart(d, d->H, d->dv, gr->dv) ||
@@ -219,9 +228,13 @@ mesa_status mesa_delta_bwd(const mesa_delta_desc* d, const mesa_delta_grad_rows*
   carve(d, true, workspace, p);
   const bool bf16 = d->dtype == MESA_BF16;
   if (d->T > 0) {
-    if (!states_in_workspace && (launch_delta_chunks(bf16, false, p, stream) != hipSuccess ||
-                                 launch_delta_scan(bf16, p, stream) != hipSuccess))
-      return MESA_ERR_HIP;
+    if (!states_in_workspace) {
+      DeltaParams states = p;  // (no outputs: queries are not needed)
+      states.q.at = nullptr;
+      if (launch_delta_chunks(bf16, false, states, stream) != hipSuccess ||
+          scan(bf16, states, stream) != hipSuccess)
+        return MESA_ERR_HIP;
+    }
     if (launch_delta_chunks(bf16, true, p, stream) != hipSuccess) return MESA_ERR_HIP;
   }
   p.d_o = rows(d_o, gr->d_o); p.dq = rows(dq, gr->dq); p.dk_ = rows(dk, gr->dk); p.dv_ = rows(dv, gr->dv);

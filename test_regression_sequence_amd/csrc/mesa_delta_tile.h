@@ -25,16 +25,25 @@ struct Planes {
   bf16x8 p[N];
 };
 
-// The planes of x: each takes what the ones before left.
+// The planes of x: each takes what the ones before left.  (Two numbers a conversion.)
 template <int N>
 __device__ __forceinline__ void split4(f32x4 x, bf16x4 (&p)[N]) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-  for (int n = 0; n < N; ++n)
+  for (int n = 0; n < N; ++n) {
+    u32x2 w;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      p[n][e] = (__bf16)x[e];
-      if (n + 1 < N) x[e] -= (float)p[n][e];
+    for (int e = 0; e < 2; ++e) {
+      w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x[2 * e], x[2 * e + 1]}, bf16x2));
+      if (n + 1 < N) {
+        x[2 * e] -= __uint_as_float(w[e] << 16);
+        x[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
+      }
     }
+    p[n] = __builtin_bit_cast(bf16x4, w);
+  }
 }
 
 __device__ __forceinline__ bf16x8 join(bf16x4 lo, bf16x4 hi) {
@@ -62,12 +71,54 @@ __device__ __forceinline__ f32x4 mma(const Planes<NA>& a, const Planes<NB>& b, f
   return c;
 }
 
-// Byte of a row-major bf16 tile of W columns, in units of 32 bytes that are
-// exchanged from row to row so that 16 rows' equal columns lie in all LDS banks.
+// The compiler moves nothing across (ON: where registers hold what that keeps alive).
+template <bool ON>
+__device__ __forceinline__ void fence() {
+  if constexpr (ON) __builtin_amdgcn_sched_barrier(0);
+}
+
+// acc[i] += a[i] b for four row tiles, their products in turn.
+template <int MAX, int NA, int NB>
+__device__ __forceinline__ void mma_tiles(const Planes<NA> (&a)[4], const Planes<NB>& b, f32x4 (&acc)[4]) {
+#pragma unroll
+  for (int sum = MAX; sum >= 0; --sum)
+#pragma unroll
+    for (int n = 0; n < NA; ++n)
+      if (sum - n >= 0 && sum - n < NB)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = mfma_bf16(a[i].p[n], b.p[sum - n], acc[i]);
+}
+
+// The same with the operands exchanged: the transposed tiles.
+template <int MAX, int NA, int NB>
+__device__ __forceinline__ void mma_tiles_t(const Planes<NA>& a, const Planes<NB> (&b)[4], f32x4 (&acc)[4]) {
+#pragma unroll
+  for (int sum = MAX; sum >= 0; --sum)
+#pragma unroll
+    for (int n = 0; n < NA; ++n)
+      if (sum - n >= 0 && sum - n < NB)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = mfma_bf16(a.p[n], b[i].p[sum - n], acc[i]);
+}
+
+// Byte of a row-major bf16 tile of W columns (a multiple of 8).  Units of 8 bytes
+// are exchanged from row to row: lanes that read equal columns of 16 rows, or 4
+// units of each of 4 rows (ds_read_b64_tr_b16), lie in different LDS banks, for 16
+// lanes over 32 banks as for 32 lanes over 64.
 template <int W>
 __device__ __forceinline__ uint32_t tile_at(int row, int byte) {
-  constexpr int kShift = W >= 128 ? 0 : W == 64 ? 1 : 2, kMask = W / 16 - 1;
-  return row * (2 * W) + ((((byte >> 5) ^ ((row >> kShift) & kMask)) << 5) | (byte & 31));
+  const int r0 = row & 1, r1 = (row >> 1) & 1, r2 = (row >> 2) & 1, r3 = (row >> 3) & 1;
+  const int swap = W >= 128 ? (r0 << 2 | r1 << 3 | r2 | r3 << 1 | r2 << 4)
+                   : W == 64 ? (r0 | r3 << 1 | (r0 ^ r2) << 2 | r1 << 3) : (r1 | r3 << 1 | (r1 ^ r2) << 2);
+  return row * (2 * W) + (((byte >> 3) ^ swap) << 3);
+}
+
+// 16 bytes from byte `byte` (a multiple of 16) of a row on.
+template <int W>
+__device__ __forceinline__ void tile_put16(char* tile, int row, int byte, u32x4 v) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  *reinterpret_cast<u32x2*>(tile + tile_at<W>(row, byte)) = u32x2{v[0], v[1]};
+  *reinterpret_cast<u32x2*>(tile + tile_at<W>(row, byte + 8)) = u32x2{v[2], v[3]};
 }
 
 // Rows row0 .. row0+15 (one a lane), columns of tiles 2 s and 2 s + 1: operand of
@@ -131,36 +182,46 @@ __device__ __forceinline__ f32x4 row_values(const char* tile, int plane, int row
   return r;
 }
 
+// A uniform address as the memory unit's descriptor: a lane's load adds its 32-bit
+// offset itself, and one from 2^31 on reads zeros and no memory.  So a tile's loads
+// are one run of instructions without a branch or a 64-bit sum, whichever rows exist;
+// with branches the compiler waited for the loads before each, four latencies a tile.
+typedef __amdgpu_buffer_rsrc_t Window;
+constexpr uint32_t kNowhere = 0x80000000u;
+__device__ __forceinline__ Window window_at(const void* at) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(at), 0, 0x7fffffff, 0x00020000);
+}
+__device__ __forceinline__ u32x4 window_load(Window w, uint32_t lane_offset, uint32_t offset) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w, lane_offset, offset, 0));
+}
+
 // 64 rows of W elements on their way from memory to an LDS tile: 16-byte pieces
 // in registers, rows at and behind `live` as zeros whatever they hold.
 template <int W, bool BF16, int THREADS>
 struct RowLoads {
-  static constexpr int kPer = BF16 ? 8 : 4;  // elements of a piece
+  static constexpr int kPer = BF16 ? 8 : 4, kSize = BF16 ? 2 : 4;  // elements of a piece, bytes of an element
   static constexpr int kPieces = 64 * W / kPer, kN = (kPieces + THREADS - 1) / THREADS;
+  static constexpr int kRows = THREADS * kPer / W;  // rows between a thread's pieces
   u32x4 r[kN];
 
-  // cols: columns that exist (the others are zeros)
+  // cols: columns that exist (the others are zeros); stride <= 2^20
   __device__ __forceinline__ void load(const void* base, int64_t row0, int64_t stride, int live, int cols, int tid) {
+    const Window from = window_at(static_cast<const char*>(base) + row0 * kSize);
+    const int row = tid / (W / kPer), col = tid % (W / kPer) * kPer;
+    const uint32_t off = (uint32_t)(row * (int)stride + col) * kSize, step = kRows * (uint32_t)stride * kSize;
+    const int rows = col < cols ? live : 0;
 #pragma unroll
-    for (int n = 0; n < kN; ++n) {
-      const int piece = tid + n * THREADS, row = piece / (W / kPer), col = piece % (W / kPer) * kPer;
-      u32x4 v = {0, 0, 0, 0};
-      if ((kPieces % THREADS == 0 || piece < kPieces) && row < live && col < cols) {
-        const int64_t at = row0 + row * stride + col;
-        v = *reinterpret_cast<const u32x4*>(static_cast<const char*>(base) + at * (BF16 ? 2 : 4));
-      }
-      r[n] = v;
-    }
+    for (int n = 0; n < kN; ++n) r[n] = window_load(from, row + n * kRows < rows ? off : kNowhere, n * step);
   }
 
   // N planes (1 for bf16, 3 for fp32)
   __device__ __forceinline__ void store(char* tile, int plane, int tid) const {
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
-      const int piece = tid + n * THREADS, row = piece / (W / kPer), col = piece % (W / kPer) * kPer;
-      if (kPieces % THREADS != 0 && piece >= kPieces) continue;
+      const int row = tid / (W / kPer) + n * kRows, col = tid % (W / kPer) * kPer;
+      if (kPieces % THREADS != 0 && row >= 64) continue;
       if constexpr (BF16) {
-        *reinterpret_cast<u32x4*>(tile + tile_at<W>(row, 2 * col)) = r[n];
+        tile_put16<W>(tile, row, 2 * col, r[n]);
       } else {
         bf16x4 p[3];
         split4<3>(__builtin_bit_cast(f32x4, r[n]), p);
@@ -171,10 +232,96 @@ struct RowLoads {
   }
 };
 
+// `BYTES` bytes on their way from memory to LDS as they are.
+template <int BYTES, int THREADS>
+struct CopyLoads {
+  static_assert(BYTES % 16 == 0, "16-byte pieces");
+  static constexpr int kPieces = BYTES / 16, kN = (kPieces + THREADS - 1) / THREADS;
+  u32x4 r[kN];
+
+  __device__ __forceinline__ void load(const void* base, int tid) {
+    const Window from = window_at(base);
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+      r[n] = window_load(from, (n + 1) * THREADS <= kPieces || tid + n * THREADS < kPieces ? (uint32_t)tid * 16 : kNowhere,
+                         n * THREADS * 16);
+  }
+  __device__ __forceinline__ void store(char* to, int tid) const {
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+      if ((n + 1) * THREADS <= kPieces || tid + n * THREADS < kPieces)
+        reinterpret_cast<u32x4*>(to + n * THREADS * 16)[tid] = r[n];
+  }
+};
+
+// A triangular 64x64 matrix as operands: six blocks of 16 rows x 32 inner indices, 8
+// numbers a lane, one after another; a plane is 6 KB.  Halves of a block beyond the
+// diagonal are zeros.
+constexpr int kBlocksBytes = 6 * 1024;
+__device__ __forceinline__ constexpr int lower_block(int i, int s) { return i < 2 ? i : 2 * i - 2 + s; }  // s <= i / 2
+__device__ __forceinline__ constexpr int upper_block(int i, int s) { return i < 2 ? 2 * i + s : 2 + i; }  // s >= i / 2
+
+template <int N>
+__device__ __forceinline__ Planes<N> block_of(const char* blocks, int block, int lane) {
+  Planes<N> f;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    f.p[n] = *reinterpret_cast<const bf16x8*>(blocks + n * kBlocksBytes + block * 1024 + lane * 16);
+  return f;
+}
+
+// acc += L b, in three pairs of blocks whose row tiles differ, each pair's loads one
+// ahead.  LOWER: L lower triangular, else upper.  SWAP: the transposed tiles.
+// `first`: the first pair, where it is loaded already.
+template <bool LOWER>
+__device__ __forceinline__ constexpr int pair_step(int n) { return LOWER ? n / 2 : (n + 1) / 2; }
+template <bool LOWER>
+__device__ __forceinline__ constexpr int pair_row(int n) { return LOWER ? (n == 0 ? 0 : 2) : (n == 2 ? 2 : 0); }
+
+template <int NA>
+struct BlockPair {
+  Planes<NA> a[2];
+};
+
+template <bool LOWER, int NA>
+__device__ __forceinline__ BlockPair<NA> pair_of(const char* blocks, int n, int lane) {
+  BlockPair<NA> f;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int i = pair_row<LOWER>(n) + e, s = pair_step<LOWER>(n);
+    f.a[e] = block_of<NA>(blocks, LOWER ? lower_block(i, s) : upper_block(i, s), lane);
+  }
+  return f;
+}
+
+template <int MAX, bool LOWER, bool SWAP, bool FENCED, int NA, int NB>
+__device__ __forceinline__ void mma_triangle(const char* blocks, BlockPair<NA> first, const Planes<NB> (&b)[2],
+                                             f32x4 (&acc)[4], int lane) {
+  BlockPair<NA> f[2];
+  f[0] = first;
+#pragma unroll
+  for (int n = 0; n < 3; ++n) {
+    if (n < 2) f[(n + 1) & 1] = pair_of<LOWER, NA>(blocks, n + 1, lane);
+    fence<FENCED>();
+#pragma unroll
+    for (int sum = MAX; sum >= 0; --sum)
+#pragma unroll
+      for (int q = 0; q < NA; ++q)
+        if (sum - q >= 0 && sum - q < NB)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bf16x8 x = f[n & 1].a[e].p[q], y = b[pair_step<LOWER>(n)].p[sum - q];
+            f32x4& to = acc[pair_row<LOWER>(n) + e];
+            to = SWAP ? mfma_bf16(y, x, to) : mfma_bf16(x, y, to);
+          }
+    fence<FENCED>();
+  }
+}
+
 // The number of valid tokens of sequence b.
 __device__ __forceinline__ int delta_length(const DeltaParams& p, int b) {
   if (!p.lengths) return p.T;
-  return min(max(p.lengths[b], 0), p.T);
+  return min(max(__builtin_amdgcn_readfirstlane(p.lengths[b]), 0), p.T);
 }
 
 // The address of token t's number.
@@ -183,7 +330,7 @@ __device__ __forceinline__ float* gate_at(const DeltaGate& x, int b, int h, int6
 }
 
 // exp2 of a difference of two logarithms that are kept in 64 bits.
-__device__ __forceinline__ float decay(double a, double b) { return exp2f((float)(a - b)); }
+__device__ __forceinline__ float decay(double a, double b) { return __builtin_amdgcn_exp2f((float)(a - b)); }
 
 // Unit `id` of `slices` workgroups for each (sequence, head): those of one head go
 // to one XCD (workgroups are handed to the 8 XCDs in turn), whose L2 they share.
