@@ -40,7 +40,7 @@ __global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
   __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
   __shared__ __attribute__((aligned(16))) DeltaGates gates;
   __shared__ float cols[8][64], part[2][64], behind[2][64], dbetas[2][64], gammas[64], red[8];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int tile = wave & 3, half = wave >> 2;
   const int64_t unit = blockIdx.x;
   const int c = (int)(unit % p.NC), bh = (int)(unit / p.NC), b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk);

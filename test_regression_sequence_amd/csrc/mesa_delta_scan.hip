@@ -13,8 +13,8 @@
 // The chain from M to the next M bounds the walk, so four more waves, one beside
 // each of the others on its SIMD, take what is not on it: they load the next
 // chunk and form o from the planes of M and U that the first four leave in LDS.
-//     first half:   chain K M, W, U            others Q M
-//     second half:  chain K^T U, planes of M   others next chunk to LDS, A U, o
+//     first half:   chain K M, W, U, half of K^T U       others Q M, the next chunk's loads
+//     second half:  chain the rest of K^T U, planes of M  others A U, next chunk to LDS, o
 #include "mesa_delta_tile.h"
 
 namespace mesa {
@@ -24,10 +24,10 @@ namespace {
 template <int DK>
 struct ScanLds {
   static constexpr int kTile = 64 * DK * 2, kMatrix = (int)delta_matrix_bytes(2), kGate = sizeof(DeltaGates);
-  static constexpr int kMPlane = DK * 32, kUPlane = 64 * 32;  // one wave's columns
+  static constexpr int kMPlane = DK * 32;  // one wave's columns
   static constexpr int kK = 0, kQ = kK + 2 * kTile, kV = kQ + kTile, kT = kV + 64 * 128, kA = kT + 3 * kBlocksBytes,
                        kGates = kA + 4 * kBlocksBytes, kM = kGates + 2 * kGate, kU = kM + 8 * kMPlane,
-                       kBytes = kU + 8 * kUPlane;
+                       kBytes = kU + 4 * 4096;
 };
 
 template <int DK, bool OUT>
@@ -35,7 +35,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
   using L = ScanLds<DK>;
   constexpr int MT = DK / 16, KS = DK / 32;
   __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
-  const int tid = threadIdx.x & 255, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x & 255, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   const bool chain = __builtin_amdgcn_readfirstlane(threadIdx.x) < 256;
   int bh, slice;
   if (!delta_unit(blockIdx.x, (p.dv + 63) / 64, p.B * p.H, bh, slice)) return;
@@ -44,7 +44,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
   const bool mine = 16 * wave < cols;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   char* const m_planes = lds + L::kM + wave * 2 * L::kMPlane + lane * 16;
-  char* const u_planes = lds + L::kU + wave * 2 * L::kUPlane + lane * 16;
+  char* const u_to = lds + L::kU + wave * 4096 + lane * 16;  // U's four tiles
 
   if (chain) {
     const int col = col0 + 16 * wave + r;  // this lane's column of the state
@@ -55,17 +55,19 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
       m[i] = zero;
       if (mine && p.s0) m[i] = *reinterpret_cast<const f32x4*>(p.s0 + state_at + 16 * i);
     }
+    const TileRows<DK> rows(lane);
+    const TileColumns<DK> columns(lane);
     Planes<3> mp[KS];
-    auto planes = [&]() {
+    auto planes = [&](int first, int last) {
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
+      for (int s = first; s < last; ++s) {
         mp[s] = split8<3>(m[2 * s], m[2 * s + 1]);
         if constexpr (OUT)
 #pragma unroll
           for (int n = 0; n < 2; ++n) *reinterpret_cast<bf16x8*>(m_planes + n * L::kMPlane + s * 1024) = mp[s].p[n];
       }
     };
-    planes();
+    planes(0, KS);
     __builtin_amdgcn_s_setprio(2);
     __syncthreads();
     for (int c = 0; c < nc; ++c) {
@@ -73,87 +75,122 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
       const DeltaGates& gates = *reinterpret_cast<const DeltaGates*>(lds + L::kGates + (c & 1) * L::kGate);
       f32x4 x[4] = {zero, zero, zero, zero}, y[4];
       Planes<3> ut[2];
+      constexpr int G = MT < 4 ? MT : 4, NG = 2 * MT / G;  // K^T in groups of 4 tiles
+      Planes<1> kt[2][4];
+      auto group = [&](int n, Planes<1> (&to)[4]) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) to[i] = columns(keys, 32 * (n * G / MT), n * G % MT + i);
+      };
+      auto mma_group = [&](int n) {
+#pragma unroll
+        for (int q = 2; q >= 0; --q)
+#pragma unroll
+          for (int i = 0; i < G; ++i)
+            m[n * G % MT + i] = mfma_bf16(kt[n & 1][i].p[0], ut[n * G / MT].p[q], m[n * G % MT + i]);
+      };
       if (mine) {
-        // operands come from LDS one step ahead of the products that take them: the
-        // fences keep their loads there
+        // Operands come from LDS one step ahead of the products that take them (the fences
+        // keep their loads there); between two fences products of one block and the
+        // conversions for the next run side by side.
         Planes<1> f[2][4];
         Planes<3> px[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[0][i] = rows_of<DK, 1>(keys, 0, 16 * i, 0, lane);
-        BlockPair<3> t;
+        for (int i = 0; i < 4; ++i) f[0][i] = rows(keys, 16 * i, 0);
+        BlockPair<3> t[2];
+        f32x4 cc[4];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {  // x = K M
           if (s + 1 < KS) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[(s + 1) & 1][i] = rows_of<DK, 1>(keys, 0, 16 * i, s + 1, lane);
+            for (int i = 0; i < 4; ++i) f[(s + 1) & 1][i] = rows(keys, 16 * i, s + 1);
           } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = column_values<64, 1>(lds + L::kV, 0, 16 * i, wave, lane);
-            t = pair_of<true, 3>(lds + L::kT, 0, lane);
+            for (int i = 0; i < 4; ++i) {
+              y[i] = column_values<64, 1>(lds + L::kV, 0, 16 * i, wave, lane);
+              cc[i] = *reinterpret_cast<const f32x4*>(&gates.c[16 * i + 4 * g]);
+            }
+            t[0] = pair_of<true, 3>(lds + L::kT, 0, lane);
           }
           fence<true>();
           mma_tiles<2>(f[s & 1], mp[s], x);
           fence<true>();
         }
         if (p.states) {
-          float* to = p.states + ((int64_t)bh * p.NC + c) * p.dv * DK + (int64_t)col * DK + 4 * g;
+          const Window to = window_at(p.states + ((int64_t)bh * p.NC + c) * p.dv * DK);
 #pragma unroll
-          for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i) = m[i];
+          for (int i = 0; i < MT; ++i) window_store(to, (col * DK + 4 * g) * 4, 64 * i, m[i]);
         }
+        t[1] = pair_of<true, 3>(lds + L::kT, 1, lane);
+        f32x4 beta[2], tail[2];
+        auto gates_of = [&](int s) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] -= *reinterpret_cast<const f32x4*>(&gates.c[16 * i + 4 * g]) * x[i];
-        px[0] = split8<3>(y[0], y[1]);
-        px[1] = split8<3>(y[2], y[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = zero;
-        mma_triangle<2, true, false, true>(lds + L::kT, t, px, x, lane);  // W
-        if (p.w) {
-          float* to = p.w + (((int64_t)bh * p.NC + c) * 64 + 4 * g) * p.dv + col;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) to[(int64_t)(16 * i + e) * p.dv] = x[i][e];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] *= *reinterpret_cast<const f32x4*>(&gates.beta[16 * i + 4 * g]);
-          y[i] = x[i] * *reinterpret_cast<const f32x4*>(&gates.tail[16 * i + 4 * g]);
-        }
-        if constexpr (OUT) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const Planes<2> u = split8<2>(x[2 * s], x[2 * s + 1]);
-#pragma unroll
-            for (int n = 0; n < 2; ++n) *reinterpret_cast<bf16x8*>(u_planes + n * L::kUPlane + s * 1024) = u.p[n];
+          for (int i = 0; i < 2; ++i) {
+            beta[i] = *reinterpret_cast<const f32x4*>(&gates.beta[32 * s + 16 * i + 4 * g]);
+            tail[i] = *reinterpret_cast<const f32x4*>(&gates.tail[32 * s + 16 * i + 4 * g]);
           }
-        }
+        };
+        auto residual = [&](int s) {  // V - c K M
 #pragma unroll
-        for (int s = 0; s < 2; ++s) ut[s] = split8<3>(y[2 * s], y[2 * s + 1]);
+          for (int i = 2 * s; i < 2 * s + 2; ++i) {
+            y[i] -= cc[i] * x[i];
+            x[i] = zero;
+          }
+          px[s] = split8<3>(y[2 * s], y[2 * s + 1]);
+        };
+        auto scaled = [&](int s) {  // W to U and tail U
+#pragma unroll
+          for (int i = 2 * s; i < 2 * s + 2; ++i) {
+            x[i] *= beta[i & 1];
+            if constexpr (OUT) *reinterpret_cast<f32x4*>(u_to + i * 1024) = x[i];
+            y[i] = x[i] * tail[i & 1];
+          }
+          ut[s] = split8<3>(y[2 * s], y[2 * s + 1]);
+        };
+        auto keep = [&](int s) {
+          if (p.w) {
+            const Window to = window_at(p.w + ((int64_t)bh * p.NC + c) * 64 * p.dv);
+#pragma unroll
+            for (int i = 2 * s; i < 2 * s + 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) window_store(to, (4 * g * p.dv + col) * 4, (16 * i + e) * p.dv * 4, x[i][e]);
+          }
+        };
+        residual(0);
+        fence<true>();
+        residual(1);
+        mma_pair<2, true, false>(0, t[0], px, x);
+        t[0] = pair_of<true, 3>(lds + L::kT, 2, lane);
+        gates_of(0);
+        group(0, kt[0]);
         const float whole = gates.c[63];
+        fence<true>();
+        keep(0);
+        scaled(0);
+        mma_pair<2, true, false>(1, t[1], px, x);
+        gates_of(1);
+        fence<true>();
+        mma_pair<2, true, false>(2, t[0], px, x);
 #pragma unroll
         for (int i = 0; i < MT; ++i) m[i] *= whole;
+#pragma unroll
+        for (int n = 0; n < NG / 2; ++n) {  // M += K^T U, the first 32 tokens
+          group(n + 1, kt[(n + 1) & 1]);
+          fence<true>();
+          mma_group(n);
+        }
+        keep(1);
+        scaled(1);
       }
       __syncthreads();
       if (mine) {
-        constexpr int G = MT < 4 ? MT : 4, NG = 2 * MT / G;  // K^T in groups of 4 tiles
-        Planes<1> kt[2][4];
-        auto group = [&](int n, Planes<1> (&to)[4]) {
 #pragma unroll
-          for (int i = 0; i < G; ++i) to[i] = columns_of<DK, 1>(keys, 0, 32 * (n * G / MT), n * G % MT + i, lane);
-        };
-        group(0, kt[0]);
-#pragma unroll
-        for (int n = 0; n < NG; ++n) {  // M += K^T U
+        for (int n = NG / 2; n < NG; ++n) {  // the other 32
           if (n + 1 < NG) group(n + 1, kt[(n + 1) & 1]);
           fence<true>();
-#pragma unroll
-          for (int q = 2; q >= 0; --q)
-#pragma unroll
-            for (int i = 0; i < G; ++i)
-              m[n * G % MT + i] = mfma_bf16(kt[n & 1][i].p[0], ut[n * G / MT].p[q], m[n * G % MT + i]);
-          fence<true>();
+          if (n == NG - 1) planes(0, KS - G / 2);
+          mma_group(n);
         }
-        planes();
+        planes(KS - G / 2, KS);
       }
       __syncthreads();
     }
@@ -166,24 +203,32 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
 
   const int hk = h / (p.H / p.Hk);
   const int64_t q0 = b * p.q.b + hk * p.q.h, k0 = b * p.k.b + hk * p.k.h, v0 = b * p.v.b + h * p.v.h + col0,
-                o0 = b * p.o.b + h * p.o.h + col0 + 16 * wave + 4 * g;
+                o0 = b * p.o.b + h * p.o.h + col0 + 16 * wave;
+  const TileRows<DK> rows(lane);
   RowLoads<DK, true, 256> kl, ql;
   RowLoads<64, true, 256> vl;
   CopyLoads<3 * kBlocksBytes, 256> tl;
   CopyLoads<2 * kBlocksBytes, 256> al;
   CopyLoads<L::kGate, 256> gl;
-  auto load = [&](int c) {
+  // part s of KS of a chunk's loads, so that they go out along the products with Q
+  auto load = [&](int c, int s) {
     const int live = min(len - 64 * c, 64);
     const int64_t t0 = 64 * (int64_t)c, unit = (int64_t)bh * p.NC + c;
     const char* matrix = p.matrices + unit * L::kMatrix;
-    kl.load(p.k.at, k0 + t0 * p.k.t, p.k.t, live, DK, tid);
-    vl.load(p.v.at, v0 + t0 * p.v.t, p.v.t, live, cols, tid);
-    tl.load(matrix, tid);
-    gl.load(p.gates + unit, tid);
-    if constexpr (OUT) {
-      ql.load(p.q.at, q0 + t0 * p.q.t, p.q.t, live, DK, tid);
-      al.load(matrix + 3 * kBlocksBytes, tid);
+    if (s == 0) kl.load(p.k.at, k0 + t0 * p.k.t, p.k.t, live, DK, tid);
+    if (OUT && s == min(1, KS - 1)) ql.load(p.q.at, q0 + t0 * p.q.t, p.q.t, live, DK, tid);
+    if (s == min(2, KS - 1)) {
+      vl.load(p.v.at, v0 + t0 * p.v.t, p.v.t, live, cols, tid);
+      tl.load(matrix, tid);
     }
+    if (s == KS - 1) {
+      if constexpr (OUT) al.load(matrix + 3 * kBlocksBytes, tid);
+      gl.load(p.gates + unit, tid);
+    }
+  };
+  auto load_all = [&](int c) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) load(c, s);
   };
   auto store = [&](int c) {
     kl.store(lds + L::kK + (c & 1) * L::kTile, 0, tid);
@@ -196,56 +241,68 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
     }
   };
   if (nc > 0) {
-    load(0);
+    load_all(0);
     store(0);
-    if (nc > 1) load(1);
   }
   __syncthreads();
+  f32x4 o[4], u[4];  // o's transpose (a lane has 4 columns of one token) and U
+  BlockPair<2> a[3];
+  auto finish = [&](int c) {  // o of chunk c: A U added to c Q M
+    const Planes<2> up[2] = {split8<2>(u[0], u[1]), split8<2>(u[2], u[3])};
+#pragma unroll
+    for (int n = 0; n < 3; ++n) mma_pair<1, true, true>(n, a[n], up, o);
+    const int live = mine ? len - 64 * c : 0;
+    const Window to = window_at(static_cast<__bf16*>(p.o.at) + o0 + 64 * (int64_t)c * p.o.t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      window_store_row<true>(to, 16 * i + r < live ? (r * (uint32_t)p.o.t + 4 * g) * 2 : kNowhere,
+                             16 * i * (uint32_t)p.o.t * 2, o[i]);
+  };
+  // Without a branch around the loads (the last chunk is loaded once more), and with
+  // products for columns that do not exist: where paths with and without loads in
+  // flight meet, the compiler waits for them.
   for (int c = 0; c < nc; ++c) {
-    f32x4 o[4] = {zero, zero, zero, zero};  // o's transpose: a lane has 4 columns of one token
-    if (OUT && mine) {
+    const int next = min(c + 1, nc - 1);
+    if constexpr (OUT) {
+      if (c > 0) finish(c - 1);
       Planes<1> f[2][4];
       Planes<2> mp[2];
       auto operands = [&](int s) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[s & 1][i] = rows_of<DK, 1>(lds + L::kQ, 0, 16 * i, s, lane);
+        for (int i = 0; i < 4; ++i) f[s & 1][i] = rows(lds + L::kQ, 16 * i, s);
 #pragma unroll
         for (int n = 0; n < 2; ++n) mp[s & 1].p[n] = *reinterpret_cast<const bf16x8*>(m_planes + n * L::kMPlane + s * 1024);
       };
       operands(0);
 #pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = zero;
+#pragma unroll
       for (int s = 0; s < KS; ++s) {
         if (s + 1 < KS) operands(s + 1);
         fence<true>();
+        load(next, s);
         mma_tiles_t<1>(mp[s & 1], f[s & 1], o);
         fence<true>();
       }
       const DeltaGates& gates = *reinterpret_cast<const DeltaGates*>(lds + L::kGates + (c & 1) * L::kGate);
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] *= gates.c[16 * i + r];
+#pragma unroll
+      for (int n = 0; n < 3; ++n) a[n] = pair_of<true, 2>(lds + L::kA + (c & 1) * 2 * kBlocksBytes, n, lane);
+    } else {
+      load_all(next);
     }
     __syncthreads();
-    if (c + 1 < nc) store(c + 1);
-    if (c + 2 < nc) load(c + 2);
-    if (OUT && mine) {
-      Planes<2> u[2];
+    if constexpr (OUT) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) u[s].p[n] = *reinterpret_cast<const bf16x8*>(u_planes + n * L::kUPlane + s * 1024);
-      const char* a = lds + L::kA + (c & 1) * 2 * kBlocksBytes;
-      mma_triangle<1, true, true, true>(a, pair_of<true, 2>(a, 0, lane), u, o, lane);
-      const int live = len - 64 * c;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = 16 * i + r;
-        if (at < live) store_out4<__bf16>(p.o.at, o0 + (64 * (int64_t)c + at) * p.o.t, o[i]);
-      }
+      for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const f32x4*>(u_to + i * 1024);
     }
+    store(c + 1);
     __syncthreads();
   }
+  if (OUT && nc > 0) finish(nc - 1);
   if (OUT && mine) {  // behind the sequence
-    for (int64_t t = len + r; t < p.T; t += 16) store_out4<__bf16>(p.o.at, o0 + t * p.o.t, zero);
+    for (int64_t t = len + r; t < p.T; t += 16) store_out4<__bf16>(p.o.at, o0 + t * p.o.t + 4 * g, zero);
   }
 }
 

@@ -23,7 +23,7 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
   using L = ScanLds<DK>;
   constexpr int NP = L::NP, NA = L::NA, MT = DK / 16, KS = DK / 32;
   __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   int bh, slice;
   if (!delta_unit(blockIdx.x, (p.dv + 63) / 64, p.B * p.H, bh, slice)) return;
   const int b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk), len = delta_length(p, b);

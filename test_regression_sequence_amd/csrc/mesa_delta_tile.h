@@ -135,6 +135,41 @@ __device__ __forceinline__ Planes<N> rows_of(const char* tile, int plane, int ro
   return r;
 }
 
+// A lane's places in a tile's first rows, computed once: the same operands as
+// rows_of and columns_of from any multiple of 16 rows on (one plane).
+template <int W>
+struct TileRows {
+  uint32_t at[W / 16];
+  __device__ __forceinline__ explicit TileRows(int lane) {
+#pragma unroll
+    for (int j = 0; j < W / 16; ++j) at[j] = tile_at<W>(lane & 15, 32 * j + 8 * (lane >> 4));
+  }
+  __device__ __forceinline__ Planes<1> operator()(const char* tile, int row0, int s) const {
+    Planes<1> r;
+    r.p[0] = join(*reinterpret_cast<const bf16x4*>(tile + at[2 * s] + row0 * 2 * W),
+                  *reinterpret_cast<const bf16x4*>(tile + at[2 * s + 1] + row0 * 2 * W));
+    return r;
+  }
+};
+template <int W>
+struct TileColumns {
+  uint32_t at[W / 16];
+  __device__ __forceinline__ explicit TileColumns(int lane) {
+#pragma unroll
+    for (int j = 0; j < W / 16; ++j) at[j] = tile_at<W>(4 * (lane >> 4) + ((lane & 15) >> 2), 32 * j + 8 * (lane & 3));
+  }
+  __device__ __forceinline__ bf16x4 four(const char* tile, int row0, int col) const {
+    const s16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4*)(const_cast<char*>(tile + at[col] + row0 * 2 * W)));
+    return __builtin_bit_cast(bf16x4, r);
+  }
+  __device__ __forceinline__ Planes<1> operator()(const char* tile, int row0, int col) const {
+    Planes<1> r;
+    r.p[0] = join(four(tile, row0, col), four(tile, row0 + 16, col));
+    return r;
+  }
+};
+
 // Rows 4 g .. 4 g + 3 behind row0, of column 16 col + lane % 16.
 template <int W>
 __device__ __forceinline__ bf16x4 column4(const char* tile, int row0, int col, int lane) {
@@ -193,6 +228,25 @@ __device__ __forceinline__ Window window_at(const void* at) {
 }
 __device__ __forceinline__ u32x4 window_load(Window w, uint32_t lane_offset, uint32_t offset) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w, lane_offset, offset, 0));
+}
+
+__device__ __forceinline__ void window_store(Window w, uint32_t lane_offset, uint32_t offset, float v) {
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), w, lane_offset, offset, 0);
+}
+__device__ __forceinline__ void window_store(Window w, uint32_t lane_offset, uint32_t offset, f32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), w, lane_offset, offset, 0);
+}
+// 4 numbers in the rows' type
+template <bool BF16>
+__device__ __forceinline__ void window_store_row(Window w, uint32_t lane_offset, uint32_t offset, f32x4 v) {
+  if constexpr (BF16) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    bf16x4 p[1];
+    split4<1>(v, p);
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, p[0]), w, lane_offset, offset, 0);
+  } else {
+    window_store(w, lane_offset, offset, v);
+  }
 }
 
 // 64 rows of W elements on their way from memory to an LDS tile: 16-byte pieces
@@ -270,9 +324,9 @@ __device__ __forceinline__ Planes<N> block_of(const char* blocks, int block, int
   return f;
 }
 
-// acc += L b, in three pairs of blocks whose row tiles differ, each pair's loads one
-// ahead.  LOWER: L lower triangular, else upper.  SWAP: the transposed tiles.
-// `first`: the first pair, where it is loaded already.
+// acc += L b goes in three pairs of blocks whose row tiles differ, each pair's loads
+// one ahead.  LOWER: L lower triangular, else upper.  SWAP: the transposed tiles.
+// `first`: the first pair, loaded before.
 template <bool LOWER>
 __device__ __forceinline__ constexpr int pair_step(int n) { return LOWER ? n / 2 : (n + 1) / 2; }
 template <bool LOWER>
@@ -294,6 +348,22 @@ __device__ __forceinline__ BlockPair<NA> pair_of(const char* blocks, int n, int 
   return f;
 }
 
+// acc += L b for pair n of L's blocks.
+template <int MAX, bool LOWER, bool SWAP, int NA, int NB>
+__device__ __forceinline__ void mma_pair(int n, const BlockPair<NA>& f, const Planes<NB> (&b)[2], f32x4 (&acc)[4]) {
+#pragma unroll
+  for (int sum = MAX; sum >= 0; --sum)
+#pragma unroll
+    for (int q = 0; q < NA; ++q)
+      if (sum - q >= 0 && sum - q < NB)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bf16x8 x = f.a[e].p[q], y = b[pair_step<LOWER>(n)].p[sum - q];
+          f32x4& to = acc[pair_row<LOWER>(n) + e];
+          to = SWAP ? mfma_bf16(y, x, to) : mfma_bf16(x, y, to);
+        }
+}
+
 template <int MAX, bool LOWER, bool SWAP, bool FENCED, int NA, int NB>
 __device__ __forceinline__ void mma_triangle(const char* blocks, BlockPair<NA> first, const Planes<NB> (&b)[2],
                                              f32x4 (&acc)[4], int lane) {
@@ -303,17 +373,7 @@ __device__ __forceinline__ void mma_triangle(const char* blocks, BlockPair<NA> f
   for (int n = 0; n < 3; ++n) {
     if (n < 2) f[(n + 1) & 1] = pair_of<LOWER, NA>(blocks, n + 1, lane);
     fence<FENCED>();
-#pragma unroll
-    for (int sum = MAX; sum >= 0; --sum)
-#pragma unroll
-      for (int q = 0; q < NA; ++q)
-        if (sum - q >= 0 && sum - q < NB)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const bf16x8 x = f[n & 1].a[e].p[q], y = b[pair_step<LOWER>(n)].p[sum - q];
-            f32x4& to = acc[pair_row<LOWER>(n) + e];
-            to = SWAP ? mfma_bf16(y, x, to) : mfma_bf16(x, y, to);
-          }
+    mma_pair<MAX, LOWER, SWAP>(n, f[n & 1], b, acc);
     fence<FENCED>();
   }
 }
