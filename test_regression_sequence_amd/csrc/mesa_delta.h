@@ -60,7 +60,8 @@ struct DeltaParams {
 hipError_t launch_delta_chunks(bool bf16, bool transposed, const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_scan(const DeltaParams& p, hipStream_t s);  // bf16 rows
 hipError_t launch_delta_scan_f32(const DeltaParams& p, hipStream_t s);
-hipError_t launch_delta_adjoint(bool bf16, const DeltaParams& p, hipStream_t s);
+hipError_t launch_delta_adjoint(const DeltaParams& p, hipStream_t s);  // bf16 rows
+hipError_t launch_delta_adjoint_f32(const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_grads(bool bf16, const DeltaParams& p, hipStream_t s);
 
 struct DeltaStepParams {

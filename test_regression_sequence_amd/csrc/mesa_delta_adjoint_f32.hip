@@ -1,0 +1,152 @@
+// Gated delta rule, backward, fp32: the walk back over a sequence's chunks.
+//
+// The walk of mesa_delta_adjoint.hip for rows that are themselves three bf16 planes: six
+// products where bf16 rows take three, and planes of keys and queries that fill the LDS
+// (161 KB at dk = 128), so the workgroup is the four waves that hold the state.
+#include "mesa_delta_tile.h"
+
+namespace mesa {
+
+namespace {
+
+template <int DK>
+struct AdjointLds {
+  static constexpr int NP = 3;
+  static constexpr int kPlane = 64 * DK * 2, kMatrices = (int)delta_matrix_bytes(3);
+  static constexpr int kK = 0, kQ = kK + NP * kPlane, kO = kQ + NP * kPlane, kT = kO + NP * 64 * 128,
+                       kA = kT + 3 * kBlocksBytes, kGates = kT + kMatrices, kBytes = kGates + sizeof(DeltaGates);
+};
+
+template <int DK>
+__global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p) {
+  using L = AdjointLds<DK>;
+  constexpr int NP = L::NP, MT = DK / 16, KS = DK / 32;
+  __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
+  int bh, slice;
+  if (!delta_unit(blockIdx.x, (p.dv + 63) / 64, p.B * p.H, bh, slice)) return;
+  const int b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk), len = delta_length(p, b);
+  const int nc = (len + 63) / 64, col0 = 64 * slice, cols = min(64, p.dv - col0);
+  const int col = col0 + 16 * wave + r;
+  const bool mine = 16 * wave < cols;
+  const int64_t state_at = ((int64_t)bh * p.dv + col) * DK;
+  const int64_t q0 = b * p.q.b + hk * p.q.h, k0 = b * p.k.b + hk * p.k.h, o0 = b * p.d_o.b + h * p.d_o.h + col0;
+
+  f32x4 m[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    m[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (mine && p.d_sfinal) m[i] = *reinterpret_cast<const f32x4*>(p.d_sfinal + state_at + 16 * i + 4 * g);
+  }
+  RowLoads<DK, false, 256> kl, ql;
+  RowLoads<64, false, 256> ol;
+  CopyLoads<L::kMatrices, 256> ml;
+  CopyLoads<sizeof(DeltaGates), 256> gl;
+  auto load = [&](int c) {
+    const int live = min(len - 64 * c, 64);
+    const int64_t t0 = 64 * (int64_t)c, unit = (int64_t)bh * p.NC + c;
+    kl.load(p.k.at, k0 + t0 * p.k.t, p.k.t, live, DK, tid);
+    ql.load(p.q.at, q0 + t0 * p.q.t, p.q.t, live, DK, tid);
+    ol.load(p.d_o.at, o0 + t0 * p.d_o.t, p.d_o.t, live, cols, tid);
+    ml.load(p.matrices_t + unit * L::kMatrices, tid);
+    gl.load(p.gates + unit, tid);
+  };
+  auto store = [&]() {
+    kl.store(lds + L::kK, L::kPlane, tid);
+    ql.store(lds + L::kQ, L::kPlane, tid);
+    ol.store(lds + L::kO, 64 * 128, tid);
+    ml.store(lds + L::kT, tid);
+    gl.store(lds + L::kGates, tid);
+  };
+
+  if (nc > 0) {
+    load(nc - 1);
+    store();
+    __syncthreads();
+  }
+  for (int c = nc - 1; c >= 0; --c) {
+    const int64_t unit = (int64_t)bh * p.NC + c;
+    const DeltaGates& gates = *reinterpret_cast<const DeltaGates*>(lds + L::kGates);
+    if (c > 0) load(c - 1);
+
+    if (mine) {
+      f32x4 x[4];  // tail K N
+      float* to = p.dstates + unit * p.dv * DK + (int64_t)col * DK + 4 * g;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i) = m[i];
+      Planes<3> mp[KS];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) mp[s] = split8<3>(m[2 * s], m[2 * s + 1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+          acc = mma<2>(rows_of<DK, NP>(lds + L::kK, L::kPlane, 16 * i, s, lane), mp[s], acc);
+        x[i] = acc * *reinterpret_cast<const f32x4*>(&gates.tail[16 * i + 4 * g]);
+      }
+      Planes<NP> of[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) of[s] = columns_of<64, NP>(lds + L::kO, 64 * 128, 32 * s, wave, lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int s = i / 2; s < 2; ++s) x[i] = mma<2>(block_of<3>(lds + L::kA, upper_block(i, s), lane), of[s], x[i]);
+      const Planes<3> px[2] = {split8<3>(x[0], x[1]), split8<3>(x[2], x[3])};
+      f32x4 y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = i / 2; s < 2; ++s) acc = mma<2>(block_of<3>(lds + L::kT, upper_block(i, s), lane), px[s], acc);
+        x[i] = acc;
+      }
+      float* e_to = p.e + (unit * 64 + 4 * g) * p.dv + col;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) e_to[(int64_t)(16 * i + e) * p.dv] = x[i][e];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 cc = *reinterpret_cast<const f32x4*>(&gates.c[16 * i + 4 * g]);
+        x[i] *= -cc * *reinterpret_cast<const f32x4*>(&gates.beta[16 * i + 4 * g]);
+        y[i] = cc * column_values<64, NP>(lds + L::kO, 64 * 128, 16 * i, wave, lane);
+      }
+      const float whole = gates.c[63];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) m[i] *= whole;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const Planes<3> ye = split8<3>(x[2 * s], x[2 * s + 1]), yo = split8<3>(y[2 * s], y[2 * s + 1]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          m[i] = mma<2>(columns_of<DK, NP>(lds + L::kQ, L::kPlane, 32 * s, i, lane), yo, m[i]);
+          m[i] = mma<2>(columns_of<DK, NP>(lds + L::kK, L::kPlane, 32 * s, i, lane), ye, m[i]);
+        }
+      }
+    }
+    __syncthreads();
+    if (c > 0) store();
+    __syncthreads();
+  }
+
+  if (mine && p.ds0) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(p.ds0 + state_at + 16 * i + 4 * g) = m[i];
+  }
+}
+
+template <int DK>
+hipError_t launch(const DeltaParams& p, hipStream_t s) {
+  const uint32_t blocks = (uint32_t)((p.B * p.H + 7) / 8 * 8 * ((p.dv + 63) / 64));
+  delta_adjoint_f32_kernel<DK><<<blocks, 256, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_adjoint_f32(const DeltaParams& p, hipStream_t s) {
+  return p.dk == 128 ? launch<128>(p, s) : p.dk == 64 ? launch<64>(p, s) : launch<32>(p, s);
+}
+
+}  // namespace mesa

@@ -239,7 +239,7 @@ mesa_status mesa_delta_bwd(const mesa_delta_desc* d, const mesa_delta_grad_rows*
   }
   p.d_o = rows(d_o, gr->d_o); p.dq = rows(dq, gr->dq); p.dk_ = rows(dk, gr->dk); p.dv_ = rows(dv, gr->dv);
   p.dgamma = gate(dgamma, gr->dgamma); p.dbeta = gate(dbeta, gr->dbeta); p.d_sfinal = d_sfinal; p.ds0 = ds0;
-  if (launch_delta_adjoint(bf16, p, stream) != hipSuccess) return MESA_ERR_HIP;
+  if ((bf16 ? launch_delta_adjoint(p, stream) : launch_delta_adjoint_f32(p, stream)) != hipSuccess) return MESA_ERR_HIP;
   return d->T > 0 ? launched(launch_delta_grads(bf16, p, stream)) : MESA_OK;
 }
 
