@@ -26,7 +26,8 @@ template <int DK, bool BF16>
 struct GradLds {
   static constexpr int NP = BF16 ? 1 : 3, NZ = BF16 ? 2 : 3;
   static constexpr int kState = 32 * DK * 2, kU = 64 * 64, kPlane = 64 * DK * 2, kZ = 64 * 128;
-  static constexpr int kS = 0, kD = 3 * kState, kUAt = 6 * kState, kFirst = kUAt + 3 * kU;
+  static constexpr int kS = 0, kD = 3 * kState, kUAt = 6 * kState, kEAt = kUAt + 3 * kU, kOAt = kEAt + 3 * kU,
+                       kFirst = kOAt + NP * kU;
   static constexpr int kK = 0, kQ = NP * kPlane, kZAt = 2 * NP * kPlane, kYAt = kZAt + NZ * kZ, kSecond = kYAt + NZ * kZ;
   static constexpr int kBytes = kFirst > kSecond ? kFirst : kSecond;
 };
@@ -39,7 +40,7 @@ __global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
   constexpr int kPieces = 8 * DK, NS = (kPieces + 511) / 512;  // 16-byte pieces of a state's slice
   __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
   __shared__ __attribute__((aligned(16))) DeltaGates gates;
-  __shared__ float cols[8][64], part[2][64], behind[2][64], dbetas[2][64], gammas[64], red[8];
+  __shared__ float cols[8][64], part[2][64], behind[2][64], dbetas[64], gammas[64], red[8];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int tile = wave & 3, half = wave >> 2;
   const int64_t unit = blockIdx.x;
@@ -88,40 +89,38 @@ __global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
   if (tid < 64) gammas[tid] = tid < live ? *gate_at(p.gamma, b, h, t0 + tid) : 1.f;
   cols[wave][lane] = 0.f;
 
-  const float *states = p.states + unit * p.dv * DK, *dstates = p.dstates + unit * p.dv * DK;
-  const float *ws = p.w + unit * 64 * p.dv, *es = p.e + unit * 64 * p.dv;
   const float beta_own = valid ? *gate_at(p.beta, b, h, tok) : 0.f;
-  const float beta_w = (tid >> 3) < live ? *gate_at(p.beta, b, h, t0 + (tid >> 3)) : 0.f;
-  const int64_t do_at = b * p.d_o.b + h * p.d_o.h + tok * p.d_o.t;
-  f32x4 sl[NS], dl[NS], wl, e_own[2], w_own[2], o_own[2];
+  // A thread's pieces of a slice: 4 columns of a row of the states, and of a token (row `from`) of W, E and dO
+  const int from = tid >> 3, at4 = (tid & 7) * 4;
+  const float beta_from = from < live ? *gate_at(p.beta, b, h, t0 + from) : 0.f;
+  const Window states = window_at(p.states + unit * p.dv * DK), dstates = window_at(p.dstates + unit * p.dv * DK),
+               ws = window_at(p.w + unit * 64 * p.dv), es = window_at(p.e + unit * 64 * p.dv),
+               dos = window_at(static_cast<const char*>(p.d_o.at) +
+                               (b * p.d_o.b + h * p.d_o.h + (int64_t)t0 * p.d_o.t) * sizeof(Out)),
+               dvs = window_at(static_cast<char*>(p.dv_.at) +
+                               (b * p.dv_.b + h * p.dv_.h + (int64_t)t0 * p.dv_.t) * sizeof(Out));
+  const uint32_t w_at = (from * p.dv + at4) * 4, do_at = (from * (uint32_t)p.d_o.t + at4) * sizeof(Out),
+                 dv_at = (from * (uint32_t)p.dv_.t + at4) * sizeof(Out);
+  f32x4 sl[NS], dl[NS], wl, el, ol;
   auto load = [&](int d0) {
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
-      const int piece = tid + 512 * n, row = piece / (DK / 4), col = piece % (DK / 4) * 4;
-      sl[n] = dl[n] = zero;
-      if (row < 32 && d0 + row < p.dv) {
-        sl[n] = *reinterpret_cast<const f32x4*>(states + (int64_t)(d0 + row) * DK + col);
-        dl[n] = *reinterpret_cast<const f32x4*>(dstates + (int64_t)(d0 + row) * DK + col);
-      }
+      const int piece = tid + 512 * n, row = piece / (DK / 4);
+      const uint32_t at = row < min(32, p.dv - d0) ? piece * 16 : kNowhere;
+      sl[n] = __builtin_bit_cast(f32x4, window_load(states, at, d0 * DK * 4));
+      dl[n] = __builtin_bit_cast(f32x4, window_load(dstates, at, d0 * DK * 4));
     }
-    const int row = tid >> 3, col = (tid & 7) * 4;
-    wl = zero;
-    if (d0 + col < p.dv) wl = *reinterpret_cast<const f32x4*>(ws + (int64_t)row * p.dv + d0 + col);
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int at = d0 + 16 * n + 4 * g;
-      e_own[n] = w_own[n] = o_own[n] = zero;
-      if (at < p.dv) {
-        e_own[n] = *reinterpret_cast<const f32x4*>(es + (int64_t)own * p.dv + at);
-        w_own[n] = *reinterpret_cast<const f32x4*>(ws + (int64_t)own * p.dv + at);
-        if (valid) o_own[n] = load4<BF16>(p.d_o.at, do_at + at);
-      }
-    }
+    const bool there = at4 < p.dv - d0;
+    wl = __builtin_bit_cast(f32x4, window_load(ws, there ? w_at : kNowhere, d0 * 4));
+    el = __builtin_bit_cast(f32x4, window_load(es, there ? w_at : kNowhere, d0 * 4));
+    ol = window_row<BF16>(dos, there && from < live ? do_at : kNowhere, d0 * sizeof(Out));
   };
 
   f32x4 zy[4] = {zero, zero, zero, zero};  // rows j, a lane's token t: U dO^T (half 0) or U E^T (half 1)
   float dbeta = 0.f, along = 0.f;
   RowLoads<DK, BF16, 512> kl, ql;
+  kl.load(p.k.at, b * p.k.b + hk * p.k.h + t0 * p.k.t, p.k.t, live, DK, tid);
+  ql.load(p.q.at, b * p.q.b + hk * p.q.h + t0 * p.q.t, p.q.t, live, DK, tid);
   load(0);
   for (int d0 = 0; d0 < p.dv; d0 += 32) {
     __syncthreads();
@@ -141,28 +140,26 @@ __global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
       for (int e = 0; e < 4; ++e) along = fmaf(sl[n][e], dl[n][e], along);
     }
     {
-      bf16x4 a[3];
-      split4<3>(wl * beta_w, a);
+      const uint32_t at = tile_at<32>(from, 2 * at4);
+      bf16x4 u[3], x[3], o[NP];
+      split4<3>(wl * beta_from, u);
+      split4<3>(el, x);
+      split4<NP>(ol, o);
 #pragma unroll
-      for (int i = 0; i < 3; ++i)
-        *reinterpret_cast<bf16x4*>(lds + L::kUAt + i * L::kU + tile_at<32>(tid >> 3, (tid & 7) * 8)) = a[i];
-    }
-    const Planes<NP> of = split8<NP>(o_own[0], o_own[1]);
-    const Planes<3> ef = split8<3>(e_own[0], e_own[1]), uf = split8<3>(w_own[0] * beta_own, w_own[1] * beta_own);
-    {
-      const f32x4 e = half ? e_own[1] : e_own[0], w = half ? w_own[1] : w_own[0];
-      const int at = d0 + 16 * half;
-      if (there && at < p.dv) store_out4<Out>(p.dv_.at, v_at + at, valid ? e * beta_own : zero);
+      for (int i = 0; i < 3; ++i) {
+        *reinterpret_cast<bf16x4*>(lds + L::kUAt + i * L::kU + at) = u[i];
+        *reinterpret_cast<bf16x4*>(lds + L::kEAt + i * L::kU + at) = x[i];
+        if (i < NP) *reinterpret_cast<bf16x4*>(lds + L::kOAt + i * L::kU + at) = o[i];
+      }
+      window_store_row<BF16>(dvs, from < here && at4 < p.dv - d0 ? dv_at : kNowhere, d0 * sizeof(Out), el * beta_from);
 #pragma unroll
-      for (int n = 0; n < 4; ++n) dbeta = fmaf(e[n], w[n], dbeta);
+      for (int n = 0; n < 4; ++n) dbeta = fmaf(el[n], wl[n], dbeta);
     }
-    if (d0 + 32 < p.dv) {
-      load(d0 + 32);
-    } else {
-      kl.load(p.k.at, b * p.k.b + hk * p.k.h + t0 * p.k.t, p.k.t, live, DK, tid);
-      ql.load(p.q.at, b * p.q.b + hk * p.q.h + t0 * p.q.t, p.q.t, live, DK, tid);
-    }
+    load(d0 + 32);  // (behind the last slice: zeros)
     __syncthreads();
+    const Planes<NP> of = rows_of<32, NP>(lds + L::kOAt, L::kU, 16 * tile, 0, lane);
+    const Planes<3> ef = rows_of<32, 3>(lds + L::kEAt, L::kU, 16 * tile, 0, lane);
+    const Planes<3> uf = rows_of<32, 3>(lds + L::kUAt, L::kU, 16 * tile, 0, lane);
 #pragma unroll
     for (int i = 0; i < MH; ++i) {
       const Planes<3> s = columns_of<DK, 3>(lds + L::kS, L::kState, 0, MH * half + i, lane);
@@ -247,13 +244,13 @@ __global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
   }
   sum = sum_lane_groups(sum);
   left = sum_lane_groups(left);
-  dbeta = sum_lane_groups(dbeta);
+  dbeta = group_sum<8>(dbeta);
   along = wave_sum(along);
   if (g == 0) {
     part[half][own] = sum;
     behind[half][own] = left;
-    dbetas[half][own] = dbeta;
   }
+  if ((tid & 7) == 0) dbetas[from] = dbeta;
   if (lane == 0) red[wave] = along;
   __syncthreads();
 
@@ -305,7 +302,7 @@ __global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
     x += gates.c[63] * whole;
     if (lane < here) {
       *gate_at(p.dgamma, b, h, t0 + lane) = lane < live ? (float)(x / (double)gammas[lane]) : 0.f;
-      *gate_at(p.dbeta, b, h, t0 + lane) = lane < live ? dbetas[0][lane] + dbetas[1][lane] : 0.f;
+      *gate_at(p.dbeta, b, h, t0 + lane) = lane < live ? dbetas[lane] : 0.f;
     }
   }
 }

@@ -230,6 +230,17 @@ __device__ __forceinline__ u32x4 window_load(Window w, uint32_t lane_offset, uin
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w, lane_offset, offset, 0));
 }
 
+// 4 numbers of a row
+template <bool BF16>
+__device__ __forceinline__ f32x4 window_row(Window w, uint32_t lane_offset, uint32_t offset) {
+  if constexpr (BF16) {
+    const u16x4 u = __builtin_bit_cast(u16x4, __builtin_amdgcn_raw_buffer_load_b64(w, lane_offset, offset, 0));
+    return f32x4{bf16_to_f32(u[0]), bf16_to_f32(u[1]), bf16_to_f32(u[2]), bf16_to_f32(u[3])};
+  } else {
+    return __builtin_bit_cast(f32x4, window_load(w, lane_offset, offset));
+  }
+}
+
 __device__ __forceinline__ void window_store(Window w, uint32_t lane_offset, uint32_t offset, float v) {
   __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), w, lane_offset, offset, 0);
 }
