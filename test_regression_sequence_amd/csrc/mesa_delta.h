@@ -40,6 +40,12 @@ struct DeltaParams {
   float* s_final;                   // [B, H, dv, dk] or null
   const int32_t* lengths;           // [B] or null
   int B, H, Hk, T, dk, dv, NC;      // NC chunks a (padded) sequence
+  // A walk in NS segments of L chunks (NS = 1: whole).  seg_map: [B H, NS, dk, dk], row j what
+  // a segment makes of the state whose row is unit vector j; seg_add: [B H, NS, dv, dk], what it
+  // makes of a zero state; seg_start: [B H, NS, dv, dk], the states the segments start from
+  int NS, L;
+  float *seg_map, *seg_add, *seg_start;
+  int probe;                        // 1: the walk that forms seg_map and seg_add
   DeltaGates* gates;                // [B H, NC]
   char* matrices;                   // [B H, NC, delta_matrix_bytes(2 or 3)]
   float* states;                    // [B H, NC, dv, dk] before each chunk, or null
@@ -63,6 +69,9 @@ hipError_t launch_delta_scan_f32(const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_adjoint(const DeltaParams& p, hipStream_t s);  // bf16 rows
 hipError_t launch_delta_adjoint_f32(const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_grads(bool bf16, const DeltaParams& p, hipStream_t s);
+
+// seg_start from seg_map, seg_add and the state at one end; `back`: from the last segment to the first.
+hipError_t launch_delta_join(bool back, const DeltaParams& p, hipStream_t s);
 
 struct DeltaStepParams {
   const void *q, *k, *v;

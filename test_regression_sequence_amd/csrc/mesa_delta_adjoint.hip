@@ -36,10 +36,10 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
   const int tid = threadIdx.x & 255, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15,
             g = lane >> 4;
   const bool chain = __builtin_amdgcn_readfirstlane(threadIdx.x) < 256;
-  int bh, slice;
-  if (!delta_unit(blockIdx.x, (p.dv + 63) / 64, p.B * p.H, bh, slice)) return;
-  const int b = bh / p.H, h = bh % p.H, len = delta_length(p, b);
-  const int nc = (len + 63) / 64, col0 = 64 * slice, cols = min(64, p.dv - col0);
+  Part part;
+  if (!part_of(p, true, blockIdx.x, part)) return;
+  const int bh = part.bh, b = part.b, h = part.h, len = part.len, first = part.first, last = part.last;
+  const int col0 = part.col0, cols = part.cols;
   const bool mine = 16 * wave < cols;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   char* const u_at = lds + L::kU + wave * 4096 + lane * 16;     // A^T dO: four tiles
@@ -49,12 +49,12 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
 
   if (chain) {
     const int col = col0 + 16 * wave + r;
-    const int64_t state_at = ((int64_t)bh * p.dv + col) * DK + 4 * g;
     f32x4 m[MT];
+    const float* const from = walk_from(p, part, p.d_sfinal, p.NS - 1, col);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       m[i] = zero;
-      if (mine && p.d_sfinal) m[i] = *reinterpret_cast<const f32x4*>(p.d_sfinal + state_at + 16 * i);
+      if (mine && from) m[i] = *reinterpret_cast<const f32x4*>(from + 16 * i + 4 * g);
     }
     const TileRows<DK> rows(lane);
     Planes<3> mp[KS];
@@ -63,7 +63,7 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
     __builtin_amdgcn_s_setprio(2);
     __syncthreads();
     __syncthreads();
-    for (int c = nc - 1; c >= 0; --c) {
+    for (int c = last - 1; c >= first; --c) {
       const char* keys = lds + L::kK + (c & 1) * L::kTile;
       const DeltaGates& gates = *reinterpret_cast<const DeltaGates*>(lds + L::kGates + (c & 1) * L::kGate);
       const int64_t unit = (int64_t)bh * p.NC + c;
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
           mma_tiles<2>(f[s & 1], mp[s], x);
           fence<true>();
         }
-        {
+        if (!p.probe) {
           const Window to = window_at(p.dstates + unit * p.dv * DK);
 #pragma unroll
           for (int i = 0; i < MT; ++i) window_store(to, (col * DK + 4 * g) * 4, 64 * i, m[i]);
@@ -127,8 +127,9 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
           const Window to = window_at(p.e + unit * 64 * p.dv);
 #pragma unroll
           for (int i = 2 * s; i < 2 * s + 2; ++i) {
+            if (!p.probe)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) window_store(to, (4 * g * p.dv + col) * 4, (16 * i + e) * p.dv * 4, x[i][e]);
+              for (int e = 0; e < 4; ++e) window_store(to, (4 * g * p.dv + col) * 4, (16 * i + e) * p.dv * 4, x[i][e]);
             y[i] = -(cc[i] * cb[i]) * x[i];
           }
           pe[s] = split8<3>(y[2 * s], y[2 * s + 1]);
@@ -175,9 +176,10 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
       }
       __syncthreads();
     }
-    if (mine && p.ds0) {
+    float* const to = walk_to(p, part, p.ds0, 0, col);
+    if (mine && to) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(p.ds0 + state_at + 16 * i) = m[i];
+      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i + 4 * g) = m[i];
     }
     return;
   }
@@ -227,19 +229,19 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(u_at + i * 1024) = u[i];
   };
-  if (nc > 0) {
-    load_first(nc - 1);
+  if (first < last) {
+    load_first(last - 1);
 #pragma unroll
-    for (int s = 0; s < KS; ++s) load_rest(nc - 1, s);
-    store_first(nc - 1);
-    store_rest(nc - 1);
-    load_first(max(nc - 2, 0));
+    for (int s = 0; s < KS; ++s) load_rest(last - 1, s);
+    store_first(last - 1);
+    store_rest(last - 1);
+    load_first(max(last - 2, first));
   }
   __syncthreads();
-  if (nc > 0) before_n(nc - 1);
+  if (first < last) before_n(last - 1);
   __syncthreads();
-  for (int c = nc - 1; c >= 0; --c) {  // (no branch around the loads: the first chunk is loaded once more)
-    const int next = max(c - 1, 0);
+  for (int c = last - 1; c >= first; --c) {  // (no branch around the loads: the first chunk is loaded once more)
+    const int next = max(c - 1, first);
     const char* rows = lds + L::kO + (c & 1) * 64 * 128;
     const DeltaGates& gates = *reinterpret_cast<const DeltaGates*>(lds + L::kGates + (c & 1) * L::kGate);
     store_first(c - 1);
@@ -278,15 +280,14 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
     __syncthreads();
     before_n(c - 1);
     store_rest(c - 1);
-    load_first(max(c - 2, 0));
+    load_first(max(c - 2, first));
     __syncthreads();
   }
 }
 
 template <int DK>
 hipError_t launch(const DeltaParams& p, hipStream_t s) {
-  const uint32_t blocks = (uint32_t)((p.B * p.H + 7) / 8 * 8 * ((p.dv + 63) / 64));
-  delta_adjoint_kernel<DK><<<blocks, 512, 0, s>>>(p);
+  delta_adjoint_kernel<DK><<<walk_blocks(p, true), 512, 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -23,20 +23,20 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p
   constexpr int NP = L::NP, MT = DK / 16, KS = DK / 32;
   __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
-  int bh, slice;
-  if (!delta_unit(blockIdx.x, (p.dv + 63) / 64, p.B * p.H, bh, slice)) return;
-  const int b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk), len = delta_length(p, b);
-  const int nc = (len + 63) / 64, col0 = 64 * slice, cols = min(64, p.dv - col0);
+  Part part;
+  if (!part_of(p, true, blockIdx.x, part)) return;
+  const int bh = part.bh, b = part.b, h = part.h, hk = h / (p.H / p.Hk), len = part.len, first = part.first, last = part.last;
+  const int col0 = part.col0, cols = part.cols;
   const int col = col0 + 16 * wave + r;
   const bool mine = 16 * wave < cols;
-  const int64_t state_at = ((int64_t)bh * p.dv + col) * DK;
   const int64_t q0 = b * p.q.b + hk * p.q.h, k0 = b * p.k.b + hk * p.k.h, o0 = b * p.d_o.b + h * p.d_o.h + col0;
 
   f32x4 m[MT];
+  const float* const from = walk_from(p, part, p.d_sfinal, p.NS - 1, col);
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     m[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (mine && p.d_sfinal) m[i] = *reinterpret_cast<const f32x4*>(p.d_sfinal + state_at + 16 * i + 4 * g);
+    if (mine && from) m[i] = *reinterpret_cast<const f32x4*>(from + 16 * i + 4 * g);
   }
   RowLoads<DK, false, 256> kl, ql;
   RowLoads<64, false, 256> ol;
@@ -59,21 +59,23 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p
     gl.store(lds + L::kGates, tid);
   };
 
-  if (nc > 0) {
-    load(nc - 1);
+  if (first < last) {
+    load(last - 1);
     store();
     __syncthreads();
   }
-  for (int c = nc - 1; c >= 0; --c) {
+  for (int c = last - 1; c >= first; --c) {
     const int64_t unit = (int64_t)bh * p.NC + c;
     const DeltaGates& gates = *reinterpret_cast<const DeltaGates*>(lds + L::kGates);
-    if (c > 0) load(c - 1);
+    if (c > first) load(c - 1);
 
     if (mine) {
       f32x4 x[4];  // tail K N
-      float* to = p.dstates + unit * p.dv * DK + (int64_t)col * DK + 4 * g;
+      if (!p.probe) {
+        float* to = p.dstates + unit * p.dv * DK + (int64_t)col * DK + 4 * g;
 #pragma unroll
-      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i) = m[i];
+        for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i) = m[i];
+      }
       Planes<3> mp[KS];
 #pragma unroll
       for (int s = 0; s < KS; ++s) mp[s] = split8<3>(m[2 * s], m[2 * s + 1]);
@@ -101,11 +103,13 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p
         for (int s = i / 2; s < 2; ++s) acc = mma<2>(block_of<3>(lds + L::kT, upper_block(i, s), lane), px[s], acc);
         x[i] = acc;
       }
-      float* e_to = p.e + (unit * 64 + 4 * g) * p.dv + col;
+      if (!p.probe) {
+        float* e_to = p.e + (unit * 64 + 4 * g) * p.dv + col;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) e_to[(int64_t)(16 * i + e) * p.dv] = x[i][e];
+          for (int e = 0; e < 4; ++e) e_to[(int64_t)(16 * i + e) * p.dv] = x[i][e];
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f32x4 cc = *reinterpret_cast<const f32x4*>(&gates.c[16 * i + 4 * g]);
@@ -126,20 +130,20 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p
       }
     }
     __syncthreads();
-    if (c > 0) store();
+    if (c > first) store();
     __syncthreads();
   }
 
-  if (mine && p.ds0) {
+  float* const to = walk_to(p, part, p.ds0, 0, col);
+  if (mine && to) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(p.ds0 + state_at + 16 * i + 4 * g) = m[i];
+    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i + 4 * g) = m[i];
   }
 }
 
 template <int DK>
 hipError_t launch(const DeltaParams& p, hipStream_t s) {
-  const uint32_t blocks = (uint32_t)((p.B * p.H + 7) / 8 * 8 * ((p.dv + 63) / 64));
-  delta_adjoint_f32_kernel<DK><<<blocks, 256, 0, s>>>(p);
+  delta_adjoint_f32_kernel<DK><<<walk_blocks(p, true), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -93,6 +93,29 @@ mesa_status check_delta(const mesa_delta_desc* d) {
   return MESA_OK;
 }
 
+// In how many segments a walk goes.  A walk of one workgroup a head and 64 columns takes
+// its chunks one after the other; with fewer of those than the 256 CUs, segments of it run
+// side by side, after a walk that finds what each makes of unit rows and of zero (dk more
+// columns) and a launch that joins them.  In times of one chunk (about 2.7 us), that launch
+// and the additional walk's take about 3 and half a chunk a segment.
+int segments_of(const mesa_delta_desc* d) {
+  const int64_t heads = (int64_t)d->B * d->H, values = (d->dv + 63) / 64, units = (d->dk + 63) / 64;
+  const int chunks = chunks_of(d);
+  const auto rounds = [](int64_t blocks) { return (double)((blocks + 255) / 256); };
+  int best = 1;
+  double least = 0.9 * chunks * rounds(heads * values);
+  for (int n = 2; n <= 32 && n * 4 <= chunks; ++n) {
+    const int per = (chunks + n - 1) / n;
+    if ((chunks + per - 1) / per != n) continue;  // (no segment stays empty)
+    const double time = per * (rounds(heads * (n - 1) * (values + units)) + rounds(heads * n * values)) + 3 + 0.5 * n;
+    if (time < least) {
+      best = n;
+      least = time;
+    }
+  }
+  return best;
+}
+
 struct Carve {
   char* base;
   size_t at = 0;
@@ -106,9 +129,15 @@ struct Carve {
 
 // Places the workspace's parts; returns its size.
 size_t carve(const mesa_delta_desc* d, bool keep, void* workspace, DeltaParams& p) {
+  p.NS = segments_of(d);
+  p.L = (chunks_of(d) + p.NS - 1) / p.NS;
   Carve w{static_cast<char*>(workspace)};
   const size_t units = (size_t)d->B * d->H * chunks_of(d), state = (size_t)d->dv * d->dk * 4;
   p.gates = w.take<DeltaGates>(units * sizeof(DeltaGates));
+  const size_t segments = p.NS > 1 ? (size_t)d->B * d->H * p.NS : 0;
+  p.seg_map = w.take<float>(segments * d->dk * d->dk * 4);
+  p.seg_add = w.take<float>(segments * state);
+  p.seg_start = w.take<float>(segments * state);
   p.matrices = w.take<char>(units * delta_matrix_bytes(d->dtype == MESA_BF16 ? 2 : 3));
   if (keep) {
     p.states = w.take<float>(units * state);
@@ -138,8 +167,34 @@ DeltaParams delta_params(const mesa_delta_desc* d, const void* q, const void* k,
   return p;
 }
 
+// A walk forward, in segments where there are few heads.
 hipError_t scan(bool bf16, const DeltaParams& p, hipStream_t s) {
-  return bf16 ? launch_delta_scan(p, s) : launch_delta_scan_f32(p, s);
+  const auto walk = [&](const DeltaParams& x) { return bf16 ? launch_delta_scan(x, s) : launch_delta_scan_f32(x, s); };
+  if (p.NS > 1) {
+    DeltaParams probe = p;
+    probe.probe = 1;
+    probe.o.at = nullptr;
+    probe.states = probe.w = nullptr;
+    hipError_t e = walk(probe);
+    if (e == hipSuccess) e = launch_delta_join(false, p, s);
+    if (e != hipSuccess) return e;
+  }
+  return walk(p);
+}
+
+// A walk back; the segments' maps are those of the walk forward.
+hipError_t adjoint(bool bf16, const DeltaParams& p, hipStream_t s) {
+  const auto walk = [&](const DeltaParams& x) {
+    return bf16 ? launch_delta_adjoint(x, s) : launch_delta_adjoint_f32(x, s);
+  };
+  if (p.NS > 1) {
+    DeltaParams probe = p;
+    probe.probe = 1;
+    hipError_t e = walk(probe);
+    if (e == hipSuccess) e = launch_delta_join(true, p, s);
+    if (e != hipSuccess) return e;
+  }
+  return walk(p);
 }
 
 mesa_status launched(hipError_t e) { return e == hipSuccess ? MESA_OK : MESA_ERR_HIP; }
@@ -239,7 +294,7 @@ mesa_status mesa_delta_bwd(const mesa_delta_desc* d, const mesa_delta_grad_rows*
   }
   p.d_o = rows(d_o, gr->d_o); p.dq = rows(dq, gr->dq); p.dk_ = rows(dk, gr->dk); p.dv_ = rows(dv, gr->dv);
   p.dgamma = gate(dgamma, gr->dgamma); p.dbeta = gate(dbeta, gr->dbeta); p.d_sfinal = d_sfinal; p.ds0 = ds0;
-  if ((bf16 ? launch_delta_adjoint(p, stream) : launch_delta_adjoint_f32(p, stream)) != hipSuccess) return MESA_ERR_HIP;
+  if (adjoint(bf16, p, stream) != hipSuccess) return MESA_ERR_HIP;
   return d->T > 0 ? launched(launch_delta_grads(bf16, p, stream)) : MESA_OK;
 }
 

@@ -1,0 +1,79 @@
+// Gated delta rule: the states that the segments of a split walk start from.
+//
+// Over a segment the state's rows go S -> S P + Q (P = seg_map, Q = seg_add: what
+// the segment makes of unit rows and of zero), and its gradients back N -> N P^T + Q.
+// From one segment to the next that is a 16 x dk by dk x dk product for each 16 rows,
+// in fp32 matrix instructions: a workgroup has 16 rows in LDS, its waves the tiles of
+// the result's columns.
+#include "mesa_delta_tile.h"
+
+namespace mesa {
+
+namespace {
+
+template <int DK, bool BACK>
+__global__ __launch_bounds__(256) void delta_join_kernel(DeltaParams p) {
+  constexpr int NT = DK / 16, PER = (NT + 3) / 4;
+  __shared__ __attribute__((aligned(16))) float rows[2][16][DK + 4];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int groups = p.dv / 16, bh = blockIdx.x / groups, row0 = blockIdx.x % groups * 16;
+  const float* given = BACK ? p.d_sfinal : p.s0;
+  for (int i = tid; i < 16 * DK; i += 256)
+    rows[0][i / DK][i % DK] = given ? given[((int64_t)bh * p.dv + row0 + i / DK) * DK + i % DK] : 0.f;
+  for (int n = 0; n + 1 < p.NS; ++n) {
+    const int seg = BACK ? p.NS - 1 - n : n, next = BACK ? seg - 1 : seg + 1;
+    const int64_t at = (int64_t)bh * p.NS + seg, to = (int64_t)bh * p.NS + next;
+    const float *map = p.seg_map + at * DK * DK, *add = p.seg_add + (at * p.dv + row0) * DK;
+    f32x4 b[PER][NT], acc[PER];
+#pragma unroll
+    for (int t = 0; t < PER; ++t) {
+      const int col = 16 * (wave + 4 * t) + r;
+      if (wave + 4 * t >= NT) continue;
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        if constexpr (BACK) {
+          b[t][k] = *reinterpret_cast<const f32x4*>(map + (int64_t)col * DK + 16 * k + 4 * g);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) b[t][k][e] = map[(int64_t)(16 * k + 4 * g + e) * DK + col];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[t][e] = add[(int64_t)(4 * g + e) * DK + col];
+    }
+    __syncthreads();
+    const auto& from = rows[n & 1];
+#pragma unroll
+    for (int t = 0; t < PER; ++t) {
+      if (wave + 4 * t >= NT) continue;
+      const int col = 16 * (wave + 4 * t) + r;
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(&from[r][16 * k + 4 * g]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[t] = mfma_f32(a[e], b[t][k][e], acc[t]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        rows[~n & 1][4 * g + e][col] = acc[t][e];
+        p.seg_start[(to * p.dv + row0 + 4 * g + e) * DK + col] = acc[t][e];
+      }
+    }
+  }
+}
+
+template <int DK>
+hipError_t launch(bool back, const DeltaParams& p, hipStream_t s) {
+  const uint32_t blocks = (uint32_t)(p.B * p.H * (p.dv / 16));
+  if (back) delta_join_kernel<DK, true><<<blocks, 256, 0, s>>>(p);
+  else delta_join_kernel<DK, false><<<blocks, 256, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_join(bool back, const DeltaParams& p, hipStream_t s) {
+  return p.dk == 128 ? launch<128>(back, p, s) : p.dk == 64 ? launch<64>(back, p, s) : launch<32>(back, p, s);
+}
+
+}  // namespace mesa

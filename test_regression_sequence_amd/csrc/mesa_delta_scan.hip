@@ -37,10 +37,10 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
   __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
   const int tid = threadIdx.x & 255, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   const bool chain = __builtin_amdgcn_readfirstlane(threadIdx.x) < 256;
-  int bh, slice;
-  if (!delta_unit(blockIdx.x, (p.dv + 63) / 64, p.B * p.H, bh, slice)) return;
-  const int b = bh / p.H, h = bh % p.H, len = delta_length(p, b);
-  const int nc = (len + 63) / 64, col0 = 64 * slice, cols = min(64, p.dv - col0);
+  Part part;
+  if (!part_of(p, false, blockIdx.x, part)) return;
+  const int bh = part.bh, b = part.b, h = part.h, len = part.len, first = part.first, last = part.last;
+  const int col0 = part.col0, cols = part.cols;
   const bool mine = 16 * wave < cols;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   char* const m_planes = lds + L::kM + wave * 2 * L::kMPlane + lane * 16;
@@ -48,12 +48,15 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
 
   if (chain) {
     const int col = col0 + 16 * wave + r;  // this lane's column of the state
-    const int64_t state_at = ((int64_t)bh * p.dv + col) * DK + 4 * g;
     f32x4 m[MT];  // rows 16 i + 4 g + e of M
+    const float* const from = walk_from(p, part, p.s0, 0, col);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       m[i] = zero;
-      if (mine && p.s0) m[i] = *reinterpret_cast<const f32x4*>(p.s0 + state_at + 16 * i);
+      if (mine && from) m[i] = *reinterpret_cast<const f32x4*>(from + 16 * i + 4 * g);
+      if (part.unit_columns)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[i][e] = 16 * i + 4 * g + e == col ? 1.f : 0.f;
     }
     const TileRows<DK> rows(lane);
     const TileColumns<DK> columns(lane);
@@ -70,7 +73,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
     planes(0, KS);
     __builtin_amdgcn_s_setprio(2);
     __syncthreads();
-    for (int c = 0; c < nc; ++c) {
+    for (int c = first; c < last; ++c) {
       const char* keys = lds + L::kK + (c & 1) * L::kTile;
       const DeltaGates& gates = *reinterpret_cast<const DeltaGates*>(lds + L::kGates + (c & 1) * L::kGate);
       f32x4 x[4] = {zero, zero, zero, zero}, y[4];
@@ -194,9 +197,10 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
       }
       __syncthreads();
     }
-    if (mine && p.s_final) {
+    float* const to = walk_to(p, part, p.s_final, p.NS - 1, col);
+    if (mine && to) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(p.s_final + state_at + 16 * i) = m[i];
+      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i + 4 * g) = m[i];
     }
     return;
   }
@@ -218,7 +222,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
     if (s == 0) kl.load(p.k.at, k0 + t0 * p.k.t, p.k.t, live, DK, tid);
     if (OUT && s == min(1, KS - 1)) ql.load(p.q.at, q0 + t0 * p.q.t, p.q.t, live, DK, tid);
     if (s == min(2, KS - 1)) {
-      vl.load(p.v.at, v0 + t0 * p.v.t, p.v.t, live, cols, tid);
+      vl.load(p.v.at, v0 + t0 * p.v.t, p.v.t, live, part.unit_columns ? 0 : cols, tid);
       tl.load(matrix, tid);
     }
     if (s == KS - 1) {
@@ -240,9 +244,9 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
       al.store(lds + L::kA + (c & 1) * 2 * kBlocksBytes, tid);
     }
   };
-  if (nc > 0) {
-    load_all(0);
-    store(0);
+  if (first < last) {
+    load_all(first);
+    store(first);
   }
   __syncthreads();
   f32x4 o[4], u[4];  // o's transpose (a lane has 4 columns of one token) and U
@@ -261,10 +265,10 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
   // Without a branch around the loads (the last chunk is loaded once more), and with
   // products for columns that do not exist: where paths with and without loads in
   // flight meet, the compiler waits for them.
-  for (int c = 0; c < nc; ++c) {
-    const int next = min(c + 1, nc - 1);
+  for (int c = first; c < last; ++c) {
+    const int next = min(c + 1, last - 1);
     if constexpr (OUT) {
-      if (c > 0) finish(c - 1);
+      if (c > first) finish(c - 1);
       Planes<1> f[2][4];
       Planes<2> mp[2];
       auto operands = [&](int s) {
@@ -300,17 +304,17 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
     store(c + 1);
     __syncthreads();
   }
-  if (OUT && nc > 0) finish(nc - 1);
+  if (OUT && first < last) finish(last - 1);
   if (OUT && mine) {  // behind the sequence
-    for (int64_t t = len + r; t < p.T; t += 16) store_out4<__bf16>(p.o.at, o0 + t * p.o.t + 4 * g, zero);
+    const int end = (int)min((int64_t)p.T, (int64_t)64 * (first + p.L));
+    for (int64_t t = max(len, 64 * first) + r; t < end; t += 16) store_out4<__bf16>(p.o.at, o0 + t * p.o.t + 4 * g, zero);
   }
 }
 
 template <int DK>
 hipError_t launch(const DeltaParams& p, hipStream_t s) {
-  const uint32_t blocks = (uint32_t)((p.B * p.H + 7) / 8 * 8 * ((p.dv + 63) / 64));
-  if (p.o.at) delta_scan_kernel<DK, true><<<blocks, 512, 0, s>>>(p);
-  else delta_scan_kernel<DK, false><<<blocks, 512, 0, s>>>(p);
+  if (p.o.at) delta_scan_kernel<DK, true><<<walk_blocks(p, false), 512, 0, s>>>(p);
+  else delta_scan_kernel<DK, false><<<walk_blocks(p, false), 512, 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -24,22 +24,25 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
   constexpr int NP = L::NP, NA = L::NA, MT = DK / 16, KS = DK / 32;
   __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
-  int bh, slice;
-  if (!delta_unit(blockIdx.x, (p.dv + 63) / 64, p.B * p.H, bh, slice)) return;
-  const int b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk), len = delta_length(p, b);
-  const int nc = (len + 63) / 64, col0 = 64 * slice, cols = min(64, p.dv - col0);
+  Part part;
+  if (!part_of(p, false, blockIdx.x, part)) return;
+  const int bh = part.bh, b = part.b, h = part.h, hk = h / (p.H / p.Hk), len = part.len, first = part.first, last = part.last;
+  const int col0 = part.col0, cols = part.cols;
   const int col = col0 + 16 * wave + r;                 // this lane's column of the state
   const bool mine = 16 * wave < cols;
-  const int64_t state_at = ((int64_t)bh * p.dv + col) * DK;
   const int64_t q0 = b * p.q.b + hk * p.q.h, k0 = b * p.k.b + hk * p.k.h, v0 = b * p.v.b + h * p.v.h + col0,
                 o0 = b * p.o.b + h * p.o.h + col0 + 16 * wave + 4 * g;
 
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   f32x4 m[MT];  // rows 16 i + 4 g + e of M, column `col`
+  const float* const from = walk_from(p, part, p.s0, 0, col);
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     m[i] = zero;
-    if (mine && p.s0) m[i] = *reinterpret_cast<const f32x4*>(p.s0 + state_at + 16 * i + 4 * g);
+    if (mine && from) m[i] = *reinterpret_cast<const f32x4*>(from + 16 * i + 4 * g);
+    if (part.unit_columns)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m[i][e] = 16 * i + 4 * g + e == col ? 1.f : 0.f;
   }
   RowLoads<DK, false, 256> kl, ql;
   RowLoads<64, false, 256> vl;
@@ -50,7 +53,7 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
     const int64_t t0 = 64 * (int64_t)c, unit = (int64_t)bh * p.NC + c;
     kl.load(p.k.at, k0 + t0 * p.k.t, p.k.t, live, DK, tid);
     if constexpr (OUT) ql.load(p.q.at, q0 + t0 * p.q.t, p.q.t, live, DK, tid);
-    vl.load(p.v.at, v0 + t0 * p.v.t, p.v.t, live, cols, tid);
+    vl.load(p.v.at, v0 + t0 * p.v.t, p.v.t, live, part.unit_columns ? 0 : cols, tid);
     ml.load(p.matrices + unit * L::kMatrices, tid);
     gl.load(p.gates + unit, tid);
   };
@@ -62,15 +65,15 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
     gl.store(lds + L::kGates, tid);
   };
 
-  if (nc > 0) {
-    load(0);
+  if (first < last) {
+    load(first);
     store();
     __syncthreads();
   }
-  for (int c = 0; c < nc; ++c) {
+  for (int c = first; c < last; ++c) {
     const int64_t unit = (int64_t)bh * p.NC + c;
     const DeltaGates& gates = *reinterpret_cast<const DeltaGates*>(lds + L::kGates);
-    if (c + 1 < nc) load(c + 1);
+    if (c + 1 < last) load(c + 1);
     f32x4 o[4] = {zero, zero, zero, zero};
 
     if (mine) {
@@ -174,7 +177,7 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
       }
     }
     __syncthreads();
-    if (c + 1 < nc) store();  // (ahead of o's stores, which then have the next chunk's time)
+    if (c + 1 < last) store();  // (ahead of o's stores, which then have the next chunk's time)
     if (OUT && mine) {
       const int live = len - 64 * c;
 #pragma unroll
@@ -189,12 +192,14 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
     __syncthreads();
   }
 
-  if (mine && p.s_final) {
+  float* const to = walk_to(p, part, p.s_final, p.NS - 1, col);
+  if (mine && to) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(p.s_final + state_at + 16 * i + 4 * g) = m[i];
+    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i + 4 * g) = m[i];
   }
   if (OUT && mine) {  // behind the sequence
-    for (int64_t t = len + r; t < p.T; t += 16) {
+    const int end = (int)min((int64_t)p.T, (int64_t)64 * (first + p.L));
+    for (int64_t t = max(len, 64 * first) + r; t < end; t += 16) {
       store_out4<float>(p.o.at, o0 + t * p.o.t, zero);
     }
   }
@@ -202,9 +207,8 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
 
 template <int DK>
 hipError_t launch(const DeltaParams& p, hipStream_t s) {
-  const uint32_t blocks = (uint32_t)((p.B * p.H + 7) / 8 * 8 * ((p.dv + 63) / 64));
-  if (p.o.at) delta_scan_f32_kernel<DK, true><<<blocks, 256, 0, s>>>(p);
-  else delta_scan_f32_kernel<DK, false><<<blocks, 256, 0, s>>>(p);
+  if (p.o.at) delta_scan_f32_kernel<DK, true><<<walk_blocks(p, false), 256, 0, s>>>(p);
+  else delta_scan_f32_kernel<DK, false><<<walk_blocks(p, false), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -403,13 +403,49 @@ __device__ __forceinline__ float* gate_at(const DeltaGate& x, int b, int h, int6
 // exp2 of a difference of two logarithms that are kept in 64 bits.
 __device__ __forceinline__ float decay(double a, double b) { return __builtin_amdgcn_exp2f((float)(a - b)); }
 
-// Unit `id` of `slices` workgroups for each (sequence, head): those of one head go
-// to one XCD (workgroups are handed to the 8 XCDs in turn), whose L2 they share.
-__device__ __forceinline__ bool delta_unit(uint32_t id, int slices, int BH, int& bh, int& slice) {
+// One workgroup's part of a walk: 64 columns of one head's state over one segment's
+// chunks first .. last - 1.  A probing walk has the columns of the unit matrix too
+// (`unit_columns`), and none for the last (back: the first) segment, which nothing follows.
+struct Part {
+  int bh, b, h, seg, col0, cols, len, first, last;
+  bool unit_columns;
+};
+
+// The workgroups of one head go to one XCD (workgroups are handed to the 8 XCDs in
+// turn), whose L2 they share.  False: no part.
+__device__ __forceinline__ bool part_of(const DeltaParams& p, bool back, uint32_t id, Part& x) {
+  const int values = (p.dv + 63) / 64, slices = values + (p.probe && !back ? (p.dk + 63) / 64 : 0);
+  const int segs = p.probe ? p.NS - 1 : p.NS, per = slices * segs;
   const uint32_t xcd = id & 7, n = id >> 3;
-  bh = (int)(n / slices) * 8 + (int)xcd;
-  slice = (int)(n % slices);
-  return bh < BH;
+  x.bh = (int)(n / per) * 8 + (int)xcd;
+  if (x.bh >= p.B * p.H) return false;
+  const int rest = (int)(n % per), slice = rest % slices;
+  x.seg = rest / slices + (p.probe && back ? 1 : 0);
+  x.b = x.bh / p.H;
+  x.h = x.bh % p.H;
+  x.unit_columns = slice >= values;
+  x.col0 = 64 * (x.unit_columns ? slice - values : slice);
+  x.cols = min(64, (x.unit_columns ? p.dk : p.dv) - x.col0);
+  x.len = delta_length(p, x.b);
+  x.first = x.seg * p.L;
+  x.last = max(min((x.len + 63) / 64, x.first + p.L), x.first);
+  return true;
+}
+inline uint32_t walk_blocks(const DeltaParams& p, bool back) {
+  const int slices = (p.dv + 63) / 64 + (p.probe && !back ? (p.dk + 63) / 64 : 0);
+  return (uint32_t)((p.B * p.H + 7) / 8 * 8 * slices * (p.probe ? p.NS - 1 : p.NS));
+}
+
+// Where a walk's state comes from and goes to: [.., dk] from column `col` on (null: zeros, nowhere).
+__device__ __forceinline__ const float* walk_from(const DeltaParams& p, const Part& x, const float* given, int edge, int col) {
+  if (p.probe) return nullptr;
+  if (x.seg != edge) return p.seg_start + (((int64_t)x.bh * p.NS + x.seg) * p.dv + col) * p.dk;
+  return given ? given + ((int64_t)x.bh * p.dv + col) * p.dk : nullptr;
+}
+__device__ __forceinline__ float* walk_to(const DeltaParams& p, const Part& x, float* wanted, int edge, int col) {
+  const int64_t at = (int64_t)x.bh * p.NS + x.seg;
+  if (p.probe) return x.unit_columns ? p.seg_map + (at * p.dk + col) * p.dk : p.seg_add + (at * p.dv + col) * p.dk;
+  return wanted && x.seg == edge ? wanted + ((int64_t)x.bh * p.dv + col) * p.dk : nullptr;
 }
 
 template <typename T>
