@@ -9,9 +9,11 @@
 // repeat, where the powers of a Neumann series grow to 10^18.  Both walks need
 // (c_t / c_j) q_t.k_j on and below the diagonal, the backward one its transpose.
 //
-// One wave a chunk: there are B H T / 64 of them, all independent, so what can be
-// done here is taken off the walks, whose chunks follow one another.  The matrices
-// leave as the walks' operands, in bf16 parts.  Logarithms of the forget factors
+// There are B H T / 64 chunks, all independent, so what can be done here is taken
+// off the walks, whose chunks follow one another.  Four waves a chunk: wave w forms row
+// tile w of both products, inverts diagonal block w and then has the inverse's column
+// of blocks w, which depends on no other column.  The matrices leave as the walks'
+// operands, in bf16 parts.  Logarithms of the forget factors
 // are summed in 64 bits, so that a ratio c_t / c_j keeps fp32's precision however
 // strong the decay before it.
 #include "mesa_delta_tile.h"
@@ -22,22 +24,48 @@ namespace {
 
 constexpr int kLd = 20;  // floats of a 16-wide row in LDS
 
-constexpr int tile_of(int i, int j) { return i * (i + 1) / 2 + j; }
+__host__ __device__ constexpr int tile_of(int i, int j) { return i * (i + 1) / 2 + j; }
 
 template <int DK, bool BF16, bool TRANSPOSED>
-__global__ __launch_bounds__(64) void delta_chunk_kernel(DeltaParams p) {
+__global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
   constexpr int NP = BF16 ? 1 : 3, ES = BF16 ? 2 : 4, NA = BF16 && !TRANSPOSED ? 2 : 3;
   __shared__ __attribute__((aligned(16))) float low[10][16 * kLd];
   __shared__ __attribute__((aligned(16))) float diag[4][16 * kLd];
+  __shared__ __attribute__((aligned(16))) float products[4][256];  // A^T's tiles on their way to pairs of rows
   __shared__ double sg[kDeltaChunk];
   __shared__ float sbeta[kDeltaChunk];
-  const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const uint32_t unit = blockIdx.x;
   const int c = unit % p.NC, bh = unit / p.NC, b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk);
   const int live = min(delta_length(p, b) - c * kDeltaChunk, kDeltaChunk);
   if (live <= 0) return;
 
-  // gates: one token a lane
+  // 16 rows of 8 columns a lane group at a time
+  auto rows = [&](const DeltaRows& x, int i, u32x4 (&f)[DK / 32][BF16 ? 1 : 2]) {
+    const Window from = window_at(static_cast<const char*>(x.at) + (b * x.b + hk * x.h + (int64_t)(c * kDeltaChunk) * x.t) * ES);
+    const uint32_t at = 16 * i + r < live ? ((16 * i + r) * (uint32_t)x.t + 8 * g) * ES : kNowhere;
+#pragma unroll
+    for (int s = 0; s < DK / 32; ++s)
+#pragma unroll
+      for (int n = 0; n < (BF16 ? 1 : 2); ++n) f[s][n] = window_load(from, at, 32 * s * ES + 16 * n);
+  };
+  auto planes = [&](const u32x4 (&f)[BF16 ? 1 : 2]) {
+    if constexpr (BF16) {
+      Planes<1> x;
+      x.p[0] = __builtin_bit_cast(bf16x8, f[0]);
+      return x;
+    } else {
+      return split8<3>(__builtin_bit_cast(f32x4, f[0]), __builtin_bit_cast(f32x4, f[1]));
+    }
+  };
+  u32x4 k_raw[4][DK / 32][BF16 ? 1 : 2], q_raw[DK / 32][BF16 ? 1 : 2];
+  rows(p.k, wave, k_raw[3]);
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+    if (j < wave) rows(p.k, j, k_raw[j]);
+  if (p.q.at) rows(p.q, wave, q_raw);
+
+  // gates: one token a lane, the same in every wave
   double lg = 0.0;
   float beta = 0.f;
   if (lane < live) {
@@ -50,39 +78,18 @@ __global__ __launch_bounds__(64) void delta_chunk_kernel(DeltaParams p) {
     const double before = __shfl_up(lg, off);
     if (lane >= off) lg += before;
   }
-  sg[lane] = lg;
-  sbeta[lane] = beta;
-  if constexpr (!TRANSPOSED) {
-    DeltaGates& out = p.gates[unit];
-    out.g[lane] = lg;
-    out.c[lane] = decay(lg, 0.0);
-    out.tail[lane] = decay(__shfl(lg, 63), lg);
-    out.beta[lane] = beta;
+  if (wave == 0) {
+    sg[lane] = lg;
+    sbeta[lane] = beta;
+    if constexpr (!TRANSPOSED) {
+      DeltaGates& out = p.gates[unit];
+      out.g[lane] = lg;
+      out.c[lane] = decay(lg, 0.0);
+      out.tail[lane] = decay(__shfl(lg, 63), lg);
+      out.beta[lane] = beta;
+    }
   }
   __syncthreads();
-
-  // 16 rows of 8 columns a lane group at a time
-  auto rows = [&](const DeltaRows& x, int i, Planes<NP> (&f)[DK / 32]) {
-    const int row = 16 * i + r;
-    const char* at = static_cast<const char*>(x.at) +
-                     (b * x.b + hk * x.h + (int64_t)(c * kDeltaChunk + min(row, live - 1)) * x.t) * ES;
-#pragma unroll
-    for (int s = 0; s < DK / 32; ++s) {
-      const u32x4* from = reinterpret_cast<const u32x4*>(at + (32 * s + 8 * g) * ES);
-      if constexpr (BF16) {
-        u32x4 v = from[0];
-        if (row >= live) v = u32x4{0, 0, 0, 0};
-        f[s].p[0] = __builtin_bit_cast(bf16x8, v);
-      } else {
-        f32x4 x0 = __builtin_bit_cast(f32x4, from[0]), x1 = __builtin_bit_cast(f32x4, from[1]);
-        if (row >= live) x0 = x1 = f32x4{0.f, 0.f, 0.f, 0.f};
-        f[s] = split8<NP>(x0, x1);
-      }
-    }
-  };
-  Planes<NP> k[4][DK / 32];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) rows(p.k, i, k[i]);
 
   char* const to = (TRANSPOSED ? p.matrices_t : p.matrices) + (int64_t)unit * delta_matrix_bytes(NA) + lane * 16;
   // A block's two tiles, in parts, to its place
@@ -94,132 +101,139 @@ __global__ __launch_bounds__(64) void delta_chunk_kernel(DeltaParams p) {
         *reinterpret_cast<bf16x8*>(to + (matrix * 3 + n) * kBlocksBytes + block * 1024) = f.p[n];
   };
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  f32x4 even[4] = {zero, zero, zero, zero};
 
-  if (p.q.at) {  // queries and keys: a lane has one query and 4 keys of a tile, transposed the other way round
+  // Row tile `wave`: keys with keys, and queries with keys (a lane has one query and 4 keys of
+  // a tile, transposed the other way round).
+  f32x4 kk[4] = {zero, zero, zero, zero}, a[4] = {zero, zero, zero, zero};  // [3]: the diagonal tile
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      Planes<NP> q[DK / 32];
-      rows(p.q, t, q);
-      f32x4 a[4] = {zero, zero, zero, zero};
+  for (int s = 0; s < DK / 32; ++s) {
+    const auto own = planes(k_raw[3][s]);
+    Planes<NP> q;
+    if (p.q.at) q = planes(q_raw[s]);
 #pragma unroll
-      for (int j = 0; j <= t; ++j) {
+    for (int j = 0; j < 4; ++j) {
+      if (j < 3 && j >= wave) continue;
+      const auto k = planes(k_raw[j][s]);
+      kk[j] = mma<2>(own, k, kk[j]);
+      if (p.q.at) a[j] = TRANSPOSED ? mma<2>(q, k, a[j]) : mma<2>(k, q, a[j]);
+    }
+  }
 #pragma unroll
-        for (int s = 0; s < DK / 32; ++s)
-          a[j] = TRANSPOSED ? mma<2>(q[s], k[j][s], a[j]) : mma<2>(k[j][s], q[s], a[j]);
+  for (int j = 0; j < 4; ++j) {
+    if (j < 3 && j >= wave) continue;
+    const int tile = j < 3 ? j : wave, col = 16 * tile + r;
+    const double gj = sg[col];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int at_t = 16 * t + (TRANSPOSED ? 4 * g + e : r), at_j = 16 * j + (TRANSPOSED ? r : 4 * g + e);
-          a[j][e] = at_j <= at_t ? a[j][e] * decay(sg[at_t], sg[at_j]) : 0.f;
-        }
-      }
-      if constexpr (!TRANSPOSED) {
-#pragma unroll
-        for (int s = 0; s <= t / 2; ++s) put(1, NA, lower_block(t, s), a[2 * s], a[2 * s + 1]);
+    for (int e = 0; e < 4; ++e) {
+      const int t = 16 * wave + 4 * g + e;
+      const float d = decay(sg[t], gj);
+      const float x = kk[j][e] * d * (TRANSPOSED ? sbeta[t] : sbeta[col]);
+      low[tile_of(wave, tile)][(4 * g + e) * kLd + r] = col < t ? x : 0.f;
+      if constexpr (TRANSPOSED) {
+        a[j][e] = col <= t ? a[j][e] * d : 0.f;
       } else {
-        // blocks of a transposed matrix pair up tiles of two queries
-        if (t & 1) {
+        const int at_t = 16 * wave + r, at_j = 16 * tile + 4 * g + e;
+        a[j][e] = at_j <= at_t ? a[j][e] * decay(sg[at_t], sg[at_j]) : 0.f;
+      }
+    }
+  }
+  if (p.q.at) {
+    if constexpr (!TRANSPOSED) {
+      const f32x4 d = a[3];
+      if (wave == 0) put(1, NA, lower_block(0, 0), d, zero);
+      else put(1, NA, lower_block(wave, 0), a[0], wave == 1 ? d : a[1]);
+      if (wave >= 2) put(1, NA, lower_block(wave, 1), wave == 2 ? d : a[2], wave == 2 ? zero : d);
+    } else if (!(wave & 1)) {  // blocks of a transposed matrix pair up tiles of two queries: an even wave's go to the next
 #pragma unroll
-          for (int j = 0; j <= t; ++j) put(1, NA, upper_block(j, t / 2), j < t ? even[j] : zero, a[j]);
-        }
+      for (int j = 0; j < 3; ++j)
+        if (j < wave) *reinterpret_cast<f32x4*>(&products[j + wave / 2][lane * 4]) = a[j];
+      *reinterpret_cast<f32x4*>(&products[wave == 0 ? 0 : 3][lane * 4]) = a[3];
+    }
+  }
+  __syncthreads();
+  if constexpr (TRANSPOSED) {
+    if (p.q.at && (wave & 1)) {
+      // wave 1: columns 0 (tiles 0 and 1) and 1 (nothing and 1); wave 3: columns 0 .. 2 with tile 2, 3 without
 #pragma unroll
-        for (int j = 0; j < 4; ++j) even[j] = a[j];
+      for (int j = 0; j < 4; ++j) {
+        if (j > wave) continue;
+        f32x4 even = zero;
+        if (j < wave) even = *reinterpret_cast<const f32x4*>(&products[wave == 1 ? 0 : j == 2 ? 3 : j + 1][lane * 4]);
+        put(1, NA, upper_block(j, wave / 2), even, j == wave ? a[3] : a[j]);
       }
     }
   }
 
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j <= i; ++j) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < DK / 32; ++s) acc = mma<2>(k[i][s], k[j][s], acc);
-      const int col = 16 * j + r;
-      const double gj = sg[col];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = 16 * i + 4 * g + e;
-        const float x = acc[e] * decay(sg[t], gj) * (TRANSPOSED ? sbeta[t] : sbeta[col]);
-        low[tile_of(i, j)][(4 * g + e) * kLd + r] = col < t ? x : 0.f;
-      }
-    }
-  __syncthreads();
-
-  {  // lane group g inverts diagonal block g, lane r its column r
-    const float* l = low[tile_of(g, g)];
+  {  // diagonal block `wave`, lane r (of each lane group) its column r
+    const float* l = low[tile_of(wave, wave)];
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float s = i == r ? 1.f : 0.f;
 #pragma unroll
       for (int m4 = 0; m4 < i; m4 += 4) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(l + i * kLd + m4);
+        const f32x4 v = *reinterpret_cast<const f32x4*>(l + i * kLd + m4);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (m4 + e < i) s = fmaf(-a[e], x[m4 + e], s);
+          if (m4 + e < i) s = fmaf(-v[e], x[m4 + e], s);
       }
       x[i] = s;
     }
+    if (g == 0)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) diag[g][i * kLd + r] = x[i];
+      for (int i = 0; i < 16; ++i) diag[wave][i * kLd + r] = x[i];
   }
   __syncthreads();
 
-  f32x4 t[4][4];  // T_ij, rows 4 g + e, column r
+  f32x4 t[4];  // T_ij of column j = wave, rows 4 g + e, column r
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 4; ++i) {
+    t[i] = zero;
+    if (i < wave) continue;
+    if (i == wave) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) t[i][i][e] = diag[i][(4 * g + e) * kLd + r];
-#pragma unroll
-  for (int s = 1; s < 4; ++s)
-#pragma unroll
-    for (int i = s; i < 4; ++i) {
-      const int j = i - s;
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f}, out = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        if (m < j || m >= i) continue;
-        const f32x4 a = *reinterpret_cast<const f32x4*>(&low[tile_of(i, m)][r * kLd + 4 * g]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc = mfma_f32(a[e], t[m][j][e], acc);
-      }
-      const f32x4 d = *reinterpret_cast<const f32x4*>(&diag[i][r * kLd + 4 * g]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) out = mfma_f32(d[e], acc[e], out);
-      t[i][j] = -out;
+      for (int e = 0; e < 4; ++e) t[i][e] = diag[i][(4 * g + e) * kLd + r];
+      continue;
     }
+    f32x4 acc = zero, out = zero;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if (m < wave || m >= i) continue;
+      const f32x4 x = *reinterpret_cast<const f32x4*>(&low[tile_of(i, m)][r * kLd + 4 * g]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc = mfma_f32(x[e], t[m][e], acc);
+    }
+    const f32x4 d = *reinterpret_cast<const f32x4*>(&diag[i][r * kLd + 4 * g]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out = mfma_f32(d[e], acc[e], out);
+    t[i] = -out;
+  }
 
   // a lane's 4 numbers lie along the later product's inner index: rows of the
   // transposed inverse as they are, rows of the inverse by way of LDS
   if constexpr (TRANSPOSED) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int s = j / 2; s < 2; ++s)
-        put(0, 3, upper_block(j, s), 2 * s < j ? zero : t[2 * s][j], t[2 * s + 1][j]);
+    if (wave < 2) put(0, 3, upper_block(wave, 0), t[0], t[1]);
+    put(0, 3, upper_block(wave, 1), t[2], t[3]);
   } else {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+      if (i < wave) continue;
 #pragma unroll
-      for (int j = 0; j <= i; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) low[tile_of(i, j)][(4 * g + e) * kLd + r] = t[i][j][e];
+      for (int e = 0; e < 4; ++e) low[tile_of(i, wave)][(4 * g + e) * kLd + r] = t[i][e];
+    }
     __syncthreads();
-    auto row = [&](int i, int j) { return *reinterpret_cast<const f32x4*>(&low[tile_of(i, j)][r * kLd + 4 * g]); };
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int s = 0; s <= i / 2; ++s) put(0, 3, lower_block(i, s), row(i, 2 * s), 2 * s + 1 <= i ? row(i, 2 * s + 1) : zero);
+    auto row = [&](int j) { return *reinterpret_cast<const f32x4*>(&low[tile_of(wave, j)][r * kLd + 4 * g]); };
+    put(0, 3, lower_block(wave, 0), row(0), wave >= 1 ? row(1) : zero);
+    if (wave >= 2) put(0, 3, lower_block(wave, 1), row(2), wave == 3 ? row(3) : zero);
   }
 }
 
 template <int DK, bool BF16>
 hipError_t launch(bool transposed, const DeltaParams& p, hipStream_t s) {
   const dim3 grid((uint32_t)((int64_t)p.B * p.H * p.NC));
-  if (transposed) delta_chunk_kernel<DK, BF16, true><<<grid, 64, 0, s>>>(p);
-  else delta_chunk_kernel<DK, BF16, false><<<grid, 64, 0, s>>>(p);
+  if (transposed) delta_chunk_kernel<DK, BF16, true><<<grid, 256, 0, s>>>(p);
+  else delta_chunk_kernel<DK, BF16, false><<<grid, 256, 0, s>>>(p);
   return hipGetLastError();
 }
 

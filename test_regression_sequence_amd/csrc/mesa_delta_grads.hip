@@ -33,75 +33,40 @@ struct GradLds {
 };
 
 template <int DK, bool BF16>
-__global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
+__global__ __launch_bounds__(512, 2) void delta_grads_kernel(DeltaParams p) {
   using L = GradLds<DK, BF16>;
   using Out = std::conditional_t<BF16, __bf16, float>;
   constexpr int NP = L::NP, NZ = L::NZ, MH = DK / 32, KS = DK / 32, OMAX = BF16 ? 1 : 2;
   constexpr int kPieces = 8 * DK, NS = (kPieces + 511) / 512;  // 16-byte pieces of a state's slice
   __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
   __shared__ __attribute__((aligned(16))) DeltaGates gates;
-  __shared__ float cols[8][64], part[2][64], behind[2][64], dbetas[64], gammas[64], red[8];
+  __shared__ float cols[8][64], rest[2][64], diag[2][64], part[2][64], behind[2][64], dbetas[64], gammas[64], red[8];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
-  const int tile = wave & 3, half = wave >> 2;
+  // waves w and w + 4 share a SIMD: tiles 0 .. 3 have 1 .. 4 tiles of pairs
+  const int half = wave >> 2, tile = half ? 7 - wave : wave;
+  const int own = 16 * tile + r;  // this lane's token
+  // a thread's pieces of a slice: 4 columns of a row of the states, and of a token (row `from`) of W, E and dO
+  const int from = tid >> 3, at4 = (tid & 7) * 4;
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  cols[wave][lane] = 0.f;
+  const TileRows<DK> rows(lane);
+  const TileRows<32> slice_rows(lane);
+  const TileRows<64> pair_rows(lane);
+  const TileColumns<DK, MH> columns(lane, MH * half);
+  const TileColumns<64, 1> pair_columns(lane, tile);
+
   const int64_t unit = blockIdx.x;
   const int c = (int)(unit % p.NC), bh = (int)(unit / p.NC), b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk);
-  const int t0 = c * 64, live = min(delta_length(p, b) - t0, 64), here = min(p.T - t0, 64);
-  const int own = 16 * tile + r;  // this lane's token
+  const int64_t t0 = 64 * (int64_t)c;
+  const int live = min(delta_length(p, b) - (int)t0, 64), here = min(p.T - (int)t0, 64);
   const bool there = own < here, valid = own < live;
-  const int64_t tok = t0 + own;
-  const int64_t v_at = b * p.dv_.b + h * p.dv_.h + tok * p.dv_.t + 4 * g;
-  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-
-  auto put = [&](const f32x4 (&dq)[MH], const f32x4 (&dk)[MH]) {
-    if (!there) return;
-    const int at = 16 * MH * half + 4 * g;
-    if (p.dq_heads) {
-      const int64_t to = ((int64_t)bh * p.T + tok) * DK + at;
-#pragma unroll
-      for (int i = 0; i < MH; ++i) {
-        *reinterpret_cast<f32x4*>(p.dq_heads + to + 16 * i) = dq[i];
-        *reinterpret_cast<f32x4*>(p.dk_heads + to + 16 * i) = dk[i];
-      }
-    } else {
-      const int64_t q_at = b * p.dq.b + hk * p.dq.h + tok * p.dq.t + at, k_at = b * p.dk_.b + hk * p.dk_.h + tok * p.dk_.t + at;
-#pragma unroll
-      for (int i = 0; i < MH; ++i) {
-        store_out4<Out>(p.dq.at, q_at + 16 * i, dq[i]);
-        store_out4<Out>(p.dk_.at, k_at + 16 * i, dk[i]);
-      }
-    }
-  };
-
-  f32x4 aq[MH], ak[MH], ad[MH];  // dO S0, E S0, U dS: columns 16 (MH half + i) + 4 g + e
-#pragma unroll
-  for (int i = 0; i < MH; ++i) aq[i] = ak[i] = ad[i] = zero;
-  if (live <= 0) {
-    put(aq, ak);
-    if (there) {
-      for (int j = half; 16 * j < p.dv; j += 2) store_out4<Out>(p.dv_.at, v_at + 16 * j, zero);
-      if (g == 0 && half == 0) *gate_at(p.dgamma, b, h, tok) = *gate_at(p.dbeta, b, h, tok) = 0.f;
-    }
-    return;
-  }
-
-  if (tid < (int)sizeof(DeltaGates) / 16)
-    reinterpret_cast<u32x4*>(&gates)[tid] = reinterpret_cast<const u32x4*>(p.gates + unit)[tid];
-  if (tid < 64) gammas[tid] = tid < live ? *gate_at(p.gamma, b, h, t0 + tid) : 1.f;
-  cols[wave][lane] = 0.f;
-
-  const float beta_own = valid ? *gate_at(p.beta, b, h, tok) : 0.f;
-  // A thread's pieces of a slice: 4 columns of a row of the states, and of a token (row `from`) of W, E and dO
-  const int from = tid >> 3, at4 = (tid & 7) * 4;
-  const float beta_from = from < live ? *gate_at(p.beta, b, h, t0 + from) : 0.f;
-  const Window states = window_at(p.states + unit * p.dv * DK), dstates = window_at(p.dstates + unit * p.dv * DK),
-               ws = window_at(p.w + unit * 64 * p.dv), es = window_at(p.e + unit * 64 * p.dv),
-               dos = window_at(static_cast<const char*>(p.d_o.at) +
-                               (b * p.d_o.b + h * p.d_o.h + (int64_t)t0 * p.d_o.t) * sizeof(Out)),
-               dvs = window_at(static_cast<char*>(p.dv_.at) +
-                               (b * p.dv_.b + h * p.dv_.h + (int64_t)t0 * p.dv_.t) * sizeof(Out));
   const uint32_t w_at = (from * p.dv + at4) * 4, do_at = (from * (uint32_t)p.d_o.t + at4) * sizeof(Out),
                  dv_at = (from * (uint32_t)p.dv_.t + at4) * sizeof(Out);
   f32x4 sl[NS], dl[NS], wl, el, ol;
+  const Window states = window_at(p.states + unit * p.dv * DK), dstates = window_at(p.dstates + unit * p.dv * DK),
+               ws = window_at(p.w + unit * 64 * p.dv), es = window_at(p.e + unit * 64 * p.dv),
+               dos = window_at(static_cast<const char*>(p.d_o.at) + (b * p.d_o.b + h * p.d_o.h + t0 * p.d_o.t) * sizeof(Out)),
+               dvs = window_at(static_cast<char*>(p.dv_.at) + (b * p.dv_.b + h * p.dv_.h + t0 * p.dv_.t) * sizeof(Out));
   auto load = [&](int d0) {
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
@@ -115,13 +80,49 @@ __global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
     el = __builtin_bit_cast(f32x4, window_load(es, there ? w_at : kNowhere, d0 * 4));
     ol = window_row<BF16>(dos, there && from < live ? do_at : kNowhere, d0 * sizeof(Out));
   };
+  RowLoads<DK, BF16, 512> kl, ql;
+  CopyLoads<sizeof(DeltaGates), 512> gl;
+
+  const bool heads = p.dq_heads != nullptr;
+  const int at_key = 16 * MH * half + 4 * g;
+  const int64_t heads_at = ((int64_t)bh * p.T + t0) * DK;
+  const Window dqs = heads ? window_at(p.dq_heads + heads_at)
+                           : window_at(static_cast<char*>(p.dq.at) + (b * p.dq.b + hk * p.dq.h + t0 * p.dq.t) * sizeof(Out));
+  const Window dks = heads ? window_at(p.dk_heads + heads_at)
+                           : window_at(static_cast<char*>(p.dk_.at) + (b * p.dk_.b + hk * p.dk_.h + t0 * p.dk_.t) * sizeof(Out));
+  auto put = [&](const f32x4 (&dq)[MH], const f32x4 (&dk)[MH]) {
+#pragma unroll
+    for (int i = 0; i < MH; ++i) {
+      if (heads) {
+        const uint32_t to = there ? (own * DK + at_key) * 4 : kNowhere;
+        window_store(dqs, to, 64 * i, dq[i]);
+        window_store(dks, to, 64 * i, dk[i]);
+      } else {
+        window_store_row<BF16>(dqs, there ? (own * (uint32_t)p.dq.t + at_key) * sizeof(Out) : kNowhere, 16 * i * sizeof(Out), dq[i]);
+        window_store_row<BF16>(dks, there ? (own * (uint32_t)p.dk_.t + at_key) * sizeof(Out) : kNowhere, 16 * i * sizeof(Out), dk[i]);
+      }
+    }
+  };
+
+  f32x4 aq[MH], ak[MH], ad[MH];  // dO S0, E S0, U dS: columns 16 (MH half + i) + 4 g + e
+#pragma unroll
+  for (int i = 0; i < MH; ++i) aq[i] = ak[i] = ad[i] = zero;
+  if (live <= 0) {  // behind the sequence
+    put(aq, ak);
+    for (int d0 = 0; d0 < p.dv; d0 += 32)
+      window_store_row<BF16>(dvs, from < here && at4 < p.dv - d0 ? dv_at : kNowhere, d0 * sizeof(Out), zero);
+    if (tid < here) *gate_at(p.dgamma, b, h, t0 + tid) = *gate_at(p.dbeta, b, h, t0 + tid) = 0.f;
+    return;
+  }
 
   f32x4 zy[4] = {zero, zero, zero, zero};  // rows j, a lane's token t: U dO^T (half 0) or U E^T (half 1)
   float dbeta = 0.f, along = 0.f;
-  RowLoads<DK, BF16, 512> kl, ql;
+  const float beta_from = p.gates[unit].beta[from];
+  load(0);
   kl.load(p.k.at, b * p.k.b + hk * p.k.h + t0 * p.k.t, p.k.t, live, DK, tid);
   ql.load(p.q.at, b * p.q.b + hk * p.q.h + t0 * p.q.t, p.q.t, live, DK, tid);
-  load(0);
+  gl.load(p.gates + unit, tid);
+  if (tid < 64) gammas[tid] = tid < live ? *gate_at(p.gamma, b, h, t0 + tid) : 1.f;
   for (int d0 = 0; d0 < p.dv; d0 += 32) {
     __syncthreads();
 #pragma unroll
@@ -141,13 +142,13 @@ __global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
     }
     {
       const uint32_t at = tile_at<32>(from, 2 * at4);
-      bf16x4 u[3], x[3], o[NP];
-      split4<3>(wl * beta_from, u);
+      bf16x4 uu[3], x[3], o[NP];
+      split4<3>(wl * beta_from, uu);
       split4<3>(el, x);
       split4<NP>(ol, o);
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
-        *reinterpret_cast<bf16x4*>(lds + L::kUAt + i * L::kU + at) = u[i];
+        *reinterpret_cast<bf16x4*>(lds + L::kUAt + i * L::kU + at) = uu[i];
         *reinterpret_cast<bf16x4*>(lds + L::kEAt + i * L::kU + at) = x[i];
         if (i < NP) *reinterpret_cast<bf16x4*>(lds + L::kOAt + i * L::kU + at) = o[i];
       }
@@ -155,39 +156,40 @@ __global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
 #pragma unroll
       for (int n = 0; n < 4; ++n) dbeta = fmaf(el[n], wl[n], dbeta);
     }
-    load(d0 + 32);  // (behind the last slice: zeros)
+    load(d0 + 32);  // (behind the last slice: zeros; with a branch around it the compiler waits, 767 -> 835 us)
     __syncthreads();
-    const Planes<NP> of = rows_of<32, NP>(lds + L::kOAt, L::kU, 16 * tile, 0, lane);
-    const Planes<3> ef = rows_of<32, 3>(lds + L::kEAt, L::kU, 16 * tile, 0, lane);
-    const Planes<3> uf = rows_of<32, 3>(lds + L::kUAt, L::kU, 16 * tile, 0, lane);
+    const Planes<NP> of = slice_rows.template planes<NP>(lds + L::kOAt, L::kU, 16 * tile, 0);
+    const Planes<3> ef = slice_rows.template planes<3>(lds + L::kEAt, L::kU, 16 * tile, 0);
+    const Planes<3> uf = slice_rows.template planes<3>(lds + L::kUAt, L::kU, 16 * tile, 0);
 #pragma unroll
     for (int i = 0; i < MH; ++i) {
-      const Planes<3> s = columns_of<DK, 3>(lds + L::kS, L::kState, 0, MH * half + i, lane);
+      const Planes<3> s = columns.template planes<3>(lds + L::kS, L::kState, 0, i);
       aq[i] = mma<2>(s, of, aq[i]);
       ak[i] = mma<2>(s, ef, ak[i]);
-      ad[i] = mma<2>(columns_of<DK, 3>(lds + L::kD, L::kState, 0, MH * half + i, lane), uf, ad[i]);
+      ad[i] = mma<2>(columns.template planes<3>(lds + L::kD, L::kState, 0, i), uf, ad[i]);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (j <= tile) {
-        const Planes<3> u = rows_of<32, 3>(lds + L::kUAt, L::kU, 16 * j, 0, lane);
-        zy[j] = half ? mma<2>(u, ef, zy[j]) : mma<2>(u, of, zy[j]);
+        const Planes<3> x = slice_rows.template planes<3>(lds + L::kUAt, L::kU, 16 * j, 0);
+        zy[j] = half ? mma<2>(x, ef, zy[j]) : mma<2>(x, of, zy[j]);
       }
   }
 
   __syncthreads();
   kl.store(lds + L::kK, L::kPlane, tid);
   ql.store(lds + L::kQ, L::kPlane, tid);
+  gl.store(reinterpret_cast<char*>(&gates), tid);
   __syncthreads();
 
-  float sum = 0.f, carry = 0.f;
+  float sum = 0.f, earlier = 0.f;
+  const float beta_own = gates.beta[own];
   char* const pairs = lds + (half ? L::kYAt : L::kZAt);
   {
     Planes<NP> f[KS];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) f[s] = rows_of<DK, NP>(lds + (half ? L::kK : L::kQ), L::kPlane, 16 * tile, s, lane);
+    for (int s = 0; s < KS; ++s) f[s] = rows.template planes<NP>(lds + (half ? L::kK : L::kQ), L::kPlane, 16 * tile, s);
     const double gt = gates.g[own];
-    const int last = own - half;  // Y has no diagonal
     const float weight = half ? -beta_own : 1.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -196,27 +198,37 @@ __global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
         f32x4 dot = zero;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
-          dot = mma<2>(rows_of<DK, NP>(lds + L::kK, L::kPlane, 16 * j, s, lane), f[s], dot);
-        float before[4], run = 0.f;  // the sums of this row's pairs in front of each
+          dot = mma<2>(rows.template planes<NP>(lds + L::kK, L::kPlane, 16 * j, s), f[s], dot);
+        const int at = 16 * j + 4 * g;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int at = 16 * j + 4 * g + e;
-          x[e] = at <= last ? zy[j][e] * decay(gt, gates.g[at]) * weight : 0.f;
-          before[e] = run;
-          run += at <= last ? x[e] * dot[e] : 0.f;
-        }
-        float front = carry;
+        for (int e = 0; e < 4; ++e) x[e] = zy[j][e] * decay(gt, gates.g[at + e]) * weight;
+        if (j < tile) {  // pairs with tokens of earlier tiles: sums over them, and over the tile's tokens
 #pragma unroll
-        for (int n = 1; n < 4; ++n) {
-          const float of_group = __shfl_up(run, 16 * n);
-          if (g >= n) front += of_group;
-        }
-        carry += sum_lane_groups(run);
+          for (int e = 0; e < 4; ++e) {
+            earlier += x[e] * dot[e];
+            const float column = group_sum<16>(x[e] * dot[e]);
+            if (r == 0) cols[wave][at + e] = column;
+          }
+        } else {  // pairs within the tile, for each token i those with t >= i > j
+          const int last = own - half;  // Y has no diagonal
+          float before[4], run = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int at = 16 * j + 4 * g + e;
-          const float column = group_sum<16>(at <= own ? front + before[e] : 0.f);
-          if (r == 0) cols[wave][at] = column;
+          for (int e = 0; e < 4; ++e) {
+            x[e] = at + e <= last ? x[e] : 0.f;
+            before[e] = run;
+            run += at + e <= last ? x[e] * dot[e] : 0.f;
+          }
+          float front = 0.f;
+#pragma unroll
+          for (int n = 1; n < 4; ++n) {
+            const float of_group = __shfl_up(run, 16 * n);
+            if (g >= n) front += of_group;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float column = group_sum<16>(at + e <= own ? front + before[e] : 0.f);
+            if (r == 0) diag[half][at + e] = column;
+          }
         }
       }
       if (j <= (tile | 1)) {
@@ -232,8 +244,8 @@ __global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
   float left = 0.f;  // what this token leaves behind the chunk
 #pragma unroll
   for (int i = 0; i < MH; ++i) {
-    const f32x4 q = row_values<DK, NP>(lds + L::kQ, L::kPlane, 16 * tile, MH * half + i, lane);
-    const f32x4 k = row_values<DK, NP>(lds + L::kK, L::kPlane, 16 * tile, MH * half + i, lane);
+    const f32x4 q = (half ? rows.template values<NP>(lds + L::kQ, L::kPlane, 16 * tile, MH + i) : rows.template values<NP>(lds + L::kQ, L::kPlane, 16 * tile, i));
+    const f32x4 k = (half ? rows.template values<NP>(lds + L::kK, L::kPlane, 16 * tile, MH + i) : rows.template values<NP>(lds + L::kK, L::kPlane, 16 * tile, i));
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       sum += cc * q[e] * aq[i][e] - cb * k[e] * ak[i][e];
@@ -244,11 +256,13 @@ __global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
   }
   sum = sum_lane_groups(sum);
   left = sum_lane_groups(left);
+  earlier = sum_lane_groups(earlier);
   dbeta = group_sum<8>(dbeta);
   along = wave_sum(along);
   if (g == 0) {
     part[half][own] = sum;
     behind[half][own] = left;
+    rest[half][own] = earlier;
   }
   if ((tid & 7) == 0) dbetas[from] = dbeta;
   if (lane == 0) red[wave] = along;
@@ -257,22 +271,22 @@ __global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     if (2 * s <= tile) {
-      const Planes<NZ> zf = rows_of<64, NZ>(lds + L::kZAt, L::kZ, 16 * tile, s, lane);
-      const Planes<NZ> yf = rows_of<64, NZ>(lds + L::kYAt, L::kZ, 16 * tile, s, lane);
+      const Planes<NZ> zf = pair_rows.template planes<NZ>(lds + L::kZAt, L::kZ, 16 * tile, s);
+      const Planes<NZ> yf = pair_rows.template planes<NZ>(lds + L::kYAt, L::kZ, 16 * tile, s);
 #pragma unroll
       for (int i = 0; i < MH; ++i) {
-        const Planes<NP> k = columns_of<DK, NP>(lds + L::kK, L::kPlane, 32 * s, MH * half + i, lane);
+        const Planes<NP> k = columns.template planes<NP>(lds + L::kK, L::kPlane, 32 * s, i);
         aq[i] = mma<OMAX>(k, zf, aq[i]);
         ak[i] = mma<OMAX>(k, yf, ak[i]);
       }
     }
     if (2 * s + 1 >= tile) {
-      const Planes<NZ> zf = columns_of<64, NZ>(lds + L::kZAt, L::kZ, 32 * s, tile, lane);
-      const Planes<NZ> yf = columns_of<64, NZ>(lds + L::kYAt, L::kZ, 32 * s, tile, lane);
+      const Planes<NZ> zf = pair_columns.template planes<NZ>(lds + L::kZAt, L::kZ, 32 * s, 0);
+      const Planes<NZ> yf = pair_columns.template planes<NZ>(lds + L::kYAt, L::kZ, 32 * s, 0);
 #pragma unroll
       for (int i = 0; i < MH; ++i) {
-        ak[i] = mma<OMAX>(columns_of<DK, NP>(lds + L::kQ, L::kPlane, 32 * s, MH * half + i, lane), zf, ak[i]);
-        ak[i] = mma<OMAX>(columns_of<DK, NP>(lds + L::kK, L::kPlane, 32 * s, MH * half + i, lane), yf, ak[i]);
+        ak[i] = mma<OMAX>(columns.template planes<NP>(lds + L::kQ, L::kPlane, 32 * s, i), zf, ak[i]);
+        ak[i] = mma<OMAX>(columns.template planes<NP>(lds + L::kK, L::kPlane, 32 * s, i), yf, ak[i]);
       }
     }
   }
@@ -282,26 +296,44 @@ __global__ __launch_bounds__(512, 1) void delta_grads_kernel(DeltaParams p) {
   }
   put(aq, ak);
 
-  // the gradient at log gamma_i, each term added up where it counts and nowhere taken away again:
-  // what tokens t >= i read of S0, what tokens j < i leave behind, S0 -> S', and pairs t >= i > j
+  // The gradient at log gamma_i, each term added up where it counts and nowhere taken away again:
+  // what tokens t >= i read of S0, what tokens j < i leave behind, S0 -> S', and the pairs t >= i > j:
+  // those within i's tile, those of t >= i in it with earlier tiles, those of later tiles with j < i.
   if (wave == 0) {
+    const int in = lane >> 4;
     double x = (double)part[0][lane] + part[1][lane], y = (double)behind[0][lane] + behind[1][lane], whole = 0.0;
+    float tiles = rest[0][lane] + rest[1][lane], later[3];
+#pragma unroll
+    for (int t = 1; t < 4; ++t) later[t - 1] = lane < 16 * t ? cols[t][lane] + cols[7 - t][lane] : 0.f;
 #pragma unroll
     for (int off = 1; off < 64; off *= 2) {
       const double after = __shfl_down(x, off), before = __shfl_up(y, off);
       if (lane + off < 64) x += after;
       if (lane >= off) y += before;
+      if (off < 16) {
+        const float below = __shfl_down(tiles, off);
+        if (r + off < 16) tiles += below;
+      }
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        const float above = __shfl_up(later[t], off);
+        if (lane >= off) later[t] += above;
+      }
     }
     y = __shfl_up(y, 1);
     if (lane > 0) x += y;
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      x += cols[n][lane];
-      whole += red[n];
+    for (int t = 1; t < 4; ++t) {
+      const float above = __shfl_up(later[t - 1], 1);
+      if (lane > 0 && in < t) x += above;
     }
+    x += (double)tiles + diag[0][lane] + diag[1][lane];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) whole += red[n];
     x += gates.c[63] * whole;
     if (lane < here) {
-      *gate_at(p.dgamma, b, h, t0 + lane) = lane < live ? (float)(x / (double)gammas[lane]) : 0.f;
+      *gate_at(p.dgamma, b, h, t0 + lane) =
+          lane < live ? (float)(x / (double)gammas[lane]) : 0.f;
       *gate_at(p.dbeta, b, h, t0 + lane) = lane < live ? dbetas[lane] : 0.f;
     }
   }

@@ -136,7 +136,7 @@ __device__ __forceinline__ Planes<N> rows_of(const char* tile, int plane, int ro
 }
 
 // A lane's places in a tile's first rows, computed once: the same operands as
-// rows_of and columns_of from any multiple of 16 rows on (one plane).
+// rows_of and columns_of from any multiple of 16 rows on.
 template <int W>
 struct TileRows {
   uint32_t at[W / 16];
@@ -144,29 +144,54 @@ struct TileRows {
 #pragma unroll
     for (int j = 0; j < W / 16; ++j) at[j] = tile_at<W>(lane & 15, 32 * j + 8 * (lane >> 4));
   }
+  template <int N>
+  __device__ __forceinline__ Planes<N> planes(const char* tile, int plane, int row0, int s) const {
+    Planes<N> r;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      r.p[n] = join(*reinterpret_cast<const bf16x4*>(tile + at[2 * s] + n * plane + row0 * 2 * W),
+                    *reinterpret_cast<const bf16x4*>(tile + at[2 * s + 1] + n * plane + row0 * 2 * W));
+    return r;
+  }
   __device__ __forceinline__ Planes<1> operator()(const char* tile, int row0, int s) const {
-    Planes<1> r;
-    r.p[0] = join(*reinterpret_cast<const bf16x4*>(tile + at[2 * s] + row0 * 2 * W),
-                  *reinterpret_cast<const bf16x4*>(tile + at[2 * s + 1] + row0 * 2 * W));
+    return planes<1>(tile, 0, row0, s);
+  }
+  // columns 16 col + 4 g .. +3 of a lane's row
+  template <int N>
+  __device__ __forceinline__ f32x4 values(const char* tile, int plane, int row0, int col) const {
+    f32x4 r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int n = N - 1; n >= 0; --n) {
+      const bf16x4 v = *reinterpret_cast<const bf16x4*>(tile + at[col] + n * plane + row0 * 2 * W);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] += (float)v[e];
+    }
     return r;
   }
 };
-template <int W>
+// COLS: 16-wide tiles of columns from `first` on.
+template <int W, int COLS = W / 16>
 struct TileColumns {
-  uint32_t at[W / 16];
-  __device__ __forceinline__ explicit TileColumns(int lane) {
+  uint32_t at[COLS];
+  __device__ __forceinline__ explicit TileColumns(int lane, int first = 0) {
 #pragma unroll
-    for (int j = 0; j < W / 16; ++j) at[j] = tile_at<W>(4 * (lane >> 4) + ((lane & 15) >> 2), 32 * j + 8 * (lane & 3));
+    for (int j = 0; j < COLS; ++j)
+      at[j] = tile_at<W>(4 * (lane >> 4) + ((lane & 15) >> 2), 32 * (first + j) + 8 * (lane & 3));
   }
   __device__ __forceinline__ bf16x4 four(const char* tile, int row0, int col) const {
     const s16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
         (__attribute__((address_space(3))) s16x4*)(const_cast<char*>(tile + at[col] + row0 * 2 * W)));
     return __builtin_bit_cast(bf16x4, r);
   }
-  __device__ __forceinline__ Planes<1> operator()(const char* tile, int row0, int col) const {
-    Planes<1> r;
-    r.p[0] = join(four(tile, row0, col), four(tile, row0 + 16, col));
+  template <int N>
+  __device__ __forceinline__ Planes<N> planes(const char* tile, int plane, int row0, int col) const {
+    Planes<N> r;
+#pragma unroll
+    for (int n = 0; n < N; ++n) r.p[n] = join(four(tile + n * plane, row0, col), four(tile + n * plane, row0 + 16, col));
     return r;
+  }
+  __device__ __forceinline__ Planes<1> operator()(const char* tile, int row0, int col) const {
+    return planes<1>(tile, 0, row0, col);
   }
 };
 
@@ -197,20 +222,6 @@ __device__ __forceinline__ f32x4 column_values(const char* tile, int plane, int 
 #pragma unroll
   for (int n = N - 1; n >= 0; --n) {
     const bf16x4 v = column4<W>(tile + n * plane, row0, col, lane);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] += (float)v[e];
-  }
-  return r;
-}
-
-// Row row0 + lane % 16, columns 16 col + 4 g .. +3.
-template <int W, int N>
-__device__ __forceinline__ f32x4 row_values(const char* tile, int plane, int row0, int col, int lane) {
-  const uint32_t at = tile_at<W>(row0 + (lane & 15), 32 * col + 8 * (lane >> 4));
-  f32x4 r = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int n = N - 1; n >= 0; --n) {
-    const bf16x4 v = *reinterpret_cast<const bf16x4*>(tile + n * plane + at);
 #pragma unroll
     for (int e = 0; e < 4; ++e) r[e] += (float)v[e];
   }
