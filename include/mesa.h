@@ -676,7 +676,7 @@ mesa_status mesa_qk_preprocess_bwd(int32_t B, int32_t H, int32_t T, int32_t d, i
  *
  *   q, k      [B, Hk, T, dk] dtype, v, o [B, H, T, dv] dtype; head h of v, o and the
  *             gates uses the queries and keys of head h / (H / Hk)
- *   gamma, beta [B, H, T]    fp32: forget factor in (0, 1] and write strength
+ *   gamma, beta [B, H, T]    fp32: forget factor in [0, 1] and write strength
  *   s0        [B, H, dv, dk] fp32 or NULL   state before token 0 (NULL = 0), dense
  *   lengths   [B] int32 or NULL   valid tokens of each sequence (device memory;
  *             values outside 0..T count as 0 or T).  Rows and gates at and behind
@@ -690,7 +690,7 @@ mesa_status mesa_qk_preprocess_bwd(int32_t B, int32_t H, int32_t T, int32_t d, i
  *
  * Vectors lie densely along dk or dv; mesa_rows gives the elements from one
  * sequence, head and token to the next, so [B, H, T, d] and [B, T, H, d] tensors and
- * slices of wider ones are taken as they are.  Strides are not negative; those of q,
+ * slices of wider ones are taken as they are.  Strides are 0 to 2^36; those of q,
  * k, v, o and their gradients are multiples of 16 bytes (one of a size of 1 does not
  * matter), gates and their gradients are aligned to 4 bytes, and no two rows of an
  * output share memory.
@@ -702,7 +702,7 @@ mesa_status mesa_qk_preprocess_bwd(int32_t B, int32_t H, int32_t T, int32_t d, i
  * checked): an infinity or NaN in one leaves that head of that sequence unspecified
  * from the start of the 64 tokens around it, and no other.
  * Supported: dk in {32, 64, 128}, dv a multiple of 16 up to 1024, H a multiple of
- * Hk, token strides of rows up to 2^20, B H max(ceil(T/64), ceil(dv/64)) <= 2^22.
+ * Hk, token strides up to 2^20, B H max(ceil(T/64), ceil(dv/64)) <= 2^22.
  * Outputs and workspace may not overlap inputs or one another but as said
  * (MESA_ERR_INVALID_ARG); token rows of several outputs may interleave in one wider
  * tensor.  Two calls may not use one workspace at the same time. */
@@ -742,7 +742,7 @@ mesa_status mesa_delta_fwd(const mesa_delta_desc* d, const void* q, const void* 
  *   d_sfinal      [B, H, dv, dk] fp32 or NULL (zero)
  *   dq, dk [B, Hk, T, dk], dv [B, H, T, dv]  dtype out
  *   dgamma, dbeta [B, H, T] fp32 out.  dgamma is formed as the gradient at
- *                 log gamma over gamma: gamma > 0
+ *                 log gamma over gamma, and is 0 where gamma is
  *   ds0           [B, H, dv, dk] fp32 out or NULL.  May be d_sfinal itself
  *   states_in_workspace  1: the forward ran with keep_states = 1 and this same
  *                 workspace, descriptor and inputs, and nothing else used the workspace

@@ -41,8 +41,9 @@ struct DeltaParams {
   const int32_t* lengths;           // [B] or null
   int B, H, Hk, T, dk, dv, NC;      // NC chunks a (padded) sequence
   // A walk in NS segments of L chunks (NS = 1: whole).  seg_map: [B H, NS, dk, dk], row j what
-  // a segment makes of the state whose row is unit vector j; seg_add: [B H, NS, dv, dk], what it
-  // makes of a zero state; seg_start: [B H, NS, dv, dk], the states the segments start from
+  // an inner segment makes of the state whose row is unit vector j; seg_add: [B H, NS, dv, dk], what
+  // it makes of a zero state (the segment at the walk's start: of the given one);
+  // seg_start: [B H, NS, dv, dk], the states that the others start from
   int NS, L;
   float *seg_map, *seg_add, *seg_start;
   int probe;                        // 1: the walk that forms seg_map and seg_add

@@ -65,7 +65,8 @@ bool floats_aligned(const float* const (&ptrs)[N]) {
   return true;
 }
 
-constexpr int64_t kMaxStride = (int64_t)1 << 40, kMaxTokenStride = 1 << 20;
+// (with B H <= 2^22 and T <= 2^28, checked below, no offset in bytes passes 2^62)
+constexpr int64_t kMaxStride = (int64_t)1 << 36, kMaxTokenStride = 1 << 20;
 
 bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
 bool strides_ok(const mesa_rows& r) { return stride_ok(r.b) && stride_ok(r.h) && stride_ok(r.t); }
@@ -86,7 +87,7 @@ mesa_status check_delta(const mesa_delta_desc* d) {
     if (!strides_ok(*r)) return MESA_ERR_INVALID_ARG;
   if ((d->dk != 32 && d->dk != 64 && d->dk != 128) || d->dv % 16 != 0 || d->dv > 1024) return MESA_ERR_UNSUPPORTED;
   // offsets within a chunk of tokens have 32 bits
-  for (const mesa_rows* r : {&d->q, &d->k, &d->v, &d->o})
+  for (const mesa_rows* r : {&d->q, &d->k, &d->v, &d->o, &d->gamma, &d->beta})
     if (d->T > 1 && r->t > kMaxTokenStride) return MESA_ERR_UNSUPPORTED;
   // launches of at most 2^32 threads
   if ((double)d->B * d->H * std::max(chunks_of(d), (d->dv + 63) / 64) > (double)(1 << 22)) return MESA_ERR_UNSUPPORTED;
@@ -107,7 +108,7 @@ int segments_of(const mesa_delta_desc* d) {
   for (int n = 2; n <= 32 && n * 4 <= chunks; ++n) {
     const int per = (chunks + n - 1) / n;
     if ((chunks + per - 1) / per != n) continue;  // (no segment stays empty)
-    const double time = per * (rounds(heads * (n - 1) * (values + units)) + rounds(heads * n * values)) + 3 + 0.5 * n;
+    const double time = per * (rounds(heads * ((n - 1) * values + (n - 2) * units)) + rounds(heads * n * values)) + 3 + 0.5 * n;
     if (time < least) {
       best = n;
       least = time;
@@ -154,14 +155,17 @@ size_t carve(const mesa_delta_desc* d, bool keep, void* workspace, DeltaParams& 
   return w.at;
 }
 
-DeltaRows rows(const void* at, const mesa_rows& r) { return {const_cast<void*>(at), r.b, r.h, r.t}; }
+// (a token stride that no index uses may be any: kernels step by it to rows that they then leave out)
+DeltaRows rows(const mesa_delta_desc* d, const void* at, const mesa_rows& r) {
+  return {const_cast<void*>(at), r.b, r.h, d->T > 1 ? r.t : 0};
+}
 
 DeltaGate gate(const float* at, const mesa_rows& r) { return {const_cast<float*>(at), r.b, r.h, r.t}; }
 
 DeltaParams delta_params(const mesa_delta_desc* d, const void* q, const void* k, const void* v, const float* gamma,
                          const float* beta, const float* s0, const int32_t* lengths) {
   DeltaParams p{};
-  p.q = rows(q, d->q); p.k = rows(k, d->k); p.v = rows(v, d->v); p.gamma = gate(gamma, d->gamma);
+  p.q = rows(d, q, d->q); p.k = rows(d, k, d->k); p.v = rows(d, v, d->v); p.gamma = gate(gamma, d->gamma);
   p.beta = gate(beta, d->beta); p.s0 = s0; p.lengths = lengths;
   p.B = d->B; p.H = d->H; p.Hk = d->Hk; p.T = d->T; p.dk = d->dk; p.dv = d->dv; p.NC = chunks_of(d);
   return p;
@@ -234,7 +238,7 @@ mesa_status mesa_delta_fwd(const mesa_delta_desc* d, const void* q, const void* 
     return MESA_ERR_INVALID_ARG;
   DeltaParams p = delta_params(d, q, k, v, gamma, beta, s0, lengths);
   carve(d, keep_states == 1, workspace, p);
-  p.o = rows(o, d->o); p.s_final = s_final;
+  p.o = rows(d, o, d->o); p.s_final = s_final;
   const bool bf16 = d->dtype == MESA_BF16;
   if (d->T > 0 && launch_delta_chunks(bf16, false, p, stream) != hipSuccess) return MESA_ERR_HIP;
   if (d->T == 0) p.o.at = nullptr;
@@ -251,7 +255,7 @@ mesa_status mesa_delta_bwd(const mesa_delta_desc* d, const mesa_delta_grad_rows*
   if (!gr || (states_in_workspace != 0 && states_in_workspace != 1)) return MESA_ERR_INVALID_ARG;
   for (const mesa_rows* r : {&gr->d_o, &gr->dq, &gr->dk, &gr->dv, &gr->dgamma, &gr->dbeta})
     if (!strides_ok(*r)) return MESA_ERR_INVALID_ARG;
-  for (const mesa_rows* r : {&gr->d_o, &gr->dq, &gr->dk, &gr->dv})
+  for (const mesa_rows* r : {&gr->d_o, &gr->dq, &gr->dk, &gr->dv, &gr->dgamma, &gr->dbeta})
     if (d->T > 1 && r->t > kMaxTokenStride) return MESA_ERR_UNSUPPORTED;
   if (d->T > 0 && (!q || !k || !v || !gamma || !beta || !d_o || !dq || !dk || !dv || !dgamma || !dbeta))
     return MESA_ERR_INVALID_ARG;
@@ -260,8 +264,8 @@ mesa_status mesa_delta_bwd(const mesa_delta_desc* d, const mesa_delta_grad_rows*
     return MESA_ERR_INVALID_ARG;
   if (!all_aligned({q, k, v, s0, lengths, d_o, d_sfinal, dq, dk, dv, ds0, workspace}) ||
       !floats_aligned({gamma, beta, dgamma, dbeta}) || !rows_aligned(d, d->Hk, d->q) ||
-      !rows_aligned(d, d->Hk, d->k) || !rows_aligned(d, d->H, d->v) || !rows_aligned(d, d->H, gr->d_o) || !rows_aligned(d, d->Hk, gr->dq) || !rows_aligned(d, d->Hk, gr->dk) ||
-      !rows_aligned(d, d->H, gr->dv))
+      !rows_aligned(d, d->Hk, d->k) || !rows_aligned(d, d->H, d->v) || !rows_aligned(d, d->H, gr->d_o) ||
+      !rows_aligned(d, d->Hk, gr->dq) || !rows_aligned(d, d->Hk, gr->dk) || !rows_aligned(d, d->H, gr->dv))
     return MESA_ERR_ALIGNMENT;
   const size_t need = mesa_delta_workspace_bytes(d, 1);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MESA_ERR_WORKSPACE;
@@ -292,7 +296,7 @@ mesa_status mesa_delta_bwd(const mesa_delta_desc* d, const mesa_delta_grad_rows*
     }
     if (launch_delta_chunks(bf16, true, p, stream) != hipSuccess) return MESA_ERR_HIP;
   }
-  p.d_o = rows(d_o, gr->d_o); p.dq = rows(dq, gr->dq); p.dk_ = rows(dk, gr->dk); p.dv_ = rows(dv, gr->dv);
+  p.d_o = rows(d, d_o, gr->d_o); p.dq = rows(d, dq, gr->dq); p.dk_ = rows(d, dk, gr->dk); p.dv_ = rows(d, dv, gr->dv);
   p.dgamma = gate(dgamma, gr->dgamma); p.dbeta = gate(dbeta, gr->dbeta); p.d_sfinal = d_sfinal; p.ds0 = ds0;
   if (adjoint(bf16, p, stream) != hipSuccess) return MESA_ERR_HIP;
   return d->T > 0 ? launched(launch_delta_grads(bf16, p, stream)) : MESA_OK;

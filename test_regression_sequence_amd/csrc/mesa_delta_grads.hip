@@ -333,7 +333,7 @@ __global__ __launch_bounds__(512, 2) void delta_grads_kernel(DeltaParams p) {
     x += gates.c[63] * whole;
     if (lane < here) {
       *gate_at(p.dgamma, b, h, t0 + lane) =
-          lane < live ? (float)(x / (double)gammas[lane]) : 0.f;
+          lane < live && gammas[lane] != 0.f ? (float)(x / (double)gammas[lane]) : 0.f;
       *gate_at(p.dbeta, b, h, t0 + lane) = lane < live ? dbetas[lane] : 0.f;
     }
   }

@@ -1,8 +1,9 @@
 // Gated delta rule: the states that the segments of a split walk start from.
 //
 // Over a segment the state's rows go S -> S P + Q (P = seg_map, Q = seg_add: what
-// the segment makes of unit rows and of zero), and its gradients back N -> N P^T + Q.
-// From one segment to the next that is a 16 x dk by dk x dk product for each 16 rows,
+// the segment makes of unit rows and of zero), and its gradients back N -> N P^T + Q;
+// the segment at the walk's start has the given state in its Q already.  From one
+// segment to the next that is a 16 x dk by dk x dk product for each 16 rows,
 // in fp32 matrix instructions: a workgroup has 16 rows in LDS, its waves the tiles of
 // the result's columns.
 #include "mesa_delta_tile.h"
@@ -17,10 +18,10 @@ __global__ __launch_bounds__(256) void delta_join_kernel(DeltaParams p) {
   __shared__ __attribute__((aligned(16))) float rows[2][16][DK + 4];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int groups = p.dv / 16, bh = blockIdx.x / groups, row0 = blockIdx.x % groups * 16;
-  const float* given = BACK ? p.d_sfinal : p.s0;
+  const int64_t edge = (int64_t)bh * p.NS + (BACK ? p.NS - 1 : 0), second = BACK ? edge - 1 : edge + 1;
   for (int i = tid; i < 16 * DK; i += 256)
-    rows[0][i / DK][i % DK] = given ? given[((int64_t)bh * p.dv + row0 + i / DK) * DK + i % DK] : 0.f;
-  for (int n = 0; n + 1 < p.NS; ++n) {
+    p.seg_start[(second * p.dv + row0) * DK + i] = rows[1][i / DK][i % DK] = p.seg_add[(edge * p.dv + row0) * DK + i];
+  for (int n = 1; n + 1 < p.NS; ++n) {
     const int seg = BACK ? p.NS - 1 - n : n, next = BACK ? seg - 1 : seg + 1;
     const int64_t at = (int64_t)bh * p.NS + seg, to = (int64_t)bh * p.NS + next;
     const float *map = p.seg_map + at * DK * DK, *add = p.seg_add + (at * p.dv + row0) * DK;

@@ -415,8 +415,10 @@ __device__ __forceinline__ float* gate_at(const DeltaGate& x, int b, int h, int6
 __device__ __forceinline__ float decay(double a, double b) { return __builtin_amdgcn_exp2f((float)(a - b)); }
 
 // One workgroup's part of a walk: 64 columns of one head's state over one segment's
-// chunks first .. last - 1.  A probing walk has the columns of the unit matrix too
-// (`unit_columns`), and none for the last (back: the first) segment, which nothing follows.
+// chunks.  The walk that finds what segments make of states (`probe`) has none for the
+// last (back: the first) segment, which nothing follows, starts the segment at the other
+// end from the given state, and forward also takes dk unit columns (`unit_columns`)
+// through the segments in between.
 struct Part {
   int bh, b, h, seg, col0, cols, len, first, last;
   bool unit_columns;
@@ -435,6 +437,7 @@ __device__ __forceinline__ bool part_of(const DeltaParams& p, bool back, uint32_
   x.b = x.bh / p.H;
   x.h = x.bh % p.H;
   x.unit_columns = slice >= values;
+  if (x.unit_columns && x.seg == 0) return false;
   x.col0 = 64 * (x.unit_columns ? slice - values : slice);
   x.cols = min(64, (x.unit_columns ? p.dk : p.dv) - x.col0);
   x.len = delta_length(p, x.b);
@@ -449,7 +452,7 @@ inline uint32_t walk_blocks(const DeltaParams& p, bool back) {
 
 // Where a walk's state comes from and goes to: [.., dk] from column `col` on (null: zeros, nowhere).
 __device__ __forceinline__ const float* walk_from(const DeltaParams& p, const Part& x, const float* given, int edge, int col) {
-  if (p.probe) return nullptr;
+  if (x.unit_columns || (p.probe && x.seg != edge)) return nullptr;
   if (x.seg != edge) return p.seg_start + (((int64_t)x.bh * p.NS + x.seg) * p.dv + col) * p.dk;
   return given ? given + ((int64_t)x.bh * p.dv + col) * p.dk : nullptr;
 }

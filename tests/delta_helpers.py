@@ -112,9 +112,11 @@ def close(got, want, e, dtype, what, rows=True):
     return worst
 
 
-def check_forward(r, a, dtype):
+def check_forward(r, a, dtype, walks=1):
+    """walks: 2 where a walk goes in segments.  A segment's start is its map times the start before it:
+    each of the map's columns is a walk of its own, whose errors meet the start in no fixed direction."""
     want = delta_forward(*(a[n] for n in NAMES[:5]), s0=a["s0"], lengths=a["lengths"])
-    e = e32(a, 12)
+    e = e32(a, 12 * walks)
     close(r["o"], want["o"], e, dtype, "o")
     if "s_final" in r:
         close(r["s_final"], want["s_final"], e, torch.float32, "s_final")
@@ -129,9 +131,9 @@ def behind(r, a, names):
                 assert not r[n][b, :, int(stop):].any(), (n, b)
 
 
-def check_backward(r, a, dtype):
+def check_backward(r, a, dtype, walks=1):
     want = delta_backward(*(a[n] for n in NAMES[:6]), s0=a["s0"], lengths=a["lengths"], d_sfinal=a["d_sfinal"])
-    e = e32(a, 20)
+    e = e32(a, 20 * walks)
     for n in ("dq", "dk", "dv"):
         close(r[n], want[n], e, dtype, n)
     close(r["dbeta"], want["dbeta"], e, torch.float32, "dbeta")

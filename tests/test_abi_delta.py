@@ -95,8 +95,22 @@ def test_gradient_strides(name):
         assert bwd(d, grad_rows(d, **{name: mesa.Rows(0, 0, 0)})) == 1          # rows over one another
     if name in ("dq", "dk", "dv"):
         assert bwd(d, grad_rows(d, **{name: mesa.Rows(4 * 130 * 64, 130 * 64, 32)})) == 1
+    assert bwd(d, grad_rows(d, **{name: mesa.Rows(1 << 28, 64, (1 << 20) + 8)})) == 2
     if name in ("d_o", "dq", "dk", "dv"):
         assert bwd(d, grad_rows(d, **{name: mesa.Rows(1 << 20, 1 << 17, 129 + 3)})) == 3
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "o", "gamma", "beta"])
+def test_strides(name):
+    """The largest strides pass up to the workspace, larger ones are refused, and those that no index uses do not matter."""
+    H, Hk, T = 4, 2, 130
+    ok = mesa.Rows(1 << 36, 1 << 30, 1 << 20)
+    d = desc(H=H, Hk=Hk, T=T, **{name: ok})
+    f = {n: (i + 1) << 44 for i, n in enumerate((*IN, "o", "s_final", "workspace"))}
+    assert fwd(d, **{**f, "workspace": 0}) == 4
+    assert fwd(desc(**{name: mesa.Rows(1 << 36, 1 << 30, (1 << 20) + 8)}), **f) == 2
+    assert fwd(desc(**{name: mesa.Rows((1 << 36) + 8, 1 << 30, 1 << 20)}), **f) == 1
+    assert fwd(desc(B=1, T=1, **{name: mesa.Rows(3, 1 << 30, 1 << 30)}), **{**f, "workspace": 0}) == 4
 
 
 def test_missing_and_misaligned():

@@ -174,3 +174,48 @@ def test_zero_gates():
     a["gamma"][:, :, 50] = 0.5
     t = to_dev(a, torch.float32)
     check_backward(backward(t), a, torch.float32)
+
+
+def test_backward_of_a_gate_that_forgets_everything():
+    """gamma = 0: the gradient at log gamma is 0 there, and so dgamma is written; all others are as defined."""
+    a = draw(2, 2, 2, 150, 64, 64, torch.float32, seed=3)
+    a["gamma"][:, :, [0, 50, 64, 149]] = 0.0
+    t = to_dev(a, torch.float32)
+    r = backward(t)
+    assert not r["dgamma"][:, :, [0, 50, 64, 149]].any()
+    check_backward(r, a, torch.float32)
+
+
+def segmented(t):
+    """Whether walks of these inputs go in segments: they have maps then, which as many heads as fill the card have not."""
+    big = {n: t[n][:1].expand(512, *t[n].shape[1:]) for n in ("q", "k", "v", "gamma", "beta")}
+    return mesa.delta_workspace_bytes(*args(t)) * 512 > t["q"].shape[0] * (mesa.delta_workspace_bytes(*args(big)) + 512 * 8192)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,Hk,T,dk,dv", [(1, 1, 1024, 64, 64), (2, 1, 1601, 128, 48), (1, 1, 2100, 32, 80), (3, 3, 1500, 128, 128)])
+def test_segments(H, Hk, T, dk, dv, dtype):
+    """Few heads and many chunks: lengths that end in each segment, at its ends, before the first and behind the last."""
+    dt = DTYPES[dtype]
+    a = draw(4, H, Hk, T, dk, dv, dt, gates="slow", lengths=[T + 5, 0, 513, T // 2])
+    t = to_dev(a, dt, "tokens")
+    assert segmented(t)
+    ws = torch.empty(mesa.delta_workspace_bytes(*args(t), keep_states=True), device="cuda", dtype=torch.uint8)
+    ws.fill_(0xFF)
+    r = forward(t, workspace=ws, keep_states=True)
+    check_forward(r, a, dt, walks=2)
+    g = backward(t, workspace=ws, states_in_workspace=True)
+    check_backward(g, a, dt, walks=2)
+    again = backward(t, workspace=ws, states_in_workspace=True)
+    alone = backward(t)
+    assert all(torch.equal(g[n], again[n]) and torch.equal(g[n], alone[n]) for n in g)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_segments_without_states(dtype):
+    dt = DTYPES[dtype]
+    a = draw(1, 2, 2, 1300, 64, 64, dt, gates="slow", s0=False)
+    t = to_dev(a, dt)
+    assert segmented(t)
+    check_forward(mesa.delta_fwd(*args(t)), a, dt, walks=2)
+    check_backward(mesa.delta_bwd(*args(t), t["d_o"]), a, dt, walks=2)
