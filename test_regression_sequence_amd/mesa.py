@@ -922,7 +922,7 @@ def _rows(t: torch.Tensor) -> Rows:
 
 def _delta_in(t: torch.Tensor, name: str, shape, dtype, dev):
     """t [..., d] of this shape and type on dev, whose last index is contiguous."""
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise MesaError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if t.dtype is not dtype or t.device != dev:
         raise MesaError(f"{name} must be {dtype} on {dev}, got {t.dtype} on {t.device}")
@@ -948,7 +948,7 @@ def _delta_desc(q, k, v, gamma, beta, stream):
 
 
 def _delta_gate(t: torch.Tensor, name: str, shape, dev):
-    if tuple(t.shape) != shape or t.dtype is not torch.float32 or t.device != dev:
+    if t.shape != shape or t.dtype is not torch.float32 or t.device != dev:
         raise MesaError(f"{name} must be float32 {shape} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
@@ -1040,14 +1040,21 @@ def delta_step(q, k, v, gamma, beta, s_state, *, out=None, stream=None) -> dict:
     """One token of N sequences: q, k [N, Hk, dk], v [N, H, dv] (fp32 or bf16, last index
     contiguous), gamma, beta [N, H] fp32, s_state [N, H, dv, dk] fp32 updated in place.
     Returns ``o`` [N, H, dv] in v's dtype."""
-    _home(q, "q", 3, stream)
-    for name, t, dims in (("k", k, 3), ("v", v, 3), ("gamma", gamma, 2), ("beta", beta, 2)):
-        if t.dim() != dims:
-            raise MesaError(f"{name} has shape {tuple(t.shape)}, expected {dims} dimensions")
-    desc, dev, dt = _delta_desc(*(t.unsqueeze(2) for t in (q, k, v, gamma, beta)), stream)
-    _want(s_state, "s_state", (desc.B, desc.H, desc.dv, desc.dk), torch.float32, dev)
-    o = _result(out, "o", v.shape, dt, dev, stream, v)
-    desc.o = Rows(o.stride(0), o.stride(1), 0)
+    dev, dt = _home(q, "q", 3, stream), q.dtype
+    code = _code_of(q, "q")
+    N, Hk, dk = q.shape
+    if v.dim() != 3:
+        raise MesaError(f"v has shape {tuple(v.shape)}, expected 3 dimensions")
+    _, H, dv = v.shape
+    _delta_in(k, "k", (N, Hk, dk), dt, dev)
+    _delta_in(v, "v", (N, H, dv), dt, dev)
+    _delta_in(q, "q", (N, Hk, dk), dt, dev)
+    _delta_gate(gamma, "gamma", (N, H), dev)
+    _delta_gate(beta, "beta", (N, H), dev)
+    _want(s_state, "s_state", (N, H, dv, dk), torch.float32, dev)
+    o = _result(out, "o", (N, H, dv), dt, dev, stream, v)
+    rows = [Rows(*t.stride()[:2], 0) for t in (q, k, v, o, gamma, beta)]
+    desc = DeltaDesc(N, H, Hk, 1, dk, dv, code, *rows)
     _launch("mesa_delta_step", dev, stream, ctypes.byref(desc), _addr(q), _addr(k), _addr(v), _addr(gamma), _addr(beta),
             _addr(s_state), _addr(o))
     return {"o": o}
@@ -1066,11 +1073,13 @@ def _clip_lists(grads, out, stream):
     if stream is not None and stream.device != dev:
         raise MesaError(f"the stream belongs to {stream.device}, grads are on {dev}")
     n = len(grads)
-    codes = [_CODES.get(g.dtype) for g in grads]
-    sizes = [g.numel() for g in grads]
+    codes, index = [], dev.index
     for i, g in enumerate(grads):
-        if codes[i] is None or g.device != dev or not g.is_contiguous():
+        code = _CODES.get(g.dtype)
+        if code is None or g.get_device() != index or not g.is_contiguous():
             raise MesaError(f"grads[{i}] must be dense float32 or bfloat16 on {dev}, got {g.dtype} on {g.device}")
+        codes.append(code)
+    sizes = [g.numel() for g in grads]
     at = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
     to = at
     if out is not None and out is not grads:
@@ -1102,7 +1111,8 @@ def grad_clip(grads, max_norm: float, *, eps: float = 1e-6, out=None, workspace:
     clipped tensors."""
     dev, n, at, to, sizes, codes = _clip_lists(grads, out, stream)
     both = _new((2,), torch.float32, dev, stream)
+    norm, scale = both.unbind()
     workspace, wbytes = _scratch(workspace, lambda: lib().mesa_grad_clip_workspace_bytes(), dev, stream)
     _launch("mesa_grad_clip", dev, stream, n, at, to, sizes, codes, max_norm, eps, _addr(both), both.data_ptr() + 4,
             _addr(workspace), wbytes)
-    return {"norm": both[0], "scale": both[1], "grads": grads if out is None else out}
+    return {"norm": norm, "scale": scale, "grads": grads if out is None else out}
