@@ -46,7 +46,7 @@ struct DeltaParams {
   // seg_start: [B H, NS, dv, dk], the states that the others start from
   int NS, L;
   float *seg_map, *seg_add, *seg_start;
-  int probe;                        // 1: the walk that forms seg_map and seg_add
+  int probe;                        // 1: the walk back that forms seg_add
   DeltaGates* gates;                // [B H, NC]
   char* matrices;                   // [B H, NC, delta_matrix_bytes(2 or 3)]
   float* states;                    // [B H, NC, dv, dk] before each chunk, or null
@@ -71,6 +71,8 @@ hipError_t launch_delta_adjoint(const DeltaParams& p, hipStream_t s);  // bf16 r
 hipError_t launch_delta_adjoint_f32(const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_grads(bool bf16, const DeltaParams& p, hipStream_t s);
 
+// seg_map and seg_add of a walk forward.
+hipError_t launch_delta_probe(bool bf16, const DeltaParams& p, hipStream_t s);
 // seg_start from seg_map, seg_add and the state at one end; `back`: from the last segment to the first.
 hipError_t launch_delta_join(bool back, const DeltaParams& p, hipStream_t s);
 

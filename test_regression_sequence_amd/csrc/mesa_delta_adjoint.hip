@@ -37,7 +37,7 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
             g = lane >> 4;
   const bool chain = __builtin_amdgcn_readfirstlane(threadIdx.x) < 256;
   Part part;
-  if (!part_of(p, true, blockIdx.x, part)) return;
+  if (!part_of(p, blockIdx.x, part)) return;
   const int bh = part.bh, b = part.b, h = part.h, len = part.len, first = part.first, last = part.last;
   const int col0 = part.col0, cols = part.cols;
   const bool mine = 16 * wave < cols;
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
 
 template <int DK>
 hipError_t launch(const DeltaParams& p, hipStream_t s) {
-  delta_adjoint_kernel<DK><<<walk_blocks(p, true), 512, 0, s>>>(p);
+  delta_adjoint_kernel<DK><<<walk_blocks(p), 512, 0, s>>>(p);
   return hipGetLastError();
 }
 

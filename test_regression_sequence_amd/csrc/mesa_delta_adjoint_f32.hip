@@ -24,7 +24,7 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p
   __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   Part part;
-  if (!part_of(p, true, blockIdx.x, part)) return;
+  if (!part_of(p, blockIdx.x, part)) return;
   const int bh = part.bh, b = part.b, h = part.h, hk = h / (p.H / p.Hk), len = part.len, first = part.first, last = part.last;
   const int col0 = part.col0, cols = part.cols;
   const int col = col0 + 16 * wave + r;
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p
 
 template <int DK>
 hipError_t launch(const DeltaParams& p, hipStream_t s) {
-  delta_adjoint_f32_kernel<DK><<<walk_blocks(p, true), 256, 0, s>>>(p);
+  delta_adjoint_f32_kernel<DK><<<walk_blocks(p), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -100,7 +100,7 @@ mesa_status check_delta(const mesa_delta_desc* d) {
 // columns) and a launch that joins them.  In times of one chunk (about 2.7 us), that launch
 // and the additional walk's take about 3 and half a chunk a segment.
 int segments_of(const mesa_delta_desc* d) {
-  const int64_t heads = (int64_t)d->B * d->H, values = (d->dv + 63) / 64, units = (d->dk + 63) / 64;
+  const int64_t heads = (int64_t)d->B * d->H, values = (d->dv + 63) / 64, both = (d->dv + d->dk + 127) / 128;
   const int chunks = chunks_of(d);
   const auto rounds = [](int64_t blocks) { return (double)((blocks + 255) / 256); };
   int best = 1;
@@ -108,7 +108,7 @@ int segments_of(const mesa_delta_desc* d) {
   for (int n = 2; n <= 32 && n * 4 <= chunks; ++n) {
     const int per = (chunks + n - 1) / n;
     if ((chunks + per - 1) / per != n) continue;  // (no segment stays empty)
-    const double time = per * (rounds(heads * ((n - 1) * values + (n - 2) * units)) + rounds(heads * n * values)) + 3 + 0.5 * n;
+    const double time = per * (rounds(heads * (n - 1) * both) + rounds(heads * n * values)) + 3 + 0.5 * n;
     if (time < least) {
       best = n;
       least = time;
@@ -173,17 +173,12 @@ DeltaParams delta_params(const mesa_delta_desc* d, const void* q, const void* k,
 
 // A walk forward, in segments where there are few heads.
 hipError_t scan(bool bf16, const DeltaParams& p, hipStream_t s) {
-  const auto walk = [&](const DeltaParams& x) { return bf16 ? launch_delta_scan(x, s) : launch_delta_scan_f32(x, s); };
   if (p.NS > 1) {
-    DeltaParams probe = p;
-    probe.probe = 1;
-    probe.o.at = nullptr;
-    probe.states = probe.w = nullptr;
-    hipError_t e = walk(probe);
+    hipError_t e = launch_delta_probe(bf16, p, s);
     if (e == hipSuccess) e = launch_delta_join(false, p, s);
     if (e != hipSuccess) return e;
   }
-  return walk(p);
+  return bf16 ? launch_delta_scan(p, s) : launch_delta_scan_f32(p, s);
 }
 
 // A walk back; the segments' maps are those of the walk forward.

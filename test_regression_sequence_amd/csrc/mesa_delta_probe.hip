@@ -1,0 +1,181 @@
+// Gated delta rule, forward: what the segments of a split walk make of states.
+//
+// Over a segment the state's rows go S -> S P + Q.  The walk of mesa_delta_scan.hip,
+// without outputs, over Q's columns (from the given state in the first segment, from
+// zero in the others) and, behind the first segment, over P's: the dk unit columns,
+// whose values are zeros.  The last segment, which nothing follows, has neither.
+//
+// Nothing is formed beside the chain of states, so all eight waves are chains, 16
+// columns each, two on a SIMD to fill one another's waits: 128 columns a workgroup, and
+// with dv = dk = 64 both kinds in one.  A chunk's keys, inverse and gates go to LDS
+// while the chunk before is in the works; values go to their lanes.
+#include "mesa_delta_tile.h"
+
+namespace mesa {
+
+namespace {
+
+template <int DK, bool BF16>
+struct ProbeLds {
+  static constexpr int NP = BF16 ? 1 : 3, kPlane = 64 * DK * 2;
+  static constexpr int kT = NP * kPlane, kGates = kT + 3 * kBlocksBytes, kBuffer = kGates + (int)sizeof(DeltaGates);
+};
+
+int slices_of(const DeltaParams& p) { return (p.dv + p.dk + 127) / 128; }
+
+template <int DK, bool BF16>
+__global__ __launch_bounds__(512, 2) void delta_probe_kernel(DeltaParams p, int slices) {
+  using L = ProbeLds<DK, BF16>;
+  constexpr int NP = L::NP, MT = DK / 16, KS = DK / 32, ES = BF16 ? 2 : 4;
+  __shared__ __attribute__((aligned(16))) char lds[2][L::kBuffer];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
+  // one head's workgroups on one XCD, whose L2 they share
+  const int per = slices * (p.NS - 1), n = blockIdx.x >> 3, rest = n % per;
+  const int bh = n / per * 8 + (blockIdx.x & 7), seg = rest / slices, slice = rest % slices;
+  if (bh >= p.B * p.H || (seg == 0 && 128 * slice >= p.dv)) return;
+  const int b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk), len = delta_length(p, b);
+  const int first = seg * p.L, last = max(min((len + 63) / 64, first + p.L), first);
+  const int col0 = 128 * slice + 16 * wave;
+  const bool unit_columns = col0 >= p.dv, mine = unit_columns ? col0 < p.dv + DK && seg > 0 : true;
+  const int col = (unit_columns ? col0 - p.dv : col0) + r;
+  const int64_t k0 = b * p.k.b + hk * p.k.h, v0 = b * p.v.b + h * p.v.h;
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+
+  f32x4 m[MT];  // rows 16 i + 4 g + e of the state's transpose, column `col`
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    m[i] = zero;
+    if (unit_columns) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m[i][e] = 16 * i + 4 * g + e == col ? 1.f : 0.f;
+    } else if (seg == 0 && p.s0) {
+      m[i] = *reinterpret_cast<const f32x4*>(p.s0 + ((int64_t)bh * p.dv + col) * DK + 16 * i + 4 * g);
+    }
+  }
+  const TileRows<DK> rows(lane);
+  const TileColumns<DK> columns(lane);
+  RowLoads<DK, BF16, 512> kl;
+  CopyLoads<3 * kBlocksBytes, 512> tl;
+  CopyLoads<sizeof(DeltaGates), 512> gl;
+  f32x4 v[4], v_next[4];  // V's rows 16 i + 4 g + e, column `col`
+  auto load = [&](int c) {
+    const int live = min(len - 64 * c, 64);
+    const int64_t t0 = 64 * (int64_t)c, unit = (int64_t)bh * p.NC + c;
+    kl.load(p.k.at, k0 + t0 * p.k.t, p.k.t, live, DK, tid);
+    tl.load(p.matrices + unit * (int64_t)delta_matrix_bytes(BF16 ? 2 : 3), tid);
+    gl.load(p.gates + unit, tid);
+    const Window from = window_at(static_cast<const char*>(p.v.at) + (v0 + t0 * p.v.t) * ES);
+    const uint32_t at = (4 * g * (uint32_t)p.v.t + col) * ES, step = (uint32_t)p.v.t * ES;
+    const int there = unit_columns ? 0 : live - 4 * g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v_next[i][e] = window_number<BF16>(from, 16 * i + e < there ? at : kNowhere, (16 * i + e) * step);
+  };
+  auto store = [&](int c) {
+    char* to = lds[c & 1];
+    kl.store(to, L::kPlane, tid);
+    tl.store(to + L::kT, tid);
+    gl.store(to + L::kGates, tid);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = v_next[i];
+  };
+
+  if (first < last) {
+    load(first);
+    store(first);
+    __syncthreads();
+  }
+  for (int c = first; c < last; ++c) {
+    const char* keys = lds[c & 1];
+    const DeltaGates& gates = *reinterpret_cast<const DeltaGates*>(keys + L::kGates);
+    load(min(c + 1, last - 1));  // (without a branch around the loads)
+    if (mine) {
+      f32x4 x[4] = {zero, zero, zero, zero}, y[4];
+      Planes<3> mp[KS], px[2], ut[2];
+      Planes<NP> f[2][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[0][i] = rows.template planes<NP>(keys, L::kPlane, 16 * i, 0);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) mp[s] = split8<3>(m[2 * s], m[2 * s + 1]);
+      BlockPair<3> t;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {  // K M
+        if (s + 1 < KS) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[(s + 1) & 1][i] = rows.template planes<NP>(keys, L::kPlane, 16 * i, s + 1);
+        } else {
+          t = pair_of<true, 3>(keys + L::kT, 0, lane);
+        }
+        fence<BF16>();
+        mma_tiles<2>(f[s & 1], mp[s], x);
+        fence<BF16>();
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[i] = v[i] - *reinterpret_cast<const f32x4*>(&gates.c[16 * i + 4 * g]) * x[i];
+        x[i] = zero;
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) px[s] = split8<3>(y[2 * s], y[2 * s + 1]);
+      mma_triangle<2, true, false, BF16>(keys + L::kT, t, px, x, lane);  // W
+      constexpr int G = MT < 4 ? MT : 4, NG = 2 * MT / G;  // K^T in groups of 4 tiles
+      Planes<NP> kt[2][4];
+      auto group = [&](int n) {
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+          kt[n & 1][i] = columns.template planes<NP>(keys, L::kPlane, 32 * (n * G / MT), n * G % MT + i);
+      };
+      group(0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] *= *reinterpret_cast<const f32x4*>(&gates.beta[16 * i + 4 * g]) *
+                *reinterpret_cast<const f32x4*>(&gates.tail[16 * i + 4 * g]);
+      const float whole = gates.c[63];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) m[i] *= whole;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) ut[s] = split8<3>(x[2 * s], x[2 * s + 1]);
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {  // M += K^T U
+        if (n + 1 < NG) group(n + 1);
+        fence<BF16>();
+#pragma unroll
+        for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+          for (int q = 0; q < NP; ++q)
+            if (sum - q >= 0)
+#pragma unroll
+              for (int i = 0; i < G; ++i)
+                m[n * G % MT + i] = mfma_bf16(kt[n & 1][i].p[q], ut[n * G / MT].p[sum - q], m[n * G % MT + i]);
+        fence<BF16>();
+      }
+    }
+    store(c + 1);
+    __syncthreads();
+  }
+  if (mine) {
+    const int64_t at = (int64_t)bh * p.NS + seg;
+    float* const to = unit_columns ? p.seg_map + (at * DK + col) * DK : p.seg_add + (at * p.dv + col) * DK;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i + 4 * g) = m[i];
+  }
+}
+
+template <int DK>
+hipError_t launch(bool bf16, const DeltaParams& p, hipStream_t s) {
+  const int slices = slices_of(p);
+  const uint32_t blocks = (uint32_t)((p.B * p.H + 7) / 8 * 8 * slices * (p.NS - 1));
+  if (bf16) delta_probe_kernel<DK, true><<<blocks, 512, 0, s>>>(p, slices);
+  else delta_probe_kernel<DK, false><<<blocks, 512, 0, s>>>(p, slices);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_probe(bool bf16, const DeltaParams& p, hipStream_t s) {
+  return p.dk == 128 ? launch<128>(bf16, p, s) : p.dk == 64 ? launch<64>(bf16, p, s) : launch<32>(bf16, p, s);
+}
+
+}  // namespace mesa

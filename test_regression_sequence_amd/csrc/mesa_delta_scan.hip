@@ -38,7 +38,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
   const int tid = threadIdx.x & 255, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   const bool chain = __builtin_amdgcn_readfirstlane(threadIdx.x) < 256;
   Part part;
-  if (!part_of(p, false, blockIdx.x, part)) return;
+  if (!part_of(p, blockIdx.x, part)) return;
   const int bh = part.bh, b = part.b, h = part.h, len = part.len, first = part.first, last = part.last;
   const int col0 = part.col0, cols = part.cols;
   const bool mine = 16 * wave < cols;
@@ -54,9 +54,6 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
     for (int i = 0; i < MT; ++i) {
       m[i] = zero;
       if (mine && from) m[i] = *reinterpret_cast<const f32x4*>(from + 16 * i + 4 * g);
-      if (part.unit_columns)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m[i][e] = 16 * i + 4 * g + e == col ? 1.f : 0.f;
     }
     const TileRows<DK> rows(lane);
     const TileColumns<DK> columns(lane);
@@ -222,7 +219,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
     if (s == 0) kl.load(p.k.at, k0 + t0 * p.k.t, p.k.t, live, DK, tid);
     if (OUT && s == min(1, KS - 1)) ql.load(p.q.at, q0 + t0 * p.q.t, p.q.t, live, DK, tid);
     if (s == min(2, KS - 1)) {
-      vl.load(p.v.at, v0 + t0 * p.v.t, p.v.t, live, part.unit_columns ? 0 : cols, tid);
+      vl.load(p.v.at, v0 + t0 * p.v.t, p.v.t, live, cols, tid);
       tl.load(matrix, tid);
     }
     if (s == KS - 1) {
@@ -313,8 +310,8 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
 
 template <int DK>
 hipError_t launch(const DeltaParams& p, hipStream_t s) {
-  if (p.o.at) delta_scan_kernel<DK, true><<<walk_blocks(p, false), 512, 0, s>>>(p);
-  else delta_scan_kernel<DK, false><<<walk_blocks(p, false), 512, 0, s>>>(p);
+  if (p.o.at) delta_scan_kernel<DK, true><<<walk_blocks(p), 512, 0, s>>>(p);
+  else delta_scan_kernel<DK, false><<<walk_blocks(p), 512, 0, s>>>(p);
   return hipGetLastError();
 }
 

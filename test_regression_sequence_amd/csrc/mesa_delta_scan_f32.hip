@@ -25,7 +25,7 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
   __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   Part part;
-  if (!part_of(p, false, blockIdx.x, part)) return;
+  if (!part_of(p, blockIdx.x, part)) return;
   const int bh = part.bh, b = part.b, h = part.h, hk = h / (p.H / p.Hk), len = part.len, first = part.first, last = part.last;
   const int col0 = part.col0, cols = part.cols;
   const int col = col0 + 16 * wave + r;                 // this lane's column of the state
@@ -40,9 +40,6 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
   for (int i = 0; i < MT; ++i) {
     m[i] = zero;
     if (mine && from) m[i] = *reinterpret_cast<const f32x4*>(from + 16 * i + 4 * g);
-    if (part.unit_columns)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) m[i][e] = 16 * i + 4 * g + e == col ? 1.f : 0.f;
   }
   RowLoads<DK, false, 256> kl, ql;
   RowLoads<64, false, 256> vl;
@@ -53,7 +50,7 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
     const int64_t t0 = 64 * (int64_t)c, unit = (int64_t)bh * p.NC + c;
     kl.load(p.k.at, k0 + t0 * p.k.t, p.k.t, live, DK, tid);
     if constexpr (OUT) ql.load(p.q.at, q0 + t0 * p.q.t, p.q.t, live, DK, tid);
-    vl.load(p.v.at, v0 + t0 * p.v.t, p.v.t, live, part.unit_columns ? 0 : cols, tid);
+    vl.load(p.v.at, v0 + t0 * p.v.t, p.v.t, live, cols, tid);
     ml.load(p.matrices + unit * L::kMatrices, tid);
     gl.load(p.gates + unit, tid);
   };
@@ -207,8 +204,8 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
 
 template <int DK>
 hipError_t launch(const DeltaParams& p, hipStream_t s) {
-  if (p.o.at) delta_scan_f32_kernel<DK, true><<<walk_blocks(p, false), 256, 0, s>>>(p);
-  else delta_scan_f32_kernel<DK, false><<<walk_blocks(p, false), 256, 0, s>>>(p);
+  if (p.o.at) delta_scan_f32_kernel<DK, true><<<walk_blocks(p), 256, 0, s>>>(p);
+  else delta_scan_f32_kernel<DK, false><<<walk_blocks(p), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 

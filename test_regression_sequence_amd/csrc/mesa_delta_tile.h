@@ -252,11 +252,22 @@ __device__ __forceinline__ f32x4 window_row(Window w, uint32_t lane_offset, uint
   }
 }
 
+// One number in the rows' type
+template <bool BF16>
+__device__ __forceinline__ float window_number(Window w, uint32_t lane_offset, uint32_t offset) {
+  if constexpr (BF16) return bf16_to_f32(__builtin_amdgcn_raw_buffer_load_b16(w, lane_offset, offset, 0));
+  else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(w, lane_offset, offset, 0));
+}
+
 __device__ __forceinline__ void window_store(Window w, uint32_t lane_offset, uint32_t offset, float v) {
   __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), w, lane_offset, offset, 0);
 }
+// 16 bytes: the offset goes to the lanes.  The hardware still reads such a store's data when
+// the next instruction runs; the compiler keeps that one from writing the registers where
+// the store has no scalar offset, and takes one with a scalar offset to be safe, which it is
+// not: zeros arrived as the product that the next instruction formed in their register.
 __device__ __forceinline__ void window_store(Window w, uint32_t lane_offset, uint32_t offset, f32x4 v) {
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), w, lane_offset, offset, 0);
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), w, lane_offset + offset, 0, 0);
 }
 // 4 numbers in the rows' type
 template <bool BF16>
@@ -415,50 +426,43 @@ __device__ __forceinline__ float* gate_at(const DeltaGate& x, int b, int h, int6
 __device__ __forceinline__ float decay(double a, double b) { return __builtin_amdgcn_exp2f((float)(a - b)); }
 
 // One workgroup's part of a walk: 64 columns of one head's state over one segment's
-// chunks.  The walk that finds what segments make of states (`probe`) has none for the
-// last (back: the first) segment, which nothing follows, starts the segment at the other
-// end from the given state, and forward also takes dk unit columns (`unit_columns`)
-// through the segments in between.
+// chunks.  The walk back that finds what segments make of zero (`probe`) has none for the
+// first segment, which nothing follows, and takes the last from the given gradient.
 struct Part {
   int bh, b, h, seg, col0, cols, len, first, last;
-  bool unit_columns;
 };
 
 // The workgroups of one head go to one XCD (workgroups are handed to the 8 XCDs in
 // turn), whose L2 they share.  False: no part.
-__device__ __forceinline__ bool part_of(const DeltaParams& p, bool back, uint32_t id, Part& x) {
-  const int values = (p.dv + 63) / 64, slices = values + (p.probe && !back ? (p.dk + 63) / 64 : 0);
-  const int segs = p.probe ? p.NS - 1 : p.NS, per = slices * segs;
+__device__ __forceinline__ bool part_of(const DeltaParams& p, uint32_t id, Part& x) {
+  const int slices = (p.dv + 63) / 64, per = slices * (p.probe ? p.NS - 1 : p.NS);
   const uint32_t xcd = id & 7, n = id >> 3;
   x.bh = (int)(n / per) * 8 + (int)xcd;
   if (x.bh >= p.B * p.H) return false;
-  const int rest = (int)(n % per), slice = rest % slices;
-  x.seg = rest / slices + (p.probe && back ? 1 : 0);
+  const int rest = (int)(n % per);
+  x.seg = rest / slices + (p.probe ? 1 : 0);
   x.b = x.bh / p.H;
   x.h = x.bh % p.H;
-  x.unit_columns = slice >= values;
-  if (x.unit_columns && x.seg == 0) return false;
-  x.col0 = 64 * (x.unit_columns ? slice - values : slice);
-  x.cols = min(64, (x.unit_columns ? p.dk : p.dv) - x.col0);
+  x.col0 = 64 * (rest % slices);
+  x.cols = min(64, p.dv - x.col0);
   x.len = delta_length(p, x.b);
   x.first = x.seg * p.L;
   x.last = max(min((x.len + 63) / 64, x.first + p.L), x.first);
   return true;
 }
-inline uint32_t walk_blocks(const DeltaParams& p, bool back) {
-  const int slices = (p.dv + 63) / 64 + (p.probe && !back ? (p.dk + 63) / 64 : 0);
-  return (uint32_t)((p.B * p.H + 7) / 8 * 8 * slices * (p.probe ? p.NS - 1 : p.NS));
+inline uint32_t walk_blocks(const DeltaParams& p) {
+  return (uint32_t)((p.B * p.H + 7) / 8 * 8 * ((p.dv + 63) / 64) * (p.probe ? p.NS - 1 : p.NS));
 }
 
 // Where a walk's state comes from and goes to: [.., dk] from column `col` on (null: zeros, nowhere).
 __device__ __forceinline__ const float* walk_from(const DeltaParams& p, const Part& x, const float* given, int edge, int col) {
-  if (x.unit_columns || (p.probe && x.seg != edge)) return nullptr;
+  if (p.probe && x.seg != edge) return nullptr;
   if (x.seg != edge) return p.seg_start + (((int64_t)x.bh * p.NS + x.seg) * p.dv + col) * p.dk;
   return given ? given + ((int64_t)x.bh * p.dv + col) * p.dk : nullptr;
 }
 __device__ __forceinline__ float* walk_to(const DeltaParams& p, const Part& x, float* wanted, int edge, int col) {
   const int64_t at = (int64_t)x.bh * p.NS + x.seg;
-  if (p.probe) return x.unit_columns ? p.seg_map + (at * p.dk + col) * p.dk : p.seg_add + (at * p.dv + col) * p.dk;
+  if (p.probe) return p.seg_add + (at * p.dv + col) * p.dk;
   return wanted && x.seg == edge ? wanted + ((int64_t)x.bh * p.dv + col) * p.dk : nullptr;
 }
 
