@@ -8,7 +8,8 @@
 // Nothing is formed beside the chain of states, so all eight waves are chains, 16
 // columns each, two on a SIMD to fill one another's waits: 128 columns a workgroup, and
 // with dv = dk = 64 both kinds in one.  A chunk's keys, inverse and gates go to LDS
-// while the chunk before is in the works; values go to their lanes.
+// while the chunk before is in the works; so do values of two bytes, those of four, whose
+// planes would not fit beside two chunks of keys, go to their lanes.
 #include "mesa_delta_tile.h"
 
 namespace mesa {
@@ -18,7 +19,8 @@ namespace {
 template <int DK, bool BF16>
 struct ProbeLds {
   static constexpr int NP = BF16 ? 1 : 3, kPlane = 64 * DK * 2;
-  static constexpr int kT = NP * kPlane, kGates = kT + 3 * kBlocksBytes, kBuffer = kGates + (int)sizeof(DeltaGates);
+  static constexpr int kT = NP * kPlane, kGates = kT + 3 * kBlocksBytes, kV = kGates + (int)sizeof(DeltaGates),
+                       kBuffer = kV + (BF16 ? 64 * 256 : 0);
 };
 
 int slices_of(const DeltaParams& p) { return (p.dv + p.dk + 127) / 128; }
@@ -26,7 +28,7 @@ int slices_of(const DeltaParams& p) { return (p.dv + p.dk + 127) / 128; }
 template <int DK, bool BF16>
 __global__ __launch_bounds__(512, 2) void delta_probe_kernel(DeltaParams p, int slices) {
   using L = ProbeLds<DK, BF16>;
-  constexpr int NP = L::NP, MT = DK / 16, KS = DK / 32, ES = BF16 ? 2 : 4;
+  constexpr int NP = L::NP, MT = DK / 16, KS = DK / 32;
   __shared__ __attribute__((aligned(16))) char lds[2][L::kBuffer];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   // one head's workgroups on one XCD, whose L2 they share
@@ -57,6 +59,7 @@ __global__ __launch_bounds__(512, 2) void delta_probe_kernel(DeltaParams p, int 
   RowLoads<DK, BF16, 512> kl;
   CopyLoads<3 * kBlocksBytes, 512> tl;
   CopyLoads<sizeof(DeltaGates), 512> gl;
+  RowLoads<128, true, 512> vl;
   f32x4 v[4], v_next[4];  // V's rows 16 i + 4 g + e, column `col`
   auto load = [&](int c) {
     const int live = min(len - 64 * c, 64);
@@ -64,20 +67,25 @@ __global__ __launch_bounds__(512, 2) void delta_probe_kernel(DeltaParams p, int 
     kl.load(p.k.at, k0 + t0 * p.k.t, p.k.t, live, DK, tid);
     tl.load(p.matrices + unit * (int64_t)delta_matrix_bytes(BF16 ? 2 : 3), tid);
     gl.load(p.gates + unit, tid);
-    const Window from = window_at(static_cast<const char*>(p.v.at) + (v0 + t0 * p.v.t) * ES);
-    const uint32_t at = (4 * g * (uint32_t)p.v.t + col) * ES, step = (uint32_t)p.v.t * ES;
-    const int there = unit_columns ? 0 : live - 4 * g;
+    if constexpr (BF16) {
+      vl.load(p.v.at, v0 + 128 * slice + t0 * p.v.t, p.v.t, live, p.dv - 128 * slice, tid);
+    } else {
+      const Window from = window_at(static_cast<const float*>(p.v.at) + v0 + t0 * p.v.t);
+      const uint32_t at = (4 * g * (uint32_t)p.v.t + col) * 4, step = (uint32_t)p.v.t * 4;
+      const int there = unit_columns ? 0 : live - 4 * g;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        v_next[i][e] = window_number<BF16>(from, 16 * i + e < there ? at : kNowhere, (16 * i + e) * step);
+        for (int e = 0; e < 4; ++e)
+          v_next[i][e] = window_number(from, 16 * i + e < there ? at : kNowhere, (16 * i + e) * step);
+    }
   };
   auto store = [&](int c) {
     char* to = lds[c & 1];
     kl.store(to, L::kPlane, tid);
     tl.store(to + L::kT, tid);
     gl.store(to + L::kGates, tid);
+    if constexpr (BF16) vl.store(to + L::kV, 0, tid);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = v_next[i];
   };
@@ -107,6 +115,9 @@ __global__ __launch_bounds__(512, 2) void delta_probe_kernel(DeltaParams p, int 
           for (int i = 0; i < 4; ++i) f[(s + 1) & 1][i] = rows.template planes<NP>(keys, L::kPlane, 16 * i, s + 1);
         } else {
           t = pair_of<true, 3>(keys + L::kT, 0, lane);
+          if constexpr (BF16)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = column_values<128, 1>(keys + L::kV, 0, 16 * i, wave, lane);
         }
         fence<BF16>();
         mma_tiles<2>(f[s & 1], mp[s], x);

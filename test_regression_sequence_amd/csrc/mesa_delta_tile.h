@@ -252,11 +252,8 @@ __device__ __forceinline__ f32x4 window_row(Window w, uint32_t lane_offset, uint
   }
 }
 
-// One number in the rows' type
-template <bool BF16>
 __device__ __forceinline__ float window_number(Window w, uint32_t lane_offset, uint32_t offset) {
-  if constexpr (BF16) return bf16_to_f32(__builtin_amdgcn_raw_buffer_load_b16(w, lane_offset, offset, 0));
-  else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(w, lane_offset, offset, 0));
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(w, lane_offset, offset, 0));
 }
 
 __device__ __forceinline__ void window_store(Window w, uint32_t lane_offset, uint32_t offset, float v) {
