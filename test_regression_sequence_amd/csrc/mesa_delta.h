@@ -29,9 +29,11 @@ struct DeltaGates {
   float beta[kDeltaChunk];  // 0 behind the sequence
 };
 
-// Bytes of a chunk's two triangular 64x64 matrices as operands of the walks: the
+// Bytes of a chunk's two triangular 64x64 matrices as operands of the walk forward: the
 // inverse in three bf16 parts and the products of its queries and keys in `parts`.
 constexpr size_t delta_matrix_bytes(int parts) { return (3 + parts) * 6 * 1024; }
+// ... and for the walk back in fp32: ten tiles each.
+constexpr size_t kDeltaMatrixBytes = 2 * 10 * 1024;
 
 struct DeltaParams {
   DeltaRows q, k, v, o;             // o.at null: the states alone
@@ -56,7 +58,7 @@ struct DeltaParams {
   DeltaGate dgamma, dbeta;
   const float* d_sfinal;
   float* ds0;
-  char* matrices_t;                 // [B H, NC, delta_matrix_bytes(3)]: the backward pass's
+  char* matrices_t;                 // [B H, NC, kDeltaMatrixBytes]: the backward pass's
   float* dstates;                   // [B H, NC, dv, dk]: the gradient behind each chunk
   float* e;                         // [B H, NC, 64, dv]: dv_t / beta_t
   float *dq_heads, *dk_heads;       // [B, H, T, dk] where heads share keys

@@ -22,7 +22,7 @@ namespace {
 
 template <int DK>
 struct AdjointLds {
-  static constexpr int kTile = 64 * DK * 2, kMatrix = (int)delta_matrix_bytes(3), kGate = sizeof(DeltaGates);
+  static constexpr int kTile = 64 * DK * 2, kGate = sizeof(DeltaGates);
   static constexpr int kK = 0, kQ = kK + 2 * kTile, kO = kQ + kTile, kT = kO + 2 * 64 * 128, kA = kT + 3 * kBlocksBytes,
                        kGates = kA + 3 * kBlocksBytes, kU = kGates + 2 * kGate, kN = kU + 4 * 4096,
                        kBytes = kN + 4 * DK * 64;
@@ -188,13 +188,13 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
   const int64_t q0 = b * p.q.b + hk * p.q.h, k0 = b * p.k.b + hk * p.k.h, o0 = b * p.d_o.b + h * p.d_o.h + col0;
   RowLoads<DK, true, 256> kl, ql;
   RowLoads<64, true, 256> ol;
-  CopyLoads<3 * kBlocksBytes, 256> tl, al;
+  TriangleLoads<3, false, 256> tl, al;
   CopyLoads<L::kGate, 256> gl;
   auto live = [&](int c) { return min(len - 64 * c, 64); };
   // what A^T dO takes of a chunk ...
   auto load_first = [&](int c) {
     ol.load(p.d_o.at, o0 + 64 * (int64_t)c * p.d_o.t, p.d_o.t, live(c), cols, tid);
-    al.load(p.matrices_t + ((int64_t)bh * p.NC + c) * L::kMatrix + 3 * kBlocksBytes, tid);
+    al.load(p.matrices_t + ((int64_t)bh * p.NC + c) * (2 * kTriangleBytes) + kTriangleBytes, tid);
   };
   auto store_first = [&](int c) {
     ol.store(lds + L::kO + (c & 1) * 64 * 128, 0, tid);
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
     const int64_t t0 = 64 * (int64_t)c, unit = (int64_t)bh * p.NC + c;
     if (s == 0) kl.load(p.k.at, k0 + t0 * p.k.t, p.k.t, live(c), DK, tid);
     if (s == min(1, KS - 1)) ql.load(p.q.at, q0 + t0 * p.q.t, p.q.t, live(c), DK, tid);
-    if (s == min(2, KS - 1)) tl.load(p.matrices_t + unit * L::kMatrix, tid);
+    if (s == min(2, KS - 1)) tl.load(p.matrices_t + unit * (2 * kTriangleBytes), tid);
     if (s == KS - 1) gl.load(p.gates + unit, tid);
   };
   auto store_rest = [&](int c) {
@@ -229,6 +229,8 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(u_at + i * 1024) = u[i];
   };
+  tl.clear(lds + L::kT, tid);
+  al.clear(lds + L::kA, tid);
   if (first < last) {
     load_first(last - 1);
 #pragma unroll

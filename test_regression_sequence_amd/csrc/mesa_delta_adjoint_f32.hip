@@ -12,9 +12,9 @@ namespace {
 template <int DK>
 struct AdjointLds {
   static constexpr int NP = 3;
-  static constexpr int kPlane = 64 * DK * 2, kMatrices = (int)delta_matrix_bytes(3);
+  static constexpr int kPlane = 64 * DK * 2;
   static constexpr int kK = 0, kQ = kK + NP * kPlane, kO = kQ + NP * kPlane, kT = kO + NP * 64 * 128,
-                       kA = kT + 3 * kBlocksBytes, kGates = kT + kMatrices, kBytes = kGates + sizeof(DeltaGates);
+                       kA = kT + 3 * kBlocksBytes, kGates = kA + 3 * kBlocksBytes, kBytes = kGates + sizeof(DeltaGates);
 };
 
 template <int DK>
@@ -40,7 +40,7 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p
   }
   RowLoads<DK, false, 256> kl, ql;
   RowLoads<64, false, 256> ol;
-  CopyLoads<L::kMatrices, 256> ml;
+  TriangleLoads<3, false, 256> tl, al;
   CopyLoads<sizeof(DeltaGates), 256> gl;
   auto load = [&](int c) {
     const int live = min(len - 64 * c, 64);
@@ -48,17 +48,21 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p
     kl.load(p.k.at, k0 + t0 * p.k.t, p.k.t, live, DK, tid);
     ql.load(p.q.at, q0 + t0 * p.q.t, p.q.t, live, DK, tid);
     ol.load(p.d_o.at, o0 + t0 * p.d_o.t, p.d_o.t, live, cols, tid);
-    ml.load(p.matrices_t + unit * L::kMatrices, tid);
+    tl.load(p.matrices_t + unit * (2 * kTriangleBytes), tid);
+    al.load(p.matrices_t + unit * (2 * kTriangleBytes) + kTriangleBytes, tid);
     gl.load(p.gates + unit, tid);
   };
   auto store = [&]() {
     kl.store(lds + L::kK, L::kPlane, tid);
     ql.store(lds + L::kQ, L::kPlane, tid);
     ol.store(lds + L::kO, 64 * 128, tid);
-    ml.store(lds + L::kT, tid);
+    tl.store(lds + L::kT, tid);
+    al.store(lds + L::kA, tid);
     gl.store(lds + L::kGates, tid);
   };
 
+  tl.clear(lds + L::kT, tid);
+  al.clear(lds + L::kA, tid);
   if (first < last) {
     load(last - 1);
     store();

@@ -143,7 +143,7 @@ size_t carve(const mesa_delta_desc* d, bool keep, void* workspace, DeltaParams& 
   if (keep) {
     p.states = w.take<float>(units * state);
     p.w = w.take<float>(units * kDeltaChunk * d->dv * 4);
-    p.matrices_t = w.take<char>(units * delta_matrix_bytes(3));
+    p.matrices_t = w.take<char>(units * kDeltaMatrixBytes);
     p.dstates = w.take<float>(units * state);
     p.e = w.take<float>(units * kDeltaChunk * d->dv * 4);
     if (d->H != d->Hk) {

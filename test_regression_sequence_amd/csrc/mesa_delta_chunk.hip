@@ -12,10 +12,13 @@
 // There are B H T / 64 chunks, all independent, so what can be done here is taken
 // off the walks, whose chunks follow one another.  Four waves a chunk: wave w forms row
 // tile w of both products, inverts diagonal block w and then has the inverse's column
-// of blocks w, which depends on no other column.  The matrices leave as the walks'
-// operands, in bf16 parts.  Logarithms of the forget factors
-// are summed in 64 bits, so that a ratio c_t / c_j keeps fp32's precision however
-// strong the decay before it.
+// of blocks w, which depends on no other column.  The forward walk's
+// matrices leave as its operands, in bf16 parts, the backward walk's in fp32, tile by tile
+// in the operands' order: two thirds of the bytes for conversions that the waves beside
+// that walk's chain have the time for (train step at B=8 H=16 T=4096 d=128: walk back 341
+// -> 317 us; forward those waves form o, and the walk went from 232 to 258 us).
+// Logarithms of the forget factors are summed in 64 bits, so that a ratio c_t / c_j keeps
+// fp32's precision however strong the decay before it.
 #include "mesa_delta_tile.h"
 
 namespace mesa {
@@ -27,11 +30,10 @@ constexpr int kLd = 20;  // floats of a 16-wide row in LDS
 __host__ __device__ constexpr int tile_of(int i, int j) { return i * (i + 1) / 2 + j; }
 
 template <int DK, bool BF16, bool TRANSPOSED>
-__global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
-  constexpr int NP = BF16 ? 1 : 3, ES = BF16 ? 2 : 4, NA = BF16 && !TRANSPOSED ? 2 : 3;
+__global__ __launch_bounds__(256, BF16 || DK == 32 ? 4 : 2) void delta_chunk_kernel(DeltaParams p) {
+  constexpr int NP = BF16 ? 1 : 3, ES = BF16 ? 2 : 4, NA = BF16 ? 2 : 3;
   __shared__ __attribute__((aligned(16))) float low[10][16 * kLd];
   __shared__ __attribute__((aligned(16))) float diag[4][16 * kLd];
-  __shared__ __attribute__((aligned(16))) float products[4][256];  // A^T's tiles on their way to pairs of rows
   __shared__ double sg[kDeltaChunk];
   __shared__ float sbeta[kDeltaChunk];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -91,7 +93,11 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
   }
   __syncthreads();
 
-  char* const to = (TRANSPOSED ? p.matrices_t : p.matrices) + (int64_t)unit * delta_matrix_bytes(NA) + lane * 16;
+  char* const to = (TRANSPOSED ? p.matrices_t + (int64_t)unit * (2 * kTriangleBytes)
+                               : p.matrices + (int64_t)unit * delta_matrix_bytes(NA)) + lane * 16;
+  auto put_tile = [&](int matrix, int i, int j, const f32x4& x) {
+    *reinterpret_cast<f32x4*>(to + matrix * kTriangleBytes + triangle_tile<false>(i, j) * 1024) = x;
+  };
   // A block's two tiles, in parts, to its place
   auto put = [&](int matrix, int parts, int block, const f32x4& lo, const f32x4& hi) {
     const Planes<3> f = split8<3>(lo, hi);
@@ -143,26 +149,14 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
       if (wave == 0) put(1, NA, lower_block(0, 0), d, zero);
       else put(1, NA, lower_block(wave, 0), a[0], wave == 1 ? d : a[1]);
       if (wave >= 2) put(1, NA, lower_block(wave, 1), wave == 2 ? d : a[2], wave == 2 ? zero : d);
-    } else if (!(wave & 1)) {  // blocks of a transposed matrix pair up tiles of two queries: an even wave's go to the next
+    } else {
 #pragma unroll
       for (int j = 0; j < 3; ++j)
-        if (j < wave) *reinterpret_cast<f32x4*>(&products[j + wave / 2][lane * 4]) = a[j];
-      *reinterpret_cast<f32x4*>(&products[wave == 0 ? 0 : 3][lane * 4]) = a[3];
+        if (j < wave) put_tile(1, j, wave, a[j]);
+      put_tile(1, wave, wave, a[3]);
     }
   }
   __syncthreads();
-  if constexpr (TRANSPOSED) {
-    if (p.q.at && (wave & 1)) {
-      // wave 1: columns 0 (tiles 0 and 1) and 1 (nothing and 1); wave 3: columns 0 .. 2 with tile 2, 3 without
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j > wave) continue;
-        f32x4 even = zero;
-        if (j < wave) even = *reinterpret_cast<const f32x4*>(&products[wave == 1 ? 0 : j == 2 ? 3 : j + 1][lane * 4]);
-        put(1, NA, upper_block(j, wave / 2), even, j == wave ? a[3] : a[j]);
-      }
-    }
-  }
 
   {  // diagonal block `wave`, lane r (of each lane group) its column r
     const float* l = low[tile_of(wave, wave)];
@@ -212,8 +206,9 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
   // a lane's 4 numbers lie along the later product's inner index: rows of the
   // transposed inverse as they are, rows of the inverse by way of LDS
   if constexpr (TRANSPOSED) {
-    if (wave < 2) put(0, 3, upper_block(wave, 0), t[0], t[1]);
-    put(0, 3, upper_block(wave, 1), t[2], t[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i >= wave) put_tile(0, wave, i, t[i]);
   } else {
     __syncthreads();
 #pragma unroll

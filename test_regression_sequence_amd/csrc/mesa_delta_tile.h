@@ -345,6 +345,45 @@ constexpr int kBlocksBytes = 6 * 1024;
 __device__ __forceinline__ constexpr int lower_block(int i, int s) { return i < 2 ? i : 2 * i - 2 + s; }  // s <= i / 2
 __device__ __forceinline__ constexpr int upper_block(int i, int s) { return i < 2 ? 2 * i + s : 2 + i; }  // s >= i / 2
 
+// In memory: the fp32 numbers of its ten tiles, each 64 lanes' four, in the order of the
+// blocks' halves.
+constexpr int kTriangleBytes = (int)kDeltaMatrixBytes / 2;
+template <bool LOWER>
+__device__ __forceinline__ constexpr int triangle_tile(int i, int j) {  // row tile i, column tile j
+  const int half = 2 * (LOWER ? lower_block(i, j / 2) : upper_block(i, j / 2)) + (j & 1);
+  return LOWER ? half - (half > 1) - (half > 7) : half - (half > 4) - (half > 10);
+}
+template <bool LOWER>
+__device__ __forceinline__ constexpr int triangle_half(int tile) {
+  return LOWER ? tile + (tile >= 1) + (tile >= 6) : tile + (tile >= 4) + (tile >= 9);
+}
+
+// Its way from there to N planes of blocks.
+template <int N, bool LOWER, int THREADS>
+struct TriangleLoads : CopyLoads<kTriangleBytes, THREADS> {
+  using Loads = CopyLoads<kTriangleBytes, THREADS>;
+  static __device__ __forceinline__ void put(char* blocks, int half, int lane, const bf16x4 (&x)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      *reinterpret_cast<bf16x4*>(blocks + n * kBlocksBytes + (half >> 1) * 1024 + (half & 1) * 8 + lane * 16) = x[n];
+  }
+  // the two halves beyond the diagonal, once
+  static __device__ __forceinline__ void clear(char* blocks, int tid) {
+    const bf16x4 none[N] = {};
+    if (tid < 64) put(blocks, LOWER ? 1 : 4, tid, none);
+    else if (tid < 128) put(blocks, LOWER ? 7 : 10, tid - 64, none);
+  }
+  __device__ __forceinline__ void store(char* blocks, int tid) const {
+#pragma unroll
+    for (int n = 0; n < Loads::kN; ++n)
+      if ((n + 1) * THREADS <= Loads::kPieces || tid + n * THREADS < Loads::kPieces) {
+        bf16x4 x[N];
+        split4<N>(__builtin_bit_cast(f32x4, Loads::r[n]), x);
+        put(blocks, triangle_half<LOWER>(__builtin_amdgcn_readfirstlane(tid >> 6) + n * (THREADS / 64)), tid & 63, x);
+      }
+  }
+};
+
 template <int N>
 __device__ __forceinline__ Planes<N> block_of(const char* blocks, int block, int lane) {
   Planes<N> f;
