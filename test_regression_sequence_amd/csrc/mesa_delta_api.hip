@@ -96,19 +96,23 @@ mesa_status check_delta(const mesa_delta_desc* d) {
 
 // In how many segments a walk goes.  A walk of one workgroup a head and 64 columns takes
 // its chunks one after the other; with fewer of those than the 256 CUs, segments of it run
-// side by side, after a walk that finds what each makes of unit rows and of zero (dk more
-// columns) and a launch that joins them.  In times of one chunk (about 2.7 us), that launch
-// and the additional walk's take about 3 and half a chunk a segment.
+// side by side, after a walk that finds what each makes of unit rows and of zero (128 of
+// dv + dk columns a workgroup) and a launch that joins them.  In times of one chunk (about
+// 2.7 us, in fp32 twice that), the two launches take about 3 and half a chunk a segment.
+// Measured, one sequence, in segments and in one walk: 1024 tokens and 4 heads of 64,
+// forward 38 and 49 us, gradients 86 and 113, in fp32 49 and 101, 109 and 210; 4 heads of
+// 128, 59 and 60, 137 and 158; 4096 tokens and 16 heads of 128, 109 and 194, 319 and 565.
 int segments_of(const mesa_delta_desc* d) {
   const int64_t heads = (int64_t)d->B * d->H, values = (d->dv + 63) / 64, both = (d->dv + d->dk + 127) / 128;
   const int chunks = chunks_of(d);
+  const double more = d->dtype == MESA_BF16 ? 1.0 : 0.5;
   const auto rounds = [](int64_t blocks) { return (double)((blocks + 255) / 256); };
   int best = 1;
   double least = 0.9 * chunks * rounds(heads * values);
-  for (int n = 2; n <= 32 && n * 4 <= chunks; ++n) {
+  for (int n = 2; n <= 32 && n * 2 <= chunks; ++n) {
     const int per = (chunks + n - 1) / n;
     if ((chunks + per - 1) / per != n) continue;  // (no segment stays empty)
-    const double time = per * (rounds(heads * (n - 1) * both) + rounds(heads * n * values)) + 3 + 0.5 * n;
+    const double time = per * (rounds(heads * (n - 1) * both) + rounds(heads * n * values)) + more * (3 + 0.5 * n);
     if (time < least) {
       best = n;
       least = time;
