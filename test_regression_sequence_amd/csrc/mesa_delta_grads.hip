@@ -27,7 +27,13 @@ struct GradLds {
   static constexpr int NP = BF16 ? 1 : 3, NZ = BF16 ? 2 : 3;
   static constexpr int kState = 32 * DK * 2, kU = 64 * 64, kPlane = 64 * DK * 2, kZ = 64 * 128;
   static constexpr int kS = 0, kD = 3 * kState, kUAt = 6 * kState, kEAt = kUAt + 3 * kU, kOAt = kEAt + 3 * kU,
-                       kFirst = kOAt + NP * kU;
+                       kSlice = kOAt + NP * kU;
+  // Two workgroups a CU hide one another's waits where 128 registers a lane do (keys and
+  // queries then wait for the slices' end): 50 -> 41 us at B=4 H=8 T=2048 d=64.  Else two
+  // slices in LDS where they fit: one is converted beside the products of the other, a
+  // barrier a slice (750 -> 730 us at B=8 H=16 T=4096 d=128 bf16).
+  static constexpr bool kPair = BF16 && DK <= 64, kTwo = !kPair && (BF16 || DK < 128);
+  static constexpr int kFirst = (kTwo ? 2 : 1) * kSlice;
   static constexpr int kK = 0, kQ = NP * kPlane, kZAt = 2 * NP * kPlane, kYAt = kZAt + NZ * kZ, kSecond = kYAt + NZ * kZ;
   static constexpr int kBytes = kFirst > kSecond ? kFirst : kSecond;
 };
@@ -37,9 +43,7 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
   using L = GradLds<DK, BF16>;
   using Out = std::conditional_t<BF16, __bf16, float>;
   constexpr int NP = L::NP, NZ = L::NZ, MH = DK / 32, KS = DK / 32, OMAX = BF16 ? 1 : 2;
-  // Two workgroups a CU hide one another's waits where 128 registers a lane do (keys and
-  // queries then wait for the slices' end): 50 -> 41 us at B=4 H=8 T=2048 d=64.
-  constexpr bool PAIR = BF16 && DK <= 64;
+  constexpr bool PAIR = L::kPair;
   constexpr int kPieces = 8 * DK, NS = (kPieces + 511) / 512;  // 16-byte pieces of a state's slice
   __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
   __shared__ __attribute__((aligned(16))) DeltaGates gates;
@@ -129,8 +133,8 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
   };
   if constexpr (!PAIR) load_rest();
   if (tid < 64) gammas[tid] = tid < live ? *gate_at(p.gamma, b, h, t0 + tid) : 1.f;
-  for (int d0 = 0; d0 < p.dv; d0 += 32) {
-    __syncthreads();
+  // the slice in registers to LDS, in planes
+  auto stage = [&](int d0, char* to) {
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
       const int piece = tid + 512 * n, row = piece / (DK / 4), col = piece % (DK / 4) * 4;
@@ -140,36 +144,34 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
       split4<3>(dl[n], d);
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
-        *reinterpret_cast<bf16x4*>(lds + L::kS + i * L::kState + tile_at<DK>(row, 2 * col)) = a[i];
-        *reinterpret_cast<bf16x4*>(lds + L::kD + i * L::kState + tile_at<DK>(row, 2 * col)) = d[i];
+        *reinterpret_cast<bf16x4*>(to + L::kS + i * L::kState + tile_at<DK>(row, 2 * col)) = a[i];
+        *reinterpret_cast<bf16x4*>(to + L::kD + i * L::kState + tile_at<DK>(row, 2 * col)) = d[i];
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) along = fmaf(sl[n][e], dl[n][e], along);
     }
-    {
-      const uint32_t at = tile_at<32>(from, 2 * at4);
-      bf16x4 uu[3], x[3], o[NP];
-      split4<3>(wl * beta_from, uu);
-      split4<3>(el, x);
-      split4<NP>(ol, o);
+    const uint32_t at = tile_at<32>(from, 2 * at4);
+    bf16x4 uu[3], x[3], o[NP];
+    split4<3>(wl * beta_from, uu);
+    split4<3>(el, x);
+    split4<NP>(ol, o);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        *reinterpret_cast<bf16x4*>(lds + L::kUAt + i * L::kU + at) = uu[i];
-        *reinterpret_cast<bf16x4*>(lds + L::kEAt + i * L::kU + at) = x[i];
-        if (i < NP) *reinterpret_cast<bf16x4*>(lds + L::kOAt + i * L::kU + at) = o[i];
-      }
-      window_store_row<BF16>(dvs, from < here && at4 < p.dv - d0 ? dv_at : kNowhere, d0 * sizeof(Out), el * beta_from);
-#pragma unroll
-      for (int n = 0; n < 4; ++n) dbeta = fmaf(el[n], wl[n], dbeta);
+    for (int i = 0; i < 3; ++i) {
+      *reinterpret_cast<bf16x4*>(to + L::kUAt + i * L::kU + at) = uu[i];
+      *reinterpret_cast<bf16x4*>(to + L::kEAt + i * L::kU + at) = x[i];
+      if (i < NP) *reinterpret_cast<bf16x4*>(to + L::kOAt + i * L::kU + at) = o[i];
     }
-    load(d0 + 32);  // (behind the last slice: zeros; with a branch around it the compiler waits, 767 -> 835 us)
-    __syncthreads();
+    window_store_row<BF16>(dvs, from < here && at4 < p.dv - d0 ? dv_at : kNowhere, d0 * sizeof(Out), el * beta_from);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) dbeta = fmaf(el[n], wl[n], dbeta);
+  };
+  auto products = [&](const char* slice) {
     {
-      const Planes<NP> of = slice_rows.template planes<NP>(lds + L::kOAt, L::kU, 16 * tile, 0);
-      const Planes<3> ef = slice_rows.template planes<3>(lds + L::kEAt, L::kU, 16 * tile, 0);
+      const Planes<NP> of = slice_rows.template planes<NP>(slice + L::kOAt, L::kU, 16 * tile, 0);
+      const Planes<3> ef = slice_rows.template planes<3>(slice + L::kEAt, L::kU, 16 * tile, 0);
 #pragma unroll
       for (int i = 0; i < MH; ++i) {
-        const Planes<3> s = columns.template planes<3>(lds + L::kS, L::kState, 0, i);
+        const Planes<3> s = columns.template planes<3>(slice + L::kS, L::kState, 0, i);
         aq[i] = mma<2>(s, of, aq[i]);
         ak[i] = mma<2>(s, ef, ak[i]);
         fence<PAIR>();
@@ -177,14 +179,34 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (j <= tile) {
-          const Planes<3> x = slice_rows.template planes<3>(lds + L::kUAt, L::kU, 16 * j, 0);
+          const Planes<3> x = slice_rows.template planes<3>(slice + L::kUAt, L::kU, 16 * j, 0);
           zy[j] = half ? mma<2>(x, ef, zy[j]) : mma<2>(x, of, zy[j]);
         }
     }
     fence<PAIR>();
-    const Planes<3> uf = slice_rows.template planes<3>(lds + L::kUAt, L::kU, 16 * tile, 0);
+    const Planes<3> uf = slice_rows.template planes<3>(slice + L::kUAt, L::kU, 16 * tile, 0);
 #pragma unroll
-    for (int i = 0; i < MH; ++i) ad[i] = mma<2>(columns.template planes<3>(lds + L::kD, L::kState, 0, i), uf, ad[i]);
+    for (int i = 0; i < MH; ++i) ad[i] = mma<2>(columns.template planes<3>(slice + L::kD, L::kState, 0, i), uf, ad[i]);
+  };
+  // (Loads behind the last slice give zeros; with a branch around them the compiler waits, 767 -> 835 us.)
+  if constexpr (L::kTwo) {
+    stage(0, lds);
+    load(32);
+    for (int d0 = 0; d0 < p.dv; d0 += 32) {
+      char *now = lds + (d0 >> 5 & 1) * L::kSlice, *next = lds + (~d0 >> 5 & 1) * L::kSlice;
+      __syncthreads();
+      products(now);
+      stage(d0 + 32, next);
+      load(d0 + 64);
+    }
+  } else {
+    for (int d0 = 0; d0 < p.dv; d0 += 32) {
+      __syncthreads();
+      stage(d0, lds);
+      load(d0 + 32);
+      __syncthreads();
+      products(lds);
+    }
   }
 
   if constexpr (PAIR) load_rest();
