@@ -1061,6 +1061,8 @@ def delta_step(q, k, v, gamma, beta, s_state, *, out=None, stream=None) -> dict:
 
 
 _CODES = {torch.float32: MESA_F32, torch.bfloat16: MESA_BF16}
+_device_index, _is_dense, _numel, _data_ptr = (torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.numel,
+                                               torch.Tensor.data_ptr)
 
 
 def _clip_lists(grads, out, stream):
@@ -1073,14 +1075,13 @@ def _clip_lists(grads, out, stream):
     if stream is not None and stream.device != dev:
         raise MesaError(f"the stream belongs to {stream.device}, grads are on {dev}")
     n = len(grads)
-    codes, index = [], dev.index
-    for i, g in enumerate(grads):
-        code = _CODES.get(g.dtype)
-        if code is None or g.get_device() != index or not g.is_contiguous():
-            raise MesaError(f"grads[{i}] must be dense float32 or bfloat16 on {dev}, got {g.dtype} on {g.device}")
-        codes.append(code)
-    sizes = [g.numel() for g in grads]
-    at = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+    codes = [_CODES.get(g.dtype) for g in grads]
+    if None in codes or set(map(_device_index, grads)) != {dev.index} or not all(map(_is_dense, grads)):
+        i, g = next((i, g) for i, g in enumerate(grads)
+                    if codes[i] is None or _device_index(g) != dev.index or not g.is_contiguous())
+        raise MesaError(f"grads[{i}] must be dense float32 or bfloat16 on {dev}, got {g.dtype} on {g.device}")
+    sizes = list(map(_numel, grads))
+    at = (ctypes.c_void_p * n)(*map(_data_ptr, grads))
     to = at
     if out is not None and out is not grads:
         if len(out) != n:
@@ -1088,7 +1089,7 @@ def _clip_lists(grads, out, stream):
         for i, (g, o) in enumerate(zip(grads, out)):
             if o.dtype is not g.dtype or o.shape != g.shape or o.device != dev or not o.is_contiguous():
                 raise MesaError(f"out[{i}] must be as grads[{i}] is")
-        to = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
+        to = (ctypes.c_void_p * n)(*map(_data_ptr, out))
     return dev, n, at, to, (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*codes)
 
 
