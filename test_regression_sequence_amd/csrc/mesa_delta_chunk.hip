@@ -19,6 +19,11 @@
 // -> 317 us; forward those waves form o, and the walk went from 232 to 258 us).
 // Logarithms of the forget factors are summed in 64 bits, so that a ratio c_t / c_j keeps
 // fp32's precision however strong the decay before it.
+//
+// Memory bounds it where there are many chunks: at B=8 H=16 T=4096 d=128 bf16 106 us for
+// 0.52 GB forward (4.9 TB/s, a large copy's rate) and 95 us for 0.44 GB back.  One round of
+// chunks is a chain of 6.5 us (fp32 9): loads 1, logarithms 1, products and decays 2, the
+// diagonal blocks 1, the others and the way out 1.5.
 #include "mesa_delta_tile.h"
 
 namespace mesa {

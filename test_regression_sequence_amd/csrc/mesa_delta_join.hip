@@ -5,7 +5,8 @@
 // the segment at the walk's start has the given state in its Q already.  From one
 // segment to the next that is a 16 x dk by dk x dk product for each 16 rows,
 // in fp32 matrix instructions: a workgroup has 16 rows in LDS, its waves the tiles of
-// the result's columns.
+// the result's columns.  8 segments: 20 us at H=16 dk=128, 7 us at 32 heads of 64; maps
+// loaded one or three steps ahead change nothing.
 #include "mesa_delta_tile.h"
 
 namespace mesa {

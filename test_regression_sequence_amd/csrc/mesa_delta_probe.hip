@@ -10,6 +10,12 @@
 // with dv = dk = 64 both kinds in one.  A chunk's keys, inverse and gates go to LDS
 // while the chunk before is in the works; so do values of two bytes, those of four, whose
 // planes would not fit beside two chunks of keys, go to their lanes.
+//
+// B=1 H=16 T=32768 d=128, 7 of 8 segments of 64 chunks: 305 us, 4.8 us a chunk and 128
+// columns, of which a SIMD's matrix unit works 38 % and its vector unit 41 %, hardly at the
+// same time (four chains of 16 columns as in the walk itself: 2.7 us for 64 columns).  The
+// two waves of a SIMD half a chunk apart, so that conversions of one meet products of the
+// other, took 333 us: the second barrier a chunk costs more.
 #include "mesa_delta_tile.h"
 
 namespace mesa {

@@ -15,6 +15,11 @@
 // chunk and form o from the planes of M and U that the first four leave in LDS.
 //     first half:   chain K M, W, U, half of K^T U       others Q M, the next chunk's loads
 //     second half:  chain the rest of K^T U, planes of M  others A U, next chunk to LDS, o
+//
+// A chunk takes 2.8 us where few workgroups run, of which the chain's 132 products are 0.9
+// and their operands' ways through conversions and LDS the rest, and 3.6 us on all CUs (B=1
+// H=16 T=32768 d=128 in 8 segments: 232 us).  With states and W kept memory bounds it: at
+// B=8 H=16 T=4096 d=128 370 us for 1.6 GB, 4.3 TB/s where a large copy reaches 4.9.
 #include "mesa_delta_tile.h"
 
 namespace mesa {

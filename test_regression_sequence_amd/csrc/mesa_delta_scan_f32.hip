@@ -3,7 +3,9 @@
 // The walk of mesa_delta_scan.hip for rows that are themselves three bf16 planes: six
 // products where bf16 rows take three, and planes of keys and queries that fill the
 // LDS (161 KB at dk = 128), so the workgroup is the four waves that hold the state, and
-// each forms its columns of o too.
+// each forms its columns of o too.  A chunk takes 5.7 us at dk = 64: 216 products (1.5 us) and,
+// between its barriers, the conversions of the next chunk's rows, which nothing hides
+// (B=5 H=6 T=777 dk=64 dv=96: 73 us in one walk, in 4 segments 25 us and 26 to form them).
 #include "mesa_delta_tile.h"
 
 namespace mesa {

