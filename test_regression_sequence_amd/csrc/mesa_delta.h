@@ -45,10 +45,12 @@ struct DeltaParams {
   // A walk in NS segments of L chunks (NS = 1: whole).  seg_map: [B H, NS, dk, dk], row j what
   // an inner segment makes of the state whose row is unit vector j; seg_add: [B H, NS, dv, dk], what
   // it makes of a zero state (the segment at the walk's start: of the given one);
-  // seg_start: [B H, NS, dv, dk], the states that the others start from
+  // seg_start: [B H, NS, dv, dk], the states that segments start from behind the join
   int NS, L;
+  int seg0, segs;                   // the segments of a launch of a walk
   float *seg_map, *seg_add, *seg_start;
-  int probe;                        // 1: the walk back that forms seg_add
+  int open;                         // 1: the launch before the join: ends go to seg_add, and a segment
+                                    // that does not start the walk starts from zero
   DeltaGates* gates;                // [B H, NC]
   char* matrices;                   // [B H, NC, delta_matrix_bytes(2 or 3)]
   float* states;                    // [B H, NC, dv, dk] before each chunk, or null
@@ -73,8 +75,9 @@ hipError_t launch_delta_adjoint(const DeltaParams& p, hipStream_t s);  // bf16 r
 hipError_t launch_delta_adjoint_f32(const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_grads(bool bf16, const DeltaParams& p, hipStream_t s);
 
-// seg_map and seg_add of a walk forward.
-hipError_t launch_delta_probe(bool bf16, const DeltaParams& p, hipStream_t s);
+// seg_map and seg_add of a walk forward; for bf16 rows the first segment whole.
+hipError_t launch_delta_open(const DeltaParams& p, hipStream_t s);  // bf16 rows
+hipError_t launch_delta_open_f32(const DeltaParams& p, hipStream_t s);
 // seg_start from seg_map, seg_add and the state at one end; `back`: from the last segment to the first.
 hipError_t launch_delta_join(bool back, const DeltaParams& p, hipStream_t s);
 

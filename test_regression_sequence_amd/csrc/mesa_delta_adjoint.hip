@@ -41,6 +41,7 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
   const bool chain = __builtin_amdgcn_readfirstlane(threadIdx.x) < 256;
   Part part;
   if (!part_of(p, blockIdx.x, part)) return;
+  const bool keep = !p.open || part.seg == p.NS - 1;  // whole: N and E go to memory
   const int bh = part.bh, b = part.b, h = part.h, len = part.len, first = part.first, last = part.last;
   const int col0 = part.col0, cols = part.cols;
   const bool mine = 16 * wave < cols;
@@ -53,11 +54,11 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
   if (chain) {
     const int col = col0 + 16 * wave + r;
     f32x4 m[MT];
-    const float* const from = walk_from(p, part, p.d_sfinal, p.NS - 1, col);
+    const float* const from = walk_from(p, part, p.d_sfinal, p.NS - 1);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       m[i] = zero;
-      if (mine && from) m[i] = *reinterpret_cast<const f32x4*>(from + 16 * i + 4 * g);
+      if (mine && from) m[i] = *reinterpret_cast<const f32x4*>(from + col * DK + 16 * i + 4 * g);
     }
     const TileRows<DK> rows(lane);
     Planes<3> mp[KS];
@@ -105,7 +106,7 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
           mma_tiles<2>(f[s & 1], mp[s], x);
           fence<true>();
         }
-        if (!p.probe) {
+        if (keep) {
           const Window to = window_at(p.dstates + unit * p.dv * DK);
 #pragma unroll
           for (int i = 0; i < MT; ++i) window_store(to, (col * DK + 4 * g) * 4, 64 * i, m[i]);
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
           const Window to = window_at(p.e + unit * 64 * p.dv);
 #pragma unroll
           for (int i = 2 * s; i < 2 * s + 2; ++i) {
-            if (!p.probe)
+            if (keep)
 #pragma unroll
               for (int e = 0; e < 4; ++e) window_store(to, (4 * g * p.dv + col) * 4, (16 * i + e) * p.dv * 4, x[i][e]);
             y[i] = -(cc[i] * cb[i]) * x[i];
@@ -179,10 +180,10 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
       }
       __syncthreads();
     }
-    float* const to = walk_to(p, part, p.ds0, 0, col);
+    float* const to = walk_to(p, part, p.ds0, 0);
     if (mine && to) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i + 4 * g) = m[i];
+      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + col * DK + 16 * i + 4 * g) = m[i];
     }
     return;
   }

@@ -26,6 +26,7 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   Part part;
   if (!part_of(p, blockIdx.x, part)) return;
+  const bool keep = !p.open || part.seg == p.NS - 1;  // whole: N and E go to memory
   const int bh = part.bh, b = part.b, h = part.h, hk = h / (p.H / p.Hk), len = part.len, first = part.first, last = part.last;
   const int col0 = part.col0, cols = part.cols;
   const int col = col0 + 16 * wave + r;
@@ -33,11 +34,11 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p
   const int64_t q0 = b * p.q.b + hk * p.q.h, k0 = b * p.k.b + hk * p.k.h, o0 = b * p.d_o.b + h * p.d_o.h + col0;
 
   f32x4 m[MT];
-  const float* const from = walk_from(p, part, p.d_sfinal, p.NS - 1, col);
+  const float* const from = walk_from(p, part, p.d_sfinal, p.NS - 1);
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     m[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (mine && from) m[i] = *reinterpret_cast<const f32x4*>(from + 16 * i + 4 * g);
+    if (mine && from) m[i] = *reinterpret_cast<const f32x4*>(from + col * DK + 16 * i + 4 * g);
   }
   RowLoads<DK, false, 256> kl, ql;
   RowLoads<64, false, 256> ol;
@@ -76,10 +77,10 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p
 
     if (mine) {
       f32x4 x[4];  // tail K N
-      if (!p.probe) {
-        float* to = p.dstates + unit * p.dv * DK + (int64_t)col * DK + 4 * g;
+      if (keep) {
+        const Window to = window_at(p.dstates + unit * p.dv * DK);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i) = m[i];
+        for (int i = 0; i < MT; ++i) window_store(to, (col * DK + 4 * g) * 4, 64 * i, m[i]);
       }
       Planes<3> mp[KS];
 #pragma unroll
@@ -108,12 +109,12 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p
         for (int s = i / 2; s < 2; ++s) acc = mma<2>(block_of<3>(lds + L::kT, upper_block(i, s), lane), px[s], acc);
         x[i] = acc;
       }
-      if (!p.probe) {
-        float* e_to = p.e + (unit * 64 + 4 * g) * p.dv + col;
+      if (keep) {
+        const Window to = window_at(p.e + unit * 64 * p.dv);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) e_to[(int64_t)(16 * i + e) * p.dv] = x[i][e];
+          for (int e = 0; e < 4; ++e) window_store(to, (4 * g * p.dv + col) * 4, (16 * i + e) * p.dv * 4, x[i][e]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -139,10 +140,10 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p
     __syncthreads();
   }
 
-  float* const to = walk_to(p, part, p.ds0, 0, col);
+  float* const to = walk_to(p, part, p.ds0, 0);
   if (mine && to) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i + 4 * g) = m[i];
+    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + col * DK + 16 * i + 4 * g) = m[i];
   }
 }
 

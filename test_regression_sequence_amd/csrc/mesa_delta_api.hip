@@ -96,8 +96,8 @@ mesa_status check_delta(const mesa_delta_desc* d) {
 
 // In how many segments a walk goes.  A walk of one workgroup a head and 64 columns takes
 // its chunks one after the other; with fewer of those than the 256 CUs, segments of it run
-// side by side, after a walk that finds what each makes of unit rows and of zero (128 of
-// dv + dk columns a workgroup) and a launch that joins them.  In times of one chunk (about
+// side by side, after a launch that finds what each makes of unit rows and of zero (128 of
+// dv + dk columns a workgroup; for bf16 rows with the first segment) and one that joins them.  In times of one chunk (about
 // 2.7 us, in fp32 twice that), the two launches take about 3 and half a chunk a segment.
 // Measured, one sequence, in segments and in one walk: 1024 tokens and 4 heads of 64,
 // forward 38 and 49 us, gradients 86 and 113, in fp32 49 and 101, 109 and 210; 4 heads of
@@ -105,14 +105,16 @@ mesa_status check_delta(const mesa_delta_desc* d) {
 int segments_of(const mesa_delta_desc* d) {
   const int64_t heads = (int64_t)d->B * d->H, values = (d->dv + 63) / 64, both = (d->dv + d->dk + 127) / 128;
   const int chunks = chunks_of(d);
-  const double more = d->dtype == MESA_BF16 ? 1.0 : 0.5;
+  const bool bf16 = d->dtype == MESA_BF16;
+  const double more = bf16 ? 1.0 : 0.5;
   const auto rounds = [](int64_t blocks) { return (double)((blocks + 255) / 256); };
   int best = 1;
   double least = 0.9 * chunks * rounds(heads * values);
   for (int n = 2; n <= 32 && n * 2 <= chunks; ++n) {
     const int per = (chunks + n - 1) / n;
     if ((chunks + per - 1) / per != n) continue;  // (no segment stays empty)
-    const double time = per * (rounds(heads * (n - 1) * both) + rounds(heads * n * values)) + more * (3 + 0.5 * n);
+    const int64_t opening = bf16 ? values + (n - 2) * both : (n - 1) * both, rest = (bf16 ? n - 1 : n) * values;
+    const double time = per * (rounds(heads * opening) + rounds(heads * rest)) + more * (3 + 0.5 * n);
     if (time < least) {
       best = n;
       least = time;
@@ -175,29 +177,47 @@ DeltaParams delta_params(const mesa_delta_desc* d, const void* q, const void* k,
   return p;
 }
 
-// A walk forward, in segments where there are few heads.
-hipError_t scan(bool bf16, const DeltaParams& p, hipStream_t s) {
+// The launches of a walk in segments: `first` for what the others start from, and, behind the
+// join, segments seg0 .. seg0 + segs - 1.  With one segment the second alone.
+template <typename First, typename Walk>
+hipError_t in_segments(const DeltaParams& p, bool back, int seg0, int segs, hipStream_t s, First&& first, Walk&& walk) {
+  DeltaParams x = p;
+  x.seg0 = 0;
+  x.segs = 1;
   if (p.NS > 1) {
-    hipError_t e = launch_delta_probe(bf16, p, s);
-    if (e == hipSuccess) e = launch_delta_join(false, p, s);
+    x.open = 1;
+    hipError_t e = first(x);
+    if (e == hipSuccess) e = launch_delta_join(back, p, s);
     if (e != hipSuccess) return e;
+    x.open = 0;
+    x.seg0 = seg0;
+    x.segs = segs;
   }
-  return bf16 ? launch_delta_scan(p, s) : launch_delta_scan_f32(p, s);
+  return walk(x);
 }
 
-// A walk back; the segments' maps are those of the walk forward.
+// A walk forward.  For bf16 rows the first segment runs beside the launch that opens the others.
+hipError_t scan(bool bf16, const DeltaParams& p, hipStream_t s) {
+  return in_segments(
+      p, false, bf16 ? 1 : 0, bf16 ? p.NS - 1 : p.NS, s,
+      [&](const DeltaParams& x) { return bf16 ? launch_delta_open(x, s) : launch_delta_open_f32(x, s); },
+      [&](const DeltaParams& x) { return bf16 ? launch_delta_scan(x, s) : launch_delta_scan_f32(x, s); });
+}
+
+// A walk back; the segments' maps are those of the walk forward, and the last segment, which
+// starts it, runs whole beside those that start from zero.
 hipError_t adjoint(bool bf16, const DeltaParams& p, hipStream_t s) {
   const auto walk = [&](const DeltaParams& x) {
     return bf16 ? launch_delta_adjoint(x, s) : launch_delta_adjoint_f32(x, s);
   };
-  if (p.NS > 1) {
-    DeltaParams probe = p;
-    probe.probe = 1;
-    hipError_t e = walk(probe);
-    if (e == hipSuccess) e = launch_delta_join(true, p, s);
-    if (e != hipSuccess) return e;
-  }
-  return walk(p);
+  return in_segments(
+      p, true, 0, p.NS - 1, s,
+      [&](DeltaParams x) {
+        x.seg0 = 1;
+        x.segs = p.NS - 1;
+        return walk(x);
+      },
+      walk);
 }
 
 mesa_status launched(hipError_t e) { return e == hipSuccess ? MESA_OK : MESA_ERR_HIP; }

@@ -1,9 +1,9 @@
 // Gated delta rule, forward: what the segments of a split walk make of states.
 //
 // Over a segment the state's rows go S -> S P + Q.  The walk of mesa_delta_scan.hip,
-// without outputs, over Q's columns (from the given state in the first segment, from
-// zero in the others) and, behind the first segment, over P's: the dk unit columns,
-// whose values are zeros.  The last segment, which nothing follows, has neither.
+// without outputs, over Q's columns (from zero, in the first segment from the given
+// state) and, behind the first segment, over P's: the dk unit columns, whose values are
+// zeros.  The last segment, which nothing follows, has neither.
 //
 // Nothing is formed beside the chain of states, so all eight waves are chains, 16
 // columns each, two on a SIMD to fill one another's waits: 128 columns a workgroup, and
@@ -11,11 +11,15 @@
 // while the chunk before is in the works; so do values of two bytes, those of four, whose
 // planes would not fit beside two chunks of keys, go to their lanes.
 //
-// B=1 H=16 T=32768 d=128, 7 of 8 segments of 64 chunks: 305 us, 4.8 us a chunk and 128
-// columns, of which a SIMD's matrix unit works 38 % and its vector unit 41 %, hardly at the
-// same time (four chains of 16 columns as in the walk itself: 2.7 us for 64 columns).  The
-// two waves of a SIMD half a chunk apart, so that conversions of one meet products of the
-// other, took 333 us: the second barrier a chunk costs more.
+// B=1 H=16 T=32768 d=128: 4.8 us a chunk and 128 columns, of which a SIMD's matrix unit
+// works 38 % and its vector unit 41 %, hardly at the same time (four chains of 16 columns as
+// in the walk itself: 2.7 us for 64 columns).  The two waves of a SIMD half a chunk apart,
+// so that conversions of one meet products of the other, took a tenth longer: the second
+// barrier a chunk costs more.  With bf16 rows the walk's first segment, which needs no
+// start, runs in the same launch: 9 segments in place of 8 on 256 CUs, 536 -> 493 us for
+// both launches of the walk.
+#pragma once
+
 #include "mesa_delta_tile.h"
 
 namespace mesa {
@@ -29,17 +33,22 @@ struct ProbeLds {
                        kBuffer = kV + (BF16 ? 64 * 256 : 0);
 };
 
-int slices_of(const DeltaParams& p) { return (p.dv + p.dk + 127) / 128; }
+inline int probe_slices(const DeltaParams& p) { return (p.dv + p.dk + 127) / 128; }
+// Workgroups of the segments from `from` to the one before the last.
+inline uint32_t probe_blocks(const DeltaParams& p, int from) {
+  return (uint32_t)((p.B * p.H + 7) / 8 * 8 * probe_slices(p) * (p.NS - 1 - from));
+}
 
+// Workgroup `id` of them.
 template <int DK, bool BF16>
-__global__ __launch_bounds__(512, 2) void delta_probe_kernel(DeltaParams p, int slices) {
+__device__ __forceinline__ void probe_segment(const DeltaParams& p, uint32_t id, int from, char* all) {
   using L = ProbeLds<DK, BF16>;
   constexpr int NP = L::NP, MT = DK / 16, KS = DK / 32;
-  __shared__ __attribute__((aligned(16))) char lds[2][L::kBuffer];
+  char (*const lds)[L::kBuffer] = reinterpret_cast<char (*)[L::kBuffer]>(all);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   // one head's workgroups on one XCD, whose L2 they share
-  const int per = slices * (p.NS - 1), n = blockIdx.x >> 3, rest = n % per;
-  const int bh = n / per * 8 + (blockIdx.x & 7), seg = rest / slices, slice = rest % slices;
+  const int slices = (p.dv + DK + 127) / 128, per = slices * (p.NS - 1 - from), n = id >> 3, rest = n % per;
+  const int bh = n / per * 8 + (id & 7), seg = from + rest / slices, slice = rest % slices;
   if (bh >= p.B * p.H || (seg == 0 && 128 * slice >= p.dv)) return;
   const int b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk), len = delta_length(p, b);
   const int first = seg * p.L, last = max(min((len + 63) / 64, first + p.L), first);
@@ -180,19 +189,6 @@ __global__ __launch_bounds__(512, 2) void delta_probe_kernel(DeltaParams p, int 
   }
 }
 
-template <int DK>
-hipError_t launch(bool bf16, const DeltaParams& p, hipStream_t s) {
-  const int slices = slices_of(p);
-  const uint32_t blocks = (uint32_t)((p.B * p.H + 7) / 8 * 8 * slices * (p.NS - 1));
-  if (bf16) delta_probe_kernel<DK, true><<<blocks, 512, 0, s>>>(p, slices);
-  else delta_probe_kernel<DK, false><<<blocks, 512, 0, s>>>(p, slices);
-  return hipGetLastError();
-}
-
 }  // namespace
-
-hipError_t launch_delta_probe(bool bf16, const DeltaParams& p, hipStream_t s) {
-  return p.dk == 128 ? launch<128>(bf16, p, s) : p.dk == 64 ? launch<64>(bf16, p, s) : launch<32>(bf16, p, s);
-}
 
 }  // namespace mesa

@@ -18,9 +18,11 @@
 //
 // A chunk takes 2.8 us where few workgroups run, of which the chain's 132 products are 0.9
 // and their operands' ways through conversions and LDS the rest, and 3.6 us on all CUs (B=1
-// H=16 T=32768 d=128 in 8 segments: 232 us).  With states and W kept memory bounds it: at
+// H=16 T=32768 d=128, 8 segments of 57 chunks side by side: 216 us).  With states and W kept memory bounds it: at
 // B=8 H=16 T=4096 d=128 370 us for 1.6 GB, 4.3 TB/s where a large copy reaches 4.9.
-#include "mesa_delta_tile.h"
+#include <algorithm>
+
+#include "mesa_delta_probe.h"
 
 namespace mesa {
 
@@ -36,14 +38,13 @@ struct ScanLds {
 };
 
 template <int DK, bool OUT>
-__global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
+__device__ __forceinline__ void walk_segment(const DeltaParams& p, uint32_t id, char* lds) {
   using L = ScanLds<DK>;
   constexpr int MT = DK / 16, KS = DK / 32;
-  __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
   const int tid = threadIdx.x & 255, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   const bool chain = __builtin_amdgcn_readfirstlane(threadIdx.x) < 256;
   Part part;
-  if (!part_of(p, blockIdx.x, part)) return;
+  if (!part_of(p, id, part)) return;
   const int bh = part.bh, b = part.b, h = part.h, len = part.len, first = part.first, last = part.last;
   const int col0 = part.col0, cols = part.cols;
   const bool mine = 16 * wave < cols;
@@ -54,11 +55,11 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
   if (chain) {
     const int col = col0 + 16 * wave + r;  // this lane's column of the state
     f32x4 m[MT];  // rows 16 i + 4 g + e of M
-    const float* const from = walk_from(p, part, p.s0, 0, col);
+    const float* const from = walk_from(p, part, p.s0, 0);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       m[i] = zero;
-      if (mine && from) m[i] = *reinterpret_cast<const f32x4*>(from + 16 * i + 4 * g);
+      if (mine && from) m[i] = *reinterpret_cast<const f32x4*>(from + col * DK + 16 * i + 4 * g);
     }
     const TileRows<DK> rows(lane);
     const TileColumns<DK> columns(lane);
@@ -199,10 +200,10 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
       }
       __syncthreads();
     }
-    float* const to = walk_to(p, part, p.s_final, p.NS - 1, col);
+    float* const to = walk_to(p, part, p.s_final, p.NS - 1);
     if (mine && to) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i + 4 * g) = m[i];
+      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + col * DK + 16 * i + 4 * g) = m[i];
     }
     return;
   }
@@ -313,6 +314,20 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
   }
 }
 
+template <int DK, bool OUT>
+__global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
+  __shared__ __attribute__((aligned(16))) char lds[ScanLds<DK>::kBytes];
+  walk_segment<DK, OUT>(p, blockIdx.x, lds);
+}
+
+// The first segment whole, and what the others but the last make of states, side by side.
+template <int DK, bool OUT>
+__global__ __launch_bounds__(512, 2) void delta_open_kernel(DeltaParams p, uint32_t probes) {
+  __shared__ __attribute__((aligned(16))) char lds[std::max(ScanLds<DK>::kBytes, 2 * ProbeLds<DK, true>::kBuffer)];
+  if (blockIdx.x < probes) probe_segment<DK, true>(p, blockIdx.x, 1, lds);
+  else walk_segment<DK, OUT>(p, blockIdx.x - probes, lds);
+}
+
 template <int DK>
 hipError_t launch(const DeltaParams& p, hipStream_t s) {
   if (p.o.at) delta_scan_kernel<DK, true><<<walk_blocks(p), 512, 0, s>>>(p);
@@ -320,10 +335,22 @@ hipError_t launch(const DeltaParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int DK>
+hipError_t open(const DeltaParams& p, hipStream_t s) {
+  const uint32_t probes = probe_blocks(p, 1);
+  if (p.o.at) delta_open_kernel<DK, true><<<probes + walk_blocks(p), 512, 0, s>>>(p, probes);
+  else delta_open_kernel<DK, false><<<probes + walk_blocks(p), 512, 0, s>>>(p, probes);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_delta_scan(const DeltaParams& p, hipStream_t s) {
   return p.dk == 128 ? launch<128>(p, s) : p.dk == 64 ? launch<64>(p, s) : launch<32>(p, s);
+}
+
+hipError_t launch_delta_open(const DeltaParams& p, hipStream_t s) {
+  return p.dk == 128 ? open<128>(p, s) : p.dk == 64 ? open<64>(p, s) : open<32>(p, s);
 }
 
 }  // namespace mesa

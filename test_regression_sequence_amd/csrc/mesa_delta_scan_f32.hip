@@ -6,7 +6,7 @@
 // each forms its columns of o too.  A chunk takes 5.7 us at dk = 64: 216 products (1.5 us) and,
 // between its barriers, the conversions of the next chunk's rows, which nothing hides
 // (B=5 H=6 T=777 dk=64 dv=96: 73 us in one walk, in 4 segments 25 us and 26 to form them).
-#include "mesa_delta_tile.h"
+#include "mesa_delta_probe.h"
 
 namespace mesa {
 
@@ -33,15 +33,15 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
   const int col = col0 + 16 * wave + r;                 // this lane's column of the state
   const bool mine = 16 * wave < cols;
   const int64_t q0 = b * p.q.b + hk * p.q.h, k0 = b * p.k.b + hk * p.k.h, v0 = b * p.v.b + h * p.v.h + col0,
-                o0 = b * p.o.b + h * p.o.h + col0 + 16 * wave + 4 * g;
+                o0 = b * p.o.b + h * p.o.h + col0 + 16 * wave;
 
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   f32x4 m[MT];  // rows 16 i + 4 g + e of M, column `col`
-  const float* const from = walk_from(p, part, p.s0, 0, col);
+  const float* const from = walk_from(p, part, p.s0, 0);
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     m[i] = zero;
-    if (mine && from) m[i] = *reinterpret_cast<const f32x4*>(from + 16 * i + 4 * g);
+    if (mine && from) m[i] = *reinterpret_cast<const f32x4*>(from + col * DK + 16 * i + 4 * g);
   }
   RowLoads<DK, false, 256> kl, ql;
   RowLoads<64, false, 256> vl;
@@ -77,9 +77,9 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
 
     if (mine) {
       if (p.states) {
-        float* to = p.states + unit * p.dv * DK + (int64_t)col * DK + 4 * g;
+        const Window to = window_at(p.states + unit * p.dv * DK);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i) = m[i];
+        for (int i = 0; i < MT; ++i) window_store(to, (col * DK + 4 * g) * 4, 64 * i, m[i]);
       }
       Planes<3> mp[KS], u[2], ut[2], px[2];
       BlockPair<3> t;
@@ -101,9 +101,9 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[(s + 1) & 1][i] = rows_of<DK, NP>(lds + L::kQ, L::kPlane, 16 * i, 0, lane);
         }
-          if (s + 1 < KS) mp[s + 1] = split8<3>(m[2 * s + 2], m[2 * s + 3]);
+        if (s + 1 < KS) mp[s + 1] = split8<3>(m[2 * s + 2], m[2 * s + 3]);
         mma_tiles<2>(f[s & 1], mp[s], x);
-        }
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         x[i] = y[i] - *reinterpret_cast<const f32x4*>(&gates.c[16 * i + 4 * g]) * x[i];
@@ -119,8 +119,8 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
           } else {
             t = pair_of<true, 3>(lds + L::kT, 0, lane);
           }
-              mma_tiles_t<2>(mp[s], f[(KS + s) & 1], o);
-            }
+          mma_tiles_t<2>(mp[s], f[(KS + s) & 1], o);
+        }
       } else {
         t = pair_of<true, 3>(lds + L::kT, 0, lane);
       }
@@ -136,11 +136,11 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
       };
       keys(0, kt[0]);
       if (p.w) {
-        float* to = p.w + (unit * 64 + 4 * g) * p.dv + col;
+        const Window to = window_at(p.w + unit * 64 * p.dv);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) to[(int64_t)(16 * i + e) * p.dv] = x[i][e];
+          for (int e = 0; e < 4; ++e) window_store(to, (4 * g * p.dv + col) * 4, (16 * i + e) * p.dv * 4, x[i][e]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
       for (int n = 0; n < NG; ++n) {  // M += K^T U
         if (n + 1 < NG) keys(n + 1, kt[(n + 1) & 1]);
         else if constexpr (OUT) a = pair_of<true, NA>(lds + L::kA, 0, lane);
-          if (OUT && n == 0) {
+        if (OUT && n == 0) {
 #pragma unroll
           for (int s = 0; s < 2; ++s) u[s] = split8<3>(x[2 * s], x[2 * s + 1]);
 #pragma unroll
@@ -170,7 +170,7 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
 #pragma unroll
               for (int i = 0; i < G; ++i)
                 m[n * G % MT + i] = mfma_bf16(kt[n & 1][i].p[q], ut[n * G / MT].p[sum - q], m[n * G % MT + i]);
-        }
+      }
       if constexpr (OUT) {
         mma_triangle<2, true, true, false>(lds + L::kA, a, u, o, lane);
       }
@@ -179,29 +179,37 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
     if (c + 1 < last) store();  // (ahead of o's stores, which then have the next chunk's time)
     if (OUT && mine) {
       const int live = len - 64 * c;
+      const Window to = window_at(static_cast<float*>(p.o.at) + o0 + 64 * (int64_t)c * p.o.t);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = 16 * i + r;
-        if (at < live) {
-          const int64_t to = o0 + (64 * (int64_t)c + at) * p.o.t;
-          store_out4<float>(p.o.at, to, o[i]);
-        }
-      }
+      for (int i = 0; i < 4; ++i)
+        window_store(to, 16 * i + r < live ? ((16 * i + r) * (uint32_t)p.o.t + 4 * g) * 4 : kNowhere, 0, o[i]);
     }
     __syncthreads();
   }
 
-  float* const to = walk_to(p, part, p.s_final, p.NS - 1, col);
+  float* const to = walk_to(p, part, p.s_final, p.NS - 1);
   if (mine && to) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + 16 * i + 4 * g) = m[i];
+    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(to + col * DK + 16 * i + 4 * g) = m[i];
   }
   if (OUT && mine) {  // behind the sequence
     const int end = (int)min((int64_t)p.T, (int64_t)64 * (first + p.L));
     for (int64_t t = max(len, 64 * first) + r; t < end; t += 16) {
-      store_out4<float>(p.o.at, o0 + t * p.o.t, zero);
+      store_out4<float>(p.o.at, o0 + t * p.o.t + 4 * g, zero);
     }
   }
+}
+
+template <int DK>
+__global__ __launch_bounds__(512, 2) void delta_open_f32_kernel(DeltaParams p) {
+  __shared__ __attribute__((aligned(16))) char lds[2 * ProbeLds<DK, false>::kBuffer];
+  probe_segment<DK, false>(p, blockIdx.x, 0, lds);
+}
+
+template <int DK>
+hipError_t open(const DeltaParams& p, hipStream_t s) {
+  delta_open_f32_kernel<DK><<<probe_blocks(p, 0), 512, 0, s>>>(p);
+  return hipGetLastError();
 }
 
 template <int DK>
@@ -215,6 +223,10 @@ hipError_t launch(const DeltaParams& p, hipStream_t s) {
 
 hipError_t launch_delta_scan_f32(const DeltaParams& p, hipStream_t s) {
   return p.dk == 128 ? launch<128>(p, s) : p.dk == 64 ? launch<64>(p, s) : launch<32>(p, s);
+}
+
+hipError_t launch_delta_open_f32(const DeltaParams& p, hipStream_t s) {
+  return p.dk == 128 ? open<128>(p, s) : p.dk == 64 ? open<64>(p, s) : open<32>(p, s);
 }
 
 }  // namespace mesa

@@ -461,9 +461,7 @@ __device__ __forceinline__ float* gate_at(const DeltaGate& x, int b, int h, int6
 // exp2 of a difference of two logarithms that are kept in 64 bits.
 __device__ __forceinline__ float decay(double a, double b) { return __builtin_amdgcn_exp2f((float)(a - b)); }
 
-// One workgroup's part of a walk: 64 columns of one head's state over one segment's
-// chunks.  The walk back that finds what segments make of zero (`probe`) has none for the
-// first segment, which nothing follows, and takes the last from the given gradient.
+// One workgroup's part of a walk: 64 columns of one head's state over one segment's chunks.
 struct Part {
   int bh, b, h, seg, col0, cols, len, first, last;
 };
@@ -471,12 +469,12 @@ struct Part {
 // The workgroups of one head go to one XCD (workgroups are handed to the 8 XCDs in
 // turn), whose L2 they share.  False: no part.
 __device__ __forceinline__ bool part_of(const DeltaParams& p, uint32_t id, Part& x) {
-  const int slices = (p.dv + 63) / 64, per = slices * (p.probe ? p.NS - 1 : p.NS);
+  const int slices = (p.dv + 63) / 64, per = slices * p.segs;
   const uint32_t xcd = id & 7, n = id >> 3;
   x.bh = (int)(n / per) * 8 + (int)xcd;
   if (x.bh >= p.B * p.H) return false;
   const int rest = (int)(n % per);
-  x.seg = rest / slices + (p.probe ? 1 : 0);
+  x.seg = rest / slices + p.seg0;
   x.b = x.bh / p.H;
   x.h = x.bh % p.H;
   x.col0 = 64 * (rest % slices);
@@ -487,19 +485,21 @@ __device__ __forceinline__ bool part_of(const DeltaParams& p, uint32_t id, Part&
   return true;
 }
 inline uint32_t walk_blocks(const DeltaParams& p) {
-  return (uint32_t)((p.B * p.H + 7) / 8 * 8 * ((p.dv + 63) / 64) * (p.probe ? p.NS - 1 : p.NS));
+  return (uint32_t)((p.B * p.H + 7) / 8 * 8 * ((p.dv + 63) / 64) * p.segs);
 }
 
-// Where a walk's state comes from and goes to: [.., dk] from column `col` on (null: zeros, nowhere).
-__device__ __forceinline__ const float* walk_from(const DeltaParams& p, const Part& x, const float* given, int edge, int col) {
-  if (p.probe && x.seg != edge) return nullptr;
-  if (x.seg != edge) return p.seg_start + (((int64_t)x.bh * p.NS + x.seg) * p.dv + col) * p.dk;
-  return given ? given + ((int64_t)x.bh * p.dv + col) * p.dk : nullptr;
+// Where a walk's state [dv, dk] comes from and goes to (null: zeros, nowhere).  `edge`: the
+// segment that starts the walk, or ends it.  Behind the join none starts from `given`, which
+// may lie under what another one of the launch ends with.
+__device__ __forceinline__ const float* walk_from(const DeltaParams& p, const Part& x, const float* given, int edge) {
+  const int64_t size = (int64_t)p.dv * p.dk;
+  if (p.NS > 1 && !p.open) return p.seg_start + ((int64_t)x.bh * p.NS + x.seg) * size;
+  return given && x.seg == edge ? given + x.bh * size : nullptr;
 }
-__device__ __forceinline__ float* walk_to(const DeltaParams& p, const Part& x, float* wanted, int edge, int col) {
-  const int64_t at = (int64_t)x.bh * p.NS + x.seg;
-  if (p.probe) return p.seg_add + (at * p.dv + col) * p.dk;
-  return wanted && x.seg == edge ? wanted + ((int64_t)x.bh * p.dv + col) * p.dk : nullptr;
+__device__ __forceinline__ float* walk_to(const DeltaParams& p, const Part& x, float* wanted, int edge) {
+  const int64_t size = (int64_t)p.dv * p.dk;
+  if (p.open) return p.seg_add + ((int64_t)x.bh * p.NS + x.seg) * size;
+  return wanted && x.seg == edge ? wanted + x.bh * size : nullptr;
 }
 
 template <typename T>

@@ -219,3 +219,19 @@ def test_segments_without_states(dtype):
     assert segmented(t)
     check_forward(mesa.delta_fwd(*args(t)), a, dt, walks=2)
     check_backward(mesa.delta_bwd(*args(t), t["d_o"]), a, dt, walks=2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_segments_in_place(dtype):
+    """s_final over s0 and ds0 over d_sfinal where most segments have no chunk and so end at once, beside
+    the one that starts from what they overwrite."""
+    dt = DTYPES[dtype]
+    B = 32
+    a = draw(B, 1, 1, 1100, 64, 64, dt, gates="slow", lengths=[1 + 7 * b for b in range(B)])
+    t = to_dev(a, dt)
+    assert segmented(t)
+    s, ds = t["s0"].clone(), t["d_sfinal"].clone()
+    r = mesa.delta_fwd(*args(t), s0=s, lengths=t["lengths"], return_state=True, out={"s_final": s})
+    check_forward(r, a, dt, walks=2)
+    g = mesa.delta_bwd(*args(t), t["d_o"], s0=t["s0"], lengths=t["lengths"], d_sfinal=ds, state_grads=True, out={"ds0": ds})
+    check_backward(g, a, dt, walks=2)
