@@ -4,8 +4,8 @@
 // the segment makes of unit rows and of zero), and its gradients back N -> N P^T + Q;
 // the segment at the walk's start has the given state in its Q already.  From one
 // segment to the next that is a 16 x dk by dk x dk product for each 16 rows,
-// in fp32 matrix instructions: a workgroup has 16 rows in LDS, its waves the tiles of
-// the result's columns.  9 segments: 23 us at H=16 dk=128, 8: 8 us at 32 heads of 64; maps
+// in fp32 matrix instructions: a workgroup has 16 rows in LDS, each of its waves a
+// tile of the result's columns.  9 segments: 18 us at H=16 dk=128, 8: 7 us at 32 heads of 64; maps
 // loaded one or three steps ahead change nothing.
 #include "mesa_delta_tile.h"
 
@@ -14,14 +14,14 @@ namespace mesa {
 namespace {
 
 template <int DK, bool BACK>
-__global__ __launch_bounds__(256) void delta_join_kernel(DeltaParams p) {
-  constexpr int NT = DK / 16, PER = (NT + 3) / 4;
+__global__ __launch_bounds__(4 * DK) void delta_join_kernel(DeltaParams p) {
+  constexpr int NT = DK / 16, kThreads = 4 * DK;
   __shared__ __attribute__((aligned(16))) float rows[2][16][DK + 4];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int groups = p.dv / 16, bh = blockIdx.x / groups, row0 = blockIdx.x % groups * 16;
   const int64_t edge = (int64_t)bh * p.NS + (BACK ? p.NS - 1 : 0), second = BACK ? edge - 1 : edge + 1;
   const float* given = BACK ? p.d_sfinal : p.s0;
-  for (int i = tid; i < 16 * DK; i += 256) {
+  for (int i = tid; i < 16 * DK; i += kThreads) {
     p.seg_start[(edge * p.dv + row0) * DK + i] = given ? given[((int64_t)bh * p.dv + row0) * DK + i] : 0.f;
     p.seg_start[(second * p.dv + row0) * DK + i] = rows[1][i / DK][i % DK] = p.seg_add[(edge * p.dv + row0) * DK + i];
   }
@@ -29,40 +29,31 @@ __global__ __launch_bounds__(256) void delta_join_kernel(DeltaParams p) {
     const int seg = BACK ? p.NS - 1 - n : n, next = BACK ? seg - 1 : seg + 1;
     const int64_t at = (int64_t)bh * p.NS + seg, to = (int64_t)bh * p.NS + next;
     const float *map = p.seg_map + at * DK * DK, *add = p.seg_add + (at * p.dv + row0) * DK;
-    f32x4 b[PER][NT], acc[PER];
+    const int col = 16 * wave + r;
+    f32x4 b[NT], acc;
 #pragma unroll
-    for (int t = 0; t < PER; ++t) {
-      const int col = 16 * (wave + 4 * t) + r;
-      if (wave + 4 * t >= NT) continue;
+    for (int k = 0; k < NT; ++k) {
+      if constexpr (BACK) {
+        b[k] = *reinterpret_cast<const f32x4*>(map + (int64_t)col * DK + 16 * k + 4 * g);
+      } else {
 #pragma unroll
-      for (int k = 0; k < NT; ++k) {
-        if constexpr (BACK) {
-          b[t][k] = *reinterpret_cast<const f32x4*>(map + (int64_t)col * DK + 16 * k + 4 * g);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) b[t][k][e] = map[(int64_t)(16 * k + 4 * g + e) * DK + col];
-        }
+        for (int e = 0; e < 4; ++e) b[k][e] = map[(int64_t)(16 * k + 4 * g + e) * DK + col];
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[t][e] = add[(int64_t)(4 * g + e) * DK + col];
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = add[(int64_t)(4 * g + e) * DK + col];
     __syncthreads();
     const auto& from = rows[n & 1];
 #pragma unroll
-    for (int t = 0; t < PER; ++t) {
-      if (wave + 4 * t >= NT) continue;
-      const int col = 16 * (wave + 4 * t) + r;
+    for (int k = 0; k < NT; ++k) {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(&from[r][16 * k + 4 * g]);
 #pragma unroll
-      for (int k = 0; k < NT; ++k) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(&from[r][16 * k + 4 * g]);
+      for (int e = 0; e < 4; ++e) acc = mfma_f32(a[e], b[k][e], acc);
+    }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[t] = mfma_f32(a[e], b[t][k][e], acc[t]);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        rows[~n & 1][4 * g + e][col] = acc[t][e];
-        p.seg_start[(to * p.dv + row0 + 4 * g + e) * DK + col] = acc[t][e];
-      }
+    for (int e = 0; e < 4; ++e) {
+      rows[~n & 1][4 * g + e][col] = acc[e];
+      p.seg_start[(to * p.dv + row0 + 4 * g + e) * DK + col] = acc[e];
     }
   }
 }
@@ -70,8 +61,8 @@ __global__ __launch_bounds__(256) void delta_join_kernel(DeltaParams p) {
 template <int DK>
 hipError_t launch(bool back, const DeltaParams& p, hipStream_t s) {
   const uint32_t blocks = (uint32_t)(p.B * p.H * (p.dv / 16));
-  if (back) delta_join_kernel<DK, true><<<blocks, 256, 0, s>>>(p);
-  else delta_join_kernel<DK, false><<<blocks, 256, 0, s>>>(p);
+  if (back) delta_join_kernel<DK, true><<<blocks, 4 * DK, 0, s>>>(p);
+  else delta_join_kernel<DK, false><<<blocks, 4 * DK, 0, s>>>(p);
   return hipGetLastError();
 }
 
