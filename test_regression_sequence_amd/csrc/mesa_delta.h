@@ -60,15 +60,15 @@ struct DeltaParams {
   DeltaGate dgamma, dbeta;
   const float* d_sfinal;
   float* ds0;
-  char* matrices_t;                 // [B H, NC, kDeltaMatrixBytes]: the backward pass's
+  char* matrices_t;                 // [B H, NC, kDeltaMatrixBytes]: the backward pass's, or null
   float* dstates;                   // [B H, NC, dv, dk]: the gradient behind each chunk
   float* e;                         // [B H, NC, 64, dv]: dv_t / beta_t
   float *dq_heads, *dk_heads;       // [B, H, T, dk] where heads share keys
 };
 
 // Each returns hipSuccess or the launch error.
-// Gates and inverses of every chunk; `transposed`: the backward pass's inverses.
-hipError_t launch_delta_chunks(bool bf16, bool transposed, const DeltaParams& p, hipStream_t s);
+// Every chunk's gates and the matrices of the walk forward, and where matrices_t is there of the walk back.
+hipError_t launch_delta_chunks(bool bf16, const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_scan(const DeltaParams& p, hipStream_t s);  // bf16 rows
 hipError_t launch_delta_scan_f32(const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_adjoint(const DeltaParams& p, hipStream_t s);  // bf16 rows

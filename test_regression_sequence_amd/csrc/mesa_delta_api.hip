@@ -259,7 +259,7 @@ mesa_status mesa_delta_fwd(const mesa_delta_desc* d, const void* q, const void* 
   carve(d, keep_states == 1, workspace, p);
   p.o = rows(d, o, d->o); p.s_final = s_final;
   const bool bf16 = d->dtype == MESA_BF16;
-  if (d->T > 0 && launch_delta_chunks(bf16, false, p, stream) != hipSuccess) return MESA_ERR_HIP;
+  if (d->T > 0 && launch_delta_chunks(bf16, p, stream) != hipSuccess) return MESA_ERR_HIP;
   if (d->T == 0) p.o.at = nullptr;
   return launched(scan(bf16, p, stream));
 }
@@ -306,14 +306,10 @@ mesa_status mesa_delta_bwd(const mesa_delta_desc* d, const mesa_delta_grad_rows*
   carve(d, true, workspace, p);
   const bool bf16 = d->dtype == MESA_BF16;
   if (d->T > 0) {
-    if (!states_in_workspace) {
-      DeltaParams states = p;  // (no outputs: queries are not needed)
-      states.q.at = nullptr;
-      if (launch_delta_chunks(bf16, false, states, stream) != hipSuccess ||
-          scan(bf16, states, stream) != hipSuccess)
-        return MESA_ERR_HIP;
-    }
-    if (launch_delta_chunks(bf16, true, p, stream) != hipSuccess) return MESA_ERR_HIP;
+    // (the walk forward here has no outputs)
+    if (!states_in_workspace &&
+        (launch_delta_chunks(bf16, p, stream) != hipSuccess || scan(bf16, p, stream) != hipSuccess))
+      return MESA_ERR_HIP;
   }
   p.d_o = rows(d, d_o, gr->d_o); p.dq = rows(d, dq, gr->dq); p.dk_ = rows(d, dk, gr->dk); p.dv_ = rows(d, dv, gr->dv);
   p.dgamma = gate(dgamma, gr->dgamma); p.dbeta = gate(dbeta, gr->dbeta); p.d_sfinal = d_sfinal; p.ds0 = ds0;

@@ -21,7 +21,7 @@
 // fp32's precision however strong the decay before it.
 //
 // Memory bounds it where there are many chunks: at B=8 H=16 T=4096 d=128 bf16 106 us for
-// 0.52 GB forward (4.9 TB/s, a large copy's rate) and 95 us for 0.44 GB back.  One round of
+// 0.52 GB forward (4.9 TB/s, a large copy's rate), 184 us for 0.95 GB for both.  One round of
 // chunks is a chain of 6.5 us (fp32 9): loads 1, logarithms 1, products and decays 2, the
 // diagonal blocks 1, the others and the way out 1.5.
 #include "mesa_delta_tile.h"
@@ -34,121 +34,123 @@ constexpr int kLd = 20;  // floats of a 16-wide row in LDS
 
 __host__ __device__ constexpr int tile_of(int i, int j) { return i * (i + 1) / 2 + j; }
 
-template <int DK, bool BF16, bool TRANSPOSED>
-__global__ __launch_bounds__(256, BF16 || DK == 32 ? 4 : 2) void delta_chunk_kernel(DeltaParams p) {
-  constexpr int NP = BF16 ? 1 : 3, ES = BF16 ? 2 : 4, NA = BF16 ? 2 : 3;
-  __shared__ __attribute__((aligned(16))) float low[10][16 * kLd];
-  __shared__ __attribute__((aligned(16))) float diag[4][16 * kLd];
-  __shared__ double sg[kDeltaChunk];
-  __shared__ float sbeta[kDeltaChunk];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-  const uint32_t unit = blockIdx.x;
-  const int c = unit % p.NC, bh = unit / p.NC, b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk);
-  const int live = min(delta_length(p, b) - c * kDeltaChunk, kDeltaChunk);
-  if (live <= 0) return;
+// BOTH: the walk back's matrices too, by workgroups behind the others.  (In place of a launch of
+// their own: 6 to 8 us less a training step of few chunks; B=8 H=16 T=4096 d=128 184 us and 197.
+// The body is a lambda: as a function of the parameters it spilled 92 registers back.)
+template <int DK, bool BF16, bool BOTH>
+__global__ __launch_bounds__(256, BF16 || DK == 32 ? 4 : 2) void delta_chunk_kernel(DeltaParams p, uint32_t units) {
+  auto form = [&](auto transposed, uint32_t unit) {
+    constexpr bool TRANSPOSED = transposed();
+    constexpr int NP = BF16 ? 1 : 3, ES = BF16 ? 2 : 4, NA = BF16 ? 2 : 3;
+    __shared__ __attribute__((aligned(16))) float low[10][16 * kLd];
+    __shared__ __attribute__((aligned(16))) float diag[4][16 * kLd];
+    __shared__ double sg[kDeltaChunk];
+    __shared__ float sbeta[kDeltaChunk];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int c = unit % p.NC, bh = unit / p.NC, b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk);
+    const int live = min(delta_length(p, b) - c * kDeltaChunk, kDeltaChunk);
+    if (live <= 0) return;
 
-  // 16 rows of 8 columns a lane group at a time
-  auto rows = [&](const DeltaRows& x, int i, u32x4 (&f)[DK / 32][BF16 ? 1 : 2]) {
-    const Window from = window_at(static_cast<const char*>(x.at) + (b * x.b + hk * x.h + (int64_t)(c * kDeltaChunk) * x.t) * ES);
-    const uint32_t at = 16 * i + r < live ? ((16 * i + r) * (uint32_t)x.t + 8 * g) * ES : kNowhere;
+    // 16 rows of 8 columns a lane group at a time
+    auto rows = [&](const DeltaRows& x, int i, u32x4 (&f)[DK / 32][BF16 ? 1 : 2]) {
+      const Window from = window_at(static_cast<const char*>(x.at) + (b * x.b + hk * x.h + (int64_t)(c * kDeltaChunk) * x.t) * ES);
+      const uint32_t at = 16 * i + r < live ? ((16 * i + r) * (uint32_t)x.t + 8 * g) * ES : kNowhere;
 #pragma unroll
-    for (int s = 0; s < DK / 32; ++s)
+      for (int s = 0; s < DK / 32; ++s)
 #pragma unroll
-      for (int n = 0; n < (BF16 ? 1 : 2); ++n) f[s][n] = window_load(from, at, 32 * s * ES + 16 * n);
-  };
-  auto planes = [&](const u32x4 (&f)[BF16 ? 1 : 2]) {
-    if constexpr (BF16) {
-      Planes<1> x;
-      x.p[0] = __builtin_bit_cast(bf16x8, f[0]);
-      return x;
-    } else {
-      return split8<3>(__builtin_bit_cast(f32x4, f[0]), __builtin_bit_cast(f32x4, f[1]));
+        for (int n = 0; n < (BF16 ? 1 : 2); ++n) f[s][n] = window_load(from, at, 32 * s * ES + 16 * n);
+    };
+    auto planes = [&](const u32x4 (&f)[BF16 ? 1 : 2]) {
+      if constexpr (BF16) {
+        Planes<1> x;
+        x.p[0] = __builtin_bit_cast(bf16x8, f[0]);
+        return x;
+      } else {
+        return split8<3>(__builtin_bit_cast(f32x4, f[0]), __builtin_bit_cast(f32x4, f[1]));
+      }
+    };
+    u32x4 k_raw[4][DK / 32][BF16 ? 1 : 2], q_raw[DK / 32][BF16 ? 1 : 2];
+    rows(p.k, wave, k_raw[3]);
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (j < wave) rows(p.k, j, k_raw[j]);
+    rows(p.q, wave, q_raw);
+
+    // gates: one token a lane, the same in every wave
+    double lg = 0.0;
+    float beta = 0.f;
+    if (lane < live) {
+      const int64_t t = c * kDeltaChunk + lane;
+      lg = fmax(log2((double)*gate_at(p.gamma, b, h, t)), -16384.0);  // a factor of 0 ends what came before
+      beta = *gate_at(p.beta, b, h, t);
     }
-  };
-  u32x4 k_raw[4][DK / 32][BF16 ? 1 : 2], q_raw[DK / 32][BF16 ? 1 : 2];
-  rows(p.k, wave, k_raw[3]);
 #pragma unroll
-  for (int j = 0; j < 3; ++j)
-    if (j < wave) rows(p.k, j, k_raw[j]);
-  if (p.q.at) rows(p.q, wave, q_raw);
-
-  // gates: one token a lane, the same in every wave
-  double lg = 0.0;
-  float beta = 0.f;
-  if (lane < live) {
-    const int64_t t = c * kDeltaChunk + lane;
-    lg = fmax(log2((double)*gate_at(p.gamma, b, h, t)), -16384.0);  // a factor of 0 ends what came before
-    beta = *gate_at(p.beta, b, h, t);
-  }
-#pragma unroll
-  for (int off = 1; off < 64; off *= 2) {
-    const double before = __shfl_up(lg, off);
-    if (lane >= off) lg += before;
-  }
-  if (wave == 0) {
-    sg[lane] = lg;
-    sbeta[lane] = beta;
-    if constexpr (!TRANSPOSED) {
-      DeltaGates& out = p.gates[unit];
-      out.g[lane] = lg;
-      out.c[lane] = decay(lg, 0.0);
-      out.tail[lane] = decay(__shfl(lg, 63), lg);
-      out.beta[lane] = beta;
+    for (int off = 1; off < 64; off *= 2) {
+      const double before = __shfl_up(lg, off);
+      if (lane >= off) lg += before;
     }
-  }
-  __syncthreads();
+    if (wave == 0) {
+      sg[lane] = lg;
+      sbeta[lane] = beta;
+      if constexpr (!TRANSPOSED) {
+        DeltaGates& out = p.gates[unit];
+        out.g[lane] = lg;
+        out.c[lane] = decay(lg, 0.0);
+        out.tail[lane] = decay(__shfl(lg, 63), lg);
+        out.beta[lane] = beta;
+      }
+    }
+    __syncthreads();
 
-  char* const to = (TRANSPOSED ? p.matrices_t + (int64_t)unit * (2 * kTriangleBytes)
-                               : p.matrices + (int64_t)unit * delta_matrix_bytes(NA)) + lane * 16;
-  auto put_tile = [&](int matrix, int i, int j, const f32x4& x) {
-    *reinterpret_cast<f32x4*>(to + matrix * kTriangleBytes + triangle_tile<false>(i, j) * 1024) = x;
-  };
-  // A block's two tiles, in parts, to its place
-  auto put = [&](int matrix, int parts, int block, const f32x4& lo, const f32x4& hi) {
-    const Planes<3> f = split8<3>(lo, hi);
+    char* const to = (TRANSPOSED ? p.matrices_t + (int64_t)unit * (2 * kTriangleBytes)
+                                 : p.matrices + (int64_t)unit * delta_matrix_bytes(NA)) + lane * 16;
+    auto put_tile = [&](int matrix, int i, int j, const f32x4& x) {
+      *reinterpret_cast<f32x4*>(to + matrix * kTriangleBytes + triangle_tile<false>(i, j) * 1024) = x;
+    };
+    // A block's two tiles, in parts, to its place
+    auto put = [&](int matrix, int parts, int block, const f32x4& lo, const f32x4& hi) {
+      const Planes<3> f = split8<3>(lo, hi);
 #pragma unroll
-    for (int n = 0; n < 3; ++n)
-      if (n < parts)
-        *reinterpret_cast<bf16x8*>(to + (matrix * 3 + n) * kBlocksBytes + block * 1024) = f.p[n];
-  };
-  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+      for (int n = 0; n < 3; ++n)
+        if (n < parts)
+          *reinterpret_cast<bf16x8*>(to + (matrix * 3 + n) * kBlocksBytes + block * 1024) = f.p[n];
+    };
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
-  // Row tile `wave`: keys with keys, and queries with keys (a lane has one query and 4 keys of
-  // a tile, transposed the other way round).
-  f32x4 kk[4] = {zero, zero, zero, zero}, a[4] = {zero, zero, zero, zero};  // [3]: the diagonal tile
+    // Row tile `wave`: keys with keys, and queries with keys (a lane has one query and 4 keys of
+    // a tile, transposed the other way round).
+    f32x4 kk[4] = {zero, zero, zero, zero}, a[4] = {zero, zero, zero, zero};  // [3]: the diagonal tile
 #pragma unroll
-  for (int s = 0; s < DK / 32; ++s) {
-    const auto own = planes(k_raw[3][s]);
-    Planes<NP> q;
-    if (p.q.at) q = planes(q_raw[s]);
+    for (int s = 0; s < DK / 32; ++s) {
+      const auto own = planes(k_raw[3][s]);
+      const auto q = planes(q_raw[s]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j < 3 && j >= wave) continue;
+        const auto k = planes(k_raw[j][s]);
+        kk[j] = mma<2>(own, k, kk[j]);
+        a[j] = TRANSPOSED ? mma<2>(q, k, a[j]) : mma<2>(k, q, a[j]);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (j < 3 && j >= wave) continue;
-      const auto k = planes(k_raw[j][s]);
-      kk[j] = mma<2>(own, k, kk[j]);
-      if (p.q.at) a[j] = TRANSPOSED ? mma<2>(q, k, a[j]) : mma<2>(k, q, a[j]);
-    }
-  }
+      const int tile = j < 3 ? j : wave, col = 16 * tile + r;
+      const double gj = sg[col];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (j < 3 && j >= wave) continue;
-    const int tile = j < 3 ? j : wave, col = 16 * tile + r;
-    const double gj = sg[col];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int t = 16 * wave + 4 * g + e;
-      const float d = decay(sg[t], gj);
-      const float x = kk[j][e] * d * (TRANSPOSED ? sbeta[t] : sbeta[col]);
-      low[tile_of(wave, tile)][(4 * g + e) * kLd + r] = col < t ? x : 0.f;
-      if constexpr (TRANSPOSED) {
-        a[j][e] = col <= t ? a[j][e] * d : 0.f;
-      } else {
-        const int at_t = 16 * wave + r, at_j = 16 * tile + 4 * g + e;
-        a[j][e] = at_j <= at_t ? a[j][e] * decay(sg[at_t], sg[at_j]) : 0.f;
+      for (int e = 0; e < 4; ++e) {
+        const int t = 16 * wave + 4 * g + e;
+        const float d = decay(sg[t], gj);
+        const float x = kk[j][e] * d * (TRANSPOSED ? sbeta[t] : sbeta[col]);
+        low[tile_of(wave, tile)][(4 * g + e) * kLd + r] = col < t ? x : 0.f;
+        if constexpr (TRANSPOSED) {
+          a[j][e] = col <= t ? a[j][e] * d : 0.f;
+        } else {
+          const int at_t = 16 * wave + r, at_j = 16 * tile + 4 * g + e;
+          a[j][e] = at_j <= at_t ? a[j][e] * decay(sg[at_t], sg[at_j]) : 0.f;
+        }
       }
     }
-  }
-  if (p.q.at) {
     if constexpr (!TRANSPOSED) {
       const f32x4 d = a[3];
       if (wave == 0) put(1, NA, lower_block(0, 0), d, zero);
@@ -160,89 +162,91 @@ __global__ __launch_bounds__(256, BF16 || DK == 32 ? 4 : 2) void delta_chunk_ker
         if (j < wave) put_tile(1, j, wave, a[j]);
       put_tile(1, wave, wave, a[3]);
     }
-  }
-  __syncthreads();
-
-  {  // diagonal block `wave`, lane r (of each lane group) its column r
-    const float* l = low[tile_of(wave, wave)];
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float s = i == r ? 1.f : 0.f;
-#pragma unroll
-      for (int m4 = 0; m4 < i; m4 += 4) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(l + i * kLd + m4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (m4 + e < i) s = fmaf(-v[e], x[m4 + e], s);
-      }
-      x[i] = s;
-    }
-    if (g == 0)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) diag[wave][i * kLd + r] = x[i];
-  }
-  __syncthreads();
-
-  f32x4 t[4];  // T_ij of column j = wave, rows 4 g + e, column r
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    t[i] = zero;
-    if (i < wave) continue;
-    if (i == wave) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t[i][e] = diag[i][(4 * g + e) * kLd + r];
-      continue;
-    }
-    f32x4 acc = zero, out = zero;
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      if (m < wave || m >= i) continue;
-      const f32x4 x = *reinterpret_cast<const f32x4*>(&low[tile_of(i, m)][r * kLd + 4 * g]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc = mfma_f32(x[e], t[m][e], acc);
-    }
-    const f32x4 d = *reinterpret_cast<const f32x4*>(&diag[i][r * kLd + 4 * g]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) out = mfma_f32(d[e], acc[e], out);
-    t[i] = -out;
-  }
-
-  // a lane's 4 numbers lie along the later product's inner index: rows of the
-  // transposed inverse as they are, rows of the inverse by way of LDS
-  if constexpr (TRANSPOSED) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i >= wave) put_tile(0, wave, i, t[i]);
-  } else {
     __syncthreads();
+
+    {  // diagonal block `wave`, lane r (of each lane group) its column r
+      const float* l = low[tile_of(wave, wave)];
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float s = i == r ? 1.f : 0.f;
+#pragma unroll
+        for (int m4 = 0; m4 < i; m4 += 4) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(l + i * kLd + m4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (m4 + e < i) s = fmaf(-v[e], x[m4 + e], s);
+        }
+        x[i] = s;
+      }
+      if (g == 0)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) diag[wave][i * kLd + r] = x[i];
+    }
+    __syncthreads();
+
+    f32x4 t[4];  // T_ij of column j = wave, rows 4 g + e, column r
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      t[i] = zero;
       if (i < wave) continue;
+      if (i == wave) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) low[tile_of(i, wave)][(4 * g + e) * kLd + r] = t[i][e];
+        for (int e = 0; e < 4; ++e) t[i][e] = diag[i][(4 * g + e) * kLd + r];
+        continue;
+      }
+      f32x4 acc = zero, out = zero;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        if (m < wave || m >= i) continue;
+        const f32x4 x = *reinterpret_cast<const f32x4*>(&low[tile_of(i, m)][r * kLd + 4 * g]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc = mfma_f32(x[e], t[m][e], acc);
+      }
+      const f32x4 d = *reinterpret_cast<const f32x4*>(&diag[i][r * kLd + 4 * g]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out = mfma_f32(d[e], acc[e], out);
+      t[i] = -out;
     }
-    __syncthreads();
-    auto row = [&](int j) { return *reinterpret_cast<const f32x4*>(&low[tile_of(wave, j)][r * kLd + 4 * g]); };
-    put(0, 3, lower_block(wave, 0), row(0), wave >= 1 ? row(1) : zero);
-    if (wave >= 2) put(0, 3, lower_block(wave, 1), row(2), wave == 3 ? row(3) : zero);
-  }
+
+    // a lane's 4 numbers lie along the later product's inner index: rows of the
+    // transposed inverse as they are, rows of the inverse by way of LDS
+    if constexpr (TRANSPOSED) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i >= wave) put_tile(0, wave, i, t[i]);
+    } else {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < wave) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) low[tile_of(i, wave)][(4 * g + e) * kLd + r] = t[i][e];
+      }
+      __syncthreads();
+      auto row = [&](int j) { return *reinterpret_cast<const f32x4*>(&low[tile_of(wave, j)][r * kLd + 4 * g]); };
+      put(0, 3, lower_block(wave, 0), row(0), wave >= 1 ? row(1) : zero);
+      if (wave >= 2) put(0, 3, lower_block(wave, 1), row(2), wave == 3 ? row(3) : zero);
+    }
+  };
+  if (!BOTH || blockIdx.x < units) form(std::false_type{}, blockIdx.x);
+  else if constexpr (BOTH) form(std::true_type{}, blockIdx.x - units);
 }
 
 template <int DK, bool BF16>
-hipError_t launch(bool transposed, const DeltaParams& p, hipStream_t s) {
-  const dim3 grid((uint32_t)((int64_t)p.B * p.H * p.NC));
-  if (transposed) delta_chunk_kernel<DK, BF16, true><<<grid, 256, 0, s>>>(p);
-  else delta_chunk_kernel<DK, BF16, false><<<grid, 256, 0, s>>>(p);
+hipError_t launch(const DeltaParams& p, hipStream_t s) {
+  const uint32_t units = (uint32_t)((int64_t)p.B * p.H * p.NC);
+  if (p.matrices_t) delta_chunk_kernel<DK, BF16, true><<<2 * units, 256, 0, s>>>(p, units);
+  else delta_chunk_kernel<DK, BF16, false><<<units, 256, 0, s>>>(p, units);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_delta_chunks(bool bf16, bool transposed, const DeltaParams& p, hipStream_t s) {
-  if (p.dk == 128) return bf16 ? launch<128, true>(transposed, p, s) : launch<128, false>(transposed, p, s);
-  if (p.dk == 64) return bf16 ? launch<64, true>(transposed, p, s) : launch<64, false>(transposed, p, s);
-  return bf16 ? launch<32, true>(transposed, p, s) : launch<32, false>(transposed, p, s);
+hipError_t launch_delta_chunks(bool bf16, const DeltaParams& p, hipStream_t s) {
+  if (p.dk == 128) return bf16 ? launch<128, true>(p, s) : launch<128, false>(p, s);
+  if (p.dk == 64) return bf16 ? launch<64, true>(p, s) : launch<64, false>(p, s);
+  return bf16 ? launch<32, true>(p, s) : launch<32, false>(p, s);
 }
 
 }  // namespace mesa
