@@ -20,8 +20,8 @@
 // Logarithms of the forget factors are summed in 64 bits, so that a ratio c_t / c_j keeps
 // fp32's precision however strong the decay before it.
 //
-// Memory bounds it where there are many chunks: at B=8 H=16 T=4096 d=128 bf16 106 us for
-// 0.52 GB forward (4.9 TB/s, a large copy's rate), 184 us for 0.95 GB for both.  One round of
+// Memory bounds it where there are many chunks: at B=8 H=16 T=4096 d=128 bf16 101 us for
+// 0.52 GB forward (5.2 TB/s; a large copy 4.9), 173 to 184 us for 0.95 GB for both.  One round of
 // chunks is a chain of 6.5 us (fp32 9): loads 1, logarithms 1, products and decays 2, the
 // diagonal blocks 1, the others and the way out 1.5.
 #include "mesa_delta_tile.h"

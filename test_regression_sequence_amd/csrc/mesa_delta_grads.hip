@@ -15,7 +15,7 @@
 // loads in flight), the second over the chunk's pairs.  What reaches the gates' fp32 gradients is multiplied in
 // three bf16 planes; Z and Y take two where dq and dk are bf16.
 //
-// At B=8 H=16 T=4096 d=128 bf16 it moves 2.4 GB in 694 to 732 us, 3.3 to 3.5 TB/s, two thirds
+// At B=8 H=16 T=4096 d=128 bf16 it moves 2.4 GB in 679 to 732 us, 3.3 to 3.6 TB/s, two thirds
 // of a large copy's rate.  The vector unit works 32 % of the time (a third of it on planes),
 // the matrix unit 22 % and LDS 24 %, hardly at once: registers leave room for two waves a SIMD,
 // which the barriers keep in step.  A workgroup that goes from chunk to chunk, its loads ahead

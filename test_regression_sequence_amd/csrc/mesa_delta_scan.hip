@@ -18,8 +18,8 @@
 //
 // A chunk takes 2.8 us where few workgroups run, of which the chain's 132 products are 0.9
 // and their operands' ways through conversions and LDS the rest, and 3.6 us on all CUs (B=1
-// H=16 T=32768 d=128, 8 segments of 57 chunks side by side: 216 us).  With states and W kept memory bounds it: at
-// B=8 H=16 T=4096 d=128 370 us for 1.6 GB, 4.3 TB/s where a large copy reaches 4.9.
+// H=16 T=32768 d=128, 8 segments of 57 chunks side by side: 214 to 219 us).  With states and W kept memory bounds it: at
+// B=8 H=16 T=4096 d=128 356 to 370 us for 1.6 GB, 4.3 to 4.5 TB/s where a large copy reaches 4.9.
 #include <algorithm>
 
 #include "mesa_delta_probe.h"
