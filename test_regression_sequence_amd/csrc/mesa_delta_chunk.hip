@@ -53,7 +53,8 @@ __global__ __launch_bounds__(256, BF16 || DK == 32 ? 4 : 2) void delta_chunk_ker
 
     // 16 rows of 8 columns a lane group at a time
     auto rows = [&](const DeltaRows& x, int i, u32x4 (&f)[DK / 32][BF16 ? 1 : 2]) {
-      const Window from = window_at(static_cast<const char*>(x.at) + (b * x.b + hk * x.h + (int64_t)(c * kDeltaChunk) * x.t) * ES);
+      const int64_t first = b * x.b + hk * x.h + (int64_t)(c * kDeltaChunk) * x.t;
+      const Window from = window_at(static_cast<const char*>(x.at) + first * ES);
       const uint32_t at = 16 * i + r < live ? ((16 * i + r) * (uint32_t)x.t + 8 * g) * ES : kNowhere;
 #pragma unroll
       for (int s = 0; s < DK / 32; ++s)

@@ -76,11 +76,13 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
   const bool there = own < here, valid = own < live;
   const uint32_t w_at = (from * p.dv + at4) * 4, do_at = (from * (uint32_t)p.d_o.t + at4) * sizeof(Out),
                  dv_at = (from * (uint32_t)p.dv_.t + at4) * sizeof(Out);
+  auto rows_at = [&](const DeltaRows& x, int head) {
+    return window_at(static_cast<const char*>(x.at) + (b * x.b + head * x.h + t0 * x.t) * sizeof(Out));
+  };
   f32x4 sl[NS], dl[NS], wl, el, ol;
   const Window states = window_at(p.states + unit * p.dv * DK), dstates = window_at(p.dstates + unit * p.dv * DK),
                ws = window_at(p.w + unit * 64 * p.dv), es = window_at(p.e + unit * 64 * p.dv),
-               dos = window_at(static_cast<const char*>(p.d_o.at) + (b * p.d_o.b + h * p.d_o.h + t0 * p.d_o.t) * sizeof(Out)),
-               dvs = window_at(static_cast<char*>(p.dv_.at) + (b * p.dv_.b + h * p.dv_.h + t0 * p.dv_.t) * sizeof(Out));
+               dos = rows_at(p.d_o, h), dvs = rows_at(p.dv_, h);
   auto load = [&](int d0) {
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
@@ -100,10 +102,8 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
   const bool heads = p.dq_heads != nullptr;
   const int at_key = 16 * MH * half + 4 * g;
   const int64_t heads_at = ((int64_t)bh * p.T + t0) * DK;
-  const Window dqs = heads ? window_at(p.dq_heads + heads_at)
-                           : window_at(static_cast<char*>(p.dq.at) + (b * p.dq.b + hk * p.dq.h + t0 * p.dq.t) * sizeof(Out));
-  const Window dks = heads ? window_at(p.dk_heads + heads_at)
-                           : window_at(static_cast<char*>(p.dk_.at) + (b * p.dk_.b + hk * p.dk_.h + t0 * p.dk_.t) * sizeof(Out));
+  const Window dqs = heads ? window_at(p.dq_heads + heads_at) : rows_at(p.dq, hk),
+               dks = heads ? window_at(p.dk_heads + heads_at) : rows_at(p.dk_, hk);
   auto put = [&](const f32x4 (&dq)[MH], const f32x4 (&dk)[MH]) {
 #pragma unroll
     for (int i = 0; i < MH; ++i) {
@@ -112,8 +112,10 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
         window_store(dqs, to, 64 * i, dq[i]);
         window_store(dks, to, 64 * i, dk[i]);
       } else {
-        window_store_row<BF16>(dqs, there ? (own * (uint32_t)p.dq.t + at_key) * sizeof(Out) : kNowhere, 16 * i * sizeof(Out), dq[i]);
-        window_store_row<BF16>(dks, there ? (own * (uint32_t)p.dk_.t + at_key) * sizeof(Out) : kNowhere, 16 * i * sizeof(Out), dk[i]);
+        window_store_row<BF16>(dqs, there ? (own * (uint32_t)p.dq.t + at_key) * sizeof(Out) : kNowhere,
+                               16 * i * sizeof(Out), dq[i]);
+        window_store_row<BF16>(dks, there ? (own * (uint32_t)p.dk_.t + at_key) * sizeof(Out) : kNowhere,
+                               16 * i * sizeof(Out), dk[i]);
       }
     }
   };
@@ -285,8 +287,11 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
   float left = 0.f;  // what this token leaves behind the chunk
 #pragma unroll
   for (int i = 0; i < MH; ++i) {
-    const f32x4 q = (half ? rows.template values<NP>(lds + L::kQ, L::kPlane, 16 * tile, MH + i) : rows.template values<NP>(lds + L::kQ, L::kPlane, 16 * tile, i));
-    const f32x4 k = (half ? rows.template values<NP>(lds + L::kK, L::kPlane, 16 * tile, MH + i) : rows.template values<NP>(lds + L::kK, L::kPlane, 16 * tile, i));
+    auto own_values = [&](const char* plane) {
+      return half ? rows.template values<NP>(plane, L::kPlane, 16 * tile, MH + i)
+                  : rows.template values<NP>(plane, L::kPlane, 16 * tile, i);
+    };
+    const f32x4 q = own_values(lds + L::kQ), k = own_values(lds + L::kK);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       sum += cc * q[e] * aq[i][e] - cb * k[e] * ak[i][e];
