@@ -235,3 +235,29 @@ def test_segments_in_place(dtype):
     check_forward(r, a, dt, walks=2)
     g = mesa.delta_bwd(*args(t), t["d_o"], s0=t["s0"], lengths=t["lengths"], d_sfinal=ds, state_grads=True, out={"ds0": ds})
     check_backward(g, a, dt, walks=2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_write_strengths_up_to_two(dtype):
+    """1 - beta between -1 and 1 does not lengthen a state either; no forgetting."""
+    dt = DTYPES[dtype]
+    a = draw(2, 2, 2, 200, 64, 64, dt, beta=(0.0, 2.0))
+    a["gamma"][:] = 1.0
+    t = to_dev(a, dt)
+    check_forward(forward(t), a, dt)
+    check_backward(backward(t), a, dt)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [150, 1300])
+def test_powers_of_two_pass_through(T, dtype):
+    """The rule is linear in (v, s0), its gradients in (d_o, d_sfinal): powers of two change exponents alone."""
+    dt = DTYPES[dtype]
+    t = to_dev(draw(2, 2, 1, T, 64, 48, dt, gates="slow"), dt)
+    k, m = 2.0 ** 30, 2.0 ** -25
+    u = dict(t, v=t["v"] * k, s0=t["s0"] * k, d_o=t["d_o"] * m, d_sfinal=t["d_sfinal"] * m)
+    f, f2, g, g2 = forward(t), forward(u), backward(t), backward(u)
+    for n in f:
+        assert torch.equal(f[n] * k, f2[n]), n
+    for n, by in (("dq", k * m), ("dk", k * m), ("dv", m), ("dgamma", k * m), ("dbeta", k * m), ("ds0", m)):
+        assert torch.equal(g[n] * by, g2[n]), n
