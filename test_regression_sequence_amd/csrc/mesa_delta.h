@@ -9,6 +9,22 @@ namespace mesa {
 
 constexpr int kDeltaChunk = 64;  // tokens that are taken together
 
+// Quotients of numbers below 2^30 by d, without a division: floor(n m / 2^shift).  m is 2^shift / d
+// rounded up and shift 31 + floor(log2 d), so n m / 2^shift exceeds n / d by less than n / d 2^-30 < 1 / d.
+// (A workgroup's place took four divisions of 200 cycles each.)
+struct Divisor {
+  uint32_t d, m, shift;
+};
+inline Divisor divisor(uint32_t d) {
+  uint32_t log = 0;
+  while (d >> (log + 1)) ++log;
+  return {d, (uint32_t)((((uint64_t)1 << (31 + log)) + d - 1) / d), 31 + log};
+}
+__host__ __device__ inline uint32_t operator/(uint32_t n, const Divisor& x) {
+  return (uint32_t)(((uint64_t)n * x.m) >> x.shift);
+}
+__host__ __device__ inline uint32_t operator%(uint32_t n, const Divisor& x) { return n - n / x * x.d; }
+
 // Vectors of B x heads x T tokens; strides in elements, the last index contiguous.
 struct DeltaRows {
   void* at;
@@ -42,12 +58,14 @@ struct DeltaParams {
   float* s_final;                   // [B, H, dv, dk] or null
   const int32_t* lengths;           // [B] or null
   int B, H, Hk, T, dk, dv, NC;      // NC chunks a (padded) sequence
+  Divisor by_h, by_shared, by_nc;   // H, H / Hk, NC
   // A walk in NS segments of L chunks (NS = 1: whole).  seg_map: [B H, NS, dk, dk], row j what
   // an inner segment makes of the state whose row is unit vector j; seg_add: [B H, NS, dv, dk], what
   // it makes of a zero state (the segment at the walk's start: of the given one);
   // seg_start: [B H, NS, dv, dk], the states that segments start from behind the join
   int NS, L;
   int seg0, segs;                   // the segments of a launch of a walk
+  Divisor by_part, by_slices;       // its workgroups of a head, and of those the ones of a segment
   float *seg_map, *seg_add, *seg_start;
   int open;                         // 1: the launch before the join: ends go to seg_add, and a segment
                                     // that does not start the walk starts from zero
@@ -88,6 +106,7 @@ struct DeltaStepParams {
   float* state;
   void* o;
   int N, H, Hk, dk, dv;
+  Divisor by_groups, by_h, by_shared;  // workgroups of a head, H, H / Hk
 };
 hipError_t launch_delta_step(bool bf16, const DeltaStepParams& p, hipStream_t s);
 

@@ -188,7 +188,7 @@ __global__ __launch_bounds__(512, 2) void delta_adjoint_kernel(DeltaParams p) {
     return;
   }
 
-  const int hk = h / (p.H / p.Hk);
+  const int hk = (uint32_t)h / p.by_shared;
   const int64_t q0 = b * p.q.b + hk * p.q.h, k0 = b * p.k.b + hk * p.k.h, o0 = b * p.d_o.b + h * p.d_o.h + col0;
   RowLoads<DK, true, 256> kl, ql;
   RowLoads<64, true, 256> ol;

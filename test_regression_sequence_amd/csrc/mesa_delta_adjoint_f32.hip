@@ -27,7 +27,8 @@ __global__ __launch_bounds__(256, 1) void delta_adjoint_f32_kernel(DeltaParams p
   Part part;
   if (!part_of(p, blockIdx.x, part)) return;
   const bool keep = !p.open || part.seg == p.NS - 1;  // whole: N and E go to memory
-  const int bh = part.bh, b = part.b, h = part.h, hk = h / (p.H / p.Hk), len = part.len, first = part.first, last = part.last;
+  const int bh = part.bh, b = part.b, h = part.h, hk = (uint32_t)h / p.by_shared, len = part.len, first = part.first,
+            last = part.last;
   const int col0 = part.col0, cols = part.cols;
   const int col = col0 + 16 * wave + r;
   const bool mine = 16 * wave < cols;

@@ -174,32 +174,41 @@ DeltaParams delta_params(const mesa_delta_desc* d, const void* q, const void* k,
   p.q = rows(d, q, d->q); p.k = rows(d, k, d->k); p.v = rows(d, v, d->v); p.gamma = gate(gamma, d->gamma);
   p.beta = gate(beta, d->beta); p.s0 = s0; p.lengths = lengths;
   p.B = d->B; p.H = d->H; p.Hk = d->Hk; p.T = d->T; p.dk = d->dk; p.dv = d->dv; p.NC = chunks_of(d);
+  p.by_h = divisor((uint32_t)d->H); p.by_shared = divisor((uint32_t)(d->H / d->Hk));
+  p.by_nc = divisor((uint32_t)std::max(p.NC, 1));
   return p;
 }
 
-// The launches of a walk in segments: `first` for what the others start from, and, behind the
-// join, segments seg0 .. seg0 + segs - 1.  With one segment the second alone.
+// The launches of a walk in segments: `first` for what the others start from (with segments
+// opened .. opened + openings - 1) and, behind the join, segments seg0 .. seg0 + segs - 1.
+// With one segment the second alone.
 template <typename First, typename Walk>
-hipError_t in_segments(const DeltaParams& p, bool back, int seg0, int segs, hipStream_t s, First&& first, Walk&& walk) {
+hipError_t in_segments(const DeltaParams& p, bool back, int opened, int openings, int seg0, int segs, hipStream_t s,
+                       First&& first, Walk&& walk) {
   DeltaParams x = p;
-  x.seg0 = 0;
-  x.segs = 1;
+  const auto range = [&](int from, int count) {
+    const uint32_t slices = (uint32_t)(p.dv + 63) / 64;
+    x.seg0 = from;
+    x.segs = count;
+    x.by_slices = divisor(slices);
+    x.by_part = divisor(slices * (uint32_t)count);
+  };
   if (p.NS > 1) {
+    range(opened, openings);
     x.open = 1;
     hipError_t e = first(x);
     if (e == hipSuccess) e = launch_delta_join(back, p, s);
     if (e != hipSuccess) return e;
     x.open = 0;
-    x.seg0 = seg0;
-    x.segs = segs;
   }
+  range(p.NS > 1 ? seg0 : 0, p.NS > 1 ? segs : 1);
   return walk(x);
 }
 
 // A walk forward.  For bf16 rows the first segment runs beside the launch that opens the others.
 hipError_t scan(bool bf16, const DeltaParams& p, hipStream_t s) {
   return in_segments(
-      p, false, bf16 ? 1 : 0, bf16 ? p.NS - 1 : p.NS, s,
+      p, false, 0, 1, bf16 ? 1 : 0, bf16 ? p.NS - 1 : p.NS, s,
       [&](const DeltaParams& x) { return bf16 ? launch_delta_open(x, s) : launch_delta_open_f32(x, s); },
       [&](const DeltaParams& x) { return bf16 ? launch_delta_scan(x, s) : launch_delta_scan_f32(x, s); });
 }
@@ -210,14 +219,7 @@ hipError_t adjoint(bool bf16, const DeltaParams& p, hipStream_t s) {
   const auto walk = [&](const DeltaParams& x) {
     return bf16 ? launch_delta_adjoint(x, s) : launch_delta_adjoint_f32(x, s);
   };
-  return in_segments(
-      p, true, 0, p.NS - 1, s,
-      [&](DeltaParams x) {
-        x.seg0 = 1;
-        x.segs = p.NS - 1;
-        return walk(x);
-      },
-      walk);
+  return in_segments(p, true, 1, p.NS - 1, 0, p.NS - 1, s, walk, walk);
 }
 
 mesa_status launched(hipError_t e) { return e == hipSuccess ? MESA_OK : MESA_ERR_HIP; }

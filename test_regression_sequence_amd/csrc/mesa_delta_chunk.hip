@@ -47,7 +47,8 @@ __global__ __launch_bounds__(256, BF16 || DK == 32 ? 4 : 2) void delta_chunk_ker
     __shared__ double sg[kDeltaChunk];
     __shared__ float sbeta[kDeltaChunk];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int c = unit % p.NC, bh = unit / p.NC, b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk);
+    const uint32_t bh = unit / p.by_nc;
+    const int c = unit % p.by_nc, b = bh / p.by_h, h = bh % p.by_h, hk = (uint32_t)h / p.by_shared;
     const int live = min(delta_length(p, b) - c * kDeltaChunk, kDeltaChunk);
     if (live <= 0) return;
 

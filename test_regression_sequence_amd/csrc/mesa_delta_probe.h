@@ -39,18 +39,19 @@ inline uint32_t probe_blocks(const DeltaParams& p, int from) {
   return (uint32_t)((p.B * p.H + 7) / 8 * 8 * probe_slices(p) * (p.NS - 1 - from));
 }
 
-// Workgroup `id` of them.
+// Workgroup `id` of them (by_part: of a head, by_slices: of those the ones of a segment).
 template <int DK, bool BF16>
-__device__ __forceinline__ void probe_segment(const DeltaParams& p, uint32_t id, int from, char* all) {
+__device__ __forceinline__ void probe_segment(const DeltaParams& p, uint32_t id, int from, const Divisor& by_part,
+                                              const Divisor& by_slices, char* all) {
   using L = ProbeLds<DK, BF16>;
   constexpr int NP = L::NP, MT = DK / 16, KS = DK / 32;
   char (*const lds)[L::kBuffer] = reinterpret_cast<char (*)[L::kBuffer]>(all);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   // one head's workgroups on one XCD, whose L2 they share
-  const int slices = (p.dv + DK + 127) / 128, per = slices * (p.NS - 1 - from), n = id >> 3, rest = n % per;
-  const int bh = n / per * 8 + (id & 7), seg = from + rest / slices, slice = rest % slices;
+  const uint32_t n = id >> 3, rest = n % by_part;
+  const int bh = n / by_part * 8 + (id & 7), seg = from + rest / by_slices, slice = rest % by_slices;
   if (bh >= p.B * p.H || (seg == 0 && 128 * slice >= p.dv)) return;
-  const int b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk), len = delta_length(p, b);
+  const int b = (uint32_t)bh / p.by_h, h = (uint32_t)bh % p.by_h, hk = (uint32_t)h / p.by_shared, len = delta_length(p, b);
   const int first = seg * p.L, last = max(min((len + 63) / 64, first + p.L), first);
   const int col0 = 128 * slice + 16 * wave;
   const bool unit_columns = col0 >= p.dv, mine = unit_columns ? col0 < p.dv + DK && seg > 0 : true;

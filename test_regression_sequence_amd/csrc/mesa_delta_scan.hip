@@ -208,7 +208,7 @@ __device__ __forceinline__ void walk_segment(const DeltaParams& p, uint32_t id, 
     return;
   }
 
-  const int hk = h / (p.H / p.Hk);
+  const int hk = (uint32_t)h / p.by_shared;
   const int64_t q0 = b * p.q.b + hk * p.q.h, k0 = b * p.k.b + hk * p.k.h, v0 = b * p.v.b + h * p.v.h + col0,
                 o0 = b * p.o.b + h * p.o.h + col0 + 16 * wave;
   const TileRows<DK> rows(lane);
@@ -322,9 +322,10 @@ __global__ __launch_bounds__(512, 2) void delta_scan_kernel(DeltaParams p) {
 
 // The first segment whole, and what the others but the last make of states, side by side.
 template <int DK, bool OUT>
-__global__ __launch_bounds__(512, 2) void delta_open_kernel(DeltaParams p, uint32_t probes) {
+__global__ __launch_bounds__(512, 2) void delta_open_kernel(DeltaParams p, uint32_t probes, Divisor by_part,
+                                                            Divisor by_slices) {
   __shared__ __attribute__((aligned(16))) char lds[std::max(ScanLds<DK>::kBytes, 2 * ProbeLds<DK, true>::kBuffer)];
-  if (blockIdx.x < probes) probe_segment<DK, true>(p, blockIdx.x, 1, lds);
+  if (blockIdx.x < probes) probe_segment<DK, true>(p, blockIdx.x, 1, by_part, by_slices, lds);
   else walk_segment<DK, OUT>(p, blockIdx.x - probes, lds);
 }
 
@@ -337,9 +338,11 @@ hipError_t launch(const DeltaParams& p, hipStream_t s) {
 
 template <int DK>
 hipError_t open(const DeltaParams& p, hipStream_t s) {
-  const uint32_t probes = probe_blocks(p, 1);
-  if (p.o.at) delta_open_kernel<DK, true><<<probes + walk_blocks(p), 512, 0, s>>>(p, probes);
-  else delta_open_kernel<DK, false><<<probes + walk_blocks(p), 512, 0, s>>>(p, probes);
+  const uint32_t probes = probe_blocks(p, 1), slices = probe_slices(p);
+  const Divisor by_slices = divisor(slices), by_part = divisor(std::max(slices * (p.NS - 2), 1u));
+  const uint32_t blocks = probes + walk_blocks(p);
+  if (p.o.at) delta_open_kernel<DK, true><<<blocks, 512, 0, s>>>(p, probes, by_part, by_slices);
+  else delta_open_kernel<DK, false><<<blocks, 512, 0, s>>>(p, probes, by_part, by_slices);
   return hipGetLastError();
 }
 

@@ -28,7 +28,8 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   Part part;
   if (!part_of(p, blockIdx.x, part)) return;
-  const int bh = part.bh, b = part.b, h = part.h, hk = h / (p.H / p.Hk), len = part.len, first = part.first, last = part.last;
+  const int bh = part.bh, b = part.b, h = part.h, hk = (uint32_t)h / p.by_shared, len = part.len, first = part.first,
+            last = part.last;
   const int col0 = part.col0, cols = part.cols;
   const int col = col0 + 16 * wave + r;                 // this lane's column of the state
   const bool mine = 16 * wave < cols;
@@ -201,14 +202,15 @@ __global__ __launch_bounds__(256, 1) void delta_scan_f32_kernel(DeltaParams p) {
 }
 
 template <int DK>
-__global__ __launch_bounds__(512, 2) void delta_open_f32_kernel(DeltaParams p) {
+__global__ __launch_bounds__(512, 2) void delta_open_f32_kernel(DeltaParams p, Divisor by_part, Divisor by_slices) {
   __shared__ __attribute__((aligned(16))) char lds[2 * ProbeLds<DK, false>::kBuffer];
-  probe_segment<DK, false>(p, blockIdx.x, 0, lds);
+  probe_segment<DK, false>(p, blockIdx.x, 0, by_part, by_slices, lds);
 }
 
 template <int DK>
 hipError_t open(const DeltaParams& p, hipStream_t s) {
-  delta_open_f32_kernel<DK><<<probe_blocks(p, 0), 512, 0, s>>>(p);
+  const uint32_t slices = probe_slices(p);
+  delta_open_f32_kernel<DK><<<probe_blocks(p, 0), 512, 0, s>>>(p, divisor(slices * (p.NS - 1)), divisor(slices));
   return hipGetLastError();
 }
 

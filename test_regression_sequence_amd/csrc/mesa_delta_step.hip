@@ -18,11 +18,10 @@ template <int DK, bool BF16, int U>
 __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepParams p) {
   constexpr int LR = DK / 8, RW = 64 / LR;  // lanes a row, rows a wave at a time
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane % LR, row0 = lane / LR;
-  const int groups = (p.dv + 4 * RW * U - 1) / (4 * RW * U);
-  const int64_t head = blockIdx.x / groups;
-  const int first = ((blockIdx.x % groups) * 4 + wave) * RW * U + row0;
-  const int h = (int)(head % p.H), hk = h / (p.H / p.Hk);
-  const int64_t n = head / p.H;
+  const uint32_t at_head = blockIdx.x / p.by_groups;
+  const int64_t head = at_head, n = at_head / p.by_h;
+  const int first = ((blockIdx.x % p.by_groups) * 4 + wave) * RW * U + row0;
+  const int h = at_head % p.by_h, hk = (uint32_t)h / p.by_shared;
   float* s = p.state + head * p.dv * DK + 4 * lr;
   f32x4 a[U], b[U];
   float v[U];
@@ -66,10 +65,13 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepParams p) {
 }
 
 template <int DK, bool BF16, int U>
-void launch(const DeltaStepParams& p, hipStream_t s) {
+void launch(DeltaStepParams p, hipStream_t s) {
   constexpr int rows = 4 * (512 / DK) * U;
-  const int64_t blocks = (int64_t)p.N * p.H * ((p.dv + rows - 1) / rows);
-  delta_step_kernel<DK, BF16, U><<<(uint32_t)blocks, 256, 0, s>>>(p);
+  const uint32_t groups = (uint32_t)((p.dv + rows - 1) / rows);
+  p.by_groups = divisor(groups);
+  p.by_h = divisor((uint32_t)p.H);
+  p.by_shared = divisor((uint32_t)(p.H / p.Hk));
+  delta_step_kernel<DK, BF16, U><<<(uint32_t)((int64_t)p.N * p.H * groups), 256, 0, s>>>(p);
 }
 
 template <int DK, bool BF16>

@@ -469,15 +469,14 @@ struct Part {
 // The workgroups of one head go to one XCD (workgroups are handed to the 8 XCDs in
 // turn), whose L2 they share.  False: no part.
 __device__ __forceinline__ bool part_of(const DeltaParams& p, uint32_t id, Part& x) {
-  const int slices = (p.dv + 63) / 64, per = slices * p.segs;
   const uint32_t xcd = id & 7, n = id >> 3;
-  x.bh = (int)(n / per) * 8 + (int)xcd;
+  x.bh = (int)(n / p.by_part) * 8 + (int)xcd;
   if (x.bh >= p.B * p.H) return false;
-  const int rest = (int)(n % per);
-  x.seg = rest / slices + p.seg0;
-  x.b = x.bh / p.H;
-  x.h = x.bh % p.H;
-  x.col0 = 64 * (rest % slices);
+  const uint32_t rest = n % p.by_part;
+  x.seg = (int)(rest / p.by_slices) + p.seg0;
+  x.b = (uint32_t)x.bh / p.by_h;
+  x.h = (uint32_t)x.bh % p.by_h;
+  x.col0 = 64 * (int)(rest % p.by_slices);
   x.cols = min(64, p.dv - x.col0);
   x.len = delta_length(p, x.b);
   x.first = x.seg * p.L;
