@@ -93,7 +93,7 @@ hipError_t launch_delta_adjoint(const DeltaParams& p, hipStream_t s);  // bf16 r
 hipError_t launch_delta_adjoint_f32(const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_grads(bool bf16, const DeltaParams& p, hipStream_t s);
 
-// seg_map and seg_add of a walk forward; for bf16 rows the first segment whole.
+// seg_map and seg_add of a walk forward, and its first segment whole.
 hipError_t launch_delta_open(const DeltaParams& p, hipStream_t s);  // bf16 rows
 hipError_t launch_delta_open_f32(const DeltaParams& p, hipStream_t s);
 // seg_start from seg_map, seg_add and the state at one end; `back`: from the last segment to the first.

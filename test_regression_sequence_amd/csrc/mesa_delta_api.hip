@@ -97,24 +97,24 @@ mesa_status check_delta(const mesa_delta_desc* d) {
 // In how many segments a walk goes.  A walk of one workgroup a head and 64 columns takes
 // its chunks one after the other; with fewer of those than the 256 CUs, segments of it run
 // side by side, after a launch that finds what each makes of unit rows and of zero (128 of
-// dv + dk columns a workgroup; for bf16 rows with the first segment) and one that joins them.  In times of one chunk (about
-// 2.7 us, in fp32 twice that), the two launches take about 3 and half a chunk a segment.
+// dv + dk columns a workgroup; the first segment runs with it) and one that joins them.  In
+// times of one chunk (about 2.7 us, in fp32 twice that), the two launches take about 3 and
+// half a chunk a segment.
 // Measured, one sequence, in segments and in one walk: 1024 tokens and 4 heads of 64,
-// forward 38 and 49 us, gradients 86 and 113, in fp32 49 and 101, 109 and 210; 4 heads of
-// 128, 59 and 60, 137 and 158; 4096 tokens and 16 heads of 128, 109 and 194, 319 and 565.
+// forward 44 and 53 us, gradients 77 and 107, in fp32 46 and 77, 98 and 175; 4 heads of
+// 128, 54 and 63, 120 and 149; 4096 tokens and 16 heads of 128, 113 and 216, 325 and 551.
 int segments_of(const mesa_delta_desc* d) {
   const int64_t heads = (int64_t)d->B * d->H, values = (d->dv + 63) / 64, both = (d->dv + d->dk + 127) / 128;
   const int chunks = chunks_of(d);
-  const bool bf16 = d->dtype == MESA_BF16;
-  const double more = bf16 ? 1.0 : 0.5;
+  const double more = d->dtype == MESA_BF16 ? 1.0 : 0.5;
   const auto rounds = [](int64_t blocks) { return (double)((blocks + 255) / 256); };
   int best = 1;
   double least = 0.9 * chunks * rounds(heads * values);
   for (int n = 2; n <= 32 && n * 2 <= chunks; ++n) {
     const int per = (chunks + n - 1) / n;
     if ((chunks + per - 1) / per != n) continue;  // (no segment stays empty)
-    const int64_t opening = bf16 ? values + (n - 2) * both : (n - 1) * both, rest = (bf16 ? n - 1 : n) * values;
-    const double time = per * (rounds(heads * opening) + rounds(heads * rest)) + more * (3 + 0.5 * n);
+    const double time =
+        per * (rounds(heads * (values + (n - 2) * both)) + rounds(heads * (n - 1) * values)) + more * (3 + 0.5 * n);
     if (time < least) {
       best = n;
       least = time;
@@ -205,10 +205,10 @@ hipError_t in_segments(const DeltaParams& p, bool back, int opened, int openings
   return walk(x);
 }
 
-// A walk forward.  For bf16 rows the first segment runs beside the launch that opens the others.
+// A walk forward: the first segment runs beside the launch that opens the others.
 hipError_t scan(bool bf16, const DeltaParams& p, hipStream_t s) {
   return in_segments(
-      p, false, 0, 1, bf16 ? 1 : 0, bf16 ? p.NS - 1 : p.NS, s,
+      p, false, 0, 1, 1, p.NS - 1, s,
       [&](const DeltaParams& x) { return bf16 ? launch_delta_open(x, s) : launch_delta_open_f32(x, s); },
       [&](const DeltaParams& x) { return bf16 ? launch_delta_scan(x, s) : launch_delta_scan_f32(x, s); });
 }

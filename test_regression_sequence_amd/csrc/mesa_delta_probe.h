@@ -1,9 +1,9 @@
 // Gated delta rule, forward: what the segments of a split walk make of states.
 //
 // Over a segment the state's rows go S -> S P + Q.  The walk of mesa_delta_scan.hip,
-// without outputs, over Q's columns (from zero, in the first segment from the given
-// state) and, behind the first segment, over P's: the dk unit columns, whose values are
-// zeros.  The last segment, which nothing follows, has neither.
+// without outputs, over Q's columns, from zero, and over P's: the dk unit columns, whose
+// values are zeros.  The first segment, which needs no start, runs whole beside it, and
+// nothing follows the last.
 //
 // Nothing is formed beside the chain of states, so all eight waves are chains, 16
 // columns each, two on a SIMD to fill one another's waits: 128 columns a workgroup, and
@@ -15,9 +15,8 @@
 // works 38 % and its vector unit 41 %, hardly at the same time (four chains of 16 columns as
 // in the walk itself: 2.7 us for 64 columns).  The two waves of a SIMD half a chunk apart,
 // so that conversions of one meet products of the other, took a tenth longer: the second
-// barrier a chunk costs more.  With bf16 rows the walk's first segment, which needs no
-// start, runs in the same launch: 9 segments in place of 8 on 256 CUs, 536 -> 493 us for
-// both launches of the walk.
+// barrier a chunk costs more.  The first segment's walk in the same launch: 9 segments in
+// place of 8 on 256 CUs, 536 -> 493 us for both launches of the walk.
 #pragma once
 
 #include "mesa_delta_tile.h"
@@ -33,15 +32,16 @@ struct ProbeLds {
                        kBuffer = kV + (BF16 ? 64 * 256 : 0);
 };
 
-inline int probe_slices(const DeltaParams& p) { return (p.dv + p.dk + 127) / 128; }
-// Workgroups of the segments from `from` to the one before the last.
-inline uint32_t probe_blocks(const DeltaParams& p, int from) {
-  return (uint32_t)((p.B * p.H + 7) / 8 * 8 * probe_slices(p) * (p.NS - 1 - from));
+// Workgroups of a head's segment, and of the segments between the first and the last.
+inline uint32_t probe_slices(const DeltaParams& p) { return (uint32_t)(p.dv + p.dk + 127) / 128; }
+inline uint32_t probe_blocks(const DeltaParams& p) {
+  return (uint32_t)((p.B * p.H + 7) / 8 * 8) * probe_slices(p) * (uint32_t)(p.NS - 2);
 }
+inline Divisor probe_part(const DeltaParams& p) { return divisor(probe_slices(p) * (uint32_t)(p.NS > 2 ? p.NS - 2 : 1)); }
 
 // Workgroup `id` of them (by_part: of a head, by_slices: of those the ones of a segment).
 template <int DK, bool BF16>
-__device__ __forceinline__ void probe_segment(const DeltaParams& p, uint32_t id, int from, const Divisor& by_part,
+__device__ __forceinline__ void probe_segment(const DeltaParams& p, uint32_t id, const Divisor& by_part,
                                               const Divisor& by_slices, char* all) {
   using L = ProbeLds<DK, BF16>;
   constexpr int NP = L::NP, MT = DK / 16, KS = DK / 32;
@@ -49,12 +49,12 @@ __device__ __forceinline__ void probe_segment(const DeltaParams& p, uint32_t id,
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, g = lane >> 4;
   // one head's workgroups on one XCD, whose L2 they share
   const uint32_t n = id >> 3, rest = n % by_part;
-  const int bh = n / by_part * 8 + (id & 7), seg = from + rest / by_slices, slice = rest % by_slices;
-  if (bh >= p.B * p.H || (seg == 0 && 128 * slice >= p.dv)) return;
+  const int bh = n / by_part * 8 + (id & 7), seg = 1 + rest / by_slices, slice = rest % by_slices;
+  if (bh >= p.B * p.H) return;
   const int b = (uint32_t)bh / p.by_h, h = (uint32_t)bh % p.by_h, hk = (uint32_t)h / p.by_shared, len = delta_length(p, b);
   const int first = seg * p.L, last = max(min((len + 63) / 64, first + p.L), first);
   const int col0 = 128 * slice + 16 * wave;
-  const bool unit_columns = col0 >= p.dv, mine = unit_columns ? col0 < p.dv + DK && seg > 0 : true;
+  const bool unit_columns = col0 >= p.dv, mine = col0 < p.dv + DK;
   const int col = (unit_columns ? col0 - p.dv : col0) + r;
   const int64_t k0 = b * p.k.b + hk * p.k.h, v0 = b * p.v.b + h * p.v.h;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -66,8 +66,6 @@ __device__ __forceinline__ void probe_segment(const DeltaParams& p, uint32_t id,
     if (unit_columns) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) m[i][e] = 16 * i + 4 * g + e == col ? 1.f : 0.f;
-    } else if (seg == 0 && p.s0) {
-      m[i] = *reinterpret_cast<const f32x4*>(p.s0 + ((int64_t)bh * p.dv + col) * DK + 16 * i + 4 * g);
     }
   }
   const TileRows<DK> rows(lane);

@@ -325,7 +325,7 @@ template <int DK, bool OUT>
 __global__ __launch_bounds__(512, 2) void delta_open_kernel(DeltaParams p, uint32_t probes, Divisor by_part,
                                                             Divisor by_slices) {
   __shared__ __attribute__((aligned(16))) char lds[std::max(ScanLds<DK>::kBytes, 2 * ProbeLds<DK, true>::kBuffer)];
-  if (blockIdx.x < probes) probe_segment<DK, true>(p, blockIdx.x, 1, by_part, by_slices, lds);
+  if (blockIdx.x < probes) probe_segment<DK, true>(p, blockIdx.x, by_part, by_slices, lds);
   else walk_segment<DK, OUT>(p, blockIdx.x - probes, lds);
 }
 
@@ -338,11 +338,9 @@ hipError_t launch(const DeltaParams& p, hipStream_t s) {
 
 template <int DK>
 hipError_t open(const DeltaParams& p, hipStream_t s) {
-  const uint32_t probes = probe_blocks(p, 1), slices = probe_slices(p);
-  const Divisor by_slices = divisor(slices), by_part = divisor(std::max(slices * (p.NS - 2), 1u));
-  const uint32_t blocks = probes + walk_blocks(p);
-  if (p.o.at) delta_open_kernel<DK, true><<<blocks, 512, 0, s>>>(p, probes, by_part, by_slices);
-  else delta_open_kernel<DK, false><<<blocks, 512, 0, s>>>(p, probes, by_part, by_slices);
+  const uint32_t probes = probe_blocks(p), blocks = probes + walk_blocks(p);
+  if (p.o.at) delta_open_kernel<DK, true><<<blocks, 512, 0, s>>>(p, probes, probe_part(p), divisor(probe_slices(p)));
+  else delta_open_kernel<DK, false><<<blocks, 512, 0, s>>>(p, probes, probe_part(p), divisor(probe_slices(p)));
   return hipGetLastError();
 }
 

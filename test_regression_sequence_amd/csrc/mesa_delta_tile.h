@@ -316,6 +316,26 @@ struct RowLoads {
   }
 };
 
+// 64 rows of W fp32 numbers in planes, between their conversion and LDS.
+template <int W, int THREADS>
+struct RowPlanes {
+  using Loads = RowLoads<W, false, THREADS>;
+  bf16x4 x[Loads::kN][3];
+  __device__ __forceinline__ explicit RowPlanes(const Loads& rows) {
+#pragma unroll
+    for (int n = 0; n < Loads::kN; ++n) split4<3>(__builtin_bit_cast(f32x4, rows.r[n]), x[n]);
+  }
+  __device__ __forceinline__ void store(char* tile, int plane, int tid) const {
+#pragma unroll
+    for (int n = 0; n < Loads::kN; ++n) {
+      const int row = tid / (W / 4) + n * Loads::kRows, col = tid % (W / 4) * 4;
+      if (Loads::kPieces % THREADS != 0 && row >= 64) continue;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x4*>(tile + i * plane + tile_at<W>(row, 2 * col)) = x[n][i];
+    }
+  }
+};
+
 // `BYTES` bytes on their way from memory to LDS as they are.
 template <int BYTES, int THREADS>
 struct CopyLoads {
