@@ -98,10 +98,10 @@ mesa_status check_delta(const mesa_delta_desc* d) {
 // its chunks one after the other; with fewer of those than the 256 CUs, segments of it run
 // side by side, after a launch that finds what each makes of unit rows and of zero (128 of
 // dv + dk columns a workgroup; the first segment runs with it) and one that joins them.  In
-// times of one chunk (about 2.7 us, in fp32 twice that), the two launches take about 3 and
+// times of one chunk (about 2.7 us, in fp32 nearly twice that), the two launches take about 3 and
 // half a chunk a segment.
 // Measured, one sequence, in segments and in one walk: 1024 tokens and 4 heads of 64,
-// forward 44 and 53 us, gradients 77 and 107, in fp32 46 and 77, 98 and 175; 4 heads of
+// forward 44 and 53 us, gradients 77 and 107, in fp32 46 and 77, 95 and 149; 4 heads of
 // 128, 54 and 63, 120 and 149; 4096 tokens and 16 heads of 128, 113 and 216, 325 and 551.
 int segments_of(const mesa_delta_desc* d) {
   const int64_t heads = (int64_t)d->B * d->H, values = (d->dv + 63) / 64, both = (d->dv + d->dk + 127) / 128;

@@ -8,7 +8,6 @@
 // The state's waves alone, with the splits between the barriers, took 5.7 us a chunk at
 // dk = 64, so it takes 4.4, of which 216 products are 1.5 (B=5 H=6 T=777 dk=64 dv=96 in 4
 // segments: 19 us for the first segment and the openings of the others, 18 for the rest).
-// At dk = 128 a chunk takes 7.2 us; there 22 registers go through scratch.
 #include <algorithm>
 
 #include "mesa_delta_probe.h"
@@ -136,7 +135,9 @@ __device__ __forceinline__ void walk_segment(const DeltaParams& p, uint32_t id, 
       for (int i = 0; i < 4; ++i) x[i] = zero;
       mma_triangle<2, true, false, false>(lds + L::kT, t, px, x, lane);  // W
       Planes<NP> kt[2][4];
-      constexpr int G = MT < 4 ? MT : 4, NG = 2 * MT / G;  // K^T in groups of 4 tiles
+      // K^T in groups of tiles (at dk = 128 four a group take 22 registers through scratch: 256 heads of
+      // 1024 tokens 346 us, so 316)
+      constexpr int G = DK == 64 ? 4 : 2, NG = 2 * MT / G;
       auto keys = [&](int n, Planes<NP> (&to)[4]) {
 #pragma unroll
         for (int i = 0; i < G; ++i)

@@ -393,14 +393,20 @@ struct TriangleLoads : CopyLoads<kTriangleBytes, THREADS> {
     if (tid < 64) put(blocks, LOWER ? 1 : 4, tid, none);
     else if (tid < 128) put(blocks, LOWER ? 7 : 10, tid - 64, none);
   }
-  __device__ __forceinline__ void store(char* blocks, int tid) const {
+  bf16x4 x[Loads::kN][N];
+  __device__ __forceinline__ void split() {
+#pragma unroll
+    for (int n = 0; n < Loads::kN; ++n) split4<N>(__builtin_bit_cast(f32x4, Loads::r[n]), x[n]);
+  }
+  __device__ __forceinline__ void put(char* blocks, int tid) const {
 #pragma unroll
     for (int n = 0; n < Loads::kN; ++n)
-      if ((n + 1) * THREADS <= Loads::kPieces || tid + n * THREADS < Loads::kPieces) {
-        bf16x4 x[N];
-        split4<N>(__builtin_bit_cast(f32x4, Loads::r[n]), x);
-        put(blocks, triangle_half<LOWER>(__builtin_amdgcn_readfirstlane(tid >> 6) + n * (THREADS / 64)), tid & 63, x);
-      }
+      if ((n + 1) * THREADS <= Loads::kPieces || tid + n * THREADS < Loads::kPieces)
+        put(blocks, triangle_half<LOWER>(__builtin_amdgcn_readfirstlane(tid >> 6) + n * (THREADS / 64)), tid & 63, x[n]);
+  }
+  __device__ __forceinline__ void store(char* blocks, int tid) {
+    split();
+    put(blocks, tid);
   }
 };
 
