@@ -6,7 +6,7 @@
 // once.  A row lies in dk / 8 lanes of 8 numbers; a wave takes 512 / dk rows at a
 // time and has all its U times as many rows' loads in flight.  Memory bounds it: 256 sequences
 // of 16 heads of 128 take 102 us for 0.54 GB of states, 5.3 TB/s (a large copy 4.9), 80 us
-// where the last step's states are in part still cached; one sequence of 8 heads 3.3 us.
+// where the last step's states are in part still cached; one sequence of 8 heads 2.9 us.
 #include "mesa_common.h"
 #include "mesa_delta.h"
 
