@@ -695,10 +695,9 @@ mesa_status mesa_qk_preprocess_bwd(int32_t B, int32_t H, int32_t T, int32_t d, i
  * matter), gates and their gradients are aligned to 4 bytes, and no two rows of an
  * output share memory.
  *
- * States, gates and sums are fp32.  Products that a state, s_final or an fp32 result
- * depends on keep fp32's precision (operands in three bf16 parts); a bf16 o is
- * rounded once, from operands of 16 bits and more.  Every sum is formed in a fixed
- * order: equal inputs give bitwise equal results.  Valid rows are finite (not
+ * States, gates and sums are fp32, and products keep fp32's precision (operands in
+ * three bf16 parts); results in bf16 are rounded once, from such numbers.  Every sum
+ * is formed in a fixed order: equal inputs give bitwise equal results.  Valid rows are finite (not
  * checked): an infinity or NaN in one leaves that head of that sequence unspecified
  * from the start of the 64 tokens around it, and no other.
  * Supported: dk in {32, 64, 128}, dv a multiple of 16 up to 1024, H a multiple of

@@ -45,9 +45,9 @@ struct DeltaGates {
   float beta[kDeltaChunk];  // 0 behind the sequence
 };
 
-// Bytes of a chunk's two triangular 64x64 matrices as operands of the walk forward: the
-// inverse in three bf16 parts and the products of its queries and keys in `parts`.
-constexpr size_t delta_matrix_bytes(int parts) { return (3 + parts) * 6 * 1024; }
+// Bytes of a chunk's two triangular 64x64 matrices for the walk forward: the inverse as operands in three
+// bf16 parts, and the products of its queries and keys in fp32, ten tiles (bf16 rows), or as operands too.
+constexpr size_t delta_matrix_bytes(bool bf16) { return (3 * 6 + (bf16 ? 10 : 3 * 6)) * 1024; }
 // ... and for the walk back in fp32: ten tiles each.
 constexpr size_t kDeltaMatrixBytes = 2 * 10 * 1024;
 
@@ -70,7 +70,7 @@ struct DeltaParams {
   int open;                         // 1: the launch before the join: ends go to seg_add, and a segment
                                     // that does not start the walk starts from zero
   DeltaGates* gates;                // [B H, NC]
-  char* matrices;                   // [B H, NC, delta_matrix_bytes(2 or 3)]
+  char* matrices;                   // [B H, NC, delta_matrix_bytes]
   float* states;                    // [B H, NC, dv, dk] before each chunk, or null
   float* w;                         // [B H, NC, 64, dv]: v_t - gamma_t S_{t-1} k_t, or null
   // backward

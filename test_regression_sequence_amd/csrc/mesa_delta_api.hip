@@ -145,7 +145,7 @@ size_t carve(const mesa_delta_desc* d, bool keep, void* workspace, DeltaParams& 
   p.seg_map = w.take<float>(segments * d->dk * d->dk * 4);
   p.seg_add = w.take<float>(segments * state);
   p.seg_start = w.take<float>(segments * state);
-  p.matrices = w.take<char>(units * delta_matrix_bytes(d->dtype == MESA_BF16 ? 2 : 3));
+  p.matrices = w.take<char>(units * delta_matrix_bytes(d->dtype == MESA_BF16));
   if (keep) {
     p.states = w.take<float>(units * state);
     p.w = w.take<float>(units * kDeltaChunk * d->dv * 4);

@@ -13,10 +13,12 @@
 // off the walks, whose chunks follow one another.  Four waves a chunk: wave w forms row
 // tile w of both products, inverts diagonal block w and then has the inverse's column
 // of blocks w, which depends on no other column.  The forward walk's
-// matrices leave as its operands, in bf16 parts, the backward walk's in fp32, tile by tile
-// in the operands' order: two thirds of the bytes for conversions that the waves beside
+// inverse leaves as its operands, in bf16 parts, and the backward walk's matrices in fp32, tile
+// by tile in the operands' order: 10 KB in place of 18 for conversions that the waves beside
 // that walk's chain have the time for (train step at B=8 H=16 T=4096 d=128: walk back 341
-// -> 317 us; forward those waves form o, and the walk went from 232 to 258 us).
+// -> 317 us; forward those waves form o, and with both matrices so the walk went from 232 to
+// 258 us).  What the queries take goes in fp32 too where rows are bf16 (256 heads of 2048
+// tokens of 64, whole call: 222 -> 205 us); fp32 walks' LDS takes both as they come.
 // Logarithms of the forget factors are summed in 64 bits, so that a ratio c_t / c_j keeps
 // fp32's precision however strong the decay before it.
 //
@@ -41,7 +43,7 @@ template <int DK, bool BF16, bool BOTH>
 __global__ __launch_bounds__(256, BF16 || DK == 32 ? 4 : 2) void delta_chunk_kernel(DeltaParams p, uint32_t units) {
   auto form = [&](auto transposed, uint32_t unit) {
     constexpr bool TRANSPOSED = transposed();
-    constexpr int NP = BF16 ? 1 : 3, ES = BF16 ? 2 : 4, NA = BF16 ? 2 : 3;
+    constexpr int ES = BF16 ? 2 : 4;
     __shared__ __attribute__((aligned(16))) float low[10][16 * kLd];
     __shared__ __attribute__((aligned(16))) float diag[4][16 * kLd];
     __shared__ double sg[kDeltaChunk];
@@ -105,17 +107,16 @@ __global__ __launch_bounds__(256, BF16 || DK == 32 ? 4 : 2) void delta_chunk_ker
     __syncthreads();
 
     char* const to = (TRANSPOSED ? p.matrices_t + (int64_t)unit * (2 * kTriangleBytes)
-                                 : p.matrices + (int64_t)unit * delta_matrix_bytes(NA)) + lane * 16;
+                                 : p.matrices + (int64_t)unit * delta_matrix_bytes(BF16)) + lane * 16;
     auto put_tile = [&](int matrix, int i, int j, const f32x4& x) {
       *reinterpret_cast<f32x4*>(to + matrix * kTriangleBytes + triangle_tile<false>(i, j) * 1024) = x;
     };
     // A block's two tiles, in parts, to its place
-    auto put = [&](int matrix, int parts, int block, const f32x4& lo, const f32x4& hi) {
+    auto put = [&](int matrix, int block, const f32x4& lo, const f32x4& hi) {
       const Planes<3> f = split8<3>(lo, hi);
 #pragma unroll
       for (int n = 0; n < 3; ++n)
-        if (n < parts)
-          *reinterpret_cast<bf16x8*>(to + (matrix * 3 + n) * kBlocksBytes + block * 1024) = f.p[n];
+        *reinterpret_cast<bf16x8*>(to + (matrix * 3 + n) * kBlocksBytes + block * 1024) = f.p[n];
     };
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
@@ -155,9 +156,16 @@ __global__ __launch_bounds__(256, BF16 || DK == 32 ? 4 : 2) void delta_chunk_ker
     }
     if constexpr (!TRANSPOSED) {
       const f32x4 d = a[3];
-      if (wave == 0) put(1, NA, lower_block(0, 0), d, zero);
-      else put(1, NA, lower_block(wave, 0), a[0], wave == 1 ? d : a[1]);
-      if (wave >= 2) put(1, NA, lower_block(wave, 1), wave == 2 ? d : a[2], wave == 2 ? zero : d);
+      if constexpr (BF16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j == 3 || j < wave)
+            *reinterpret_cast<f32x4*>(to + 3 * kBlocksBytes + triangle_tile<true>(wave, j < 3 ? j : wave) * 1024) = a[j];
+      } else {
+        if (wave == 0) put(1, lower_block(0, 0), d, zero);
+        else put(1, lower_block(wave, 0), a[0], wave == 1 ? d : a[1]);
+        if (wave >= 2) put(1, lower_block(wave, 1), wave == 2 ? d : a[2], wave == 2 ? zero : d);
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < 3; ++j)
@@ -227,8 +235,8 @@ __global__ __launch_bounds__(256, BF16 || DK == 32 ? 4 : 2) void delta_chunk_ker
       }
       __syncthreads();
       auto row = [&](int j) { return *reinterpret_cast<const f32x4*>(&low[tile_of(wave, j)][r * kLd + 4 * g]); };
-      put(0, 3, lower_block(wave, 0), row(0), wave >= 1 ? row(1) : zero);
-      if (wave >= 2) put(0, 3, lower_block(wave, 1), row(2), wave == 3 ? row(3) : zero);
+      put(0, lower_block(wave, 0), row(0), wave >= 1 ? row(1) : zero);
+      if (wave >= 2) put(0, lower_block(wave, 1), row(2), wave == 3 ? row(3) : zero);
     }
   };
   if (!BOTH || blockIdx.x < units) form(std::false_type{}, blockIdx.x);

@@ -12,8 +12,7 @@
 // key dimension (and of Z and Y one), a lane one token in every result tile, so
 // that rows are scaled by lane constants and leave in pieces of 4 columns.  The first part
 // runs over the value dimension in slices of 32 (S0, dS and U through LDS, the next slice's
-// loads in flight), the second over the chunk's pairs.  What reaches the gates' fp32 gradients is multiplied in
-// three bf16 planes; Z and Y take two where dq and dk are bf16.
+// loads in flight), the second over the chunk's pairs.  All products keep fp32's precision (three bf16 planes).
 //
 // At B=8 H=16 T=4096 d=128 bf16 it moves 2.4 GB in 679 to 732 us, 3.3 to 3.6 TB/s, two thirds
 // of a large copy's rate.  The vector unit works 32 % of the time (a third of it on planes),
@@ -31,7 +30,7 @@ namespace {
 
 template <int DK, bool BF16>
 struct GradLds {
-  static constexpr int NP = BF16 ? 1 : 3, NZ = BF16 ? 2 : 3;
+  static constexpr int NP = BF16 ? 1 : 3, NZ = 3;
   static constexpr int kState = 32 * DK * 2, kU = 64 * 64, kPlane = 64 * DK * 2, kZ = 64 * 128;
   static constexpr int kS = 0, kD = 3 * kState, kUAt = 6 * kState, kEAt = kUAt + 3 * kU, kOAt = kEAt + 3 * kU,
                        kSlice = kOAt + NP * kU;
@@ -49,7 +48,7 @@ template <int DK, bool BF16>
 __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_kernel(DeltaParams p) {
   using L = GradLds<DK, BF16>;
   using Out = std::conditional_t<BF16, __bf16, float>;
-  constexpr int NP = L::NP, NZ = L::NZ, MH = DK / 32, KS = DK / 32, OMAX = BF16 ? 1 : 2;
+  constexpr int NP = L::NP, NZ = L::NZ, MH = DK / 32, KS = DK / 32;
   constexpr bool PAIR = L::kPair;
   constexpr int kPieces = 8 * DK, NS = (kPieces + 511) / 512;  // 16-byte pieces of a state's slice
   __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
@@ -323,8 +322,8 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
 #pragma unroll
       for (int i = 0; i < MH; ++i) {
         const Planes<NP> k = columns.template planes<NP>(lds + L::kK, L::kPlane, 32 * s, i);
-        aq[i] = mma<OMAX>(k, zf, aq[i]);
-        ak[i] = mma<OMAX>(k, yf, ak[i]);
+        aq[i] = mma<2>(k, zf, aq[i]);
+        ak[i] = mma<2>(k, yf, ak[i]);
       }
     }
     if (2 * s + 1 >= tile) {
@@ -332,8 +331,8 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
       const Planes<NZ> yf = pair_columns.template planes<NZ>(lds + L::kYAt, L::kZ, 32 * s, 0);
 #pragma unroll
       for (int i = 0; i < MH; ++i) {
-        ak[i] = mma<OMAX>(columns.template planes<NP>(lds + L::kQ, L::kPlane, 32 * s, i), zf, ak[i]);
-        ak[i] = mma<OMAX>(columns.template planes<NP>(lds + L::kK, L::kPlane, 32 * s, i), yf, ak[i]);
+        ak[i] = mma<2>(columns.template planes<NP>(lds + L::kQ, L::kPlane, 32 * s, i), zf, ak[i]);
+        ak[i] = mma<2>(columns.template planes<NP>(lds + L::kK, L::kPlane, 32 * s, i), yf, ak[i]);
       }
     }
   }

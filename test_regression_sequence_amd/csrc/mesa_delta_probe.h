@@ -79,7 +79,7 @@ __device__ __forceinline__ void probe_segment(const DeltaParams& p, uint32_t id,
     const int live = min(len - 64 * c, 64);
     const int64_t t0 = 64 * (int64_t)c, unit = (int64_t)bh * p.NC + c;
     kl.load(p.k.at, k0 + t0 * p.k.t, p.k.t, live, DK, tid);
-    tl.load(p.matrices + unit * (int64_t)delta_matrix_bytes(BF16 ? 2 : 3), tid);
+    tl.load(p.matrices + unit * (int64_t)delta_matrix_bytes(BF16), tid);
     gl.load(p.gates + unit, tid);
     if constexpr (BF16) {
       vl.load(p.v.at, v0 + 128 * slice + t0 * p.v.t, p.v.t, live, p.dv - 128 * slice, tid);

@@ -6,9 +6,9 @@
 // products without passing LDS.  Per chunk of 64 tokens
 //     W = T (V - c K M),  U = beta W,  M <- c_C M + K^T diag(c_C / c) U,
 //     O = c Q M + A U,    T = (I + X diag(beta))^-1,  A = lower(D Q K^T),
-// T and A from mesa_delta_chunk.hip.  Everything that a state depends on is
-// multiplied in three bf16 planes (fp32's precision); o takes two, whose error is
-// far below its own rounding.
+// T and A from mesa_delta_chunk.hip.  Everything that a state or o depends on is
+// multiplied in three bf16 planes (fp32's precision).  With two for o, whose error is far
+// below its own rounding, one in 2000 of its numbers was not the nearest.
 //
 // The chain from M to the next M bounds the walk, so four more waves, one beside
 // each of the others on its SIMD, take what is not on it: they load the next
@@ -30,10 +30,10 @@ namespace {
 
 template <int DK>
 struct ScanLds {
-  static constexpr int kTile = 64 * DK * 2, kMatrix = (int)delta_matrix_bytes(2), kGate = sizeof(DeltaGates);
+  static constexpr int kTile = 64 * DK * 2, kMatrix = (int)delta_matrix_bytes(true), kGate = sizeof(DeltaGates);
   static constexpr int kMPlane = DK * 32;  // one wave's columns
   static constexpr int kK = 0, kQ = kK + 2 * kTile, kV = kQ + kTile, kT = kV + 64 * 128, kA = kT + 3 * kBlocksBytes,
-                       kGates = kA + 4 * kBlocksBytes, kM = kGates + 2 * kGate, kU = kM + 8 * kMPlane,
+                       kGates = kA + 3 * kBlocksBytes, kM = kGates + 2 * kGate, kU = kM + 12 * kMPlane,
                        kBytes = kU + 4 * 4096;
 };
 
@@ -49,7 +49,7 @@ __device__ __forceinline__ void walk_segment(const DeltaParams& p, uint32_t id, 
   const int col0 = part.col0, cols = part.cols;
   const bool mine = 16 * wave < cols;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  char* const m_planes = lds + L::kM + wave * 2 * L::kMPlane + lane * 16;
+  char* const m_planes = lds + L::kM + wave * 3 * L::kMPlane + lane * 16;
   char* const u_to = lds + L::kU + wave * 4096 + lane * 16;  // U's four tiles
 
   if (chain) {
@@ -70,7 +70,7 @@ __device__ __forceinline__ void walk_segment(const DeltaParams& p, uint32_t id, 
         mp[s] = split8<3>(m[2 * s], m[2 * s + 1]);
         if constexpr (OUT)
 #pragma unroll
-          for (int n = 0; n < 2; ++n) *reinterpret_cast<bf16x8*>(m_planes + n * L::kMPlane + s * 1024) = mp[s].p[n];
+          for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8*>(m_planes + n * L::kMPlane + s * 1024) = mp[s].p[n];
       }
     };
     planes(0, KS);
@@ -215,7 +215,7 @@ __device__ __forceinline__ void walk_segment(const DeltaParams& p, uint32_t id, 
   RowLoads<DK, true, 256> kl, ql;
   RowLoads<64, true, 256> vl;
   CopyLoads<3 * kBlocksBytes, 256> tl;
-  CopyLoads<2 * kBlocksBytes, 256> al;
+  TriangleLoads<3, true, 256> al;
   CopyLoads<L::kGate, 256> gl;
   // part s of KS of a chunk's loads, so that they go out along the products with Q
   auto load = [&](int c, int s) {
@@ -244,20 +244,21 @@ __device__ __forceinline__ void walk_segment(const DeltaParams& p, uint32_t id, 
     gl.store(lds + L::kGates + (c & 1) * L::kGate, tid);
     if constexpr (OUT) {
       ql.store(lds + L::kQ, 0, tid);
-      al.store(lds + L::kA + (c & 1) * 2 * kBlocksBytes, tid);
+      al.store(lds + L::kA, tid);
     }
   };
+  if constexpr (OUT) al.clear(lds + L::kA, tid);
   if (first < last) {
     load_all(first);
     store(first);
   }
   __syncthreads();
   f32x4 o[4], u[4];  // o's transpose (a lane has 4 columns of one token) and U
-  BlockPair<2> a[3];
+  BlockPair<3> a[3];
   auto finish = [&](int c) {  // o of chunk c: A U added to c Q M
-    const Planes<2> up[2] = {split8<2>(u[0], u[1]), split8<2>(u[2], u[3])};
+    const Planes<3> up[2] = {split8<3>(u[0], u[1]), split8<3>(u[2], u[3])};
 #pragma unroll
-    for (int n = 0; n < 3; ++n) mma_pair<1, true, true>(n, a[n], up, o);
+    for (int n = 0; n < 3; ++n) mma_pair<2, true, true>(n, a[n], up, o);
     const int live = mine ? len - 64 * c : 0;
     const Window to = window_at(static_cast<__bf16*>(p.o.at) + o0 + 64 * (int64_t)c * p.o.t);
 #pragma unroll
@@ -271,14 +272,13 @@ __device__ __forceinline__ void walk_segment(const DeltaParams& p, uint32_t id, 
   for (int c = first; c < last; ++c) {
     const int next = min(c + 1, last - 1);
     if constexpr (OUT) {
-      if (c > first) finish(c - 1);
       Planes<1> f[2][4];
-      Planes<2> mp[2];
+      Planes<3> mp[2];
       auto operands = [&](int s) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[s & 1][i] = rows(lds + L::kQ, 16 * i, s);
 #pragma unroll
-        for (int n = 0; n < 2; ++n) mp[s & 1].p[n] = *reinterpret_cast<const bf16x8*>(m_planes + n * L::kMPlane + s * 1024);
+        for (int n = 0; n < 3; ++n) mp[s & 1].p[n] = *reinterpret_cast<const bf16x8*>(m_planes + n * L::kMPlane + s * 1024);
       };
       operands(0);
 #pragma unroll
@@ -288,14 +288,14 @@ __device__ __forceinline__ void walk_segment(const DeltaParams& p, uint32_t id, 
         if (s + 1 < KS) operands(s + 1);
         fence<true>();
         load(next, s);
-        mma_tiles_t<1>(mp[s & 1], f[s & 1], o);
+        mma_tiles_t<2>(mp[s & 1], f[s & 1], o);
         fence<true>();
       }
       const DeltaGates& gates = *reinterpret_cast<const DeltaGates*>(lds + L::kGates + (c & 1) * L::kGate);
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] *= gates.c[16 * i + r];
 #pragma unroll
-      for (int n = 0; n < 3; ++n) a[n] = pair_of<true, 2>(lds + L::kA + (c & 1) * 2 * kBlocksBytes, n, lane);
+      for (int n = 0; n < 3; ++n) a[n] = pair_of<true, 3>(lds + L::kA, n, lane);
     } else {
       load_all(next);
     }
@@ -305,9 +305,9 @@ __device__ __forceinline__ void walk_segment(const DeltaParams& p, uint32_t id, 
       for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const f32x4*>(u_to + i * 1024);
     }
     store(c + 1);
+    if constexpr (OUT) finish(c);
     __syncthreads();
   }
-  if (OUT && first < last) finish(last - 1);
   if (OUT && mine) {  // behind the sequence
     const int end = (int)min((int64_t)p.T, (int64_t)64 * (first + p.L));
     for (int64_t t = max(len, 64 * first) + r; t < end; t += 16) store_out4<__bf16>(p.o.at, o0 + t * p.o.t + 4 * g, zero);

@@ -18,8 +18,8 @@ namespace {
 
 template <int DK>
 struct ScanLds {
-  static constexpr int NP = 3, NA = 3;
-  static constexpr int kPlane = 64 * DK * 2, kMatrices = (int)delta_matrix_bytes(NA);
+  static constexpr int NP = 3;
+  static constexpr int kPlane = 64 * DK * 2, kMatrices = (int)delta_matrix_bytes(false);
   static constexpr int kK = 0, kQ = kK + NP * kPlane, kV = kQ + NP * kPlane, kT = kV + NP * 64 * 128,
                        kA = kT + 3 * kBlocksBytes, kGates = kT + kMatrices, kBytes = kGates + sizeof(DeltaGates);
 };
@@ -27,7 +27,7 @@ struct ScanLds {
 template <int DK, bool OUT>
 __device__ __forceinline__ void walk_segment(const DeltaParams& p, uint32_t id, char* lds) {
   using L = ScanLds<DK>;
-  constexpr int NP = L::NP, NA = L::NA, MT = DK / 16, KS = DK / 32;
+  constexpr int NP = L::NP, MT = DK / 16, KS = DK / 32;
   const int tid = threadIdx.x & 255, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15,
             g = lane >> 4;
   const bool chain = __builtin_amdgcn_readfirstlane(threadIdx.x) < 256;
@@ -102,7 +102,7 @@ __device__ __forceinline__ void walk_segment(const DeltaParams& p, uint32_t id, 
       }
       Planes<3> mp[2], u[2], ut[2], px[2];
       BlockPair<3> t;
-      BlockPair<NA> a;
+      BlockPair<3> a;
       Planes<NP> f[2][4];
       f32x4 x[4] = {zero, zero, zero, zero}, y[4] = {zero, zero, zero, zero};
       constexpr int E = OUT ? 2 : 1;
@@ -164,7 +164,7 @@ __device__ __forceinline__ void walk_segment(const DeltaParams& p, uint32_t id, 
 #pragma unroll
       for (int n = 0; n < NG; ++n) {  // M += K^T U
         if (n + 1 < NG) keys(n + 1, kt[(n + 1) & 1]);
-        else if constexpr (OUT) a = pair_of<true, NA>(lds + L::kA, 0, lane);
+        else if constexpr (OUT) a = pair_of<true, 3>(lds + L::kA, 0, lane);
         if (OUT && n == NG - 1) {
 #pragma unroll
           for (int s = 0; s < 2; ++s) u[s] = split8<3>(x[2 * s], x[2 * s + 1]);
