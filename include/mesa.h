@@ -740,8 +740,7 @@ mesa_status mesa_delta_fwd(const mesa_delta_desc* d, const void* q, const void* 
  *   d_o           [B, H, T, dv] dtype
  *   d_sfinal      [B, H, dv, dk] fp32 or NULL (zero)
  *   dq, dk [B, Hk, T, dk], dv [B, H, T, dv]  dtype out
- *   dgamma, dbeta [B, H, T] fp32 out.  dgamma is formed as the gradient at
- *                 log gamma over gamma, and is 0 where gamma is
+ *   dgamma, dbeta [B, H, T] fp32 out
  *   ds0           [B, H, dv, dk] fp32 out or NULL.  May be d_sfinal itself
  *   states_in_workspace  1: the forward ran with keep_states = 1 and this same
  *                 workspace, descriptor and inputs, and nothing else used the workspace

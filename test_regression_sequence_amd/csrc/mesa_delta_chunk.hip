@@ -99,8 +99,8 @@ __global__ __launch_bounds__(256, BF16 || DK == 32 ? 4 : 2) void delta_chunk_ker
       if constexpr (!TRANSPOSED) {
         DeltaGates& out = p.gates[unit];
         out.g[lane] = lg;
-        out.c[lane] = decay(lg, 0.0);
-        out.tail[lane] = decay(__shfl(lg, 63), lg);
+        out.c[lane] = decay_exact(lg, 0.0);
+        out.tail[lane] = decay_exact(__shfl(lg, 63), lg);
         out.beta[lane] = beta;
       }
     }

@@ -7,6 +7,9 @@
 //     dK = tail U dS - c beta E S0 + Z^T Q + (Y + Y^T) K,
 // and the logarithm of token i's forget factor acts on every pair t >= i > j, on
 // what tokens t >= i read of S0, on what tokens j < i leave behind, and on S0 -> S'.
+// Each of these terms has the factor itself as a factor, so their sum over it is the
+// gradient at it; for factors below 2^-64, 0 among them, the terms are added up once more
+// with the factor left out, as the products with it leave fp32's range.
 //
 // One workgroup a (sequence, head, chunk): a wave owns 16 tokens and half of the
 // key dimension (and of Z and Y one), a lane one token in every result tile, so
@@ -40,9 +43,13 @@ struct GradLds {
   // barrier a slice (750 -> 730 us at B=8 H=16 T=4096 d=128 bf16).
   static constexpr bool kPair = BF16 && DK <= 64, kTwo = !kPair && (BF16 || DK < 128);
   static constexpr int kFirst = (kTwo ? 2 : 1) * kSlice;
-  static constexpr int kK = 0, kQ = NP * kPlane, kZAt = 2 * NP * kPlane, kYAt = kZAt + NZ * kZ, kSecond = kYAt + NZ * kZ;
+  static constexpr int kK = 0, kQ = NP * kPlane, kZAt = 2 * NP * kPlane, kYAt = kZAt + NZ * kZ,
+                       kSmall = kYAt + NZ * kZ, kSecond = kSmall + 12 * 64 * 4;
   static constexpr int kBytes = kFirst > kSecond ? kFirst : kSecond;
 };
+
+// Forget factors below this have their gradient from terms without them.
+constexpr float kSmallGate = 0x1p-64f;
 
 template <int DK, bool BF16>
 __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_kernel(DeltaParams p) {
@@ -225,6 +232,14 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
   gl.store(reinterpret_cast<char*>(&gates), tid);
   __syncthreads();
 
+  // The tokens with small factors; for each of these, what a wave's pairs across it give, and what any token reads
+  // of S0 and leaves behind, all without its factor
+  const uint64_t small = __ballot(gammas[lane] < kSmallGate);
+  float(*const across)[64] = reinterpret_cast<float(*)[64]>(lds + L::kSmall), (*const reads)[64] = across + 8,
+                             (*const leaves)[64] = across + 10;
+  if (small) across[wave][lane] = 0.f;
+  auto own_log = [&](int i) { return gates.g[i] - (i ? gates.g[i - 1] : 0.0); };
+
   float sum = 0.f, earlier = 0.f;
   const float beta_own = gates.beta[own];
   char* const pairs = lds + (half ? L::kYAt : L::kZAt);
@@ -243,8 +258,19 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
         for (int s = 0; s < KS; ++s)
           dot = mma<2>(rows.template planes<NP>(lds + L::kK, L::kPlane, 16 * j, s), f[s], dot);
         const int at = 16 * j + 4 * g;
+        for (uint64_t left = small; left; left &= left - 1) {
+          const int i = __builtin_ctzll(left);
+          if (i <= 16 * j || i >= 16 * tile + 16) continue;
+          const double without = gt - own_log(i);
+          float pairs = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = zy[j][e] * decay(gt, gates.g[at + e]) * weight;
+          for (int e = 0; e < 4; ++e)
+            pairs += at + e < i && i <= own ? zy[j][e] * weight * dot[e] * decay_exact(without, gates.g[at + e]) : 0.f;
+          pairs = wave_sum(pairs);
+          if (lane == 0) across[wave][i] += pairs;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = zy[j][e] * decay_exact(gt, gates.g[at + e]) * weight;
         if (j < tile) {  // pairs with tokens of earlier tiles: sums over them, and over the tile's tokens
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -285,13 +311,31 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
   }
   const float cc = gates.c[own], tail = gates.tail[own], cb = cc * beta_own;
   float left = 0.f;  // what this token leaves behind the chunk
+  auto own_values = [&](const char* plane, int i) {
+    return half ? rows.template values<NP>(plane, L::kPlane, 16 * tile, MH + i)
+                : rows.template values<NP>(plane, L::kPlane, 16 * tile, i);
+  };
+  if (small) {
+    float of_state = 0.f, behind_it = 0.f;
+#pragma unroll
+    for (int i = 0; i < MH; ++i) {
+      const f32x4 q = own_values(lds + L::kQ, i), k = own_values(lds + L::kK, i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        of_state += q[e] * aq[i][e] - beta_own * k[e] * ak[i][e];
+        behind_it += k[e] * ad[i][e];
+      }
+    }
+    of_state = sum_lane_groups(of_state);
+    behind_it = sum_lane_groups(behind_it);
+    if (g == 0) {
+      reads[half][own] = of_state;
+      leaves[half][own] = behind_it;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < MH; ++i) {
-    auto own_values = [&](const char* plane) {
-      return half ? rows.template values<NP>(plane, L::kPlane, 16 * tile, MH + i)
-                  : rows.template values<NP>(plane, L::kPlane, 16 * tile, i);
-    };
-    const f32x4 q = own_values(lds + L::kQ), k = own_values(lds + L::kK);
+    const f32x4 q = own_values(lds + L::kQ, i), k = own_values(lds + L::kK, i);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       sum += cc * q[e] * aq[i][e] - cb * k[e] * ak[i][e];
@@ -376,10 +420,21 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
     x += (double)tiles + diag[0][lane] + diag[1][lane];
 #pragma unroll
     for (int n = 0; n < 8; ++n) whole += red[n];
-    x += gates.c[63] * whole;
+    x = (x + gates.c[63] * whole) / (double)gammas[lane];
+    for (uint64_t left = small; left; left &= left - 1) {
+      const int i = __builtin_ctzll(left);
+      const double without = own_log(i), all = gates.g[63] - without;
+      double sum = lane >= i ? ((double)reads[0][lane] + reads[1][lane]) * decay_exact(gates.g[lane], without)
+                             : ((double)leaves[0][lane] + leaves[1][lane]) * decay_exact(all, gates.g[lane]);
+#pragma unroll
+      for (int off = 1; off < 64; off *= 2) sum += __shfl_xor(sum, off);
+      sum += decay_exact(all, 0.0) * whole;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) sum += across[n][i];
+      if (lane == i) x = sum;
+    }
     if (lane < here) {
-      *gate_at(p.dgamma, b, h, t0 + lane) =
-          lane < live && gammas[lane] != 0.f ? (float)(x / (double)gammas[lane]) : 0.f;
+      *gate_at(p.dgamma, b, h, t0 + lane) = lane < live ? (float)x : 0.f;
       *gate_at(p.dbeta, b, h, t0 + lane) = lane < live ? dbetas[lane] : 0.f;
     }
   }

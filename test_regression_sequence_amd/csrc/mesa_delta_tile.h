@@ -486,6 +486,13 @@ __device__ __forceinline__ float* gate_at(const DeltaGate& x, int b, int h, int6
 
 // exp2 of a difference of two logarithms that are kept in 64 bits.
 __device__ __forceinline__ float decay(double a, double b) { return __builtin_amdgcn_exp2f((float)(a - b)); }
+// The same with fp32's precision for small results too: the whole part becomes an exponent, where rounding 20.3
+// to fp32 alone costs 2^-20 of the result.
+__device__ __forceinline__ float decay_exact(double a, double b) {
+  const double x = a - b;
+  const float whole = rintf((float)x);
+  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((float)(x - (double)whole)), (int)whole);
+}
 
 // One workgroup's part of a walk: 64 columns of one head's state over one segment's chunks.
 struct Part {
