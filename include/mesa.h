@@ -697,9 +697,11 @@ mesa_status mesa_qk_preprocess_bwd(int32_t B, int32_t H, int32_t T, int32_t d, i
  *
  * States, gates and sums are fp32, and products keep fp32's precision (operands in
  * three bf16 parts); results in bf16 are rounded once, from such numbers.  Every sum
- * is formed in a fixed order: equal inputs give bitwise equal results.  Valid rows are finite (not
- * checked): an infinity or NaN in one leaves that head of that sequence unspecified
- * from the start of the 64 tokens around it, and no other.
+ * is formed in a fixed order: equal inputs give bitwise equal results.  Valid rows are
+ * finite (not checked): an infinity or NaN in one leaves that head of that sequence
+ * unspecified from the start of the 64 tokens around it, and no other.  A gamma of
+ * NaN, and for whole sequences one below 0, makes o and the states NaN from its token
+ * on, and gradients on both sides of it.
  * Supported: dk in {32, 64, 128}, dv a multiple of 16 up to 1024, H a multiple of
  * Hk, token strides up to 2^20, B H max(ceil(T/64), ceil(dv/64)) <= 2^22.
  * Outputs and workspace may not overlap inputs or one another but as said

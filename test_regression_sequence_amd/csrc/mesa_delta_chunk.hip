@@ -85,7 +85,8 @@ __global__ __launch_bounds__(256, BF16 || DK == 32 ? 4 : 2) void delta_chunk_ker
     float beta = 0.f;
     if (lane < live) {
       const int64_t t = c * kDeltaChunk + lane;
-      lg = fmax(log2((double)*gate_at(p.gamma, b, h, t)), -16384.0);  // a factor of 0 ends what came before
+      lg = log2((double)*gate_at(p.gamma, b, h, t));
+      if (lg < -16384.0) lg = -16384.0;  // a factor of 0 ends what came before; a NaN or a negative one's stays NaN
       beta = *gate_at(p.beta, b, h, t);
     }
 #pragma unroll

@@ -114,3 +114,29 @@ def test_against_differences_of_the_forward():
         bound = 2.0 ** -20 * (np.linalg.norm(a["d_o"]) * 32 ** 0.5 * 3 + np.linalg.norm(a["d_sfinal"]) * 8) / step
         assert bool(((num - g[:, :, i].double()).abs() <= bound).all()), (num, g[:, :, i], bound)
         assert bool((g[:, :, i].abs() > 4 * bound).any())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,at", [(1, 0), (50, 20), (130, 64), (130, 127), (1300, 700)])
+@pytest.mark.parametrize("value", [float("nan"), -0.5])
+def test_a_factor_that_is_none(value, T, at, dtype):
+    """A NaN, or a number below 0, is not taken for a factor that forgets everything: as in the definition a NaN's state is
+    NaN from its token on, and its gradients are before it and behind it.  Other heads are as without it."""
+    a = draw(1, 2, 1, T, 64, 48, DTYPES[dtype], seed=10)
+    t = to_dev(a, DTYPES[dtype])
+    want = mesa.delta_fwd(*(t[n] for n in NAMES), s0=t["s0"], return_state=True)
+    t["gamma"][0, 1, at] = value
+    ws = torch.empty(mesa.delta_workspace_bytes(*(t[n] for n in NAMES), keep_states=True), device="cuda", dtype=torch.uint8)
+    r = mesa.delta_fwd(*(t[n] for n in NAMES), s0=t["s0"], return_state=True, keep_states=True, workspace=ws)
+    assert bool(r["o"][0, 1, at:].isnan().all()) and bool(r["s_final"][0, 1].isnan().all())
+    first = at // 64 * 64
+    assert torch.equal(r["o"][0, 1, :first], want["o"][0, 1, :first])
+    for n in ("o", "s_final"):
+        assert torch.equal(r[n][0, 0], want[n][0, 0])
+    for kept in (False, True):
+        g = mesa.delta_bwd(*(t[n] for n in NAMES), t["d_o"], s0=t["s0"], d_sfinal=t["d_sfinal"], state_grads=True,
+                           workspace=ws if kept else None, states_in_workspace=kept)
+        assert bool(g["ds0"][0, 1].isnan().all()) and bool(g["dv"][0, 1, :at].isnan().all())
+        assert bool(g["dgamma"][0, 1, at:].isnan().all()) and bool(g["dbeta"][0, 1, at:].isnan().all())
+        assert bool(g["dq"][0, 0, at:].isnan().all())  # (shared by both heads)
+        assert bool(g["dv"][0, 0].isfinite().all()) and bool(g["dgamma"][0, 0].isfinite().all())
