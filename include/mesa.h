@@ -721,7 +721,8 @@ typedef struct {
 
 /* Scratch bytes of mesa_delta_fwd (keep_states 0), or of a forward that leaves its
  * states and of mesa_delta_bwd (1); 0 for an invalid or unsupported descriptor and
- * for T == 0. */
+ * for T == 0.  With all else equal more sequences or tokens never take less, so a
+ * buffer for the largest call serves all smaller ones. */
 size_t mesa_delta_workspace_bytes(const mesa_delta_desc* d, int32_t keep_states);
 
 mesa_status mesa_delta_fwd(const mesa_delta_desc* d, const void* q, const void* k, const void* v,

@@ -103,14 +103,27 @@ mesa_status check_delta(const mesa_delta_desc* d) {
 // Measured, one sequence, in segments and in one walk: 1024 tokens and 4 heads of 64,
 // forward 44 and 53 us, gradients 77 and 107, in fp32 46 and 77, 95 and 149; 4 heads of
 // 128, 54 and 63, 120 and 149; 4096 tokens and 16 heads of 128, 113 and 216, 325 and 551.
+constexpr int kMaxSegments = 32;
+
+int64_t values_of(const mesa_delta_desc* d) { return (d->dv + 63) / 64; }
+int64_t both_of(const mesa_delta_desc* d) { return (d->dv + d->dk + 127) / 128; }
+
+// Bounds of heads and of heads times segments where a walk goes in segments (of all B and T).  Where the
+// openings take no fewer workgroups than the walk the rule itself gives them (128 and 472 workgroups of
+// 64 columns); else they bind it, to at most a tenth more by its own reckoning, as 31 short segments that
+// take many rounds would save no more and hold 8184 workgroups' states.
+int64_t most_heads(const mesa_delta_desc* d) { return (both_of(d) < values_of(d) ? 341 : 128) / values_of(d); }
+int64_t most_segments(const mesa_delta_desc* d) { return (both_of(d) < values_of(d) ? 1024 : 472) / values_of(d); }
+
 int segments_of(const mesa_delta_desc* d) {
-  const int64_t heads = (int64_t)d->B * d->H, values = (d->dv + 63) / 64, both = (d->dv + d->dk + 127) / 128;
+  const int64_t heads = (int64_t)d->B * d->H, values = values_of(d), both = both_of(d);
   const int chunks = chunks_of(d);
+  if (heads > most_heads(d)) return 1;
   const double more = d->dtype == MESA_BF16 ? 1.0 : 0.5;
   const auto rounds = [](int64_t blocks) { return (double)((blocks + 255) / 256); };
   int best = 1;
   double least = 0.9 * chunks * rounds(heads * values);
-  for (int n = 2; n <= 32 && n * 2 <= chunks; ++n) {
+  for (int n = 2; n <= kMaxSegments && n * 2 <= chunks && n * heads <= most_segments(d); ++n) {
     const int per = (chunks + n - 1) / n;
     if ((chunks + per - 1) / per != n) continue;  // (no segment stays empty)
     const double time =
@@ -134,14 +147,11 @@ struct Carve {
   }
 };
 
-// Places the workspace's parts; returns its size.
-size_t carve(const mesa_delta_desc* d, bool keep, void* workspace, DeltaParams& p) {
-  p.NS = segments_of(d);
-  p.L = (chunks_of(d) + p.NS - 1) / p.NS;
+// Places the workspace's parts for that many heads, `segments` segments of them all; returns its size.
+size_t place(const mesa_delta_desc* d, size_t heads, size_t segments, bool keep, void* workspace, DeltaParams& p) {
   Carve w{static_cast<char*>(workspace)};
-  const size_t units = (size_t)d->B * d->H * chunks_of(d), state = (size_t)d->dv * d->dk * 4;
+  const size_t units = heads * chunks_of(d), state = (size_t)d->dv * d->dk * 4;
   p.gates = w.take<DeltaGates>(units * sizeof(DeltaGates));
-  const size_t segments = p.NS > 1 ? (size_t)d->B * d->H * p.NS : 0;
   p.seg_map = w.take<float>(segments * d->dk * d->dk * 4);
   p.seg_add = w.take<float>(segments * state);
   p.seg_start = w.take<float>(segments * state);
@@ -153,12 +163,28 @@ size_t carve(const mesa_delta_desc* d, bool keep, void* workspace, DeltaParams& 
     p.dstates = w.take<float>(units * state);
     p.e = w.take<float>(units * kDeltaChunk * d->dv * 4);
     if (d->H != d->Hk) {
-      const size_t rows = (size_t)d->B * d->H * d->T * d->dk * 4;
+      const size_t rows = heads * d->T * d->dk * 4;
       p.dq_heads = w.take<float>(rows);
       p.dk_heads = w.take<float>(rows);
     }
   }
   return w.at;
+}
+
+void carve(const mesa_delta_desc* d, bool keep, void* workspace, DeltaParams& p) {
+  const size_t heads = (size_t)d->B * d->H;
+  p.NS = segments_of(d);
+  p.L = (chunks_of(d) + p.NS - 1) / p.NS;
+  place(d, heads, p.NS > 1 ? heads * p.NS : 0, keep, workspace, p);
+}
+
+// Room for what carve() places here and for any smaller B and T: without segments, or with as many as
+// so many heads and chunks may be given.
+size_t room(const mesa_delta_desc* d, bool keep) {
+  DeltaParams p{};
+  const size_t heads = (size_t)d->B * d->H, few = std::min(heads, (size_t)most_heads(d)),
+               segments = std::min(few * std::min(kMaxSegments, chunks_of(d) / 2), (size_t)most_segments(d));
+  return std::max(place(d, heads, 0, keep, nullptr, p), place(d, few, segments, keep, nullptr, p));
 }
 
 // (a token stride that no index uses may be any: kernels step by it to rows that they then leave out)
@@ -230,8 +256,7 @@ extern "C" {
 
 size_t mesa_delta_workspace_bytes(const mesa_delta_desc* d, int32_t keep_states) {
   if (check_delta(d) != MESA_OK || (keep_states != 0 && keep_states != 1)) return 0;
-  DeltaParams p{};
-  return carve(d, keep_states == 1, nullptr, p);
+  return room(d, keep_states == 1);
 }
 
 mesa_status mesa_delta_fwd(const mesa_delta_desc* d, const void* q, const void* k, const void* v, const float* gamma,
