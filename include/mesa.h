@@ -786,7 +786,8 @@ mesa_status mesa_delta_step(const mesa_delta_desc* d, const void* q, const void*
  *
  * Squares and sums are 64-bit, in a fixed order: equal inputs give bitwise equal
  * results.  g scale is fp32, rounded once to g's type.  A NaN makes norm, scale and
- * every output NaN; an infinite gradient gives an infinite norm and a scale of 0.
+ * every output NaN; an infinite gradient gives an infinite norm and a scale of 0, or
+ * of 1 where max_norm is infinite.
  * The host arrays are read before the call returns.  Supported: count <= 4096, 2^44
  * elements in all.  mesa_grad_norm writes the norm alone. */
 size_t mesa_grad_clip_workspace_bytes(void);

@@ -96,7 +96,8 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, const
   double sum = 0.0;
   for (int i = threadIdx.x; i < n_sums; i += kThreads) sum += sums[i];
   const double norm = sqrt(block_sum(sum)), ratio = (double)max_norm / (norm + (double)eps);
-  const float scale = ratio >= 1.0 ? 1.f : (float)ratio;  // (a NaN stays one)
+  // no bound leaves infinite gradients too as they are; a NaN stays one
+  const float scale = ratio >= 1.0 || (max_norm == INFINITY && norm == norm) ? 1.f : (float)ratio;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     if (norm_out) *norm_out = (float)norm;
     if (scale_out) *scale_out = scale;
