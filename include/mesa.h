@@ -785,7 +785,8 @@ mesa_status mesa_delta_step(const mesa_delta_desc* d, const void* q, const void*
  *   workspace     mesa_grad_clip_workspace_bytes() bytes
  *
  * Squares and sums are 64-bit, in a fixed order: equal inputs give bitwise equal
- * results.  g scale is fp32, rounded once to g's type.  A NaN makes norm, scale and
+ * results.  g scale is fp32, rounded once to g's type, and a scale below fp32's
+ * normal numbers keeps its precision there.  A NaN makes norm, scale and
  * every output NaN; an infinite gradient gives an infinite norm and a scale of 0, or
  * of 1 where max_norm is infinite.
  * The host arrays are read before the call returns.  Supported: count <= 4096, 2^44

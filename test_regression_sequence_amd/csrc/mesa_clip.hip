@@ -74,7 +74,7 @@ __global__ __launch_bounds__(kThreads) void clip_squares_kernel(ClipTable t, dou
 }
 
 template <bool BF16>
-__device__ __forceinline__ void scaled(const void* grad, void* out, int64_t at, int64_t n, float scale) {
+__device__ __forceinline__ void scaled(const void* grad, void* out, int64_t at, int64_t n, float factor, int power) {
   Raw8<BF16> r[kVectors];
 #pragma unroll
   for (int i = 0; i < kVectors; ++i) {
@@ -86,7 +86,7 @@ __device__ __forceinline__ void scaled(const void* grad, void* out, int64_t at, 
     const int64_t from = at + (int64_t)(i * kThreads + threadIdx.x) * 8;
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = r[i].at(e) * scale;
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_amdgcn_ldexpf(r[i].at(e) * factor, power);
     store_raw8<BF16, true>(out, from, v, (int)min(n - from, (int64_t)8));
   }
 }
@@ -102,13 +102,16 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, const
     if (norm_out) *norm_out = (float)norm;
     if (scale_out) *scale_out = scale;
   }
+  // A scale below fp32's normal numbers has few bits left there: as a number from 1/2 on and a power of two
+  int power = 0;
+  const float factor = scale < 0x1p-126f ? (float)frexp(ratio, &power) : scale;
   const int64_t all = t.first[t.count];
   for (int64_t id = all - 1 - blockIdx.x; id >= 0; id -= gridDim.x) {
     const int i = tensor_of(t, id);
     if (!t.out[i] || (t.out[i] == t.grad[i] && scale == 1.f)) continue;
     const int64_t at = (id - t.first[i]) * kClipPiece;
-    if (t.bf16[i]) scaled<true>(t.grad[i], t.out[i], at, t.n[i], scale);
-    else scaled<false>(t.grad[i], t.out[i], at, t.n[i], scale);
+    if (t.bf16[i]) scaled<true>(t.grad[i], t.out[i], at, t.n[i], factor, power);
+    else scaled<false>(t.grad[i], t.out[i], at, t.n[i], factor, power);
   }
 }
 

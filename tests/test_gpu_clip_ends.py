@@ -37,3 +37,24 @@ def test_no_bound_and_infinite_gradients(into, dtype):
         else:
             assert float(r["norm"]) == math.inf and float(r["scale"]) == scale
             assert all(torch.equal(g, k) for g, k in zip(r["grads"], kept))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("size", [1e36, 1e38])
+@pytest.mark.parametrize("bound", [1.0, 1e-3, 1e-6, 2.0 ** -126])
+def test_scales_below_the_normal_numbers(bound, size, dtype):
+    """Gradients near fp32's end, whose scale is subnormal or less: outputs are as near as any (the scale's rounding and a
+    product's, 2^-24 each, in bf16 one to it, 2^-8), where they are normal numbers themselves."""
+    x = [(some(F32) * size).to(dtype), torch.full((3,), -size, device="cuda", dtype=dtype)]
+    norm = math.sqrt(sum(float(g.double().square().sum()) for g in x))
+    scale = bound / (norm + 1e-6)
+    assert scale < 2.0 ** -116
+    r = mesa.grad_clip(x, bound, out=[torch.empty_like(g) for g in x])
+    half = (2.0 ** -8 if dtype is BF16 else 0.0) + 3 * 2.0 ** -24
+    for g, o in zip(x, r["grads"]):
+        want = g.double() * scale
+        assert bool(((o.double() - want).abs() <= half * want.abs() + 2.0 ** -149 + (2.0 ** -134 if dtype is BF16 else 0.0)).all())
+    assert abs(float(r["scale"]) - scale) <= 2.0 ** -23 * scale + 2.0 ** -150
+    in_place = [g.clone() for g in x]
+    mesa.grad_clip(in_place, bound)
+    assert all(torch.equal(g, o) for g, o in zip(in_place, r["grads"]))
