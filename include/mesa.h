@@ -784,11 +784,11 @@ mesa_status mesa_delta_step(const mesa_delta_desc* d, const void* q, const void*
  *   norm, scale   device, one fp32 each, out; scale may be NULL
  *   workspace     mesa_grad_clip_workspace_bytes() bytes
  *
- * Squares and sums are 64-bit, in a fixed order: equal inputs give bitwise equal
- * results.  g scale is fp32, rounded once to g's type, and a scale below fp32's
- * normal numbers keeps its precision there.  A NaN makes norm, scale and
- * every output NaN; an infinite gradient gives an infinite norm and a scale of 0, or
- * of 1 where max_norm is infinite.
+ * Squares, sums and the scale up to its rounding are 64-bit, in a fixed order: equal
+ * inputs give bitwise equal results.  g scale is fp32, rounded once to g's type, and a
+ * scale below fp32's normal numbers keeps its precision there.  A NaN makes norm, scale
+ * and every output NaN; an infinite gradient gives an infinite norm and a scale of 0,
+ * or of 1 where max_norm is infinite.
  * The host arrays are read before the call returns.  Supported: count <= 4096, 2^44
  * elements in all.  mesa_grad_norm writes the norm alone. */
 size_t mesa_grad_clip_workspace_bytes(void);
@@ -798,7 +798,7 @@ mesa_status mesa_grad_norm(int32_t count, const void* const* grads, const int64_
                            size_t workspace_bytes, hipStream_t stream);
 
 mesa_status mesa_grad_clip(int32_t count, const void* const* grads, void* const* outs,
-                           const int64_t* sizes, const mesa_dtype* dtypes, float max_norm, float eps,
+                           const int64_t* sizes, const mesa_dtype* dtypes, double max_norm, double eps,
                            float* norm, float* scale, void* workspace, size_t workspace_bytes,
                            hipStream_t stream);
 

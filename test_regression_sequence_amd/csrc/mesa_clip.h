@@ -25,7 +25,7 @@ struct ClipTable {
 hipError_t launch_clip_squares(const ClipTable& t, int blocks, double* sums, hipStream_t s);
 // norm = sqrt of all sums, scale = min(1, max_norm / (norm + eps)), outputs scaled.
 // norm, scale: written by the first workgroup where not null.
-hipError_t launch_clip_scale(const ClipTable& t, int blocks, const double* sums, int n_sums, float max_norm, float eps,
+hipError_t launch_clip_scale(const ClipTable& t, int blocks, const double* sums, int n_sums, double max_norm, double eps,
                              float* norm, float* scale, hipStream_t s);
 
 }  // namespace mesa

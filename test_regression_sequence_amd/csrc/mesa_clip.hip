@@ -91,11 +91,11 @@ __device__ __forceinline__ void scaled(const void* grad, void* out, int64_t at, 
   }
 }
 
-__global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, const double* sums, int n_sums, float max_norm,
-                                                              float eps, float* norm_out, float* scale_out) {
+__global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, const double* sums, int n_sums, double max_norm,
+                                                              double eps, float* norm_out, float* scale_out) {
   double sum = 0.0;
   for (int i = threadIdx.x; i < n_sums; i += kThreads) sum += sums[i];
-  const double norm = sqrt(block_sum(sum)), ratio = (double)max_norm / (norm + (double)eps);
+  const double norm = sqrt(block_sum(sum)), ratio = max_norm / (norm + eps);
   // no bound leaves infinite gradients too as they are; a NaN stays one
   const float scale = ratio >= 1.0 || (max_norm == INFINITY && norm == norm) ? 1.f : (float)ratio;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -122,7 +122,7 @@ hipError_t launch_clip_squares(const ClipTable& t, int blocks, double* sums, hip
   return hipGetLastError();
 }
 
-hipError_t launch_clip_scale(const ClipTable& t, int blocks, const double* sums, int n_sums, float max_norm, float eps,
+hipError_t launch_clip_scale(const ClipTable& t, int blocks, const double* sums, int n_sums, double max_norm, double eps,
                              float* norm, float* scale, hipStream_t s) {
   clip_scale_kernel<<<blocks, kThreads, 0, s>>>(t, sums, n_sums, max_norm, eps, norm, scale);
   return hipGetLastError();

@@ -468,7 +468,7 @@ bool each_table(int32_t count, const void* const* grads, void* const* outs, cons
 }
 
 mesa_status clip(int32_t count, const void* const* grads, void* const* outs, bool need_outs, const int64_t* sizes,
-                 const mesa_dtype* dtypes, float max_norm, float eps, float* norm, float* scale, void* workspace,
+                 const mesa_dtype* dtypes, double max_norm, double eps, float* norm, float* scale, void* workspace,
                  size_t workspace_bytes, hipStream_t stream) {
   const mesa_status st = check_clip(count, grads, outs, need_outs, sizes, dtypes);
   if (st != MESA_OK) return st;
@@ -507,13 +507,13 @@ size_t mesa_grad_clip_workspace_bytes(void) { return pad256(kClipSums * sizeof(d
 mesa_status mesa_grad_norm(int32_t count, const void* const* grads, const int64_t* sizes, const mesa_dtype* dtypes,
                            float* norm, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (!norm) return MESA_ERR_INVALID_ARG;
-  return clip(count, grads, nullptr, false, sizes, dtypes, 1.f, 1.f, norm, nullptr, workspace, workspace_bytes, stream);
+  return clip(count, grads, nullptr, false, sizes, dtypes, 1.0, 1.0, norm, nullptr, workspace, workspace_bytes, stream);
 }
 
 mesa_status mesa_grad_clip(int32_t count, const void* const* grads, void* const* outs, const int64_t* sizes,
-                           const mesa_dtype* dtypes, float max_norm, float eps, float* norm, float* scale,
+                           const mesa_dtype* dtypes, double max_norm, double eps, float* norm, float* scale,
                            void* workspace, size_t workspace_bytes, hipStream_t stream) {
-  if (!norm || !(max_norm >= 0.f) || !(eps >= 0x1p-126f) || std::isinf(eps)) return MESA_ERR_INVALID_ARG;
+  if (!norm || !(max_norm >= 0.0) || !(eps >= 0x1p-126) || std::isinf(eps)) return MESA_ERR_INVALID_ARG;
   return clip(count, grads, outs, true, sizes, dtypes, max_norm, eps, norm, scale, workspace, workspace_bytes, stream);
 }
 

@@ -156,7 +156,7 @@ def lib() -> ctypes.CDLL:
         L.mesa_grad_norm.restype = ctypes.c_int
         L.mesa_grad_norm.argtypes = [I32] + [P] * 5 + [S, P]
         L.mesa_grad_clip.restype = ctypes.c_int
-        L.mesa_grad_clip.argtypes = [I32] + [P] * 4 + [F, F] + [P] * 3 + [S, P]
+        L.mesa_grad_clip.argtypes = [I32] + [P] * 4 + [ctypes.c_double] * 2 + [P] * 3 + [S, P]
         _LIB = L
     return _LIB
 

@@ -58,3 +58,20 @@ def test_scales_below_the_normal_numbers(bound, size, dtype):
     in_place = [g.clone() for g in x]
     mesa.grad_clip(in_place, bound)
     assert all(torch.equal(g, o) for g, o in zip(in_place, r["grads"]))
+
+
+def test_bounds_are_taken_as_given():
+    """The scale is bound / (norm + eps) in 64 bits, rounded once: a bound or eps of Python is not rounded to fp32 before."""
+    x = [torch.tensor([3.0], device="cuda")]
+    for i in range(1, 60):
+        bound, eps = 0.1 * i / 3, 1e-6 * i
+        want = torch.tensor(min(1.0, bound / (3.0 + eps)), dtype=torch.float64).float()
+        assert float(mesa.grad_clip(x, bound, eps=eps, out=[torch.empty_like(x[0])])["scale"]) == float(want), (bound, eps)
+
+
+def test_bounds_above_the_largest_float():
+    x = [torch.full((100,), 3e38, device="cuda")]
+    kept = x[0].double()
+    r = mesa.grad_clip(x, 1e39)
+    assert abs(float(r["scale"]) - 1 / 3) <= 2.0 ** -22
+    assert bool((x[0].double() / kept * 3 - 1).abs().max() <= 2.0 ** -22)
