@@ -40,21 +40,25 @@ bool apart(const mesa_delta_desc* d, int heads, int width, const mesa_rows& r) {
   return true;
 }
 
-// What such rows of `width` elements of `bytes` bytes fill: pieces at one stride
-// where the strides give that, else all from the first element to the last.
-Span span_of(const mesa_delta_desc* d, int heads, int width, size_t bytes, const mesa_rows& r, const void* at) {
+// What such rows of `width` elements of `bytes` bytes fill; where rows share elements or lie
+// between one another, all from the first element to the last.
+Blocks blocks_of(const mesa_delta_desc* d, int heads, int width, size_t bytes, const mesa_rows& r, const void* at) {
   Dim dims[3];
   const int n = dims_of(d, heads, r, dims);
   if (d->T == 0) return {at, 0};
-  int64_t piece = width, extent = width, rows = 1;
-  for (int i = 0; i < n; ++i) extent += dims[i].stride * (dims[i].size - 1);
+  int64_t piece = width, extent = width;
+  bool nested = true;
   int i = 0;
   while (i < n && dims[i].stride == piece) piece *= dims[i++].size;
-  if (i == n) return {at, piece * bytes};
-  const int64_t stride = dims[i].stride;
-  while (i < n && dims[i].stride == stride * rows) rows *= dims[i++].size;
-  if (i < n || stride < piece) return {at, extent * bytes};
-  return {at, piece * bytes, (size_t)rows, stride * bytes};
+  Blocks x{at, piece * bytes};
+  for (int64_t reach = piece; i < n; ++i) {
+    nested = nested && dims[i].stride >= reach;
+    reach += dims[i].stride * (dims[i].size - 1);
+    x.step[x.dims++] = {(size_t)dims[i].size, dims[i].stride * bytes};
+  }
+  if (nested) return x;
+  for (i = 0; i < n; ++i) extent += dims[i].stride * (dims[i].size - 1);
+  return {at, extent * bytes};
 }
 
 // Gates are read one by one.
@@ -274,13 +278,13 @@ mesa_status mesa_delta_fwd(const mesa_delta_desc* d, const void* q, const void* 
   const size_t need = mesa_delta_workspace_bytes(d, keep_states);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MESA_ERR_WORKSPACE;
   const size_t e = dtype_bytes(d->dtype), state = (size_t)d->B * d->H * d->dv * d->dk * 4;
-  const Span ins[] = {span_of(d, d->Hk, d->dk, e, d->q, q), span_of(d, d->Hk, d->dk, e, d->k, k),
-                      span_of(d, d->H, d->dv, e, d->v, v), span_of(d, d->H, 1, 4, d->gamma, gamma),
-                      span_of(d, d->H, 1, 4, d->beta, beta), {lengths, (size_t)d->B * 4}};
-  const Span outs[] = {span_of(d, d->H, d->dv, e, d->o, o), {workspace, need}, {s_final, state}}, start{s0, state};
+  const Blocks ins[] = {blocks_of(d, d->Hk, d->dk, e, d->q, q), blocks_of(d, d->Hk, d->dk, e, d->k, k),
+                      blocks_of(d, d->H, d->dv, e, d->v, v), blocks_of(d, d->H, 1, 4, d->gamma, gamma),
+                      blocks_of(d, d->H, 1, 4, d->beta, beta), {lengths, (size_t)d->B * 4}};
+  const Blocks outs[] = {blocks_of(d, d->H, d->dv, e, d->o, o), {workspace, need}, {s_final, state}}, start{s0, state};
   // s_final may be s0, and nothing else may lie over s0
-  if (overlap(outs, ins) || overlap(outs) || overlap({outs[0], outs[1]}, {start}) ||
-      (s_final != s0 && overlap({outs[2]}, {start})))
+  if (overlap(outs, ins) || overlap(outs) || overlap<Blocks>({outs[0], outs[1]}, {start}) ||
+      (s_final != s0 && overlap<Blocks>({outs[2]}, {start})))
     return MESA_ERR_INVALID_ARG;
   DeltaParams p = delta_params(d, q, k, v, gamma, beta, s0, lengths);
   carve(d, keep_states == 1, workspace, p);
@@ -316,18 +320,18 @@ mesa_status mesa_delta_bwd(const mesa_delta_desc* d, const mesa_delta_grad_rows*
   const size_t need = mesa_delta_workspace_bytes(d, 1);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MESA_ERR_WORKSPACE;
   const size_t e = dtype_bytes(d->dtype), state = (size_t)d->B * d->H * d->dv * d->dk * 4;
-  const Span ins[] = {span_of(d, d->Hk, d->dk, e, d->q, q), span_of(d, d->Hk, d->dk, e, d->k, k),
-                      span_of(d, d->H, d->dv, e, d->v, v), span_of(d, d->H, 1, 4, d->gamma, gamma),
-                      span_of(d, d->H, 1, 4, d->beta, beta), {lengths, (size_t)d->B * 4}, {s0, state},
-                      span_of(d, d->H, d->dv, e, gr->d_o, d_o)};
-  const Span outs[] = {span_of(d, d->Hk, d->dk, e, gr->dq, dq), span_of(d, d->Hk, d->dk, e, gr->dk, dk),
-                       span_of(d, d->H, d->dv, e, gr->dv, dv), span_of(d, d->H, 1, 4, gr->dgamma, dgamma),
-                       span_of(d, d->H, 1, 4, gr->dbeta, dbeta), {workspace, need}, {ds0, state}};
-  const Span last{d_sfinal, state};
+  const Blocks ins[] = {blocks_of(d, d->Hk, d->dk, e, d->q, q), blocks_of(d, d->Hk, d->dk, e, d->k, k),
+                      blocks_of(d, d->H, d->dv, e, d->v, v), blocks_of(d, d->H, 1, 4, d->gamma, gamma),
+                      blocks_of(d, d->H, 1, 4, d->beta, beta), {lengths, (size_t)d->B * 4}, {s0, state},
+                      blocks_of(d, d->H, d->dv, e, gr->d_o, d_o)};
+  const Blocks outs[] = {blocks_of(d, d->Hk, d->dk, e, gr->dq, dq), blocks_of(d, d->Hk, d->dk, e, gr->dk, dk),
+                       blocks_of(d, d->H, d->dv, e, gr->dv, dv), blocks_of(d, d->H, 1, 4, gr->dgamma, dgamma),
+                       blocks_of(d, d->H, 1, 4, gr->dbeta, dbeta), {workspace, need}, {ds0, state}};
+  const Blocks last{d_sfinal, state};
   // ds0 may be d_sfinal, and nothing else may lie over d_sfinal
   if (overlap(outs, ins) || overlap(outs) ||
-      overlap({outs[0], outs[1], outs[2], outs[3], outs[4], outs[5]}, {last}) ||
-      (ds0 != d_sfinal && overlap({outs[6]}, {last})))
+      overlap<Blocks>({outs[0], outs[1], outs[2], outs[3], outs[4], outs[5]}, {last}) ||
+      (ds0 != d_sfinal && overlap<Blocks>({outs[6]}, {last})))
     return MESA_ERR_INVALID_ARG;
   DeltaParams p = delta_params(d, q, k, v, gamma, beta, s0, lengths);
   carve(d, true, workspace, p);
@@ -354,10 +358,10 @@ mesa_status mesa_delta_step(const mesa_delta_desc* d, const void* q, const void*
       !rows_aligned(d, d->Hk, d->k) || !rows_aligned(d, d->H, d->v) || !rows_aligned(d, d->H, d->o))
     return MESA_ERR_ALIGNMENT;
   const size_t e = dtype_bytes(d->dtype), state = (size_t)d->B * d->H * d->dv * d->dk * 4;
-  const Span ins[] = {span_of(d, d->Hk, d->dk, e, d->q, q), span_of(d, d->Hk, d->dk, e, d->k, k),
-                      span_of(d, d->H, d->dv, e, d->v, v), span_of(d, d->H, 1, 4, d->gamma, gamma),
-                      span_of(d, d->H, 1, 4, d->beta, beta)};
-  const Span outs[] = {span_of(d, d->H, d->dv, e, d->o, o), {s_state, state}};
+  const Blocks ins[] = {blocks_of(d, d->Hk, d->dk, e, d->q, q), blocks_of(d, d->Hk, d->dk, e, d->k, k),
+                      blocks_of(d, d->H, d->dv, e, d->v, v), blocks_of(d, d->H, 1, 4, d->gamma, gamma),
+                      blocks_of(d, d->H, 1, 4, d->beta, beta)};
+  const Blocks outs[] = {blocks_of(d, d->H, d->dv, e, d->o, o), {s_state, state}};
   if (overlap(outs, ins) || overlap(outs)) return MESA_ERR_INVALID_ARG;
   DeltaStepParams p{};
   p.q = q; p.k = k; p.v = v; p.gamma = gamma; p.beta = beta; p.state = s_state; p.o = o;
