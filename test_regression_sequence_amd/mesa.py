@@ -1039,7 +1039,7 @@ def delta_bwd(q, k, v, gamma, beta, d_o, *, s0=None, lengths=None, d_sfinal=None
 def delta_step(q, k, v, gamma, beta, s_state, *, out=None, stream=None) -> dict:
     """One token of N sequences: q, k [N, Hk, dk], v [N, H, dv] (fp32 or bf16, last index
     contiguous), gamma, beta [N, H] fp32, s_state [N, H, dv, dk] fp32 updated in place.
-    Returns ``o`` [N, H, dv] in v's dtype."""
+    Returns ``o`` [N, H, dv] in v's dtype; out["o"] may be a slice of a wider tensor."""
     dev, dt = _home(q, "q", 3, stream), q.dtype
     code = _code_of(q, "q")
     N, Hk, dk = q.shape
@@ -1052,7 +1052,11 @@ def delta_step(q, k, v, gamma, beta, s_state, *, out=None, stream=None) -> dict:
     _delta_gate(gamma, "gamma", (N, H), dev)
     _delta_gate(beta, "beta", (N, H), dev)
     _want(s_state, "s_state", (N, H, dv, dk), torch.float32, dev)
-    o = _result(out, "o", (N, H, dv), dt, dev, stream, v)
+    if out and out.get("o") is not None:
+        o = out["o"]
+        _delta_in(o, "o", (N, H, dv), dt, dev)
+    else:
+        o = _new((N, H, dv), dt, dev, stream, v)
     rows = [Rows(*t.stride()[:2], 0) for t in (q, k, v, o, gamma, beta)]
     desc = DeltaDesc(N, H, Hk, 1, dk, dv, code, *rows)
     _launch("mesa_delta_step", dev, stream, ctypes.byref(desc), _addr(q), _addr(k), _addr(v), _addr(gamma), _addr(beta),

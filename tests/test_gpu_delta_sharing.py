@@ -66,6 +66,21 @@ def test_parts_of_a_prompt_into_one_tensor():
     assert torch.equal(o, want["o"]) and torch.equal(state, want["s_final"])
 
 
+def test_steps_into_slices():
+    """One token of a batch whose rows lie in one padded tensor."""
+    a = inputs(3, 5, 4, 2, 1, 64, 64)
+    x = {n: t[:, :, 0].contiguous() for n, t in a.items() if n in INPUTS}
+    s = a["s0"].clone()
+    want = mesa.delta_step(*x.values(), s)["o"]
+    wide = torch.zeros((5, 14, 64), device="cuda", dtype=BF16)
+    q, k, v, o = wide[:, 0:2], wide[:, 2:4], wide[:, 5:9], wide[:, 9:13]
+    for n, t in zip(("q", "k", "v"), (q, k, v)):
+        t.copy_(x[n])
+    s2 = a["s0"].clone()
+    mesa.delta_step(q, k, v, x["gamma"], x["beta"], s2, out={"o": o})
+    assert torch.equal(o, want) and torch.equal(s, s2)
+
+
 def test_rows_that_are_shared_are_refused():
     """In the same padded tensors: one that reaches into another's rows, or into the next sequence's."""
     B, H, T, d = 3, 2, 70, 64
