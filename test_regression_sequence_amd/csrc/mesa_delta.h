@@ -62,7 +62,7 @@ struct DeltaParams {
   // A walk in NS segments of L chunks (NS = 1: whole).  seg_map: [B H, NS, dk, dk], row j what
   // an inner segment makes of the state whose row is unit vector j; seg_add: [B H, NS, dv, dk], what
   // it makes of a zero state (the segment at the walk's start: of the given one);
-  // seg_start: [B H, NS, dv, dk], the states that segments start from behind the join
+  // seg_start: [B H, NS, dv, dk], the states that segments start from behind the join (all but the walk's first)
   int NS, L;
   int seg0, segs;                   // the segments of a launch of a walk
   Divisor by_part, by_slices;       // its workgroups of a head, and of those the ones of a segment
@@ -96,7 +96,7 @@ hipError_t launch_delta_grads(bool bf16, const DeltaParams& p, hipStream_t s);
 // seg_map and seg_add of a walk forward, and its first segment whole.
 hipError_t launch_delta_open(const DeltaParams& p, hipStream_t s);  // bf16 rows
 hipError_t launch_delta_open_f32(const DeltaParams& p, hipStream_t s);
-// seg_start from seg_map, seg_add and the state at one end; `back`: from the last segment to the first.
+// seg_start from seg_map and seg_add; `back`: from the last segment to the first.
 hipError_t launch_delta_join(bool back, const DeltaParams& p, hipStream_t s);
 
 struct DeltaStepParams {

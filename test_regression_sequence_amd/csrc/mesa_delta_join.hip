@@ -20,11 +20,8 @@ __global__ __launch_bounds__(4 * DK) void delta_join_kernel(DeltaParams p) {
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int groups = p.dv / 16, bh = blockIdx.x / groups, row0 = blockIdx.x % groups * 16;
   const int64_t edge = (int64_t)bh * p.NS + (BACK ? p.NS - 1 : 0), second = BACK ? edge - 1 : edge + 1;
-  const float* given = BACK ? p.d_sfinal : p.s0;
-  for (int i = tid; i < 16 * DK; i += kThreads) {
-    p.seg_start[(edge * p.dv + row0) * DK + i] = given ? given[((int64_t)bh * p.dv + row0) * DK + i] : 0.f;
+  for (int i = tid; i < 16 * DK; i += kThreads)
     p.seg_start[(second * p.dv + row0) * DK + i] = rows[1][i / DK][i % DK] = p.seg_add[(edge * p.dv + row0) * DK + i];
-  }
   for (int n = 1; n + 1 < p.NS; ++n) {
     const int seg = BACK ? p.NS - 1 - n : n, next = BACK ? seg - 1 : seg + 1;
     const int64_t at = (int64_t)bh * p.NS + seg, to = (int64_t)bh * p.NS + next;
