@@ -64,28 +64,23 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepParams p) {
   }
 }
 
-template <int DK, bool BF16, int U>
-void launch(DeltaStepParams p, hipStream_t s) {
-  constexpr int rows = 4 * (512 / DK) * U;
+template <int DK, bool BF16>
+hipError_t launch(DeltaStepParams p, hipStream_t s) {
+  constexpr int rows = 128, U = rows / (4 * (512 / DK));  // of a workgroup, and of a lane group
   const uint32_t groups = (uint32_t)((p.dv + rows - 1) / rows);
   p.by_groups = divisor(groups);
   p.by_h = divisor((uint32_t)p.H);
   p.by_shared = divisor((uint32_t)(p.H / p.Hk));
   delta_step_kernel<DK, BF16, U><<<(uint32_t)((int64_t)p.N * p.H * groups), 256, 0, s>>>(p);
-}
-
-template <int DK, bool BF16>
-hipError_t choose(const DeltaStepParams& p, hipStream_t s) {
-  launch<DK, BF16, DK / 16>(p, s);  // 128 rows a workgroup
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_delta_step(bool bf16, const DeltaStepParams& p, hipStream_t s) {
-  if (p.dk == 128) return bf16 ? choose<128, true>(p, s) : choose<128, false>(p, s);
-  if (p.dk == 64) return bf16 ? choose<64, true>(p, s) : choose<64, false>(p, s);
-  return bf16 ? choose<32, true>(p, s) : choose<32, false>(p, s);
+  if (p.dk == 128) return bf16 ? launch<128, true>(p, s) : launch<128, false>(p, s);
+  if (p.dk == 64) return bf16 ? launch<64, true>(p, s) : launch<64, false>(p, s);
+  return bf16 ? launch<32, true>(p, s) : launch<32, false>(p, s);
 }
 
 }  // namespace mesa
