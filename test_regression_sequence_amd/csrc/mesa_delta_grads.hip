@@ -234,7 +234,7 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
 
   // The tokens with small factors; for each of these, what a wave's pairs across it give, and what any token reads
   // of S0 and leaves behind, all without its factor
-  const uint64_t small = __ballot(gammas[lane] < kSmallGate);
+  const uint64_t small = __ballot(gammas[lane] < kSmallGate), zeros = __ballot(gammas[lane] == 0.f);
   float(*const across)[64] = reinterpret_cast<float(*)[64]>(lds + L::kSmall), (*const reads)[64] = across + 8,
                              (*const leaves)[64] = across + 10;
   if (small) across[wave][lane] = 0.f;
@@ -258,9 +258,11 @@ __global__ __launch_bounds__(512, BF16 && DK <= 64 ? 4 : 2) void delta_grads_ker
         for (int s = 0; s < KS; ++s)
           dot = mma<2>(rows.template planes<NP>(lds + L::kK, L::kPlane, 16 * j, s), f[s], dot);
         const int at = 16 * j + 4 * g;
+        // (factors of 0 that every pair of these tiles lies across)
+        const uint64_t between = zeros & ((2ull << (16 * tile)) - 1) & ~((1ull << (16 * j + 15) << 1) - 1);
         for (uint64_t left = small; left; left &= left - 1) {
           const int i = __builtin_ctzll(left);
-          if (i <= 16 * j || i >= 16 * tile + 16) continue;
+          if (i <= 16 * j || i >= 16 * tile + 16 || (between & ~(1ull << i))) continue;
           const double without = gt - own_log(i);
           float pairs = 0.f;
 #pragma unroll
