@@ -696,7 +696,8 @@ mesa_status mesa_qk_preprocess_bwd(int32_t B, int32_t H, int32_t T, int32_t d, i
  * output share memory.
  *
  * States, gates and sums are fp32, and products keep fp32's precision (operands in
- * three bf16 parts); results in bf16 are rounded once, from such numbers.  Every sum
+ * three bf16 parts; numbers below about 2^-100 lose parts of theirs); results in bf16
+ * are rounded once, from such numbers.  Every sum
  * is formed in a fixed order: equal inputs give bitwise equal results.  Valid rows are
  * finite (not checked): an infinity or NaN in one leaves that head of that sequence
  * unspecified from the start of the 64 tokens around it, and no other.  A gamma of

@@ -15,7 +15,7 @@
 //     first half:   chain K N, E, half of K^T E     others Q^T (c dO), loads
 //     second half:  chain the rest, N, its planes   others A^T dO of the next chunk, loads
 //
-// Memory bounds it: at B=8 H=16 T=4096 d=128 322 us for 1.4 GB, 4.3 TB/s where a large copy
+// Memory bounds it: at B=8 H=16 T=4096 d=128 312 to 319 us for 1.4 GB, 4.4 TB/s where a large copy
 // reaches 4.9; the chain itself takes about 3 us a chunk.
 #include "mesa_delta_tile.h"
 

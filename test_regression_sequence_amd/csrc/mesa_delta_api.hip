@@ -102,11 +102,12 @@ mesa_status check_delta(const mesa_delta_desc* d) {
 // its chunks one after the other; with fewer of those than the 256 CUs, segments of it run
 // side by side, after a launch that finds what each makes of unit rows and of zero (128 of
 // dv + dk columns a workgroup; the first segment runs with it) and one that joins them.  In
-// times of one chunk (about 2.7 us, in fp32 nearly twice that), the two launches take about 3 and
-// half a chunk a segment.
-// Measured, one sequence, in segments and in one walk: 1024 tokens and 4 heads of 64,
-// forward 44 and 53 us, gradients 77 and 107, in fp32 46 and 77, 95 and 149; 4 heads of
-// 128, 54 and 63, 120 and 149; 4096 tokens and 16 heads of 128, 113 and 216, 325 and 551.
+// times of one chunk (of 128: 3.4 us, in fp32 5.6), the two launches take about 3 and
+// half a chunk a segment; half of that in fp32, as when its chunk took twice a bf16 one's time.
+// Measured, one sequence, calls in segments and in one walk, forward and gradients on kept
+// states: 1024 tokens and 4 heads of 64, 38 and 57 us, 42 and 62, in fp32 44 and 76, 51 and 87;
+// 4 heads of 128, 52 and 70, 67 and 87, in fp32 68 and 110, 86 and 140; 4096 tokens and 16
+// heads of 128, 109 and 244, 194 and 337, in fp32 162 and 398, 273 and 564.
 constexpr int kMaxSegments = 32;
 
 int64_t values_of(const mesa_delta_desc* d) { return (d->dv + 63) / 64; }

@@ -12,8 +12,7 @@
 // There are B H T / 64 chunks, all independent, so what can be done here is taken
 // off the walks, whose chunks follow one another.  Four waves a chunk: wave w forms row
 // tile w of both products, inverts diagonal block w and then has the inverse's column
-// of blocks w, which depends on no other column.  The forward walk's
-// inverse leaves as its operands, in bf16 parts, and the backward walk's matrices in fp32, tile
+// of blocks w, which depends on no other column.  The forward walk's inverse leaves as its operands, in bf16 parts, and the backward walk's matrices in fp32, tile
 // by tile in the operands' order: 10 KB in place of 18 for conversions that the waves beside
 // that walk's chain have the time for (train step at B=8 H=16 T=4096 d=128: walk back 341
 // -> 317 us; forward those waves form o, and with both matrices so the walk went from 232 to
@@ -22,10 +21,10 @@
 // Logarithms of the forget factors are summed in 64 bits, so that a ratio c_t / c_j keeps
 // fp32's precision however strong the decay before it.
 //
-// Memory bounds it where there are many chunks: at B=8 H=16 T=4096 d=128 bf16 101 us for
-// 0.52 GB forward (5.2 TB/s; a large copy 4.9), 173 to 184 us for 0.95 GB for both.  One round of
-// chunks is a chain of 6.5 us (fp32 9): loads 1, logarithms 1, products and decays 2, the
-// diagonal blocks 1, the others and the way out 1.5.
+// Memory bounds it where there are many chunks: at B=1 H=16 T=32768 d=128 bf16 99 to 107 us for
+// 0.52 GB forward (4.8 to 5.2 TB/s; a large copy 4.9), at B=8 H=16 T=4096 168 to 174 us for 0.96 GB
+// for both.  One round of chunks is a chain of 6.5 us (fp32 9): loads 1, logarithms 1, products and
+// decays 2, the diagonal blocks 1, the others and the way out 1.5.
 #include "mesa_delta_tile.h"
 
 namespace mesa {

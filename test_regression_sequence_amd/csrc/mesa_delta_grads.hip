@@ -17,11 +17,11 @@
 // runs over the value dimension in slices of 32 (S0, dS and U through LDS, the next slice's
 // loads in flight), the second over the chunk's pairs.  All products keep fp32's precision (three bf16 planes).
 //
-// At B=8 H=16 T=4096 d=128 bf16 it moves 2.4 GB in 679 to 732 us, 3.3 to 3.6 TB/s, two thirds
-// of a large copy's rate.  The vector unit works 32 % of the time (a third of it on planes),
-// the matrix unit 22 % and LDS 24 %, hardly at once: registers leave room for two waves a SIMD,
+// At B=8 H=16 T=4096 d=128 bf16 it moves 2.45 GB in 691 to 718 us, 3.4 to 3.6 TB/s, 70 %
+// of a large copy's rate.  The vector unit works 33 % of the time (a third of it on planes),
+// the matrix unit 23 % and LDS 26 %, hardly at once: registers leave room for two waves a SIMD,
 // which the barriers keep in step.  A workgroup that goes from chunk to chunk, its loads ahead
-// across the second part, takes the same 732 us.  Sums for the gates by eight lanes a token in
+// across the second part, took the same time.  Sums for the gates by eight lanes a token in
 // place of one wave's scans cost more in LDS than they saved (730 -> 805 us).
 #include <algorithm>
 
@@ -38,9 +38,9 @@ struct GradLds {
   static constexpr int kS = 0, kD = 3 * kState, kUAt = 6 * kState, kEAt = kUAt + 3 * kU, kOAt = kEAt + 3 * kU,
                        kSlice = kOAt + NP * kU;
   // Two workgroups a CU hide one another's waits where 128 registers a lane do (keys and
-  // queries then wait for the slices' end): 50 -> 41 us at B=4 H=8 T=2048 d=64.  Else two
-  // slices in LDS where they fit: one is converted beside the products of the other, a
-  // barrier a slice (750 -> 730 us at B=8 H=16 T=4096 d=128 bf16).
+  // queries then wait for the slices' end): 50 -> 41 us at B=4 H=8 T=2048 d=64 (44 with three
+  // planes for Z and Y).  Else two slices in LDS where they fit: one is converted beside the
+  // products of the other, a barrier a slice (750 -> 730 us at B=8 H=16 T=4096 d=128 bf16).
   static constexpr bool kPair = BF16 && DK <= 64, kTwo = !kPair && (BF16 || DK < 128);
   static constexpr int kFirst = (kTwo ? 2 : 1) * kSlice;
   static constexpr int kK = 0, kQ = NP * kPlane, kZAt = 2 * NP * kPlane, kYAt = kZAt + NZ * kZ,

@@ -5,7 +5,7 @@
 // the segment at the walk's start has the given state in its Q already.  From one
 // segment to the next that is a 16 x dk by dk x dk product for each 16 rows,
 // in fp32 matrix instructions: a workgroup has 16 rows in LDS, each of its waves a
-// tile of the result's columns.  9 segments: 18 us at H=16 dk=128, 8: 7 us at 32 heads of 64; maps
+// tile of the result's columns.  9 segments: 17 us at H=16 dk=128, 5: 7 us at 32 heads of 64; maps
 // loaded one or three steps ahead change nothing.
 #include "mesa_delta_tile.h"
 

@@ -11,8 +11,8 @@
 // while the chunk before is in the works; so do values of two bytes, those of four, whose
 // planes would not fit beside two chunks of keys, go to their lanes.
 //
-// B=1 H=16 T=32768 d=128: 4.8 us a chunk and 128 columns, of which a SIMD's matrix unit
-// works 38 % and its vector unit 41 %, hardly at the same time (four chains of 16 columns as
+// B=1 H=16 T=32768 d=128: 4.8 to 5.3 us a chunk and 128 columns, of which a SIMD's matrix unit
+// works 40 % and its vector unit 42 %, hardly at the same time (four chains of 16 columns as
 // in the walk itself: 2.7 us for 64 columns).  The two waves of a SIMD half a chunk apart,
 // so that conversions of one meet products of the other, took a tenth longer: the second
 // barrier a chunk costs more.  The first segment's walk in the same launch: 9 segments in

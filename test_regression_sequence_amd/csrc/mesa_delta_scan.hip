@@ -16,10 +16,13 @@
 //     first half:   chain K M, W, U, half of K^T U       others Q M, the next chunk's loads
 //     second half:  chain the rest of K^T U, planes of M  others A U, next chunk to LDS, o
 //
-// A chunk takes 2.8 us where few workgroups run, of which the chain's 132 products are 0.9
-// and their operands' ways through conversions and LDS the rest, and 3.6 us on all CUs (B=1
-// H=16 T=32768 d=128, 8 segments of 57 chunks side by side: 214 to 219 us).  With states and W kept memory bounds it: at
-// B=8 H=16 T=4096 d=128 356 to 370 us for 1.6 GB, 4.3 to 4.5 TB/s where a large copy reaches 4.9.
+// A chunk takes 3.4 us where few workgroups run, of which the chain's 132 products are 0.9
+// and their operands' ways through conversions and LDS the rest, and 4.3 to 4.7 on all CUs
+// (B=1 H=16 T=32768 d=128, 8 segments of 57 chunks side by side: 244 to 266 us, the matrix unit
+// 38 %, the vector unit 36 % and LDS 43 % of them).  With states and W kept memory is next: at
+// B=8 H=16 T=4096 d=128 388 to 400 us for 1.6 GB, 4.0 to 4.1 TB/s where a large copy reaches 4.9.
+// (o's products in two planes took 220 to 237 and 356 to 371 us.  In three, with A U in the walk's
+// first half as then, prefill calls of 128 heads of 2048 tokens took 212 us, so 189.)
 #include <algorithm>
 
 #include "mesa_delta_probe.h"

@@ -7,7 +7,7 @@
 // split its rows in registers meanwhile, and between the two barriers only write them.
 // The state's waves alone, with the splits between the barriers, took 5.7 us a chunk at
 // dk = 64, so it takes 4.4, of which 216 products are 1.5 (B=5 H=6 T=777 dk=64 dv=96 in 4
-// segments: 19 us for the first segment and the openings of the others, 18 for the rest).
+// segments: 18 to 19 us for the first segment and the openings of the others, 17 for the rest).
 #include <algorithm>
 
 #include "mesa_delta_probe.h"
